@@ -20,7 +20,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 HOST_SOURCES = ["glq_codebook.cpp", "glq_encode.cpp", "glq_ep.cpp"]
-HIP_SOURCES = ["glq_kernels.hip"]
+HIP_SOURCES = ["glq_kernels.hip", "glq_attn.hip"]
 
 
 def _run(cmd):

@@ -1,0 +1,805 @@
+// glq_attn.hip -- paged key-value cache and attention (gfx950) and their
+// entry points of the C ABI: what a model runs between its compressed q, k, v
+// projections and its output projection.
+//
+// Kernels:
+//   kv_append_k     tokens' keys and values -> bf16, 8-bit or 4-bit rows
+//   kv_read_k       cached rows -> dense keys and values
+//   attn_decode_k   one new token per sequence over the paged cache
+//   attn_prompt_k   packed prompts, float32 matrix instructions
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+
+#include "glq.h"
+
+namespace glq {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// The error text of this thread: glq_last_error()'s 256-byte buffer.
+int hip_status(hipError_t e, const char *where = "launch") {
+  if (e == hipSuccess) return GLQ_OK;
+  snprintf(const_cast<char *>(glq_last_error()), 256, "%s: %s (%d)", where, hipGetErrorString(e), (int)e);
+  return GLQ_ERR_HIP;
+}
+
+// two floats to packed bf16 (round to nearest even), one v_cvt_pk_bf16_f32
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+// the high halves of two floats: exact where both are bf16 values
+__device__ __forceinline__ uint32_t pack_high(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// 8 elements at p (16-byte aligned) as floats
+template <bool F32>
+__device__ __forceinline__ void load8(const void *p, float *x) {
+  if constexpr (F32) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    x[0] = bf16_lo(u.x), x[1] = bf16_hi(u.x), x[2] = bf16_lo(u.y), x[3] = bf16_hi(u.y);
+    x[4] = bf16_lo(u.z), x[5] = bf16_hi(u.z), x[6] = bf16_lo(u.w), x[7] = bf16_hi(u.w);
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void *p, const float *x) {
+  if constexpr (F32) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4 *>(p) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  }
+}
+
+// ------------------------------------------------------------ cache write / read
+
+template <int FMT> __host__ __device__ constexpr int row_bytes(int d) {
+  return FMT == GLQ_KV_BF16 ? 2 * d : FMT == GLQ_KV_INT8 ? d : d / 2;
+}
+
+struct KvIo {
+  void *cache[2];              // keys, values
+  float *scale[2];
+  void *dense[2];              // [tokens][heads][d], rows stride[] elements apart
+  int64_t stride[2];
+  const int32_t *slots;
+  int64_t tokens;
+  int32_t heads, page_shift;
+  uint32_t capacity;           // slots in the cache
+};
+
+// cache row of head h at a slot (rows are [page][head][token of the page])
+__device__ __forceinline__ int64_t cache_row(uint32_t slot, int h, int heads, int page_shift) {
+  const uint32_t page = slot >> page_shift, at = slot & ((1u << page_shift) - 1);
+  return (((int64_t)page * heads + h) << page_shift) + at;
+}
+
+// One lane holds 8 elements of one (token, head) row, d / 8 lanes a row; keys
+// in grid y = 0, values in y = 1. a = max |x| is taken on the bit patterns, so a
+// NaN is the largest and reaches the scale.
+template <int FMT, int D, bool F32>
+__global__ void __launch_bounds__(256) kv_append_k(KvIo io) {
+  constexpr int LPR = D / 8;
+  const int which = blockIdx.y;
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+  const int at = threadIdx.x % LPR;
+  if (row >= io.tokens * io.heads) return;           // whole rows leave together
+  const int64_t token = row / io.heads;
+  const int h = (int)(row - token * io.heads);
+  const uint32_t slot = (uint32_t)io.slots[token];
+  if (slot >= io.capacity) return;
+  const int64_t esize = F32 ? 4 : 2;
+  float x[8];
+  load8<F32>(reinterpret_cast<const uint8_t *>(io.dense[which]) +
+                 esize * (token * io.stride[which] + (int64_t)h * D + 8 * at), x);
+  const int64_t cr = cache_row(slot, h, io.heads, io.page_shift);
+  uint8_t *out = reinterpret_cast<uint8_t *>(io.cache[which]) + cr * row_bytes<FMT>(D);
+  if constexpr (FMT == GLQ_KV_BF16) {
+    store8<false>(out + 16 * at, x);
+  } else {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+      top = b > top ? b : top;
+    }
+#pragma unroll
+    for (int s = 1; s < LPR; s <<= 1) {
+      const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
+      top = o > top ? o : top;
+    }
+    constexpr float Q = FMT == GLQ_KV_INT8 ? 127.0f : 7.0f;
+    const float a = __uint_as_float(top);
+    // x Q must not overflow: both sides of the quotient are scaled by 2^-32
+    // (exact; what leaves the float range there has code 0 anyway)
+    const float pre = a > 0x1p100f ? 0x1p-32f : 1.0f;
+    const bool codes = top > 0 && top < 0x7F800000u;  // a = 0, inf and NaN have codes 0
+    const float div = codes ? a * pre : 1.0f;
+    int q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = codes ? __float2int_rn(x[i] * pre * Q / div) : 0;
+    if constexpr (FMT == GLQ_KV_INT8) {
+      uint32_t lo = 0, hi = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo |= (uint32_t)(q[i] & 255) << (8 * i);
+        hi |= (uint32_t)(q[4 + i] & 255) << (8 * i);
+      }
+      *reinterpret_cast<uint2 *>(out + 8 * at) = make_uint2(lo, hi);
+    } else {
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w |= (uint32_t)(q[i] + 8) << (4 * i);
+      *reinterpret_cast<uint32_t *>(out + 4 * at) = w;
+    }
+    if (at == 0) io.scale[which][cr] = a / Q;
+  }
+}
+
+// The other way: 8 elements a lane, a slot outside the cache gives zeros.
+template <int FMT, int D, bool F32>
+__global__ void __launch_bounds__(256) kv_read_k(KvIo io) {
+  constexpr int LPR = D / 8;
+  const int which = blockIdx.y;
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+  const int at = threadIdx.x % LPR;
+  if (row >= io.tokens * io.heads) return;
+  const int64_t token = row / io.heads;
+  const int h = (int)(row - token * io.heads);
+  const uint32_t slot = (uint32_t)io.slots[token];
+  float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (slot < io.capacity) {
+    const int64_t cr = cache_row(slot, h, io.heads, io.page_shift);
+    const uint8_t *in = reinterpret_cast<const uint8_t *>(io.cache[which]) + cr * row_bytes<FMT>(D);
+    if constexpr (FMT == GLQ_KV_BF16) {
+      load8<false>(in + 16 * at, x);
+    } else {
+      const float s = io.scale[which][cr];
+      if constexpr (FMT == GLQ_KV_INT8) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(in + 8 * at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = (float)(int8_t)(w.x >> (8 * i)) * s;
+          x[4 + i] = (float)(int8_t)(w.y >> (8 * i)) * s;
+        }
+      } else {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(in + 4 * at);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (float)((int)((w >> (4 * i)) & 15u) - 8) * s;
+      }
+    }
+  }
+  const int64_t esize = F32 ? 4 : 2;
+  store8<F32>(reinterpret_cast<uint8_t *>(io.dense[which]) +
+                  esize * (token * io.stride[which] + (int64_t)h * D + 8 * at), x);
+}
+
+// ------------------------------------------------------------ one new token
+
+struct DecodeArgs {
+  const void *k, *v;
+  const float *ks, *vs;
+  const void *q;
+  void *out;
+  int64_t q_stride, out_stride;
+  const int32_t *table, *lens;
+  int64_t max_pages, max_len;
+  int32_t heads, group, row_tiles, page_shift, num_pages;
+  float scale2;                // scale * log2(e)
+};
+
+// The wave works on tiles of 32 cached tokens, two 16-token halves. Scores
+// are taken transposed, S^T = K Q^T (16x16x32 products, A = 16 tokens, B = the
+// group's query heads padded to 16): lane (g, n) = (lane >> 4, lane & 15) then
+// holds head n's scores of tokens 4 g .. 4 g + 3 of each half, which is the B
+// operand of O^T = V^T P^T as it stands if its 8 k-slots mean those 8 tokens.
+// V^T's A operand wants the same 8 tokens of one dimension a lane: the lane
+// loads D / 16 neighbouring dimensions of each of its 8 tokens (whole rows per
+// load) and puts pairs of tokens together in registers, so nothing passes
+// through LDS until the waves join.
+template <int FMT, int D> struct Tile {
+  static constexpr int RB = row_bytes<FMT>(D);
+  static constexpr int KW = RB / 16;                 // dwords of K per lane and half
+  static constexpr int VB = RB / 16;                 // bytes of V per lane and token
+  static constexpr int VW = VB < 4 ? 1 : VB / 4;
+  uint32_t k[2][KW], v[8][VW];
+  float ks[8], vs[8];
+};
+
+// dimension of element e of k-step c in quarter g (the order in which a lane's K
+// bytes come out; Q is loaded in the same order)
+template <int FMT, int D> __device__ __forceinline__ int k_dim(int c, int g, int e) {
+  if constexpr (FMT == GLQ_KV_BF16) return 32 * c + 8 * g + e;
+  if constexpr (FMT == GLQ_KV_INT8) return 64 * (c >> 1) + 16 * g + 8 * (c & 1) + e;
+  const int o = (e >> 1) + 4 * (e & 1);              // pairs of nibbles 4 apart
+  if constexpr (D == 64) return 16 * g + 8 * c + o;
+  return 128 * (c >> 2) + 32 * g + 8 * (c & 3) + o;
+}
+
+template <int N> __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
+      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void load_tile(const DecodeArgs &a, const int32_t *table, int h, int lane, int t, int end,
+                                          Tile<FMT, D> &x) {
+  using T = Tile<FMT, D>;
+  const int g = lane >> 4, n = lane & 15;
+  const uint8_t *kp = reinterpret_cast<const uint8_t *>(a.k), *vp = reinterpret_cast<const uint8_t *>(a.v);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int ts = t + 16 * s < end ? t + 16 * s : t;          // a half past the end repeats the first
+    uint32_t page = (uint32_t)table[ts >> a.page_shift];
+    page = page < (uint32_t)a.num_pages ? page : (int32_t)page < 0 ? 0u : (uint32_t)a.num_pages - 1;
+    const int64_t row = (((int64_t)page * a.heads + h) << a.page_shift) + (ts & ((1 << a.page_shift) - 1));
+    const uint8_t *kr = kp + (row + n) * T::RB;
+    if constexpr (T::RB >= 64) {
+#pragma unroll
+      for (int i = 0; i < T::RB / 64; ++i) load_words<4>(kr + 64 * i + 16 * g, &x.k[s][4 * i]);
+    } else {
+      load_words<2>(kr + 8 * g, x.k[s]);
+    }
+    const uint8_t *vr = vp + (row + 4 * g) * T::RB + n * T::VB;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if constexpr (T::VB == 2) x.v[4 * s + r][0] = *reinterpret_cast<const uint16_t *>(vr + r * T::RB);
+      else load_words<T::VW>(vr + r * T::RB, x.v[4 * s + r]);
+    }
+    if constexpr (FMT != GLQ_KV_BF16) {
+      const float4 u = *reinterpret_cast<const float4 *>(a.ks + row + 4 * g);
+      const float4 w = *reinterpret_cast<const float4 *>(a.vs + row + 4 * g);
+      x.ks[4 * s] = u.x, x.ks[4 * s + 1] = u.y, x.ks[4 * s + 2] = u.z, x.ks[4 * s + 3] = u.w;
+      x.vs[4 * s] = w.x, x.vs[4 * s + 1] = w.y, x.vs[4 * s + 2] = w.z, x.vs[4 * s + 3] = w.w;
+    }
+  }
+}
+
+// nibble j of each 16-bit half as bf16 16 + code + 8: the code's 4 bits go
+// into the top of the mantissa of 16
+__device__ __forceinline__ uint32_t nibbles(uint32_t x, int j) {
+  const uint32_t y = j == 0 ? x << 3 : x >> (4 * j - 3);
+  return (y & 0x00780078u) | 0x41804180u;
+}
+constexpr float kBias4 = 24.0f;                      // what nibbles() adds to a code
+// the same pair as the codes themselves (float32 path: the biased sums would
+// cost it a decimal digit)
+__device__ __forceinline__ uint32_t nibbles_unbiased(uint32_t x, int j) {
+  return pack_high((float)((x >> (4 * j)) & 15u) - 8.0f, (float)((x >> (16 + 4 * j)) & 15u) - 8.0f);
+}
+template <bool BIASED> __device__ __forceinline__ uint32_t nibble_pair(uint32_t x, int j) {
+  if constexpr (BIASED) return nibbles(x, j);
+  else return nibbles_unbiased(x, j);
+}
+
+template <int FMT, int D, bool BIASED>
+__device__ __forceinline__ bf16x8 k_operand(const Tile<FMT, D> &x, int s, int c) {
+  uint4 u;
+  if constexpr (FMT == GLQ_KV_BF16) {
+    u = make_uint4(x.k[s][4 * c], x.k[s][4 * c + 1], x.k[s][4 * c + 2], x.k[s][4 * c + 3]);
+  } else if constexpr (FMT == GLQ_KV_INT8) {
+    const uint32_t a = x.k[s][2 * c], b = x.k[s][2 * c + 1];
+    u.x = pack_high((float)(int8_t)a, (float)(int8_t)(a >> 8));
+    u.y = pack_high((float)(int8_t)(a >> 16), (float)(int8_t)(a >> 24));
+    u.z = pack_high((float)(int8_t)b, (float)(int8_t)(b >> 8));
+    u.w = pack_high((float)(int8_t)(b >> 16), (float)(int8_t)(b >> 24));
+  } else {
+    const uint32_t a = x.k[s][c];
+    u = make_uint4(nibble_pair<BIASED>(a, 0), nibble_pair<BIASED>(a, 1), nibble_pair<BIASED>(a, 2),
+                   nibble_pair<BIASED>(a, 3));
+  }
+  return __builtin_bit_cast(bf16x8, u);
+}
+
+// dimension n D / 16 + i of the lane's 8 tokens
+template <int FMT, int D, bool BIASED>
+__device__ __forceinline__ bf16x8 v_operand(const Tile<FMT, D> &x, int i) {
+  uint32_t u[4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    if constexpr (FMT == GLQ_KV_BF16) {
+      u[p] = __builtin_amdgcn_perm(x.v[2 * p + 1][i >> 1], x.v[2 * p][i >> 1], (i & 1) ? 0x07060302u : 0x05040100u);
+    } else if constexpr (FMT == GLQ_KV_INT8) {
+      const int sh = 8 * (i & 3);
+      u[p] = pack_high((float)(int8_t)(x.v[2 * p][i >> 2] >> sh), (float)(int8_t)(x.v[2 * p + 1][i >> 2] >> sh));
+    } else {
+      const uint32_t w = __builtin_amdgcn_perm(x.v[2 * p + 1][i >> 3], x.v[2 * p][i >> 3],
+                                               (i & 4) ? 0x07060302u : 0x05040100u);
+      u[p] = nibble_pair<BIASED>(w, i & 3);
+    }
+  }
+  return __builtin_bit_cast(bf16x8, make_uint4(u[0], u[1], u[2], u[3]));
+}
+
+// 8 floats as NP bf16 operands whose sum they are (1: rounded to nearest even; 2:
+// 16 bits; 3: all 24). The cache is what this kernel waits for, so the weights of
+// the bf16 path take two parts as well: few tokens, or a few that outweigh
+// the rest, would show the 2^-8 of one.
+template <int NP>
+__device__ __forceinline__ void split8(const float *x, bf16x8 *o) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u[i] = pack_bf16(r[2 * i], r[2 * i + 1]);
+      if (p + 1 < NP) r[2 * i] -= bf16_lo(u[i]), r[2 * i + 1] -= bf16_hi(u[i]);
+    }
+    o[p] = __builtin_bit_cast(bf16x8, make_uint4(u[0], u[1], u[2], u[3]));
+  }
+}
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+template <int FMT, int D, bool F32>
+__global__ void __launch_bounds__(256) attn_decode_k(DecodeArgs a) {
+  constexpr int NP = F32 ? 3 : 1, KS = D / 32, DT = D / 16;
+  constexpr int WP = F32 ? 3 : 2;                    // bf16 parts of a weight
+  constexpr bool BIASED = FMT == GLQ_KV_INT4 && !F32;
+  extern __shared__ float shm[];                     // [4][16][D] sums, [4][16] maxima, [4][16] totals
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, n = lane & 15;
+  const int unit = blockIdx.x, rt = unit % a.row_tiles, bh = unit / a.row_tiles;
+  const int h = bh % a.heads;
+  const int64_t b = bh / a.heads;
+  const int32_t *table = a.table + b * a.max_pages;
+  const int head0 = h * a.group + 16 * rt, rows = min(16, a.group - 16 * rt);
+  int len = __builtin_amdgcn_readfirstlane(a.lens[b]);
+  len = len < 0 ? 0 : len > a.max_len ? (int)a.max_len : len;
+
+  const int64_t esize = F32 ? 4 : 2;
+  bf16x8 q[NP][KS];
+  float qsum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < KS; ++c) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint8_t *p = reinterpret_cast<const uint8_t *>(a.q) +
+                         esize * (b * a.q_stride + (int64_t)(head0 + (n < rows ? n : 0)) * D + k_dim<FMT, D>(c, g, e));
+      x[e] = F32 ? *reinterpret_cast<const float *>(p) : bf16_lo(*reinterpret_cast<const uint16_t *>(p));
+      qsum += x[e];
+    }
+    bf16x8 o[NP];
+    split8<NP>(x, o);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) q[p][c] = o[p];
+  }
+  qsum += __shfl_xor(qsum, 16);
+  qsum += __shfl_xor(qsum, 32);
+  const float s0 = BIASED ? -kBias4 * qsum : 0.0f;
+
+  float m = -INFINITY, l = 0.0f;
+  f32x4 acc[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) acc[i] = (f32x4){0, 0, 0, 0};
+
+  for (int t = 32 * wave; t < len; t += 128) {
+    Tile<FMT, D> x;
+    load_tile<FMT, D>(a, table, h, lane, t, len, x);
+    const bool tail = t + 32 > len;
+    float s[8];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      f32x4 c4 = {s0, s0, s0, s0};
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        const bf16x8 kk = k_operand<FMT, D, BIASED>(x, half, c);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) c4 = mfma16(kk, q[p][c], c4);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        s[4 * half + r] = c4[r] * (FMT == GLQ_KV_BF16 ? a.scale2 : a.scale2 * x.ks[4 * half + r]);
+    }
+    if (tail) {                                      // tokens past the end: no weight, and values that are 0
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = t + 16 * (j >> 2) + 4 * g + (j & 3) < len;
+        s[j] = in ? s[j] : -INFINITY;
+        x.vs[j] = in ? x.vs[j] : 0.0f;
+        if constexpr (FMT == GLQ_KV_BF16) {
+#pragma unroll
+          for (int w = 0; w < Tile<FMT, D>::VW; ++w) x.v[j][w] = in ? x.v[j][w] : 0u;
+        }
+      }
+    }
+    float mt = s[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) mt = fmaxf(mt, s[j]);
+    mt = fmaxf(mt, __shfl_xor(mt, 16));
+    mt = fmaxf(mt, __shfl_xor(mt, 32));
+    const float mn = fmaxf(m, mt), base = mn == -INFINITY ? 0.0f : mn;
+    const float alpha = __builtin_amdgcn_exp2f(m - base);
+    m = mn;
+    l *= alpha;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) acc[i] *= alpha;
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[j] = __builtin_amdgcn_exp2f(s[j] - base);
+      l += w[j];
+      if constexpr (FMT != GLQ_KV_BF16) w[j] *= x.vs[j];
+    }
+    bf16x8 pw[WP];
+    split8<WP>(w, pw);
+    const uint32_t nb = 0xC1C0C1C0u;                 // -kBias4 twice
+    const bf16x8 bias = __builtin_bit_cast(bf16x8, make_uint4(nb, nb, nb, nb));
+#pragma unroll
+    for (int i = 0; i < DT; ++i) {
+      const bf16x8 vv = v_operand<FMT, D, BIASED>(x, i);
+#pragma unroll
+      for (int p = 0; p < WP; ++p) {
+        // the 4-bit operand's bias leaves at once, tile by tile: over a long
+        // cache the biased sums would outgrow the result they hide
+        if constexpr (BIASED) acc[i] = mfma16(bias, pw[p], acc[i]);
+        acc[i] = mfma16(vv, pw[p], acc[i]);
+      }
+    }
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+
+  // join the waves
+  float *so = shm, *sm = shm + 4 * 16 * D, *sl = sm + 64;
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) so[(wave * 16 + n) * D + (4 * g + r) * DT + i] = acc[i][r];
+  if (g == 0) sm[16 * wave + n] = m, sl[16 * wave + n] = l;
+  __syncthreads();
+  for (int e = threadIdx.x; e < rows * (D / 8); e += 256) {
+    const int row = e / (D / 8), d0 = 8 * (e % (D / 8));
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, sm[16 * w + row]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float total = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = __builtin_amdgcn_exp2f(sm[16 * w + row] - base);
+      total += f * sl[16 * w + row];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] += f * so[(16 * w + row) * D + d0 + i];
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= inv;
+    store8<F32>(reinterpret_cast<uint8_t *>(a.out) + esize * (b * a.out_stride + (int64_t)(head0 + row) * D + d0), o);
+  }
+}
+
+// ------------------------------------------------------------ prompts
+
+struct PromptArgs {
+  const void *q, *k, *v;
+  void *out;
+  int64_t q_stride, k_stride, v_stride, out_stride, total_q, total_k;
+  const int32_t *cu_q, *cu_k;
+  int32_t q_heads, kv_heads, q_tiles, causal;
+  float scale2;
+};
+
+__device__ __forceinline__ int clamped(int x, int64_t top) { return x < 0 ? 0 : x > top ? (int)top : x; }
+
+template <bool F32> __device__ __forceinline__ float4 load4(const void *p, int64_t at) {
+  if constexpr (F32) return *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + at);
+  const uint2 u = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + at);
+  return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+}
+
+// A weight of 0 times a value that is not finite is NaN, and would reach
+// queries that do not see the key. In a tile with such pairs the values that
+// are not finite become 0, and the queries that do see one get NaN.
+__device__ __forceinline__ void keep_unseen_out(float4 &x, bool seen, f32x4 *acc) {
+  float *v = reinterpret_cast<float *>(&x);
+  bool bad = false;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) bad |= !(fabsf(v[c]) < INFINITY);
+  if (!__any(bad)) return;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const bool b = !(fabsf(v[c]) < INFINITY);
+    v[c] = b ? 0.0f : v[c];
+    const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x4f32(b ? 1.0f : 0.0f, seen ? 1.0f : 0.0f, (f32x4){0, 0, 0, 0},
+                                                           0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[c][r] = hit[r] > 0.0f ? NAN : acc[c][r];
+  }
+}
+
+// A wave takes 16 queries of one head against 16 keys at a time with float32
+// 16x16x4 products, transposed as in the decode kernel: S^T = K Q^T leaves lane
+// (g, n) query n's scores of keys 4 g + r, the B operand of the r-th step of
+// O^T = V^T P^T. k-slot g of step 4 i + r of the scores means dimension 16 i +
+// 4 g + r, row n of value tile (i, c) means dimension 64 i + 4 n + c: both are 16-byte loads.
+template <int D, bool F32>
+__global__ void __launch_bounds__(256) attn_prompt_k(PromptArgs a) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, n = lane & 15;
+  const int tile = blockIdx.x % a.q_tiles;
+  const int bh = blockIdx.x / a.q_tiles, head = bh % a.q_heads;
+  const int64_t b = bh / a.q_heads;
+  const int q0 = clamped(a.cu_q[b], a.total_q), q1 = clamped(a.cu_q[b + 1], a.total_q);
+  const int k0 = clamped(a.cu_k[b], a.total_k), k1 = clamped(a.cu_k[b + 1], a.total_k);
+  const int lq = q1 - q0, lk = k1 - k0 > 0 ? k1 - k0 : 0;
+  const int row0 = 64 * tile + 16 * wave;
+  if (row0 >= lq) return;
+  const int row = row0 + n < lq ? row0 + n : lq - 1;
+  const int kvh = head / (a.q_heads / a.kv_heads);
+  float4 q[D / 16];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+    q[i] = load4<F32>(a.q, (int64_t)(q0 + row) * a.q_stride + (int64_t)head * D + 16 * i + 4 * g);
+  const int shift = lk - lq;
+  const int last = a.causal ? row + shift : lk - 1;  // this lane's last key
+  int end = a.causal ? row0 + 16 + shift : lk;       // keys any query of the wave sees
+  end = end < lk ? end : lk;
+  f32x4 acc[D / 16];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) acc[i] = (f32x4){0, 0, 0, 0};
+  float m = -INFINITY, l = 0.0f;
+  for (int j0 = 0; j0 < end; j0 += 16) {
+    const int kr = j0 + n < lk ? j0 + n : lk - 1;
+    f32x4 s = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const float4 x = load4<F32>(a.k, (int64_t)(k0 + kr) * a.k_stride + (int64_t)kvh * D + 16 * i + 4 * g);
+      s = __builtin_amdgcn_mfma_f32_16x16x4f32(x.x, q[i].x, s, 0, 0, 0);
+      s = __builtin_amdgcn_mfma_f32_16x16x4f32(x.y, q[i].y, s, 0, 0, 0);
+      s = __builtin_amdgcn_mfma_f32_16x16x4f32(x.z, q[i].z, s, 0, 0, 0);
+      s = __builtin_amdgcn_mfma_f32_16x16x4f32(x.w, q[i].w, s, 0, 0, 0);
+    }
+    float mt = -INFINITY;
+    bool seen[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int j = j0 + 4 * g + r;
+      seen[r] = j <= last && j < lk;
+      s[r] = seen[r] ? s[r] * a.scale2 : -INFINITY;
+      mt = fmaxf(mt, s[r]);
+    }
+    const bool masked = a.causal && j0 + 15 > row0 + shift;     // some query does not see some key
+    mt = fmaxf(mt, __shfl_xor(mt, 16));
+    mt = fmaxf(mt, __shfl_xor(mt, 32));
+    const float mn = fmaxf(m, mt), base = mn == -INFINITY ? 0.0f : mn;
+    const float alpha = __builtin_amdgcn_exp2f(m - base);
+    m = mn;
+    l *= alpha;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) acc[i] *= alpha;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float p = __builtin_amdgcn_exp2f(s[r] - base);
+      l += p;
+      const int j = j0 + 4 * g + r;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        float4 x = load4<F32>(a.v, (int64_t)(k0 + (j < lk ? j : lk - 1)) * a.v_stride + (int64_t)kvh * D + 64 * i + 4 * n);
+        if (j >= lk) x = make_float4(0, 0, 0, 0);
+        if (masked) keep_unseen_out(x, seen[r], &acc[4 * i]);
+        acc[4 * i] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.x, p, acc[4 * i], 0, 0, 0);
+        acc[4 * i + 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.y, p, acc[4 * i + 1], 0, 0, 0);
+        acc[4 * i + 2] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.z, p, acc[4 * i + 2], 0, 0, 0);
+        acc[4 * i + 3] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.w, p, acc[4 * i + 3], 0, 0, 0);
+      }
+    }
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (row0 + n >= lq) return;
+  const int64_t o0 = (int64_t)(q0 + row) * a.out_stride + (int64_t)head * D;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t at = o0 + 64 * i + 4 * (4 * g + r);
+      const float x = acc[4 * i][r] * inv, y = acc[4 * i + 1][r] * inv, z = acc[4 * i + 2][r] * inv,
+                  w = acc[4 * i + 3][r] * inv;
+      if constexpr (F32) *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at) = make_float4(x, y, z, w);
+      else *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) =
+               make_uint2(pack_bf16(x, y), pack_bf16(z, w));
+    }
+}
+
+// ------------------------------------------------------------ argument checks
+
+bool valid_dtype(int dt) { return dt == GLQ_F32 || dt == GLQ_BF16; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool valid_dim(int d) { return d == 64 || d == 128 || d == 256; }
+int log2_of(int x) { return 31 - __builtin_clz((unsigned)x); }
+
+int check_cache(const glq_kv_cache *C) {
+  if (!C || C->format < GLQ_KV_BF16 || C->format > GLQ_KV_INT4) return GLQ_ERR_ARG;
+  if (C->kv_heads < 1 || C->num_pages < 1) return GLQ_ERR_ARG;
+  if (C->page_size < 16 || C->page_size > 1024 || (C->page_size & (C->page_size - 1))) return GLQ_ERR_ARG;
+  if (!C->k || !C->v || !aligned16(C->k) || !aligned16(C->v)) return GLQ_ERR_ARG;
+  if (C->format != GLQ_KV_BF16 && (!C->k_scale || !C->v_scale || !aligned16(C->k_scale) || !aligned16(C->v_scale)))
+    return GLQ_ERR_ARG;
+  if (!valid_dim(C->head_dim) || C->kv_heads > 65536) return GLQ_ERR_UNSUPPORTED;
+  if (C->num_pages > 0x7FFFFFFF / C->page_size) return GLQ_ERR_UNSUPPORTED;
+  return GLQ_OK;
+}
+
+// pointer and row stride (elements) of a [rows][heads][d] operand
+bool valid_rows(const void *p, int64_t stride, int64_t heads, int64_t d, int dt) {
+  const int64_t esize = dt == GLQ_F32 ? 4 : 2;
+  return p && aligned16(p) && stride >= heads * d && stride < (int64_t(1) << 40) && (stride * esize) % 16 == 0;
+}
+
+template <bool READ, int FMT, int D>
+int launch_kv(const KvIo &io, glq_dtype dt, hipStream_t st) {
+  const int64_t blocks = (io.tokens * io.heads * (D / 8) + 255) / 256;
+  if (blocks > 0x7FFFFFFF) return GLQ_ERR_UNSUPPORTED;
+  auto kern = READ ? (dt == GLQ_F32 ? kv_read_k<FMT, D, true> : kv_read_k<FMT, D, false>)
+                   : (dt == GLQ_F32 ? kv_append_k<FMT, D, true> : kv_append_k<FMT, D, false>);
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks, 2), dim3(256), 0, st, io);
+  return hip_status(hipGetLastError(), READ ? "kv_read_k" : "kv_append_k");
+}
+
+template <bool READ, int FMT>
+int launch_kv_dim(const KvIo &io, int d, glq_dtype dt, hipStream_t st) {
+  return d == 64 ? launch_kv<READ, FMT, 64>(io, dt, st) : d == 128 ? launch_kv<READ, FMT, 128>(io, dt, st)
+                                                                  : launch_kv<READ, FMT, 256>(io, dt, st);
+}
+
+template <bool READ>
+int kv_io(const glq_kv_cache *C, void *k, void *v, glq_dtype dt, int64_t k_stride, int64_t v_stride,
+          const int32_t *slots, int64_t tokens, void *hip_stream) {
+  const int rc = check_cache(C);
+  if (rc) return rc;
+  if (!valid_dtype(dt) || tokens < 0) return GLQ_ERR_ARG;
+  if (tokens == 0) return GLQ_OK;
+  if (!valid_rows(k, k_stride, C->kv_heads, C->head_dim, dt) || !valid_rows(v, v_stride, C->kv_heads, C->head_dim, dt) ||
+      !slots || (reinterpret_cast<uintptr_t>(slots) & 3))
+    return GLQ_ERR_ARG;
+  if (tokens > 0x7FFFFFFF) return GLQ_ERR_UNSUPPORTED;
+  const KvIo io = {{C->k, C->v}, {C->k_scale, C->v_scale}, {k, v}, {k_stride, v_stride}, slots, tokens, C->kv_heads,
+                   log2_of(C->page_size), (uint32_t)(C->num_pages * C->page_size)};
+  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  switch (C->format) {
+    case GLQ_KV_BF16: return launch_kv_dim<READ, GLQ_KV_BF16>(io, C->head_dim, dt, st);
+    case GLQ_KV_INT8: return launch_kv_dim<READ, GLQ_KV_INT8>(io, C->head_dim, dt, st);
+    default: return launch_kv_dim<READ, GLQ_KV_INT4>(io, C->head_dim, dt, st);
+  }
+}
+
+int check_decode(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t max_len) {
+  const int rc = check_cache(C);
+  if (rc) return rc;
+  if (batch < 0 || q_heads < 1 || q_heads % C->kv_heads || max_len < 0) return GLQ_ERR_ARG;
+  if (max_len > 0x7FFFFFFF - 4096 || q_heads > 65536) return GLQ_ERR_UNSUPPORTED;
+  const int64_t tiles = (q_heads / C->kv_heads + 15) / 16;
+  if (batch > 0x7FFFFFFF / ((int64_t)C->kv_heads * tiles)) return GLQ_ERR_UNSUPPORTED;
+  return GLQ_OK;
+}
+
+template <int FMT, int D>
+int launch_decode(const DecodeArgs &a, glq_dtype dt, int64_t units, hipStream_t st) {
+  const size_t shm = (4 * 16 * D + 128) * sizeof(float);
+  auto kern = dt == GLQ_F32 ? attn_decode_k<FMT, D, true> : attn_decode_k<FMT, D, false>;
+  if (shm > 64 * 1024) {
+    const int rc = hip_status(hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm),
+                              "hipFuncSetAttribute");
+    if (rc) return rc;
+  }
+  hipLaunchKernelGGL(kern, dim3((unsigned)units), dim3(256), shm, st, a);
+  return hip_status(hipGetLastError(), "attn_decode_k");
+}
+
+template <int FMT>
+int launch_decode_dim(const DecodeArgs &a, int d, glq_dtype dt, int64_t units, hipStream_t st) {
+  return d == 64 ? launch_decode<FMT, 64>(a, dt, units, st) : d == 128 ? launch_decode<FMT, 128>(a, dt, units, st)
+                                                                      : launch_decode<FMT, 256>(a, dt, units, st);
+}
+
+}  // namespace
+}  // namespace glq
+
+using namespace glq;
+
+extern "C" int glq_kv_append(const glq_kv_cache *C, const void *k, const void *v, glq_dtype dt, int64_t k_stride,
+                             int64_t v_stride, const int32_t *slots, int64_t tokens, void *hip_stream) {
+  return kv_io<false>(C, const_cast<void *>(k), const_cast<void *>(v), dt, k_stride, v_stride, slots, tokens,
+                      hip_stream);
+}
+
+extern "C" int glq_kv_read(const glq_kv_cache *C, const int32_t *slots, int64_t tokens, void *k, void *v,
+                           glq_dtype dt, int64_t k_stride, int64_t v_stride, void *hip_stream) {
+  return kv_io<true>(C, k, v, dt, k_stride, v_stride, slots, tokens, hip_stream);
+}
+
+extern "C" size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t max_len) {
+  if (check_decode(C, batch, q_heads, max_len)) return 0;
+  return GLQ_ATTN_CTRL_BYTES;
+}
+
+extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype dt, int64_t q_stride, int64_t batch,
+                               int32_t q_heads, const int32_t *page_table, int64_t max_pages, const int32_t *lens,
+                               int64_t max_len, float scale, void *out, int64_t out_stride, void *workspace,
+                               size_t ws_bytes, void *hip_stream) {
+  const int rc = check_decode(C, batch, q_heads, max_len);
+  if (rc) return rc;
+  if (!valid_dtype(dt) || !std::isfinite(scale) || max_pages < 0) return GLQ_ERR_ARG;
+  if (batch == 0) return GLQ_OK;
+  if (max_len > max_pages * C->page_size) return GLQ_ERR_ARG;
+  if (!valid_rows(q, q_stride, q_heads, C->head_dim, dt) || !valid_rows(out, out_stride, q_heads, C->head_dim, dt) ||
+      !lens || (!page_table && max_len > 0) || (reinterpret_cast<uintptr_t>(lens) & 3) ||
+      (reinterpret_cast<uintptr_t>(page_table) & 3))
+    return GLQ_ERR_ARG;
+  if (!workspace || ws_bytes < glq_attn_decode_workspace(C, batch, q_heads, max_len) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return GLQ_ERR_WORKSPACE;
+  const int32_t group = q_heads / C->kv_heads, tiles = (group + 15) / 16;
+  const DecodeArgs a = {C->k, C->v, C->k_scale, C->v_scale, q, out, q_stride, out_stride, page_table, lens, max_pages,
+                        max_len, C->kv_heads, group, tiles, log2_of(C->page_size), (int32_t)C->num_pages,
+                        scale * 1.4426950408889634f};
+  const int64_t units = batch * C->kv_heads * tiles;
+  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  switch (C->format) {
+    case GLQ_KV_BF16: return launch_decode_dim<GLQ_KV_BF16>(a, C->head_dim, dt, units, st);
+    case GLQ_KV_INT8: return launch_decode_dim<GLQ_KV_INT8>(a, C->head_dim, dt, units, st);
+    default: return launch_decode_dim<GLQ_KV_INT4>(a, C->head_dim, dt, units, st);
+  }
+}
+
+extern "C" int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_stream) {
+  if (!P || (flags & ~1u) || !valid_dtype(P->dt) || !std::isfinite(P->scale)) return GLQ_ERR_ARG;
+  if (P->q_heads < 1 || P->kv_heads < 1 || P->q_heads % P->kv_heads) return GLQ_ERR_ARG;
+  if (P->total_q < 0 || P->total_k < 0 || P->batch < 0 || P->max_q < 0) return GLQ_ERR_ARG;
+  if (!valid_dim(P->head_dim) || P->q_heads > 65536) return GLQ_ERR_UNSUPPORTED;
+  if (P->total_q > 0x7FFFFFFF || P->total_k > 0x7FFFFFFF) return GLQ_ERR_UNSUPPORTED;
+  if (P->batch == 0 || P->total_q == 0 || P->max_q == 0) return GLQ_OK;
+  if (!P->cu_q || !P->cu_k || (reinterpret_cast<uintptr_t>(P->cu_q) & 3) || (reinterpret_cast<uintptr_t>(P->cu_k) & 3))
+    return GLQ_ERR_ARG;
+  if (!valid_rows(P->q, P->q_stride, P->q_heads, P->head_dim, P->dt) ||
+      !valid_rows(P->out, P->out_stride, P->q_heads, P->head_dim, P->dt))
+    return GLQ_ERR_ARG;
+  if (P->total_k > 0 && (!valid_rows(P->k, P->k_stride, P->kv_heads, P->head_dim, P->dt) ||
+                         !valid_rows(P->v, P->v_stride, P->kv_heads, P->head_dim, P->dt)))
+    return GLQ_ERR_ARG;
+  const int64_t most = P->max_q < P->total_q ? P->max_q : P->total_q;
+  const int64_t tiles = (most + 63) / 64;
+  if (P->batch > 0x7FFFFFFF / (P->q_heads * tiles)) return GLQ_ERR_UNSUPPORTED;
+  const PromptArgs a = {P->q, P->k, P->v, P->out, P->q_stride, P->k_stride, P->v_stride, P->out_stride, P->total_q,
+                        P->total_k, P->cu_q, P->cu_k, P->q_heads, P->kv_heads, (int32_t)tiles,
+                        (flags & GLQ_ATTN_CAUSAL) ? 1 : 0, P->scale * 1.4426950408889634f};
+  const bool f = P->dt == GLQ_F32;
+  auto kern = P->head_dim == 64 ? (f ? attn_prompt_k<64, true> : attn_prompt_k<64, false>)
+              : P->head_dim == 128 ? (f ? attn_prompt_k<128, true> : attn_prompt_k<128, false>)
+                                   : (f ? attn_prompt_k<256, true> : attn_prompt_k<256, false>);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(P->batch * P->q_heads * tiles)), dim3(256), 0,
+                     reinterpret_cast<hipStream_t>(hip_stream), a);
+  return hip_status(hipGetLastError(), "attn_prompt_k");
+}

@@ -20,12 +20,15 @@ GLQ_OK, GLQ_ERR_ARG, GLQ_ERR_UNSUPPORTED, GLQ_ERR_HIP, GLQ_ERR_WORKSPACE = 0, -1
 GLQ_F32, GLQ_BF16 = 0, 1
 GLQ_CB_INT8_2X, GLQ_CB_DEVICE = 0, 1
 FLAG_NO_INPUT_RHT, FLAG_NO_OUTPUT_RHT = 1, 2
+KV_BF16, KV_INT8, KV_INT4 = 0, 1, 2
+ATTN_CAUSAL = 1
 
 EXPORTS = ("glq_build_codebook", "glq_encode_ref", "glq_encode_ldlq", "glq_rht_apply", "glq_decode_weights",
            "glq_fused_linear_workspace", "glq_fused_linear", "glq_fused_linear_noalloc", "glq_status_string",
            "glq_last_error",
            "glq_version", "glq_ep_encode", "glq_ep_build_lut", "glq_ep_decode_weights",
-           "glq_ep_fused_linear_workspace", "glq_ep_fused_linear")
+           "glq_ep_fused_linear_workspace", "glq_ep_fused_linear", "glq_kv_append", "glq_kv_read",
+           "glq_attn_decode_workspace", "glq_attn_decode", "glq_attn_prompt")
 EP_LANES, EP_TABLES, EP_MAX_SYMS = 64, 5, 256
 EP_LUT_BYTES = 64 + EP_TABLES * 2048 * 4
 
@@ -60,6 +63,18 @@ class EpLayerStruct(ctypes.Structure):
                 ("sign_k", _vp), ("sign_n", _vp)]
 
 
+class KvCacheStruct(ctypes.Structure):
+    _fields_ = [("format", _i32), ("kv_heads", _i32), ("head_dim", _i32), ("page_size", _i32), ("num_pages", _i64),
+                ("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp)]
+
+
+class PromptStruct(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("out", _vp), ("dt", _i32), ("q_heads", _i32),
+                ("kv_heads", _i32), ("head_dim", _i32), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64),
+                ("out_stride", _i64), ("total_q", _i64), ("total_k", _i64), ("batch", _i64), ("cu_q", _vp),
+                ("cu_k", _vp), ("max_q", _i64), ("scale", _f32)]
+
+
 _lib.glq_build_codebook.argtypes = [_i32, _vp, _sz, ctypes.POINTER(_sz)]
 _lib.glq_encode_ref.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _f32, ctypes.POINTER(_f32), _vp, _vp, _i32, _vp]
 _lib.glq_encode_ldlq.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _vp, ctypes.c_double, _f32,
@@ -79,13 +94,21 @@ _lib.glq_ep_decode_weights.argtypes = [ctypes.POINTER(EpLayerStruct), _vp, _i32,
 _lib.glq_ep_fused_linear_workspace.argtypes = [ctypes.POINTER(EpLayerStruct), _i64]
 _lib.glq_ep_fused_linear_workspace.restype = _sz
 _lib.glq_ep_fused_linear.argtypes = [ctypes.POINTER(EpLayerStruct), _vp, _i32, _i64, _vp, _i32, _vp, _sz, _u32, _vp]
+_kvc = ctypes.POINTER(KvCacheStruct)
+_lib.glq_kv_append.argtypes = [_kvc, _vp, _vp, _i32, _i64, _i64, _vp, _i64, _vp]
+_lib.glq_kv_read.argtypes = [_kvc, _vp, _i64, _vp, _vp, _i32, _i64, _i64, _vp]
+_lib.glq_attn_decode_workspace.argtypes = [_kvc, _i64, _i32, _i64]
+_lib.glq_attn_decode_workspace.restype = _sz
+_lib.glq_attn_decode.argtypes = [_kvc, _vp, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _f32, _vp, _i64, _vp, _sz,
+                                 _vp]
+_lib.glq_attn_prompt.argtypes = [ctypes.POINTER(PromptStruct), _u32, _vp]
 _lib.glq_status_string.argtypes = [_i32]
 _lib.glq_status_string.restype = ctypes.c_char_p
 _lib.glq_version.restype = _u32
 _lib.glq_last_error.restype = ctypes.c_char_p
 for _name in ("glq_build_codebook", "glq_encode_ref", "glq_encode_ldlq", "glq_rht_apply", "glq_decode_weights",
               "glq_fused_linear", "glq_ep_encode", "glq_ep_build_lut", "glq_ep_decode_weights",
-              "glq_ep_fused_linear"):
+              "glq_ep_fused_linear", "glq_kv_append", "glq_kv_read", "glq_attn_decode", "glq_attn_prompt"):
     getattr(_lib, _name).restype = ctypes.c_int
 
 
@@ -552,3 +575,180 @@ def fused_linear(layer: Layer, x, y, workspace, flags: int = 0, stream=None):
                                flags, _stream_ptr(stream))
     _check(rc, "glq_fused_linear")
     return y
+
+
+# ------------------------------------------------------- attention and its cache
+
+_HEAD_DIMS = (64, 128, 256)
+
+
+class KvCache:
+    """Device tensors of a paged key-value cache, and its glq_kv_cache struct.
+
+    k, v: [num_pages, kv_heads, page_size, row], bfloat16 rows of head_dim,
+    int8 rows of head_dim codes, or uint8 rows of head_dim / 2 (two 4-bit codes
+    a byte); k_scale, v_scale: float32 [num_pages, kv_heads, page_size], None
+    for bfloat16. The tensors are checked here once: keep them as they are.
+    """
+    k: object
+    k_scale: object
+    v: object
+    v_scale: object
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        torch = _torch()
+        if getattr(k, "dim", lambda: 0)() != 4:
+            raise ValueError("k: must be [num_pages, kv_heads, page_size, row]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        formats = {torch.bfloat16: KV_BF16, torch.int8: KV_INT8, torch.uint8: KV_INT4}
+        if k.dtype not in formats:
+            raise ValueError(f"k: dtype {k.dtype}, expected one of {tuple(formats)}")
+        self.format = formats[k.dtype]
+        self.num_pages, self.kv_heads, self.page_size, row = k.shape
+        self.head_dim = 2 * row if self.format == KV_INT4 else row
+        if self.head_dim not in _HEAD_DIMS:
+            raise ValueError(f"k: head_dim {self.head_dim}, expected one of {_HEAD_DIMS}")
+        if self.page_size not in (16, 32, 64, 128, 256, 512, 1024):
+            raise ValueError(f"k: page_size {self.page_size}, expected a power of two from 16 to 1024")
+        dev = self.device = _dev_tensor(k, "k").device
+        _dev_tensor(v, "v", dev, shape=k.shape, dtypes=(k.dtype,))
+        for s, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if self.format != KV_BF16:
+                _dev_tensor(s, nm, dev, shape=k.shape[:3], dtypes=(torch.float32,))
+            elif s is not None:
+                raise ValueError(f"{nm}: must be None for a bfloat16 cache")
+        for t, nm in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None and t.data_ptr() % 16:
+                raise ValueError(f"{nm}: must be 16-byte aligned")
+        self._st = KvCacheStruct(self.format, self.kv_heads, self.head_dim, self.page_size, self.num_pages,
+                                 k.data_ptr(), v.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
+                                 0 if v_scale is None else v_scale.data_ptr())
+
+    def struct(self) -> KvCacheStruct:
+        return self._st
+
+    @staticmethod
+    def empty(num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int, device="cuda") -> "KvCache":
+        """A zeroed cache of the format KV_BF16, KV_INT8 or KV_INT4."""
+        torch = _torch()
+        if fmt not in (KV_BF16, KV_INT8, KV_INT4):
+            raise ValueError(f"fmt: {fmt}, expected KV_BF16, KV_INT8 or KV_INT4")
+        dtype = {KV_BF16: torch.bfloat16, KV_INT8: torch.int8, KV_INT4: torch.uint8}[fmt]
+        shape = (num_pages, kv_heads, page_size, head_dim // 2 if fmt == KV_INT4 else head_dim)
+        k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+        if fmt == KV_BF16:
+            return KvCache(k, v)
+        ks, vs = (torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
+        return KvCache(k, v, ks, vs)
+
+
+def _rows(t, name, device, heads, dim, dtype=None, total=None):
+    """A [rows, heads, head_dim] operand: heads dense, rows any 16-byte multiple
+    apart. Returns the row stride in elements."""
+    torch = _torch()
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name}: must be a device (cuda) tensor")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.dtype is not dtype if dtype is not None else t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype or 'float32 or bfloat16'}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or (total is not None and shape[0] != total):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected ({'rows' if total is None else total}, {heads}, {dim})")
+    step, sh, sd = t.stride()
+    if sd != 1 or (heads > 1 and sh != dim):
+        raise ValueError(f"{name}: heads of one row must be dense")
+    if shape[0] <= 1 or step == 0 and shape[0] == 0:
+        step = heads * dim                               # a single row has no stride of its own
+    if step < heads * dim or (step * t.element_size()) % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{name}: rows must not overlap and start at multiples of 16 bytes")
+    return step
+
+
+def _ints(t, name, device, shape):
+    torch = _torch()
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name}: must be a device (cuda) tensor")
+    if t.device != device or t.dtype is not torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected dense int32 {shape} on {device}")
+    return t.data_ptr()
+
+
+def _kv_args(cache, k, v, slots):
+    ks = _rows(k, "k", cache.device, cache.kv_heads, cache.head_dim)
+    vs = _rows(v, "v", cache.device, cache.kv_heads, cache.head_dim, k.dtype, k.shape[0])
+    return ks, vs, _ints(slots, "slots", cache.device, (k.shape[0],))
+
+
+def kv_append(cache: KvCache, k, v, slots, stream=None):
+    """Write the tokens' keys and values [tokens, kv_heads, head_dim] into the
+    cache at int32 slots [tokens] (page * page_size + row; a slot outside the
+    cache drops its token) (glq_kv_append)."""
+    ks, vs, sp = _kv_args(cache, k, v, slots)
+    _check(_lib.glq_kv_append(ctypes.byref(cache._st), k.data_ptr(), v.data_ptr(), _dtype_code(k), ks, vs, sp,
+                              k.shape[0], _stream_ptr(stream)), "glq_kv_append")
+
+
+def kv_read(cache: KvCache, slots, k, v, stream=None):
+    """Read the tokens at the slots back into k and v [tokens, kv_heads,
+    head_dim], float32 or bfloat16 (glq_kv_read)."""
+    ks, vs, sp = _kv_args(cache, k, v, slots)
+    _check(_lib.glq_kv_read(ctypes.byref(cache._st), sp, k.shape[0], k.data_ptr(), v.data_ptr(), _dtype_code(k), ks,
+                            vs, _stream_ptr(stream)), "glq_kv_read")
+    return k, v
+
+
+def attn_decode_workspace_bytes(cache: KvCache, batch: int, q_heads: int, max_len: int) -> int:
+    return int(_lib.glq_attn_decode_workspace(ctypes.byref(cache._st), batch, q_heads, max_len))
+
+
+def attn_decode(cache: KvCache, q, page_table, lens, out, workspace, max_len: int, scale=None, stream=None):
+    """Attention of one new token per sequence, q and out [batch, q_heads,
+    head_dim], over the cached tokens t < lens[b] of the pages page_table[b]
+    (int32 [batch, max_pages]); max_len bounds lens. workspace: uint8, zeroed
+    once, attn_decode_workspace_bytes (glq_attn_decode). scale: 1 / sqrt(head_dim)
+    unless given."""
+    dev, dim = cache.device, cache.head_dim
+    if len(q.shape) != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected (batch, q_heads, {dim})")
+    batch, heads = q.shape[0], q.shape[1]
+    qs = _rows(q, "q", dev, heads, dim)
+    os_ = _rows(out, "out", dev, heads, dim, q.dtype, batch)
+    lp = _ints(lens, "lens", dev, (batch,))
+    pages = page_table.shape[-1]
+    tp = _ints(page_table, "page_table", dev, (batch, pages))
+    if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous on {dev}")
+    rc = _lib.glq_attn_decode(ctypes.byref(cache._st), q.data_ptr(), _dtype_code(q), qs, batch, heads, tp, pages, lp,
+                              max_len, dim ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+                              workspace.data_ptr(), _nbytes(workspace), _stream_ptr(stream))
+    _check(rc, "glq_attn_decode")
+    return out
+
+
+def attn_prompt(q, k, v, out, cu_q, cu_k=None, max_q: int | None = None, causal: bool = True, scale=None,
+                stream=None):
+    """Attention of packed prompts: q and out [total_q, q_heads, head_dim], k and
+    v [total_k, kv_heads, head_dim]; sequence b's queries are rows cu_q[b] ..
+    cu_q[b + 1] - 1, its keys rows cu_k[b] .. (cu_q unless given; more keys than
+    queries: the queries are the last ones) (glq_attn_prompt). max_q bounds the
+    queries of a sequence (total_q unless given)."""
+    if len(q.shape) != 3 or len(k.shape) != 3:
+        raise ValueError("q, k: must be [rows, heads, head_dim]")
+    dev, heads, dim, kvh = q.device, q.shape[1], q.shape[2], k.shape[1]
+    if dim not in _HEAD_DIMS or kvh < 1 or heads % kvh:
+        raise ValueError(f"q, k: {heads} and {kvh} heads of {dim}")
+    qs = _rows(q, "q", dev, heads, dim)
+    ks = _rows(k, "k", dev, kvh, dim, q.dtype)
+    vs = _rows(v, "v", dev, kvh, dim, q.dtype, k.shape[0])
+    os_ = _rows(out, "out", dev, heads, dim, q.dtype, q.shape[0])
+    if cu_k is None:
+        cu_k = cu_q
+    batch = cu_q.shape[0] - 1
+    qp, kp = _ints(cu_q, "cu_q", dev, (batch + 1,)), _ints(cu_k, "cu_k", dev, (batch + 1,))
+    st = PromptStruct(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _dtype_code(q), heads, kvh, dim, qs,
+                      ks, vs, os_, q.shape[0], k.shape[0], batch, qp, kp, q.shape[0] if max_q is None else max_q,
+                      dim ** -0.5 if scale is None else scale)
+    _check(_lib.glq_attn_prompt(ctypes.byref(st), ATTN_CAUSAL if causal else 0, _stream_ptr(stream)),
+           "glq_attn_prompt")
+    return out

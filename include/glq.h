@@ -356,6 +356,135 @@ size_t glq_ep_fused_linear_workspace(const glq_ep_layer *L, int64_t m);
 int glq_ep_fused_linear(const glq_ep_layer *L, const void *x, glq_dtype x_dt, int64_t m, void *y,
                         glq_dtype y_dt, void *workspace, size_t ws_bytes, uint32_t flags, void *hip_stream);
 
+/* ------------------------------------------------------------------------
+ * Attention beside the compressed linears: a paged key-value cache held as
+ * bf16, 8-bit or 4-bit codes, the write and read of it, the attention of one
+ * new token per sequence over it, and the attention of whole prompts. The
+ * q, k, v and output projections around them are layers as above; rotating
+ * q and k (and v, undone on the output) by glq_rht_apply along the head
+ * dimension before the cache leaves every score as it was and spreads
+ * outlier channels over the codes.
+ *
+ * A sequence's token t lives in page page_table[b][t / page_size], at row
+ * t % page_size of it; its slot is page * page_size + row. Query head h
+ * reads kept head h / (q_heads / kv_heads).
+ *
+ * Codes: per token and head, a = max |x| over head_dim and Q = 127 (8 bits)
+ * or 7 (4 bits); code = x Q / a rounded half to even (the product and the
+ * quotient each rounded to float32; for bf16 x the product is exact), 0 for
+ * a = 0; scale = a / Q, value = fl32(code * scale). A non-finite x makes its
+ * token's head read back as NaN.
+ * ---------------------------------------------------------------------- */
+typedef enum { GLQ_KV_BF16 = 0, GLQ_KV_INT8 = 1, GLQ_KV_INT4 = 2 } glq_kv_format;
+
+/* The struct lives in host memory; its pointers are device pointers owned by
+ * the caller, 16-byte aligned. row bytes = 2 head_dim, head_dim or head_dim/2
+ * (4-bit rows: byte j holds code + 8 of dimension 2j in its low half and of
+ * 2j + 1 in its high half). */
+typedef struct {
+    int32_t format;           /* glq_kv_format */
+    int32_t kv_heads;         /* >= 1 */
+    int32_t head_dim;         /* 64, 128 or 256 */
+    int32_t page_size;        /* tokens per page: a power of two, 16 .. 1024 */
+    int64_t num_pages;        /* >= 1; num_pages * page_size < 2^31 */
+    void  *k, *v;             /* [num_pages][kv_heads][page_size][row bytes] */
+    float *k_scale, *v_scale; /* [num_pages][kv_heads][page_size]; NULL for GLQ_KV_BF16 */
+} glq_kv_cache;
+
+/*
+ * glq_kv_append -- write tokens' keys and values into the cache.
+ *   k, v        device [tokens][kv_heads][head_dim] of dt, tokens k_stride and
+ *               v_stride elements apart (>= kv_heads * head_dim; pointers and
+ *               strides multiples of 16 bytes)
+ *   slots       device int32 [tokens]; a slot outside the cache (negative, or
+ *               >= num_pages * page_size) drops its token. Two tokens with one
+ *               slot leave it with either's contents.
+ * tokens == 0 is a successful no-op. GLQ_KV_BF16 rounds to nearest even.
+ */
+int glq_kv_append(const glq_kv_cache *C, const void *k, const void *v, glq_dtype dt, int64_t k_stride,
+                  int64_t v_stride, const int32_t *slots, int64_t tokens, void *hip_stream);
+
+/*
+ * glq_kv_read -- read cached tokens back as dense keys and values (for the
+ * attention of a later chunk of a prompt). Arguments as in glq_kv_append; a
+ * slot outside the cache gives rows of zeros. bf16 output = round to nearest
+ * even of the value.
+ */
+int glq_kv_read(const glq_kv_cache *C, const int32_t *slots, int64_t tokens, void *k, void *v, glq_dtype dt,
+                int64_t k_stride, int64_t v_stride, void *hip_stream);
+
+/* Bytes of device workspace glq_attn_decode needs, its control words
+ * (GLQ_ATTN_CTRL_BYTES) included; 0 for arguments it would refuse. */
+#define GLQ_ATTN_CTRL_BYTES 65536
+size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t max_len);
+
+/*
+ * glq_attn_decode -- attention of one new token per sequence over the cache:
+ * out[b][h] = sum_t softmax_t(scale * q[b][h] . k_t) v_t over the cached
+ * tokens t < lens[b] (the new token among them, once appended).
+ *   q, out      device [batch][q_heads][head_dim] of dt, sequences q_stride and
+ *               out_stride elements apart (>= q_heads * head_dim; pointers and
+ *               strides multiples of 16 bytes)
+ *   page_table  device int32 [batch][max_pages]; entries past a sequence's
+ *               length are not used. An entry outside the cache is read as
+ *               the nearest page inside it.
+ *   lens        device int32 [batch], read as 0 .. max_len; a length of 0 gives
+ *               a row of zeros
+ *   max_len     host: no length exceeds it; <= max_pages * page_size. The
+ *               launch is sized by it.
+ *   scale       finite
+ *   dt          GLQ_BF16: the weights are taken as sums of two bf16 values (16 bits)
+ *               for the matrix cores; GLQ_F32: q and the weights as sums of three,
+ *               so every product is that of float32 operands. Sums are float32.
+ *   workspace   device, 256-byte aligned. Its first GLQ_ATTN_CTRL_BYTES must be zero
+ *               before the first call with it and are left zero by every call whose
+ *               kernels complete; concurrent calls need workspaces of their own,
+ *               and other entry points must not write there in between.
+ * What lies in the cache past a sequence's length is never used, NaN among it.
+ * Results do not depend on the order in which workgroups finish. q_heads must be
+ * a multiple of kv_heads. batch == 0 is a successful no-op; GLQ_ERR_UNSUPPORTED
+ * for launches past 2^31 workgroups.
+ */
+int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype dt, int64_t q_stride, int64_t batch,
+                    int32_t q_heads, const int32_t *page_table, int64_t max_pages, const int32_t *lens,
+                    int64_t max_len, float scale, void *out, int64_t out_stride, void *workspace,
+                    size_t ws_bytes, void *hip_stream);
+
+/* flags for glq_attn_prompt */
+enum { GLQ_ATTN_CAUSAL = 1u };
+
+/* Packed prompts: sequence b's queries are rows cu_q[b] .. cu_q[b + 1] - 1 of
+ * q and out, its keys rows cu_k[b] .. cu_k[b + 1] - 1 of k and v. The struct
+ * lives in host memory; its pointers are device pointers. */
+typedef struct {
+    const void *q, *k, *v;    /* [total][heads][head_dim] of dt, rows *_stride elements apart */
+    void *out;                /* [total_q][q_heads][head_dim] of dt */
+    int32_t dt;               /* glq_dtype of q, k, v and out */
+    int32_t q_heads, kv_heads, head_dim;   /* q_heads a multiple of kv_heads; head_dim 64, 128 or 256 */
+    int64_t q_stride, k_stride, v_stride, out_stride;  /* >= heads * head_dim; pointers and strides
+                                                          multiples of 16 bytes */
+    int64_t total_q, total_k; /* rows of q and out, of k and v; < 2^31 */
+    int64_t batch;
+    const int32_t *cu_q, *cu_k;   /* [batch + 1], not decreasing, within 0 .. total */
+    int64_t max_q;            /* no sequence has more queries; the launch is sized by it */
+    float scale;              /* finite */
+} glq_prompt;
+
+/*
+ * glq_attn_prompt -- out[i][h] = sum_j softmax_j(scale * q[i][h] . k_j) v_j over
+ * the keys j of i's own sequence; with GLQ_ATTN_CAUSAL query i of Lq sees keys
+ * j <= i + Lk - Lq (the last query sees every key: keys may begin with a cached
+ * prefix). A query that sees no key gets a row of zeros; rows outside every
+ * sequence are not written. Offsets are read as the nearest value within 0 ..
+ * total. A key that a query does not see never reaches it, NaN and infinities
+ * in it included; an infinite value that it sees may give NaN.
+ *   dt = GLQ_BF16: bf16 matrix-core path, weights rounded to bf16, float32 sums
+ *   dt = GLQ_F32:  float32 products and sums
+ * batch == 0, total_q == 0 or max_q == 0 is a successful no-op. out must not
+ * overlap q, k or v.
+ */
+int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_stream);
+
 /* Static text for a status code. */
 const char *glq_status_string(int status);
 

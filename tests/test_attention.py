@@ -1,0 +1,543 @@
+"""The paged key-value cache and the attention over it: GPU results against
+plain 64-bit formulas, the refusals of the C ABI and of the binding on the CPU.
+
+Tolerances. With A = sum_j p_j |v_j| (the same weights, absolute values):
+  float32  1e-5 A: a score's error is a few float32 roundings of |s| <= ~30 (at
+           most ~100 units of 2^-24 = 6e-6), and it is the weight's relative error;
+  bf16     2^-9 (A + |o|) for the output's own rounding (at most 2^-8 |o|, and A >=
+           |o|), 1e-5 A for the rest: the weights keep 16 bits or more.
+Codes, scales and values read back are held to equality: for bf16 inputs Q x is
+exact in float32 and Q x / a is a quotient of 8-bit numbers times Q, further than
+a float32 rounding from every half unless it is one.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+glq = pytest.importorskip("dequant_e8_codebook_amd.glq")
+
+FORMATS = {"bf16": glq.KV_BF16, "int8": glq.KV_INT8, "int4": glq.KV_INT4}
+LEVELS = {"int8": 127, "int4": 7}
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture
+def gen():
+    return torch.Generator().manual_seed(11)
+
+
+def _normal(gen, *shape, dtype=torch.float32):
+    return torch.randn(*shape, generator=gen).to(dtype)
+
+
+# ------------------------------------------------------------- 64-bit formulas
+
+def _ref_codes(x, fmt):
+    """Codes (float64) and scales (float32) of x [..., d] (float64)."""
+    top = x.abs().amax(-1, keepdim=True)
+    q = LEVELS[fmt]
+    code = torch.where(top > 0, torch.round(x * q / torch.where(top > 0, top, 1.0)), torch.zeros_like(x))
+    return code, (top / q).squeeze(-1).to(torch.float32)
+
+
+def _ref_values(x, fmt):
+    """float32 values that the cache stands for."""
+    if fmt == "bf16":
+        return x.to(torch.bfloat16).to(torch.float32)
+    code, scale = _ref_codes(x.double(), fmt)
+    return code.to(torch.float32) * scale[..., None]
+
+
+def _ref_attend(q, k, v, scale, seen):
+    """float64 attention of q [n, d] over k, v [m, d], seen [n, m] bool: the result
+    and A = sum p |v|; rows that see nothing are zero."""
+    q, k, v = q.double(), k.double(), v.double()
+    out, mag = torch.zeros(q.shape[0], v.shape[1], dtype=torch.float64), torch.zeros(q.shape[0], v.shape[1],
+                                                                                      dtype=torch.float64)
+    rows = seen.any(1)
+    if rows.any():
+        s = (q[rows] @ k.T) * scale
+        s = s.masked_fill(~seen[rows], -math.inf)
+        p = torch.softmax(s, 1)
+        out[rows] = p @ v
+        mag[rows] = p @ v.abs()
+    return out, mag
+
+
+def _held(got, ref, mag, dtype):
+    tol = 1e-5 * mag + (0 if dtype == "f32" else 2.0 ** -9 * 1.01 * (mag + ref.abs())) + 1e-30
+    err = (got.double().cpu() - ref).abs()
+    assert torch.isfinite(got).all()
+    assert (err <= tol).all(), f"worst {(err / tol).max().item():.3g} of the tolerance"
+
+
+# -------------------------------------------------------------- write and read
+
+def _slots(gen, tokens, capacity):
+    return torch.randperm(capacity, generator=gen)[:tokens].to(torch.int32)
+
+
+def _unpack(cache):
+    """Codes of a quantised cache as float64 [pages, heads, page, d]."""
+    out = []
+    for t in (cache.k, cache.v):
+        t = t.cpu()
+        if cache.format == glq.KV_INT4:
+            t = torch.stack(((t & 15).to(torch.int32) - 8, (t >> 4).to(torch.int32) - 8), -1).flatten(-2)
+        out.append(t.double())
+    return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("tokens,heads,dim,page,dtype", [(1, 1, 64, 16, "bf16"), (37, 3, 128, 16, "bf16"),
+                                                         (130, 8, 64, 64, "f32"), (77, 5, 256, 32, "bf16"),
+                                                         (1000, 2, 128, 1024, "bf16")])
+def test_append_and_read(gen, fmt, tokens, heads, dim, page, dtype):
+    pages = -(-tokens // page) + 2
+    cache = glq.KvCache.empty(pages, page, heads, dim, FORMATS[fmt])
+    slots = _slots(gen, tokens, pages * page)
+    # k and v as halves of one projection's rows: strided
+    kv = _normal(gen, tokens, 2 * heads, dim, dtype=torch.bfloat16) * 3
+    kv[tokens // 2, 0] = 0
+    kv = kv.to(DTYPES[dtype]).cuda()
+    k, v = kv[:, :heads], kv[:, heads:]
+    dropped = torch.full_like(slots, -1)
+    dropped[0] = pages * page
+    glq.kv_append(cache, k, v, dropped.cuda())
+    assert not cache.k.any() and not cache.v.any()
+    glq.kv_append(cache, k, v, slots.cuda())
+    for fill, dt in ((7.0, torch.bfloat16), (7.0, torch.float32)):
+        ko, vo = (torch.full((tokens + 1, heads, dim), fill, dtype=dt, device="cuda") for _ in range(2))
+        where = torch.cat((slots, torch.tensor([-5], dtype=torch.int32))).cuda()
+        glq.kv_read(cache, where, ko, vo)
+        for x, o in ((k, ko), (v, vo)):
+            want = _ref_values(x.cpu().float(), fmt)
+            assert torch.equal(o[:tokens].cpu(), want.to(dt))
+            assert not o[tokens].any()               # a slot outside the cache
+    if fmt != "bf16":
+        at = slots.long()
+        for x, codes, scale in ((k, _unpack(cache)[0], cache.k_scale), (v, _unpack(cache)[1], cache.v_scale)):
+            code, s = _ref_codes(x.cpu().double(), fmt)
+            assert torch.equal(codes[at // page, :, at % page], code)
+            assert torch.equal(scale.cpu()[at // page, :, at % page], s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "int4"])
+def test_append_special_values(fmt):
+    big = 3e38
+    rows = [[math.nan, 1.0], [math.inf, 1.0], [-math.inf, math.nan], [big, -big / 2], [1e-30, -1e-30], [0.0, -0.0],
+            [big, 1e-30]]
+    x = torch.zeros(len(rows), 1, 64)
+    for i, r in enumerate(rows):
+        x[i, 0, 5], x[i, 0, 40] = r
+    cache = glq.KvCache.empty(1, 16, 1, 64, FORMATS[fmt])
+    slots = torch.arange(len(rows), dtype=torch.int32, device="cuda")
+    glq.kv_append(cache, x.cuda(), x.cuda(), slots)
+    ko, vo = torch.empty_like(x, device="cuda"), torch.empty_like(x, device="cuda")
+    glq.kv_read(cache, slots, ko, vo)
+    ko = ko.cpu()
+    assert torch.equal(torch.nan_to_num(ko, 7.0), torch.nan_to_num(vo.cpu(), 7.0))
+    assert torch.isnan(ko[:3]).all()
+    q = LEVELS[fmt]
+    for i in (3, 4, 6):
+        assert ko[i, 0, 5].item() == pytest.approx(rows[i][0], rel=1e-6)
+        assert abs(ko[i, 0, 40].item() - rows[i][1]) <= abs(rows[i][0]) / (2 * q) * 1.0001
+    assert not ko[5].any()
+
+
+# ------------------------------------------------------------------ one new token
+
+def _decode_case(gen, fmt, lens, q_heads, kv_heads, dim, page, dtype, spread=1.5, stride=0):
+    """A cache filled through shuffled pages, garbage wherever no token is."""
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + 2
+    if fmt == "bf16":
+        k, v = (_normal(gen, pages, kv_heads, page, dim, dtype=torch.bfloat16) for _ in range(2))
+        parts = [k, v, None, None]
+        dense = (k.float(), v.float())
+    else:
+        parts, dense = [], []
+        for _ in range(2):
+            code, scale = _ref_codes(_normal(gen, pages, kv_heads, page, dim).double(), fmt)
+            dense.append(code.to(torch.float32) * scale[..., None])
+            c = code.to(torch.int8) if fmt == "int8" else ((code[..., 0::2] + 8).to(torch.uint8)
+                                                           | (code[..., 1::2] + 8).to(torch.uint8) << 4)
+            parts += [c, scale]
+        parts = [parts[0], parts[2], parts[1], parts[3]]
+    order = torch.randperm(pages, generator=gen).to(torch.int32)
+    most = max(1, max(need)) + 1
+    table = torch.full((len(lens), most), -1, dtype=torch.int32)
+    table[:, -1] = 2 ** 31 - 1
+    used = torch.zeros(pages, page, dtype=torch.bool)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        for i in range(n):
+            used[order[at + i].item(), :min(page, lens[b] - i * page)] = True
+        at += n
+    free = ~used[:, None, :].expand(pages, kv_heads, page)
+    for t in parts[2:] if fmt != "bf16" else parts[:2]:
+        t[free] = math.nan
+    q = _normal(gen, len(lens), q_heads + stride, dim, dtype=DTYPES[dtype]) * spread
+    q = q.cuda()[:, :q_heads]
+    cache = glq.KvCache(*[None if t is None else t.contiguous().cuda() for t in parts])
+    ref = torch.zeros(len(lens), q_heads, dim, dtype=torch.float64)
+    mag = torch.zeros_like(ref)
+    for b, n in enumerate(lens):
+        if not n:
+            continue
+        pg, off = table[b].long()[torch.arange(n) // page], torch.arange(n) % page
+        for h in range(kv_heads):
+            kk, vv = dense[0][pg, h, off], dense[1][pg, h, off]
+            r = slice(h * (q_heads // kv_heads), (h + 1) * (q_heads // kv_heads))
+            ref[b, r], mag[b, r] = _ref_attend(q[b, r].cpu(), kk, vv, dim ** -0.5,
+                                               torch.ones(q_heads // kv_heads, n, dtype=torch.bool))
+    return cache, q, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), ref, mag
+
+
+def _decode(cache, q, table, lens, max_len, workspace=None, **kw):
+    if workspace is None:
+        workspace = torch.zeros(glq.attn_decode_workspace_bytes(cache, q.shape[0], q.shape[1], max_len),
+                                dtype=torch.uint8, device="cuda")
+    out = torch.full((q.shape[0], q.shape[1], q.shape[2]), 7.0, dtype=q.dtype, device="cuda")
+    glq.attn_decode(cache, q, table, lens, out, workspace, max_len, **kw)
+    return out, workspace
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_decode_lengths(gen, fmt, dim, dtype):
+    lens = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 65, 127, 128, 129, 300]
+    cache, q, table, ln, ref, mag = _decode_case(gen, fmt, lens, 6, 2, dim, 16, dtype, stride=1)
+    out, ws = _decode(cache, q, table, ln, 300)
+    _held(out, ref, mag, dtype)
+    assert not out[0].any()                          # no tokens: zeros
+    assert not ws[:65536].any()                      # control words left as they were
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_heads,kv_heads", [(1, 1), (8, 8), (16, 1), (17, 1), (40, 2), (24, 3), (7, 7)])
+@pytest.mark.parametrize("fmt,page", [("bf16", 32), ("int8", 64), ("int4", 128)])
+def test_decode_groups_and_pages(gen, q_heads, kv_heads, fmt, page):
+    lens = [200, 0, 77, 1]
+    cache, q, table, ln, ref, mag = _decode_case(gen, fmt, lens, q_heads, kv_heads, 128, page, "bf16")
+    out, _ = _decode(cache, q, table, ln, 200)
+    _held(out, ref, mag, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,dtype", [("bf16", "bf16"), ("int8", "f32"), ("int4", "bf16"), ("int4", "f32")])
+@pytest.mark.parametrize("spread", [1.5, 0.0])
+def test_decode_long(gen, fmt, dtype, spread):
+    # long enough that the work is split over the length; spread 0: every token
+    # has the same weight, the largest cancellation of the sums
+    lens = [20011, 9000, 3]
+    cache, q, table, ln, ref, mag = _decode_case(gen, fmt, lens, 4, 1, 128, 64, dtype, spread=spread)
+    out, ws = _decode(cache, q, table, ln, 20011)
+    _held(out, ref, mag, dtype)
+    again, ws = _decode(cache, q, table, ln, 20011, ws)
+    assert torch.equal(out, again)                   # and the order of the workgroups does not show
+    # lens are read as at most max_len
+    few, _ = _decode(cache, q, table, torch.full_like(ln, 2 ** 30), 3, ws)
+    assert torch.equal(few[2], out[2])
+
+
+@pytest.mark.gpu
+def test_decode_peaked_and_extreme_scores(gen):
+    # one token far ahead of the rest (early, or in the last tile), and scores of
+    # +-1e4, whose differences leave the range of exp
+    for at in (3, 498):
+        cache, q, table, ln, _, _ = _decode_case(gen, "bf16", [500], 2, 1, 64, 16, "bf16")
+        pg = table[0, at // 16].item()
+        cache.k[pg, 0, at % 16] = (q[0, 0].float() * 100).to(torch.bfloat16)
+        out, _ = _decode(cache, q, table, ln, 500)
+        assert torch.equal(out[0, 0], cache.v[pg, 0, at % 16])
+        assert torch.isfinite(out).all()
+
+
+@pytest.mark.gpu
+def test_decode_scale_stream_and_graph(gen):
+    lens = [1500, 20]
+    cache, q, table, ln, ref, mag = _decode_case(gen, "int8", lens, 8, 2, 128, 32, "bf16")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out, ws = _decode(cache, q, table, ln, 1500)
+        also, ws = _decode(cache, (q.float() * 2).to(torch.bfloat16), table, ln, 1500, ws, scale=0.5 * 128 ** -0.5)
+    side.synchronize()
+    _held(out, ref, mag, "bf16")
+    assert torch.equal(out, also)                    # twice the query at half the scale
+    res = torch.zeros_like(out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        glq.attn_decode(cache, q, table, ln, res, ws, 1500)
+    for _ in range(3):
+        res.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(res, out)
+        ln.copy_(ln)                                 # eager work in between
+        torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------------ prompts
+
+def _prompt_case(gen, lens_q, lens_k, q_heads, kv_heads, dim, dtype, causal, scale=None, fused=False):
+    dt = DTYPES[dtype]
+    tq, tk = sum(lens_q), sum(lens_k)
+    if fused:                                        # q, k and v as parts of one projection's rows
+        qkv = _normal(gen, tq, q_heads + 2 * kv_heads, dim, dtype=dt).cuda()
+        q, k, v = qkv[:, :q_heads], qkv[:, q_heads:q_heads + kv_heads], qkv[:, q_heads + kv_heads:]
+    else:
+        q = (_normal(gen, tq, q_heads, dim, dtype=dt) * 1.5).cuda()
+        k, v = (_normal(gen, tk, kv_heads, dim, dtype=dt).cuda() for _ in range(2))
+    cu_q, cu_k = (torch.tensor(np.concatenate(([0], np.cumsum(x))), dtype=torch.int32) for x in (lens_q, lens_k))
+    ref, mag = torch.zeros(tq, q_heads, dim, dtype=torch.float64), torch.zeros(tq, q_heads, dim, dtype=torch.float64)
+    qc, kc, vc = q.cpu(), k.cpu(), v.cpu()
+    for b, (n, m) in enumerate(zip(lens_q, lens_k)):
+        a, c = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        seen = torch.ones(n, m, dtype=torch.bool)
+        if causal:
+            seen = torch.arange(m)[None] <= torch.arange(n)[:, None] + (m - n)
+        for h in range(q_heads):
+            g = h // (q_heads // kv_heads)
+            ref[a, h], mag[a, h] = _ref_attend(qc[a, h], kc[c, g], vc[c, g], scale or dim ** -0.5, seen)
+    return q, k, v, cu_q.cuda(), cu_k.cuda(), ref, mag
+
+
+def _prompt(q, k, v, cu_q, cu_k, **kw):
+    out = torch.full((q.shape[0], q.shape[1], q.shape[2]), 7.0, dtype=q.dtype, device="cuda")
+    return glq.attn_prompt(q, k, v, out, cu_q, cu_k, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_lengths(gen, dtype, dim, causal):
+    lens = [1, 0, 2, 31, 32, 33, 64, 0, 65, 127, 129, 200]
+    q, k, v, cu, _, ref, mag = _prompt_case(gen, lens, lens, 4, 2, dim, dtype, causal, fused=True)
+    _held(_prompt(q, k, v, cu, None, max_q=200, causal=causal), ref, mag, dtype)
+    _held(_prompt(q, k, v, cu, None, causal=causal), ref, mag, dtype)     # max_q left at the total
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_heads,kv_heads", [(1, 1), (12, 4), (7, 7), (9, 1)])
+def test_prompt_prefixes_and_empty_rows(gen, dtype, causal, q_heads, kv_heads):
+    # keys before the queries (a cached prefix), one token on a prefix, fewer
+    # keys than queries (causal: the first rows see nothing), no keys at all
+    lens_q, lens_k = [40, 1, 70, 5, 3], [300, 257, 30, 0, 3]
+    q, k, v, cu_q, cu_k, ref, mag = _prompt_case(gen, lens_q, lens_k, q_heads, kv_heads, 64, dtype, causal)
+    out = _prompt(q, k, v, cu_q, cu_k, max_q=70, causal=causal)
+    _held(out, ref, mag, dtype)
+    if causal:
+        assert not out[41:41 + 40].any()
+    assert not out[111:116].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,dim,causal", [("bf16", 128, True), ("bf16", 128, False), ("f32", 64, True)])
+def test_prompt_long(gen, dtype, dim, causal):
+    lens = [1111, 700]
+    q, k, v, cu, _, ref, mag = _prompt_case(gen, lens, lens, 4, 1, dim, dtype, causal)
+    _held(_prompt(q, k, v, cu, None, max_q=1111, causal=causal), ref, mag, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompt_unseen_values_do_not_reach(gen, dtype, dim):
+    # NaN and infinities in keys and values that only later queries see
+    n = 150
+    for where in (0, 17, 70, 149):
+        q, k, v, cu, _, ref, mag = _prompt_case(gen, [n, 40], [n, 40], 2, 1, dim, dtype, True)
+        k[where, 0, 3], v[where, 0, 5], v[where, 0, dim - 1] = math.inf, math.nan, -math.inf
+        out = _prompt(q, k, v, cu, None, max_q=n)
+        _held(out[:where], ref[:where], mag[:where], dtype)
+        _held(out[n:], ref[n:], mag[n:], dtype)
+        # value dimension 5 of a query that sees the NaN with a finite weight
+        k[where, 0, 3] = 0.5
+        out = _prompt(q, k, v, cu, None, max_q=n)
+        assert torch.isnan(out[where:n, :, 5]).all()
+        assert not torch.isfinite(out[where:n, :, dim - 1]).any()
+        assert torch.isfinite(out[where:n, :, 6]).all() and torch.isfinite(out[:where]).all()
+        assert torch.isfinite(out[n:]).all()
+
+
+@pytest.mark.gpu
+def test_prompt_rows_outside_sequences_and_wide_offsets(gen):
+    # offsets that do not start at 0 or end at the total: other rows stay as
+    # they are; offsets past the rows are read as the nearest
+    q, k, v, cu, _, ref, mag = _prompt_case(gen, [20, 30], [20, 30], 2, 2, 64, "bf16", True)
+    cu2 = torch.tensor([20, 50], dtype=torch.int32, device="cuda")
+    out = _prompt(q, k, v, cu2, None, max_q=30)
+    assert (out[:20] == 7).all()
+    _held(out[20:], ref[20:], mag[20:], "bf16")
+    cu3 = torch.tensor([-4, 20, 2 ** 30], dtype=torch.int32, device="cuda")
+    _held(_prompt(q, k, v, cu3, None, max_q=2 ** 30), ref, mag, "bf16")
+
+
+@pytest.mark.gpu
+def test_prompt_scale_and_extreme_scores(gen):
+    q, k, v, cu, _, ref, mag = _prompt_case(gen, [90], [90], 2, 1, 128, "bf16", True, scale=0.02)
+    _held(_prompt(q, k, v, cu, None, scale=0.02), ref, mag, "bf16")
+    # every score -inf (finite products that overflow): no weight anywhere, zeros
+    big = torch.full_like(q, -3e38)
+    out = _prompt(big, torch.full_like(k, 3e38), v, cu, None)
+    assert not out.any()
+
+
+@pytest.mark.gpu
+def test_prompt_agrees_with_decode(gen):
+    # the last row of a causal prompt is what one new token sees
+    n, heads, kvh, dim = 333, 8, 2, 128
+    q, k, v, cu, _, ref, mag = _prompt_case(gen, [n], [n], heads, kvh, dim, "f32", True)
+    cache = glq.KvCache.empty(12, 32, kvh, dim, glq.KV_INT8)
+    table = torch.randperm(12, generator=gen).to(torch.int32)[None].cuda()
+    at = torch.arange(n, device="cuda")
+    slots = (table[0].long()[at // 32] * 32 + at % 32).to(torch.int32)
+    glq.kv_append(cache, k, v, slots)
+    k8, v8 = torch.empty_like(k), torch.empty_like(v)
+    glq.kv_read(cache, slots, k8, v8)
+    out = _prompt(q, k8, v8, cu, None)
+    one, _ = _decode(cache, q[n - 1:], table, torch.tensor([n], dtype=torch.int32, device="cuda"), n)
+    assert (one[0] - out[n - 1]).abs().max() <= 2e-5 * out[n - 1].abs().max()
+
+
+# --------------------------------------------------------------- refusals (CPU)
+
+def _cache_struct(**kw):
+    c = dict(format=1, kv_heads=2, head_dim=128, page_size=32, num_pages=4, k=256, v=256, k_scale=256, v_scale=256)
+    c.update(kw)
+    return glq.KvCacheStruct(*[c[f[0]] for f in glq.KvCacheStruct._fields_])
+
+
+BAD_CACHES = [(dict(format=3), "ARG"), (dict(format=-1), "ARG"), (dict(kv_heads=0), "ARG"), (dict(num_pages=0), "ARG"),
+              (dict(page_size=8), "ARG"), (dict(page_size=48), "ARG"), (dict(page_size=2048), "ARG"),
+              (dict(k=0), "ARG"), (dict(v=0), "ARG"), (dict(k=264), "ARG"), (dict(k_scale=0), "ARG"),
+              (dict(v_scale=260), "ARG"), (dict(head_dim=96), "UNSUPPORTED"), (dict(head_dim=0), "UNSUPPORTED"),
+              (dict(num_pages=1 << 40), "UNSUPPORTED"), (dict(kv_heads=1 << 20), "UNSUPPORTED")]
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_cache_refusals(bad, status):
+    lib, c, want = glq.raw(), _cache_struct(**bad), getattr(glq, "GLQ_ERR_" + status)
+    r = ctypes.byref(c)
+    assert lib.glq_kv_append(r, 256, 256, 1, 256, 256, 256, 1, None) == want
+    assert lib.glq_kv_read(r, 256, 1, 256, 256, 1, 256, 256, None) == want
+    assert lib.glq_attn_decode_workspace(r, 1, 2, 10) == 0
+    assert lib.glq_attn_decode(r, 256, 1, 256, 1, 2, 256, 1, 256, 10, 0.1, 256, 256, 256, 1 << 20, None) == want
+
+
+def test_cache_io_refusals():
+    lib, c = glq.raw(), _cache_struct()
+    good = dict(k=256, v=256, dt=1, ks=256, vs=256, slots=256, tokens=1)
+    for bad in (dict(k=0), dict(v=0), dict(k=258), dict(dt=2), dict(dt=-1), dict(ks=255), dict(ks=128), dict(vs=260),
+                dict(slots=0), dict(slots=258), dict(tokens=-1)):
+        a = dict(good, **bad)
+        assert lib.glq_kv_append(ctypes.byref(c), a["k"], a["v"], a["dt"], a["ks"], a["vs"], a["slots"], a["tokens"],
+                                 None) == glq.GLQ_ERR_ARG, bad
+        assert lib.glq_kv_read(ctypes.byref(c), a["slots"], a["tokens"], a["k"], a["v"], a["dt"], a["ks"], a["vs"],
+                               None) == glq.GLQ_ERR_ARG, bad
+    assert lib.glq_kv_append(None, 256, 256, 1, 256, 256, 256, 1, None) == glq.GLQ_ERR_ARG
+    assert lib.glq_kv_append(ctypes.byref(c), 0, 0, 1, 0, 0, 0, 0, None) == glq.GLQ_OK
+    assert lib.glq_kv_append(ctypes.byref(c), 256, 256, 1, 256, 256, 256, 1 << 40, None) == glq.GLQ_ERR_UNSUPPORTED
+
+
+def test_decode_refusals():
+    lib, c = glq.raw(), _cache_struct()
+
+    def call(**kw):
+        a = dict(q=256, dt=1, qs=512, batch=2, heads=4, table=256, pages=3, lens=256, most=96, scale=0.1, out=256,
+                 os=512, ws=256, bytes=1 << 30)
+        a.update(kw)
+        return lib.glq_attn_decode(ctypes.byref(c), a["q"], a["dt"], a["qs"], a["batch"], a["heads"], a["table"],
+                                   a["pages"], a["lens"], a["most"], a["scale"], a["out"], a["os"], a["ws"],
+                                   a["bytes"], None)
+    for bad in (dict(q=0), dict(q=264), dict(dt=5), dict(qs=511), dict(qs=500), dict(batch=-1), dict(heads=0),
+                dict(heads=3), dict(table=0), dict(table=258), dict(pages=-1), dict(pages=2), dict(lens=0),
+                dict(lens=257), dict(most=-1), dict(most=97), dict(scale=math.nan), dict(scale=math.inf), dict(out=0),
+                dict(out=260), dict(os=508)):
+        assert call(**bad) == glq.GLQ_ERR_ARG, bad
+    for bad in (dict(ws=0), dict(ws=128), dict(bytes=100)):
+        assert call(**bad) == glq.GLQ_ERR_WORKSPACE, bad
+    assert call(most=2 ** 31 - 1, pages=1 << 40) == glq.GLQ_ERR_UNSUPPORTED
+    assert call(batch=1 << 40) == glq.GLQ_ERR_UNSUPPORTED
+    assert call(batch=0, q=0, out=0) == glq.GLQ_OK
+    assert lib.glq_attn_decode_workspace(ctypes.byref(c), 2, 3, 10) == 0
+    assert lib.glq_attn_decode_workspace(ctypes.byref(c), 2, 4, 10) >= 65536
+
+
+def test_prompt_refusals():
+    lib = glq.raw()
+
+    def call(flags=1, **kw):
+        a = dict(q=256, k=256, v=256, out=256, dt=1, q_heads=4, kv_heads=2, head_dim=64, q_stride=256, k_stride=128,
+                 v_stride=128, out_stride=256, total_q=5, total_k=5, batch=1, cu_q=256, cu_k=256, max_q=5, scale=0.1)
+        a.update(kw)
+        return lib.glq_attn_prompt(ctypes.byref(glq.PromptStruct(*[a[f[0]] for f in glq.PromptStruct._fields_])),
+                                   flags, None)
+    for bad in (dict(q=0), dict(k=8), dict(v=0), dict(out=0), dict(dt=2), dict(q_heads=0), dict(q_heads=5),
+                dict(kv_heads=0), dict(q_stride=255), dict(k_stride=130), dict(v_stride=64), dict(out_stride=0),
+                dict(total_q=-1), dict(total_k=-1), dict(batch=-1), dict(max_q=-1), dict(cu_q=0), dict(cu_k=2),
+                dict(scale=math.inf), dict(flags=2)):
+        assert call(**bad) == glq.GLQ_ERR_ARG, bad
+    for bad in (dict(head_dim=80, q_stride=320, k_stride=160, v_stride=160, out_stride=320),
+                dict(total_q=1 << 33), dict(total_k=1 << 33), dict(batch=1 << 40)):
+        assert call(**bad) == glq.GLQ_ERR_UNSUPPORTED, bad
+    assert lib.glq_attn_prompt(None, 0, None) == glq.GLQ_ERR_ARG
+    for nothing in (dict(batch=0), dict(total_q=0), dict(max_q=0)):
+        assert call(**nothing, q=0, cu_q=0) == glq.GLQ_OK
+
+
+def test_binding_refuses_host_tensors():
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 2], dtype=torch.int32)
+    with pytest.raises(ValueError):
+        glq.attn_prompt(q, q, q, q.clone(), cu)
+    with pytest.raises(ValueError):
+        glq.KvCache.empty(2, 16, 1, 64, glq.KV_BF16, device="cpu")
+    with pytest.raises(ValueError):
+        glq.KvCache.empty(2, 16, 1, 64, 9, device="cpu")
+
+
+@pytest.mark.gpu
+def test_binding_refusals(gen):
+    cache, q, table, ln, _, _ = _decode_case(gen, "int8", [20, 3], 4, 2, 64, 16, "bf16")
+    ws = torch.zeros(glq.attn_decode_workspace_bytes(cache, 2, 4, 20), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    good = dict(q=q, page_table=table, lens=ln, out=out, workspace=ws, max_len=20)
+    glq.attn_decode(cache, **good)
+    for bad in (dict(q=q.cpu()), dict(q=q[:, :3].transpose(0, 1)), dict(q=q.half()), dict(lens=ln.long()),
+                dict(lens=ln[:1]), dict(page_table=table.long()), dict(out=out.float()), dict(out=out[:1]),
+                dict(page_table=table.T), dict(workspace=ws.cpu())):
+        with pytest.raises(ValueError):
+            glq.attn_decode(cache, **dict(good, **bad))
+    for bad in (dict(q=q[:, :3], out=out[:, :3].contiguous()), dict(max_len=2 ** 20)):
+        with pytest.raises(glq.GlqError):
+            glq.attn_decode(cache, **dict(good, **bad))
+    k = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(5, dtype=torch.int32, device="cuda")
+    glq.kv_append(cache, k, k, slots)
+    for bad in ((k[:, :1], k, slots), (k, k.float(), slots), (k, k[:4], slots), (k, k, slots.long()),
+                (k, k, slots[:4]), (k.cpu(), k, slots)):
+        with pytest.raises(ValueError):
+            glq.kv_append(cache, *bad)
+    with pytest.raises(ValueError):
+        glq.KvCache(cache.k, cache.v)                # scales missing
+    with pytest.raises(ValueError):
+        glq.KvCache(cache.k, cache.v[:1], cache.k_scale, cache.v_scale)
+    cu = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        glq.attn_prompt(k, k, k, k.clone(), cu.long())
+    with pytest.raises(ValueError):
+        glq.attn_prompt(torch.cat((k, k[:, :1]), 1), k, k, torch.cat((k, k[:, :1]), 1), cu)
