@@ -6,7 +6,8 @@
 //   kv_append_k     tokens' keys and values -> bf16, 8-bit or 4-bit rows
 //   kv_read_k       cached rows -> dense keys and values
 //   attn_decode_k   one new token per sequence over the paged cache
-//   attn_prompt_k   packed prompts, float32 matrix instructions
+//   attn_prompt_bf16  packed prompts, bf16 matrix instructions
+//   attn_prompt_f32   packed prompts, float32 matrix instructions
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -505,8 +506,10 @@ struct PromptArgs {
   void *out;
   int64_t q_stride, k_stride, v_stride, out_stride, total_q, total_k;
   const int32_t *cu_q, *cu_k;
-  int32_t q_heads, kv_heads, q_tiles, causal;
-  float scale2;
+  int32_t q_heads, kv_heads, q_tiles, causal, items;   // items: batch * q_heads
+  float scale2;                // scale * log2(e)
+  float abs_scale2;            // bf16 path: its magnitude, the sign in q_xor; for a
+  uint32_t q_and, q_xor;       // scale of 0, 1 and queries of 0 (q_and)
 };
 
 __device__ __forceinline__ int clamped(int x, int64_t top) { return x < 0 ? 0 : x > top ? (int)top : x; }
@@ -543,17 +546,9 @@ __device__ __forceinline__ void keep_unseen_out(float4 &x, bool seen, f32x4 *acc
 // O^T = V^T P^T. k-slot g of step 4 i + r of the scores means dimension 16 i +
 // 4 g + r, row n of value tile (i, c) means dimension 64 i + 4 n + c: both are 16-byte loads.
 template <int D, bool F32>
-__global__ void __launch_bounds__(256) attn_prompt_k(PromptArgs a) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__device__ __forceinline__ void prompt_wave(const PromptArgs &a, int lane, int head, int q0, int lq, int k0, int lk,
+                                            int row0) {
   const int g = lane >> 4, n = lane & 15;
-  const int tile = blockIdx.x % a.q_tiles;
-  const int bh = blockIdx.x / a.q_tiles, head = bh % a.q_heads;
-  const int64_t b = bh / a.q_heads;
-  const int q0 = clamped(a.cu_q[b], a.total_q), q1 = clamped(a.cu_q[b + 1], a.total_q);
-  const int k0 = clamped(a.cu_k[b], a.total_k), k1 = clamped(a.cu_k[b + 1], a.total_k);
-  const int lq = q1 - q0, lk = k1 - k0 > 0 ? k1 - k0 : 0;
-  const int row0 = 64 * tile + 16 * wave;
-  if (row0 >= lq) return;
   const int row = row0 + n < lq ? row0 + n : lq - 1;
   const int kvh = head / (a.q_heads / a.kv_heads);
   float4 q[D / 16];
@@ -630,6 +625,234 @@ __global__ void __launch_bounds__(256) attn_prompt_k(PromptArgs a) {
       else *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) =
                make_uint2(pack_bf16(x, y), pack_bf16(z, w));
     }
+}
+
+// the sequence of a workgroup: its first query and key row and their numbers
+struct Span { int q0, lq, k0, lk; };
+__device__ __forceinline__ Span span_of(const PromptArgs &a, int64_t b) {
+  const int q0 = clamped(a.cu_q[b], a.total_q), q1 = clamped(a.cu_q[b + 1], a.total_q);
+  const int k0 = clamped(a.cu_k[b], a.total_k), k1 = clamped(a.cu_k[b + 1], a.total_k);
+  return {q0, q1 - q0, k0, k1 - k0 > 0 ? k1 - k0 : 0};
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) attn_prompt_f32(PromptArgs a) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int bh = blockIdx.x / a.q_tiles, head = bh % a.q_heads;
+  const Span s = span_of(a, bh / a.q_heads);
+  const int row0 = 64 * (blockIdx.x % a.q_tiles) + 16 * wave;
+  if (row0 < s.lq) prompt_wave<D, true>(a, lane, head, s.q0, s.lq, s.k0, s.lk, row0);
+}
+
+// The bf16 path. A workgroup takes 128 queries of one head, 32 a wave, against
+// tiles of 64 keys that its waves share in LDS. 32x32x16 products, transposed:
+// S^T = K Q^T leaves lane (h, n) = (lane >> 5, lane & 31) 16 of the scores of
+// query n per 32 keys (keys 8 i + 4 h + r), so a softmax step is within a lane up
+// to one exchange with lane ^ 32, and its weights are the B operand of O^T =
+// V^T P^T as they stand if k-slot 4 i + r of half h means key 8 i + 4 h + r.
+// V^T's A operand in that order is two transposing LDS reads of 4 keys each.
+//
+// The tiles go from memory to LDS without passing registers, 16 bytes a lane;
+// chunk c of a row lies at chunk c ^ swizzle(row), which spreads both the 16
+// rows of a K read and the 4 rows x 64 bytes of a V read over all banks.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <int D> __host__ __device__ constexpr int swizzle(int row) {
+  return D == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3) : (row & 3) << 2 | ((row >> 2) & 3);
+}
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float across32(float x) {   // the value of lane ^ 32
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(threadIdx.x & 32 ? r[0] : r[1]);
+}
+
+constexpr int kKeys = 64;                            // keys of a tile
+
+// 64 rows of D bf16 values from src (rows stride_bytes apart, `rows` of them
+// there: the rest reads as zeros) into LDS at dst, a quarter by each wave
+template <int D>
+__device__ __forceinline__ void stage_tile(const uint8_t *src, int stride_bytes, int rows, uint32_t dst, int wave,
+                                           const int *voff) {
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc((void *)src, 0, rows * stride_bytes, 0x00020000);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(uintptr_t)(dst + 1024 * (D / 32 * wave + i)), 16,
+                                             voff[i], 0, 0, 0);
+}
+
+template <int D>
+__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(PromptArgs a) {
+  constexpr int KS = D / 16, DT = D / 32, RB = 2 * D, TB = kKeys * RB;
+  // LDS: K tiles at 0 and TB, V tiles at 2 TB and 3 TB
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 5, n = lane & 31;
+  int head_item = blockIdx.x % a.items, tile = a.q_tiles - 1 - blockIdx.x / a.items;
+  const int head = head_item % a.q_heads;
+  const Span sp = span_of(a, head_item / a.q_heads);
+  const int row_wg = 128 * tile;
+  if (row_wg >= sp.lq) return;
+  const int row0 = row_wg + 32 * wave, row = row0 + n < sp.lq ? row0 + n : sp.lq - 1;
+  const int kvh = head / (a.q_heads / a.kv_heads);
+  const int shift = sp.lk - sp.lq;
+  const int last = a.causal ? row + shift : sp.lk - 1;          // this lane's last key
+  const int last_wave = a.causal ? min(row0 + 31, sp.lq - 1) + shift : sp.lk - 1;
+  const int first_wave = a.causal ? row0 + shift : sp.lk - 1;   // keys up to here are seen by the whole wave
+  const int end = (a.causal ? min(row_wg + 127, sp.lq - 1) + shift : sp.lk - 1) + 1;
+  const int tiles = (end + kKeys - 1) / kKeys;
+
+  bf16x8 q[KS];
+  {
+    const uint16_t *qp = reinterpret_cast<const uint16_t *>(a.q) + (int64_t)(sp.q0 + row) * a.q_stride +
+                         (int64_t)head * D + 8 * h;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      uint4 u = *reinterpret_cast<const uint4 *>(qp + 16 * i);
+      u.x = (u.x & a.q_and) ^ a.q_xor, u.y = (u.y & a.q_and) ^ a.q_xor;
+      u.z = (u.z & a.q_and) ^ a.q_xor, u.w = (u.w & a.q_and) ^ a.q_xor;
+      q[i] = __builtin_bit_cast(bf16x8, u);
+    }
+  }
+  // staging: lane i of run r of a wave writes LDS chunk 64 r + i of the wave's
+  // quarter; the chunk of the row that belongs there is fetched
+  int koff[D / 32], voff[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int chunk = 64 * (D / 32 * wave + i) + lane, r = chunk / (RB / 16), c = chunk % (RB / 16);
+    const int from = (c ^ swizzle<D>(r)) * 16;
+    koff[i] = r * (int)(2 * a.k_stride) + from;
+    voff[i] = r * (int)(2 * a.v_stride) + from;
+  }
+  const uint8_t *kp = reinterpret_cast<const uint8_t *>(a.k) + 2 * ((int64_t)sp.k0 * a.k_stride + (int64_t)kvh * D);
+  const uint8_t *vp = reinterpret_cast<const uint8_t *>(a.v) + 2 * ((int64_t)sp.k0 * a.v_stride + (int64_t)kvh * D);
+  const int k_step = (int)(2 * a.k_stride), v_step = (int)(2 * a.v_stride);
+  auto stage = [&](int t) {
+    const int rows = min(kKeys, sp.lk - kKeys * t), buf = t & 1;
+    stage_tile<D>(kp + (int64_t)kKeys * t * k_step, k_step, rows, buf * TB, wave, koff);
+    stage_tile<D>(vp + (int64_t)kKeys * t * v_step, v_step, rows, (2 + buf) * TB, wave, voff);
+  };
+
+  // read addresses within a tile
+  const uint32_t k_rd = n * RB + ((h ^ swizzle<D>(n)) << 4);    // k-step i: ^ (2 i) << 4
+  const int al = lane & 15, gg = (lane >> 4) & 1;
+  const int vrow = 4 * h + (al >> 2);
+  // dimension tile i: ^ i << 6; keys + 8: ^ 2 << 4 and + 8 rows (D = 64: row + 8
+  // flips the same bit of the swizzle)
+  const uint32_t v_rd = vrow * RB + (((2 * gg + ((al & 3) >> 1)) ^ swizzle<D>(vrow)) << 4) + 8 * (al & 1);
+
+  f32x16 acc[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
+  float m = -INFINITY, base = 0.0f, l = 0.0f;
+
+  if (tiles > 0) stage(0);
+  __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0)
+  __syncthreads();
+  for (int t = 0; t < tiles; ++t) {
+    if (t + 1 < tiles) stage(t + 1);
+    const int j0 = kKeys * t;
+    if (j0 <= last_wave) {
+      const uint32_t kb = (t & 1) * TB + k_rd, vb = (2 + (t & 1)) * TB + v_rd;
+      f32x16 s[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[u][r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
+          const bf16x8 kk = *reinterpret_cast<lds_bf16x8 *>((uintptr_t)((kb ^ (i << 5)) + 32 * RB * u));
+          s[u] = mfma32(kk, q[i], s[u]);
+        }
+      }
+      if (j0 + kKeys - 1 > first_wave) {             // some query does not see some key of the tile
+        const int rel = last - j0 - 4 * h;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[u][r] = 32 * u + 8 * (r >> 2) + (r & 3) <= rel ? s[u][r] : -INFINITY;
+      }
+      float mt = s[0][0];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[u][r]);
+      mt = fmaxf(mt, across32(mt)) * a.abs_scale2;
+      // the running maximum follows only where it is outgrown by 2^8: weights of
+      // up to 2^8 lose nothing, and the sums are rarely rescaled
+      if (__any(mt > m + 8.0f)) {
+        m = fmaxf(m, mt);
+        const float now = m == -INFINITY ? 0.0f : m;
+        const float alpha = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(base - now);
+        base = now;
+        l *= alpha;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) acc[i] *= alpha;
+      }
+      bf16x8 p[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], a.abs_scale2, -base));
+          l += s[u][r];
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          p[2 * u + w] = __builtin_bit_cast(
+              bf16x8, make_uint4(pack_bf16(s[u][8 * w], s[u][8 * w + 1]), pack_bf16(s[u][8 * w + 2], s[u][8 * w + 3]),
+                                 pack_bf16(s[u][8 * w + 4], s[u][8 * w + 5]),
+                                 pack_bf16(s[u][8 * w + 6], s[u][8 * w + 7])));
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+          typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+          const uint32_t at = (vb ^ (i << 6)) + 16 * RB * w;
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)at);
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)((at ^ 32) + 8 * RB));
+          typedef short s16x8 __attribute__((ext_vector_type(8)));
+          acc[i] = mfma32(__builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)), p[w],
+                          acc[i]);
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);              // the next tile is there
+    __syncthreads();
+  }
+  if (row0 >= sp.lq) return;
+  l += across32(l);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      acc[i][r] *= inv;
+      bad |= !(fabsf(acc[i][r]) < INFINITY);
+    }
+  // a weight of 0 times an infinity or a NaN that the query does not see: such
+  // a wave is done over, pair by pair
+  if (__any(bad)) {
+    prompt_wave<D, false>(a, lane, head, sp.q0, sp.lq, sp.k0, sp.lk, row0);
+    if (row0 + 16 < sp.lq) prompt_wave<D, false>(a, lane, head, sp.q0, sp.lq, sp.k0, sp.lk, row0 + 16);
+    return;
+  }
+  if (row0 + n >= sp.lq) return;
+  uint16_t *o = reinterpret_cast<uint16_t *>(a.out) + (int64_t)(sp.q0 + row) * a.out_stride + (int64_t)head * D + 4 * h;
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+      *reinterpret_cast<uint2 *>(o + 32 * i + 2 * r) =
+          make_uint2(pack_bf16(acc[i][r], acc[i][r + 1]), pack_bf16(acc[i][r + 2], acc[i][r + 3]));
 }
 
 // ------------------------------------------------------------ argument checks
@@ -724,6 +947,23 @@ int launch_decode_dim(const DecodeArgs &a, int d, glq_dtype dt, int64_t units, h
                                                                       : launch_decode<FMT, 256>(a, dt, units, st);
 }
 
+template <int D>
+int launch_prompt(const PromptArgs &a, bool f32, dim3 grid, hipStream_t st) {
+  if (f32) {
+    hipLaunchKernelGGL(attn_prompt_f32<D>, grid, dim3(256), 0, st, a);
+    return hip_status(hipGetLastError(), "attn_prompt_f32");
+  }
+  constexpr size_t shm = 4 * kKeys * 2 * D;
+  if constexpr (shm > 64 * 1024) {
+    const int rc = hip_status(hipFuncSetAttribute(reinterpret_cast<const void *>(attn_prompt_bf16<D>),
+                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm),
+                              "hipFuncSetAttribute");
+    if (rc) return rc;
+  }
+  hipLaunchKernelGGL(attn_prompt_bf16<D>, grid, dim3(256), shm, st, a);
+  return hip_status(hipGetLastError(), "attn_prompt_bf16");
+}
+
 }  // namespace
 }  // namespace glq
 
@@ -780,6 +1020,8 @@ extern "C" int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_st
   if (P->total_q < 0 || P->total_k < 0 || P->batch < 0 || P->max_q < 0) return GLQ_ERR_ARG;
   if (!valid_dim(P->head_dim) || P->q_heads > 65536) return GLQ_ERR_UNSUPPORTED;
   if (P->total_q > 0x7FFFFFFF || P->total_k > 0x7FFFFFFF) return GLQ_ERR_UNSUPPORTED;
+  // byte offsets within a tile of 64 rows are 32 bits wide
+  if (P->k_stride > (1 << 22) || P->v_stride > (1 << 22)) return GLQ_ERR_UNSUPPORTED;
   if (P->batch == 0 || P->total_q == 0 || P->max_q == 0) return GLQ_OK;
   if (!P->cu_q || !P->cu_k || (reinterpret_cast<uintptr_t>(P->cu_q) & 3) || (reinterpret_cast<uintptr_t>(P->cu_k) & 3))
     return GLQ_ERR_ARG;
@@ -790,16 +1032,20 @@ extern "C" int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_st
                          !valid_rows(P->v, P->v_stride, P->kv_heads, P->head_dim, P->dt)))
     return GLQ_ERR_ARG;
   const int64_t most = P->max_q < P->total_q ? P->max_q : P->total_q;
-  const int64_t tiles = (most + 63) / 64;
+  const bool f = P->dt == GLQ_F32;
+  const int64_t tiles = f ? (most + 63) / 64 : (most + 127) / 128;
   if (P->batch > 0x7FFFFFFF / (P->q_heads * tiles)) return GLQ_ERR_UNSUPPORTED;
+  const float scale2 = P->scale * 1.4426950408889634f;
   const PromptArgs a = {P->q, P->k, P->v, P->out, P->q_stride, P->k_stride, P->v_stride, P->out_stride, P->total_q,
                         P->total_k, P->cu_q, P->cu_k, P->q_heads, P->kv_heads, (int32_t)tiles,
-                        (flags & GLQ_ATTN_CAUSAL) ? 1 : 0, P->scale * 1.4426950408889634f};
-  const bool f = P->dt == GLQ_F32;
-  auto kern = P->head_dim == 64 ? (f ? attn_prompt_k<64, true> : attn_prompt_k<64, false>)
-              : P->head_dim == 128 ? (f ? attn_prompt_k<128, true> : attn_prompt_k<128, false>)
-                                   : (f ? attn_prompt_k<256, true> : attn_prompt_k<256, false>);
-  hipLaunchKernelGGL(kern, dim3((unsigned)(P->batch * P->q_heads * tiles)), dim3(256), 0,
-                     reinterpret_cast<hipStream_t>(hip_stream), a);
-  return hip_status(hipGetLastError(), "attn_prompt_k");
+                        (flags & GLQ_ATTN_CAUSAL) ? 1 : 0, (int32_t)(P->batch * P->q_heads),
+                        scale2, scale2 == 0.0f ? 1.0f : fabsf(scale2), scale2 == 0.0f ? 0u : 0xFFFFFFFFu,
+                        scale2 < 0.0f ? 0x80008000u : 0u};
+  const dim3 grid((unsigned)(P->batch * P->q_heads * tiles));
+  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  switch (P->head_dim) {
+    case 64: return launch_prompt<64>(a, f, grid, st);
+    case 128: return launch_prompt<128>(a, f, grid, st);
+    default: return launch_prompt<256>(a, f, grid, st);
+  }
 }

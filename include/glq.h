@@ -481,7 +481,7 @@ typedef struct {
  *   dt = GLQ_BF16: bf16 matrix-core path, weights rounded to bf16, float32 sums
  *   dt = GLQ_F32:  float32 products and sums
  * batch == 0, total_q == 0 or max_q == 0 is a successful no-op. out must not
- * overlap q, k or v.
+ * overlap q, k or v. GLQ_ERR_UNSUPPORTED for k_stride or v_stride above 2^22.
  */
 int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_stream);
 
