@@ -200,6 +200,10 @@ struct DecodeArgs {
   int64_t max_pages, max_len;
   int32_t heads, group, row_tiles, page_shift, num_pages;
   float scale2;                // scale * log2(e)
+  int32_t units, chunk;        // batch * heads * row_tiles; tokens of a workgroup (a multiple of 128)
+  int32_t part_floats;         // of one workgroup's partial sums
+  unsigned int *tickets;       // [units], zero between calls
+  float *part;                 // [units][chunks][part_floats]
 };
 
 // The wave works on tiles of 32 cached tokens, two 16-token halves. Scores
@@ -360,21 +364,74 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// max or sum over the four lanes of one column (lane & 15)
+__device__ __forceinline__ float column_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float column_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+// written through to, and read from, the memory side that the eight XCDs share (sc1)
+__device__ __forceinline__ void store_shared(__amdgpu_buffer_rsrc_t r, int at, f32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, 4 * at, 0, 16);
+}
+__device__ __forceinline__ f32x4 load_shared(__amdgpu_buffer_rsrc_t r, int at) {
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, 4 * at, 0, 16));
+}
+
+// A part of a row's sums: values, their maximum and total
+struct Sums {
+  float o[8], top, total;
+};
+__device__ __forceinline__ void merge(Sums &s, const float *o, float top, float total) {
+  const float mn = fmaxf(s.top, top), base = mn == -INFINITY ? 0.0f : mn;
+  const float f = __builtin_amdgcn_exp2f(s.top - base), g = __builtin_amdgcn_exp2f(top - base);
+  s.top = mn;
+  s.total = s.total * f + total * g;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s.o[i] = s.o[i] * f + o[i] * g;
+}
+
+// One workgroup: `chunk` tokens of one (sequence, kept head, up to 16 of its
+// query heads), its waves taking every fourth tile of 32, the next tile's loads
+// in flight while one is worked on. Where a sequence has several chunks each
+// workgroup leaves its sums in the workspace and takes a ticket; the one
+// with the last ticket joins them, in the order of the chunks. (Two waves per
+// SIMD at least where the registers of two tiles leave room for them.)
 template <int FMT, int D, bool F32>
-__global__ void __launch_bounds__(256) attn_decode_k(DecodeArgs a) {
+__global__ void __launch_bounds__(256, D == 256 || F32 ? 1 : 2) attn_decode_k(DecodeArgs a) {
   constexpr int NP = F32 ? 3 : 1, KS = D / 32, DT = D / 16;
   constexpr int WP = F32 ? 3 : 2;                    // bf16 parts of a weight
   constexpr bool BIASED = FMT == GLQ_KV_INT4 && !F32;
   extern __shared__ float shm[];                     // [4][16][D] sums, [4][16] maxima, [4][16] totals
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
-  const int unit = blockIdx.x, rt = unit % a.row_tiles, bh = unit / a.row_tiles;
+  const int unit = blockIdx.x % a.units, chunk_at = blockIdx.x / a.units;
+  const int rt = unit % a.row_tiles, bh = unit / a.row_tiles;
   const int h = bh % a.heads;
   const int64_t b = bh / a.heads;
   const int32_t *table = a.table + b * a.max_pages;
   const int head0 = h * a.group + 16 * rt, rows = min(16, a.group - 16 * rt);
   int len = __builtin_amdgcn_readfirstlane(a.lens[b]);
   len = len < 0 ? 0 : len > a.max_len ? (int)a.max_len : len;
+  const int from = chunk_at * a.chunk;
+  if (from >= len && chunk_at > 0) return;
+  const int chunks = (len + a.chunk - 1) / a.chunk;  // of this sequence
+  const int end = min(len, from + a.chunk);
+
+  // float32 heads of 256 over bf16 rows: two tiles would not fit the registers
+  constexpr bool AHEAD = !(F32 && D == 256 && FMT == GLQ_KV_BF16);
+  Tile<FMT, D> tile[AHEAD ? 2 : 1];
+  const int t0 = from + 32 * wave;
+  if (AHEAD && t0 < end) load_tile<FMT, D>(a, table, h, lane, t0, end, tile[0]);
 
   const int64_t esize = F32 ? 4 : 2;
   bf16x8 q[NP][KS];
@@ -394,19 +451,14 @@ __global__ void __launch_bounds__(256) attn_decode_k(DecodeArgs a) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) q[p][c] = o[p];
   }
-  qsum += __shfl_xor(qsum, 16);
-  qsum += __shfl_xor(qsum, 32);
-  const float s0 = BIASED ? -kBias4 * qsum : 0.0f;
+  const float s0 = BIASED ? -kBias4 * column_sum(qsum) : 0.0f;
 
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, base = 0.0f, l = 0.0f;
   f32x4 acc[DT];
 #pragma unroll
   for (int i = 0; i < DT; ++i) acc[i] = (f32x4){0, 0, 0, 0};
 
-  for (int t = 32 * wave; t < len; t += 128) {
-    Tile<FMT, D> x;
-    load_tile<FMT, D>(a, table, h, lane, t, len, x);
-    const bool tail = t + 32 > len;
+  auto work = [&](Tile<FMT, D> &x, int t) {
     float s[8];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -421,29 +473,34 @@ __global__ void __launch_bounds__(256) attn_decode_k(DecodeArgs a) {
       for (int r = 0; r < 4; ++r)
         s[4 * half + r] = c4[r] * (FMT == GLQ_KV_BF16 ? a.scale2 : a.scale2 * x.ks[4 * half + r]);
     }
-    if (tail) {                                      // tokens past the end: no weight, and values that are 0
+    if (t + 32 > end) {                              // tokens past the end: no weight, and values that are 0
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const bool in = t + 16 * (j >> 2) + 4 * g + (j & 3) < len;
+        const bool in = t + 16 * (j >> 2) + 4 * g + (j & 3) < end;
         s[j] = in ? s[j] : -INFINITY;
-        x.vs[j] = in ? x.vs[j] : 0.0f;
         if constexpr (FMT == GLQ_KV_BF16) {
 #pragma unroll
           for (int w = 0; w < Tile<FMT, D>::VW; ++w) x.v[j][w] = in ? x.v[j][w] : 0u;
+        } else {
+          x.vs[j] = in ? x.vs[j] : 0.0f;
         }
       }
     }
     float mt = s[0];
 #pragma unroll
     for (int j = 1; j < 8; ++j) mt = fmaxf(mt, s[j]);
-    mt = fmaxf(mt, __shfl_xor(mt, 16));
-    mt = fmaxf(mt, __shfl_xor(mt, 32));
-    const float mn = fmaxf(m, mt), base = mn == -INFINITY ? 0.0f : mn;
-    const float alpha = __builtin_amdgcn_exp2f(m - base);
-    m = mn;
-    l *= alpha;
+    mt = column_max(mt);
+    // the running maximum follows only where it is outgrown by 2^8: weights of up
+    // to 2^8 lose nothing, and the sums are rarely rescaled
+    if (__any(mt > m + 8.0f)) {
+      m = fmaxf(m, mt);
+      const float now = m == -INFINITY ? 0.0f : m;
+      const float alpha = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(base - now);
+      base = now;
+      l *= alpha;
 #pragma unroll
-    for (int i = 0; i < DT; ++i) acc[i] *= alpha;
+      for (int i = 0; i < DT; ++i) acc[i] *= alpha;
+    }
     float w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -466,9 +523,20 @@ __global__ void __launch_bounds__(256) attn_decode_k(DecodeArgs a) {
         acc[i] = mfma16(vv, pw[p], acc[i]);
       }
     }
+  };
+  if constexpr (!AHEAD) {
+    for (int t = t0; t < end; t += 128) {
+      load_tile<FMT, D>(a, table, h, lane, t, end, tile[0]);
+      work(tile[0], t);
+    }
+  } else for (int t = t0; t < end; t += 256) {
+    if (t + 128 < end) load_tile<FMT, D>(a, table, h, lane, t + 128, end, tile[1]);
+    work(tile[0], t);
+    if (t + 128 >= end) break;
+    if (t + 256 < end) load_tile<FMT, D>(a, table, h, lane, t + 256, end, tile[0]);
+    work(tile[1], t + 128);
   }
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+  l = column_sum(l);
 
   // join the waves
   float *so = shm, *sm = shm + 4 * 16 * D, *sl = sm + 64;
@@ -476,26 +544,83 @@ __global__ void __launch_bounds__(256) attn_decode_k(DecodeArgs a) {
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) so[(wave * 16 + n) * D + (4 * g + r) * DT + i] = acc[i][r];
-  if (g == 0) sm[16 * wave + n] = m, sl[16 * wave + n] = l;
+  if (g == 0) sm[16 * wave + n] = l == 0.0f ? -INFINITY : base, sl[16 * wave + n] = l;
   __syncthreads();
-  for (int e = threadIdx.x; e < rows * (D / 8); e += 256) {
+  const int items = rows * (D / 8);
+  float *part = a.part + ((int64_t)unit * (int64_t)((a.max_len + a.chunk - 1) / a.chunk)) * a.part_floats;
+  auto finish = [&](int e, const Sums &x) {
     const int row = e / (D / 8), d0 = 8 * (e % (D / 8));
-    float top = -INFINITY;
+    const float inv = x.total == 0.0f ? 0.0f : 1.0f / x.total;
+    float o[8];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, sm[16 * w + row]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    float total = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = __builtin_amdgcn_exp2f(sm[16 * w + row] - base);
-      total += f * sl[16 * w + row];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] += f * so[(16 * w + row) * D + d0 + i];
-    }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= inv;
+    for (int i = 0; i < 8; ++i) o[i] = x.o[i] * inv;
     store8<F32>(reinterpret_cast<uint8_t *>(a.out) + esize * (b * a.out_stride + (int64_t)(head0 + row) * D + d0), o);
+  };
+  for (int e = threadIdx.x; e < items; e += 256) {
+    const int row = e / (D / 8), d0 = 8 * (e % (D / 8));
+    Sums x = {{0, 0, 0, 0, 0, 0, 0, 0}, -INFINITY, 0.0f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) merge(x, &so[(16 * w + row) * D + d0], sm[16 * w + row], sl[16 * w + row]);
+    if (chunks <= 1) {
+      finish(e, x);
+    } else {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          (void *)(part + (int64_t)chunk_at * a.part_floats), 0, 4 * a.part_floats, 0x00020000);
+      store_shared(r, 8 * e, (f32x4){x.o[0], x.o[1], x.o[2], x.o[3]});
+      store_shared(r, 8 * e + 4, (f32x4){x.o[4], x.o[5], x.o[6], x.o[7]});
+      if (d0 == 0) store_shared(r, rows * D + 4 * row, (f32x4){x.top, x.total, 0, 0});
+    }
+  }
+  if (chunks <= 1) return;
+  __builtin_amdgcn_s_waitcnt(0);                     // the sums are at the memory side
+  __syncthreads();
+  int *flag = reinterpret_cast<int *>(sm);
+  if (threadIdx.x == 0)
+    *flag = (int)__hip_atomic_fetch_add(a.tickets + unit, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (*flag != chunks - 1) return;
+  if (threadIdx.x == 0) __hip_atomic_store(a.tickets + unit, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  // few items: slices of the threads take every slices-th chunk, and meet in LDS
+  const int slices = items >= 256 ? 1 : 256 / items;
+  const __amdgpu_buffer_rsrc_t r =
+      __builtin_amdgcn_make_buffer_rsrc((void *)part, 0, 4 * a.part_floats * chunks, 0x00020000);
+  for (int e0 = 0; e0 < items; e0 += 256) {
+    const int e = slices == 1 ? e0 + threadIdx.x : threadIdx.x % items, slice = slices == 1 ? 0 : threadIdx.x / items;
+    Sums x = {{0, 0, 0, 0, 0, 0, 0, 0}, -INFINITY, 0.0f};
+    if (e < items && slice < slices) {
+      const int row = e / (D / 8);
+      for (int c0 = slice; c0 < chunks; c0 += 4 * slices) {
+        f32x4 lo[4], hi[4], mt[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {                // four chunks' loads in flight; past the last: the last, weightless
+          const int c = min(c0 + j * slices, chunks - 1) * a.part_floats;
+          lo[j] = load_shared(r, c + 8 * e), hi[j] = load_shared(r, c + 8 * e + 4);
+          mt[j] = load_shared(r, c + rows * D + 4 * row);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (c0 + j * slices >= chunks) break;
+          const float o[8] = {lo[j][0], lo[j][1], lo[j][2], lo[j][3], hi[j][0], hi[j][1], hi[j][2], hi[j][3]};
+          merge(x, o, mt[j][0], mt[j][1]);
+        }
+      }
+      if (slices == 1) finish(e, x);
+      else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) shm[10 * threadIdx.x + i] = x.o[i];
+        shm[10 * threadIdx.x + 8] = x.top, shm[10 * threadIdx.x + 9] = x.total;
+      }
+    }
+    if (slices == 1) continue;
+    __syncthreads();
+    if ((int)threadIdx.x < items) {
+      for (int s = 1; s < slices; ++s) {
+        const float *y = shm + 10 * (s * items + threadIdx.x);
+        merge(x, y, y[8], y[9]);
+      }
+      finish(e, x);
+    }
   }
 }
 
@@ -927,6 +1052,28 @@ int check_decode(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t 
   return GLQ_OK;
 }
 
+// Tokens a workgroup takes: as many workgroups as keep every CU busy a few
+// times over where the lengths allow, 128 tokens (one tile a wave) at least. A
+// launch of more units than there are ticket counters is not split.
+constexpr int64_t kTickets = GLQ_ATTN_CTRL_BYTES / 4, kDecodeGroups = 2048;
+int64_t decode_chunk(int64_t units, int64_t max_len) {
+  const int64_t tiles = max_len > 0 ? (max_len + 127) / 128 : 1;
+  int64_t want = units > kTickets ? 1 : kDecodeGroups / units;
+  want = want < 1 ? 1 : want > tiles ? tiles : want;
+  return (tiles + want - 1) / want * 128;
+}
+struct DecodePlan { int64_t units, chunk, chunks, part_floats, ws_bytes; };
+DecodePlan decode_plan(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t max_len) {
+  const int64_t group = q_heads / C->kv_heads, rows = group < 16 ? group : 16;
+  DecodePlan p;
+  p.units = batch * C->kv_heads * ((group + 15) / 16);
+  p.chunk = decode_chunk(p.units > 0 ? p.units : 1, max_len);
+  p.chunks = max_len > 0 ? (max_len + p.chunk - 1) / p.chunk : 1;
+  p.part_floats = rows * (C->head_dim + 4);
+  p.ws_bytes = GLQ_ATTN_CTRL_BYTES + (p.chunks > 1 ? p.units * p.chunks * p.part_floats * 4 : 0);
+  return p;
+}
+
 template <int FMT, int D>
 int launch_decode(const DecodeArgs &a, glq_dtype dt, int64_t units, hipStream_t st) {
   const size_t shm = (4 * 16 * D + 128) * sizeof(float);
@@ -982,7 +1129,7 @@ extern "C" int glq_kv_read(const glq_kv_cache *C, const int32_t *slots, int64_t 
 
 extern "C" size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t max_len) {
   if (check_decode(C, batch, q_heads, max_len)) return 0;
-  return GLQ_ATTN_CTRL_BYTES;
+  return (size_t)decode_plan(C, batch, q_heads, max_len).ws_bytes;
 }
 
 extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype dt, int64_t q_stride, int64_t batch,
@@ -998,14 +1145,18 @@ extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype d
       !lens || (!page_table && max_len > 0) || (reinterpret_cast<uintptr_t>(lens) & 3) ||
       (reinterpret_cast<uintptr_t>(page_table) & 3))
     return GLQ_ERR_ARG;
-  if (!workspace || ws_bytes < glq_attn_decode_workspace(C, batch, q_heads, max_len) ||
+  const DecodePlan p = decode_plan(C, batch, q_heads, max_len);
+  if (!workspace || ws_bytes < (size_t)p.ws_bytes ||
       (reinterpret_cast<uintptr_t>(workspace) & 255))
     return GLQ_ERR_WORKSPACE;
   const int32_t group = q_heads / C->kv_heads, tiles = (group + 15) / 16;
   const DecodeArgs a = {C->k, C->v, C->k_scale, C->v_scale, q, out, q_stride, out_stride, page_table, lens, max_pages,
                         max_len, C->kv_heads, group, tiles, log2_of(C->page_size), (int32_t)C->num_pages,
-                        scale * 1.4426950408889634f};
-  const int64_t units = batch * C->kv_heads * tiles;
+                        scale * 1.4426950408889634f, (int32_t)p.units, (int32_t)p.chunk, (int32_t)p.part_floats,
+                        reinterpret_cast<unsigned int *>(workspace),
+                        reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + GLQ_ATTN_CTRL_BYTES)};
+  const int64_t units = p.units * p.chunks;          // workgroups
+  if (units > 0x7FFFFFFF) return GLQ_ERR_UNSUPPORTED;
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   switch (C->format) {
     case GLQ_KV_BF16: return launch_decode_dim<GLQ_KV_BF16>(a, C->head_dim, dt, units, st);
