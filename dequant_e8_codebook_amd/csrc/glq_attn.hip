@@ -190,6 +190,10 @@ __global__ void __launch_bounds__(256) kv_read_k(KvIo io) {
 
 // ------------------------------------------------------------ one new token
 
+constexpr int decode_per_cu(int format, int dim, bool f32) {
+  return dim == 256 ? 1 : dim == 128 ? (f32 ? 1 : format == GLQ_KV_INT4 ? 3 : 2) : f32 ? 2 : 4;
+}
+
 struct DecodeArgs {
   const void *k, *v;
   const float *ks, *vs;
@@ -200,10 +204,10 @@ struct DecodeArgs {
   int64_t max_pages, max_len;
   int32_t heads, group, row_tiles, page_shift, num_pages;
   float scale2;                // scale * log2(e)
-  int32_t units, chunk;        // batch * heads * row_tiles; tokens of a workgroup (a multiple of 128)
-  int32_t part_floats;         // of one workgroup's partial sums
-  unsigned int *tickets;       // [units], zero between calls
-  float *part;                 // [units][chunks][part_floats]
+  int32_t batch, part_floats;  // floats of one workgroup's sums
+  int32_t whole;               // no unit is split
+  unsigned int *tickets;       // [workgroups], zero between calls
+  float *part;                 // [workgroups][part_floats]
 };
 
 // The wave works on tiles of 32 cached tokens, two 16-token halves. Scores
@@ -249,26 +253,39 @@ template <int N> __device__ __forceinline__ void load_words(const uint8_t *p, ui
   }
 }
 
+// what no kernel of this call writes: read by scalar loads where the address is uniform
+typedef __attribute__((address_space(4))) const int32_t *scalar_ints;
+
+// the pages of a tile's two halves (a half past the end repeats the first)
+struct Pages { uint32_t p[2]; };
+__device__ __forceinline__ Pages pages_of(const DecodeArgs &a, scalar_ints table, int t, int end) {
+  Pages x;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int32_t page = table[(t + 16 * s < end ? t + 16 * s : t) >> a.page_shift];
+    x.p[s] = page < 0 ? 0u : page < a.num_pages ? (uint32_t)page : (uint32_t)a.num_pages - 1;
+  }
+  return x;
+}
+
 template <int FMT, int D>
-__device__ __forceinline__ void load_tile(const DecodeArgs &a, const int32_t *table, int h, int lane, int t, int end,
+__device__ __forceinline__ void load_tile(const DecodeArgs &a, const Pages &pages, int h, int lane, int t, int end,
                                           Tile<FMT, D> &x) {
   using T = Tile<FMT, D>;
   const int g = lane >> 4, n = lane & 15;
   const uint8_t *kp = reinterpret_cast<const uint8_t *>(a.k), *vp = reinterpret_cast<const uint8_t *>(a.v);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    const int ts = t + 16 * s < end ? t + 16 * s : t;          // a half past the end repeats the first
-    uint32_t page = (uint32_t)table[ts >> a.page_shift];
-    page = page < (uint32_t)a.num_pages ? page : (int32_t)page < 0 ? 0u : (uint32_t)a.num_pages - 1;
-    const int64_t row = (((int64_t)page * a.heads + h) << a.page_shift) + (ts & ((1 << a.page_shift) - 1));
-    const uint8_t *kr = kp + (row + n) * T::RB;
+    const int ts = t + 16 * s < end ? t + 16 * s : t;
+    const int64_t row = (((int64_t)pages.p[s] * a.heads + h) << a.page_shift) + (ts & ((1 << a.page_shift) - 1));
+    const uint8_t *kr = kp + row * T::RB + n * T::RB;
     if constexpr (T::RB >= 64) {
 #pragma unroll
       for (int i = 0; i < T::RB / 64; ++i) load_words<4>(kr + 64 * i + 16 * g, &x.k[s][4 * i]);
     } else {
       load_words<2>(kr + 8 * g, x.k[s]);
     }
-    const uint8_t *vr = vp + (row + 4 * g) * T::RB + n * T::VB;
+    const uint8_t *vr = vp + row * T::RB + 4 * g * T::RB + n * T::VB;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if constexpr (T::VB == 2) x.v[4 * s + r][0] = *reinterpret_cast<const uint16_t *>(vr + r * T::RB);
@@ -400,226 +417,328 @@ __device__ __forceinline__ void merge(Sums &s, const float *o, float top, float 
   for (int i = 0; i < 8; ++i) s.o[i] = s.o[i] * f + o[i] * g;
 }
 
-// One workgroup: `chunk` tokens of one (sequence, kept head, up to 16 of its
-// query heads), its waves taking every fourth tile of 32, the next tile's loads
-// in flight while one is worked on. Where a sequence has several chunks each
-// workgroup leaves its sums in the workspace and takes a ticket; the one
-// with the last ticket joins them, in the order of the chunks. (Two waves per
-// SIMD at least where the registers of two tiles leave room for them.)
+// What a workgroup does: one part of one unit (a sequence, a kept head and up to
+// 16 of its query heads; 128-token tiles).
+struct Place {
+  int b, unit, part, parts;    // unit within the sequence; of `parts` (0: nothing to do)
+  int tiles;                   // of the unit
+};
+
+__device__ __forceinline__ int length_of(const DecodeArgs &a, int b) {
+  const int len = ((scalar_ints)(uintptr_t)a.lens)[b];
+  return len < 0 ? 0 : len > a.max_len ? (int)a.max_len : len;
+}
+
+// Parts of a unit of `tiles` tiles where a part should have 1 / inv of them.
+// Splitting costs a workgroup what about 5 tiles take (its sums' way to memory,
+// the ticket, and their way back: 8 us of 1.2 us a tile at 512 tokens), so a
+// unit that little longer stays whole. Any value from 1 on is right; every
+// workgroup computes the same one.
+__device__ __forceinline__ int parts_of(int tiles, float inv) {
+  const float n = (float)tiles * inv;
+  return tiles == 0 ? 0 : (float)(tiles - 5) * inv <= 1.0f ? 1 : (int)(n + 0.999f);
+}
+
+// The smallest share for which the launch has workgroups enough for all parts,
+// found by every workgroup alike: up to 64 sequences by trying 64 shares, one a
+// lane; beyond, by parts <= tiles / share + 1.
+__device__ __forceinline__ Place find_place(const DecodeArgs &a, int lane) {
+  const int each = (a.batch + 63) / 64, units = a.heads * a.row_tiles;
+  const int64_t groups = gridDim.x;
+  float inv = 0.0f;
+  int t = 0;
+  if (a.whole) {
+    if (each == 1) t = lane < a.batch ? (length_of(a, lane) + 127) >> 7 : 0;
+  } else if (each == 1) {
+    t = lane < a.batch ? (length_of(a, lane) + 127) >> 7 : 0;
+    int most = t;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) most = max(most, __shfl_xor(most, s));
+    inv = 1.0f / (float)max(1, (int)(((int64_t)most * (lane + 1) + 63) >> 6));
+    int count = 0;
+    for (int b = 0; b < a.batch; ++b) count += parts_of(__builtin_amdgcn_readlane(t, b), inv);
+    const uint64_t fits = __builtin_amdgcn_ballot_w64((int64_t)count * units <= groups);   // the last lane's does
+    inv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), fits ? __builtin_ctzll(fits) : 63));
+  } else {
+    int64_t total = 0;
+    for (int b = lane; b < a.batch; b += 64) total += (length_of(a, b) + 127) >> 7;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) total += __shfl_xor(total, s);
+    inv = 1.0f / (float)(total * units / (groups - (int64_t)a.batch * units) + 2);
+  }
+  int mine = 0;
+  if (each == 1) mine = parts_of(t, inv);
+  else
+    for (int b = lane * each; b < min(a.batch, (lane + 1) * each); ++b) mine += parts_of((length_of(a, b) + 127) >> 7, inv);
+  int upto = mine;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const int o = __shfl_up(upto, s);
+    upto += lane >= s ? o : 0;
+  }
+  Place p = {0, 0, 0, 0, 0};
+  const int at = blockIdx.x;
+  const uint64_t here = __builtin_amdgcn_ballot_w64((upto - mine) * units <= at && at < upto * units);
+  if (!here) return p;
+  const int from = __builtin_ctzll(here);
+  int base = __builtin_amdgcn_readlane(upto - mine, from) * units;
+  p.b = from * each;
+  while (true) {                                     // ends: the part is of one of the lane's sequences
+    p.tiles = (length_of(a, p.b) + 127) >> 7;
+    p.parts = __builtin_amdgcn_readfirstlane(parts_of(p.tiles, inv));
+    if (at < base + p.parts * units) break;
+    base += p.parts * units;
+    ++p.b;
+  }
+  p.unit = (at - base) / p.parts;
+  p.part = (at - base) - p.unit * p.parts;
+  return p;
+}
+
+// The waves of a workgroup take every fourth 32-token tile, the next tile's
+// loads in flight while one is worked on. A unit of several parts: each leaves
+// its sums in the workspace and takes a ticket; the one with the last ticket
+// joins them, in the order of the tiles. Workgroups per CU: what the registers
+// of two tiles leave room for.
 template <int FMT, int D, bool F32>
-__global__ void __launch_bounds__(256, D == 256 || F32 ? 1 : 2) attn_decode_k(DecodeArgs a) {
+__global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode_k(DecodeArgs a) {
   constexpr int NP = F32 ? 3 : 1, KS = D / 32, DT = D / 16;
   constexpr int WP = F32 ? 3 : 2;                    // bf16 parts of a weight
   constexpr bool BIASED = FMT == GLQ_KV_INT4 && !F32;
-  extern __shared__ float shm[];                     // [4][16][D] sums, [4][16] maxima, [4][16] totals
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = lane >> 4, n = lane & 15;
-  const int unit = blockIdx.x % a.units, chunk_at = blockIdx.x / a.units;
-  const int rt = unit % a.row_tiles, bh = unit / a.row_tiles;
-  const int h = bh % a.heads;
-  const int64_t b = bh / a.heads;
-  const int32_t *table = a.table + b * a.max_pages;
-  const int head0 = h * a.group + 16 * rt, rows = min(16, a.group - 16 * rt);
-  int len = __builtin_amdgcn_readfirstlane(a.lens[b]);
-  len = len < 0 ? 0 : len > a.max_len ? (int)a.max_len : len;
-  const int from = chunk_at * a.chunk;
-  if (from >= len && chunk_at > 0) return;
-  const int chunks = (len + a.chunk - 1) / a.chunk;  // of this sequence
-  const int end = min(len, from + a.chunk);
-
   // float32 heads of 256 over bf16 rows: two tiles would not fit the registers
   constexpr bool AHEAD = !(F32 && D == 256 && FMT == GLQ_KV_BF16);
-  Tile<FMT, D> tile[AHEAD ? 2 : 1];
-  const int t0 = from + 32 * wave;
-  if (AHEAD && t0 < end) load_tile<FMT, D>(a, table, h, lane, t0, end, tile[0]);
-
+  extern __shared__ float shm[];                     // [4][16][D] sums, [4][16] maxima, [4][16] totals
+  float *so = shm, *sm = shm + 4 * 16 * D, *sl = sm + 64;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, n = lane & 15;
   const int64_t esize = F32 ? 4 : 2;
-  bf16x8 q[NP][KS];
-  float qsum = 0.0f;
-#pragma unroll
-  for (int c = 0; c < KS; ++c) {
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint8_t *p = reinterpret_cast<const uint8_t *>(a.q) +
-                         esize * (b * a.q_stride + (int64_t)(head0 + (n < rows ? n : 0)) * D + k_dim<FMT, D>(c, g, e));
-      x[e] = F32 ? *reinterpret_cast<const float *>(p) : bf16_lo(*reinterpret_cast<const uint16_t *>(p));
-      qsum += x[e];
-    }
-    bf16x8 o[NP];
-    split8<NP>(x, o);
-#pragma unroll
-    for (int p = 0; p < NP; ++p) q[p][c] = o[p];
-  }
-  const float s0 = BIASED ? -kBias4 * column_sum(qsum) : 0.0f;
-
-  float m = -INFINITY, base = 0.0f, l = 0.0f;
-  f32x4 acc[DT];
-#pragma unroll
-  for (int i = 0; i < DT; ++i) acc[i] = (f32x4){0, 0, 0, 0};
-
-  auto work = [&](Tile<FMT, D> &x, int t) {
-    float s[8];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      f32x4 c4 = {s0, s0, s0, s0};
-#pragma unroll
-      for (int c = 0; c < KS; ++c) {
-        const bf16x8 kk = k_operand<FMT, D, BIASED>(x, half, c);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) c4 = mfma16(kk, q[p][c], c4);
+  const int q_heads = a.heads * a.group;
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x)      // sequences without tokens: zeros
+    if (length_of(a, b) == 0)
+      for (int e = threadIdx.x; e < q_heads * (D / 8); e += 256) {
+        const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        store8<F32>(reinterpret_cast<uint8_t *>(a.out) + esize * (b * a.out_stride + 8 * (int64_t)e), zero);
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        s[4 * half + r] = c4[r] * (FMT == GLQ_KV_BF16 ? a.scale2 : a.scale2 * x.ks[4 * half + r]);
+
+  const Place at = find_place(a, lane);
+  if (at.parts == 0) return;
+  const int rt = at.unit % a.row_tiles, h = at.unit / a.row_tiles;
+  const int head0 = h * a.group + 16 * rt, rows = min(16, a.group - 16 * rt);
+  const int64_t b = at.b;
+  const scalar_ints table = (scalar_ints)(uintptr_t)(a.table + b * a.max_pages);
+  const int tile0 = (int)((int64_t)at.tiles * at.part / at.parts);
+  const int tile1 = (int)((int64_t)at.tiles * (at.part + 1) / at.parts);
+  const int t0 = 128 * tile0 + 32 * wave, end = min(length_of(a, at.b), 128 * tile1);
+  {
+    Tile<FMT, D> tile;
+    Pages next = {{0, 0}};
+    if (t0 < end) {
+      const Pages first = pages_of(a, table, t0, end);
+      next = pages_of(a, table, t0 + 128 < end ? t0 + 128 : t0, end);
+      load_tile<FMT, D>(a, first, h, lane, t0, end, tile);
     }
-    if (t + 32 > end) {                              // tokens past the end: no weight, and values that are 0
+
+    bf16x8 q[NP][KS];
+    float qsum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < KS; ++c) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(a.q) +
+                           esize * (b * a.q_stride + (int64_t)(head0 + (n < rows ? n : 0)) * D + k_dim<FMT, D>(c, g, e));
+        x[e] = F32 ? *reinterpret_cast<const float *>(p) : bf16_lo(*reinterpret_cast<const uint16_t *>(p));
+        qsum += x[e];
+      }
+      bf16x8 o[NP];
+      split8<NP>(x, o);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) q[p][c] = o[p];
+    }
+    const float s0 = BIASED ? -kBias4 * column_sum(qsum) : 0.0f;
+
+    float m = -INFINITY, base = 0.0f, l = 0.0f;
+    f32x4 acc[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i) acc[i] = (f32x4){0, 0, 0, 0};
+
+    auto work = [&](Tile<FMT, D> &x, int t) {
+      float s[8];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        f32x4 c4 = {s0, s0, s0, s0};
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          const bf16x8 kk = k_operand<FMT, D, BIASED>(x, half, c);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) c4 = mfma16(kk, q[p][c], c4);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          s[4 * half + r] = c4[r] * (FMT == GLQ_KV_BF16 ? a.scale2 : a.scale2 * x.ks[4 * half + r]);
+      }
+      if (t + 32 > end) {                            // tokens past the end: no weight, and values that are 0
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool in = t + 16 * (j >> 2) + 4 * g + (j & 3) < end;
+          s[j] = in ? s[j] : -INFINITY;
+          if constexpr (FMT == GLQ_KV_BF16) {
+#pragma unroll
+            for (int w = 0; w < Tile<FMT, D>::VW; ++w) x.v[j][w] = in ? x.v[j][w] : 0u;
+          } else {
+            x.vs[j] = in ? x.vs[j] : 0.0f;
+          }
+        }
+      }
+      float mt = s[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) mt = fmaxf(mt, s[j]);
+      mt = column_max(mt);
+      // the running maximum follows only where it is outgrown by 2^8: weights of
+      // up to 2^8 lose nothing, and the sums are rarely rescaled
+      if (__any(mt > m + 8.0f)) {
+        m = fmaxf(m, mt);
+        const float now = m == -INFINITY ? 0.0f : m;
+        const float alpha = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(base - now);
+        base = now;
+        l *= alpha;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) acc[i] *= alpha;
+      }
+      float w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const bool in = t + 16 * (j >> 2) + 4 * g + (j & 3) < end;
-        s[j] = in ? s[j] : -INFINITY;
-        if constexpr (FMT == GLQ_KV_BF16) {
+        w[j] = __builtin_amdgcn_exp2f(s[j] - base);
+        l += w[j];
+        if constexpr (FMT != GLQ_KV_BF16) w[j] *= x.vs[j];
+      }
+      bf16x8 pw[WP];
+      split8<WP>(w, pw);
+      const uint32_t nb = 0xC1C0C1C0u;               // -kBias4 twice
+      const bf16x8 bias = __builtin_bit_cast(bf16x8, make_uint4(nb, nb, nb, nb));
 #pragma unroll
-          for (int w = 0; w < Tile<FMT, D>::VW; ++w) x.v[j][w] = in ? x.v[j][w] : 0u;
+      for (int i = 0; i < DT; ++i) {
+        const bf16x8 vv = v_operand<FMT, D, BIASED>(x, i);
+#pragma unroll
+        for (int p = 0; p < WP; ++p) {
+          // the 4-bit operand's bias leaves at once, tile by tile: over a long
+          // cache the biased sums would outgrow the result they hide
+          if constexpr (BIASED) acc[i] = mfma16(bias, pw[p], acc[i]);
+          acc[i] = mfma16(vv, pw[p], acc[i]);
+        }
+      }
+    };
+    // The page numbers are read one tile further ahead than the tiles. No branch
+    // lies between a tile's loads and its use but those that skip the use: where
+    // paths with and without newer loads met, the wait for the older ones would
+    // be a wait for all.
+    auto ahead = [&](int t, Tile<FMT, D> &x) {
+      const Pages now = next;
+      next = pages_of(a, table, t + 128 < end ? t + 128 : t, end);
+      load_tile<FMT, D>(a, now, h, lane, t, end, x);
+    };
+    if (t0 < end) {
+      int t = t0;
+      for (; t + 128 < end; t += 128) {
+        if constexpr (AHEAD) {
+          Tile<FMT, D> x;
+          ahead(t + 128, x);
+          __builtin_amdgcn_sched_barrier(0);         // the loads go out before the work
+          work(tile, t);
+          tile = x;
         } else {
-          x.vs[j] = in ? x.vs[j] : 0.0f;
+          work(tile, t);
+          ahead(t + 128, tile);
         }
       }
+      work(tile, t);
     }
-    float mt = s[0];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) mt = fmaxf(mt, s[j]);
-    mt = column_max(mt);
-    // the running maximum follows only where it is outgrown by 2^8: weights of up
-    // to 2^8 lose nothing, and the sums are rarely rescaled
-    if (__any(mt > m + 8.0f)) {
-      m = fmaxf(m, mt);
-      const float now = m == -INFINITY ? 0.0f : m;
-      const float alpha = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(base - now);
-      base = now;
-      l *= alpha;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) acc[i] *= alpha;
-    }
-    float w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[j] = __builtin_amdgcn_exp2f(s[j] - base);
-      l += w[j];
-      if constexpr (FMT != GLQ_KV_BF16) w[j] *= x.vs[j];
-    }
-    bf16x8 pw[WP];
-    split8<WP>(w, pw);
-    const uint32_t nb = 0xC1C0C1C0u;                 // -kBias4 twice
-    const bf16x8 bias = __builtin_bit_cast(bf16x8, make_uint4(nb, nb, nb, nb));
-#pragma unroll
-    for (int i = 0; i < DT; ++i) {
-      const bf16x8 vv = v_operand<FMT, D, BIASED>(x, i);
-#pragma unroll
-      for (int p = 0; p < WP; ++p) {
-        // the 4-bit operand's bias leaves at once, tile by tile: over a long
-        // cache the biased sums would outgrow the result they hide
-        if constexpr (BIASED) acc[i] = mfma16(bias, pw[p], acc[i]);
-        acc[i] = mfma16(vv, pw[p], acc[i]);
-      }
-    }
-  };
-  if constexpr (!AHEAD) {
-    for (int t = t0; t < end; t += 128) {
-      load_tile<FMT, D>(a, table, h, lane, t, end, tile[0]);
-      work(tile[0], t);
-    }
-  } else for (int t = t0; t < end; t += 256) {
-    if (t + 128 < end) load_tile<FMT, D>(a, table, h, lane, t + 128, end, tile[1]);
-    work(tile[0], t);
-    if (t + 128 >= end) break;
-    if (t + 256 < end) load_tile<FMT, D>(a, table, h, lane, t + 256, end, tile[0]);
-    work(tile[1], t + 128);
-  }
-  l = column_sum(l);
+    l = column_sum(l);
 
-  // join the waves
-  float *so = shm, *sm = shm + 4 * 16 * D, *sl = sm + 64;
+    // join the waves
 #pragma unroll
-  for (int i = 0; i < DT; ++i)
+    for (int i = 0; i < DT; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) so[(wave * 16 + n) * D + (4 * g + r) * DT + i] = acc[i][r];
-  if (g == 0) sm[16 * wave + n] = l == 0.0f ? -INFINITY : base, sl[16 * wave + n] = l;
-  __syncthreads();
-  const int items = rows * (D / 8);
-  float *part = a.part + ((int64_t)unit * (int64_t)((a.max_len + a.chunk - 1) / a.chunk)) * a.part_floats;
-  auto finish = [&](int e, const Sums &x) {
-    const int row = e / (D / 8), d0 = 8 * (e % (D / 8));
-    const float inv = x.total == 0.0f ? 0.0f : 1.0f / x.total;
-    float o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = x.o[i] * inv;
-    store8<F32>(reinterpret_cast<uint8_t *>(a.out) + esize * (b * a.out_stride + (int64_t)(head0 + row) * D + d0), o);
-  };
-  for (int e = threadIdx.x; e < items; e += 256) {
-    const int row = e / (D / 8), d0 = 8 * (e % (D / 8));
-    Sums x = {{0, 0, 0, 0, 0, 0, 0, 0}, -INFINITY, 0.0f};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) merge(x, &so[(16 * w + row) * D + d0], sm[16 * w + row], sl[16 * w + row]);
-    if (chunks <= 1) {
-      finish(e, x);
-    } else {
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          (void *)(part + (int64_t)chunk_at * a.part_floats), 0, 4 * a.part_floats, 0x00020000);
-      store_shared(r, 8 * e, (f32x4){x.o[0], x.o[1], x.o[2], x.o[3]});
-      store_shared(r, 8 * e + 4, (f32x4){x.o[4], x.o[5], x.o[6], x.o[7]});
-      if (d0 == 0) store_shared(r, rows * D + 4 * row, (f32x4){x.top, x.total, 0, 0});
-    }
-  }
-  if (chunks <= 1) return;
-  __builtin_amdgcn_s_waitcnt(0);                     // the sums are at the memory side
-  __syncthreads();
-  int *flag = reinterpret_cast<int *>(sm);
-  if (threadIdx.x == 0)
-    *flag = (int)__hip_atomic_fetch_add(a.tickets + unit, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (*flag != chunks - 1) return;
-  if (threadIdx.x == 0) __hip_atomic_store(a.tickets + unit, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  // few items: slices of the threads take every slices-th chunk, and meet in LDS
-  const int slices = items >= 256 ? 1 : 256 / items;
-  const __amdgpu_buffer_rsrc_t r =
-      __builtin_amdgcn_make_buffer_rsrc((void *)part, 0, 4 * a.part_floats * chunks, 0x00020000);
-  for (int e0 = 0; e0 < items; e0 += 256) {
-    const int e = slices == 1 ? e0 + threadIdx.x : threadIdx.x % items, slice = slices == 1 ? 0 : threadIdx.x / items;
-    Sums x = {{0, 0, 0, 0, 0, 0, 0, 0}, -INFINITY, 0.0f};
-    if (e < items && slice < slices) {
-      const int row = e / (D / 8);
-      for (int c0 = slice; c0 < chunks; c0 += 4 * slices) {
-        f32x4 lo[4], hi[4], mt[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {                // four chunks' loads in flight; past the last: the last, weightless
-          const int c = min(c0 + j * slices, chunks - 1) * a.part_floats;
-          lo[j] = load_shared(r, c + 8 * e), hi[j] = load_shared(r, c + 8 * e + 4);
-          mt[j] = load_shared(r, c + rows * D + 4 * row);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (c0 + j * slices >= chunks) break;
-          const float o[8] = {lo[j][0], lo[j][1], lo[j][2], lo[j][3], hi[j][0], hi[j][1], hi[j][2], hi[j][3]};
-          merge(x, o, mt[j][0], mt[j][1]);
-        }
-      }
-      if (slices == 1) finish(e, x);
-      else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) shm[10 * threadIdx.x + i] = x.o[i];
-        shm[10 * threadIdx.x + 8] = x.top, shm[10 * threadIdx.x + 9] = x.total;
-      }
-    }
-    if (slices == 1) continue;
+      for (int r = 0; r < 4; ++r) so[(wave * 16 + n) * D + (4 * g + r) * DT + i] = acc[i][r];
+    if (g == 0) sm[16 * wave + n] = l == 0.0f ? -INFINITY : base, sl[16 * wave + n] = l;
     __syncthreads();
-    if ((int)threadIdx.x < items) {
-      for (int s = 1; s < slices; ++s) {
-        const float *y = shm + 10 * (s * items + threadIdx.x);
-        merge(x, y, y[8], y[9]);
+    const int items = rows * (D / 8);
+    auto finish = [&](int e, const Sums &x) {
+      const int row = e / (D / 8), d0 = 8 * (e % (D / 8));
+      const float inv = x.total == 0.0f ? 0.0f : 1.0f / x.total;
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = x.o[i] * inv;
+      store8<F32>(reinterpret_cast<uint8_t *>(a.out) + esize * (b * a.out_stride + (int64_t)(head0 + row) * D + d0), o);
+    };
+    const int first = blockIdx.x - at.part, count = at.parts;
+    const __amdgpu_buffer_rsrc_t mine = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(a.part + (int64_t)blockIdx.x * a.part_floats), 0, 4 * a.part_floats, 0x00020000);
+    for (int e = threadIdx.x; e < items; e += 256) {
+      const int row = e / (D / 8), d0 = 8 * (e % (D / 8));
+      Sums x = {{0, 0, 0, 0, 0, 0, 0, 0}, -INFINITY, 0.0f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) merge(x, &so[(16 * w + row) * D + d0], sm[16 * w + row], sl[16 * w + row]);
+      if (count == 1) {
+        finish(e, x);
+      } else {
+        store_shared(mine, 8 * e, (f32x4){x.o[0], x.o[1], x.o[2], x.o[3]});
+        store_shared(mine, 8 * e + 4, (f32x4){x.o[4], x.o[5], x.o[6], x.o[7]});
+        if (d0 == 0) store_shared(mine, rows * D + 4 * row, (f32x4){x.top, x.total, 0, 0});
       }
-      finish(e, x);
+    }
+    if (count > 1) {
+      __builtin_amdgcn_s_waitcnt(0);                 // the sums are at the memory side
+      __syncthreads();
+      int *flag = reinterpret_cast<int *>(sm);
+      if (threadIdx.x == 0)
+        *flag = (int)__hip_atomic_fetch_add(a.tickets + first, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      if (*flag == count - 1) {
+        if (threadIdx.x == 0) __hip_atomic_store(a.tickets + first, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        // few items: slices of the threads take every slices-th part, and meet in LDS
+        const int slices = items >= 256 ? 1 : 256 / items;
+        const __amdgpu_buffer_rsrc_t all =
+            __builtin_amdgcn_make_buffer_rsrc((void *)(a.part + (int64_t)first * a.part_floats), 0,
+                                              4 * a.part_floats * count, 0x00020000);
+        for (int e0 = 0; e0 < items; e0 += 256) {
+          const int e = slices == 1 ? e0 + threadIdx.x : threadIdx.x % items;
+          const int slice = slices == 1 ? 0 : threadIdx.x / items;
+          Sums x = {{0, 0, 0, 0, 0, 0, 0, 0}, -INFINITY, 0.0f};
+          if (e < items && slice < slices) {
+            const int row = e / (D / 8);
+            for (int c0 = slice; c0 < count; c0 += 4 * slices) {
+              f32x4 lo[4], hi[4], mt[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {          // four parts' loads in flight; past the last: the last, unused
+                const int p = min(c0 + j * slices, count - 1) * a.part_floats;
+                lo[j] = load_shared(all, p + 8 * e), hi[j] = load_shared(all, p + 8 * e + 4);
+                mt[j] = load_shared(all, p + rows * D + 4 * row);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (c0 + j * slices >= count) break;
+                const float o[8] = {lo[j][0], lo[j][1], lo[j][2], lo[j][3], hi[j][0], hi[j][1], hi[j][2], hi[j][3]};
+                merge(x, o, mt[j][0], mt[j][1]);
+              }
+            }
+            if (slices == 1) finish(e, x);
+          }
+          if (slices == 1) continue;
+          __syncthreads();                           // everyone has read the flag
+#pragma unroll
+          for (int i = 0; i < 8; ++i) shm[10 * threadIdx.x + i] = x.o[i];
+          shm[10 * threadIdx.x + 8] = x.top, shm[10 * threadIdx.x + 9] = x.total;
+          __syncthreads();
+          if ((int)threadIdx.x < items) {
+            for (int s = 1; s < slices; ++s) {
+              const float *y = shm + 10 * (s * items + threadIdx.x);
+              merge(x, y, y[8], y[9]);
+            }
+            finish(e, x);
+          }
+        }
+      }
     }
   }
 }
@@ -1052,30 +1171,27 @@ int check_decode(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t 
   return GLQ_OK;
 }
 
-// Tokens a workgroup takes: as many workgroups as keep every CU busy a few
-// times over where the lengths allow, 128 tokens (one tile a wave) at least. A
-// launch of more units than there are ticket counters is not split.
-constexpr int64_t kTickets = GLQ_ATTN_CTRL_BYTES / 4, kDecodeGroups = 2048;
-int64_t decode_chunk(int64_t units, int64_t max_len) {
-  const int64_t tiles = max_len > 0 ? (max_len + 127) / 128 : 1;
-  int64_t want = units > kTickets ? 1 : kDecodeGroups / units;
-  want = want < 1 ? 1 : want > tiles ? tiles : want;
-  return (tiles + want - 1) / want * 128;
-}
-struct DecodePlan { int64_t units, chunk, chunks, part_floats, ws_bytes; };
-DecodePlan decode_plan(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t max_len) {
+// Workgroups of a launch: as many as run at once, or half of that more than
+// there are units where these are many; the units' parts are made to fit. Past
+// the ticket counters (one a workgroup) units are not split.
+constexpr int64_t kCus = 256, kTickets = GLQ_ATTN_CTRL_BYTES / 4;
+struct DecodePlan { int64_t groups, part_floats, ws_bytes; bool whole; };
+DecodePlan decode_plan(const glq_kv_cache *C, int dt, int64_t batch, int32_t q_heads, int64_t max_len) {
   const int64_t group = q_heads / C->kv_heads, rows = group < 16 ? group : 16;
+  const int64_t units = batch * C->kv_heads * ((group + 15) / 16), tiles = (max_len + 127) / 128;
+  const int64_t once = kCus * decode_per_cu(C->format, C->head_dim, dt == GLQ_F32);
   DecodePlan p;
-  p.units = batch * C->kv_heads * ((group + 15) / 16);
-  p.chunk = decode_chunk(p.units > 0 ? p.units : 1, max_len);
-  p.chunks = max_len > 0 ? (max_len + p.chunk - 1) / p.chunk : 1;
+  p.groups = once > units + once / 2 ? once : units + once / 2;
+  p.whole = p.groups > kTickets || tiles <= 1;
+  if (p.whole) p.groups = units;
+  else if (batch <= 64 && p.groups > units * tiles) p.groups = units * tiles;   // a part is a tile at least
   p.part_floats = rows * (C->head_dim + 4);
-  p.ws_bytes = GLQ_ATTN_CTRL_BYTES + (p.chunks > 1 ? p.units * p.chunks * p.part_floats * 4 : 0);
+  p.ws_bytes = GLQ_ATTN_CTRL_BYTES + (p.whole ? 0 : p.groups * p.part_floats * 4);
   return p;
 }
 
 template <int FMT, int D>
-int launch_decode(const DecodeArgs &a, glq_dtype dt, int64_t units, hipStream_t st) {
+int launch_decode(const DecodeArgs &a, glq_dtype dt, int64_t groups, hipStream_t st) {
   const size_t shm = (4 * 16 * D + 128) * sizeof(float);
   auto kern = dt == GLQ_F32 ? attn_decode_k<FMT, D, true> : attn_decode_k<FMT, D, false>;
   if (shm > 64 * 1024) {
@@ -1084,14 +1200,14 @@ int launch_decode(const DecodeArgs &a, glq_dtype dt, int64_t units, hipStream_t 
                               "hipFuncSetAttribute");
     if (rc) return rc;
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)units), dim3(256), shm, st, a);
+  hipLaunchKernelGGL(kern, dim3((unsigned)groups), dim3(256), shm, st, a);
   return hip_status(hipGetLastError(), "attn_decode_k");
 }
 
 template <int FMT>
-int launch_decode_dim(const DecodeArgs &a, int d, glq_dtype dt, int64_t units, hipStream_t st) {
-  return d == 64 ? launch_decode<FMT, 64>(a, dt, units, st) : d == 128 ? launch_decode<FMT, 128>(a, dt, units, st)
-                                                                      : launch_decode<FMT, 256>(a, dt, units, st);
+int launch_decode_dim(const DecodeArgs &a, int d, glq_dtype dt, int64_t groups, hipStream_t st) {
+  return d == 64 ? launch_decode<FMT, 64>(a, dt, groups, st) : d == 128 ? launch_decode<FMT, 128>(a, dt, groups, st)
+                                                                      : launch_decode<FMT, 256>(a, dt, groups, st);
 }
 
 template <int D>
@@ -1129,7 +1245,9 @@ extern "C" int glq_kv_read(const glq_kv_cache *C, const int32_t *slots, int64_t 
 
 extern "C" size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t max_len) {
   if (check_decode(C, batch, q_heads, max_len)) return 0;
-  return (size_t)decode_plan(C, batch, q_heads, max_len).ws_bytes;
+  const int64_t f = decode_plan(C, GLQ_F32, batch, q_heads, max_len).ws_bytes;
+  const int64_t b = decode_plan(C, GLQ_BF16, batch, q_heads, max_len).ws_bytes;
+  return (size_t)(f > b ? f : b);
 }
 
 extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype dt, int64_t q_stride, int64_t batch,
@@ -1140,28 +1258,27 @@ extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype d
   if (rc) return rc;
   if (!valid_dtype(dt) || !std::isfinite(scale) || max_pages < 0) return GLQ_ERR_ARG;
   if (batch == 0) return GLQ_OK;
-  if (max_len > max_pages * C->page_size) return GLQ_ERR_ARG;
+  if (max_len > (max_pages < 0x7FFFFFFF ? max_pages : 0x7FFFFFFF) * C->page_size) return GLQ_ERR_ARG;
   if (!valid_rows(q, q_stride, q_heads, C->head_dim, dt) || !valid_rows(out, out_stride, q_heads, C->head_dim, dt) ||
       !lens || (!page_table && max_len > 0) || (reinterpret_cast<uintptr_t>(lens) & 3) ||
       (reinterpret_cast<uintptr_t>(page_table) & 3))
     return GLQ_ERR_ARG;
-  const DecodePlan p = decode_plan(C, batch, q_heads, max_len);
+  const DecodePlan p = decode_plan(C, dt, batch, q_heads, max_len);
   if (!workspace || ws_bytes < (size_t)p.ws_bytes ||
       (reinterpret_cast<uintptr_t>(workspace) & 255))
     return GLQ_ERR_WORKSPACE;
   const int32_t group = q_heads / C->kv_heads, tiles = (group + 15) / 16;
   const DecodeArgs a = {C->k, C->v, C->k_scale, C->v_scale, q, out, q_stride, out_stride, page_table, lens, max_pages,
                         max_len, C->kv_heads, group, tiles, log2_of(C->page_size), (int32_t)C->num_pages,
-                        scale * 1.4426950408889634f, (int32_t)p.units, (int32_t)p.chunk, (int32_t)p.part_floats,
+                        scale * 1.4426950408889634f, (int32_t)batch, (int32_t)p.part_floats,
+                        p.whole ? 1 : 0,
                         reinterpret_cast<unsigned int *>(workspace),
                         reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + GLQ_ATTN_CTRL_BYTES)};
-  const int64_t units = p.units * p.chunks;          // workgroups
-  if (units > 0x7FFFFFFF) return GLQ_ERR_UNSUPPORTED;
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   switch (C->format) {
-    case GLQ_KV_BF16: return launch_decode_dim<GLQ_KV_BF16>(a, C->head_dim, dt, units, st);
-    case GLQ_KV_INT8: return launch_decode_dim<GLQ_KV_INT8>(a, C->head_dim, dt, units, st);
-    default: return launch_decode_dim<GLQ_KV_INT4>(a, C->head_dim, dt, units, st);
+    case GLQ_KV_BF16: return launch_decode_dim<GLQ_KV_BF16>(a, C->head_dim, dt, p.groups, st);
+    case GLQ_KV_INT8: return launch_decode_dim<GLQ_KV_INT8>(a, C->head_dim, dt, p.groups, st);
+    default: return launch_decode_dim<GLQ_KV_INT4>(a, C->head_dim, dt, p.groups, st);
   }
 }
 
