@@ -203,7 +203,7 @@ struct DecodeArgs {
   const int32_t *table, *lens;
   int64_t max_pages, max_len;
   int32_t heads, group, row_tiles, page_shift, num_pages;
-  float scale2;                // scale * log2(e)
+  float abs_scale2, q_sign;    // |scale| log2(e) and the sign; for a scale of 0, 1 and 0
   int32_t batch, part_floats;  // floats of one workgroup's sums
   int32_t whole;               // no unit is split
   unsigned int *tickets;       // [workgroups], zero between calls
@@ -302,9 +302,14 @@ __device__ __forceinline__ void load_tile(const DecodeArgs &a, const Pages &page
 
 // nibble j of each 16-bit half as bf16 16 + code + 8: the code's 4 bits go
 // into the top of the mantissa of 16
-__device__ __forceinline__ uint32_t nibbles(uint32_t x, int j) {
+struct Nibbles {
+  uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+  // kept in registers: v_and_or_b32 takes no literals, and as literals they cost an instruction more
+  __device__ __forceinline__ Nibbles() { asm("" : "+v"(mask), "+v"(sixteen)); }
+};
+__device__ __forceinline__ uint32_t nibbles(uint32_t x, int j, const Nibbles &c) {
   const uint32_t y = j == 0 ? x << 3 : x >> (4 * j - 3);
-  return (y & 0x00780078u) | 0x41804180u;
+  return (y & c.mask) | c.sixteen;
 }
 constexpr float kBias4 = 24.0f;                      // what nibbles() adds to a code
 // the same pair as the codes themselves (float32 path: the biased sums would
@@ -312,13 +317,13 @@ constexpr float kBias4 = 24.0f;                      // what nibbles() adds to a
 __device__ __forceinline__ uint32_t nibbles_unbiased(uint32_t x, int j) {
   return pack_high((float)((x >> (4 * j)) & 15u) - 8.0f, (float)((x >> (16 + 4 * j)) & 15u) - 8.0f);
 }
-template <bool BIASED> __device__ __forceinline__ uint32_t nibble_pair(uint32_t x, int j) {
-  if constexpr (BIASED) return nibbles(x, j);
+template <bool BIASED> __device__ __forceinline__ uint32_t nibble_pair(uint32_t x, int j, const Nibbles &c) {
+  if constexpr (BIASED) return nibbles(x, j, c);
   else return nibbles_unbiased(x, j);
 }
 
 template <int FMT, int D, bool BIASED>
-__device__ __forceinline__ bf16x8 k_operand(const Tile<FMT, D> &x, int s, int c) {
+__device__ __forceinline__ bf16x8 k_operand(const Tile<FMT, D> &x, int s, int c, const Nibbles &nib) {
   uint4 u;
   if constexpr (FMT == GLQ_KV_BF16) {
     u = make_uint4(x.k[s][4 * c], x.k[s][4 * c + 1], x.k[s][4 * c + 2], x.k[s][4 * c + 3]);
@@ -330,15 +335,15 @@ __device__ __forceinline__ bf16x8 k_operand(const Tile<FMT, D> &x, int s, int c)
     u.w = pack_high((float)(int8_t)(b >> 16), (float)(int8_t)(b >> 24));
   } else {
     const uint32_t a = x.k[s][c];
-    u = make_uint4(nibble_pair<BIASED>(a, 0), nibble_pair<BIASED>(a, 1), nibble_pair<BIASED>(a, 2),
-                   nibble_pair<BIASED>(a, 3));
+    u = make_uint4(nibble_pair<BIASED>(a, 0, nib), nibble_pair<BIASED>(a, 1, nib), nibble_pair<BIASED>(a, 2, nib),
+                   nibble_pair<BIASED>(a, 3, nib));
   }
   return __builtin_bit_cast(bf16x8, u);
 }
 
 // dimension n D / 16 + i of the lane's 8 tokens
 template <int FMT, int D, bool BIASED>
-__device__ __forceinline__ bf16x8 v_operand(const Tile<FMT, D> &x, int i) {
+__device__ __forceinline__ bf16x8 v_operand(const Tile<FMT, D> &x, int i, const Nibbles &nib) {
   uint32_t u[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
@@ -350,7 +355,7 @@ __device__ __forceinline__ bf16x8 v_operand(const Tile<FMT, D> &x, int i) {
     } else {
       const uint32_t w = __builtin_amdgcn_perm(x.v[2 * p + 1][i >> 3], x.v[2 * p][i >> 3],
                                                (i & 4) ? 0x07060302u : 0x05040100u);
-      u[p] = nibble_pair<BIASED>(w, i & 3);
+      u[p] = nibble_pair<BIASED>(w, i & 3, nib);
     }
   }
   return __builtin_bit_cast(bf16x8, make_uint4(u[0], u[1], u[2], u[3]));
@@ -439,45 +444,53 @@ __device__ __forceinline__ int parts_of(int tiles, float inv) {
   return tiles == 0 ? 0 : (float)(tiles - 5) * inv <= 1.0f ? 1 : (int)(n + 0.999f);
 }
 
+// inclusive sum, or maximum of values from 0 on, over the lanes up to each (DPP
+// row shifts and broadcasts; the whole wave's in lane 63)
+template <bool MAX> __device__ __forceinline__ int wave_scan(int x) {
+  auto with = [](int a, int b) { return MAX ? (a > b ? a : b) : a + b; };
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));   // row_shr 1, 2, 4, 8
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));   // row_bcast 15 into rows 1 and 3
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));   // row_bcast 31 into rows 2 and 3
+  return x;
+}
+
 // The smallest share for which the launch has workgroups enough for all parts,
 // found by every workgroup alike: up to 64 sequences by trying 64 shares, one a
 // lane; beyond, by parts <= tiles / share + 1.
 __device__ __forceinline__ Place find_place(const DecodeArgs &a, int lane) {
-  const int each = (a.batch + 63) / 64, units = a.heads * a.row_tiles;
-  const int64_t groups = gridDim.x;
-  float inv = 0.0f;
-  int t = 0;
+  const int each = (a.batch + 63) / 64, units = a.heads * a.row_tiles, at = blockIdx.x;
+  Place p = {0, 0, 0, 0, 0};
   if (a.whole) {
-    if (each == 1) t = lane < a.batch ? (length_of(a, lane) + 127) >> 7 : 0;
-  } else if (each == 1) {
-    t = lane < a.batch ? (length_of(a, lane) + 127) >> 7 : 0;
-    int most = t;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) most = max(most, __shfl_xor(most, s));
+    p.b = at / units;
+    p.unit = at - p.b * units;
+    p.tiles = (length_of(a, p.b) + 127) >> 7;
+    p.parts = p.tiles > 0 ? 1 : 0;
+    return p;
+  }
+  const int64_t groups = gridDim.x;
+  float inv;
+  int mine = 0;
+  if (each == 1) {
+    const int t = lane < a.batch ? (length_of(a, lane) + 127) >> 7 : 0;
+    const int most = __builtin_amdgcn_readlane(wave_scan<true>(t), 63);
     inv = 1.0f / (float)max(1, (int)(((int64_t)most * (lane + 1) + 63) >> 6));
     int count = 0;
     for (int b = 0; b < a.batch; ++b) count += parts_of(__builtin_amdgcn_readlane(t, b), inv);
     const uint64_t fits = __builtin_amdgcn_ballot_w64((int64_t)count * units <= groups);   // the last lane's does
     inv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), fits ? __builtin_ctzll(fits) : 63));
+    mine = parts_of(t, inv);
   } else {
     int64_t total = 0;
     for (int b = lane; b < a.batch; b += 64) total += (length_of(a, b) + 127) >> 7;
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) total += __shfl_xor(total, s);
     inv = 1.0f / (float)(total * units / (groups - (int64_t)a.batch * units) + 2);
-  }
-  int mine = 0;
-  if (each == 1) mine = parts_of(t, inv);
-  else
     for (int b = lane * each; b < min(a.batch, (lane + 1) * each); ++b) mine += parts_of((length_of(a, b) + 127) >> 7, inv);
-  int upto = mine;
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) {
-    const int o = __shfl_up(upto, s);
-    upto += lane >= s ? o : 0;
   }
-  Place p = {0, 0, 0, 0, 0};
-  const int at = blockIdx.x;
+  const int upto = wave_scan<false>(mine);
   const uint64_t here = __builtin_amdgcn_ballot_w64((upto - mine) * units <= at && at < upto * units);
   if (!here) return p;
   const int from = __builtin_ctzll(here);
@@ -548,6 +561,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode
         const uint8_t *p = reinterpret_cast<const uint8_t *>(a.q) +
                            esize * (b * a.q_stride + (int64_t)(head0 + (n < rows ? n : 0)) * D + k_dim<FMT, D>(c, g, e));
         x[e] = F32 ? *reinterpret_cast<const float *>(p) : bf16_lo(*reinterpret_cast<const uint16_t *>(p));
+        x[e] = a.q_sign == 0.0f ? 0.0f : x[e] * a.q_sign;
         qsum += x[e];
       }
       bf16x8 o[NP];
@@ -562,6 +576,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode
 #pragma unroll
     for (int i = 0; i < DT; ++i) acc[i] = (f32x4){0, 0, 0, 0};
 
+    const Nibbles nib;
     auto work = [&](Tile<FMT, D> &x, int t) {
       float s[8];
 #pragma unroll
@@ -569,13 +584,13 @@ __global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode
         f32x4 c4 = {s0, s0, s0, s0};
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
-          const bf16x8 kk = k_operand<FMT, D, BIASED>(x, half, c);
+          const bf16x8 kk = k_operand<FMT, D, BIASED>(x, half, c, nib);
 #pragma unroll
           for (int p = 0; p < NP; ++p) c4 = mfma16(kk, q[p][c], c4);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          s[4 * half + r] = c4[r] * (FMT == GLQ_KV_BF16 ? a.scale2 : a.scale2 * x.ks[4 * half + r]);
+          s[4 * half + r] = FMT == GLQ_KV_BF16 ? c4[r] : c4[r] * x.ks[4 * half + r];
       }
       if (t + 32 > end) {                            // tokens past the end: no weight, and values that are 0
 #pragma unroll
@@ -593,7 +608,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode
       float mt = s[0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) mt = fmaxf(mt, s[j]);
-      mt = column_max(mt);
+      mt = column_max(mt) * a.abs_scale2;
       // the running maximum follows only where it is outgrown by 2^8: weights of
       // up to 2^8 lose nothing, and the sums are rarely rescaled
       if (__any(mt > m + 8.0f)) {
@@ -608,7 +623,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode
       float w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        w[j] = __builtin_amdgcn_exp2f(s[j] - base);
+        w[j] = __builtin_amdgcn_exp2f(fmaf(s[j], a.abs_scale2, -base));
         l += w[j];
         if constexpr (FMT != GLQ_KV_BF16) w[j] *= x.vs[j];
       }
@@ -618,7 +633,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode
       const bf16x8 bias = __builtin_bit_cast(bf16x8, make_uint4(nb, nb, nb, nb));
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
-        const bf16x8 vv = v_operand<FMT, D, BIASED>(x, i);
+        const bf16x8 vv = v_operand<FMT, D, BIASED>(x, i, nib);
 #pragma unroll
         for (int p = 0; p < WP; ++p) {
           // the 4-bit operand's bias leaves at once, tile by tile: over a long
@@ -707,16 +722,16 @@ __global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode
           Sums x = {{0, 0, 0, 0, 0, 0, 0, 0}, -INFINITY, 0.0f};
           if (e < items && slice < slices) {
             const int row = e / (D / 8);
-            for (int c0 = slice; c0 < count; c0 += 4 * slices) {
-              f32x4 lo[4], hi[4], mt[4];
+            for (int c0 = slice; c0 < count; c0 += 8 * slices) {
+              f32x4 lo[8], hi[8], mt[8];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {          // four parts' loads in flight; past the last: the last, unused
+              for (int j = 0; j < 8; ++j) {          // eight parts' loads in flight; past the last: the last, unused
                 const int p = min(c0 + j * slices, count - 1) * a.part_floats;
                 lo[j] = load_shared(all, p + 8 * e), hi[j] = load_shared(all, p + 8 * e + 4);
                 mt[j] = load_shared(all, p + rows * D + 4 * row);
               }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < 8; ++j) {
                 if (c0 + j * slices >= count) break;
                 const float o[8] = {lo[j][0], lo[j][1], lo[j][2], lo[j][3], hi[j][0], hi[j][1], hi[j][2], hi[j][3]};
                 merge(x, o, mt[j][0], mt[j][1]);
@@ -1268,9 +1283,11 @@ extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype d
       (reinterpret_cast<uintptr_t>(workspace) & 255))
     return GLQ_ERR_WORKSPACE;
   const int32_t group = q_heads / C->kv_heads, tiles = (group + 15) / 16;
+  const float scale2 = scale * 1.4426950408889634f;
   const DecodeArgs a = {C->k, C->v, C->k_scale, C->v_scale, q, out, q_stride, out_stride, page_table, lens, max_pages,
                         max_len, C->kv_heads, group, tiles, log2_of(C->page_size), (int32_t)C->num_pages,
-                        scale * 1.4426950408889634f, (int32_t)batch, (int32_t)p.part_floats,
+                        scale2 == 0.0f ? 1.0f : fabsf(scale2), scale2 == 0.0f ? 0.0f : copysignf(1.0f, scale2),
+                        (int32_t)batch, (int32_t)p.part_floats,
                         p.whole ? 1 : 0,
                         reinterpret_cast<unsigned int *>(workspace),
                         reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + GLQ_ATTN_CTRL_BYTES)};

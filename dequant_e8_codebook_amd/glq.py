@@ -623,6 +623,7 @@ class KvCache:
         self._st = KvCacheStruct(self.format, self.kv_heads, self.head_dim, self.page_size, self.num_pages,
                                  k.data_ptr(), v.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
                                  0 if v_scale is None else v_scale.data_ptr())
+        self._ref = ctypes.byref(self._st)
 
     def struct(self) -> KvCacheStruct:
         return self._st
@@ -642,64 +643,82 @@ class KvCache:
         return KvCache(k, v, ks, vs)
 
 
-def _rows(t, name, device, heads, dim, dtype=None, total=None):
-    """A [rows, heads, head_dim] operand: heads dense, rows any 16-byte multiple
-    apart. Returns the row stride in elements."""
-    torch = _torch()
-    if not getattr(t, "is_cuda", False):
-        raise ValueError(f"{name}: must be a device (cuda) tensor")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.dtype is not dtype if dtype is not None else t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype or 'float32 or bfloat16'}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or (total is not None and shape[0] != total):
-        raise ValueError(f"{name}: shape {tuple(shape)}, expected ({'rows' if total is None else total}, {heads}, {dim})")
-    step, sh, sd = t.stride()
-    if sd != 1 or (heads > 1 and sh != dim):
-        raise ValueError(f"{name}: heads of one row must be dense")
-    if shape[0] <= 1 or step == 0 and shape[0] == 0:
-        step = heads * dim                               # a single row has no stride of its own
-    if step < heads * dim or (step * t.element_size()) % 16 or t.data_ptr() % 16:
-        raise ValueError(f"{name}: rows must not overlap and start at multiples of 16 bytes")
-    return step
+# These calls are as short as a few microseconds on the GPU, so what they check
+# is read from the tensors once, in the order that a right call passes quickest.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the current stream without an object for it
 
 
-def _ints(t, name, device, shape):
-    torch = _torch()
-    if not getattr(t, "is_cuda", False):
+def _stream_on(device, stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream_ptr(stream)
+
+
+def _rows(t, name, device, dtype, total, heads, dim):
+    """A [total, heads, head_dim] operand: heads dense, rows any 16-byte multiple
+    apart. Returns its address and the row stride in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name}: must be a device (cuda) tensor")
-    if t.device != device or t.dtype is not torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != (total, heads, dim) or t.device != device:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {(total, heads, dim)} on "
+                         f"{device}")
+    at, step = t.data_ptr(), heads * dim
+    if not t.is_contiguous():
+        step, between, inner = t.stride()
+        if inner != 1 or (heads > 1 and between != dim):
+            raise ValueError(f"{name}: the heads of a row must be dense")
+        if step < heads * dim or (step * t.element_size()) % 16:
+            raise ValueError(f"{name}: rows must not overlap and start at multiples of 16 bytes")
+    if at % 16:
+        raise ValueError(f"{name}: must be 16-byte aligned")
+    return at, step
+
+
+def _ints(t, name, device, *shape):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: must be a device (cuda) tensor")
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected dense int32 {shape} on {device}")
     return t.data_ptr()
 
 
+_ATTN_DTYPES = {torch.float32: GLQ_F32, torch.bfloat16: GLQ_BF16}
+
+
+def _attn_dtype(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _ATTN_DTYPES or t.dim() != 3:
+        raise ValueError(f"{name}: must be a float32 or bfloat16 tensor of rows, heads and head_dim")
+    return _ATTN_DTYPES[t.dtype]
+
+
 def _kv_args(cache, k, v, slots):
-    ks = _rows(k, "k", cache.device, cache.kv_heads, cache.head_dim)
-    vs = _rows(v, "v", cache.device, cache.kv_heads, cache.head_dim, k.dtype, k.shape[0])
-    return ks, vs, _ints(slots, "slots", cache.device, (k.shape[0],))
+    dt, dev, total = _attn_dtype(k, "k"), cache.device, k.shape[0]
+    kp, ks = _rows(k, "k", dev, k.dtype, total, cache.kv_heads, cache.head_dim)
+    vp, vs = _rows(v, "v", dev, k.dtype, total, cache.kv_heads, cache.head_dim)
+    return dt, kp, ks, vp, vs, _ints(slots, "slots", dev, total), total
 
 
 def kv_append(cache: KvCache, k, v, slots, stream=None):
     """Write the tokens' keys and values [tokens, kv_heads, head_dim] into the
     cache at int32 slots [tokens] (page * page_size + row; a slot outside the
     cache drops its token) (glq_kv_append)."""
-    ks, vs, sp = _kv_args(cache, k, v, slots)
-    _check(_lib.glq_kv_append(ctypes.byref(cache._st), k.data_ptr(), v.data_ptr(), _dtype_code(k), ks, vs, sp,
-                              k.shape[0], _stream_ptr(stream)), "glq_kv_append")
+    dt, kp, ks, vp, vs, sp, total = _kv_args(cache, k, v, slots)
+    _check(_lib.glq_kv_append(cache._ref, kp, vp, dt, ks, vs, sp, total, _stream_on(cache.device, stream)),
+           "glq_kv_append")
 
 
 def kv_read(cache: KvCache, slots, k, v, stream=None):
     """Read the tokens at the slots back into k and v [tokens, kv_heads,
     head_dim], float32 or bfloat16 (glq_kv_read)."""
-    ks, vs, sp = _kv_args(cache, k, v, slots)
-    _check(_lib.glq_kv_read(ctypes.byref(cache._st), sp, k.shape[0], k.data_ptr(), v.data_ptr(), _dtype_code(k), ks,
-                            vs, _stream_ptr(stream)), "glq_kv_read")
+    dt, kp, ks, vp, vs, sp, total = _kv_args(cache, k, v, slots)
+    _check(_lib.glq_kv_read(cache._ref, sp, total, kp, vp, dt, ks, vs, _stream_on(cache.device, stream)),
+           "glq_kv_read")
     return k, v
 
 
 def attn_decode_workspace_bytes(cache: KvCache, batch: int, q_heads: int, max_len: int) -> int:
-    return int(_lib.glq_attn_decode_workspace(ctypes.byref(cache._st), batch, q_heads, max_len))
+    return int(_lib.glq_attn_decode_workspace(cache._ref, batch, q_heads, max_len))
 
 
 def attn_decode(cache: KvCache, q, page_table, lens, out, workspace, max_len: int, scale=None, stream=None):
@@ -708,20 +727,17 @@ def attn_decode(cache: KvCache, q, page_table, lens, out, workspace, max_len: in
     (int32 [batch, max_pages]); max_len bounds lens. workspace: uint8, zeroed
     once, attn_decode_workspace_bytes (glq_attn_decode). scale: 1 / sqrt(head_dim)
     unless given."""
-    dev, dim = cache.device, cache.head_dim
-    if len(q.shape) != 3:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected (batch, q_heads, {dim})")
+    dt, dev, dim = _attn_dtype(q, "q"), cache.device, cache.head_dim
     batch, heads = q.shape[0], q.shape[1]
-    qs = _rows(q, "q", dev, heads, dim)
-    os_ = _rows(out, "out", dev, heads, dim, q.dtype, batch)
-    lp = _ints(lens, "lens", dev, (batch,))
-    pages = page_table.shape[-1]
-    tp = _ints(page_table, "page_table", dev, (batch, pages))
+    qp, qs = _rows(q, "q", dev, q.dtype, batch, heads, dim)
+    op, os_ = _rows(out, "out", dev, q.dtype, batch, heads, dim)
+    lp, pages = _ints(lens, "lens", dev, batch), page_table.shape[-1]
+    tp = _ints(page_table, "page_table", dev, batch, pages)
     if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: must be contiguous on {dev}")
-    rc = _lib.glq_attn_decode(ctypes.byref(cache._st), q.data_ptr(), _dtype_code(q), qs, batch, heads, tp, pages, lp,
-                              max_len, dim ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-                              workspace.data_ptr(), _nbytes(workspace), _stream_ptr(stream))
+    rc = _lib.glq_attn_decode(cache._ref, qp, dt, qs, batch, heads, tp, pages, lp, max_len,
+                              dim ** -0.5 if scale is None else scale, op, os_, workspace.data_ptr(), workspace.nbytes,
+                              _stream_on(dev, stream))
     _check(rc, "glq_attn_decode")
     return out
 
@@ -733,22 +749,21 @@ def attn_prompt(q, k, v, out, cu_q, cu_k=None, max_q: int | None = None, causal:
     cu_q[b + 1] - 1, its keys rows cu_k[b] .. (cu_q unless given; more keys than
     queries: the queries are the last ones) (glq_attn_prompt). max_q bounds the
     queries of a sequence (total_q unless given)."""
-    if len(q.shape) != 3 or len(k.shape) != 3:
-        raise ValueError("q, k: must be [rows, heads, head_dim]")
-    dev, heads, dim, kvh = q.device, q.shape[1], q.shape[2], k.shape[1]
+    dt = _attn_dtype(q, "q")
+    _attn_dtype(k, "k")
+    dev, total_q, heads, dim = q.device, *q.shape
+    total_k, kvh = k.shape[0], k.shape[1]
     if dim not in _HEAD_DIMS or kvh < 1 or heads % kvh:
         raise ValueError(f"q, k: {heads} and {kvh} heads of {dim}")
-    qs = _rows(q, "q", dev, heads, dim)
-    ks = _rows(k, "k", dev, kvh, dim, q.dtype)
-    vs = _rows(v, "v", dev, kvh, dim, q.dtype, k.shape[0])
-    os_ = _rows(out, "out", dev, heads, dim, q.dtype, q.shape[0])
-    if cu_k is None:
-        cu_k = cu_q
+    qp, qs = _rows(q, "q", dev, q.dtype, total_q, heads, dim)
+    kp, ks = _rows(k, "k", dev, q.dtype, total_k, kvh, dim)
+    vp, vs = _rows(v, "v", dev, q.dtype, total_k, kvh, dim)
+    op, os_ = _rows(out, "out", dev, q.dtype, total_q, heads, dim)
     batch = cu_q.shape[0] - 1
-    qp, kp = _ints(cu_q, "cu_q", dev, (batch + 1,)), _ints(cu_k, "cu_k", dev, (batch + 1,))
-    st = PromptStruct(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _dtype_code(q), heads, kvh, dim, qs,
-                      ks, vs, os_, q.shape[0], k.shape[0], batch, qp, kp, q.shape[0] if max_q is None else max_q,
-                      dim ** -0.5 if scale is None else scale)
-    _check(_lib.glq_attn_prompt(ctypes.byref(st), ATTN_CAUSAL if causal else 0, _stream_ptr(stream)),
+    cq = _ints(cu_q, "cu_q", dev, batch + 1)
+    ck = cq if cu_k is None else _ints(cu_k, "cu_k", dev, batch + 1)
+    st = PromptStruct(qp, kp, vp, op, dt, heads, kvh, dim, qs, ks, vs, os_, total_q, total_k, batch, cq, ck,
+                      total_q if max_q is None else max_q, dim ** -0.5 if scale is None else scale)
+    _check(_lib.glq_attn_prompt(ctypes.byref(st), ATTN_CAUSAL if causal else 0, _stream_on(dev, stream)),
            "glq_attn_prompt")
     return out
