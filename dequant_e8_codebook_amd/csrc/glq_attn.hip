@@ -765,7 +765,7 @@ struct PromptArgs {
   void *out;
   int64_t q_stride, k_stride, v_stride, out_stride, total_q, total_k;
   const int32_t *cu_q, *cu_k;
-  int32_t q_heads, kv_heads, q_tiles, causal, items;   // items: batch * q_heads
+  int32_t q_heads, kv_heads, q_tiles, causal, items;   // items: sequences times heads (bf16) or kept heads (float32)
   float scale2;                // scale * log2(e)
   float abs_scale2;            // bf16 path: its magnitude, the sign in q_xor; for a
   uint32_t q_and, q_xor;       // scale of 0, 1 and queries of 0 (q_and)
@@ -782,8 +782,9 @@ template <bool F32> __device__ __forceinline__ float4 load4(const void *p, int64
 // A weight of 0 times a value that is not finite is NaN, and would reach
 // queries that do not see the key. In a tile with such pairs the values that
 // are not finite become 0, and the queries that do see one get NaN.
-__device__ __forceinline__ void keep_unseen_out(float4 &x, bool seen, f32x4 *acc) {
-  float *v = reinterpret_cast<float *>(&x);
+template <int CT, class Acc>
+__device__ __forceinline__ void keep_unseen_out(float4 &x, const bool (&seen)[CT][4], int r, Acc acc) {
+  float v[4] = {x.x, x.y, x.z, x.w};
   bool bad = false;
 #pragma unroll
   for (int c = 0; c < 4; ++c) bad |= !(fabsf(v[c]) < INFINITY);
@@ -792,98 +793,172 @@ __device__ __forceinline__ void keep_unseen_out(float4 &x, bool seen, f32x4 *acc
   for (int c = 0; c < 4; ++c) {
     const bool b = !(fabsf(v[c]) < INFINITY);
     v[c] = b ? 0.0f : v[c];
-    const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x4f32(b ? 1.0f : 0.0f, seen ? 1.0f : 0.0f, (f32x4){0, 0, 0, 0},
-                                                           0, 0, 0);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) acc[c][r] = hit[r] > 0.0f ? NAN : acc[c][r];
+    for (int t = 0; t < CT; ++t) {
+      const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x4f32(b ? 1.0f : 0.0f, seen[t][r] ? 1.0f : 0.0f,
+                                                             (f32x4){0, 0, 0, 0}, 0, 0, 0);
+      f32x4 &o = acc(t)[c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = hit[e] > 0.0f ? NAN : o[e];
+    }
+  }
+  x = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// Rows of attention in float32: a wave takes CT tiles of 16 rows against every
+// `step`-th 16 keys from `first` on, with float32 16x16x4 products, transposed as
+// in the decode kernel: S^T = K Q^T leaves lane (g, n) row n's scores of keys 4 g +
+// r, the B operand of the r-th step of O^T = V^T P^T. k-slot g of step 4 i + r of
+// the scores means dimension 16 i + 4 g + r, row n of value tile (i, c) means
+// dimension 64 i + 4 n + c: both are 16-byte loads. Row x is head head0 + x % group
+// of query x / group. The next keys' loads are in flight while these are worked on.
+struct RowJob {
+  int head0, group, kvh, row0, rows;   // rows: of the sequence (queries * group)
+  int q0, k0, lk, shift;               // first query and key row, keys, keys ahead of the queries
+};
+template <int D, int CT> struct RowSums {
+  f32x4 acc[CT][D / 16];
+  float m[CT], l[CT];                  // maximum and this lane's part of the total
+};
+template <int D> struct KvRows {
+  float4 k[D / 16], v[4][D / 64];
+};
+
+template <int D, bool F32>
+__device__ __forceinline__ void load_rows(const PromptArgs &a, const RowJob &w, int lane, int j0, KvRows<D> &x) {
+  const int g = lane >> 4, n = lane & 15;
+  const int64_t kr = w.k0 + min(j0 + n, w.lk - 1);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) x.k[i] = load4<F32>(a.k, kr * a.k_stride + (int64_t)w.kvh * D + 16 * i + 4 * g);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int64_t vr = w.k0 + min(j0 + 4 * g + r, w.lk - 1);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) x.v[r][i] = load4<F32>(a.v, vr * a.v_stride + (int64_t)w.kvh * D + 64 * i + 4 * n);
   }
 }
 
-// A wave takes 16 queries of one head against 16 keys at a time with float32
-// 16x16x4 products, transposed as in the decode kernel: S^T = K Q^T leaves lane
-// (g, n) query n's scores of keys 4 g + r, the B operand of the r-th step of
-// O^T = V^T P^T. k-slot g of step 4 i + r of the scores means dimension 16 i +
-// 4 g + r, row n of value tile (i, c) means dimension 64 i + 4 n + c: both are 16-byte loads.
-template <int D, bool F32>
-__device__ __forceinline__ void prompt_wave(const PromptArgs &a, int lane, int head, int q0, int lq, int k0, int lk,
-                                            int row0) {
+template <int D, bool F32, int CT>
+__device__ __forceinline__ void attend_rows(const PromptArgs &a, const RowJob &w, int lane, int first, int step,
+                                            RowSums<D, CT> &o) {
   const int g = lane >> 4, n = lane & 15;
-  const int row = row0 + n < lq ? row0 + n : lq - 1;
-  const int kvh = head / (a.q_heads / a.kv_heads);
-  float4 q[D / 16];
+  float4 q[CT][D / 16];
+  int last[CT];                                      // this lane's rows' last keys
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i)
-    q[i] = load4<F32>(a.q, (int64_t)(q0 + row) * a.q_stride + (int64_t)head * D + 16 * i + 4 * g);
-  const int shift = lk - lq;
-  const int last = a.causal ? row + shift : lk - 1;  // this lane's last key
-  int end = a.causal ? row0 + 16 + shift : lk;       // keys any query of the wave sees
-  end = end < lk ? end : lk;
-  f32x4 acc[D / 16];
+  for (int t = 0; t < CT; ++t) {
+    const int row = min(w.row0 + 16 * t + n, w.rows - 1), query = row / w.group;
+    last[t] = a.causal ? query + w.shift : w.lk - 1;
+    const int64_t at = (int64_t)(w.q0 + query) * a.q_stride + (int64_t)(w.head0 + row - query * w.group) * D + 4 * g;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) acc[i] = (f32x4){0, 0, 0, 0};
-  float m = -INFINITY, l = 0.0f;
-  for (int j0 = 0; j0 < end; j0 += 16) {
-    const int kr = j0 + n < lk ? j0 + n : lk - 1;
-    f32x4 s = {0, 0, 0, 0};
+    for (int i = 0; i < D / 16; ++i) q[t][i] = load4<F32>(a.q, at + 16 * i);
+    o.m[t] = -INFINITY, o.l[t] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const float4 x = load4<F32>(a.k, (int64_t)(k0 + kr) * a.k_stride + (int64_t)kvh * D + 16 * i + 4 * g);
-      s = __builtin_amdgcn_mfma_f32_16x16x4f32(x.x, q[i].x, s, 0, 0, 0);
-      s = __builtin_amdgcn_mfma_f32_16x16x4f32(x.y, q[i].y, s, 0, 0, 0);
-      s = __builtin_amdgcn_mfma_f32_16x16x4f32(x.z, q[i].z, s, 0, 0, 0);
-      s = __builtin_amdgcn_mfma_f32_16x16x4f32(x.w, q[i].w, s, 0, 0, 0);
-    }
-    float mt = -INFINITY;
-    bool seen[4];
+    for (int i = 0; i < D / 16; ++i) o.acc[t][i] = (f32x4){0, 0, 0, 0};
+  }
+  // keys that all rows of the wave see, and that any of them sees
+  const int all = a.causal ? w.row0 / w.group + w.shift : w.lk - 1;
+  const int top = min(w.row0 + 16 * CT, w.rows) - 1;
+  const int end = min(w.lk, a.causal ? top / w.group + w.shift + 1 : w.lk);
+  if (first >= end) return;
+  auto work = [&](KvRows<D> &x, int j0) {
+    const bool masked = j0 + 15 > all || j0 + 16 > w.lk;
+    f32x4 s[CT];
+    bool seen[CT][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int j = j0 + 4 * g + r;
-      seen[r] = j <= last && j < lk;
-      s[r] = seen[r] ? s[r] * a.scale2 : -INFINITY;
-      mt = fmaxf(mt, s[r]);
-    }
-    const bool masked = a.causal && j0 + 15 > row0 + shift;     // some query does not see some key
-    mt = fmaxf(mt, __shfl_xor(mt, 16));
-    mt = fmaxf(mt, __shfl_xor(mt, 32));
-    const float mn = fmaxf(m, mt), base = mn == -INFINITY ? 0.0f : mn;
-    const float alpha = __builtin_amdgcn_exp2f(m - base);
-    m = mn;
-    l *= alpha;
+    for (int t = 0; t < CT; ++t) {
+      s[t] = (f32x4){0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) acc[i] *= alpha;
+      for (int i = 0; i < D / 16; ++i) {
+        s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.k[i].x, q[t][i].x, s[t], 0, 0, 0);
+        s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.k[i].y, q[t][i].y, s[t], 0, 0, 0);
+        s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.k[i].z, q[t][i].z, s[t], 0, 0, 0);
+        s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.k[i].w, q[t][i].w, s[t], 0, 0, 0);
+      }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float p = __builtin_amdgcn_exp2f(s[r] - base);
-      l += p;
-      const int j = j0 + 4 * g + r;
+      for (int r = 0; r < 4; ++r) {
+        const int j = j0 + 4 * g + r;
+        seen[t][r] = j <= last[t] && j < w.lk;
+        s[t][r] = seen[t][r] ? s[t][r] * a.scale2 : -INFINITY;
+      }
+      const float mt = column_max(fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3])));
+      if (__any(mt > o.m[t])) {
+        const float mn = fmaxf(o.m[t], mt);
+        const float alpha = o.m[t] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(o.m[t] - mn);
+        o.m[t] = mn;
+        o.l[t] *= alpha;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        float4 x = load4<F32>(a.v, (int64_t)(k0 + (j < lk ? j : lk - 1)) * a.v_stride + (int64_t)kvh * D + 64 * i + 4 * n);
-        if (j >= lk) x = make_float4(0, 0, 0, 0);
-        if (masked) keep_unseen_out(x, seen[r], &acc[4 * i]);
-        acc[4 * i] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.x, p, acc[4 * i], 0, 0, 0);
-        acc[4 * i + 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.y, p, acc[4 * i + 1], 0, 0, 0);
-        acc[4 * i + 2] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.z, p, acc[4 * i + 2], 0, 0, 0);
-        acc[4 * i + 3] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.w, p, acc[4 * i + 3], 0, 0, 0);
+        for (int i = 0; i < D / 16; ++i) o.acc[t][i] *= alpha;
+      }
+      const float base = o.m[t] == -INFINITY ? 0.0f : o.m[t];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        s[t][r] = __builtin_amdgcn_exp2f(s[t][r] - base);
+        o.l[t] += s[t][r];
       }
     }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        float4 v = x.v[r][i];
+        if (masked) {
+          if (j0 + 4 * g + r >= w.lk) v = make_float4(0, 0, 0, 0);
+          keep_unseen_out<CT>(v, seen, r, [&](int t) { return &o.acc[t][4 * i]; });
+        }
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+          o.acc[t][4 * i] = __builtin_amdgcn_mfma_f32_16x16x4f32(v.x, s[t][r], o.acc[t][4 * i], 0, 0, 0);
+          o.acc[t][4 * i + 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(v.y, s[t][r], o.acc[t][4 * i + 1], 0, 0, 0);
+          o.acc[t][4 * i + 2] = __builtin_amdgcn_mfma_f32_16x16x4f32(v.z, s[t][r], o.acc[t][4 * i + 2], 0, 0, 0);
+          o.acc[t][4 * i + 3] = __builtin_amdgcn_mfma_f32_16x16x4f32(v.w, s[t][r], o.acc[t][4 * i + 3], 0, 0, 0);
+        }
+      }
+  };
+  KvRows<D> x;
+  int j0 = first;
+  if constexpr (!F32) {                              // (the bf16 kernel's way out: registers, not haste)
+    for (; j0 < end; j0 += step) {
+      load_rows<D, F32>(a, w, lane, j0, x);
+      work(x, j0);
+    }
+    return;
   }
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (row0 + n >= lq) return;
-  const int64_t o0 = (int64_t)(q0 + row) * a.out_stride + (int64_t)head * D;
+  load_rows<D, F32>(a, w, lane, first, x);
+  for (; j0 + step < end; j0 += step) {
+    KvRows<D> y;
+    load_rows<D, F32>(a, w, lane, j0 + step, y);
+    __builtin_amdgcn_sched_barrier(0);               // the loads go out before the work
+    work(x, j0);
+    x = y;
+  }
+  work(x, j0);
+}
+
+// row x's values of a lane to memory, divided by the row's total
+template <int D, bool F32>
+__device__ __forceinline__ void store_row(const PromptArgs &a, const RowJob &w, int row, int d, float4 v) {
+  const int query = row / w.group;
+  const int64_t at = (int64_t)(w.q0 + query) * a.out_stride + (int64_t)(w.head0 + row - query * w.group) * D + d;
+  if constexpr (F32) *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at) = v;
+  else *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) =
+           make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+// one wave, all keys, 16 rows: the bf16 kernel's way out where values are not finite
+template <int D>
+__device__ __forceinline__ void rows_alone(const PromptArgs &a, const RowJob &w, int lane) {
+  RowSums<D, 1> o;
+  attend_rows<D, false, 1>(a, w, lane, 0, 16, o);
+  const float l = column_sum(o.l[0]), inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int g = lane >> 4, row = w.row0 + (lane & 15);
+  if (row >= w.rows) return;
 #pragma unroll
   for (int i = 0; i < D / 64; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t at = o0 + 64 * i + 4 * (4 * g + r);
-      const float x = acc[4 * i][r] * inv, y = acc[4 * i + 1][r] * inv, z = acc[4 * i + 2][r] * inv,
-                  w = acc[4 * i + 3][r] * inv;
-      if constexpr (F32) *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at) = make_float4(x, y, z, w);
-      else *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) =
-               make_uint2(pack_bf16(x, y), pack_bf16(z, w));
-    }
+    for (int r = 0; r < 4; ++r)
+      store_row<D, false>(a, w, row, 64 * i + 4 * (4 * g + r),
+                          make_float4(o.acc[0][4 * i][r] * inv, o.acc[0][4 * i + 1][r] * inv,
+                                      o.acc[0][4 * i + 2][r] * inv, o.acc[0][4 * i + 3][r] * inv));
 }
 
 // the sequence of a workgroup: its first query and key row and their numbers
@@ -894,13 +969,51 @@ __device__ __forceinline__ Span span_of(const PromptArgs &a, int64_t b) {
   return {q0, q1 - q0, k0, k1 - k0 > 0 ? k1 - k0 : 0};
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) attn_prompt_f32(PromptArgs a) {
+// The float32 path. A workgroup takes 16 CT rows (queries times the heads that
+// share a kept head), its waves a quarter of the keys each; they join in LDS.
+template <int D, int CT>
+__global__ void __launch_bounds__(256, D == 64 ? 2 : 1) attn_prompt_f32(PromptArgs a) {
+  extern __shared__ float shm[];                     // [4][16 CT][D] sums, [4][16 CT] maxima, [4][16 CT] totals
+  constexpr int R = 16 * CT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int bh = blockIdx.x / a.q_tiles, head = bh % a.q_heads;
-  const Span s = span_of(a, bh / a.q_heads);
-  const int row0 = 64 * (blockIdx.x % a.q_tiles) + 16 * wave;
-  if (row0 < s.lq) prompt_wave<D, true>(a, lane, head, s.q0, s.lq, s.k0, s.lk, row0);
+  const int item = blockIdx.x % a.items, kvh = item % a.kv_heads, group = a.q_heads / a.kv_heads;
+  const Span s = span_of(a, item / a.kv_heads);
+  const int row0 = R * (a.q_tiles - 1 - (int)(blockIdx.x / a.items));
+  if (s.lq <= 0 || row0 >= (int64_t)s.lq * group) return;
+  const RowJob w = {kvh * group, group, kvh, row0, s.lq * group, s.q0, s.k0, s.lk, s.lk - s.lq};
+  RowSums<D, CT> o;
+  attend_rows<D, true, CT>(a, w, lane, 16 * wave, 64, o);
+  const int g = lane >> 4, n = lane & 15;
+  float *so = shm, *sm = shm + 4 * R * D, *sl = sm + 4 * R;
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    const float l = column_sum(o.l[t]);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4 *>(so + (R * wave + 16 * t + n) * D + 64 * i + 4 * (4 * g + r)) =
+            make_float4(o.acc[t][4 * i][r], o.acc[t][4 * i + 1][r], o.acc[t][4 * i + 2][r], o.acc[t][4 * i + 3][r]);
+    if (g == 0) sm[R * wave + 16 * t + n] = l == 0.0f ? -INFINITY : o.m[t], sl[R * wave + 16 * t + n] = l;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < R * (D / 4); e += 256) {
+    const int row = e / (D / 4), d = 4 * (e % (D / 4));
+    if (row0 + row >= w.rows) break;
+    float top = -INFINITY, total = 0.0f;
+    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) top = fmaxf(top, sm[R * x + row]);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float f = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sm[R * x + row] - top);
+      const float4 u = *reinterpret_cast<const float4 *>(so + (R * x + row) * D + d);
+      total += f * sl[R * x + row];
+      v.x += f * u.x, v.y += f * u.y, v.z += f * u.z, v.w += f * u.w;
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    store_row<D, true>(a, w, row0 + row, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+  }
 }
 
 // The bf16 path. A workgroup takes 128 queries of one head, 32 a wave, against
@@ -1100,8 +1213,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(Prompt
   // a weight of 0 times an infinity or a NaN that the query does not see: such
   // a wave is done over, pair by pair
   if (__any(bad)) {
-    prompt_wave<D, false>(a, lane, head, sp.q0, sp.lq, sp.k0, sp.lk, row0);
-    if (row0 + 16 < sp.lq) prompt_wave<D, false>(a, lane, head, sp.q0, sp.lq, sp.k0, sp.lk, row0 + 16);
+    RowJob w = {head, 1, kvh, row0, sp.lq, sp.q0, sp.k0, sp.lk, shift};
+    rows_alone<D>(a, w, lane);
+    w.row0 += 16;
+    if (w.row0 < sp.lq) rows_alone<D>(a, w, lane);
     return;
   }
   if (row0 + n >= sp.lq) return;
@@ -1225,21 +1340,37 @@ int launch_decode_dim(const DecodeArgs &a, int d, glq_dtype dt, int64_t groups, 
                                                                       : launch_decode<FMT, 256>(a, dt, groups, st);
 }
 
-template <int D>
-int launch_prompt(const PromptArgs &a, bool f32, dim3 grid, hipStream_t st) {
-  if (f32) {
-    hipLaunchKernelGGL(attn_prompt_f32<D>, grid, dim3(256), 0, st, a);
-    return hip_status(hipGetLastError(), "attn_prompt_f32");
-  }
-  constexpr size_t shm = 4 * kKeys * 2 * D;
-  if constexpr (shm > 64 * 1024) {
-    const int rc = hip_status(hipFuncSetAttribute(reinterpret_cast<const void *>(attn_prompt_bf16<D>),
+template <class K>
+int launch_lds(K kernel, const PromptArgs &a, int64_t groups, size_t shm, hipStream_t st, const char *name) {
+  if (shm > 64 * 1024) {
+    const int rc = hip_status(hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm),
                               "hipFuncSetAttribute");
     if (rc) return rc;
   }
-  hipLaunchKernelGGL(attn_prompt_bf16<D>, grid, dim3(256), shm, st, a);
-  return hip_status(hipGetLastError(), "attn_prompt_bf16");
+  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(256), shm, st, a);
+  return hip_status(hipGetLastError(), name);
+}
+
+// most: queries of a sequence, at most
+template <int D>
+int launch_prompt(PromptArgs a, bool f32, int64_t batch, int64_t most, hipStream_t st) {
+  if (!f32) {
+    a.items = (int32_t)(batch * a.q_heads);
+    a.q_tiles = (int32_t)((most + 127) / 128);
+    return launch_lds(attn_prompt_bf16<D>, a, (int64_t)a.items * a.q_tiles, 4 * kKeys * 2 * D, st, "attn_prompt_bf16");
+  }
+  // 32 rows a workgroup where that leaves a few for every CU, 16 otherwise
+  // (heads of 256: always, two tiles' sums and queries would not fit the registers)
+  a.items = (int32_t)(batch * a.kv_heads);
+  const int64_t rows = most * (a.q_heads / a.kv_heads);
+  const int ct = D < 256 && a.items * ((rows + 31) / 32) >= 4 * kCus ? 2 : 1;
+  a.q_tiles = (int32_t)((rows + 16 * ct - 1) / (16 * ct));
+  const size_t shm = 4 * 16 * ct * (D + 2) * sizeof(float);
+  const int64_t groups = (int64_t)a.items * a.q_tiles;
+  if constexpr (D < 256)
+    if (ct == 2) return launch_lds(attn_prompt_f32<D, 2>, a, groups, shm, st, "attn_prompt_f32");
+  return launch_lds(attn_prompt_f32<D, 1>, a, groups, shm, st, "attn_prompt_f32");
 }
 
 }  // namespace
@@ -1318,19 +1449,19 @@ extern "C" int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_st
     return GLQ_ERR_ARG;
   const int64_t most = P->max_q < P->total_q ? P->max_q : P->total_q;
   const bool f = P->dt == GLQ_F32;
-  const int64_t tiles = f ? (most + 63) / 64 : (most + 127) / 128;
-  if (P->batch > 0x7FFFFFFF / (P->q_heads * tiles)) return GLQ_ERR_UNSUPPORTED;
+  // workgroups: no more than this in either kernel
+  if (P->batch > 0x7FFFFFFF / (P->q_heads * ((most + 15) / 16 + 1)) || most * P->q_heads > 0x7FFFFFFF - 64)
+    return GLQ_ERR_UNSUPPORTED;
   const float scale2 = P->scale * 1.4426950408889634f;
   const PromptArgs a = {P->q, P->k, P->v, P->out, P->q_stride, P->k_stride, P->v_stride, P->out_stride, P->total_q,
-                        P->total_k, P->cu_q, P->cu_k, P->q_heads, P->kv_heads, (int32_t)tiles,
-                        (flags & GLQ_ATTN_CAUSAL) ? 1 : 0, (int32_t)(P->batch * P->q_heads),
+                        P->total_k, P->cu_q, P->cu_k, P->q_heads, P->kv_heads, 0,
+                        (flags & GLQ_ATTN_CAUSAL) ? 1 : 0, 0,
                         scale2, scale2 == 0.0f ? 1.0f : fabsf(scale2), scale2 == 0.0f ? 0u : 0xFFFFFFFFu,
                         scale2 < 0.0f ? 0x80008000u : 0u};
-  const dim3 grid((unsigned)(P->batch * P->q_heads * tiles));
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   switch (P->head_dim) {
-    case 64: return launch_prompt<64>(a, f, grid, st);
-    case 128: return launch_prompt<128>(a, f, grid, st);
-    default: return launch_prompt<256>(a, f, grid, st);
+    case 64: return launch_prompt<64>(a, f, P->batch, most, st);
+    case 128: return launch_prompt<128>(a, f, P->batch, most, st);
+    default: return launch_prompt<256>(a, f, P->batch, most, st);
   }
 }
