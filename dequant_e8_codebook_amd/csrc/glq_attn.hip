@@ -13,11 +13,14 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <type_traits>
 
 #include "glq.h"
 
 namespace glq {
 namespace {
+
+#define INLINED __attribute__((always_inline))   // lambdas on register arrays
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -577,7 +580,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode
     for (int i = 0; i < DT; ++i) acc[i] = (f32x4){0, 0, 0, 0};
 
     const Nibbles nib;
-    auto work = [&](Tile<FMT, D> &x, int t) {
+    auto work = [&](Tile<FMT, D> &x, int t) INLINED {
       float s[8];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode
     // lies between a tile's loads and its use but those that skip the use: where
     // paths with and without newer loads met, the wait for the older ones would
     // be a wait for all.
-    auto ahead = [&](int t, Tile<FMT, D> &x) {
+    auto ahead = [&](int t, Tile<FMT, D> &x) INLINED {
       const Pages now = next;
       next = pages_of(a, table, t + 128 < end ? t + 128 : t, end);
       load_tile<FMT, D>(a, now, h, lane, t, end, x);
@@ -765,7 +768,8 @@ struct PromptArgs {
   void *out;
   int64_t q_stride, k_stride, v_stride, out_stride, total_q, total_k;
   const int32_t *cu_q, *cu_k;
-  int32_t q_heads, kv_heads, q_tiles, causal, items;   // items: sequences times heads (bf16) or kept heads (float32)
+  int64_t max_q;
+  int32_t q_heads, kv_heads, batch, causal;
   float scale2;                // scale * log2(e)
   float abs_scale2;            // bf16 path: its magnitude, the sign in q_xor; for a
   uint32_t q_and, q_xor;       // scale of 0, 1 and queries of 0 (q_and)
@@ -860,7 +864,7 @@ __device__ __forceinline__ void attend_rows(const PromptArgs &a, const RowJob &w
   const int top = min(w.row0 + 16 * CT, w.rows) - 1;
   const int end = min(w.lk, a.causal ? top / w.group + w.shift + 1 : w.lk);
   if (first >= end) return;
-  auto work = [&](KvRows<D> &x, int j0) {
+  auto work = [&](KvRows<D> &x, int j0) INLINED {
     const bool masked = j0 + 15 > all || j0 + 16 > w.lk;
     f32x4 s[CT];
     bool seen[CT][4];
@@ -966,7 +970,54 @@ struct Span { int q0, lq, k0, lk; };
 __device__ __forceinline__ Span span_of(const PromptArgs &a, int64_t b) {
   const int q0 = clamped(a.cu_q[b], a.total_q), q1 = clamped(a.cu_q[b + 1], a.total_q);
   const int k0 = clamped(a.cu_k[b], a.total_k), k1 = clamped(a.cu_k[b + 1], a.total_k);
-  return {q0, q1 - q0, k0, k1 - k0 > 0 ? k1 - k0 : 0};
+  return {__builtin_amdgcn_readfirstlane(q0), __builtin_amdgcn_readfirstlane(q1 - q0),
+          __builtin_amdgcn_readfirstlane(k0), __builtin_amdgcn_readfirstlane(k1 - k0 > 0 ? k1 - k0 : 0)};
+}
+
+// Workgroups of sequence b (R rows each: queries times the heads of a kept head)
+template <int R> __device__ __forceinline__ int tiles_of(const PromptArgs &a, int b) {
+  const int64_t q = clamped(a.cu_q[b + 1], a.total_q) - clamped(a.cu_q[b], a.total_q);
+  const int64_t n = q < a.max_q ? q : a.max_q;       // more than the launch was made for are not done
+  return n > 0 ? (int)((n * (a.q_heads / a.kv_heads) + R - 1) / R) : 0;
+}
+
+// The sequence and tile of a kept head's at-th workgroup. In a causal prompt the
+// last tiles see the most keys and come first, over all sequences (up to 64 of
+// them: the highest tile for which few enough come before it, by bisection on
+// counts; beyond, sequence by sequence). Workgroups without a tile are the last: between
+// the others they would hold their places up (one prompt of 2048 among 11 empty
+// ones took 115 us instead of 52).
+struct Spot { int b, tile; };                        // b < 0: none
+template <int R> __device__ __forceinline__ Spot find_tile(const PromptArgs &a, int lane, int at) {
+  if (a.batch <= 64) {
+    const int tiles = lane < a.batch ? tiles_of<R>(a, lane) : 0;
+    auto from = [&](int tile) INLINED {              // workgroups of tiles from `tile` on
+      return __builtin_amdgcn_readlane(wave_scan<false>(max(tiles - tile, 0)), 63);
+    };
+    if (at >= from(0)) return {-1, 0};
+    int lo = 0, hi = __builtin_amdgcn_readlane(wave_scan<true>(tiles), 63), after = 0;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1, n = from(mid);
+      if (n > at) lo = mid;
+      else hi = mid, after = n;
+    }
+    const uint64_t in = __builtin_amdgcn_ballot_w64(tiles > lo);
+    const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0u));
+    return {__builtin_ctzll(__builtin_amdgcn_ballot_w64(tiles > lo && before == at - after)), lo};
+  }
+  const int each = (a.batch + 63) / 64;
+  int mine = 0;
+  for (int b = lane * each; b < min(a.batch, (lane + 1) * each); ++b) mine += tiles_of<R>(a, b);
+  const int upto = wave_scan<false>(mine);
+  const uint64_t here = __builtin_amdgcn_ballot_w64(upto - mine <= at && at < upto);
+  if (!here) return {-1, 0};
+  int base = __builtin_amdgcn_readlane(upto - mine, __builtin_ctzll(here)), b = __builtin_ctzll(here) * each;
+  while (true) {                                     // ends: the tile is of one of the lane's sequences
+    const int n = __builtin_amdgcn_readfirstlane(tiles_of<R>(a, b));
+    if (at < base + n) return {b, n - 1 - (at - base)};
+    base += n;
+    ++b;
+  }
 }
 
 // The float32 path. A workgroup takes 16 CT rows (queries times the heads that
@@ -976,11 +1027,12 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) attn_prompt_f32(PromptAr
   extern __shared__ float shm[];                     // [4][16 CT][D] sums, [4][16 CT] maxima, [4][16 CT] totals
   constexpr int R = 16 * CT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int item = blockIdx.x % a.items, kvh = item % a.kv_heads, group = a.q_heads / a.kv_heads;
-  const Span s = span_of(a, item / a.kv_heads);
-  const int row0 = R * (a.q_tiles - 1 - (int)(blockIdx.x / a.items));
-  if (s.lq <= 0 || row0 >= (int64_t)s.lq * group) return;
-  const RowJob w = {kvh * group, group, kvh, row0, s.lq * group, s.q0, s.k0, s.lk, s.lk - s.lq};
+  const int kvh = blockIdx.x % a.kv_heads, group = a.q_heads / a.kv_heads;
+  const Spot spot = find_tile<R>(a, lane, blockIdx.x / a.kv_heads);
+  if (spot.b < 0) return;
+  const Span s = span_of(a, spot.b);
+  const int row0 = R * spot.tile, rows = (int)min((int64_t)s.lq, a.max_q) * group;
+  const RowJob w = {kvh * group, group, kvh, row0, rows, s.q0, s.k0, s.lk, s.lk - s.lq};
   RowSums<D, CT> o;
   attend_rows<D, true, CT>(a, w, lane, 16 * wave, 64, o);
   const int g = lane >> 4, n = lane & 15;
@@ -1016,13 +1068,20 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) attn_prompt_f32(PromptAr
   }
 }
 
-// The bf16 path. A workgroup takes 128 queries of one head, 32 a wave, against
-// tiles of 64 keys that its waves share in LDS. 32x32x16 products, transposed:
-// S^T = K Q^T leaves lane (h, n) = (lane >> 5, lane & 31) 16 of the scores of
-// query n per 32 keys (keys 8 i + 4 h + r), so a softmax step is within a lane up
-// to one exchange with lane ^ 32, and its weights are the B operand of O^T =
-// V^T P^T as they stand if k-slot 4 i + r of half h means key 8 i + 4 h + r.
-// V^T's A operand in that order is two transposing LDS reads of 4 keys each.
+// The bf16 path. A workgroup takes 32 rows a wave (queries times the heads that
+// share a kept head) against tiles of 64 keys that its waves share in LDS.
+// 32x32x16 products, transposed: S^T = K Q^T leaves lane (h, n) = (lane >> 5, lane
+// & 31) 16 of the scores of row n per 32 keys (keys 8 i + 4 h + r), so a softmax step
+// is within a lane up to one exchange with lane ^ 32, and its weights are the B
+// operand of O^T = V^T P^T as they stand if k-slot 4 i + r of half h means key 8 i +
+// 4 h + r. V^T's A operand in that order is two transposing LDS reads of 4 keys
+// each.
+//
+// The products of a tile and its softmax step take about as long as each other,
+// one on the matrix cores, the other on the VALU. The eight waves, two a SIMD, work
+// in two groups half a tile apart, barriers between the halves: while one group
+// is at its products (the values of the tile before, the scores of this one) the
+// other is at its softmax step.
 //
 // The tiles go from memory to LDS without passing registers, 16 bytes a lane;
 // chunk c of a row lies at chunk c ^ swizzle(row), which spreads both the 16
@@ -1046,42 +1105,62 @@ __device__ __forceinline__ float across32(float x) {   // the value of lane ^ 32
 constexpr int kKeys = 64;                            // keys of a tile
 
 // 64 rows of D bf16 values from src (rows stride_bytes apart, `rows` of them
-// there: the rest reads as zeros) into LDS at dst, a quarter by each wave
-template <int D>
+// there: the rest is not read) into LDS at dst, RUNS KiB by each wave. Written
+// as instructions: these loads have no result registers, and the compiler,
+// which cannot tell the tile they fill from the ones being read, would wait for
+// them before the next LDS read. The wait is the caller's, before the barrier
+// that publishes the tile.
+template <int RUNS>
 __device__ __forceinline__ void stage_tile(const uint8_t *src, int stride_bytes, int rows, uint32_t dst, int wave,
                                            const int *voff) {
-  const __amdgpu_buffer_rsrc_t rs =
-      __builtin_amdgcn_make_buffer_rsrc((void *)src, 0, rows * stride_bytes, 0x00020000);
+  const uint64_t at = reinterpret_cast<uintptr_t>(src);
+  const int lo = __builtin_amdgcn_readfirstlane((int)at), hi = __builtin_amdgcn_readfirstlane((int)(at >> 32));
+  const int bytes = __builtin_amdgcn_readfirstlane(rows * stride_bytes);
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(uintptr_t)(dst + 1024 * (D / 32 * wave + i)), 16,
-                                             voff[i], 0, 0, 0);
+  for (int i = 0; i < RUNS; ++i)
+    asm volatile(
+        "s_mov_b32 s84, %0\n\ts_mov_b32 s85, %1\n\ts_mov_b32 s86, %2\n\ts_mov_b32 s87, 0x20000\n\t"   // a raw buffer
+        "s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, s[84:87], 0 offen lds"
+        :
+        : "s"(lo), "s"(hi), "s"(bytes), "s"(__builtin_amdgcn_readfirstlane((int)(dst + 1024 * (RUNS * wave + i)))),
+          "v"(voff[i])
+        : "memory", "s84", "s85", "s86", "s87");
 }
 
+// barrier between the halves of a tile: LDS reads of before are done where their
+// products are, and none of after may move up
+__device__ __forceinline__ void half_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void staged_tiles_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+constexpr int prompt_waves(int d) { return 4; }
+
 template <int D>
-__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(PromptArgs a) {
-  constexpr int KS = D / 16, DT = D / 32, RB = 2 * D, TB = kKeys * RB;
+__global__ void __launch_bounds__(64 * prompt_waves(D), D == 256 ? 1 : 2) attn_prompt_bf16(PromptArgs a) {
+  constexpr int KS = D / 16, DT = D / 32, RB = 2 * D, TB = kKeys * RB, NW = prompt_waves(D), RUNS = TB / 1024 / NW;
   // LDS: K tiles at 0 and TB, V tiles at 2 TB and 3 TB
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, n = lane & 31;
-  int head_item = blockIdx.x % a.items, tile = a.q_tiles - 1 - blockIdx.x / a.items;
-  const int head = head_item % a.q_heads;
-  const Span sp = span_of(a, head_item / a.q_heads);
-  const int row_wg = 128 * tile;
-  if (row_wg >= sp.lq) return;
-  const int row0 = row_wg + 32 * wave, row = row0 + n < sp.lq ? row0 + n : sp.lq - 1;
-  const int kvh = head / (a.q_heads / a.kv_heads);
+  const int kvh = blockIdx.x % a.kv_heads, group = a.q_heads / a.kv_heads;
+  const Spot spot = find_tile<32 * NW>(a, lane, blockIdx.x / a.kv_heads);
+  if (spot.b < 0) return;
+  const Span sp = span_of(a, spot.b);
+  const int row_wg = 32 * NW * spot.tile, rows = (int)min((int64_t)sp.lq, a.max_q) * group;
+  const int row0 = row_wg + 32 * wave, row = min(row0 + n, rows - 1), query = row / group;
   const int shift = sp.lk - sp.lq;
-  const int last = a.causal ? row + shift : sp.lk - 1;          // this lane's last key
-  const int last_wave = a.causal ? min(row0 + 31, sp.lq - 1) + shift : sp.lk - 1;
-  const int first_wave = a.causal ? row0 + shift : sp.lk - 1;   // keys up to here are seen by the whole wave
-  const int end = (a.causal ? min(row_wg + 127, sp.lq - 1) + shift : sp.lk - 1) + 1;
-  const int tiles = (end + kKeys - 1) / kKeys;
+  const int last = a.causal ? query + shift : sp.lk - 1;        // this lane's last key
+  // keys up to first_wave are seen by all rows of the wave
+  const int first_wave = a.causal ? row0 / group + shift : sp.lk - 1;
+  const int end = (a.causal ? min(row_wg + 32 * NW, rows) - 1 : 0) / group + (a.causal ? shift : sp.lk - 1) + 1;
+  const int tiles = end > 0 ? (end + kKeys - 1) / kKeys : 0;
 
   bf16x8 q[KS];
   {
-    const uint16_t *qp = reinterpret_cast<const uint16_t *>(a.q) + (int64_t)(sp.q0 + row) * a.q_stride +
-                         (int64_t)head * D + 8 * h;
+    const uint16_t *qp = reinterpret_cast<const uint16_t *>(a.q) + (int64_t)(sp.q0 + query) * a.q_stride +
+                         (int64_t)(kvh * group + row - query * group) * D + 8 * h;
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       uint4 u = *reinterpret_cast<const uint4 *>(qp + 16 * i);
@@ -1091,11 +1170,11 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(Prompt
     }
   }
   // staging: lane i of run r of a wave writes LDS chunk 64 r + i of the wave's
-  // quarter; the chunk of the row that belongs there is fetched
-  int koff[D / 32], voff[D / 32];
+  // part; the chunk of the row that belongs there is fetched
+  int koff[RUNS], voff[RUNS];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int chunk = 64 * (D / 32 * wave + i) + lane, r = chunk / (RB / 16), c = chunk % (RB / 16);
+  for (int i = 0; i < RUNS; ++i) {
+    const int chunk = 64 * (RUNS * wave + i) + lane, r = chunk / (RB / 16), c = chunk % (RB / 16);
     const int from = (c ^ swizzle<D>(r)) * 16;
     koff[i] = r * (int)(2 * a.k_stride) + from;
     voff[i] = r * (int)(2 * a.v_stride) + from;
@@ -1103,103 +1182,173 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(Prompt
   const uint8_t *kp = reinterpret_cast<const uint8_t *>(a.k) + 2 * ((int64_t)sp.k0 * a.k_stride + (int64_t)kvh * D);
   const uint8_t *vp = reinterpret_cast<const uint8_t *>(a.v) + 2 * ((int64_t)sp.k0 * a.v_stride + (int64_t)kvh * D);
   const int k_step = (int)(2 * a.k_stride), v_step = (int)(2 * a.v_stride);
-  auto stage = [&](int t) {
-    const int rows = min(kKeys, sp.lk - kKeys * t), buf = t & 1;
-    stage_tile<D>(kp + (int64_t)kKeys * t * k_step, k_step, rows, buf * TB, wave, koff);
-    stage_tile<D>(vp + (int64_t)kKeys * t * v_step, v_step, rows, (2 + buf) * TB, wave, voff);
+  auto stage_k = [&](int t) INLINED {
+    stage_tile<RUNS>(kp + (int64_t)kKeys * t * k_step, k_step, min(kKeys, sp.lk - kKeys * t), (t & 1) * TB, wave, koff);
+  };
+  auto stage_v = [&](int t) INLINED {
+    stage_tile<RUNS>(vp + (int64_t)kKeys * t * v_step, v_step, min(kKeys, sp.lk - kKeys * t), (2 + (t & 1)) * TB, wave,
+                     voff);
   };
 
-  // read addresses within a tile
-  const uint32_t k_rd = n * RB + ((h ^ swizzle<D>(n)) << 4);    // k-step i: ^ (2 i) << 4
-  const int al = lane & 15, gg = (lane >> 4) & 1;
-  const int vrow = 4 * h + (al >> 2);
-  // dimension tile i: ^ i << 6; keys + 8: ^ 2 << 4 and + 8 rows (D = 64: row + 8
-  // flips the same bit of the swizzle)
-  const uint32_t v_rd = vrow * RB + (((2 * gg + ((al & 3) >> 1)) ^ swizzle<D>(vrow)) << 4) + 8 * (al & 1);
+  // LDS addresses of the reads: of K's k-steps and of V's dimension tiles (keys 4 h
+  // on and 8 further); they change between the two tiles' places by ^ TB
+  const int al = lane & 15, gg = (lane >> 4) & 1, vrow = 4 * h + (al >> 2);
+  uint32_t k_at[KS], v_at[DT][2];
+#pragma unroll
+  for (int i = 0; i < KS; ++i) k_at[i] = n * RB + (((2 * i + h) ^ swizzle<D>(n)) << 4);
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = vrow + 8 * e;
+      v_at[i][e] = 2 * TB + r * RB + (((4 * i + 2 * gg + ((al & 3) >> 1)) ^ swizzle<D>(r)) << 4) + 8 * (al & 1);
+    }
+  typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-  f32x16 acc[DT];
+  f32x16 acc[DT], s[2];
+  bf16x8 p[4];
 #pragma unroll
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
   float m = -INFINITY, base = 0.0f, l = 0.0f;
 
-  if (tiles > 0) stage(0);
-  __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0)
-  __syncthreads();
-  for (int t = 0; t < tiles; ++t) {
-    if (t + 1 < tiles) stage(t + 1);
+  // Products FROM .. TO - 1 of a tile's NV + NS: O^T += V^T P^T of a tile, then S^T =
+  // K Q^T of the next. The LDS reads are kept AHEAD products before their use, by
+  // hand: left to itself the compiler reads late and a product waits for every
+  // operand, or reads all at once.
+  constexpr int NV = 4 * DT, NS = 2 * KS, AHEAD = 6;
+  auto operand = [&](int j) INLINED {
+    if (j >= NV) {
+      const int i = (j - NV) >> 1, u = j & 1;
+      return *reinterpret_cast<lds_bf16x8 *>((uintptr_t)(k_at[i] + 32 * RB * u));
+    }
+    const int w = j / DT, i = j % DT;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(v_at[i][0] + 16 * RB * w));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(v_at[i][1] + 16 * RB * w));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto products = [&](auto from, auto to) INLINED {
+    constexpr int F = decltype(from)::value, T = decltype(to)::value;
+    bf16x8 ring[AHEAD];
+#pragma unroll
+    for (int j = F; j < F + AHEAD; ++j) ring[(j - F) % AHEAD] = operand(j);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma clang loop unroll(full)
+    for (int j = F; j < T; ++j) {
+      const bf16x8 x = ring[(j - F) % AHEAD];
+      if (j < NV) {
+        acc[j % DT] = mfma32(x, p[j / DT], acc[j % DT]);
+      } else {
+        const int i = (j - NV) >> 1, u = j & 1;
+        f32x16 zero;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
+        s[u] = mfma32(x, q[i], i == 0 ? zero : s[u]);
+      }
+      if (j + AHEAD < T) ring[(j - F) % AHEAD] = operand(j + AHEAD);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto next_tiles = [&](bool k, bool v) INLINED {            // the reads go on in the other tile's place
+#pragma unroll
+    for (int i = 0; i < KS; ++i) k_at[i] ^= k ? TB : 0;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) v_at[i][0] ^= v ? TB : 0, v_at[i][1] ^= v ? TB : 0;
+  };
+  typedef std::integral_constant<int, 0> first_t;
+  typedef std::integral_constant<int, NV> mid_t;
+  typedef std::integral_constant<int, NV + NS> all_t;
+  auto softmax = [&](int t) INLINED {
     const int j0 = kKeys * t;
-    if (j0 <= last_wave) {
-      const uint32_t kb = (t & 1) * TB + k_rd, vb = (2 + (t & 1)) * TB + v_rd;
-      f32x16 s[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[u][r] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
-          const bf16x8 kk = *reinterpret_cast<lds_bf16x8 *>((uintptr_t)((kb ^ (i << 5)) + 32 * RB * u));
-          s[u] = mfma32(kk, q[i], s[u]);
-        }
-      }
-      if (j0 + kKeys - 1 > first_wave) {             // some query does not see some key of the tile
-        const int rel = last - j0 - 4 * h;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[u][r] = 32 * u + 8 * (r >> 2) + (r & 3) <= rel ? s[u][r] : -INFINITY;
-      }
-      float mt = s[0][0];
+    if (j0 + kKeys - 1 > first_wave) {               // some row does not see some key of the tile
+      const int rel = last - j0 - 4 * h;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[u][r]);
-      mt = fmaxf(mt, across32(mt)) * a.abs_scale2;
-      // the running maximum follows only where it is outgrown by 2^8: weights of
-      // up to 2^8 lose nothing, and the sums are rarely rescaled
-      if (__any(mt > m + 8.0f)) {
-        m = fmaxf(m, mt);
-        const float now = m == -INFINITY ? 0.0f : m;
-        const float alpha = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(base - now);
-        base = now;
-        l *= alpha;
-#pragma unroll
-        for (int i = 0; i < DT; ++i) acc[i] *= alpha;
-      }
-      bf16x8 p[4];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], a.abs_scale2, -base));
-          l += s[u][r];
-        }
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          p[2 * u + w] = __builtin_bit_cast(
-              bf16x8, make_uint4(pack_bf16(s[u][8 * w], s[u][8 * w + 1]), pack_bf16(s[u][8 * w + 2], s[u][8 * w + 3]),
-                                 pack_bf16(s[u][8 * w + 4], s[u][8 * w + 5]),
-                                 pack_bf16(s[u][8 * w + 6], s[u][8 * w + 7])));
-      }
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int i = 0; i < DT; ++i) {
-          typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-          const uint32_t at = (vb ^ (i << 6)) + 16 * RB * w;
-          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)at);
-          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)((at ^ 32) + 8 * RB));
-          typedef short s16x8 __attribute__((ext_vector_type(8)));
-          acc[i] = mfma32(__builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)), p[w],
-                          acc[i]);
-        }
+        for (int r = 0; r < 16; ++r) s[u][r] = 32 * u + 8 * (r >> 2) + (r & 3) <= rel ? s[u][r] : -INFINITY;
     }
-    __builtin_amdgcn_s_waitcnt(0x0F70);              // the next tile is there
-    __syncthreads();
+    float mt = s[0][0];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[u][r]);
+    mt = fmaxf(mt, across32(mt)) * a.abs_scale2;
+    // the running maximum follows only where it is outgrown by 2^8: weights of
+    // up to 2^8 lose nothing, and the sums are rarely rescaled
+    if (__any(mt > m + 8.0f)) {
+      m = fmaxf(m, mt);
+      const float now = m == -INFINITY ? 0.0f : m;
+      const float alpha = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(base - now);
+      base = now;
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) acc[i] *= alpha;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], a.abs_scale2, -base));
+        l += s[u][r];
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        p[2 * u + w] = __builtin_bit_cast(
+            bf16x8, make_uint4(pack_bf16(s[u][8 * w], s[u][8 * w + 1]), pack_bf16(s[u][8 * w + 2], s[u][8 * w + 3]),
+                               pack_bf16(s[u][8 * w + 4], s[u][8 * w + 5]), pack_bf16(s[u][8 * w + 6], s[u][8 * w + 7])));
+    }
+    // done here: put off, the sum would keep all 32 weights in registers, and the
+    // packing would go into the products' phase
+    asm volatile("" : "+v"(l), "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]));
+  };
+
+  // Phases, one barrier each: the first group has its products of tile t in phase
+  // 2 t and its softmax step in 2 t + 1, the second group one phase later. K(t) is
+  // read in phases 2 t and 2 t + 1, V(t) in 2 t + 2 and 2 t + 3; K(t + 1) and V(t) are
+  // asked for in phase 2 t, when what lay in their place was last read in 2 t - 1,
+  // and waited for at the end of 2 t + 1.
+  // Every wave goes through every tile of the workgroup: those that see less would
+  // only wait, and one path keeps the sums in one place.
+  const int late = NW == 8 ? wave >> 2 : 0;
+  auto ask = [&](int t) INLINED {                            // what is asked for in phase 2 t
+    if (t + 1 < tiles) stage_k(t + 1);
+    if (t < tiles) stage_v(t);
+  };
+  if (tiles > 0) {
+    stage_k(0);
+    ask(0);                                          // (in phase 0 for the second group, too)
+    // K(0) is there once no more than what ask(0) brought is on its way
+    if (tiles > 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * RUNS) : "memory");
+    else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(RUNS) : "memory");
+    half_barrier();
+    if (late) half_barrier();                        // phase 0 of the second group
+    products(mid_t(), all_t());
+    next_tiles(true, false);
+    auto half = [&](int t) INLINED {                         // the softmax step's phase and the barriers around it
+      if (late) staged_tiles_landed();
+      if (NW == 8) half_barrier();
+      if (late) ask(t + 1);
+      softmax(t);
+      if (!late) staged_tiles_landed();
+      half_barrier();
+    };
+    for (int t = 0; t + 1 < tiles; ++t) {
+      half(t);
+      if (!late) ask(t + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
+      products(first_t(), all_t());
+      __builtin_amdgcn_s_setprio(0);
+      next_tiles(true, true);
+    }
+    half(tiles - 1);
+    products(first_t(), mid_t());
   }
-  if (row0 >= sp.lq) return;
+  if (NW == 8 && !late) half_barrier();              // the second group's last phase but one
+  if (row0 >= rows) return;
   l += across32(l);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   bool bad = false;
@@ -1210,23 +1359,20 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(Prompt
       acc[i][r] *= inv;
       bad |= !(fabsf(acc[i][r]) < INFINITY);
     }
-  // a weight of 0 times an infinity or a NaN that the query does not see: such
-  // a wave is done over, pair by pair
+  RowJob w = {kvh * group, group, kvh, row0, rows, sp.q0, sp.k0, sp.lk, shift};
+  // a weight of 0 times an infinity or a NaN that the row does not see: such a
+  // wave is done over, pair by pair
   if (__any(bad)) {
-    RowJob w = {head, 1, kvh, row0, sp.lq, sp.q0, sp.k0, sp.lk, shift};
-    rows_alone<D>(a, w, lane);
-    w.row0 += 16;
-    if (w.row0 < sp.lq) rows_alone<D>(a, w, lane);
+    for (; w.row0 < min(row0 + 32, rows); w.row0 += 16) rows_alone<D>(a, w, lane);
     return;
   }
-  if (row0 + n >= sp.lq) return;
-  uint16_t *o = reinterpret_cast<uint16_t *>(a.out) + (int64_t)(sp.q0 + row) * a.out_stride + (int64_t)head * D + 4 * h;
+  if (row0 + n >= rows) return;
 #pragma unroll
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int r = 0; r < 16; r += 4)
-      *reinterpret_cast<uint2 *>(o + 32 * i + 2 * r) =
-          make_uint2(pack_bf16(acc[i][r], acc[i][r + 1]), pack_bf16(acc[i][r + 2], acc[i][r + 3]));
+      store_row<D, false>(a, w, row, 32 * i + 2 * r + 4 * h,
+                          make_float4(acc[i][r], acc[i][r + 1], acc[i][r + 2], acc[i][r + 3]));
 }
 
 // ------------------------------------------------------------ argument checks
@@ -1341,36 +1487,39 @@ int launch_decode_dim(const DecodeArgs &a, int d, glq_dtype dt, int64_t groups, 
 }
 
 template <class K>
-int launch_lds(K kernel, const PromptArgs &a, int64_t groups, size_t shm, hipStream_t st, const char *name) {
+int launch_lds(K kernel, const PromptArgs &a, int64_t groups, int threads, size_t shm, hipStream_t st, const char *name) {
   if (shm > 64 * 1024) {
     const int rc = hip_status(hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm),
                               "hipFuncSetAttribute");
     if (rc) return rc;
   }
-  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(256), shm, st, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), shm, st, a);
   return hip_status(hipGetLastError(), name);
 }
 
-// most: queries of a sequence, at most
+// workgroups of R rows that a launch can need: no sequence has more than max_q
+// queries, and all together no more than total_q
+int64_t prompt_groups(const PromptArgs &a, int R) {
+  const int64_t group = a.q_heads / a.kv_heads, one = (a.max_q * group + R - 1) / R;
+  const int64_t all = (a.total_q * group) / R + a.batch;
+  return (a.batch * one < all ? a.batch * one : all) * a.kv_heads;
+}
+
 template <int D>
-int launch_prompt(PromptArgs a, bool f32, int64_t batch, int64_t most, hipStream_t st) {
+int launch_prompt(const PromptArgs &a, bool f32, hipStream_t st) {
   if (!f32) {
-    a.items = (int32_t)(batch * a.q_heads);
-    a.q_tiles = (int32_t)((most + 127) / 128);
-    return launch_lds(attn_prompt_bf16<D>, a, (int64_t)a.items * a.q_tiles, 4 * kKeys * 2 * D, st, "attn_prompt_bf16");
+    constexpr int NW = prompt_waves(D);
+    return launch_lds(attn_prompt_bf16<D>, a, prompt_groups(a, 32 * NW), 64 * NW, 4 * kKeys * 2 * D, st,
+                      "attn_prompt_bf16");
   }
   // 32 rows a workgroup where that leaves a few for every CU, 16 otherwise
   // (heads of 256: always, two tiles' sums and queries would not fit the registers)
-  a.items = (int32_t)(batch * a.kv_heads);
-  const int64_t rows = most * (a.q_heads / a.kv_heads);
-  const int ct = D < 256 && a.items * ((rows + 31) / 32) >= 4 * kCus ? 2 : 1;
-  a.q_tiles = (int32_t)((rows + 16 * ct - 1) / (16 * ct));
+  const int ct = D < 256 && prompt_groups(a, 32) >= 4 * kCus ? 2 : 1;
   const size_t shm = 4 * 16 * ct * (D + 2) * sizeof(float);
-  const int64_t groups = (int64_t)a.items * a.q_tiles;
   if constexpr (D < 256)
-    if (ct == 2) return launch_lds(attn_prompt_f32<D, 2>, a, groups, shm, st, "attn_prompt_f32");
-  return launch_lds(attn_prompt_f32<D, 1>, a, groups, shm, st, "attn_prompt_f32");
+    if (ct == 2) return launch_lds(attn_prompt_f32<D, 2>, a, prompt_groups(a, 32), 256, shm, st, "attn_prompt_f32");
+  return launch_lds(attn_prompt_f32<D, 1>, a, prompt_groups(a, 16), 256, shm, st, "attn_prompt_f32");
 }
 
 }  // namespace
@@ -1454,14 +1603,14 @@ extern "C" int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_st
     return GLQ_ERR_UNSUPPORTED;
   const float scale2 = P->scale * 1.4426950408889634f;
   const PromptArgs a = {P->q, P->k, P->v, P->out, P->q_stride, P->k_stride, P->v_stride, P->out_stride, P->total_q,
-                        P->total_k, P->cu_q, P->cu_k, P->q_heads, P->kv_heads, 0,
-                        (flags & GLQ_ATTN_CAUSAL) ? 1 : 0, 0,
+                        P->total_k, P->cu_q, P->cu_k, most, P->q_heads, P->kv_heads, (int32_t)P->batch,
+                        (flags & GLQ_ATTN_CAUSAL) ? 1 : 0,
                         scale2, scale2 == 0.0f ? 1.0f : fabsf(scale2), scale2 == 0.0f ? 0u : 0xFFFFFFFFu,
                         scale2 < 0.0f ? 0x80008000u : 0u};
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   switch (P->head_dim) {
-    case 64: return launch_prompt<64>(a, f, P->batch, most, st);
-    case 128: return launch_prompt<128>(a, f, P->batch, most, st);
-    default: return launch_prompt<256>(a, f, P->batch, most, st);
+    case 64: return launch_prompt<64>(a, f, st);
+    case 128: return launch_prompt<128>(a, f, st);
+    default: return launch_prompt<256>(a, f, st);
   }
 }
