@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(256) kv_read_k(KvIo io) {
 
 // ------------------------------------------------------------ one new token
 
-constexpr int decode_per_cu(int format, int dim, bool f32) {
-  return dim == 256 ? 1 : dim == 128 ? (f32 ? 1 : format == GLQ_KV_INT4 ? 3 : 2) : f32 ? 2 : 4;
+constexpr int decode_per_cu(int dim, bool f32) {
+  return dim == 256 ? 1 : dim == 128 ? (f32 ? 1 : 2) : f32 ? 2 : 3;
 }
 
 struct DecodeArgs {
@@ -517,7 +517,7 @@ __device__ __forceinline__ Place find_place(const DecodeArgs &a, int lane) {
 // joins them, in the order of the tiles. Workgroups per CU: what the registers
 // of two tiles leave room for.
 template <int FMT, int D, bool F32>
-__global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode_k(DecodeArgs a) {
+__global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(DecodeArgs a) {
   constexpr int NP = F32 ? 3 : 1, KS = D / 32, DT = D / 16;
   constexpr int WP = F32 ? 3 : 2;                    // bf16 parts of a weight
   constexpr bool BIASED = FMT == GLQ_KV_INT4 && !F32;
@@ -657,19 +657,42 @@ __global__ void __launch_bounds__(256, (decode_per_cu(FMT, D, F32))) attn_decode
     };
     if (t0 < end) {
       int t = t0;
-      for (; t + 128 < end; t += 128) {
-        if constexpr (AHEAD) {
+      if constexpr (AHEAD && D == 256) {             // no registers for two copies of the work
+        for (; t + 128 < end; t += 128) {
           Tile<FMT, D> x;
           ahead(t + 128, x);
-          __builtin_amdgcn_sched_barrier(0);         // the loads go out before the work
+          __builtin_amdgcn_sched_barrier(0);
           work(tile, t);
           tile = x;
-        } else {
+        }
+        work(tile, t);
+      } else if constexpr (AHEAD) {
+        Tile<FMT, D> tile2;
+        while (true) {                               // two tiles in turn: a copy would wait for the loads
+          if (t + 128 >= end) {
+            work(tile, t);
+            break;
+          }
+          ahead(t + 128, tile2);
+          __builtin_amdgcn_sched_barrier(0);         // the loads go out before the work
+          work(tile, t);
+          t += 128;
+          if (t + 128 >= end) {
+            work(tile2, t);
+            break;
+          }
+          ahead(t + 128, tile);
+          __builtin_amdgcn_sched_barrier(0);
+          work(tile2, t);
+          t += 128;
+        }
+      } else {
+        for (; t + 128 < end; t += 128) {
           work(tile, t);
           ahead(t + 128, tile);
         }
+        work(tile, t);
       }
-      work(tile, t);
     }
     l = column_sum(l);
 
@@ -927,9 +950,9 @@ __device__ __forceinline__ void attend_rows(const PromptArgs &a, const RowJob &w
     }
     return;
   }
-  load_rows<D, F32>(a, w, lane, first, x);
+  KvRows<D> y;
+  load_rows<D, F32>(a, w, lane, j0, x);
   for (; j0 + step < end; j0 += step) {
-    KvRows<D> y;
     load_rows<D, F32>(a, w, lane, j0 + step, y);
     __builtin_amdgcn_sched_barrier(0);               // the loads go out before the work
     work(x, j0);
@@ -1455,7 +1478,7 @@ struct DecodePlan { int64_t groups, part_floats, ws_bytes; bool whole; };
 DecodePlan decode_plan(const glq_kv_cache *C, int dt, int64_t batch, int32_t q_heads, int64_t max_len) {
   const int64_t group = q_heads / C->kv_heads, rows = group < 16 ? group : 16;
   const int64_t units = batch * C->kv_heads * ((group + 15) / 16), tiles = (max_len + 127) / 128;
-  const int64_t once = kCus * decode_per_cu(C->format, C->head_dim, dt == GLQ_F32);
+  const int64_t once = kCus * decode_per_cu(C->head_dim, dt == GLQ_F32);
   DecodePlan p;
   p.groups = once > units + once / 2 ? once : units + once / 2;
   p.whole = p.groups > kTickets || tiles <= 1;
