@@ -10,6 +10,7 @@
 //   attn_prompt_f32   packed prompts, float32 matrix instructions
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -68,6 +69,21 @@ __device__ __forceinline__ void store8(void *p, const float *x) {
   }
 }
 
+template <int N> __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
+      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+}
+
 // ------------------------------------------------------------ cache write / read
 
 template <int FMT> __host__ __device__ constexpr int row_bytes(int d) {
@@ -80,37 +96,53 @@ struct KvIo {
   void *dense[2];              // [tokens][heads][d], rows stride[] elements apart
   int64_t stride[2];
   const int32_t *slots;
-  int64_t tokens;
+  uint32_t rows;               // tokens * heads
   int32_t heads, page_shift;
   uint32_t capacity;           // slots in the cache
 };
 
-// cache row of head h at a slot (rows are [page][head][token of the page])
-__device__ __forceinline__ int64_t cache_row(uint32_t slot, int h, int heads, int page_shift) {
-  const uint32_t page = slot >> page_shift, at = slot & ((1u << page_shift) - 1);
-  return (((int64_t)page * heads + h) << page_shift) + at;
+// One lane holds 8 elements of one (token, head) row of the keys and of the values,
+// d / 8 lanes a row.
+template <int D> struct KvPart {
+  uint32_t slot;
+  int64_t cached, dense[2];    // row of the cache, first element of the row in the dense operands
+  __device__ __forceinline__ bool place(const KvIo &io) {
+    const uint32_t row = (blockIdx.x * 256u + threadIdx.x) / (D / 8);
+    if (row >= io.rows) return false;                // whole rows leave together
+    const uint32_t token = row / (uint32_t)io.heads;
+    const int h = (int)(row - token * (uint32_t)io.heads);
+    slot = (uint32_t)io.slots[token];
+    // rows of the cache are [page][head][token of the page]
+    const uint32_t page = slot >> io.page_shift, in_page = slot & ((1u << io.page_shift) - 1);
+    cached = (((int64_t)page * io.heads + h) << io.page_shift) + in_page;
+    dense[0] = token * io.stride[0] + (int64_t)h * D, dense[1] = token * io.stride[1] + (int64_t)h * D;
+    return true;
+  }
+};
+
+// the largest of x over the d / 8 lanes of a row
+template <int LPR> __device__ __forceinline__ uint32_t row_max(uint32_t x) {
+  auto with = [](uint32_t a, int b) { return a > (uint32_t)b ? a : (uint32_t)b; };
+  x = with(x, __builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, false));      // quad_perm: lane ^ 1, lane ^ 2
+  x = with(x, __builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, false));
+  x = with(x, __builtin_amdgcn_mov_dpp((int)x, 0x141, 0xF, 0xF, false));     // half row mirror: the other four
+  if constexpr (LPR >= 16) x = with(x, __builtin_amdgcn_mov_dpp((int)x, 0x140, 0xF, 0xF, false));   // row mirror
+  if constexpr (LPR == 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = r[0] > r[1] ? r[0] : r[1];
+  }
+  return x;
 }
 
-// One lane holds 8 elements of one (token, head) row, d / 8 lanes a row; keys
-// in grid y = 0, values in y = 1. a = max |x| is taken on the bit patterns, so a
-// NaN is the largest and reaches the scale.
-template <int FMT, int D, bool F32>
-__global__ void __launch_bounds__(256) kv_append_k(KvIo io) {
-  constexpr int LPR = D / 8;
-  const int which = blockIdx.y;
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
-  const int at = threadIdx.x % LPR;
-  if (row >= io.tokens * io.heads) return;           // whole rows leave together
-  const int64_t token = row / io.heads;
-  const int h = (int)(row - token * io.heads);
-  const uint32_t slot = (uint32_t)io.slots[token];
-  if (slot >= io.capacity) return;
-  const int64_t esize = F32 ? 4 : 2;
-  float x[8];
-  load8<F32>(reinterpret_cast<const uint8_t *>(io.dense[which]) +
-                 esize * (token * io.stride[which] + (int64_t)h * D + 8 * at), x);
-  const int64_t cr = cache_row(slot, h, io.heads, io.page_shift);
-  uint8_t *out = reinterpret_cast<uint8_t *>(io.cache[which]) + cr * row_bytes<FMT>(D);
+// a = max |x| is taken on the bit patterns, so a NaN is the largest and reaches
+// the scale. The quotient x Q / a comes from a's reciprocal r: y = xQ r, then y + (xQ
+// - y a) r, which is the correctly rounded quotient where r is the correctly
+// rounded reciprocal (Markstein); one division a lane instead of eight (16 ->
+// 11 us for 8192 tokens of 8 heads of 128 into 4 bits). What bounds it
+// then is the memory, and the launch for few tokens.
+template <int FMT, int D>
+__device__ __forceinline__ void append_row(const KvIo &io, const KvPart<D> &p, int which, int at, const float *x) {
+  uint8_t *out = reinterpret_cast<uint8_t *>(io.cache[which]) + p.cached * row_bytes<FMT>(D);
   if constexpr (FMT == GLQ_KV_BF16) {
     store8<false>(out + 16 * at, x);
   } else {
@@ -120,21 +152,20 @@ __global__ void __launch_bounds__(256) kv_append_k(KvIo io) {
       const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
       top = b > top ? b : top;
     }
-#pragma unroll
-    for (int s = 1; s < LPR; s <<= 1) {
-      const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
-      top = o > top ? o : top;
-    }
+    top = row_max<D / 8>(top);
     constexpr float Q = FMT == GLQ_KV_INT8 ? 127.0f : 7.0f;
     const float a = __uint_as_float(top);
-    // x Q must not overflow: both sides of the quotient are scaled by 2^-32
-    // (exact; what leaves the float range there has code 0 anyway)
-    const float pre = a > 0x1p100f ? 0x1p-32f : 1.0f;
     const bool codes = top > 0 && top < 0x7F800000u;  // a = 0, inf and NaN have codes 0
-    const float div = codes ? a * pre : 1.0f;
+    // a moved away from the ends of the range by a power of two: exact, but for
+    // elements that have code 0 anyway
+    const float pre = a > 0x1p64f ? 0x1p-96f : a < 0x1p-64f ? 0x1p96f : 1.0f;
+    const float b = codes ? a * pre : 1.0f, r = 1.0f / b, preq = codes ? pre * Q : 0.0f;
     int q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = codes ? __float2int_rn(x[i] * pre * Q / div) : 0;
+    for (int i = 0; i < 8; ++i) {
+      const float n = codes ? x[i] * preq : 0.0f, y = n * r;
+      q[i] = __float2int_rn(fmaf(fmaf(-y, b, n), r, y));
+    }
     if constexpr (FMT == GLQ_KV_INT8) {
       uint32_t lo = 0, hi = 0;
 #pragma unroll
@@ -149,50 +180,57 @@ __global__ void __launch_bounds__(256) kv_append_k(KvIo io) {
       for (int i = 0; i < 8; ++i) w |= (uint32_t)(q[i] + 8) << (4 * i);
       *reinterpret_cast<uint32_t *>(out + 4 * at) = w;
     }
-    if (at == 0) io.scale[which][cr] = a / Q;
+    if (at == 0) io.scale[which][p.cached] = a / Q;
   }
 }
 
-// The other way: 8 elements a lane, a slot outside the cache gives zeros.
+template <int FMT, int D, bool F32>
+__global__ void __launch_bounds__(256) kv_append_k(KvIo io) {
+  KvPart<D> p;
+  if (!p.place(io) || p.slot >= io.capacity) return;
+  const int at = threadIdx.x % (D / 8);
+  float x[2][8];
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+    load8<F32>(reinterpret_cast<const uint8_t *>(io.dense[w]) + (F32 ? 4 : 2) * (p.dense[w] + 8 * at), x[w]);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) append_row<FMT, D>(io, p, w, at, x[w]);
+}
+
+// The other way: a slot outside the cache gives zeros. Bound by the memory: 50,001
+// tokens of 8 heads of 128 from 8 bits in 64 us, 4.9 TB/s, what a large copy reaches.
 template <int FMT, int D, bool F32>
 __global__ void __launch_bounds__(256) kv_read_k(KvIo io) {
-  constexpr int LPR = D / 8;
-  const int which = blockIdx.y;
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
-  const int at = threadIdx.x % LPR;
-  if (row >= io.tokens * io.heads) return;
-  const int64_t token = row / io.heads;
-  const int h = (int)(row - token * io.heads);
-  const uint32_t slot = (uint32_t)io.slots[token];
-  float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (slot < io.capacity) {
-    const int64_t cr = cache_row(slot, h, io.heads, io.page_shift);
-    const uint8_t *in = reinterpret_cast<const uint8_t *>(io.cache[which]) + cr * row_bytes<FMT>(D);
-    if constexpr (FMT == GLQ_KV_BF16) {
-      load8<false>(in + 16 * at, x);
-    } else {
-      const float s = io.scale[which][cr];
-      if constexpr (FMT == GLQ_KV_INT8) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(in + 8 * at);
+  constexpr int WORDS = row_bytes<FMT>(D) / (D / 8) / 4;       // dwords a lane
+  KvPart<D> p;
+  if (!p.place(io)) return;
+  const int at = threadIdx.x % (D / 8);
+  const bool in = p.slot < io.capacity;
+  uint32_t word[2][WORDS];
+  float scale[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = (float)(int8_t)(w.x >> (8 * i)) * s;
-          x[4 + i] = (float)(int8_t)(w.y >> (8 * i)) * s;
-        }
-      } else {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(in + 4 * at);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (float)((int)((w >> (4 * i)) & 15u) - 8) * s;
-      }
-    }
+  for (int w = 0; w < 2; ++w) {
+    const int64_t row = in ? p.cached : 0;
+    load_words<WORDS>(reinterpret_cast<const uint8_t *>(io.cache[w]) + row * row_bytes<FMT>(D) + 4 * WORDS * at, word[w]);
+    scale[w] = FMT == GLQ_KV_BF16 ? 1.0f : io.scale[w][row];
   }
-  const int64_t esize = F32 ? 4 : 2;
-  store8<F32>(reinterpret_cast<uint8_t *>(io.dense[which]) +
-                  esize * (token * io.stride[which] + (int64_t)h * D + 8 * at), x);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (FMT == GLQ_KV_BF16) x[i] = (i & 1) ? bf16_hi(word[w][i / 2]) : bf16_lo(word[w][i / 2]);
+      else if constexpr (FMT == GLQ_KV_INT8) x[i] = (float)(int8_t)(word[w][i / 4] >> (8 * (i % 4))) * scale[w];
+      else x[i] = (float)((int)((word[w][0] >> (4 * i)) & 15u) - 8) * scale[w];
+      x[i] = in ? x[i] : 0.0f;
+    }
+    store8<F32>(reinterpret_cast<uint8_t *>(io.dense[w]) + (F32 ? 4 : 2) * (p.dense[w] + 8 * at), x);
+  }
 }
 
 // ------------------------------------------------------------ one new token
 
+constexpr int64_t kCus = 256;
 constexpr int decode_per_cu(int dim, bool f32) {
   return dim == 256 ? 1 : dim == 128 ? (f32 ? 1 : 2) : f32 ? 2 : 3;
 }
@@ -209,6 +247,7 @@ struct DecodeArgs {
   float abs_scale2, q_sign;    // |scale| log2(e) and the sign; for a scale of 0, 1 and 0
   int32_t batch, part_floats;  // floats of one workgroup's sums
   int32_t whole;               // no unit is split
+  int32_t even_groups;         // workgroups that are enough where they get even shares
   unsigned int *tickets;       // [workgroups], zero between calls
   float *part;                 // [workgroups][part_floats]
 };
@@ -239,21 +278,6 @@ template <int FMT, int D> __device__ __forceinline__ int k_dim(int c, int g, int
   const int o = (e >> 1) + 4 * (e & 1);              // pairs of nibbles 4 apart
   if constexpr (D == 64) return 16 * g + 8 * c + o;
   return 128 * (c >> 2) + 32 * g + 8 * (c & 3) + o;
-}
-
-template <int N> __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
-  if constexpr (N >= 4) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
-      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-    }
-  } else if constexpr (N == 2) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    w[0] = u.x, w[1] = u.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t *>(p);
-  }
 }
 
 // what no kernel of this call writes: read by scalar loads where the address is uniform
@@ -438,13 +462,15 @@ __device__ __forceinline__ int length_of(const DecodeArgs &a, int b) {
 }
 
 // Parts of a unit of `tiles` tiles where a part should have 1 / inv of them.
-// Splitting costs a workgroup what about 5 tiles take (its sums' way to memory,
-// the ticket, and their way back: 8 us of 1.2 us a tile at 512 tokens), so a
-// unit that little longer stays whole. Any value from 1 on is right; every
-// workgroup computes the same one.
-__device__ __forceinline__ int parts_of(int tiles, float inv) {
+// Splitting costs a workgroup what some tiles take (its sums' way to memory, the
+// ticket, and their way back), so a unit that is no more than `spare` tiles
+// longer stays whole. Where there is a unit for every CU the memory is busy
+// anyway and the cost is paid in full: 32 x 2048 tokens, 8 kept heads, 8 bits: 28.6
+// us whole, 34.9 in halves; one sequence of 1024: 11.9 in eight parts, 13.0 in one.
+// Any value from 1 on is right; every workgroup computes the same one.
+__device__ __forceinline__ int parts_of(int tiles, float inv, int spare) {
   const float n = (float)tiles * inv;
-  return tiles == 0 ? 0 : (float)(tiles - 5) * inv <= 1.0f ? 1 : (int)(n + 0.999f);
+  return tiles == 0 ? 0 : (float)(tiles - spare) * inv <= 1.0f ? 1 : (int)(n + 0.999f);
 }
 
 // inclusive sum, or maximum of values from 0 on, over the lanes up to each (DPP
@@ -461,8 +487,8 @@ template <bool MAX> __device__ __forceinline__ int wave_scan(int x) {
 }
 
 // The smallest share for which the launch has workgroups enough for all parts,
-// found by every workgroup alike: up to 64 sequences by trying 64 shares, one a
-// lane; beyond, by parts <= tiles / share + 1.
+// found by every workgroup alike: up to 64 sequences, one a lane, by bisection;
+// beyond, by parts <= tiles / share + 1.
 __device__ __forceinline__ Place find_place(const DecodeArgs &a, int lane) {
   const int each = (a.batch + 63) / 64, units = a.heads * a.row_tiles, at = blockIdx.x;
   Place p = {0, 0, 0, 0, 0};
@@ -474,24 +500,35 @@ __device__ __forceinline__ Place find_place(const DecodeArgs &a, int lane) {
     return p;
   }
   const int64_t groups = gridDim.x;
+  const int spare = (int64_t)a.batch * units >= kCus ? 8 : 5;
   float inv;
   int mine = 0;
   if (each == 1) {
     const int t = lane < a.batch ? (length_of(a, lane) + 127) >> 7 : 0;
     const int most = __builtin_amdgcn_readlane(wave_scan<true>(t), 63);
-    inv = 1.0f / (float)max(1, (int)(((int64_t)most * (lane + 1) + 63) >> 6));
-    int count = 0;
-    for (int b = 0; b < a.batch; ++b) count += parts_of(__builtin_amdgcn_readlane(t, b), inv);
-    const uint64_t fits = __builtin_amdgcn_ballot_w64((int64_t)count * units <= groups);   // the last lane's does
-    inv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), fits ? __builtin_ctzll(fits) : 63));
-    mine = parts_of(t, inv);
+    const int total = __builtin_amdgcn_readlane(wave_scan<false>(t), 63);
+    // One workgroup a CU streams as fast as two and splits less (one sequence of
+    // 8192, 8 bits: 14.4 us, 18.6 with two), unless that leaves the shares uneven
+    // (32 users of up to 4096: 48 us, 43 with two).
+    for (int64_t limit = min((int64_t)a.even_groups, groups);; limit = groups) {
+      int lo = 0, hi = max(1, most);                 // shares: too small, large enough
+      while (hi - lo > 1) {
+        const int share = (lo + hi) >> 1;
+        const int count = __builtin_amdgcn_readlane(wave_scan<false>(parts_of(t, __builtin_amdgcn_rcpf((float)share), spare)), 63);
+        if ((int64_t)count * units <= limit) hi = share;
+        else lo = share;
+      }
+      inv = __builtin_amdgcn_rcpf((float)hi);
+      if (limit == groups || (float)hi * (float)limit <= 1.15f * (float)total * (float)units) break;
+    }
+    mine = parts_of(t, inv, spare);
   } else {
     int64_t total = 0;
     for (int b = lane; b < a.batch; b += 64) total += (length_of(a, b) + 127) >> 7;
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) total += __shfl_xor(total, s);
     inv = 1.0f / (float)(total * units / (groups - (int64_t)a.batch * units) + 2);
-    for (int b = lane * each; b < min(a.batch, (lane + 1) * each); ++b) mine += parts_of((length_of(a, b) + 127) >> 7, inv);
+    for (int b = lane * each; b < min(a.batch, (lane + 1) * each); ++b) mine += parts_of((length_of(a, b) + 127) >> 7, inv, spare);
   }
   const int upto = wave_scan<false>(mine);
   const uint64_t here = __builtin_amdgcn_ballot_w64((upto - mine) * units <= at && at < upto * units);
@@ -501,7 +538,7 @@ __device__ __forceinline__ Place find_place(const DecodeArgs &a, int lane) {
   p.b = from * each;
   while (true) {                                     // ends: the part is of one of the lane's sequences
     p.tiles = (length_of(a, p.b) + 127) >> 7;
-    p.parts = __builtin_amdgcn_readfirstlane(parts_of(p.tiles, inv));
+    p.parts = __builtin_amdgcn_readfirstlane(parts_of(p.tiles, inv, spare));
     if (at < base + p.parts * units) break;
     base += p.parts * units;
     ++p.b;
@@ -523,8 +560,11 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
   constexpr bool BIASED = FMT == GLQ_KV_INT4 && !F32;
   // float32 heads of 256 over bf16 rows: two tiles would not fit the registers
   constexpr bool AHEAD = !(F32 && D == 256 && FMT == GLQ_KV_BF16);
-  extern __shared__ float shm[];                     // [4][16][D] sums, [4][16] maxima, [4][16] totals
-  float *so = shm, *sm = shm + 4 * 16 * D, *sl = sm + 64;
+  // [4][16] rows of sums, [4][16] maxima, [4][16] totals; rows a float4 longer than
+  // D, so that the 16 lanes of a column write to different banks
+  constexpr int P = D + 4;
+  extern __shared__ float shm[];
+  float *so = shm, *sm = shm + 4 * 16 * P, *sl = sm + 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
   const int64_t esize = F32 ? 4 : 2;
@@ -698,9 +738,11 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
 
     // join the waves
 #pragma unroll
-    for (int i = 0; i < DT; ++i)
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) so[(wave * 16 + n) * D + (4 * g + r) * DT + i] = acc[i][r];
+      for (int i = 0; i < DT; i += 4)
+        *reinterpret_cast<float4 *>(so + (wave * 16 + n) * P + (4 * g + r) * DT + i) =
+            make_float4(acc[i][r], acc[i + 1][r], acc[i + 2][r], acc[i + 3][r]);
     if (g == 0) sm[16 * wave + n] = l == 0.0f ? -INFINITY : base, sl[16 * wave + n] = l;
     __syncthreads();
     const int items = rows * (D / 8);
@@ -719,7 +761,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
       const int row = e / (D / 8), d0 = 8 * (e % (D / 8));
       Sums x = {{0, 0, 0, 0, 0, 0, 0, 0}, -INFINITY, 0.0f};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) merge(x, &so[(16 * w + row) * D + d0], sm[16 * w + row], sl[16 * w + row]);
+      for (int w = 0; w < 4; ++w) merge(x, &so[(16 * w + row) * P + d0], sm[16 * w + row], sl[16 * w + row]);
       if (count == 1) {
         finish(e, x);
       } else {
@@ -748,19 +790,23 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
           Sums x = {{0, 0, 0, 0, 0, 0, 0, 0}, -INFINITY, 0.0f};
           if (e < items && slice < slices) {
             const int row = e / (D / 8);
-            for (int c0 = slice; c0 < count; c0 += 8 * slices) {
-              f32x4 lo[8], hi[8], mt[8];
+            constexpr int FLY = D == 64 ? 8 : F32 || D == 256 ? 24 : 16;     // parts whose loads are in flight
+            for (int c0 = slice; c0 < count; c0 += FLY * slices) {
+              f32x4 lo[FLY], hi[FLY], mt[FLY];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {          // eight parts' loads in flight; past the last: the last, unused
+              for (int j = 0; j < FLY; ++j) {        // past the last: the last, unused
                 const int p = min(c0 + j * slices, count - 1) * a.part_floats;
                 lo[j] = load_shared(all, p + 8 * e), hi[j] = load_shared(all, p + 8 * e + 4);
                 mt[j] = load_shared(all, p + rows * D + 4 * row);
               }
+              __builtin_amdgcn_sched_barrier(0);     // all of them go out before the first is used
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                if (c0 + j * slices >= count) break;
-                const float o[8] = {lo[j][0], lo[j][1], lo[j][2], lo[j][3], hi[j][0], hi[j][1], hi[j][2], hi[j][3]};
-                merge(x, o, mt[j][0], mt[j][1]);
+              for (int j = 0; j < FLY; ++j) {
+                const bool in = c0 + j * slices < count;
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = in ? lo[j][i] : 0.0f, o[4 + i] = in ? hi[j][i] : 0.0f;
+                merge(x, o, in ? mt[j][0] : -INFINITY, in ? mt[j][1] : 0.0f);
               }
             }
             if (slices == 1) finish(e, x);
@@ -1425,11 +1471,10 @@ bool valid_rows(const void *p, int64_t stride, int64_t heads, int64_t d, int dt)
 
 template <bool READ, int FMT, int D>
 int launch_kv(const KvIo &io, glq_dtype dt, hipStream_t st) {
-  const int64_t blocks = (io.tokens * io.heads * (D / 8) + 255) / 256;
-  if (blocks > 0x7FFFFFFF) return GLQ_ERR_UNSUPPORTED;
+  const uint64_t blocks = ((uint64_t)io.rows * (D / 8) + 255) / 256;
   auto kern = READ ? (dt == GLQ_F32 ? kv_read_k<FMT, D, true> : kv_read_k<FMT, D, false>)
                    : (dt == GLQ_F32 ? kv_append_k<FMT, D, true> : kv_append_k<FMT, D, false>);
-  hipLaunchKernelGGL(kern, dim3((unsigned)blocks, 2), dim3(256), 0, st, io);
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, st, io);
   return hip_status(hipGetLastError(), READ ? "kv_read_k" : "kv_append_k");
 }
 
@@ -1449,8 +1494,10 @@ int kv_io(const glq_kv_cache *C, void *k, void *v, glq_dtype dt, int64_t k_strid
   if (!valid_rows(k, k_stride, C->kv_heads, C->head_dim, dt) || !valid_rows(v, v_stride, C->kv_heads, C->head_dim, dt) ||
       !slots || (reinterpret_cast<uintptr_t>(slots) & 3))
     return GLQ_ERR_ARG;
-  if (tokens > 0x7FFFFFFF) return GLQ_ERR_UNSUPPORTED;
-  const KvIo io = {{C->k, C->v}, {C->k_scale, C->v_scale}, {k, v}, {k_stride, v_stride}, slots, tokens, C->kv_heads,
+  // threads are numbered in 32 bits
+  if (tokens > 0x7FFFFFFF / ((int64_t)C->kv_heads * (C->head_dim / 8))) return GLQ_ERR_UNSUPPORTED;
+  const KvIo io = {{C->k, C->v}, {C->k_scale, C->v_scale}, {k, v}, {k_stride, v_stride}, slots,
+                   (uint32_t)(tokens * C->kv_heads), C->kv_heads,
                    log2_of(C->page_size), (uint32_t)(C->num_pages * C->page_size)};
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   switch (C->format) {
@@ -1473,13 +1520,14 @@ int check_decode(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t 
 // Workgroups of a launch: as many as run at once, or half of that more than
 // there are units where these are many; the units' parts are made to fit. Past
 // the ticket counters (one a workgroup) units are not split.
-constexpr int64_t kCus = 256, kTickets = GLQ_ATTN_CTRL_BYTES / 4;
-struct DecodePlan { int64_t groups, part_floats, ws_bytes; bool whole; };
+constexpr int64_t kTickets = GLQ_ATTN_CTRL_BYTES / 4;
+struct DecodePlan { int64_t units, groups, part_floats, ws_bytes; bool whole; };
 DecodePlan decode_plan(const glq_kv_cache *C, int dt, int64_t batch, int32_t q_heads, int64_t max_len) {
   const int64_t group = q_heads / C->kv_heads, rows = group < 16 ? group : 16;
   const int64_t units = batch * C->kv_heads * ((group + 15) / 16), tiles = (max_len + 127) / 128;
   const int64_t once = kCus * decode_per_cu(C->head_dim, dt == GLQ_F32);
   DecodePlan p;
+  p.units = units;
   p.groups = once > units + once / 2 ? once : units + once / 2;
   p.whole = p.groups > kTickets || tiles <= 1;
   if (p.whole) p.groups = units;
@@ -1489,18 +1537,34 @@ DecodePlan decode_plan(const glq_kv_cache *C, int dt, int64_t batch, int32_t q_h
   return p;
 }
 
+// Dynamic LDS above the default limit of 64 KiB, asked for once per kernel and device
+template <auto Kernel> int allow_lds(size_t bytes) {
+  if (bytes <= 64 * 1024) return GLQ_OK;
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  const int rc = hip_status(hipGetDevice(&dev), "hipGetDevice");
+  if (rc) return rc;
+  if (dev < 64 && (allowed.load(std::memory_order_relaxed) >> dev & 1)) return GLQ_OK;
+  const int rc2 = hip_status(hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes),
+                             "hipFuncSetAttribute");
+  if (rc2 == GLQ_OK && dev < 64) allowed.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  return rc2;
+}
+
+template <int FMT, int D, bool F32>
+int launch_decode_kernel(const DecodeArgs &a, int64_t groups, hipStream_t st) {
+  constexpr size_t shm = (4 * 16 * (D + 4) + 128) * sizeof(float);
+  const int rc = allow_lds<attn_decode_k<FMT, D, F32>>(shm);
+  if (rc) return rc;
+  hipLaunchKernelGGL((attn_decode_k<FMT, D, F32>), dim3((unsigned)groups), dim3(256), shm, st, a);
+  return hip_status(hipGetLastError(), "attn_decode_k");
+}
+
 template <int FMT, int D>
 int launch_decode(const DecodeArgs &a, glq_dtype dt, int64_t groups, hipStream_t st) {
-  const size_t shm = (4 * 16 * D + 128) * sizeof(float);
-  auto kern = dt == GLQ_F32 ? attn_decode_k<FMT, D, true> : attn_decode_k<FMT, D, false>;
-  if (shm > 64 * 1024) {
-    const int rc = hip_status(hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm),
-                              "hipFuncSetAttribute");
-    if (rc) return rc;
-  }
-  hipLaunchKernelGGL(kern, dim3((unsigned)groups), dim3(256), shm, st, a);
-  return hip_status(hipGetLastError(), "attn_decode_k");
+  return dt == GLQ_F32 ? launch_decode_kernel<FMT, D, true>(a, groups, st)
+                       : launch_decode_kernel<FMT, D, false>(a, groups, st);
 }
 
 template <int FMT>
@@ -1509,15 +1573,11 @@ int launch_decode_dim(const DecodeArgs &a, int d, glq_dtype dt, int64_t groups, 
                                                                       : launch_decode<FMT, 256>(a, dt, groups, st);
 }
 
-template <class K>
-int launch_lds(K kernel, const PromptArgs &a, int64_t groups, int threads, size_t shm, hipStream_t st, const char *name) {
-  if (shm > 64 * 1024) {
-    const int rc = hip_status(hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm),
-                              "hipFuncSetAttribute");
-    if (rc) return rc;
-  }
-  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), shm, st, a);
+template <auto Kernel>
+int launch_rows(const PromptArgs &a, int64_t groups, size_t shm, hipStream_t st, const char *name) {
+  const int rc = allow_lds<Kernel>(shm);
+  if (rc) return rc;
+  hipLaunchKernelGGL(Kernel, dim3((unsigned)groups), dim3(256), shm, st, a);
   return hip_status(hipGetLastError(), name);
 }
 
@@ -1531,18 +1591,15 @@ int64_t prompt_groups(const PromptArgs &a, int R) {
 
 template <int D>
 int launch_prompt(const PromptArgs &a, bool f32, hipStream_t st) {
-  if (!f32) {
-    constexpr int NW = prompt_waves(D);
-    return launch_lds(attn_prompt_bf16<D>, a, prompt_groups(a, 32 * NW), 64 * NW, 4 * kKeys * 2 * D, st,
-                      "attn_prompt_bf16");
-  }
+  if (!f32)
+    return launch_rows<attn_prompt_bf16<D>>(a, prompt_groups(a, 128), 4 * kKeys * 2 * D, st, "attn_prompt_bf16");
   // 32 rows a workgroup where that leaves a few for every CU, 16 otherwise
   // (heads of 256: always, two tiles' sums and queries would not fit the registers)
-  const int ct = D < 256 && prompt_groups(a, 32) >= 4 * kCus ? 2 : 1;
-  const size_t shm = 4 * 16 * ct * (D + 2) * sizeof(float);
+  const int64_t groups = prompt_groups(a, 32);
+  constexpr size_t shm = 4 * 16 * (D + 2) * sizeof(float);
   if constexpr (D < 256)
-    if (ct == 2) return launch_lds(attn_prompt_f32<D, 2>, a, prompt_groups(a, 32), 256, shm, st, "attn_prompt_f32");
-  return launch_lds(attn_prompt_f32<D, 1>, a, prompt_groups(a, 16), 256, shm, st, "attn_prompt_f32");
+    if (groups >= 4 * kCus) return launch_rows<attn_prompt_f32<D, 2>>(a, groups, 2 * shm, st, "attn_prompt_f32");
+  return launch_rows<attn_prompt_f32<D, 1>>(a, prompt_groups(a, 16), shm, st, "attn_prompt_f32");
 }
 
 }  // namespace
@@ -1592,6 +1649,9 @@ extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype d
                         scale2 == 0.0f ? 1.0f : fabsf(scale2), scale2 == 0.0f ? 0.0f : copysignf(1.0f, scale2),
                         (int32_t)batch, (int32_t)p.part_floats,
                         p.whole ? 1 : 0,
+                        // (4-bit operands want two workgroups a CU for their VALU work)
+                        C->head_dim == 128 && C->format != GLQ_KV_INT4 && p.groups >= kCus && p.units <= kCus
+                            ? (int32_t)kCus : (int32_t)p.groups,
                         reinterpret_cast<unsigned int *>(workspace),
                         reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + GLQ_ATTN_CTRL_BYTES)};
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);

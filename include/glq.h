@@ -399,7 +399,8 @@ typedef struct {
  *   slots       device int32 [tokens]; a slot outside the cache (negative, or
  *               >= num_pages * page_size) drops its token. Two tokens with one
  *               slot leave it with either's contents.
- * tokens == 0 is a successful no-op. GLQ_KV_BF16 rounds to nearest even.
+ * tokens == 0 is a successful no-op; GLQ_ERR_UNSUPPORTED for tokens * kv_heads *
+ * head_dim >= 2^34. GLQ_KV_BF16 rounds to nearest even.
  */
 int glq_kv_append(const glq_kv_cache *C, const void *k, const void *v, glq_dtype dt, int64_t k_stride,
                   int64_t v_stride, const int32_t *slots, int64_t tokens, void *hip_stream);
