@@ -545,3 +545,22 @@ def test_binding_refusals(gen):
         glq.attn_prompt(k, k, k, k.clone(), cu.long())
     with pytest.raises(ValueError):
         glq.attn_prompt(torch.cat((k, k[:, :1]), 1), k, k, torch.cat((k, k[:, :1]), 1), cu)
+
+
+# ------------------------------------------------------------------- all together
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cache,most", [("bf16", 0.02), ("int8", 0.025), ("int4", 0.2)])
+def test_attention_block_example(cache, most):
+    # the example: compressed projections, rotated keys in the cache, a prompt in
+    # two chunks, then tokens. bf16: a few roundings of 2^-8 of projections, weights
+    # and sums; 8 bits: steps of max / 127 of about 2.5 sigma, 0.006 sigma rms, in
+    # keys and values; 4 bits: 0.1 sigma rms in each
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_block.py")
+    spec = importlib.util.spec_from_file_location("attention_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for err in mod.run(cache=cache, tokens=4):
+        assert err <= most
