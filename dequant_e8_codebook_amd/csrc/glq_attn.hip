@@ -453,7 +453,7 @@ __device__ __forceinline__ void merge(Sums &s, const float *o, float top, float 
 // 16 of its query heads; 128-token tiles).
 struct Place {
   int b, unit, part, parts;    // unit within the sequence; of `parts` (0: nothing to do)
-  int tiles;                   // of the unit
+  int len, tiles;              // of the sequence; tiles of the unit
 };
 
 __device__ __forceinline__ int length_of(const DecodeArgs &a, int b) {
@@ -491,11 +491,12 @@ template <bool MAX> __device__ __forceinline__ int wave_scan(int x) {
 // beyond, by parts <= tiles / share + 1.
 __device__ __forceinline__ Place find_place(const DecodeArgs &a, int lane) {
   const int each = (a.batch + 63) / 64, units = a.heads * a.row_tiles, at = blockIdx.x;
-  Place p = {0, 0, 0, 0, 0};
+  Place p = {0, 0, 0, 0, 0, 0};
   if (a.whole) {
     p.b = at / units;
     p.unit = at - p.b * units;
-    p.tiles = (length_of(a, p.b) + 127) >> 7;
+    p.len = length_of(a, p.b);
+    p.tiles = (p.len + 127) >> 7;
     p.parts = p.tiles > 0 ? 1 : 0;
     return p;
   }
@@ -503,8 +504,10 @@ __device__ __forceinline__ Place find_place(const DecodeArgs &a, int lane) {
   const int spare = (int64_t)a.batch * units >= kCus ? 8 : 5;
   float inv;
   int mine = 0;
+  int len = 0;                                       // of the lane's sequence
   if (each == 1) {
-    const int t = lane < a.batch ? (length_of(a, lane) + 127) >> 7 : 0;
+    len = lane < a.batch ? length_of(a, lane) : 0;
+    const int t = (len + 127) >> 7;
     const int most = __builtin_amdgcn_readlane(wave_scan<true>(t), 63);
     const int total = __builtin_amdgcn_readlane(wave_scan<false>(t), 63);
     // One workgroup a CU streams as fast as two and splits less (one sequence of
@@ -537,7 +540,8 @@ __device__ __forceinline__ Place find_place(const DecodeArgs &a, int lane) {
   int base = __builtin_amdgcn_readlane(upto - mine, from) * units;
   p.b = from * each;
   while (true) {                                     // ends: the part is of one of the lane's sequences
-    p.tiles = (length_of(a, p.b) + 127) >> 7;
+    p.len = each == 1 ? __builtin_amdgcn_readlane(len, from) : length_of(a, p.b);
+    p.tiles = (p.len + 127) >> 7;
     p.parts = __builtin_amdgcn_readfirstlane(parts_of(p.tiles, inv, spare));
     if (at < base + p.parts * units) break;
     base += p.parts * units;
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
   const scalar_ints table = (scalar_ints)(uintptr_t)(a.table + b * a.max_pages);
   const int tile0 = (int)((int64_t)at.tiles * at.part / at.parts);
   const int tile1 = (int)((int64_t)at.tiles * (at.part + 1) / at.parts);
-  const int t0 = 128 * tile0 + 32 * wave, end = min(length_of(a, at.b), 128 * tile1);
+  const int t0 = 128 * tile0 + 32 * wave, end = min(at.len, 128 * tile1);
   {
     Tile<FMT, D> tile;
     Pages next = {{0, 0}};
@@ -1034,36 +1038,38 @@ __device__ __forceinline__ void rows_alone(const PromptArgs &a, const RowJob &w,
                                       o.acc[0][4 * i + 2][r] * inv, o.acc[0][4 * i + 3][r] * inv));
 }
 
-// the sequence of a workgroup: its first query and key row and their numbers
+// a sequence: its first query and key row and their numbers
 struct Span { int q0, lq, k0, lk; };
 __device__ __forceinline__ Span span_of(const PromptArgs &a, int64_t b) {
   const int q0 = clamped(a.cu_q[b], a.total_q), q1 = clamped(a.cu_q[b + 1], a.total_q);
   const int k0 = clamped(a.cu_k[b], a.total_k), k1 = clamped(a.cu_k[b + 1], a.total_k);
-  return {__builtin_amdgcn_readfirstlane(q0), __builtin_amdgcn_readfirstlane(q1 - q0),
-          __builtin_amdgcn_readfirstlane(k0), __builtin_amdgcn_readfirstlane(k1 - k0 > 0 ? k1 - k0 : 0)};
+  return {q0, q1 - q0, k0, k1 - k0 > 0 ? k1 - k0 : 0};
 }
 
-// Workgroups of sequence b (R rows each: queries times the heads of a kept head)
-template <int R> __device__ __forceinline__ int tiles_of(const PromptArgs &a, int b) {
-  const int64_t q = clamped(a.cu_q[b + 1], a.total_q) - clamped(a.cu_q[b], a.total_q);
-  const int64_t n = q < a.max_q ? q : a.max_q;       // more than the launch was made for are not done
+// Workgroups of a sequence of lq queries (R rows each: queries times the heads of a
+// kept head); more queries than the launch was made for are not done
+template <int R> __device__ __forceinline__ int tiles_of(const PromptArgs &a, int lq) {
+  const int64_t n = lq < a.max_q ? lq : a.max_q;
   return n > 0 ? (int)((n * (a.q_heads / a.kv_heads) + R - 1) / R) : 0;
 }
 
 // The sequence and tile of a kept head's at-th workgroup. In a causal prompt the
 // last tiles see the most keys and come first, over all sequences (up to 64 of
-// them: the highest tile for which few enough come before it, by bisection on
-// counts; beyond, sequence by sequence). Workgroups without a tile are the last: between
-// the others they would hold their places up (one prompt of 2048 among 11 empty
-// ones took 115 us instead of 52).
-struct Spot { int b, tile; };                        // b < 0: none
+// them, one a lane: the highest tile for which few enough come before it, by
+// bisection on counts; beyond, sequence by sequence). Workgroups without a tile are the
+// last: between the others they would hold their places up (one prompt of 2048 among 11
+// empty ones took 115 us instead of 52).
+struct Spot { Span span; int tile; };                // tile < 0: none
 template <int R> __device__ __forceinline__ Spot find_tile(const PromptArgs &a, int lane, int at) {
+  const Spot none = {{0, 0, 0, 0}, -1};
   if (a.batch <= 64) {
-    const int tiles = lane < a.batch ? tiles_of<R>(a, lane) : 0;
+    Span mine = {0, 0, 0, 0};
+    if (lane < a.batch) mine = span_of(a, lane);
+    const int tiles = tiles_of<R>(a, mine.lq);
     auto from = [&](int tile) INLINED {              // workgroups of tiles from `tile` on
       return __builtin_amdgcn_readlane(wave_scan<false>(max(tiles - tile, 0)), 63);
     };
-    if (at >= from(0)) return {-1, 0};
+    if (at >= from(0)) return none;
     int lo = 0, hi = __builtin_amdgcn_readlane(wave_scan<true>(tiles), 63), after = 0;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1, n = from(mid);
@@ -1072,18 +1078,23 @@ template <int R> __device__ __forceinline__ Spot find_tile(const PromptArgs &a, 
     }
     const uint64_t in = __builtin_amdgcn_ballot_w64(tiles > lo);
     const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0u));
-    return {__builtin_ctzll(__builtin_amdgcn_ballot_w64(tiles > lo && before == at - after)), lo};
+    const int b = __builtin_ctzll(__builtin_amdgcn_ballot_w64(tiles > lo && before == at - after));
+    return {{__builtin_amdgcn_readlane(mine.q0, b), __builtin_amdgcn_readlane(mine.lq, b),
+             __builtin_amdgcn_readlane(mine.k0, b), __builtin_amdgcn_readlane(mine.lk, b)}, lo};
   }
   const int each = (a.batch + 63) / 64;
   int mine = 0;
-  for (int b = lane * each; b < min(a.batch, (lane + 1) * each); ++b) mine += tiles_of<R>(a, b);
+  for (int b = lane * each; b < min(a.batch, (lane + 1) * each); ++b) mine += tiles_of<R>(a, span_of(a, b).lq);
   const int upto = wave_scan<false>(mine);
   const uint64_t here = __builtin_amdgcn_ballot_w64(upto - mine <= at && at < upto);
-  if (!here) return {-1, 0};
+  if (!here) return none;
   int base = __builtin_amdgcn_readlane(upto - mine, __builtin_ctzll(here)), b = __builtin_ctzll(here) * each;
   while (true) {                                     // ends: the tile is of one of the lane's sequences
-    const int n = __builtin_amdgcn_readfirstlane(tiles_of<R>(a, b));
-    if (at < base + n) return {b, n - 1 - (at - base)};
+    const Span s = span_of(a, b);
+    const int n = __builtin_amdgcn_readfirstlane(tiles_of<R>(a, s.lq));
+    if (at < base + n)
+      return {{__builtin_amdgcn_readfirstlane(s.q0), __builtin_amdgcn_readfirstlane(s.lq),
+               __builtin_amdgcn_readfirstlane(s.k0), __builtin_amdgcn_readfirstlane(s.lk)}, n - 1 - (at - base)};
     base += n;
     ++b;
   }
@@ -1098,8 +1109,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) attn_prompt_f32(PromptAr
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kvh = blockIdx.x % a.kv_heads, group = a.q_heads / a.kv_heads;
   const Spot spot = find_tile<R>(a, lane, blockIdx.x / a.kv_heads);
-  if (spot.b < 0) return;
-  const Span s = span_of(a, spot.b);
+  if (spot.tile < 0) return;
+  const Span s = spot.span;
   const int row0 = R * spot.tile, rows = (int)min((int64_t)s.lq, a.max_q) * group;
   const RowJob w = {kvh * group, group, kvh, row0, rows, s.q0, s.k0, s.lk, s.lk - s.lq};
   RowSums<D, CT> o;
@@ -1215,8 +1226,8 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), D == 256 ? 1 : 2) attn_p
   const int h = lane >> 5, n = lane & 31;
   const int kvh = blockIdx.x % a.kv_heads, group = a.q_heads / a.kv_heads;
   const Spot spot = find_tile<32 * NW>(a, lane, blockIdx.x / a.kv_heads);
-  if (spot.b < 0) return;
-  const Span sp = span_of(a, spot.b);
+  if (spot.tile < 0) return;
+  const Span sp = spot.span;
   const int row_wg = 32 * NW * spot.tile, rows = (int)min((int64_t)sp.lq, a.max_q) * group;
   const int row0 = row_wg + 32 * wave, row = min(row0 + n, rows - 1), query = row / group;
   const int shift = sp.lk - sp.lq;
