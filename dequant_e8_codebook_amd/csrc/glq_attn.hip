@@ -1148,8 +1148,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) attn_prompt_f32(PromptAr
   }
 }
 
-// The bf16 path. A workgroup takes 32 rows a wave (queries times the heads that
-// share a kept head) against tiles of 64 keys that its waves share in LDS.
+// The bf16 path. A workgroup takes 128 rows (queries times the heads that share a
+// kept head), 32 a wave, against tiles of 64 keys that its waves share in LDS.
 // 32x32x16 products, transposed: S^T = K Q^T leaves lane (h, n) = (lane >> 5, lane
 // & 31) 16 of the scores of row n per 32 keys (keys 8 i + 4 h + r), so a softmax step
 // is within a lane up to one exchange with lane ^ 32, and its weights are the B
@@ -1157,11 +1157,13 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) attn_prompt_f32(PromptAr
 // 4 h + r. V^T's A operand in that order is two transposing LDS reads of 4 keys
 // each.
 //
-// The products of a tile and its softmax step take about as long as each other,
-// one on the matrix cores, the other on the VALU. The eight waves, two a SIMD, work
-// in two groups half a tile apart, barriers between the halves: while one group
-// is at its products (the values of the tile before, the scores of this one) the
-// other is at its softmax step.
+// The products of a tile (1024 cycles of the matrix cores) and its softmax step (about
+// 980 of the VALU) are phases of their own; two workgroups share a CU and are rarely
+// in the same one. Measured level or slower: eight waves in two groups half a tile
+// apart, with barriers between the phases (4096 tokens, 24 heads, no mask: 219
+// us against 204, for the coarser workgroups), and the softmax step spread
+// between the products of one wave (207; 8192 tokens, 32 heads, causal 519
+// against 493): the clock falls by as much as the overlap gains (1.8 GHz).
 //
 // The tiles go from memory to LDS without passing registers, 16 bytes a lane;
 // chunk c of a row lies at chunk c ^ swizzle(row), which spreads both the 16
@@ -1207,20 +1209,18 @@ __device__ __forceinline__ void stage_tile(const uint8_t *src, int stride_bytes,
         : "memory", "s84", "s85", "s86", "s87");
 }
 
-// barrier between the halves of a tile: LDS reads of before are done where their
-// products are, and none of after may move up
-__device__ __forceinline__ void half_barrier() {
+// The barrier of a step: LDS reads of before are done where their products are, and none
+// of after may move up
+__device__ __forceinline__ void tile_barrier() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 __device__ __forceinline__ void staged_tiles_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-constexpr int prompt_waves(int d) { return 4; }
-
 template <int D>
-__global__ void __launch_bounds__(64 * prompt_waves(D), D == 256 ? 1 : 2) attn_prompt_bf16(PromptArgs a) {
-  constexpr int KS = D / 16, DT = D / 32, RB = 2 * D, TB = kKeys * RB, NW = prompt_waves(D), RUNS = TB / 1024 / NW;
+__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(PromptArgs a) {
+  constexpr int KS = D / 16, DT = D / 32, RB = 2 * D, TB = kKeys * RB, NW = 4, RUNS = TB / 1024 / NW;
   // LDS: K tiles at 0 and TB, V tiles at 2 TB and 3 TB
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, n = lane & 31;
@@ -1385,49 +1385,38 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), D == 256 ? 1 : 2) attn_p
     asm volatile("" : "+v"(l), "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]));
   };
 
-  // Phases, one barrier each: the first group has its products of tile t in phase
-  // 2 t and its softmax step in 2 t + 1, the second group one phase later. K(t) is
-  // read in phases 2 t and 2 t + 1, V(t) in 2 t + 2 and 2 t + 3; K(t + 1) and V(t) are
-  // asked for in phase 2 t, when what lay in their place was last read in 2 t - 1,
-  // and waited for at the end of 2 t + 1.
-  // Every wave goes through every tile of the workgroup: those that see less would
-  // only wait, and one path keeps the sums in one place.
-  const int late = NW == 8 ? wave >> 2 : 0;
-  auto ask = [&](int t) INLINED {                            // what is asked for in phase 2 t
+  // Step t: the softmax step of tile t, then the values of tile t and the scores of tile
+  // t + 1. Asked for before the products of step t - 1: K(t + 1) and V(t), whose places
+  // were last read in step t - 2; the barrier between softmax step and products
+  // finds them landed. Every wave goes through every tile of the workgroup: those
+  // that see less would only wait, and one path keeps the sums in one place.
+  auto ask = [&](int t) INLINED {
     if (t + 1 < tiles) stage_k(t + 1);
     if (t < tiles) stage_v(t);
   };
   if (tiles > 0) {
     stage_k(0);
-    ask(0);                                          // (in phase 0 for the second group, too)
+    ask(0);
     // K(0) is there once no more than what ask(0) brought is on its way
     if (tiles > 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * RUNS) : "memory");
     else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(RUNS) : "memory");
-    half_barrier();
-    if (late) half_barrier();                        // phase 0 of the second group
+    tile_barrier();
     products(mid_t(), all_t());
     next_tiles(true, false);
-    auto half = [&](int t) INLINED {                         // the softmax step's phase and the barriers around it
-      if (late) staged_tiles_landed();
-      if (NW == 8) half_barrier();
-      if (late) ask(t + 1);
-      softmax(t);
-      if (!late) staged_tiles_landed();
-      half_barrier();
-    };
     for (int t = 0; t + 1 < tiles; ++t) {
-      half(t);
-      if (!late) ask(t + 1);
+      softmax(t);
+      staged_tiles_landed();
+      tile_barrier();
+      ask(t + 1);
       __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_setprio(1);
       products(first_t(), all_t());
-      __builtin_amdgcn_s_setprio(0);
       next_tiles(true, true);
     }
-    half(tiles - 1);
+    softmax(tiles - 1);
+    staged_tiles_landed();
+    tile_barrier();
     products(first_t(), mid_t());
   }
-  if (NW == 8 && !late) half_barrier();              // the second group's last phase but one
   if (row0 >= rows) return;
   l += across32(l);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
