@@ -572,16 +572,18 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
   const int64_t esize = F32 ? 4 : 2;
-  const int q_heads = a.heads * a.group;
-  for (int b = blockIdx.x; b < a.batch; b += gridDim.x)      // sequences without tokens: zeros
-    if (length_of(a, b) == 0)
-      for (int e = threadIdx.x; e < q_heads * (D / 8); e += 256) {
-        const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        store8<F32>(reinterpret_cast<uint8_t *>(a.out) + esize * (b * a.out_stride + 8 * (int64_t)e), zero);
-      }
+  // sequences without tokens: zeros (last, so that no load waits for it)
+  auto zero_rows = [&]() INLINED {
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x)
+      if (length_of(a, b) == 0)
+        for (int e = threadIdx.x; e < a.heads * a.group * (D / 8); e += 256) {
+          const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+          store8<F32>(reinterpret_cast<uint8_t *>(a.out) + esize * (b * a.out_stride + 8 * (int64_t)e), zero);
+        }
+  };
 
   const Place at = find_place(a, lane);
-  if (at.parts == 0) return;
+  if (at.parts == 0) return zero_rows();
   const int rt = at.unit % a.row_tiles, h = at.unit / a.row_tiles;
   const int head0 = h * a.group + 16 * rt, rows = min(16, a.group - 16 * rt);
   const int64_t b = at.b;
@@ -832,6 +834,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
       }
     }
   }
+  zero_rows();
 }
 
 // ------------------------------------------------------------ prompts

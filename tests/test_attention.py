@@ -291,6 +291,70 @@ def test_decode_scale_stream_and_graph(gen):
         torch.cuda.synchronize()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,fmt,dtype", [(70, "int8", "bf16"), (130, "int4", "bf16"), (65, "bf16", "f32")])
+def test_decode_many_sequences(gen, batch, fmt, dtype):
+    # more than 64 sequences: the parts are found in another way; one sequence far
+    # longer than the rest, and empty ones
+    lens = [int(x) for x in torch.randint(0, 200, (batch,), generator=gen)]
+    lens[0], lens[5], lens[batch - 1] = 0, 3000, 17
+    cache, q, table, ln, ref, mag = _decode_case(gen, fmt, lens, 4, 2, 64, 16, dtype)
+    out, ws = _decode(cache, q, table, ln, 3000)
+    _held(out, ref, mag, dtype)
+    assert not ws[:65536].any()
+
+
+@pytest.mark.gpu
+def test_decode_one_workspace_for_many_calls(gen):
+    # one workspace, large enough for all, under batches and lengths that change
+    cases = [_decode_case(gen, "int8", lens, 8, 2, 128, 32, "bf16")
+             for lens in ([5000], [40] * 9, [1, 700, 0], [3000, 2999, 12, 1024])]
+    size = max(glq.attn_decode_workspace_bytes(c[0], c[1].shape[0], 8, 5000) for c in cases)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for cache, q, table, ln, ref, mag in cases:
+            out, _ = _decode(cache, q, table, ln, int(ln.max()), ws)
+            _held(out, ref, mag, "bf16")
+            assert not ws[:65536].any()
+
+
+@pytest.mark.gpu
+def test_decode_nothing_cached(gen):
+    cache, q, table, ln, _, _ = _decode_case(gen, "bf16", [0, 0, 0], 2, 1, 64, 16, "bf16")
+    out, _ = _decode(cache, q, table, ln, 0)
+    assert not out.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "bf16"])
+def test_cache_beyond_32_bits(gen, fmt):
+    # pages whose rows lie past 2^32 bytes (and 2^31 elements) into the cache
+    heads, dim, page = 8, 128, 64
+    pages = 2 ** 32 // (heads * page * dim) + 40
+    dt = torch.int8 if fmt == "int8" else torch.bfloat16
+    k, v = (torch.empty(pages, heads, page, dim, dtype=dt, device="cuda") for _ in range(2))
+    scales = [torch.empty(pages, heads, page, device="cuda") for _ in range(2)] if fmt == "int8" else [None, None]
+    cache = glq.KvCache(k, v, *scales)
+    n = 150
+    x, y = (_normal(gen, n, heads, dim, dtype=torch.bfloat16).cuda() for _ in range(2))
+    table = torch.tensor([[pages - 1, 3, pages - 7]], dtype=torch.int32, device="cuda")
+    at = torch.arange(n, device="cuda")
+    slots = (table[0].long()[at // page] * page + at % page).to(torch.int32)
+    glq.kv_append(cache, x, y, slots)
+    xo, yo = torch.empty_like(x), torch.empty_like(y)
+    glq.kv_read(cache, slots, xo, yo)
+    assert torch.equal(xo.cpu(), _ref_values(x.cpu().float(), fmt).to(torch.bfloat16))
+    assert torch.equal(yo.cpu(), _ref_values(y.cpu().float(), fmt).to(torch.bfloat16))
+    q = _normal(gen, 1, 16, dim, dtype=torch.bfloat16).cuda()
+    out, _ = _decode(cache, q, table, torch.tensor([n], dtype=torch.int32, device="cuda"), n)
+    kk, vv = (_ref_values(z.cpu().float(), fmt) for z in (x, y))
+    for h in range(16):
+        ref, mag = _ref_attend(q[0, h:h + 1].cpu(), kk[:, h // 2], vv[:, h // 2], dim ** -0.5, torch.ones(1, n, dtype=torch.bool))
+        _held(out[0, h:h + 1], ref, mag, "bf16")
+    del cache, k, v, scales
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------------ prompts
 
 def _prompt_case(gen, lens_q, lens_k, q_heads, kv_heads, dim, dtype, causal, scale=None, fused=False):
@@ -398,6 +462,49 @@ def test_prompt_scale_and_extreme_scores(gen):
     big = torch.full_like(q, -3e38)
     out = _prompt(big, torch.full_like(k, 3e38), v, cu, None)
     assert not out.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_many_sequences(gen, dtype, causal):
+    # more than 64 sequences: the workgroups find theirs in another way
+    lens = [int(x) for x in torch.randint(0, 90, (67,), generator=gen)]
+    lens[0], lens[3], lens[66] = 0, 400, 1
+    q, k, v, cu, _, ref, mag = _prompt_case(gen, lens, lens, 4, 2, 64, dtype, causal)
+    _held(_prompt(q, k, v, cu, None, max_q=400, causal=causal), ref, mag, dtype, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompt_row_strides(gen, dim):
+    # rows 16 bytes further apart than their heads need, out among them
+    n, heads, kvh = 200, 4, 2
+    q, k, v, cu, _, ref, mag = _prompt_case(gen, [n], [n], heads, kvh, dim, "bf16", True)
+
+    def wide(t, by):
+        w = torch.full((t.shape[0], t.shape[1] * dim + by), math.nan, dtype=t.dtype, device="cuda")
+        w[:, :t.shape[1] * dim] = t.flatten(1)
+        return w[:, :t.shape[1] * dim].unflatten(1, (t.shape[1], dim))
+    q, k, v, out = wide(q, 8), wide(k, 8), wide(v, 24), wide(torch.zeros_like(q), 40)
+    _held(glq.attn_prompt(q, k, v, out, cu), ref, mag, "bf16", True)
+    assert torch.isnan(out.as_strided((n, 40), (out.stride(0), 1), heads * dim)).all()      # between the rows: as it was
+
+
+@pytest.mark.gpu
+def test_prompt_keys_beyond_32_bits(gen):
+    # a sequence whose keys lie past 2^31 elements into k and v
+    n, heads, dim, stride = 100, 2, 64, 32768
+    rows = 2 ** 31 // stride + 200
+    k, v = (torch.empty(rows, stride, dtype=torch.bfloat16, device="cuda")[:, :heads * dim].unflatten(1, (heads, dim))
+            for _ in range(2))
+    q, kd, vd, _, _, ref, mag = _prompt_case(gen, [n], [n], heads, heads, dim, "bf16", True)
+    k[rows - n:], v[rows - n:] = kd, vd
+    cu_q = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    cu_k = torch.tensor([rows - n, rows], dtype=torch.int32, device="cuda")
+    _held(_prompt(q, k, v, cu_q, cu_k), ref, mag, "bf16", True)
+    del k, v
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.gpu
