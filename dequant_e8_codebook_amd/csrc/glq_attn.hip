@@ -892,6 +892,12 @@ __device__ __forceinline__ void keep_unseen_out(float4 &x, const bool (&seen)[CT
 // the scores means dimension 16 i + 4 g + r, row n of value tile (i, c) means
 // dimension 64 i + 4 n + c: both are 16-byte loads. Row x is head head0 + x % group
 // of query x / group. The next keys' loads are in flight while these are worked on.
+// Bound by issue: these products and the VALU do not run at once (0 cycles of both by
+// the counters), a tile's 32 products (heads of 64) take 1024 cycles and the rest, about
+// 110 instructions, 450. So addresses are stepped, masks only where keys end, sums
+// rescaled when a maximum rises by more than 8: 146 us against 153 for eight prompts of
+// 333 on 1000, 16 heads on 2 of 64, and 233 against 299 with 16 on 4 of 128 (8
+// heads of 128, three prompts of 200 on 500: 38.2 against 44.9).
 struct RowJob {
   int head0, group, kvh, row0, rows;   // rows: of the sequence (queries * group)
   int q0, k0, lk, shift;               // first query and key row, keys, keys ahead of the queries
@@ -904,18 +910,26 @@ template <int D> struct KvRows {
   float4 k[D / 16], v[4][D / 64];
 };
 
-template <int D, bool F32>
-__device__ __forceinline__ void load_rows(const PromptArgs &a, const RowJob &w, int lane, int j0, KvRows<D> &x) {
+// a lane's element of its key row and of its four value rows of the keys from j0 on
+// (rows past the last one: that one)
+struct RowsAt { int64_t k, v[4]; };
+__device__ __forceinline__ RowsAt rows_at(const PromptArgs &a, const RowJob &w, int lane, int D, int j0) {
   const int g = lane >> 4, n = lane & 15;
-  const int64_t kr = w.k0 + min(j0 + n, w.lk - 1);
+  RowsAt p;
+  p.k = (w.k0 + min(j0 + n, w.lk - 1)) * a.k_stride + (int64_t)w.kvh * D + 4 * g;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) x.k[i] = load4<F32>(a.k, kr * a.k_stride + (int64_t)w.kvh * D + 16 * i + 4 * g);
+  for (int r = 0; r < 4; ++r) p.v[r] = (w.k0 + min(j0 + 4 * g + r, w.lk - 1)) * a.v_stride + (int64_t)w.kvh * D + 4 * n;
+  return p;
+}
+
+template <int D, bool F32>
+__device__ __forceinline__ void load_rows(const PromptArgs &a, const RowsAt &p, KvRows<D> &x) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int64_t vr = w.k0 + min(j0 + 4 * g + r, w.lk - 1);
+  for (int i = 0; i < D / 16; ++i) x.k[i] = load4<F32>(a.k, p.k + 16 * i);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) x.v[r][i] = load4<F32>(a.v, vr * a.v_stride + (int64_t)w.kvh * D + 64 * i + 4 * n);
-  }
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) x.v[r][i] = load4<F32>(a.v, p.v[r] + 64 * i);
 }
 
 template <int D, bool F32, int CT>
@@ -955,13 +969,16 @@ __device__ __forceinline__ void attend_rows(const PromptArgs &a, const RowJob &w
         s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.k[i].w, q[t][i].w, s[t], 0, 0, 0);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int j = j0 + 4 * g + r;
-        seen[t][r] = j <= last[t] && j < w.lk;
-        s[t][r] = seen[t][r] ? s[t][r] * a.scale2 : -INFINITY;
-      }
+      for (int r = 0; r < 4; ++r) s[t][r] *= a.scale2;
+      if (masked)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = j0 + 4 * g + r;
+          seen[t][r] = j <= last[t] && j < w.lk;
+          s[t][r] = seen[t][r] ? s[t][r] : -INFINITY;
+        }
       const float mt = column_max(fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3])));
-      if (__any(mt > o.m[t])) {
+      if (__any(mt > o.m[t] + 8.0f)) {               // weights of up to 2^8 go with the old base
         const float mn = fmaxf(o.m[t], mt);
         const float alpha = o.m[t] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(o.m[t] - mn);
         o.m[t] = mn;
@@ -998,17 +1015,30 @@ __device__ __forceinline__ void attend_rows(const PromptArgs &a, const RowJob &w
   int j0 = first;
   if constexpr (!F32) {                              // (the bf16 kernel's way out: registers, not haste)
     for (; j0 < end; j0 += step) {
-      load_rows<D, F32>(a, w, lane, j0, x);
+      load_rows<D, F32>(a, rows_at(a, w, lane, D, j0), x);
       work(x, j0);
     }
     return;
   }
   KvRows<D> y;
-  load_rows<D, F32>(a, w, lane, j0, x);
-  for (; j0 + step < end; j0 += step) {
-    load_rows<D, F32>(a, w, lane, j0 + step, y);
+  RowsAt p = rows_at(a, w, lane, D, j0);
+  const int64_t k_step = step * a.k_stride, v_step = step * a.v_stride;
+  auto next = [&](KvRows<D> &to) INLINED {
+    if (j0 + step + 16 > w.lk) {
+      p = rows_at(a, w, lane, D, j0 + step);
+    } else {
+      p.k += k_step;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) p.v[r] += v_step;
+    }
+    load_rows<D, F32>(a, p, to);
     __builtin_amdgcn_sched_barrier(0);               // the loads go out before the work
+  };
+  load_rows<D, F32>(a, p, x);
+  while (j0 + step < end) {
+    next(y);
     work(x, j0);
+    j0 += step;
     x = y;
   }
   work(x, j0);
@@ -1106,7 +1136,7 @@ template <int R> __device__ __forceinline__ Spot find_tile(const PromptArgs &a, 
 // The float32 path. A workgroup takes 16 CT rows (queries times the heads that
 // share a kept head), its waves a quarter of the keys each; they join in LDS.
 template <int D, int CT>
-__global__ void __launch_bounds__(256, D == 64 ? 2 : 1) attn_prompt_f32(PromptArgs a) {
+__global__ void __launch_bounds__(256, (D == 64 || (D == 128 && CT == 1) ? 2 : 1)) attn_prompt_f32(PromptArgs a) {
   extern __shared__ float shm[];                     // [4][16 CT][D] sums, [4][16 CT] maxima, [4][16 CT] totals
   constexpr int R = 16 * CT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
