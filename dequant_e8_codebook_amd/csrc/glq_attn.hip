@@ -1181,7 +1181,7 @@ __global__ void __launch_bounds__(256, (D == 64 || (D == 128 && CT == 1) ? 2 : 1
   }
 }
 
-// The bf16 path. A workgroup takes 128 rows (queries times the heads that share a
+// The bf16 path. A workgroup mostly takes 128 rows (queries times the heads that share a
 // kept head), 32 a wave, against tiles of 64 keys that its waves share in LDS.
 // 32x32x16 products, transposed: S^T = K Q^T leaves lane (h, n) = (lane >> 5, lane
 // & 31) 16 of the scores of row n per 32 keys (keys 8 i + 4 h + r), so a softmax step
@@ -1197,6 +1197,11 @@ __global__ void __launch_bounds__(256, (D == 64 || (D == 128 && CT == 1) ? 2 : 1
 // us against 204, for the coarser workgroups), and the softmax step spread
 // between the products of one wave (207; 8192 tokens, 32 heads, causal 519
 // against 493): the clock falls by as much as the overlap gains (1.8 GHz).
+//
+// Few rows (a chunk of a prompt, or drafted tokens, on a long prefix) take 32 a workgroup
+// instead, all waves the same ones: each goes through its share of the keys alone, with a
+// tile of K and one of V of its own and no barriers, and they join their sums at the end.
+// There the loads bound it: 128 KiB a CU in flight or in use, 82 GB/s a CU out of L2.
 //
 // The tiles go from memory to LDS without passing registers, 16 bytes a lane;
 // chunk c of a row lies at chunk c ^ swizzle(row), which spreads both the 16
@@ -1251,23 +1256,82 @@ __device__ __forceinline__ void tile_barrier() {
 }
 __device__ __forceinline__ void staged_tiles_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// Few rows: waves that each hold a tile of K and one of V in LDS
+template <int D> constexpr int few_waves() { return D == 256 ? 2 : 4; }
+
+// A workgroup's 32 rows from its waves' sums over their keys, 32 / NW rows a wave
 template <int D>
-__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(PromptArgs a) {
-  constexpr int KS = D / 16, DT = D / 32, RB = 2 * D, TB = kKeys * RB, NW = 4, RUNS = TB / 1024 / NW;
-  // LDS: K tiles at 0 and TB, V tiles at 2 TB and 3 TB
+__device__ __forceinline__ void join_few(const PromptArgs &a, RowJob w, int lane, int wave, const f32x16 (&acc)[D / 32],
+                                         float base, float l) {
+  constexpr int NW = few_waves<D>(), RS = D + 4;     // (4 more: rows start in other banks)
+  extern __shared__ float shm[];                     // [NW][32][RS] sums, [NW][32] bases, [NW][32] totals
+  float *sb = shm + NW * 32 * RS, *sl = sb + NW * 32;
+  const int h = lane >> 5, n = lane & 31;
+  __syncthreads();                                   // the tiles' places are free
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+      *reinterpret_cast<float4 *>(shm + (32 * wave + n) * RS + 32 * i + 2 * r + 4 * h) =
+          make_float4(acc[i][r], acc[i][r + 1], acc[i][r + 2], acc[i][r + 3]);
+  if (h == 0) sb[32 * wave + n] = l == 0.0f ? -INFINITY : base, sl[32 * wave + n] = l;
+  __syncthreads();
+  constexpr int OWN = 32 / NW, LANES = 64 / OWN, PARTS = D / (4 * LANES);   // a wave's rows, a row's lanes
+  const int at = OWN * wave + lane / LANES, row = w.row0 + at, d0 = 4 * (lane % LANES);
+  float top = -INFINITY, total = 0.0f, f[NW];
+#pragma unroll
+  for (int x = 0; x < NW; ++x) top = fmaxf(top, sb[32 * x + at]);
+#pragma unroll
+  for (int x = 0; x < NW; ++x) {
+    f[x] = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sb[32 * x + at] - top);
+    total += f[x] * sl[32 * x + at];
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  bool bad = false;
+  float4 v[PARTS];
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    v[i] = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int x = 0; x < NW; ++x) {
+      const float4 u = *reinterpret_cast<const float4 *>(shm + (32 * x + at) * RS + 4 * LANES * i + d0);
+      v[i].x += f[x] * u.x, v[i].y += f[x] * u.y, v[i].z += f[x] * u.z, v[i].w += f[x] * u.w;
+    }
+    v[i].x *= inv, v[i].y *= inv, v[i].z *= inv, v[i].w *= inv;
+    bad |= !(fabsf(v[i].x) < INFINITY && fabsf(v[i].y) < INFINITY && fabsf(v[i].z) < INFINITY &&
+             fabsf(v[i].w) < INFINITY);
+  }
+  w.row0 += OWN * wave;
+  w.rows = min(w.rows, w.row0 + OWN);
+  if (w.row0 >= w.rows) return;
+  if (__any(bad)) {                                  // as in the kernel below, for the wave's rows
+    rows_alone<D>(a, w, lane);
+  } else if (row < w.rows) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) store_row<D, false>(a, w, row, 4 * LANES * i + d0, v[i]);
+  }
+}
+
+template <int D, bool FEW>
+__global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 256 ? 1 : 2)
+    attn_prompt_bf16(PromptArgs a) {
+  constexpr int KS = D / 16, DT = D / 32, RB = 2 * D, TB = kKeys * RB, NW = FEW ? few_waves<D>() : 4;
+  constexpr int RUNS = TB / 1024 / (FEW ? 1 : NW);
+  constexpr int R = FEW ? 32 : 32 * NW;              // rows of a workgroup
+  // LDS: K tiles at 0 and TB, V tiles at 2 TB and 3 TB; FEW: a wave's K at 2 TB wave, its V TB further
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, n = lane & 31;
   const int kvh = blockIdx.x % a.kv_heads, group = a.q_heads / a.kv_heads;
-  const Spot spot = find_tile<32 * NW>(a, lane, blockIdx.x / a.kv_heads);
+  const Spot spot = find_tile<R>(a, lane, blockIdx.x / a.kv_heads);
   if (spot.tile < 0) return;
   const Span sp = spot.span;
-  const int row_wg = 32 * NW * spot.tile, rows = (int)min((int64_t)sp.lq, a.max_q) * group;
-  const int row0 = row_wg + 32 * wave, row = min(row0 + n, rows - 1), query = row / group;
+  const int row_wg = R * spot.tile, rows = (int)min((int64_t)sp.lq, a.max_q) * group;
+  const int row0 = row_wg + (FEW ? 0 : 32 * wave), row = min(row0 + n, rows - 1), query = row / group;
   const int shift = sp.lk - sp.lq;
   const int last = a.causal ? query + shift : sp.lk - 1;        // this lane's last key
   // keys up to first_wave are seen by all rows of the wave
   const int first_wave = a.causal ? row0 / group + shift : sp.lk - 1;
-  const int end = (a.causal ? min(row_wg + 32 * NW, rows) - 1 : 0) / group + (a.causal ? shift : sp.lk - 1) + 1;
+  const int end = (a.causal ? min(row_wg + R, rows) - 1 : 0) / group + (a.causal ? shift : sp.lk - 1) + 1;
   const int tiles = end > 0 ? (end + kKeys - 1) / kKeys : 0;
 
   bf16x8 q[KS];
@@ -1287,7 +1351,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(Prompt
   int koff[RUNS], voff[RUNS];
 #pragma unroll
   for (int i = 0; i < RUNS; ++i) {
-    const int chunk = 64 * (RUNS * wave + i) + lane, r = chunk / (RB / 16), c = chunk % (RB / 16);
+    const int chunk = 64 * ((FEW ? 0 : RUNS * wave) + i) + lane, r = chunk / (RB / 16), c = chunk % (RB / 16);
     const int from = (c ^ swizzle<D>(r)) * 16;
     koff[i] = r * (int)(2 * a.k_stride) + from;
     voff[i] = r * (int)(2 * a.v_stride) + from;
@@ -1296,11 +1360,12 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(Prompt
   const uint8_t *vp = reinterpret_cast<const uint8_t *>(a.v) + 2 * ((int64_t)sp.k0 * a.v_stride + (int64_t)kvh * D);
   const int k_step = (int)(2 * a.k_stride), v_step = (int)(2 * a.v_stride);
   auto stage_k = [&](int t) INLINED {
-    stage_tile<RUNS>(kp + (int64_t)kKeys * t * k_step, k_step, min(kKeys, sp.lk - kKeys * t), (t & 1) * TB, wave, koff);
+    stage_tile<RUNS>(kp + (int64_t)kKeys * t * k_step, k_step, min(kKeys, sp.lk - kKeys * t),
+                     FEW ? 2 * TB * wave : (t & 1) * TB, FEW ? 0 : wave, koff);
   };
   auto stage_v = [&](int t) INLINED {
-    stage_tile<RUNS>(vp + (int64_t)kKeys * t * v_step, v_step, min(kKeys, sp.lk - kKeys * t), (2 + (t & 1)) * TB, wave,
-                     voff);
+    stage_tile<RUNS>(vp + (int64_t)kKeys * t * v_step, v_step, min(kKeys, sp.lk - kKeys * t),
+                     FEW ? 2 * TB * wave + TB : (2 + (t & 1)) * TB, FEW ? 0 : wave, voff);
   };
 
   // LDS addresses of the reads: of K's k-steps and of V's dimension tiles (keys 4 h
@@ -1308,13 +1373,13 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(Prompt
   const int al = lane & 15, gg = (lane >> 4) & 1, vrow = 4 * h + (al >> 2);
   uint32_t k_at[KS], v_at[DT][2];
 #pragma unroll
-  for (int i = 0; i < KS; ++i) k_at[i] = n * RB + (((2 * i + h) ^ swizzle<D>(n)) << 4);
+  for (int i = 0; i < KS; ++i) k_at[i] = (FEW ? 2 * TB * wave : 0) + n * RB + (((2 * i + h) ^ swizzle<D>(n)) << 4);
 #pragma unroll
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = vrow + 8 * e;
-      v_at[i][e] = 2 * TB + r * RB + (((4 * i + 2 * gg + ((al & 3) >> 1)) ^ swizzle<D>(r)) << 4) + 8 * (al & 1);
+      v_at[i][e] = (FEW ? 2 * TB * wave + TB : 2 * TB) + r * RB + (((4 * i + 2 * gg + ((al & 3) >> 1)) ^ swizzle<D>(r)) << 4) + 8 * (al & 1);
     }
   typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -1427,6 +1492,37 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attn_prompt_bf16(Prompt
     if (t + 1 < tiles) stage_k(t + 1);
     if (t < tiles) stage_v(t);
   };
+  if constexpr (FEW) {
+    // every wave for itself, over every NW-th tile: the next K is asked for where the last
+    // one's products end, and so is the next V
+    auto landed = [&](bool more) INLINED {           // all, or all but the tile asked for last
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(RUNS) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (wave < tiles) {
+      stage_k(wave);
+      stage_v(wave);
+      landed(true);
+      products(mid_t(), all_t());
+      if (wave + NW < tiles) stage_k(wave + NW);
+      for (int t = wave;; t += NW) {
+        const bool more = t + NW < tiles;
+        softmax(t);
+        landed(more);
+        products(first_t(), mid_t());
+        if (!more) break;
+        stage_v(t + NW);
+        landed(true);
+        products(mid_t(), all_t());
+        if (t + 2 * NW < tiles) stage_k(t + 2 * NW);
+      }
+    }
+    join_few<D>(a, {kvh * group, group, kvh, row0, rows, sp.q0, sp.k0, sp.lk, shift}, lane, wave, acc, base,
+                l + across32(l));
+    return;
+  }
   if (tiles > 0) {
     stage_k(0);
     ask(0);
@@ -1607,10 +1703,10 @@ int launch_decode_dim(const DecodeArgs &a, int d, glq_dtype dt, int64_t groups, 
 }
 
 template <auto Kernel>
-int launch_rows(const PromptArgs &a, int64_t groups, size_t shm, hipStream_t st, const char *name) {
+int launch_rows(const PromptArgs &a, int64_t groups, int threads, size_t shm, hipStream_t st, const char *name) {
   const int rc = allow_lds<Kernel>(shm);
   if (rc) return rc;
-  hipLaunchKernelGGL(Kernel, dim3((unsigned)groups), dim3(256), shm, st, a);
+  hipLaunchKernelGGL(Kernel, dim3((unsigned)groups), dim3((unsigned)threads), shm, st, a);
   return hip_status(hipGetLastError(), name);
 }
 
@@ -1624,15 +1720,27 @@ int64_t prompt_groups(const PromptArgs &a, int R) {
 
 template <int D>
 int launch_prompt(const PromptArgs &a, bool f32, hipStream_t st) {
-  if (!f32)
-    return launch_rows<attn_prompt_bf16<D>>(a, prompt_groups(a, 128), 4 * kKeys * 2 * D, st, "attn_prompt_bf16");
+  if (!f32) {
+    // Few rows, with the keys over the waves, where the card holds all workgroups of 32
+    // rows at once (by LDS: one a CU, two with heads of 64) and sequences have more than a
+    // tile of keys on average. Us with workgroups of 128 rows and of 32, 32 heads on 8
+    // of 128, causal: 64 tokens on 2000 42.0 and 22.5, on 30000 493 and 192, on 32
+    // 10.0 and 8.8; four times 64 on 448 16.7 and 11.9, seven times (448 workgroups) 17.7
+    // and 22.3; 17 tokens alone 8.0 and 9.7 (one wave works). 16 heads on 2 of 64, 64 on
+    // 2000: 30.1 and 14.9; 8 on 1 of 256: 79.8 and 53.6.
+    constexpr int lds = 4 * kKeys * 2 * D, few_lds = few_waves<D>() * lds / 2;
+    const int64_t few = prompt_groups(a, 32);
+    if (few <= (D == 64 ? 2 : 1) * kCus && a.total_k > kKeys * a.batch)
+      return launch_rows<attn_prompt_bf16<D, true>>(a, few, 64 * few_waves<D>(), few_lds, st, "attn_prompt_bf16");
+    return launch_rows<attn_prompt_bf16<D, false>>(a, prompt_groups(a, 128), 256, lds, st, "attn_prompt_bf16");
+  }
   // 32 rows a workgroup where that leaves a few for every CU, 16 otherwise
   // (heads of 256: always, two tiles' sums and queries would not fit the registers)
   const int64_t groups = prompt_groups(a, 32);
   constexpr size_t shm = 4 * 16 * (D + 2) * sizeof(float);
   if constexpr (D < 256)
-    if (groups >= 4 * kCus) return launch_rows<attn_prompt_f32<D, 2>>(a, groups, 2 * shm, st, "attn_prompt_f32");
-  return launch_rows<attn_prompt_f32<D, 1>>(a, prompt_groups(a, 16), shm, st, "attn_prompt_f32");
+    if (groups >= 4 * kCus) return launch_rows<attn_prompt_f32<D, 2>>(a, groups, 256, 2 * shm, st, "attn_prompt_f32");
+  return launch_rows<attn_prompt_f32<D, 1>>(a, prompt_groups(a, 16), 256, shm, st, "attn_prompt_f32");
 }
 
 }  // namespace

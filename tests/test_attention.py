@@ -421,6 +421,37 @@ def test_prompt_long(gen, dtype, dim, causal):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_few_rows_on_many_keys(gen, dim, causal):
+    # rows enough for a part of the card only: keys up to several tiles of each wave,
+    # tiles that only some waves have, sequences without keys or queries
+    lens_q, lens_k = [3, 1, 40, 0, 5, 70], [700, 64, 1030, 300, 0, 65]
+    q, k, v, cu_q, cu_k, ref, mag = _prompt_case(gen, lens_q, lens_k, 6, 2, dim, "bf16", causal)
+    out = _prompt(q, k, v, cu_q, cu_k, max_q=70, causal=causal)
+    _held(out, ref, mag, "bf16", True)
+    assert torch.equal(out, _prompt(q, k, v, cu_q, cu_k, max_q=70, causal=causal))
+    if causal:                                       # keys that only the last of 40 queries sees
+        at = 64 + 700 + 1029
+        k[at, 1, 0], v[at, 1, 7], v[at, 1, dim - 2] = 0.5, math.nan, math.inf
+        got = _prompt(q, k, v, cu_q, cu_k, max_q=70, causal=causal)
+        assert torch.isnan(got[43, 3:, 7]).all() and not torch.isfinite(got[43, 3:, dim - 2]).any()
+        got[43], out[43] = 0, 0
+        assert torch.isfinite(got).all()
+        _held(got[:43], ref[:43], mag[:43], "bf16", True)
+        assert torch.equal(got[44:], out[44:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_rows_for_the_whole_card(gen, dim, causal):
+    lens_q, lens_k = [400, 90, 33, 301], [430, 90, 600, 301]
+    q, k, v, cu_q, cu_k, ref, mag = _prompt_case(gen, lens_q, lens_k, 24, 3, dim, "bf16", causal)
+    _held(_prompt(q, k, v, cu_q, cu_k, max_q=400, causal=causal), ref, mag, "bf16", True)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_prompt_unseen_values_do_not_reach(gen, dtype, dim):
