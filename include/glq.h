@@ -397,8 +397,9 @@ typedef struct {
  *               v_stride elements apart (>= kv_heads * head_dim; pointers and
  *               strides multiples of 16 bytes)
  *   slots       device int32 [tokens]; a slot outside the cache (negative, or
- *               >= num_pages * page_size) drops its token. Two tokens with one
- *               slot leave it with either's contents.
+ *               >= num_pages * page_size) drops its token. Two tokens of a call
+ *               with one slot leave that slot undefined (the rest is as it
+ *               should be).
  * tokens == 0 is a successful no-op; GLQ_ERR_UNSUPPORTED for tokens * kv_heads *
  * head_dim >= 2^34. GLQ_KV_BF16 rounds to nearest even.
  */
