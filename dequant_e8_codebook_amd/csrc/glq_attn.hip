@@ -1331,6 +1331,11 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   constexpr int KS = D / 16, DT = D / 32, RB = 2 * D, TB = kKeys * RB, NW = FEW ? few_waves<D>() : 4;
   constexpr int RUNS = TB / 1024 / (FEW ? 1 : NW);
   constexpr int R = FEW ? 32 : 32 * NW;              // rows of a workgroup
+  // Two steps a turn of the loop, each with its tiles' places in the reads' offsets, or
+  // one, and the addresses change: 16 VALU instructions more (prompts of 8192, 32 heads
+  // on 8 of 128: 517 us, 510 with two), but two steps of heads of 256 spill registers
+  // (4096, 16 on 2: 208 us, 179 with one).
+  constexpr bool TWO = !FEW && D < 256;
   // LDS: K tiles at 0 and TB, V tiles at 2 TB and 3 TB; FEW: a wave's K at 2 TB wave, its V TB further
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, n = lane & 31;
@@ -1382,7 +1387,7 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   };
 
   // LDS addresses of the reads: of K's k-steps and of V's dimension tiles (keys 4 h
-  // on and 8 further); they change between the two tiles' places by ^ TB
+  // on and 8 further), in the first of the two places
   const int al = lane & 15, gg = (lane >> 4) & 1, vrow = 4 * h + (al >> 2);
   uint32_t k_at[KS], v_at[DT][2];
 #pragma unroll
@@ -1411,21 +1416,23 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   // hand: left to itself the compiler reads late and a product waits for every
   // operand, or reads all at once.
   constexpr int NV = 4 * DT, NS = 2 * KS, AHEAD = 6;
-  auto operand = [&](int j) INLINED {
+  auto operand = [&](int j, int kv, int kk) INLINED {
     if (j >= NV) {
       const int i = (j - NV) >> 1, u = j & 1;
-      return *reinterpret_cast<lds_bf16x8 *>((uintptr_t)(k_at[i] + 32 * RB * u));
+      return *reinterpret_cast<lds_bf16x8 *>((uintptr_t)(k_at[i] + 32 * RB * u + TB * kk));
     }
-    const int w = j / DT, i = j % DT;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(v_at[i][0] + 16 * RB * w));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(v_at[i][1] + 16 * RB * w));
+    const int w = j / DT, i = j % DT, at = 16 * RB * w + TB * kv;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(v_at[i][0] + at));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(v_at[i][1] + at));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  auto products = [&](auto from, auto to) INLINED {
-    constexpr int F = decltype(from)::value, T = decltype(to)::value;
+  // the V tile is in place VP, the K tile in the other (!TWO: where the addresses say)
+  auto products = [&](auto from, auto to, auto vp) INLINED {
+    constexpr int F = decltype(from)::value, T = decltype(to)::value, VP = decltype(vp)::value;
+    constexpr int KP = TWO ? 1 - VP : 0;
     bf16x8 ring[AHEAD];
 #pragma unroll
-    for (int j = F; j < F + AHEAD; ++j) ring[(j - F) % AHEAD] = operand(j);
+    for (int j = F; j < F + AHEAD; ++j) ring[(j - F) % AHEAD] = operand(j, VP, KP);
     __builtin_amdgcn_sched_barrier(0);
 #pragma clang loop unroll(full)
     for (int j = F; j < T; ++j) {
@@ -1439,18 +1446,21 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
         for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
         s[u] = mfma32(x, q[i], i == 0 ? zero : s[u]);
       }
-      if (j + AHEAD < T) ring[(j - F) % AHEAD] = operand(j + AHEAD);
+      if (j + AHEAD < T) ring[(j - F) % AHEAD] = operand(j + AHEAD, VP, KP);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto next_tiles = [&](bool k, bool v) INLINED {            // the reads go on in the other tile's place
+  auto next_tiles = [&](bool v) INLINED {            // !TWO: the reads go on in the other place
+    if constexpr (TWO) return;
 #pragma unroll
-    for (int i = 0; i < KS; ++i) k_at[i] ^= k ? TB : 0;
+    for (int i = 0; i < KS; ++i) k_at[i] ^= TB;
 #pragma unroll
     for (int i = 0; i < DT; ++i) v_at[i][0] ^= v ? TB : 0, v_at[i][1] ^= v ? TB : 0;
   };
   typedef std::integral_constant<int, 0> first_t;
   typedef std::integral_constant<int, NV> mid_t;
+  typedef std::integral_constant<int, 0> place0_t;
+  typedef std::integral_constant<int, 1> place1_t;
   typedef std::integral_constant<int, NV + NS> all_t;
   auto softmax = [&](int t) INLINED {
     const int j0 = kKeys * t;
@@ -1518,17 +1528,17 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
       stage_k(wave);
       stage_v(wave);
       landed(true);
-      products(mid_t(), all_t());
+      products(mid_t(), all_t(), place0_t());
       if (wave + NW < tiles) stage_k(wave + NW);
       for (int t = wave;; t += NW) {
         const bool more = t + NW < tiles;
         softmax(t);
         landed(more);
-        products(first_t(), mid_t());
+        products(first_t(), mid_t(), place0_t());
         if (!more) break;
         stage_v(t + NW);
         landed(true);
-        products(mid_t(), all_t());
+        products(mid_t(), all_t(), place0_t());
         if (t + 2 * NW < tiles) stage_k(t + 2 * NW);
       }
     }
@@ -1543,21 +1553,29 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
     if (tiles > 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * RUNS) : "memory");
     else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(RUNS) : "memory");
     tile_barrier();
-    products(mid_t(), all_t());
-    next_tiles(true, false);
-    for (int t = 0; t + 1 < tiles; ++t) {
+    products(mid_t(), all_t(), std::integral_constant<int, TWO>());   // (K in place 0)
+    next_tiles(false);
+    auto step = [&](int t, auto vp) INLINED {
       softmax(t);
       staged_tiles_landed();
       tile_barrier();
       ask(t + 1);
       __builtin_amdgcn_sched_barrier(0);
-      products(first_t(), all_t());
-      next_tiles(true, true);
-    }
-    softmax(tiles - 1);
+      products(first_t(), all_t(), vp);
+      next_tiles(true);
+    };
+    int t = 0;
+    if constexpr (TWO)
+      for (; t + 2 < tiles; t += 2) {
+        step(t, place0_t());
+        step(t + 1, place1_t());
+      }
+    for (; t + 1 < tiles; ++t) step(t, place0_t());  // (TWO: the last one, if their number is even)
+    softmax(t);
     staged_tiles_landed();
     tile_barrier();
-    products(first_t(), mid_t());
+    if (TWO && (t & 1)) products(first_t(), mid_t(), place1_t());
+    else products(first_t(), mid_t(), place0_t());
   }
   if (row0 >= rows) return;
   l += across32(l);
