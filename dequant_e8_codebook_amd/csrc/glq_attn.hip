@@ -1344,7 +1344,20 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   if (spot.tile < 0) return;
   const Span sp = spot.span;
   const int row_wg = R * spot.tile, rows = (int)min((int64_t)sp.lq, a.max_q) * group;
-  const int row0 = row_wg + (FEW ? 0 : 32 * wave), row = min(row0 + n, rows - 1), query = row / group;
+  const int row0 = row_wg + (FEW ? 0 : 32 * wave);
+  // the query of a row and its place in the operand q or out; rows past the last one: that
+  // one's (x + 1/2 over a group of up to 2^16, x below that and 128: the float32 quotient
+  // is never off by as much as the half)
+  const int query_wg = row_wg / group, rem = row_wg - query_wg * group;
+  const float per_group = __builtin_amdgcn_rcpf((float)group);
+  auto query_of = [&](int row) INLINED {
+    return query_wg + (int)(((float)(min(row, rows - 1) - row_wg + rem) + 0.5f) * per_group);
+  };
+  auto element_of = [&](int row, int64_t stride) INLINED {
+    const int query = query_of(row);
+    return (int64_t)(sp.q0 + query) * stride + (int64_t)(kvh * group + min(row, rows - 1) - query * group) * D;
+  };
+  const int query = query_of(row0 + n);
   const int shift = sp.lk - sp.lq;
   const int last = a.causal ? query + shift : sp.lk - 1;        // this lane's last key
   // keys up to first_wave are seen by all rows of the wave
@@ -1352,18 +1365,6 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   const int end = (a.causal ? min(row_wg + R, rows) - 1 : 0) / group + (a.causal ? shift : sp.lk - 1) + 1;
   const int tiles = end > 0 ? (end + kKeys - 1) / kKeys : 0;
 
-  bf16x8 q[KS];
-  {
-    const uint16_t *qp = reinterpret_cast<const uint16_t *>(a.q) + (int64_t)(sp.q0 + query) * a.q_stride +
-                         (int64_t)(kvh * group + row - query * group) * D + 8 * h;
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      uint4 u = *reinterpret_cast<const uint4 *>(qp + 16 * i);
-      u.x = (u.x & a.q_and) ^ a.q_xor, u.y = (u.y & a.q_and) ^ a.q_xor;
-      u.z = (u.z & a.q_and) ^ a.q_xor, u.w = (u.w & a.q_and) ^ a.q_xor;
-      q[i] = __builtin_bit_cast(bf16x8, u);
-    }
-  }
   // staging: lane i of run r of a wave writes LDS chunk 64 r + i of the wave's
   // part; the chunk of the row that belongs there is fetched
   int koff[RUNS], voff[RUNS];
@@ -1402,6 +1403,39 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+  // A wave's 32 queries come by way of the V tiles' places, rows in whole lines (straight into
+  // registers, an instruction would fetch 32 bytes of each of 32 rows); sums leave likewise by
+  // way of the K tiles'.
+  constexpr int ROW_RUNS = 32 * RB / 1024;
+  const uint32_t q_place = FEW ? 2 * TB * wave + TB : 2 * TB + 32 * RB * wave, out_place = 32 * RB * wave;
+  auto stage_q = [&]() INLINED {
+#pragma unroll
+    for (int i = 0; i < ROW_RUNS; ++i) {
+      const int chunk = 64 * i + lane, r = chunk / (RB / 16), c = chunk % (RB / 16);
+      const uint16_t *from = reinterpret_cast<const uint16_t *>(a.q) + element_of(row0 + r, a.q_stride) +
+                             8 * (c ^ swizzle<D>(r));
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                   :
+                   : "s"(__builtin_amdgcn_readfirstlane((int)(q_place + 1024 * i))), "v"(from)
+                   : "memory");
+    }
+  };
+  bf16x8 q[KS];
+  auto read_q = [&]() INLINED {
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      const uint32_t at = q_place + n * RB + (((2 * i + h) ^ swizzle<D>(n)) << 4);
+      uint4 u = __builtin_bit_cast(uint4, *reinterpret_cast<lds_bf16x8 *>((uintptr_t)at));
+      u.x = (u.x & a.q_and) ^ a.q_xor, u.y = (u.y & a.q_and) ^ a.q_xor;
+      u.z = (u.z & a.q_and) ^ a.q_xor, u.w = (u.w & a.q_and) ^ a.q_xor;
+      q[i] = __builtin_bit_cast(bf16x8, u);
+    }
+    // in registers before the place is another tile's
+#pragma unroll
+    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i]));
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
 
   f32x16 acc[DT], s[2];
   bf16x8 p[4];
@@ -1526,8 +1560,10 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
     };
     if (wave < tiles) {
       stage_k(wave);
+      stage_q();
+      landed(false);
+      read_q();
       stage_v(wave);
-      landed(true);
       products(mid_t(), all_t(), place0_t());
       if (wave + NW < tiles) stage_k(wave + NW);
       for (int t = wave;; t += NW) {
@@ -1548,11 +1584,12 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   }
   if (tiles > 0) {
     stage_k(0);
-    ask(0);
-    // K(0) is there once no more than what ask(0) brought is on its way
-    if (tiles > 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * RUNS) : "memory");
-    else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(RUNS) : "memory");
+    stage_q();
+    staged_tiles_landed();
+    read_q();
     tile_barrier();
+    ask(0);
+    __builtin_amdgcn_sched_barrier(0);
     products(mid_t(), all_t(), std::integral_constant<int, TWO>());   // (K in place 0)
     next_tiles(false);
     auto step = [&](int t, auto vp) INLINED {
@@ -1595,13 +1632,23 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
     for (; w.row0 < min(row0 + 32, rows); w.row0 += 16) rows_alone<D>(a, w, lane);
     return;
   }
-  if (row0 + n >= rows) return;
+  // (the K tiles were last read before the last barrier)
+  typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+  typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
 #pragma unroll
   for (int i = 0; i < DT; ++i)
 #pragma unroll
-    for (int r = 0; r < 16; r += 4)
-      store_row<D, false>(a, w, row, 32 * i + 2 * r + 4 * h,
-                          make_float4(acc[i][r], acc[i][r + 1], acc[i][r + 2], acc[i][r + 3]));
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<lds_u32x2 *>((uintptr_t)(out_place + n * RB + (((4 * i + r) ^ swizzle<D>(n)) << 4) + 8 * h)) =
+          (u32x2){pack_bf16(acc[i][4 * r], acc[i][4 * r + 1]), pack_bf16(acc[i][4 * r + 2], acc[i][4 * r + 3])};
+#pragma unroll
+  for (int i = 0; i < ROW_RUNS; ++i) {
+    const int chunk = 64 * i + lane, r = chunk / (RB / 16), c = chunk % (RB / 16);
+    const u32x4 u = *reinterpret_cast<lds_u32x4 *>((uintptr_t)(out_place + r * RB + ((c ^ swizzle<D>(r)) << 4)));
+    if (row0 + r < rows)
+      *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(a.out) + element_of(row0 + r, a.out_stride) + 8 * c) = u;
+  }
 }
 
 // ------------------------------------------------------------ argument checks
