@@ -1345,19 +1345,19 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   const Span sp = spot.span;
   const int row_wg = R * spot.tile, rows = (int)min((int64_t)sp.lq, a.max_q) * group;
   const int row0 = row_wg + (FEW ? 0 : 32 * wave);
-  // the query of a row and its place in the operand q or out; rows past the last one: that
-  // one's (x + 1/2 over a group of up to 2^16, x below that and 128: the float32 quotient
-  // is never off by as much as the half)
+  // A row's query and its place in q or out, from the tile's first query on; rows past the
+  // last one: that one's. (x is the row and 1/2, over a group of up to 2^16 and below that
+  // and 128: the float32 quotient is never off by as much as the half.)
   const int query_wg = row_wg / group, rem = row_wg - query_wg * group;
-  const float per_group = __builtin_amdgcn_rcpf((float)group);
-  auto query_of = [&](int row) INLINED {
-    return query_wg + (int)(((float)(min(row, rows - 1) - row_wg + rem) + 0.5f) * per_group);
+  const float per_group = __builtin_amdgcn_rcpf((float)group), last_x = (float)(rows - 1 - row_wg + rem) + 0.5f;
+  const float x_wave = (float)(row0 - row_wg + rem) + 0.5f;
+  auto element_of = [&](float x, int64_t stride) INLINED {
+    x = fminf(x, last_x);
+    const int query = (int)(x * per_group);
+    return query * stride + ((int)x - query * group) * D;
   };
-  auto element_of = [&](int row, int64_t stride) INLINED {
-    const int query = query_of(row);
-    return (int64_t)(sp.q0 + query) * stride + (int64_t)(kvh * group + min(row, rows - 1) - query * group) * D;
-  };
-  const int query = query_of(row0 + n);
+  const int64_t q_wg = sp.q0 + query_wg;
+  const int query = query_wg + (int)(fminf(x_wave + (float)n, last_x) * per_group);
   const int shift = sp.lk - sp.lq;
   const int last = a.causal ? query + shift : sp.lk - 1;        // this lane's last key
   // keys up to first_wave are seen by all rows of the wave
@@ -1387,6 +1387,30 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
                      FEW ? 2 * TB * wave + TB : (2 + (t & 1)) * TB, FEW ? 0 : wave, voff);
   };
 
+  // A wave's 32 queries come by way of the V tiles' places, rows in whole lines (straight into
+  // registers, an instruction would fetch 32 bytes of each of 32 rows); sums leave likewise by
+  // way of the K tiles'.
+  constexpr int ROW_RUNS = 32 * RB / 1024;
+  const uint32_t q_place = FEW ? 2 * TB * wave + TB : 2 * TB + 32 * RB * wave, out_place = 32 * RB * wave;
+  auto stage_q = [&]() INLINED {
+#pragma unroll
+    for (int i = 0; i < ROW_RUNS; ++i) {
+      const int chunk = 64 * i + lane, r = chunk / (RB / 16), c = chunk % (RB / 16);
+      const uint16_t *from = reinterpret_cast<const uint16_t *>(a.q) + (q_wg * a.q_stride + (int64_t)kvh * group * D) +
+                             (element_of(x_wave + (float)r, a.q_stride) + 8 * (c ^ swizzle<D>(r)));
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                   :
+                   : "s"(__builtin_amdgcn_readfirstlane((int)(q_place + 1024 * i))), "v"(from)
+                   : "memory");
+    }
+  };
+  const int tile0 = FEW ? wave : 0;
+  if (tile0 < tiles) {
+    stage_k(tile0);
+    stage_q();
+  }
+  __builtin_amdgcn_sched_barrier(0);                 // on their way while the rest is set up
+
   // LDS addresses of the reads: of K's k-steps and of V's dimension tiles (keys 4 h
   // on and 8 further), in the first of the two places
   const int al = lane & 15, gg = (lane >> 4) & 1, vrow = 4 * h + (al >> 2);
@@ -1404,23 +1428,6 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-  // A wave's 32 queries come by way of the V tiles' places, rows in whole lines (straight into
-  // registers, an instruction would fetch 32 bytes of each of 32 rows); sums leave likewise by
-  // way of the K tiles'.
-  constexpr int ROW_RUNS = 32 * RB / 1024;
-  const uint32_t q_place = FEW ? 2 * TB * wave + TB : 2 * TB + 32 * RB * wave, out_place = 32 * RB * wave;
-  auto stage_q = [&]() INLINED {
-#pragma unroll
-    for (int i = 0; i < ROW_RUNS; ++i) {
-      const int chunk = 64 * i + lane, r = chunk / (RB / 16), c = chunk % (RB / 16);
-      const uint16_t *from = reinterpret_cast<const uint16_t *>(a.q) + element_of(row0 + r, a.q_stride) +
-                             8 * (c ^ swizzle<D>(r));
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                   :
-                   : "s"(__builtin_amdgcn_readfirstlane((int)(q_place + 1024 * i))), "v"(from)
-                   : "memory");
-    }
-  };
   bf16x8 q[KS];
   auto read_q = [&]() INLINED {
 #pragma unroll
@@ -1559,8 +1566,6 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
       __builtin_amdgcn_sched_barrier(0);
     };
     if (wave < tiles) {
-      stage_k(wave);
-      stage_q();
       landed(false);
       read_q();
       stage_v(wave);
@@ -1583,8 +1588,6 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
     return;
   }
   if (tiles > 0) {
-    stage_k(0);
-    stage_q();
     staged_tiles_landed();
     read_q();
     tile_barrier();
@@ -1617,18 +1620,19 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   if (row0 >= rows) return;
   l += across32(l);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  bool bad = false;
+  float nans[4] = {0, 0, 0, 0};                      // 0, or NaN for a value that is not finite
 #pragma unroll
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       acc[i][r] *= inv;
-      bad |= !(fabsf(acc[i][r]) < INFINITY);
+      nans[r & 3] = fmaf(acc[i][r], 0.0f, nans[r & 3]);
     }
+  const float nan = (nans[0] + nans[1]) + (nans[2] + nans[3]);
   RowJob w = {kvh * group, group, kvh, row0, rows, sp.q0, sp.k0, sp.lk, shift};
   // a weight of 0 times an infinity or a NaN that the row does not see: such a
   // wave is done over, pair by pair
-  if (__any(bad)) {
+  if (__any(nan != nan)) {
     for (; w.row0 < min(row0 + 32, rows); w.row0 += 16) rows_alone<D>(a, w, lane);
     return;
   }
@@ -1647,7 +1651,8 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
     const int chunk = 64 * i + lane, r = chunk / (RB / 16), c = chunk % (RB / 16);
     const u32x4 u = *reinterpret_cast<lds_u32x4 *>((uintptr_t)(out_place + r * RB + ((c ^ swizzle<D>(r)) << 4)));
     if (row0 + r < rows)
-      *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(a.out) + element_of(row0 + r, a.out_stride) + 8 * c) = u;
+      *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(a.out) + (q_wg * a.out_stride + (int64_t)kvh * group * D) +
+                                 (element_of(x_wave + (float)r, a.out_stride) + 8 * c)) = u;
   }
 }
 
