@@ -1216,6 +1216,10 @@ __global__ void __launch_bounds__(256, (D == 64 || (D == 128 && CT == 1) ? 2 : 1
 // tile of K and one of V of its own and no barriers, and they join their sums at the end.
 // There the loads bound it: 128 KiB a CU in flight or in use, 82 GB/s a CU out of L2.
 //
+// Queries and sums pass LDS on their way too: rows in whole lines (12 packed prompts of up to
+// 2048 tokens, 32 heads on 8: 184 us, 195 with each lane's 16 and 8 bytes straight from
+// and to its row). A workgroup's start and end are still about six tiles' time.
+//
 // The tiles go from memory to LDS without passing registers, 16 bytes a lane;
 // chunk c of a row lies at chunk c ^ swizzle(row), which spreads both the 16
 // rows of a K read and the 4 rows x 64 bytes of a V read over all banks.
