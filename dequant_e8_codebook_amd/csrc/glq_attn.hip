@@ -1809,15 +1809,15 @@ template <int D>
 int launch_prompt(const PromptArgs &a, bool f32, hipStream_t st) {
   if (!f32) {
     // Few rows, with the keys over the waves, where the card holds all workgroups of 32
-    // rows at once (by LDS: one a CU, two with heads of 64) and sequences have more than a
-    // tile of keys on average. Us with workgroups of 128 rows and of 32, 32 heads on 8
-    // of 128, causal: 64 tokens on 2000 42.0 and 22.5, on 30000 493 and 192, on 32
-    // 10.0 and 8.8; four times 64 on 448 16.7 and 11.9, seven times (448 workgroups) 17.7
-    // and 22.3; 17 tokens alone 8.0 and 9.7 (one wave works). 16 heads on 2 of 64, 64 on
-    // 2000: 30.1 and 14.9; 8 on 1 of 256: 79.8 and 53.6.
+    // rows at once (by LDS: one a CU, two with heads of 64) and sequences have more than two
+    // tiles of keys on average. Us with workgroups of 128 rows and of 32, 32 heads on 8
+    // of 128, causal: 64 tokens on 2000 39.3 and 22.5, on 30000 471 and 190, on 192
+    // 10.3 and 9.3, on 64 8.3 and 9.0; four times 64 on 448 14.8 and 11.6, seven times (448
+    // workgroups) 15.8 and 21.3. 16 heads on 2 of 64, 64 on 2000: 28.2 and 15.1; 8 on 1 of
+    // 256: 77.2 and 53.1.
     constexpr int lds = 4 * kKeys * 2 * D, few_lds = few_waves<D>() * lds / 2;
     const int64_t few = prompt_groups(a, 32);
-    if (few <= (D == 64 ? 2 : 1) * kCus && a.total_k > kKeys * a.batch)
+    if (few <= (D == 64 ? 2 : 1) * kCus && a.total_k > 2 * kKeys * a.batch)
       return launch_rows<attn_prompt_bf16<D, true>>(a, few, 64 * few_waves<D>(), few_lds, st, "attn_prompt_bf16");
     return launch_rows<attn_prompt_bf16<D, false>>(a, prompt_groups(a, 128), 256, lds, st, "attn_prompt_bf16");
   }

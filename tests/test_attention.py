@@ -443,6 +443,15 @@ def test_prompt_few_rows_on_many_keys(gen, dim, causal):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("q_heads,kv_heads,lens", [(300, 2, [3, 40, 1]), (131, 1, [130, 7]), (129, 3, [64, 129])])
+def test_prompt_large_groups(gen, dtype, q_heads, kv_heads, lens):
+    # a query's heads over several tiles of rows, tiles that begin within a query
+    q, k, v, cu, _, ref, mag = _prompt_case(gen, lens, lens, q_heads, kv_heads, 64, dtype, True)
+    _held(_prompt(q, k, v, cu, None, max_q=max(lens)), ref, mag, dtype, True)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("causal", [True, False])
 def test_prompt_rows_for_the_whole_card(gen, dim, causal):
