@@ -909,8 +909,8 @@ __device__ __forceinline__ void keep_unseen_out(float4 &x, const bool (&seen)[CT
 // the counters), a tile's 32 products (heads of 64) take 1024 cycles and the rest, about
 // 110 instructions, 450. So addresses are stepped, masks only where keys end, sums
 // rescaled when a maximum rises by more than 8: 146 us against 153 for eight prompts of
-// 333 on 1000, 16 heads on 2 of 64, and 233 against 299 with 16 on 4 of 128 (8
-// heads of 128, three prompts of 200 on 500: 38.2 against 44.9).
+// 333 on 1000, 16 heads on 2 of 64 (in tiles of 32 rows); 8 heads of 128, three prompts of
+// 200 on 500: 38.2 against 44.9.
 struct RowJob {
   int head0, group, kvh, row0, rows;   // rows: of the sequence (queries * group)
   int q0, k0, lk, shift;               // first query and key row, keys, keys ahead of the queries
@@ -1149,7 +1149,7 @@ template <int R> __device__ __forceinline__ Spot find_tile(const PromptArgs &a, 
 // The float32 path. A workgroup takes 16 CT rows (queries times the heads that
 // share a kept head), its waves a quarter of the keys each; they join in LDS.
 template <int D, int CT>
-__global__ void __launch_bounds__(256, (D == 64 || (D == 128 && CT == 1) ? 2 : 1)) attn_prompt_f32(PromptArgs a) {
+__global__ void __launch_bounds__(256, (D < 256 ? 2 : 1)) attn_prompt_f32(PromptArgs a) {
   extern __shared__ float shm[];                     // [4][16 CT][D] sums, [4][16 CT] maxima, [4][16 CT] totals
   constexpr int R = 16 * CT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1821,12 +1821,14 @@ int launch_prompt(const PromptArgs &a, bool f32, hipStream_t st) {
       return launch_rows<attn_prompt_bf16<D, true>>(a, few, 64 * few_waves<D>(), few_lds, st, "attn_prompt_bf16");
     return launch_rows<attn_prompt_bf16<D, false>>(a, prompt_groups(a, 128), 256, lds, st, "attn_prompt_bf16");
   }
-  // 32 rows a workgroup where that leaves a few for every CU, 16 otherwise
-  // (heads of 256: always, two tiles' sums and queries would not fit the registers)
+  // Heads of 64: 32 rows a workgroup where that leaves many for every CU, 16 otherwise: 12
+  // prompts of 400, 32 heads on 32 (4,992 workgroups of 32) 124 us and 138, eight of 333 on
+  // 1000, 16 on 2 (1,332) 148 and 141, 64 on 2000 48.5 and 29.9. Larger heads: two tiles'
+  // sums and queries leave one workgroup a CU (eight of 333 on 1000, 16 on 4 of 128: 233 us and 184)
   const int64_t groups = prompt_groups(a, 32);
   constexpr size_t shm = 4 * 16 * (D + 2) * sizeof(float);
-  if constexpr (D < 256)
-    if (groups >= 4 * kCus) return launch_rows<attn_prompt_f32<D, 2>>(a, groups, 256, 2 * shm, st, "attn_prompt_f32");
+  if constexpr (D == 64)
+    if (groups >= 8 * kCus) return launch_rows<attn_prompt_f32<D, 2>>(a, groups, 256, 2 * shm, st, "attn_prompt_f32");
   return launch_rows<attn_prompt_f32<D, 1>>(a, prompt_groups(a, 16), 256, shm, st, "attn_prompt_f32");
 }
 

@@ -443,6 +443,20 @@ def test_prompt_few_rows_on_many_keys(gen, dim, causal):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_many_float32_rows(gen, causal):
+    lens_q, lens_k = [520, 505, 33], [520, 515, 33]
+    q, k, v, cu_q, cu_k, ref, mag = _prompt_case(gen, lens_q, lens_k, 64, 64, 64, "f32", causal)
+    at = 520 + 514                                   # a value that the last of 505 queries sees alone
+    got = _prompt(q, k, v, cu_q, cu_k, max_q=520, causal=causal)
+    _held(got, ref, mag, "f32", True)
+    if causal:
+        v[at, 5, 9] = math.nan
+        nan = torch.isnan(_prompt(q, k, v, cu_q, cu_k, max_q=520))
+        assert nan[1024, 5, 9] and nan.sum() == 1
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("q_heads,kv_heads,lens", [(300, 2, [3, 40, 1]), (131, 1, [130, 7]), (129, 3, [64, 129])])
 def test_prompt_large_groups(gen, dtype, q_heads, kv_heads, lens):
