@@ -674,9 +674,12 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
       // the running maximum follows only where it is outgrown by 2^8: weights of
       // up to 2^8 lose nothing, and the sums are rarely rescaled
       if (__any(mt > m + 8.0f)) {
+        // nothing summed yet: known by the row's maximum, as l is this lane's tokens only, and acc
+        // all four lanes'
+        const bool none = m == -INFINITY;
         m = fmaxf(m, mt);
         const float now = m == -INFINITY ? 0.0f : m;
-        const float alpha = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(base - now);
+        const float alpha = none ? 0.0f : __builtin_amdgcn_exp2f(base - now);
         base = now;
         l *= alpha;
 #pragma unroll

@@ -725,3 +725,41 @@ def test_attention_block_example(cache, most):
     spec.loader.exec_module(mod)
     for err in mod.run(cache=cache, tokens=4):
         assert err <= most
+
+
+# ------------------------------------------------------ sums beyond one lane's keys
+
+def _leading_key(n, dim, at, later, gen):
+    """Keys and values of one kept head and two queries of opposite tastes: at scale 1
+    query 0 has score 160 on key `at` and 0 elsewhere (230 in base 2: every other
+    weight is 0 in float32), query 1 has 32 on the keys `later` and 0 elsewhere, so
+    its maximum rises where those begin and the sums of both are rescaled there."""
+    k = _normal(gen, n, 1, dim, dtype=torch.bfloat16).float()
+    v = _normal(gen, n, 1, dim, dtype=torch.bfloat16)
+    k[:, 0, :2] = 0
+    k[at, 0, 0] = 10
+    k[later, 0, 1] = 2
+    q = torch.zeros(2, dim)
+    q[0, 0], q[1, 1] = 16, 16
+    return q, k, v.float()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_decode_leading_token_before_a_rise(gen, fmt, dim, dtype):
+    # the leading token in each quarter of a wave's tokens and in both halves of its
+    # tile: lanes that hold only weights of 0 hold other tokens' values all the same
+    n, page = 300, 32
+    for at in (1, 6, 9, 14, 19, 30):
+        q, k, v = _leading_key(n, dim, at, [128, 135, 140, 151, 258], gen)
+        k, v, q = k.cuda(), v.cuda(), q.to(DTYPES[dtype]).cuda()[None]
+        cache = glq.KvCache.empty(10, page, 1, dim, FORMATS[fmt])
+        glq.kv_append(cache, k, v, torch.arange(n, dtype=torch.int32, device="cuda"))
+        table = torch.arange(10, dtype=torch.int32, device="cuda")[None]
+        out, _ = _decode(cache, q, table, torch.tensor([n], dtype=torch.int32, device="cuda"), n, scale=1.0)
+        kk, vv = (_ref_values(x.cpu(), fmt)[:, 0] for x in (k, v))
+        ref, mag = _ref_attend(q[0].cpu(), kk, vv, 1.0, torch.ones(2, n, dtype=torch.bool))
+        assert (ref[0] - vv[at].double()).abs().max() < 1e-60
+        _held(out[0], ref, mag, dtype)
