@@ -1528,9 +1528,12 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
     // the running maximum follows only where it is outgrown by 2^8: weights of
     // up to 2^8 lose nothing, and the sums are rarely rescaled
     if (__any(mt > m + 8.0f)) {
+      // nothing summed yet: known by the row's maximum, as l is this half's keys only, and acc both
+      // halves'
+      const bool none = m == -INFINITY;
       m = fmaxf(m, mt);
       const float now = m == -INFINITY ? 0.0f : m;
-      const float alpha = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(base - now);
+      const float alpha = none ? 0.0f : __builtin_amdgcn_exp2f(base - now);
       base = now;
       l *= alpha;
 #pragma unroll

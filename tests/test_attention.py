@@ -763,3 +763,26 @@ def test_decode_leading_token_before_a_rise(gen, fmt, dim, dtype):
         ref, mag = _ref_attend(q[0].cpu(), kk, vv, 1.0, torch.ones(2, n, dtype=torch.bool))
         assert (ref[0] - vv[at].double()).abs().max() < 1e-60
         _held(out[0], ref, mag, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n", [128, 600])
+def test_prompt_leading_key_before_a_rise(gen, dtype, dim, causal, n):
+    # 128 keys: two tiles that the waves share; 600: a wave's own tiles
+    for at in (1, 6, 34, 61):
+        q, k, v = _leading_key(n, dim, at, list(range(70, n - 1, 64)), gen)
+        # the queries as two tokens of one head, and as two heads of each of two tokens
+        for heads in (1, 2):
+            qq = q[:, None] if heads == 1 else q[None].repeat(2, 1, 1)
+            qq, kk, vv = (x.to(DTYPES[dtype]).cuda() for x in (qq, k, v))
+            cu = [torch.tensor([0, x], dtype=torch.int32, device="cuda") for x in (2, n)]
+            out = _prompt(qq, kk, vv, *cu, causal=causal, scale=1.0)
+            seen = torch.ones(2, n, dtype=torch.bool)
+            if causal:
+                seen[0, n - 1] = False
+            for h in range(heads):
+                ref, mag = _ref_attend(qq[:, h].cpu(), kk[:, 0].cpu(), vv[:, 0].cpu(), 1.0, seen)
+                _held(out[:, h], ref, mag, dtype, True)
