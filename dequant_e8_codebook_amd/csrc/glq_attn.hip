@@ -193,7 +193,9 @@ __device__ __forceinline__ void append_row(const KvIo &io, const KvPart<D> &p, i
       for (int i = 0; i < 8; ++i) w |= (uint32_t)(q[i] + 8) << (4 * i);
       *reinterpret_cast<uint32_t *>(out + 4 * at) = w;
     }
-    if (at == 0) io.scale[which][p.cached] = a / Q;
+    // NaN for an infinity too: with a scale of inf, the codes of 0 would count on a score's sum being
+    // exactly 0 to give NaN, and the 4-bit operands' is 0 up to rounding
+    if (at == 0) io.scale[which][p.cached] = top < 0x7F800000u ? a / Q : NAN;
   }
 }
 

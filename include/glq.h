@@ -372,8 +372,9 @@ int glq_ep_fused_linear(const glq_ep_layer *L, const void *x, glq_dtype x_dt, in
  * Codes: per token and head, a = max |x| over head_dim and Q = 127 (8 bits)
  * or 7 (4 bits); code = x Q / a rounded half to even (the product and the
  * quotient each rounded to float32; for bf16 x the product is exact), 0 for
- * a = 0; scale = a / Q, value = fl32(code * scale). A non-finite x makes its
- * token's head read back as NaN.
+ * a = 0; scale = a / Q, value = fl32(code * scale). A non-finite x gives its
+ * token's head codes of 0 and a scale of NaN: it reads back as NaN, and so does
+ * the attention that sees it.
  * ---------------------------------------------------------------------- */
 typedef enum { GLQ_KV_BF16 = 0, GLQ_KV_INT8 = 1, GLQ_KV_INT4 = 2 } glq_kv_format;
 

@@ -786,3 +786,25 @@ def test_prompt_leading_key_before_a_rise(gen, dtype, dim, causal, n):
             for h in range(heads):
                 ref, mag = _ref_attend(qq[:, h].cpu(), kk[:, 0].cpu(), vv[:, 0].cpu(), 1.0, seen)
                 _held(out[:, h], ref, mag, dtype, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "int4"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_decode_sees_values_that_are_not_finite(gen, fmt, dtype, dim, which, bad):
+    # a token's head that holds an infinity or a NaN reads back as NaN: so does what sees it,
+    # and no other kept head does. Queries of very different sizes: their sums are rounded
+    n, heads, kvh = 40, 16, 2
+    x = {"k": _normal(gen, n, kvh, dim), "v": _normal(gen, n, kvh, dim)}
+    x[which][17, 1, 3] = bad
+    cache = glq.KvCache.empty(3, 16, kvh, dim, FORMATS[fmt])
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    glq.kv_append(cache, x["k"].cuda(), x["v"].cuda(), slots)
+    q = (_normal(gen, 8, heads, dim) * torch.exp(2 * _normal(gen, 8, heads, dim))).to(DTYPES[dtype]).cuda()
+    table = torch.arange(3, dtype=torch.int32, device="cuda")[None].repeat(8, 1)
+    out, _ = _decode(cache, q, table, torch.full((8,), n, dtype=torch.int32, device="cuda"), n)
+    assert torch.isnan(out[:, heads // 2:]).all()
+    assert torch.isfinite(out[:, :heads // 2]).all()
