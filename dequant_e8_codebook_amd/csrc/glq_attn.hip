@@ -451,6 +451,16 @@ __device__ __forceinline__ f32x4 load_shared(__amdgpu_buffer_rsrc_t r, int at) {
   return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, 4 * at, 0, 16));
 }
 
+// The running maxima are taken this much too high (in base 2), so that a row's weights, each
+// at most 2^8 of the largest one's base, add up to no more than 1/2: the sum of weights
+// times values is then no larger than the largest value, and a mean of finite values stays
+// finite. It costs nothing (one multiply-add where a multiplication was) and takes its bits from
+// where weights and values vanish. By the sequence's own number of keys, so that a result does not
+// depend on what else is in the call. `extra`: for operands larger than the values they stand for.
+__device__ __forceinline__ float headroom_of(int keys, int extra = 0) {
+  return (float)(9 + extra + (keys > 1 ? 32 - __builtin_clz((unsigned)(keys - 1)) : 0));
+}
+
 // A part of a row's sums: values, their maximum and total
 struct Sums {
   float o[8], top, total;
@@ -635,6 +645,8 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
     }
     const float s0 = BIASED ? -kBias4 * column_sum(qsum) : 0.0f;
 
+    // (4-bit operands carry a bias of kBias4 on codes of up to 7)
+    const float headroom = headroom_of(at.len, BIASED ? 3 : 0);
     float m = -INFINITY, base = 0.0f, l = 0.0f;
     f32x4 acc[DT];
 #pragma unroll
@@ -672,7 +684,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
       float mt = s[0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) mt = fmaxf(mt, s[j]);
-      mt = column_max(mt) * a.abs_scale2;
+      mt = fmaf(column_max(mt), a.abs_scale2, headroom);
       // the running maximum follows only where it is outgrown by 2^8: weights of
       // up to 2^8 lose nothing, and the sums are rarely rescaled
       if (__any(mt > m + 8.0f)) {
@@ -972,6 +984,7 @@ __device__ __forceinline__ void attend_rows(const PromptArgs &a, const RowJob &w
   const int top = min(w.row0 + 16 * CT, w.rows) - 1;
   const int end = min(w.lk, a.causal ? top / w.group + w.shift + 1 : w.lk);
   if (first >= end) return;
+  const float headroom = headroom_of(w.lk);
   auto work = [&](KvRows<D> &x, int j0) INLINED {
     const bool masked = j0 + 15 > all || j0 + 16 > w.lk;
     f32x4 s[CT];
@@ -995,7 +1008,7 @@ __device__ __forceinline__ void attend_rows(const PromptArgs &a, const RowJob &w
           seen[t][r] = j <= last[t] && j < w.lk;
           s[t][r] = seen[t][r] ? s[t][r] : -INFINITY;
         }
-      const float mt = column_max(fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3])));
+      const float mt = column_max(fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3]))) + headroom;
       if (__any(mt > o.m[t] + 8.0f)) {               // weights of up to 2^8 go with the old base
         const float mn = fmaxf(o.m[t], mt);
         const float alpha = o.m[t] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(o.m[t] - mn);
@@ -1459,6 +1472,7 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
+  const float headroom = headroom_of(sp.lk);
   float m = -INFINITY, base = 0.0f, l = 0.0f;
 
   // Products FROM .. TO - 1 of a tile's NV + NS: O^T += V^T P^T of a tile, then S^T =
@@ -1526,7 +1540,7 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[u][r]);
-    mt = fmaxf(mt, across32(mt)) * a.abs_scale2;
+    mt = fmaf(fmaxf(mt, across32(mt)), a.abs_scale2, headroom);
     // the running maximum follows only where it is outgrown by 2^8: weights of
     // up to 2^8 lose nothing, and the sums are rarely rescaled
     if (__any(mt > m + 8.0f)) {

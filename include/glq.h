@@ -444,6 +444,10 @@ size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q
  *               kernels complete; concurrent calls need workspaces of their own,
  *               and other entry points must not write there in between.
  * What lies in the cache past a sequence's length is never used, NaN among it.
+ * Values may be of any finite size: the sums of weights are kept below 1, so that no
+ * sum overflows. Where all values are below about 1e-27 in a quantised cache, or 1e-32,
+ * they come out with fewer bits. Scores are float32: one that overflows to +inf gives
+ * NaN, one of -inf no weight, and a row of -inf alone zeros.
  * Results do not depend on the order in which workgroups finish. q_heads must be
  * a multiple of kv_heads. batch == 0 is a successful no-op; GLQ_ERR_UNSUPPORTED
  * for launches past 2^31 workgroups.
@@ -480,7 +484,8 @@ typedef struct {
  * prefix). A query that sees no key gets a row of zeros; rows outside every
  * sequence are not written. Offsets are read as the nearest value within 0 ..
  * total. A key that a query does not see never reaches it, NaN and infinities
- * in it included; an infinite value that it sees may give NaN.
+ * in it included; an infinite value that it sees may give NaN. Finite values and
+ * scores that overflow: as in glq_attn_decode.
  *   dt = GLQ_BF16: bf16 matrix-core path, weights rounded to bf16, float32 sums
  *   dt = GLQ_F32:  float32 products and sums
  * batch == 0, total_q == 0 or max_q == 0 is a successful no-op. out must not

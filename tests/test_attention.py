@@ -808,3 +808,58 @@ def test_decode_sees_values_that_are_not_finite(gen, fmt, dtype, dim, which, bad
     out, _ = _decode(cache, q, table, torch.full((8,), n, dtype=torch.int32, device="cuda"), n)
     assert torch.isnan(out[:, heads // 2:]).all()
     assert torch.isfinite(out[:, :heads // 2]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,dtype", [("bf16", "bf16"), ("bf16", "f32"), ("int8", "bf16"), ("int8", "f32"),
+                                       ("int4", "bf16"), ("int4", "f32")])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[300, 7], [4000, 2500]])
+def test_decode_values_near_the_largest(gen, fmt, dtype, dim, lens):
+    # finite values of up to 3e38 (the largest bf16 is 3.39e38): their weighted mean is
+    # finite, whatever the number of tokens
+    heads, page = 2, 32
+    pages = [-(-n // page) for n in lens]
+    table = torch.zeros(2, max(pages), dtype=torch.int32)
+    table[0, :pages[0]] = torch.arange(pages[0])
+    table[1, :pages[1]] = pages[0] + torch.arange(pages[1])
+    cache = glq.KvCache.empty(sum(pages), page, 1, dim, FORMATS[fmt])
+    q = _normal(gen, 2, heads, dim, dtype=DTYPES[dtype]) * 1.5
+    out = None
+    kv = []
+    for b, n in enumerate(lens):
+        k = _normal(gen, n, 1, dim, dtype=torch.bfloat16)
+        v = (torch.rand(n, 1, dim, generator=gen) * 1e38 + 2e38).to(torch.bfloat16)
+        v[..., ::2] *= -1
+        slots = table[b].long()[torch.arange(n) // page] * page + torch.arange(n) % page
+        glq.kv_append(cache, k.cuda(), v.cuda(), slots.to(torch.int32).cuda())
+        kv.append((k, v))
+    out, _ = _decode(cache, q.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens))
+    for b, (k, v) in enumerate(kv):
+        kk, vv = (_ref_values(x.float(), fmt)[:, 0] for x in (k, v))
+        ref, mag = _ref_attend(q[b], kk, vv, dim ** -0.5, torch.ones(heads, lens[b], dtype=torch.bool))
+        _held(out[b], ref, mag, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens_q,lens_k", [([150, 90], [150, 90]), ([9, 3], [700, 1500]), ([600, 513, 700], [600, 513, 700])])
+def test_prompt_values_near_the_largest(gen, dtype, dim, lens_q, lens_k):
+    # shared tiles, few rows on many keys, launches that fill the card
+    heads, kvh = (24, 3) if sum(lens_q) > 1000 else (4, 2)
+    tq, tk = sum(lens_q), sum(lens_k)
+    q = (_normal(gen, tq, heads, dim) * 1.5).to(DTYPES[dtype])
+    k = _normal(gen, tk, kvh, dim).to(DTYPES[dtype])
+    v = (torch.rand(tk, kvh, dim, generator=gen) * 1e38 + 2e38).to(DTYPES[dtype])
+    v[..., ::2] *= -1
+    cu_q, cu_k = (torch.tensor(np.concatenate(([0], np.cumsum(x))), dtype=torch.int32) for x in (lens_q, lens_k))
+    for causal in (True, False):
+        out = _prompt(q.cuda(), k.cuda(), v.cuda(), cu_q.cuda(), cu_k.cuda(), max_q=max(lens_q), causal=causal)
+        for b, (n, m) in enumerate(zip(lens_q, lens_k)):
+            a, c = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+            seen = torch.arange(m)[None] <= torch.arange(n)[:, None] + (m - n if causal else m)
+            for h in range(0, heads, 3):
+                g = h // (heads // kvh)
+                ref, mag = _ref_attend(q[a, h], k[c, g], v[c, g], dim ** -0.5, seen)
+                _held(out[a, h], ref, mag, dtype, True)
