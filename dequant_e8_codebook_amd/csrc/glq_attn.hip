@@ -492,10 +492,10 @@ __device__ __forceinline__ int length_of(const DecodeArgs &a, int b) {
 // longer stays whole. Where there is a unit for every CU the memory is busy
 // anyway and the cost is paid in full: 32 x 2048 tokens, 8 kept heads, 8 bits: 28.6
 // us whole, 34.9 in halves; one sequence of 1024: 11.9 in eight parts, 13.0 in one.
-// Any value from 1 on is right; every workgroup computes the same one.
+// Any value from 1 on is right; every workgroup computes the same one (the multiply-add is written
+// out, so that each copy of this rounds alike: find_place's last loop ends by it).
 __device__ __forceinline__ int parts_of(int tiles, float inv, int spare) {
-  const float n = (float)tiles * inv;
-  return tiles == 0 ? 0 : (float)(tiles - spare) * inv <= 1.0f ? 1 : (int)(n + 0.999f);
+  return tiles == 0 ? 0 : (float)(tiles - spare) * inv <= 1.0f ? 1 : (int)__builtin_fmaf((float)tiles, inv, 0.999f);
 }
 
 // inclusive sum, or maximum of values from 0 on, over the lanes up to each (DPP
@@ -1152,16 +1152,17 @@ template <int R> __device__ __forceinline__ Spot find_tile(const PromptArgs &a, 
   const int upto = wave_scan<false>(mine);
   const uint64_t here = __builtin_amdgcn_ballot_w64(upto - mine <= at && at < upto);
   if (!here) return none;
-  int base = __builtin_amdgcn_readlane(upto - mine, __builtin_ctzll(here)), b = __builtin_ctzll(here) * each;
-  while (true) {                                     // ends: the tile is of one of the lane's sequences
+  const int lane_of = __builtin_ctzll(here);
+  int base = __builtin_amdgcn_readlane(upto - mine, lane_of);
+  for (int b = lane_of * each; b < min(a.batch, (lane_of + 1) * each); ++b) {  // the tile is of one of the lane's sequences
     const Span s = span_of(a, b);
     const int n = __builtin_amdgcn_readfirstlane(tiles_of<R>(a, s.lq));
     if (at < base + n)
       return {{__builtin_amdgcn_readfirstlane(s.q0), __builtin_amdgcn_readfirstlane(s.lq),
                __builtin_amdgcn_readfirstlane(s.k0), __builtin_amdgcn_readfirstlane(s.lk)}, n - 1 - (at - base)};
     base += n;
-    ++b;
   }
+  return none;
 }
 
 // The float32 path. A workgroup takes 16 CT rows (queries times the heads that
