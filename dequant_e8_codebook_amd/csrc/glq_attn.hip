@@ -1688,6 +1688,8 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
 bool valid_dtype(int dt) { return dt == GLQ_F32 || dt == GLQ_BF16; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool valid_dim(int d) { return d == 64 || d == 128 || d == 256; }
+// workgroups of 256 that a launch can have: its threads are counted in 32 bits
+constexpr int64_t kMaxGroups = 0xFFFFFFFFu / 256;
 int log2_of(int x) { return 31 - __builtin_clz((unsigned)x); }
 
 int check_cache(const glq_kv_cache *C) {
@@ -1752,7 +1754,7 @@ int check_decode(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t 
   if (batch < 0 || q_heads < 1 || q_heads % C->kv_heads || max_len < 0) return GLQ_ERR_ARG;
   if (max_len > 0x7FFFFFFF - 4096 || q_heads > 65536) return GLQ_ERR_UNSUPPORTED;
   const int64_t tiles = (q_heads / C->kv_heads + 15) / 16;
-  if (batch > 0x7FFFFFFF / ((int64_t)C->kv_heads * tiles)) return GLQ_ERR_UNSUPPORTED;
+  if (batch > kMaxGroups / ((int64_t)C->kv_heads * tiles)) return GLQ_ERR_UNSUPPORTED;
   return GLQ_OK;
 }
 
@@ -1814,6 +1816,7 @@ int launch_decode_dim(const DecodeArgs &a, int d, glq_dtype dt, int64_t groups, 
 
 template <auto Kernel>
 int launch_rows(const PromptArgs &a, int64_t groups, int threads, size_t shm, hipStream_t st, const char *name) {
+  if (groups > kMaxGroups) return GLQ_ERR_UNSUPPORTED;
   const int rc = allow_lds<Kernel>(shm);
   if (rc) return rc;
   hipLaunchKernelGGL(Kernel, dim3((unsigned)groups), dim3((unsigned)threads), shm, st, a);
@@ -1821,7 +1824,8 @@ int launch_rows(const PromptArgs &a, int64_t groups, int threads, size_t shm, hi
 }
 
 // workgroups of R rows that a launch can need: no sequence has more than max_q
-// queries, and all together no more than total_q
+// queries, and all together no more than total_q (no overflow: batch and rows are below 2^31, heads
+// below 2^17, and the smaller of the two counts is below 2^46)
 int64_t prompt_groups(const PromptArgs &a, int R) {
   const int64_t group = a.q_heads / a.kv_heads, one = (a.max_q * group + R - 1) / R;
   const int64_t all = (a.total_q * group) / R + a.batch;
@@ -1934,9 +1938,7 @@ extern "C" int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_st
     return GLQ_ERR_ARG;
   const int64_t most = P->max_q < P->total_q ? P->max_q : P->total_q;
   const bool f = P->dt == GLQ_F32;
-  // workgroups: no more than this in either kernel
-  if (P->batch > 0x7FFFFFFF / (P->q_heads * ((most + 15) / 16 + 1)) || most * P->q_heads > 0x7FFFFFFF - 64)
-    return GLQ_ERR_UNSUPPORTED;
+  if (P->batch >= 0x7FFFFFFF || most * P->q_heads > 0x7FFFFFFF - 64) return GLQ_ERR_UNSUPPORTED;
   const float scale2 = P->scale * 1.4426950408889634f;
   const PromptArgs a = {P->q, P->k, P->v, P->out, P->q_stride, P->k_stride, P->v_stride, P->out_stride, P->total_q,
                         P->total_k, P->cu_q, P->cu_k, most, P->q_heads, P->kv_heads, (int32_t)P->batch,

@@ -450,7 +450,8 @@ size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q
  * NaN, one of -inf no weight, and a row of -inf alone zeros.
  * Results do not depend on the order in which workgroups finish. q_heads must be
  * a multiple of kv_heads. batch == 0 is a successful no-op; GLQ_ERR_UNSUPPORTED
- * for launches past 2^31 workgroups.
+ * for launches of 2^24 workgroups (sequences times kept heads, times 16s of the query
+ * heads that share one).
  */
 int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype dt, int64_t q_stride, int64_t batch,
                     int32_t q_heads, const int32_t *page_table, int64_t max_pages, const int32_t *lens,
@@ -489,7 +490,9 @@ typedef struct {
  *   dt = GLQ_BF16: bf16 matrix-core path, weights rounded to bf16, float32 sums
  *   dt = GLQ_F32:  float32 products and sums
  * batch == 0, total_q == 0 or max_q == 0 is a successful no-op. out must not
- * overlap q, k or v. GLQ_ERR_UNSUPPORTED for k_stride or v_stride above 2^22.
+ * overlap q, k or v. GLQ_ERR_UNSUPPORTED for k_stride or v_stride above 2^22, for
+ * max_q (or total_q) * q_heads of about 2^31, and for launches of 2^24 workgroups
+ * (at least 16 queries times heads of a kept head each, and one more a sequence).
  */
 int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_stream);
 

@@ -863,3 +863,42 @@ def test_prompt_values_near_the_largest(gen, dtype, dim, lens_q, lens_k):
                 g = h // (heads // kvh)
                 ref, mag = _ref_attend(q[a, h], k[c, g], v[c, g], dim ** -0.5, seen)
                 _held(out[a, h], ref, mag, dtype, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_prompt_very_many_sequences(gen, dtype):
+    # as many sequences as tokens allow, and no bound given on their lengths: the size of the launch
+    # comes from the totals
+    batch, heads, kvh, dim = 20000, 32, 8, 64
+    lens = torch.randint(0, 9, (batch,), generator=gen)
+    cu = torch.cat((torch.zeros(1, dtype=torch.long), lens.cumsum(0))).to(torch.int32)
+    total = int(cu[-1])
+    q = _normal(gen, total, heads, dim, dtype=DTYPES[dtype])
+    k, v = (_normal(gen, total, kvh, dim, dtype=DTYPES[dtype]) for _ in range(2))
+    out = _prompt(q.cuda(), k.cuda(), v.cuda(), cu.cuda(), None)
+    assert not (out == 7).all(-1).any()              # every row is written
+    for b in list(range(0, batch, 1111)) + [batch - 1]:
+        n, a = int(lens[b]), slice(cu[b], cu[b + 1])
+        seen = torch.ones(n, n, dtype=torch.bool).tril()
+        for h in (0, 13, 31):
+            ref, mag = _ref_attend(q[a, h], k[a, h // 4], v[a, h // 4], dim ** -0.5, seen)
+            _held(out[a, h], ref, mag, dtype, True)
+
+
+def test_launches_past_the_grid_are_refused():
+    # threads of a launch are counted in 32 bits: 2^24 - 1 workgroups of 256
+    lib = glq.raw()
+    c = ctypes.byref(_cache_struct())
+    for batch, heads in ((2 ** 23, 4), (2 ** 22, 36)):
+        assert lib.glq_attn_decode_workspace(c, batch, heads, 10) == 0
+        assert lib.glq_attn_decode(c, 256, 1, 128 * heads, batch, heads, 256, 1, 256, 10, 0.1, 256, 128 * heads, 256,
+                                   1 << 40, None) == glq.GLQ_ERR_UNSUPPORTED
+    assert lib.glq_attn_decode_workspace(c, 2 ** 23 - 1, 4, 10) >= 65536
+    p = dict(q=256, k=256, v=256, out=256, dt=1, q_heads=4, kv_heads=2, head_dim=64, q_stride=256, k_stride=128,
+             v_stride=128, out_stride=256, total_q=2 ** 24, total_k=2 ** 24, batch=2 ** 24, cu_q=256, cu_k=256, max_q=1,
+             scale=0.1)
+    for bad in (dict(), dict(dt=0), dict(batch=2 ** 31 - 1), dict(batch=2 ** 62), dict(total_q=2 ** 31 - 1, max_q=2 ** 31)):
+        a = dict(p, **bad)
+        assert lib.glq_attn_prompt(ctypes.byref(glq.PromptStruct(*[a[f[0]] for f in glq.PromptStruct._fields_])), 1,
+                                   None) == glq.GLQ_ERR_UNSUPPORTED, bad
