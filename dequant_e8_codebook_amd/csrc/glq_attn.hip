@@ -1877,9 +1877,18 @@ extern "C" int glq_kv_read(const glq_kv_cache *C, const int32_t *slots, int64_t 
 
 extern "C" size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t max_len) {
   if (check_decode(C, batch, q_heads, max_len)) return 0;
-  const int64_t f = decode_plan(C, GLQ_F32, batch, q_heads, max_len).ws_bytes;
-  const int64_t b = decode_plan(C, GLQ_BF16, batch, q_heads, max_len).ws_bytes;
-  return (size_t)(f > b ? f : b);
+  // the need grows with the batch as long as units are split, and is the control words alone
+  // beyond: the largest batch up to this one that is split needs most
+  const int64_t each = (int64_t)C->kv_heads * ((q_heads / C->kv_heads + 15) / 16);
+  int64_t bytes = 0;
+  for (const int dt : {GLQ_F32, GLQ_BF16}) {
+    const int64_t split = (kTickets - kCus * decode_per_cu(C->head_dim, dt == GLQ_F32) / 2) / each;
+    for (const int64_t b : {batch, batch < split ? batch : split}) {
+      const int64_t need = decode_plan(C, dt, b, q_heads, max_len).ws_bytes;
+      bytes = need > bytes ? need : bytes;
+    }
+  }
+  return (size_t)bytes;
 }
 
 extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype dt, int64_t q_stride, int64_t batch,

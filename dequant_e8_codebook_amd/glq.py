@@ -718,6 +718,7 @@ def kv_read(cache: KvCache, slots, k, v, stream=None):
 
 
 def attn_decode_workspace_bytes(cache: KvCache, batch: int, q_heads: int, max_len: int) -> int:
+    """Bytes that attn_decode needs for up to `batch` sequences of up to max_len tokens."""
     return int(_lib.glq_attn_decode_workspace(cache._ref, batch, q_heads, max_len))
 
 

@@ -417,7 +417,8 @@ int glq_kv_read(const glq_kv_cache *C, const int32_t *slots, int64_t tokens, voi
                 int64_t k_stride, int64_t v_stride, void *hip_stream);
 
 /* Bytes of device workspace glq_attn_decode needs, its control words
- * (GLQ_ATTN_CTRL_BYTES) included; 0 for arguments it would refuse. */
+ * (GLQ_ATTN_CTRL_BYTES) included, for this batch and max_len or any smaller ones
+ * (one of the largest sizes serves them all); 0 for arguments it would refuse. */
 #define GLQ_ATTN_CTRL_BYTES 65536
 size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q_heads, int64_t max_len);
 

@@ -902,3 +902,31 @@ def test_launches_past_the_grid_are_refused():
         a = dict(p, **bad)
         assert lib.glq_attn_prompt(ctypes.byref(glq.PromptStruct(*[a[f[0]] for f in glq.PromptStruct._fields_])), 1,
                                    None) == glq.GLQ_ERR_UNSUPPORTED, bad
+
+
+@pytest.mark.parametrize("kv_heads,q_heads", [(1, 1), (8, 32), (40, 40), (2, 300), (7, 7), (512, 512), (20000, 20000)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_decode_workspace_grows_with_the_batch(kv_heads, q_heads, dim):
+    # one workspace for the largest batch and length serves every smaller one
+    lib, c = glq.raw(), _cache_struct(kv_heads=kv_heads, head_dim=dim)
+
+    def need(batch, most):
+        return lib.glq_attn_decode_workspace(ctypes.byref(c), batch, q_heads, most)
+    edge = 16384 // kv_heads
+    for most in (100, 129, 5000, 200000):
+        sizes = [need(b, most) for b in sorted({1, 2, 63, 64, 65, 100, 300, 2000, 4096, 9000, *range(max(1, edge - 500), edge + 3, 7)})]
+        sizes = sizes[:sizes.index(0)] if 0 in sizes else sizes     # (0: past what a launch holds)
+        assert sizes == sorted(sizes) and sizes[0] >= 65536
+    for b in (1, 64, 65, 300, 3000):
+        sizes = [need(b, most) for most in (0, 1, 128, 129, 256, 257, 4000, 10 ** 6)]
+        assert sizes == sorted(sizes)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_decode_workspace_of_a_larger_batch(gen, dtype):
+    # sized for a batch that is not split any more, used for one that is
+    cache, q, table, ln, ref, mag = _decode_case(gen, "int8", [3000, 700], 4, 2, 128, 32, dtype)
+    ws = torch.zeros(glq.attn_decode_workspace_bytes(cache, 9000, 4, 3000), dtype=torch.uint8, device="cuda")
+    out, _ = _decode(cache, q, table, ln, 3000, ws)
+    _held(out, ref, mag, dtype)
