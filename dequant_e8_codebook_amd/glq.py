@@ -650,8 +650,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the cur
 
 
 def _stream_on(device, stream):
+    """The stream's handle (the current one's unless given). A launch goes to the current
+    device, whatever the tensors are on, so that has to be theirs, and the stream's."""
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
     if stream is None and _raw_stream is not None:
         return _raw_stream(device.index)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, expected {device}")
     return _stream_ptr(stream)
 
 

@@ -34,7 +34,8 @@
  *    launch; no error aborts the process or escapes as an exception.
  *  - GPU calls are asynchronous on the given HIP stream (NULL = default
  *    stream), never synchronise the host, and keep no state between calls:
- *    calls on different streams may run concurrently.
+ *    calls on different streams may run concurrently. They run on the current
+ *    device, which has to be the pointers' and the stream's.
  *  - Layouts are dense row-major with no padding.
  */
 #ifndef GLQ_H

@@ -930,3 +930,31 @@ def test_decode_workspace_of_a_larger_batch(gen, dtype):
     ws = torch.zeros(glq.attn_decode_workspace_bytes(cache, 9000, 4, 3000), dtype=torch.uint8, device="cuda")
     out, _ = _decode(cache, q, table, ln, 3000, ws)
     _held(out, ref, mag, dtype)
+
+
+@pytest.mark.gpu
+def test_attention_refuses_another_device(gen, monkeypatch):
+    # a launch goes to the current device: tensors or a stream of another one are refused
+    cache, q, table, ln, _, _ = _decode_case(gen, "int8", [20, 3], 4, 2, 64, 16, "bf16")
+    ws = torch.zeros(glq.attn_decode_workspace_bytes(cache, 2, 4, 20), dtype=torch.uint8, device="cuda")
+    k = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(5, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    calls = (lambda **s: glq.kv_append(cache, k, k, slots, **s),
+             lambda **s: glq.kv_read(cache, slots, k.clone(), k.clone(), **s),
+             lambda **s: glq.attn_decode(cache, q, table, ln, torch.empty_like(q), ws, 20, **s),
+             lambda **s: glq.attn_prompt(k, k, k, k.clone(), cu, **s))
+
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+    for call in calls:
+        call()
+        call(stream=torch.cuda.Stream())
+        with pytest.raises(ValueError, match="stream"):
+            call(stream=Elsewhere())
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
