@@ -255,9 +255,15 @@ def _torch():
     return torch
 
 
-def _stream_ptr(stream=None):
+def _stream_ptr(stream, device):
+    """The stream's handle (the current one's unless given). A launch goes to the current
+    device, whatever the tensors are on, so that has to be theirs, and the stream's."""
     torch = _torch()
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
     s = stream if stream is not None else torch.cuda.current_stream()
+    if stream is not None and s.device != device:
+        raise ValueError(f"stream: on {s.device}, expected {device}")
     return ctypes.c_void_p(s.cuda_stream)
 
 
@@ -491,7 +497,7 @@ def fused_linear_noalloc(layer: Layer, x, y, flags: int = 0, stream=None):
         raise ValueError("flags: unknown bits")
     st = layer.struct()
     rc = _lib.glq_fused_linear_noalloc(ctypes.byref(st), x.data_ptr(), _dtype_code(x), x.shape[0], y.data_ptr(),
-                                       _dtype_code(y), flags, _stream_ptr(stream))
+                                       _dtype_code(y), flags, _stream_ptr(stream, dev))
     _check(rc, "glq_fused_linear_noalloc")
     return y
 
@@ -504,7 +510,7 @@ def ep_decode_weights(layer: EpLayer, out, stream=None):
     if out.data_ptr() % 16:
         raise ValueError("out: must be 16-byte aligned")
     st = layer.struct()
-    _check(_lib.glq_ep_decode_weights(ctypes.byref(st), out.data_ptr(), _dtype_code(out), _stream_ptr(stream)),
+    _check(_lib.glq_ep_decode_weights(ctypes.byref(st), out.data_ptr(), _dtype_code(out), _stream_ptr(stream, dev)),
            "glq_ep_decode_weights")
     return out
 
@@ -521,7 +527,7 @@ def ep_fused_linear(layer: EpLayer, x, y, workspace, flags: int = 0, stream=None
     st = layer.struct()
     rc = _lib.glq_ep_fused_linear(ctypes.byref(st), x.data_ptr(), _dtype_code(x), m, y.data_ptr(),
                                   _dtype_code(y), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                  flags, _stream_ptr(stream))
+                                  flags, _stream_ptr(stream, dev))
     _check(rc, "glq_ep_fused_linear")
     return y
 
@@ -544,7 +550,7 @@ def rht_apply(inp, out, signs, transpose: bool, stream=None):
     if out.data_ptr() == inp.data_ptr() and out.dtype != inp.dtype:
         raise ValueError("out: in place needs the same dtype")
     rc = _lib.glq_rht_apply(inp.data_ptr(), _dtype_code(inp), out.data_ptr(), _dtype_code(out), rows, n,
-                            signs.data_ptr(), int(bool(transpose)), _stream_ptr(stream))
+                            signs.data_ptr(), int(bool(transpose)), _stream_ptr(stream, dev))
     _check(rc, "glq_rht_apply")
     return out
 
@@ -555,7 +561,7 @@ def decode_weights(layer: Layer, out, stream=None):
     dev = _check_layer(layer, False, False)
     _dev_tensor(out, "out", dev, shape=(layer.n, layer.k), dtypes=(torch.float32, torch.bfloat16))
     st = layer.struct()
-    _check(_lib.glq_decode_weights(ctypes.byref(st), out.data_ptr(), _dtype_code(out), _stream_ptr(stream)),
+    _check(_lib.glq_decode_weights(ctypes.byref(st), out.data_ptr(), _dtype_code(out), _stream_ptr(stream, dev)),
            "glq_decode_weights")
     return out
 
@@ -572,7 +578,7 @@ def fused_linear(layer: Layer, x, y, workspace, flags: int = 0, stream=None):
     st = layer.struct()
     rc = _lib.glq_fused_linear(ctypes.byref(st), x.data_ptr(), _dtype_code(x), m, y.data_ptr(),
                                _dtype_code(y), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               flags, _stream_ptr(stream))
+                               flags, _stream_ptr(stream, dev))
     _check(rc, "glq_fused_linear")
     return y
 
@@ -650,15 +656,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the cur
 
 
 def _stream_on(device, stream):
-    """The stream's handle (the current one's unless given). A launch goes to the current
-    device, whatever the tensors are on, so that has to be theirs, and the stream's."""
-    if torch.cuda.current_device() != device.index:
-        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
-    if stream is None and _raw_stream is not None:
+    if stream is None and _raw_stream is not None and torch.cuda.current_device() == device.index:
         return _raw_stream(device.index)
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream: on {stream.device}, expected {device}")
-    return _stream_ptr(stream)
+    return _stream_ptr(stream, device)
 
 
 def _rows(t, name, device, dtype, total, heads, dim):

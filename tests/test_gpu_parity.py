@@ -1010,3 +1010,34 @@ def test_binding_rejects_bad_arguments(G, cb):
     G.fused_linear(L, x, y, ws)
     torch.cuda.synchronize()
     assert torch.isfinite(y.float()).all()
+
+
+def test_calls_refuse_another_device(G, cb, monkeypatch):
+    # a launch goes to the current device: tensors or a stream of another one are refused
+    n, k, m = 64, 128, 3
+    i1, i2 = _random_layer(n, k, 2, 5)
+    L = G.Layer.from_numpy(i1, i2, np.float32(0.02), workloads.signs(n, 1), workloads.signs(k, 2), cb)
+    x = torch.zeros(m, k, device="cuda", dtype=torch.bfloat16)
+    y = torch.empty(m, n, device="cuda", dtype=torch.bfloat16)
+    w = torch.empty(n, k, device="cuda", dtype=torch.bfloat16)
+    ws = torch.zeros(G.workspace_bytes(L, m), device="cuda", dtype=torch.uint8)
+    weights, sn, sk = _ep_weights(64, 128, 3)
+    E = G.EpLayer.from_host(G.ep_encode(weights, sn, sk, 0.22, 1), sign_k=sk, sign_n=sn)
+    ews = torch.zeros(G.ep_workspace_bytes(E, m), device="cuda", dtype=torch.uint8)
+    calls = (lambda **s: G.fused_linear(L, x, y, ws, **s), lambda **s: G.fused_linear_noalloc(L, x, y, **s),
+             lambda **s: G.decode_weights(L, w, **s), lambda **s: G.rht_apply(x, x.clone(), L.sign_k, False, **s),
+             lambda **s: G.ep_decode_weights(E, w, **s), lambda **s: G.ep_fused_linear(E, x, y, ews, **s))
+
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+    for call in calls:
+        call()
+        call(stream=torch.cuda.current_stream())
+        with pytest.raises(ValueError, match="stream"):
+            call(stream=Elsewhere())
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
