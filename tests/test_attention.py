@@ -958,3 +958,34 @@ def test_attention_refuses_another_device(gen, monkeypatch):
     for call in calls:
         with pytest.raises(ValueError, match="current device"):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "int4"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("size", [1.0, 1e-25, 1e30])
+def test_append_float32_mantissas(gen, fmt, dim, size):
+    # float32 inputs with all their bits: the product x Q and the quotient by a are
+    # each rounded to float32, the code is that rounded half to even
+    tokens, heads, q = 600, 3, np.float32(LEVELS[fmt])
+    x = _normal(gen, tokens, heads, dim).numpy() * np.float32(size)
+    # quotients next to the halves, where one rounding more or less shows
+    a = np.abs(x).max(-1, keepdims=True)
+    half = np.float32(0.5) + np.arange(dim, dtype=np.float32) % np.float32(LEVELS[fmt] - 1)
+    near = (half * a / q).astype(np.float32)
+    for token in range(0, tokens, 2):
+        step = token // 2 % 7 - 3
+        x[token] = near[token]
+        for _ in range(abs(step)):
+            x[token] = np.nextafter(x[token], np.float32(np.inf if step > 0 else 0))
+        x[token, :, -1] = a[token, :, 0]
+    a = np.abs(x).max(-1, keepdims=True)
+    want = np.rint((x * q).astype(np.float32) / a)
+    assert (x * q).dtype == np.float32 and want.dtype == np.float32
+    cache = glq.KvCache.empty(-(-tokens // 64), 64, heads, dim, FORMATS[fmt])
+    t = torch.from_numpy(x).cuda()
+    glq.kv_append(cache, t, -t, torch.arange(tokens, dtype=torch.int32, device="cuda"))
+    at = torch.arange(tokens)
+    for codes, scale, sign in zip(_unpack(cache), (cache.k_scale, cache.v_scale), (1, -1)):
+        assert torch.equal(codes[at // 64, :, at % 64], sign * torch.from_numpy(want).double())
+        assert torch.equal(scale.cpu()[at // 64, :, at % 64], torch.from_numpy((a / q)[..., 0]))
