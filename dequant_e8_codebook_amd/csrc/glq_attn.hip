@@ -1687,6 +1687,8 @@ __global__ void __launch_bounds__(FEW ? 64 * few_waves<D>() : 256, FEW || D == 2
 
 bool valid_dtype(int dt) { return dt == GLQ_F32 || dt == GLQ_BF16; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+constexpr float kLog2e = 1.4426950408889634f;
+bool valid_scale(float scale) { return std::isfinite(scale * kLog2e); }      // the kernels' exponentials are of base 2
 bool valid_dim(int d) { return d == 64 || d == 128 || d == 256; }
 // workgroups of 256 that a launch can have: its threads are counted in 32 bits
 constexpr int64_t kMaxGroups = 0xFFFFFFFFu / 256;
@@ -1897,7 +1899,7 @@ extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype d
                                size_t ws_bytes, void *hip_stream) {
   const int rc = check_decode(C, batch, q_heads, max_len);
   if (rc) return rc;
-  if (!valid_dtype(dt) || !std::isfinite(scale) || max_pages < 0) return GLQ_ERR_ARG;
+  if (!valid_dtype(dt) || !valid_scale(scale) || max_pages < 0) return GLQ_ERR_ARG;
   if (batch == 0) return GLQ_OK;
   if (max_len > (max_pages < 0x7FFFFFFF ? max_pages : 0x7FFFFFFF) * C->page_size) return GLQ_ERR_ARG;
   if (!valid_rows(q, q_stride, q_heads, C->head_dim, dt) || !valid_rows(out, out_stride, q_heads, C->head_dim, dt) ||
@@ -1909,7 +1911,7 @@ extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype d
       (reinterpret_cast<uintptr_t>(workspace) & 255))
     return GLQ_ERR_WORKSPACE;
   const int32_t group = q_heads / C->kv_heads, tiles = (group + 15) / 16;
-  const float scale2 = scale * 1.4426950408889634f;
+  const float scale2 = scale * kLog2e;
   const DecodeArgs a = {C->k, C->v, C->k_scale, C->v_scale, q, out, q_stride, out_stride, page_table, lens, max_pages,
                         max_len, C->kv_heads, group, tiles, log2_of(C->page_size), (int32_t)C->num_pages,
                         scale2 == 0.0f ? 1.0f : fabsf(scale2), scale2 == 0.0f ? 0.0f : copysignf(1.0f, scale2),
@@ -1929,7 +1931,7 @@ extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype d
 }
 
 extern "C" int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_stream) {
-  if (!P || (flags & ~1u) || !valid_dtype(P->dt) || !std::isfinite(P->scale)) return GLQ_ERR_ARG;
+  if (!P || (flags & ~1u) || !valid_dtype(P->dt) || !valid_scale(P->scale)) return GLQ_ERR_ARG;
   if (P->q_heads < 1 || P->kv_heads < 1 || P->q_heads % P->kv_heads) return GLQ_ERR_ARG;
   if (P->total_q < 0 || P->total_k < 0 || P->batch < 0 || P->max_q < 0) return GLQ_ERR_ARG;
   if (!valid_dim(P->head_dim) || P->q_heads > 65536) return GLQ_ERR_UNSUPPORTED;
@@ -1948,7 +1950,7 @@ extern "C" int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_st
   const int64_t most = P->max_q < P->total_q ? P->max_q : P->total_q;
   const bool f = P->dt == GLQ_F32;
   if (P->batch >= 0x7FFFFFFF || most * P->q_heads > 0x7FFFFFFF - 64) return GLQ_ERR_UNSUPPORTED;
-  const float scale2 = P->scale * 1.4426950408889634f;
+  const float scale2 = P->scale * kLog2e;
   const PromptArgs a = {P->q, P->k, P->v, P->out, P->q_stride, P->k_stride, P->v_stride, P->out_stride, P->total_q,
                         P->total_k, P->cu_q, P->cu_k, most, P->q_heads, P->kv_heads, (int32_t)P->batch,
                         (flags & GLQ_ATTN_CAUSAL) ? 1 : 0,

@@ -437,7 +437,7 @@ size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q
  *               a row of zeros
  *   max_len     host: no length exceeds it; <= max_pages * page_size. The
  *               launch is sized by it.
- *   scale       finite
+ *   scale       finite, and times log2(e) too (below 2.35e38)
  *   dt          GLQ_BF16: the weights are taken as sums of two bf16 values (16 bits)
  *               for the matrix cores; GLQ_F32: q and the weights as sums of three,
  *               so every product is that of float32 operands. Sums are float32.
@@ -477,7 +477,7 @@ typedef struct {
     int64_t batch;
     const int32_t *cu_q, *cu_k;   /* [batch + 1], not decreasing, within 0 .. total */
     int64_t max_q;            /* no sequence has more queries; the launch is sized by it */
-    float scale;              /* finite */
+    float scale;              /* as in glq_attn_decode */
 } glq_prompt;
 
 /*

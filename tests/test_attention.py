@@ -989,3 +989,36 @@ def test_append_float32_mantissas(gen, fmt, dim, size):
     for codes, scale, sign in zip(_unpack(cache), (cache.k_scale, cache.v_scale), (1, -1)):
         assert torch.equal(codes[at // 64, :, at % 64], sign * torch.from_numpy(want).double())
         assert torch.equal(scale.cpu()[at // 64, :, at % 64], torch.from_numpy((a / q)[..., 0]))
+
+
+def test_scale_refusals():
+    # a scale that is finite, but not once the kernels' exponentials of base 2 are paid for: products
+    # of 0 would give NaN
+    lib, c = glq.raw(), _cache_struct()
+    for scale in (2.4e38, -2.4e38, 3.4e38):
+        assert lib.glq_attn_decode(ctypes.byref(c), 256, 1, 512, 2, 4, 256, 3, 256, 96, scale, 256, 512, 256, 1 << 30,
+                                   None) == glq.GLQ_ERR_ARG
+        st = glq.PromptStruct(256, 256, 256, 256, 1, 4, 2, 64, 256, 128, 128, 256, 5, 5, 1, 256, 256, 5, scale)
+        assert lib.glq_attn_prompt(ctypes.byref(st), 1, None) == glq.GLQ_ERR_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30, 1e30])
+def test_signs_and_sizes_of_the_scale(gen, dtype, scale):
+    # queries made to fit the scale's size: scores of about 0.3 |q.k|
+    n, dim = 70, 64
+    size = 0.3 / abs(scale) if abs(scale) in (1e-30, 1e30) else 1.0
+    q = (_normal(gen, 5, 4, dim) * size).to(DTYPES[dtype])
+    k, v = (_normal(gen, n, 2, dim, dtype=torch.bfloat16).to(DTYPES[dtype]) for _ in range(2))
+    cu = [torch.tensor([0, x], dtype=torch.int32, device="cuda") for x in (5, n)]
+    out = _prompt(q.cuda(), k.cuda(), v.cuda(), *cu, causal=False, scale=scale)
+    cache = glq.KvCache.empty(5, 16, 2, dim, glq.KV_BF16)
+    glq.kv_append(cache, k.cuda(), v.cuda(), torch.arange(n, dtype=torch.int32, device="cuda"))
+    table = torch.arange(5, dtype=torch.int32, device="cuda")[None].repeat(5, 1)
+    one, _ = _decode(cache, q.cuda(), table, torch.full((5,), n, dtype=torch.int32, device="cuda"), n, scale=scale)
+    for h in range(4):
+        ref, mag = _ref_attend(q[:, h], k[:, h // 2], v[:, h // 2], float(np.float32(scale)),
+                               torch.ones(5, n, dtype=torch.bool))
+        _held(out[:, h], ref, mag, dtype, True)
+        _held(one[:, h], ref, mag, dtype)
