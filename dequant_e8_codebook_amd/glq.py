@@ -689,6 +689,10 @@ def _ints(t, name, device, *shape):
     return t.data_ptr()
 
 
+def _last_size(t):                                   # (-1: what _ints refuses)
+    return t.shape[-1] if isinstance(t, torch.Tensor) and t.dim() else -1
+
+
 _ATTN_DTYPES = {torch.float32: GLQ_F32, torch.bfloat16: GLQ_BF16}
 
 
@@ -738,9 +742,9 @@ def attn_decode(cache: KvCache, q, page_table, lens, out, workspace, max_len: in
     batch, heads = q.shape[0], q.shape[1]
     qp, qs = _rows(q, "q", dev, q.dtype, batch, heads, dim)
     op, os_ = _rows(out, "out", dev, q.dtype, batch, heads, dim)
-    lp, pages = _ints(lens, "lens", dev, batch), page_table.shape[-1]
+    lp, pages = _ints(lens, "lens", dev, batch), _last_size(page_table)
     tp = _ints(page_table, "page_table", dev, batch, pages)
-    if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: must be contiguous on {dev}")
     rc = _lib.glq_attn_decode(cache._ref, qp, dt, qs, batch, heads, tp, pages, lp, max_len,
                               dim ** -0.5 if scale is None else scale, op, os_, workspace.data_ptr(), workspace.nbytes,
@@ -766,7 +770,7 @@ def attn_prompt(q, k, v, out, cu_q, cu_k=None, max_q: int | None = None, causal:
     kp, ks = _rows(k, "k", dev, q.dtype, total_k, kvh, dim)
     vp, vs = _rows(v, "v", dev, q.dtype, total_k, kvh, dim)
     op, os_ = _rows(out, "out", dev, q.dtype, total_q, heads, dim)
-    batch = cu_q.shape[0] - 1
+    batch = _last_size(cu_q) - 1
     cq = _ints(cu_q, "cu_q", dev, batch + 1)
     ck = cq if cu_k is None else _ints(cu_k, "cu_k", dev, batch + 1)
     st = PromptStruct(qp, kp, vp, op, dt, heads, kvh, dim, qs, ks, vs, os_, total_q, total_k, batch, cq, ck,

@@ -1022,3 +1022,28 @@ def test_signs_and_sizes_of_the_scale(gen, dtype, scale):
                                torch.ones(5, n, dtype=torch.bool))
         _held(out[:, h], ref, mag, dtype, True)
         _held(one[:, h], ref, mag, dtype)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_what_is_no_tensor(gen):
+    cache, q, table, ln, _, _ = _decode_case(gen, "int8", [20, 3], 4, 2, 64, 16, "bf16")
+    ws = torch.zeros(glq.attn_decode_workspace_bytes(cache, 2, 4, 20), dtype=torch.uint8, device="cuda")
+    good = dict(q=q, page_table=table, lens=ln, out=torch.empty_like(q), workspace=ws, max_len=20)
+    k = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    for bad in (None, [[0, 1]], 7, torch.tensor(3, dtype=torch.int32, device="cuda")):
+        for name in ("q", "page_table", "lens", "out"):
+            with pytest.raises(ValueError):
+                glq.attn_decode(cache, **dict(good, **{name: bad}))
+        with pytest.raises(ValueError):
+            glq.attn_prompt(k, k, k, k.clone(), bad)
+        with pytest.raises(ValueError):
+            glq.kv_append(cache, k, k, bad)
+        if bad is not None:
+            with pytest.raises(ValueError):
+                glq.attn_prompt(k, k, k, k.clone(), cu, bad)
+    for bad in (None, 7, ws.cpu(), ws[::2]):
+        with pytest.raises(ValueError):
+            glq.attn_decode(cache, **dict(good, workspace=bad))
+    with pytest.raises(glq.GlqError):
+        glq.attn_prompt(k, k, k, k.clone(), cu[:0])
