@@ -824,27 +824,36 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
           const int e = slices == 1 ? e0 + threadIdx.x : threadIdx.x % items;
           const int slice = slices == 1 ? 0 : threadIdx.x / items;
           Sums x = {{0, 0, 0, 0, 0, 0, 0, 0}, -INFINITY, 0.0f};
+          // Parts a thread has in flight: 8 where that is all of them, since loads past the last cost as
+          // much as others (four sequences of up to 3000, 32 heads on 8 of 128, bf16: 12.4 us, 16.2 with
+          // 16; one of 1000, float32: 10.0, 12.5 with 24), and as many as the registers hold otherwise (24
+          // parts, 8 heads on 1 of 256: 15.6 us with 24, 16.3 with 8). Heads of 64, three workgroups a CU,
+          // have registers for 8 (one of 8192: 11.9 us, 18.5 with 16).
           if (e < items && slice < slices) {
             const int row = e / (D / 8);
-            constexpr int FLY = D == 64 ? 8 : F32 || D == 256 ? 24 : 16;     // parts whose loads are in flight
-            for (int c0 = slice; c0 < count; c0 += FLY * slices) {
-              f32x4 lo[FLY], hi[FLY], mt[FLY];
+            auto take = [&](auto fly) INLINED {
+              constexpr int FLY = decltype(fly)::value;                      // parts whose loads are in flight
+              for (int c0 = slice; c0 < count; c0 += FLY * slices) {
+                f32x4 lo[FLY], hi[FLY], mt[FLY];
 #pragma unroll
-              for (int j = 0; j < FLY; ++j) {        // past the last: the last, unused
-                const int p = min(c0 + j * slices, count - 1) * a.part_floats;
-                lo[j] = load_shared(all, p + 8 * e), hi[j] = load_shared(all, p + 8 * e + 4);
-                mt[j] = load_shared(all, p + rows * D + 4 * row);
+                for (int j = 0; j < FLY; ++j) {      // past the last: the last, unused
+                  const int p = min(c0 + j * slices, count - 1) * a.part_floats;
+                  lo[j] = load_shared(all, p + 8 * e), hi[j] = load_shared(all, p + 8 * e + 4);
+                  mt[j] = load_shared(all, p + rows * D + 4 * row);
+                }
+                __builtin_amdgcn_sched_barrier(0);   // all of them go out before the first is used
+#pragma unroll
+                for (int j = 0; j < FLY; ++j) {
+                  const bool in = c0 + j * slices < count;
+                  float o[8];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[i] = in ? lo[j][i] : 0.0f, o[4 + i] = in ? hi[j][i] : 0.0f;
+                  merge(x, o, in ? mt[j][0] : -INFINITY, in ? mt[j][1] : 0.0f);
+                }
               }
-              __builtin_amdgcn_sched_barrier(0);     // all of them go out before the first is used
-#pragma unroll
-              for (int j = 0; j < FLY; ++j) {
-                const bool in = c0 + j * slices < count;
-                float o[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = in ? lo[j][i] : 0.0f, o[4 + i] = in ? hi[j][i] : 0.0f;
-                merge(x, o, in ? mt[j][0] : -INFINITY, in ? mt[j][1] : 0.0f);
-              }
-            }
+            };
+            if (D == 64 || count <= 8 * slices) take(std::integral_constant<int, 8>());
+            else take(std::integral_constant<int, D == 64 ? 8 : F32 || D == 256 ? 24 : 16>());
             if (slices == 1) finish(e, x);
           }
           if (slices == 1) continue;
