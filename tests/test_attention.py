@@ -1047,3 +1047,43 @@ def test_binding_refuses_what_is_no_tensor(gen):
             glq.attn_decode(cache, **dict(good, workspace=bad))
     with pytest.raises(glq.GlqError):
         glq.attn_prompt(k, k, k, k.clone(), cu[:0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_prompt_chunks_over_a_cached_prefix(gen, fmt, dtype):
+    # a prompt in chunks: each chunk's keys are appended, everything cached is read back
+    # through shuffled pages and seen by the chunk's queries; float32 inputs with all their bits
+    heads, kvh, dim, page, total = 6, 2, 128, 32, 330
+    cache = glq.KvCache.empty(14, page, kvh, dim, FORMATS[fmt])
+    table = torch.randperm(14, generator=gen)[:-(-total // page)]
+    at = torch.arange(total)
+    slots = (table[at // page] * page + at % page).to(torch.int32).cuda()
+    q = (_normal(gen, total, heads, dim) * 1.5).to(DTYPES[dtype])
+    k, v = (_normal(gen, total, kvh, dim).to(DTYPES[dtype]) for _ in range(2))
+    kk, vv = k, v
+    if fmt == "bf16":
+        kk, vv = (x.to(torch.bfloat16).float() for x in (k, v))
+    else:
+        def held(x):
+            x = x.float().numpy()
+            a, levels = np.abs(x).max(-1, keepdims=True), np.float32(LEVELS[fmt])
+            return torch.from_numpy(np.rint(x * levels / a) * (a / levels))
+        kk, vv = held(k), held(v)
+    kk, vv = kk.to(DTYPES[dtype]), vv.to(DTYPES[dtype])
+    first = 0
+    for n in (130, 1, 70, 2, 127):
+        end = first + n
+        glq.kv_append(cache, k[first:end].cuda(), v[first:end].cuda(), slots[first:end])
+        ko, vo = (torch.empty(end, kvh, dim, dtype=DTYPES[dtype], device="cuda") for _ in range(2))
+        glq.kv_read(cache, slots[:end], ko, vo)
+        assert torch.equal(ko.cpu(), kk[:end]) and torch.equal(vo.cpu(), vv[:end])
+        cu = [torch.tensor([0, x], dtype=torch.int32, device="cuda") for x in (n, end)]
+        out = _prompt(q[first:end].cuda(), ko, vo, *cu, max_q=n)
+        seen = torch.arange(end)[None] <= torch.arange(n)[:, None] + first
+        for h in range(heads):
+            ref, mag = _ref_attend(q[first:end, h], kk[:end, h // 3], vv[:end, h // 3], dim ** -0.5, seen)
+            _held(out[:, h], ref, mag, dtype, True)
+        first = end
+    assert first == total
