@@ -151,8 +151,10 @@ template <int LPR> __device__ __forceinline__ uint32_t row_max(uint32_t x) {
 // the scale. The quotient x Q / a comes from a's reciprocal r: y = xQ r, then y + (xQ
 // - y a) r, which is the correctly rounded quotient where r is the correctly
 // rounded reciprocal (Markstein); one division a lane instead of eight (16 ->
-// 11 us for 8192 tokens of 8 heads of 128 into 4 bits). What bounds it
-// then is the memory, and the launch for few tokens.
+// 11 us for 8192 tokens of 8 heads of 128 into 4 bits, the same ones again). What is left:
+// the launch for few tokens, and otherwise the memory's latency, with one row of a lane in flight:
+// those 8192 in 13.9 us from tensors that no cache holds (3.1 TB/s; 15.9, 4.2, to bf16), 50,001 in 59
+// (4.4; 76, 5.4).
 template <int FMT, int D>
 __device__ __forceinline__ void append_row(const KvIo &io, const KvPart<D> &p, int which, int at, const float *x) {
   uint8_t *out = reinterpret_cast<uint8_t *>(io.cache[which]) + p.cached * row_bytes<FMT>(D);
@@ -213,8 +215,10 @@ __global__ void __launch_bounds__(256) kv_append_k(KvIo io) {
 }
 
 // The other way: a slot outside the cache gives zeros. Bound by the memory: 50,001
-// tokens of 8 heads of 128 from 8 bits in 59.0 us, 5.3 TB/s; with stores that stay in the
-// caches 64.5, 4.8 TB/s, what a large copy reaches.
+// tokens of 8 heads of 128 from 8 bits to bf16 in 57 us, 5.4 TB/s, over several sets of tensors in
+// turn (the same set again, whose codes the 256 MB cache then holds: 45); with stores that stay in
+// the caches 64.5, 4.8 TB/s, what a large copy reaches. To float32 3.5 TB/s: a lane's 32 bytes
+// go out in two stores, half a line of the row each.
 template <int FMT, int D, bool F32>
 __global__ void __launch_bounds__(256) kv_read_k(KvIo io) {
   constexpr int WORDS = row_bytes<FMT>(D) / (D / 8) / 4;       // dwords a lane
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(256) kv_read_k(KvIo io) {
 
 // ------------------------------------------------------------ one new token
 
-constexpr int64_t kCus = 256;
+constexpr int64_t kCus = 256;                        // of an MI355X; only how work is shared out hangs on it
 constexpr int decode_per_cu(int dim, bool f32) {
   return dim == 256 ? 1 : dim == 128 ? (f32 ? 1 : 2) : f32 ? 2 : 3;
 }
@@ -455,8 +459,8 @@ __device__ __forceinline__ f32x4 load_shared(__amdgpu_buffer_rsrc_t r, int at) {
 // at most 2^8 of the largest one's base, add up to no more than 1/2: the sum of weights
 // times values is then no larger than the largest value, and a mean of finite values stays
 // finite. It costs nothing (one multiply-add where a multiplication was) and takes its bits from
-// where weights and values vanish. By the sequence's own number of keys, so that a result does not
-// depend on what else is in the call. `extra`: for operands larger than the values they stand for.
+// where weights and values vanish. By the sequence's own number of keys, not the call's bound on
+// it, on which a result should not depend. `extra`: for operands larger than the values they stand for.
 __device__ __forceinline__ float headroom_of(int keys, int extra = 0) {
   return (float)(9 + extra + (keys > 1 ? 32 - __builtin_clz((unsigned)(keys - 1)) : 0));
 }
@@ -490,8 +494,10 @@ __device__ __forceinline__ int length_of(const DecodeArgs &a, int b) {
 // Splitting costs a workgroup what some tiles take (its sums' way to memory, the
 // ticket, and their way back), so a unit that is no more than `spare` tiles
 // longer stays whole. Where there is a unit for every CU the memory is busy
-// anyway and the cost is paid in full: 32 x 2048 tokens, 8 kept heads, 8 bits: 28.6
-// us whole, 34.9 in halves; one sequence of 1024: 11.9 in eight parts, 13.0 in one.
+// anyway and the cost is paid in full, so that there the difference is 8 tiles, and 5 otherwise. 32
+// heads on 8 of 128, 8 bits but where said: one sequence of 256 6.8 us whole, 8.7 in parts; eight of 640
+// 10.2 and 12.3; 32 of 1024 in 4 bits 13.1 and 15.7; one of 1024 (8 tiles) 12.1 and 9.9. Against it:
+// heads of 256 would gain from 5 tiles on (one of 640 17.3 and 11.4).
 // Any value from 1 on is right; every workgroup computes the same one (the multiply-add is written
 // out, so that each copy of this rounds alike: find_place's last loop ends by it).
 __device__ __forceinline__ int parts_of(int tiles, float inv, int spare) {
@@ -535,9 +541,12 @@ __device__ __forceinline__ Place find_place(const DecodeArgs &a, int lane) {
     const int t = (len + 127) >> 7;
     const int most = __builtin_amdgcn_readlane(wave_scan<true>(t), 63);
     const int total = __builtin_amdgcn_readlane(wave_scan<false>(t), 63);
-    // One workgroup a CU streams as fast as two and splits less (one sequence of
-    // 8192, 8 bits: 14.4 us, 18.6 with two), unless that leaves the shares uneven
-    // (32 users of up to 4096: 48 us, 43 with two).
+    // One workgroup a CU streams as fast as two and splits less (heads of 128, one sequence of
+    // 8192, 8 bits: 11.7 us, 16.6 with two), unless that leaves the shares uneven (32 of up
+    // to 4096: 37.9 us, 33.4 with two). Only rows of 8 bits and more of heads of 128 (even_groups):
+    // 4 bits want the second one's VALU (two of up to 131,072: 56.7 us, 62.1 with one a CU; one of
+    // 8192, though, 14.3 and 11.0), heads of 64 have three (the same two in 8 bits 45.9 and 48.3, in
+    // 4 bits 39.4 and 50.7; one of 100,000 in bf16 44.1 and 37.9), heads of 256 have one.
     for (int64_t limit = min((int64_t)a.even_groups, groups);; limit = groups) {
       int lo = 0, hi = max(1, most);                 // shares: too small, large enough
       while (hi - lo > 1) {
@@ -1230,6 +1239,11 @@ __global__ void __launch_bounds__(256, (D < 256 ? 2 : 1)) attn_prompt_f32(Prompt
 // operand of O^T = V^T P^T as they stand if k-slot 4 i + r of half h means key 8 i +
 // 4 h + r. V^T's A operand in that order is two transposing LDS reads of 4 keys
 // each.
+//
+// Weights are rounded to bf16 for that product (8 bits; their total is summed before): the second
+// part that the decode kernel gives them would double one of the two products of a kernel that
+// waits for the matrix cores. Error against 64 bits: 0.0021 of the result's size, 0.0016 with
+// float32 weights, which is the result's own rounding.
 //
 // The products of a tile (1024 cycles of the matrix cores) and its softmax step (about
 // 980 of the VALU) are phases of their own; two workgroups share a CU and are rarely
@@ -1926,7 +1940,7 @@ extern "C" int glq_attn_decode(const glq_kv_cache *C, const void *q, glq_dtype d
                         scale2 == 0.0f ? 1.0f : fabsf(scale2), scale2 == 0.0f ? 0.0f : copysignf(1.0f, scale2),
                         (int32_t)batch, (int32_t)p.part_floats,
                         p.whole ? 1 : 0,
-                        // (4-bit operands want two workgroups a CU for their VALU work)
+                        // (where, and why: find_place)
                         C->head_dim == 128 && C->format != GLQ_KV_INT4 && p.groups >= kCus && p.units <= kCus
                             ? (int32_t)kCus : (int32_t)p.groups,
                         reinterpret_cast<unsigned int *>(workspace),

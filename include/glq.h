@@ -447,7 +447,7 @@ size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q
  *               and other entry points must not write there in between.
  * What lies in the cache past a sequence's length is never used, NaN among it.
  * Values may be of any finite size: the sums of weights are kept below 1, so that no
- * sum overflows. Where all values are below about 1e-27 in a quantised cache, or 1e-32,
+ * sum overflows (an infinite value gives an infinity or NaN). Where all values are below about 1e-27 in a quantised cache, or 1e-32,
  * they come out with fewer bits. Scores are float32: one that overflows to +inf gives
  * NaN, one of -inf no weight, and a row of -inf alone zeros.
  * Results do not depend on the order in which workgroups finish. q_heads must be
