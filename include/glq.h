@@ -439,7 +439,8 @@ size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q
  *               launch is sized by it.
  *   scale       finite, and times log2(e) too (below 2.35e38)
  *   dt          GLQ_BF16: the weights are taken as sums of two bf16 values (16 bits)
- *               for the matrix cores; GLQ_F32: q and the weights as sums of three,
+ *               for the matrix cores, 4-bit codes with a bias of 24 that is taken off again
+ *               (rounding of about 1e-6 of a row's largest value); GLQ_F32: q and the weights as sums of three,
  *               so every product is that of float32 operands. Sums are float32.
  *   workspace   device, 256-byte aligned. Its first GLQ_ATTN_CTRL_BYTES must be zero
  *               before the first call with it and are left zero by every call whose

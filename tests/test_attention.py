@@ -1087,3 +1087,41 @@ def test_prompt_chunks_over_a_cached_prefix(gen, fmt, dtype):
             _held(out[:, h], ref, mag, dtype, True)
         first = end
     assert first == total
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,lens_q,lens_k,heads", [("bf16", [30, 4], [700, 400], 4), ("bf16", [100, 28], [100, 28], 4),
+                                                       ("f32", [50, 20], [80, 20], 4), ("f32", [600, 500], [600, 500], 64)])
+def test_prompt_and_cache_in_a_graph(gen, dtype, lens_q, lens_k, heads):
+    # a captured chunk: write, read back and attention, replayed with other inputs in the same tensors
+    # and eager work between, against the eager calls; on a stream that is not the tensors' own
+    kvh, dim, page = 2, 64, 16
+    q, k, v, cu_q, cu_k, _, _ = _prompt_case(gen, lens_q, lens_k, heads, kvh, dim, dtype, True)
+    n = k.shape[0]
+    cache = glq.KvCache.empty(-(-n // page), page, kvh, dim, glq.KV_INT8)
+    slots = _slots(gen, n, -(-n // page) * page).cuda()
+    ko, vo, out = torch.empty_like(k), torch.empty_like(v), torch.empty_like(q)
+
+    def step():
+        glq.kv_append(cache, k, v, slots)
+        glq.kv_read(cache, slots, ko, vo)
+        glq.attn_prompt(q, ko, vo, out, cu_q, cu_k, max_q=max(lens_q))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        k.copy_((k.float() * 0.9 + 0.1).to(k.dtype))
+        q.copy_(q.flip(0))
+        out.zero_(), ko.zero_(), vo.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (out, ko, vo)]
+        out.zero_(), ko.zero_(), vo.zero_()
+        step()
+        assert all(torch.equal(a, b) for a, b in zip(got, (out, ko, vo))) and out.any()
