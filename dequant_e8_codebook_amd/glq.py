@@ -255,16 +255,21 @@ def _torch():
     return torch
 
 
+# the current stream without an object for it, the current device without torch's own checks (0.1 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream_ptr(stream, device):
     """The stream's handle (the current one's unless given). A launch goes to the current
     device, whatever the tensors are on, so that has to be theirs, and the stream's."""
-    torch = _torch()
-    if torch.cuda.current_device() != device.index:
-        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
-    s = stream if stream is not None else torch.cuda.current_stream()
-    if stream is not None and s.device != device:
-        raise ValueError(f"stream: on {s.device}, expected {device}")
-    return ctypes.c_void_p(s.cuda_stream)
+    if _current_device() != device.index:
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{_current_device()}")
+    if stream is None:
+        return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream().cuda_stream
+    if stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, expected {device}")
+    return stream.cuda_stream
 
 
 def _dtype_code(t) -> int:
@@ -652,14 +657,6 @@ class KvCache:
 # These calls are as short as a few microseconds on the GPU, so what they check
 # is read from the tensors once, in the order that a right call passes quickest.
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the current stream without an object for it
-
-
-def _stream_on(device, stream):
-    if stream is None and _raw_stream is not None and torch.cuda.current_device() == device.index:
-        return _raw_stream(device.index)
-    return _stream_ptr(stream, device)
-
 
 def _rows(t, name, device, dtype, total, heads, dim):
     """A [total, heads, head_dim] operand: heads dense, rows any 16-byte multiple
@@ -690,7 +687,10 @@ def _ints(t, name, device, *shape):
 
 
 def _last_size(t):                                   # (-1: what _ints refuses)
-    return t.shape[-1] if isinstance(t, torch.Tensor) and t.dim() else -1
+    try:
+        return t.shape[-1]
+    except (AttributeError, IndexError):
+        return -1
 
 
 _ATTN_DTYPES = {torch.float32: GLQ_F32, torch.bfloat16: GLQ_BF16}
@@ -714,7 +714,7 @@ def kv_append(cache: KvCache, k, v, slots, stream=None):
     cache at int32 slots [tokens] (page * page_size + row; a slot outside the
     cache drops its token) (glq_kv_append)."""
     dt, kp, ks, vp, vs, sp, total = _kv_args(cache, k, v, slots)
-    _check(_lib.glq_kv_append(cache._ref, kp, vp, dt, ks, vs, sp, total, _stream_on(cache.device, stream)),
+    _check(_lib.glq_kv_append(cache._ref, kp, vp, dt, ks, vs, sp, total, _stream_ptr(stream, cache.device)),
            "glq_kv_append")
 
 
@@ -722,7 +722,7 @@ def kv_read(cache: KvCache, slots, k, v, stream=None):
     """Read the tokens at the slots back into k and v [tokens, kv_heads,
     head_dim], float32 or bfloat16 (glq_kv_read)."""
     dt, kp, ks, vp, vs, sp, total = _kv_args(cache, k, v, slots)
-    _check(_lib.glq_kv_read(cache._ref, sp, total, kp, vp, dt, ks, vs, _stream_on(cache.device, stream)),
+    _check(_lib.glq_kv_read(cache._ref, sp, total, kp, vp, dt, ks, vs, _stream_ptr(stream, cache.device)),
            "glq_kv_read")
     return k, v
 
@@ -748,7 +748,7 @@ def attn_decode(cache: KvCache, q, page_table, lens, out, workspace, max_len: in
         raise ValueError(f"workspace: must be contiguous on {dev}")
     rc = _lib.glq_attn_decode(cache._ref, qp, dt, qs, batch, heads, tp, pages, lp, max_len,
                               dim ** -0.5 if scale is None else scale, op, os_, workspace.data_ptr(), workspace.nbytes,
-                              _stream_on(dev, stream))
+                              _stream_ptr(stream, dev))
     _check(rc, "glq_attn_decode")
     return out
 
@@ -775,6 +775,6 @@ def attn_prompt(q, k, v, out, cu_q, cu_k=None, max_q: int | None = None, causal:
     ck = cq if cu_k is None else _ints(cu_k, "cu_k", dev, batch + 1)
     st = PromptStruct(qp, kp, vp, op, dt, heads, kvh, dim, qs, ks, vs, os_, total_q, total_k, batch, cq, ck,
                       total_q if max_q is None else max_q, dim ** -0.5 if scale is None else scale)
-    _check(_lib.glq_attn_prompt(ctypes.byref(st), ATTN_CAUSAL if causal else 0, _stream_on(dev, stream)),
+    _check(_lib.glq_attn_prompt(ctypes.byref(st), ATTN_CAUSAL if causal else 0, _stream_ptr(stream, dev)),
            "glq_attn_prompt")
     return out

@@ -954,7 +954,7 @@ def test_attention_refuses_another_device(gen, monkeypatch):
         with pytest.raises(ValueError, match="stream"):
             call(stream=Elsewhere())
     torch.cuda.synchronize()
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(glq, "_current_device", lambda: 1)
     for call in calls:
         with pytest.raises(ValueError, match="current device"):
             call()

@@ -1037,7 +1037,7 @@ def test_calls_refuse_another_device(G, cb, monkeypatch):
         with pytest.raises(ValueError, match="stream"):
             call(stream=Elsewhere())
     torch.cuda.synchronize()
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(G, "_current_device", lambda: 1)
     for call in calls:
         with pytest.raises(ValueError, match="current device"):
             call()
