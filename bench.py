@@ -52,14 +52,17 @@ sys.path.insert(0, ROOT)
 
 HBM_PEAK_GBS = 8000.0
 MFMA_BF16_PEAK_TFLOPS = 2500.0
-KERNEL_SRC = os.path.join(ROOT, "dequant_e8_codebook_amd", "csrc", "glq_kernels.hip")
+KERNEL_SRCS = [os.path.join(ROOT, "dequant_e8_codebook_amd", "csrc", f) for f in ("glq_decode.h", "glq_kernels.hip")]
 PROFILE_DIR = os.path.join(ROOT, "profiles")
 COPY_BYTES = 256 << 20
 
 
 def kernel_source_hash() -> str:
-    with open(KERNEL_SRC, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+    h = hashlib.sha256()
+    for p in KERNEL_SRCS:
+        with open(p, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
 
 
 def _profile_path(workload):

@@ -4,6 +4,7 @@ Usage: python -m dequant_e8_codebook_amd.build
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
@@ -31,18 +32,17 @@ def _run(cmd):
 def build(verbose: bool = True) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(BUILD_DIR, exist_ok=True)
-    objs = []
+    objs, jobs = [], []
     common = ["-std=c++17", "-fPIC", "-I" + INC, "-I" + CSRC]
-    for src in HOST_SOURCES:
+    for src in HIP_SOURCES + HOST_SOURCES:
         obj = os.path.join(BUILD_DIR, src + ".o")
-        _run(["g++", "-O2", "-Wall", "-pthread"] + common + ["-c", os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
-    for src in HIP_SOURCES:
-        obj = os.path.join(BUILD_DIR, src + ".o")
-        _run([HIPCC, "-O3", "--offload-arch=" + ARCH,
-              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
-             + common + ["-c", os.path.join(CSRC, src), "-o", obj])
-        objs.append(obj)
+        how = (["g++", "-O2", "-Wall", "-pthread"] if src in HOST_SOURCES else
+               [HIPCC, "-O3", "--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"])
+        jobs.append(how + common + ["-c", os.path.join(CSRC, src), "-o", obj])
+    # one compiler a source, the slowest first: the sources are few
+    with concurrent.futures.ThreadPoolExecutor(len(jobs)) as pool:
+        list(pool.map(_run, jobs))
     tmp = LIB + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-pthread", "-o", tmp] + objs)
     os.replace(tmp, LIB)
