@@ -1,0 +1,640 @@
+// glq_step.hip -- what a serving step does around the compressed linears and the
+// paged cache (gfx950), and its entry points of the C ABI.
+//
+// Kernels:
+//   kv_plan_k        request lengths -> pages taken, slots, positions, offsets
+//   qk_norm_rope_k   norms of query and key heads, rotation, write into the cache
+//   route_pick_k     router scores -> each token's experts and weights
+//   route_place_k    rows in the experts' order, for more tokens than one workgroup takes
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "glq.h"
+#include "glq_cache.h"
+
+namespace glq {
+namespace {
+
+// Largest of x over the 64 lanes of a wave, in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = row_max<32>(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return r[0] > r[1] ? r[0] : r[1];
+}
+
+// Sum of x over LPR lanes (8, 16, 32 or 64 of them in a row), in every one of them.
+template <int LPR> __device__ __forceinline__ float lanes_sum(float x) {
+  auto moved = [](float v, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  x += moved(x, std::integral_constant<int, 0xB1>());          // quad_perm: lane ^ 1, lane ^ 2
+  x += moved(x, std::integral_constant<int, 0x4E>());
+  x += moved(x, std::integral_constant<int, 0x141>());         // half row mirror: the other four
+  if constexpr (LPR >= 16) x += moved(x, std::integral_constant<int, 0x140>());   // row mirror
+  if constexpr (LPR >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (LPR == 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return x;
+}
+
+// ------------------------------------------------------------ pages and slots
+
+struct PlanArgs {
+  const int32_t *lens, *added, *free_pages;
+  int32_t *table, *new_lens, *cu_q, *slots, *positions, *cu_k, *read_slots, *used;
+  int64_t batch, max_pages, num_free, num_pages, max_tokens, max_read;
+  int32_t page_shift;
+  uint32_t q_tiles, r_tiles, p_groups;     // workgroups of the three lists
+};
+
+constexpr int kPlanThreads = 256, kPlanTile = 2048, kPlanChunk = 1024;
+
+enum PlanList { kNew, kRead, kPages };
+
+// Every workgroup writes one tile of one of three lists: the new tokens' slots
+// and positions, all cached tokens' slots, the pages taken. It sums up the requests'
+// counts itself (1024 requests at a time, in 64 bits), which costs less than a
+// launch that would do it for all; an entry finds its request by bisection in
+// LDS. A page taken in this call is read from the list of free pages, never
+// from the table, so no workgroup waits for another.
+struct PlanShared {
+  int64_t begin[kPlanChunk], taken[kPlanChunk];      // entries of the list and pages before a request
+  int32_t len[kPlanChunk], held[kPlanChunk];
+  int64_t wave_sum[2][kPlanThreads / 64];
+};
+
+// Returns the number of entries that the list has in all (the tokens lists: counted as far as the tile).
+template <PlanList LIST>
+__device__ __forceinline__ int64_t plan_tile(const PlanArgs &a, PlanShared &sh, int64_t tile, bool first) {
+  auto &begin = sh.begin, &taken = sh.taken;
+  auto &len = sh.len, &held = sh.held;
+  auto &wave_sum = sh.wave_sum;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t most = LIST == kNew ? a.max_tokens : LIST == kRead ? a.max_read : INT64_MAX;
+  const int64_t t0 = tile * kPlanTile;
+  int64_t t1 = t0 + kPlanTile < most ? t0 + kPlanTile : most;
+  const int64_t page = int64_t(1) << a.page_shift;
+  auto pages_of = [&](int64_t tokens) {
+    const int64_t p = (tokens + page - 1) >> a.page_shift;
+    return p < a.max_pages ? p : a.max_pages;
+  };
+  int64_t before = 0, pages_before = 0;                        // of the chunks behind
+  for (int64_t c = 0; c < a.batch; c += kPlanChunk) {
+    if (LIST != kPages && !first && before >= t1) break;       // uniform
+    int64_t n[4], p[4], nsum = 0, psum = 0;
+    int32_t l[4], h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t b = c + 4 * tid + i;
+      const int64_t have = b < a.batch && a.lens[b] > 0 ? a.lens[b] : 0, add = b < a.batch && a.added[b] > 0 ? a.added[b] : 0;
+      const int64_t ph = pages_of(have), pt = pages_of(have + add);
+      l[i] = (int32_t)have;
+      h[i] = (int32_t)ph;
+      p[i] = psum;
+      n[i] = nsum;
+      psum += pt - ph;
+      nsum += LIST == kNew ? add : LIST == kRead ? have + add : pt - ph;
+      if (LIST == kNew && first && b < a.batch)
+        a.new_lens[b] = (int32_t)(have + add < INT32_MAX ? have + add : INT32_MAX);
+    }
+    int64_t nup = nsum, pup = psum;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int64_t x = __shfl_up(nup, s), y = __shfl_up(pup, s);
+      if (lane >= s) nup += x, pup += y;
+    }
+    __syncthreads();                                           // the chunk before is done with LDS
+    if (lane == 63) wave_sum[0][wave] = nup, wave_sum[1][wave] = pup;
+    __syncthreads();
+    int64_t nbase = before + nup - nsum, pbase = pages_before + pup - psum, ntotal = 0, ptotal = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 64; ++w) {
+      if (w < wave) nbase += wave_sum[0][w], pbase += wave_sum[1][w];
+      ntotal += wave_sum[0][w], ptotal += wave_sum[1][w];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = 4 * tid + i;
+      begin[at] = nbase + n[i];
+      taken[at] = pbase + p[i];
+      len[at] = l[i];
+      held[at] = h[i];
+      if (LIST != kPages && first && c + at < a.batch) {
+        int32_t *cu = LIST == kNew ? a.cu_q : a.cu_k;
+        cu[c + at] = (int32_t)(nbase + n[i] < most ? nbase + n[i] : most);
+      }
+    }
+    __syncthreads();
+    const int64_t end = before + ntotal < t1 ? before + ntotal : t1;
+    for (int64_t i = (t0 > before ? t0 : before) + tid; i < end; i += kPlanThreads) {
+      int at = 0;                                              // the last request that begins at i or before
+#pragma unroll
+      for (int s = kPlanChunk / 2; s; s >>= 1)
+        if (begin[at + s] <= i) at += s;
+      const int64_t b = c + at, nth = i - begin[at];
+      if constexpr (LIST == kPages) {
+        a.table[b * a.max_pages + held[at] + nth] = i < a.num_free ? a.free_pages[i] : -1;
+      } else {
+        const int64_t t = LIST == kNew ? len[at] + nth : nth, e = t >> a.page_shift;
+        int32_t pg = -1;
+        if (e < held[at]) {
+          pg = a.table[b * a.max_pages + e];
+        } else if (e < a.max_pages) {
+          const int64_t f = taken[at] + e - held[at];
+          if (f < a.num_free) pg = a.free_pages[f];
+        }
+        const int32_t slot = pg >= 0 && pg < a.num_pages ? (pg << a.page_shift) + (int32_t)(t & (page - 1)) : -1;
+        if constexpr (LIST == kNew) {
+          a.slots[i] = slot;
+          a.positions[i] = (int32_t)(t < INT32_MAX ? t : INT32_MAX);
+        } else {
+          a.read_slots[i] = slot;
+        }
+      }
+    }
+    before += ntotal;
+    pages_before += ptotal;
+  }
+  if constexpr (LIST == kPages) {
+    if (first && tid == 0) *a.used = (int32_t)(before < INT32_MAX ? before : INT32_MAX);
+  } else {
+    if (first && tid == 0) (LIST == kNew ? a.cu_q : a.cu_k)[a.batch] = (int32_t)(before < most ? before : most);
+    for (int64_t i = (t0 > before ? t0 : before) + tid; i < t1; i += kPlanThreads) {   // behind the last token
+      if constexpr (LIST == kNew) a.slots[i] = -1, a.positions[i] = 0;
+      else a.read_slots[i] = -1;
+    }
+  }
+  return before;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_k(PlanArgs a) {
+  __shared__ PlanShared sh;
+  const uint32_t g = blockIdx.x;
+  if (g < a.q_tiles) {
+    plan_tile<kNew>(a, sh, g, g == 0);
+  } else if (g < a.q_tiles + a.r_tiles) {
+    plan_tile<kRead>(a, sh, g - a.q_tiles, g == a.q_tiles);
+  } else {
+    // one tile each where no more than max_tokens are new; the lengths alone say how many pages there are
+    const int64_t mine = g - a.q_tiles - a.r_tiles;
+    for (int64_t tile = mine;; tile += a.p_groups)
+      if (plan_tile<kPages>(a, sh, tile, tile == 0) <= (tile + a.p_groups) * kPlanTile) break;
+  }
+}
+
+// ------------------------------------------------------------ head norms and rotation
+
+struct NormArgs {
+  const void *q, *k;
+  void *q_out, *k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  const float *q_weight, *k_weight, *rotary;
+  const int32_t *positions;
+  int64_t max_positions;
+  int64_t groups;                    // of D / 8 lanes
+  int32_t q_heads, heads, rot;       // heads: queries, keys, and values where there is a cache
+  float eps;
+  KvIo io;                           // the cache, and v as its dense[1]
+};
+
+constexpr int kNoCache = -1;
+
+// Lanes hold 8 elements of a head's row each, D / 8 lanes a row: the mean of squares is a
+// sum over those lanes, the partner of an element i of a half rotation (i + rot / 2) is
+// in the lane rot / 16 further, that of a pair rotation in the same lane. Values are float32
+// until the one rounding to the operands' type; the cache gets the rounded key, as
+// if it were appended afterwards. Bound by the memory.
+template <int FMT, int D, bool F32, bool PAIRS>
+__global__ void __launch_bounds__(256) qk_norm_rope_k(NormArgs a) {
+  constexpr int LPR = D / 8, ES = F32 ? 4 : 2;
+  const int64_t g = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+  if (g >= a.groups) return;                          // whole rows leave together
+  const int at = threadIdx.x % LPR;
+  const int64_t token = g / a.heads;
+  const int head = (int)(g - token * a.heads), kv_heads = a.io.heads;
+  const int which = head < a.q_heads ? 0 : head < a.q_heads + kv_heads ? 1 : 2;      // query, key, value
+  const int h = which == 0 ? head : head - a.q_heads - (which == 2 ? kv_heads : 0);
+  const uint8_t *from = which == 0 ? reinterpret_cast<const uint8_t *>(a.q) + ES * (token * a.q_stride + (int64_t)h * D)
+                        : which == 1 ? reinterpret_cast<const uint8_t *>(a.k) + ES * (token * a.k_stride + (int64_t)h * D)
+                        : reinterpret_cast<const uint8_t *>(a.io.dense[1]) + ES * (token * a.io.stride[1] + (int64_t)h * D);
+  float x[8];
+  load8<F32>(from + ES * 8 * at, x);
+  if (which < 2) {
+    const float *weight = which == 0 ? a.q_weight : a.k_weight;
+    if (weight) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+      s = lanes_sum<LPR>(s);
+      const float r = 1.0f / sqrtf(s / (float)D + a.eps);
+      float w[8];
+      load8<true>(weight + 8 * at, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= w[i] * r;
+    }
+    if (a.rot > 0) {
+      int64_t p = a.positions[token];
+      p = p < 0 ? 0 : p < a.max_positions ? p : a.max_positions - 1;
+      const float *row = a.rotary + p * a.rot;
+      const bool in = 8 * at < a.rot;
+      if constexpr (PAIRS) {
+        if (in) {
+          const float4 c = *reinterpret_cast<const float4 *>(row + 4 * at);
+          const float4 n = *reinterpret_cast<const float4 *>(row + a.rot / 2 + 4 * at);
+          const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {n.x, n.y, n.z, n.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float u = x[2 * i], v = x[2 * i + 1];
+            x[2 * i] = u * cs[i] - v * sn[i];
+            x[2 * i + 1] = v * cs[i] + u * sn[i];
+          }
+        }
+      } else {
+        const int half = a.rot / 16;                  // lanes of one half
+        const bool upper = at >= half;
+        const int other = in ? (upper ? threadIdx.x - half : threadIdx.x + half) : threadIdx.x;
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], other & 63);
+        if (in) {
+          const int f = 8 * (upper ? at - half : at);
+          float cs[8], sn[8];
+          load8<true>(row + f, cs);
+          load8<true>(row + a.rot / 2 + f, sn);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = upper ? x[i] * cs[i] + y[i] * sn[i] : x[i] * cs[i] - y[i] * sn[i];
+        }
+      }
+    }
+    if constexpr (!F32) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const uint32_t u = pack_bf16(x[i], x[i + 1]);
+        x[i] = bf16_lo(u), x[i + 1] = bf16_hi(u);
+      }
+    }
+    uint8_t *to = reinterpret_cast<uint8_t *>(which == 0 ? a.q_out : a.k_out);
+    if (to) store8<F32>(to + ES * (token * (which == 0 ? a.q_out_stride : a.k_out_stride) + (int64_t)h * D + 8 * at), x);
+  }
+  if constexpr (FMT != kNoCache) {
+    if (which > 0) {
+      KvPart<D> part;
+      part.slot = (uint32_t)a.io.slots[token];
+      if (part.slot < a.io.capacity) {
+        const uint32_t pg = part.slot >> a.io.page_shift, in_page = part.slot & ((1u << a.io.page_shift) - 1);
+        part.cached = (((int64_t)pg * kv_heads + h) << a.io.page_shift) + in_page;
+        append_row<FMT, D>(a.io, part, which - 1, at, x);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ routing
+
+struct RouteArgs {
+  const void *logits;
+  int64_t tokens, blocks;
+  int32_t experts, top;
+  int32_t normalize;
+  float *weights;
+  int32_t *ids, *pos, *src, *offsets, *counts;     // counts [blocks][experts], workspace
+};
+
+constexpr int kRouteTokens = 64, kRouteThreads = 1024, kRouteMost = 1024;
+
+// Order of scores as unsigned numbers, 0 for those that choose nothing (-inf, NaN); both zeros are one.
+__device__ __forceinline__ uint32_t score_order(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  if (!(x > -INFINITY)) return 0u;
+  return (int32_t)u < 0 ? ~u : u | 0x80000000u;
+}
+
+// Exclusive sums of one number a thread over the workgroup's threads; total in *sum.
+__device__ __forceinline__ int32_t group_before(int32_t x, int32_t *sum) {
+  __shared__ int32_t part[kRouteThreads / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int32_t up = x;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const int32_t y = __shfl_up(up, s);
+    if (lane >= s) up += y;
+  }
+  if (lane == 63) part[wave] = up;
+  __syncthreads();
+  int32_t base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kRouteThreads / 64; ++w) {
+    if (w < wave) base += part[w];
+    all += part[w];
+  }
+  *sum = all;
+  return base + up - x;
+}
+
+// A wave takes a token, its lanes experts lane, lane + 64, ...: `top` times the largest
+// score left, the lowest index among equals. 64 tokens a workgroup: who chose an
+// expert is a mask of 64 bits in LDS (or-ed in any order, the same whatever it is), so
+// a choice's place among the workgroup's is the number of lower bits, and nothing
+// depends on which wave comes first. One workgroup alone (up to 64 tokens) goes on
+// to the rows itself: one launch.
+template <int NV, bool F32>
+__global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
+  __shared__ unsigned long long chose[kRouteMost];
+  __shared__ int32_t first[kRouteMost];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e < a.experts; e += kRouteThreads) chose[e] = 0;
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens;
+  constexpr int PER = kRouteTokens / (kRouteThreads / 64);     // tokens a wave
+  int32_t mine[PER];                                           // lane j: the token's choice j
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int in = wave * PER + i;
+    const int64_t t = t0 + in;
+    mine[i] = -1;
+    if (t >= a.tokens) continue;                               // uniform
+    float x[NV];
+    uint32_t order[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = lane + 64 * v;
+      x[v] = -INFINITY;
+      if (e < a.experts) {
+        const size_t o = (size_t)t * a.experts + e;
+        x[v] = F32 ? reinterpret_cast<const float *>(a.logits)[o]
+                   : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(a.logits)[o] << 16);
+      }
+      order[v] = score_order(x[v]);
+    }
+    float value = -INFINITY, peak = 0.0f;
+    for (int j = 0; j < a.top; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) best = order[v] > best ? order[v] : best;
+      best = wave_max(best);
+      if (best == 0) break;                                    // uniform
+      uint32_t far = 0;                                        // kRouteMost - index: the largest is the lowest index
+#pragma unroll
+      for (int v = NV - 1; v >= 0; --v) far = order[v] == best ? kRouteMost - (lane + 64 * v) : far;
+      const int e = kRouteMost - (int)wave_max(far);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (lane + 64 * v == e) order[v] = 0;
+      const float s = __uint_as_float((int32_t)best < 0 ? best & 0x7FFFFFFFu : ~best);
+      if (j == 0) peak = s;
+      if (lane == j) mine[i] = e, value = s;
+    }
+    const float w = mine[i] >= 0 ? expf(value - peak) : 0.0f;
+    float sum = 0.0f;
+    if (a.normalize) {
+      sum = w;
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) sum += x[v] > -INFINITY ? expf(x[v] - peak) : 0.0f;
+    }
+    sum = lanes_sum<64>(sum);
+    if (lane < a.top) {
+      a.weights[t * a.top + lane] = mine[i] >= 0 ? w / sum : 0.0f;
+      a.ids[t * a.top + lane] = mine[i];
+    }
+    if (mine[i] >= 0) atomicOr(&chose[mine[i]], 1ull << in);
+  }
+  __syncthreads();
+  const bool alone = gridDim.x == 1;
+  int32_t total = 0;
+  if (alone) {
+    const int32_t count = tid < a.experts ? __popcll(chose[tid]) : 0;
+    const int32_t before = group_before(count, &total);
+    if (tid < a.experts) {
+      first[tid] = before;
+      a.offsets[tid] = before;
+    }
+    if (tid == 0) a.offsets[a.experts] = total;
+    __syncthreads();
+  } else {
+    for (int e = tid; e < a.experts; e += kRouteThreads)
+      a.counts[(size_t)blockIdx.x * a.experts + e] = __popcll(chose[e]);
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int in = wave * PER + i;
+    const int64_t t = t0 + in;
+    if (t >= a.tokens || lane >= a.top) continue;
+    int32_t at = -1;
+    if (mine[i] >= 0) {
+      at = __popcll(chose[mine[i]] & ((1ull << in) - 1));
+      if (alone) {
+        at += first[mine[i]];
+        a.src[at] = (int32_t)t;
+      }
+    }
+    a.pos[t * a.top + lane] = at;
+  }
+  if (alone)
+    for (int64_t r = total + tid; r < a.tokens * a.top; r += kRouteThreads) a.src[r] = -1;
+}
+
+// Rows of one workgroup's tokens: those of earlier workgroups and of earlier experts come
+// before. Every workgroup adds up all counts (128 by 128 of them for 8192 tokens and
+// 128 experts, from L2), instead of a launch between the two that would.
+__global__ void __launch_bounds__(kRouteThreads) route_place_k(RouteArgs a) {
+  __shared__ int32_t sums[2][kRouteThreads];                   // before this workgroup's, and all
+  __shared__ int32_t first[kRouteMost];
+  const int tid = threadIdx.x;
+  int width = 1;                                               // experts up to a power of two
+  while (width < a.experts) width <<= 1;
+  const int parts = kRouteThreads / width, e = tid & (width - 1), part = tid / width;
+  int32_t before = 0, all = 0;
+  if (e < a.experts)
+    for (int64_t b = part; b < a.blocks; b += parts) {
+      const int32_t n = a.counts[b * a.experts + e];
+      all += n;
+      if (b < (int64_t)blockIdx.x) before += n;
+    }
+  sums[0][tid] = before, sums[1][tid] = all;
+  __syncthreads();
+  if (tid < width) {
+    before = all = 0;
+    for (int p = 0; p < parts; ++p) before += sums[0][tid + p * width], all += sums[1][tid + p * width];
+  } else {
+    before = all = 0;
+  }
+  int32_t total;
+  const int32_t start = group_before(all, &total);
+  if (tid < a.experts) {
+    first[tid] = start + before;
+    if (blockIdx.x == 0) a.offsets[tid] = start;
+  }
+  if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = total;
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens;
+  const int64_t n = (a.tokens - t0 < kRouteTokens ? a.tokens - t0 : kRouteTokens) * a.top;
+  for (int64_t i = tid; i < n; i += kRouteThreads) {
+    const int64_t o = t0 * a.top + i;
+    const int32_t id = a.ids[o];
+    if (id < 0) continue;
+    const int32_t at = a.pos[o] + first[id];
+    a.pos[o] = at;
+    a.src[at] = (int32_t)(o / a.top);
+  }
+  for (int64_t r = total + (int64_t)blockIdx.x * kRouteThreads + tid; r < a.tokens * a.top;
+       r += (int64_t)gridDim.x * kRouteThreads)
+    a.src[r] = -1;
+}
+
+// ------------------------------------------------------------ argument checks and launches
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+template <int FMT, int D, bool F32>
+int launch_norm(const NormArgs &a, bool pairs, hipStream_t st) {
+  const int64_t blocks = (a.groups * (D / 8) + 255) / 256;
+  if (blocks > kMaxGroups) return GLQ_ERR_UNSUPPORTED;
+  auto kern = pairs ? qk_norm_rope_k<FMT, D, F32, true> : qk_norm_rope_k<FMT, D, F32, false>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, st, a);
+  return hip_status(hipGetLastError(), "qk_norm_rope_k");
+}
+
+template <int FMT>
+int launch_norm_dim(const NormArgs &a, int d, glq_dtype dt, bool pairs, hipStream_t st) {
+  if (dt == GLQ_F32)
+    return d == 64 ? launch_norm<FMT, 64, true>(a, pairs, st) : d == 128 ? launch_norm<FMT, 128, true>(a, pairs, st)
+                                                                         : launch_norm<FMT, 256, true>(a, pairs, st);
+  return d == 64 ? launch_norm<FMT, 64, false>(a, pairs, st) : d == 128 ? launch_norm<FMT, 128, false>(a, pairs, st)
+                                                                        : launch_norm<FMT, 256, false>(a, pairs, st);
+}
+
+int check_route(int64_t tokens, int32_t experts, int32_t top) {
+  if (tokens < 0 || experts < 1 || top < 1 || top > experts) return GLQ_ERR_ARG;
+  if (experts > kRouteMost || top > 64 || tokens > 0x7FFFFFFF / 64) return GLQ_ERR_UNSUPPORTED;
+  return GLQ_OK;
+}
+
+int64_t route_blocks(int64_t tokens) { return (tokens + kRouteTokens - 1) / kRouteTokens; }
+
+template <int NV>
+void launch_pick(const RouteArgs &a, glq_dtype dt, hipStream_t st) {
+  if (dt == GLQ_F32) hipLaunchKernelGGL((route_pick_k<NV, true>), dim3((unsigned)a.blocks), dim3(kRouteThreads), 0, st, a);
+  else hipLaunchKernelGGL((route_pick_k<NV, false>), dim3((unsigned)a.blocks), dim3(kRouteThreads), 0, st, a);
+}
+
+}  // namespace
+}  // namespace glq
+
+using namespace glq;
+
+extern "C" int glq_kv_plan(const glq_plan *P, void *hip_stream) {
+  if (!P || P->batch < 0 || P->max_pages < 1 || P->num_pages < 1 || P->num_free < 0 || P->max_tokens < 0 || P->max_read < 0)
+    return GLQ_ERR_ARG;
+  if (P->page_size < 16 || P->page_size > 1024 || (P->page_size & (P->page_size - 1))) return GLQ_ERR_ARG;
+  const bool read = P->max_read > 0 || P->read_slots || P->cu_k;
+  if (!P->cu_q || !P->used || (P->batch > 0 && (!P->lens || !P->added || !P->page_table || !P->new_lens))) return GLQ_ERR_ARG;
+  if (P->num_free > 0 && !P->free_pages) return GLQ_ERR_ARG;
+  if (P->max_tokens > 0 && (!P->slots || !P->positions)) return GLQ_ERR_ARG;
+  if (read && (!P->cu_k || (P->max_read > 0 && !P->read_slots))) return GLQ_ERR_ARG;
+  const void *const words[] = {P->lens, P->added, P->free_pages, P->page_table, P->new_lens, P->cu_q,
+                               P->slots, P->positions, P->cu_k, P->read_slots, P->used};
+  for (const void *p : words)
+    if (!aligned4(p)) return GLQ_ERR_ARG;
+  if (P->batch > 0 && (P->new_lens == P->lens || P->new_lens == P->added)) return GLQ_ERR_ARG;
+  if (P->num_pages > 0x7FFFFFFF / P->page_size || P->max_pages > 0x7FFFFFFF / P->page_size ||
+      P->max_tokens > 0x7FFFFFFF || P->max_read > 0x7FFFFFFF || P->num_free > 0x7FFFFFFF || P->batch > 0x7FFFFFFF ||
+      (P->batch > 0 && P->max_pages > (int64_t(1) << 40) / P->batch))
+    return GLQ_ERR_UNSUPPORTED;
+  auto tiles = [](int64_t n) { return (uint32_t)((n + kPlanTile - 1) / kPlanTile); };
+  PlanArgs a = {P->lens, P->added, P->free_pages, P->page_table, P->new_lens, P->cu_q, P->slots, P->positions, P->cu_k,
+                P->read_slots, P->used, P->batch, P->max_pages, P->num_free, P->num_pages, P->max_tokens, P->max_read,
+                log2_of(P->page_size), 1, 0, 0};
+  if (P->max_tokens > 0) a.q_tiles = tiles(P->max_tokens);
+  if (read) a.r_tiles = P->max_read > 0 ? tiles(P->max_read) : 1;
+  // pages that max_tokens new ones can take
+  const int64_t pages = P->max_tokens / P->page_size + P->batch;
+  a.p_groups = pages > 0 ? tiles(pages < P->batch * P->max_pages ? pages : P->batch * P->max_pages) : 1;
+  const int64_t groups = (int64_t)a.q_tiles + a.r_tiles + a.p_groups;
+  if (groups > kMaxGroups) return GLQ_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(kv_plan_k, dim3((unsigned)groups), dim3(kPlanThreads), 0, reinterpret_cast<hipStream_t>(hip_stream), a);
+  return hip_status(hipGetLastError(), "kv_plan_k");
+}
+
+extern "C" int glq_qk_norm_rope(const glq_qk *N, const glq_kv_cache *C, uint32_t flags, void *hip_stream) {
+  if (!N || (flags & ~(uint32_t)GLQ_ROPE_PAIRS) || !valid_dtype(N->dt) || N->tokens < 0) return GLQ_ERR_ARG;
+  if (N->q_heads < 1 || N->kv_heads < 1 || N->rotary_dim < 0 || N->rotary_dim > N->head_dim) return GLQ_ERR_ARG;
+  if (!std::isfinite(N->eps) || N->eps < 0.0f) return GLQ_ERR_ARG;
+  if (!valid_dim(N->head_dim) || N->rotary_dim % 16 || N->q_heads > 65536 || N->kv_heads > 65536) return GLQ_ERR_UNSUPPORTED;
+  if (C) {
+    const int rc = check_cache(C);
+    if (rc) return rc;
+    if (C->kv_heads != N->kv_heads || C->head_dim != N->head_dim) return GLQ_ERR_ARG;
+  }
+  if (N->tokens == 0) return GLQ_OK;
+  const int d = N->head_dim;
+  if (!valid_rows(N->q, N->q_stride, N->q_heads, d, N->dt) || !valid_rows(N->q_out, N->q_out_stride, N->q_heads, d, N->dt) ||
+      !valid_rows(N->k, N->k_stride, N->kv_heads, d, N->dt))
+    return GLQ_ERR_ARG;
+  if ((N->k_out || !C) && !valid_rows(N->k_out, N->k_out_stride, N->kv_heads, d, N->dt)) return GLQ_ERR_ARG;
+  if (C && (!valid_rows(N->v, N->v_stride, N->kv_heads, d, N->dt) || !N->slots || !aligned4(N->slots))) return GLQ_ERR_ARG;
+  if (!aligned16(N->q_weight) || !aligned16(N->k_weight)) return GLQ_ERR_ARG;
+  if (N->rotary_dim > 0 && (!N->positions || !aligned4(N->positions) || !N->rotary || !aligned16(N->rotary) || N->max_positions < 1))
+    return GLQ_ERR_ARG;
+  const int64_t heads = (int64_t)N->q_heads + N->kv_heads * (C ? 2 : 1);
+  if (N->tokens > (int64_t(1) << 40) / heads) return GLQ_ERR_UNSUPPORTED;
+  NormArgs a = {N->q, N->k, N->q_out, N->k_out, N->q_stride, N->k_stride, N->q_out_stride, N->k_out_stride,
+                N->q_weight, N->k_weight, N->rotary, N->positions, N->max_positions, N->tokens * heads,
+                N->q_heads, (int32_t)heads, N->rotary_dim, N->eps, {}};
+  a.io.heads = N->kv_heads;
+  const glq_dtype dt = (glq_dtype)N->dt;
+  const bool pairs = flags & GLQ_ROPE_PAIRS;
+  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  if (!C) return launch_norm_dim<kNoCache>(a, d, dt, pairs, st);
+  a.io.cache[0] = C->k, a.io.cache[1] = C->v;
+  a.io.scale[0] = C->k_scale, a.io.scale[1] = C->v_scale;
+  a.io.dense[1] = const_cast<void *>(N->v), a.io.stride[1] = N->v_stride;
+  a.io.slots = N->slots;
+  a.io.page_shift = log2_of(C->page_size), a.io.capacity = (uint32_t)(C->num_pages * C->page_size);
+  switch (C->format) {
+    case GLQ_KV_BF16: return launch_norm_dim<GLQ_KV_BF16>(a, d, dt, pairs, st);
+    case GLQ_KV_INT8: return launch_norm_dim<GLQ_KV_INT8>(a, d, dt, pairs, st);
+    default: return launch_norm_dim<GLQ_KV_INT4>(a, d, dt, pairs, st);
+  }
+}
+
+extern "C" size_t glq_route_workspace(int64_t tokens, int32_t experts, int32_t top_k) {
+  if (check_route(tokens, experts, top_k)) return 0;
+  // (one workgroup needs none; a size of 0 says that the call would be refused)
+  return 256 + (route_blocks(tokens) > 1 ? (size_t)route_blocks(tokens) * experts * 4 : 0);
+}
+
+extern "C" int glq_route(const void *logits, glq_dtype dt, int64_t tokens, int32_t experts, int32_t top_k, uint32_t flags,
+                         float *weights, int32_t *ids, int32_t *pos, int32_t *src, int32_t *offsets, void *workspace,
+                         size_t ws_bytes, void *hip_stream) {
+  if (!valid_dtype(dt) || (flags & ~(uint32_t)GLQ_ROUTE_NORMALIZE)) return GLQ_ERR_ARG;
+  const int rc = check_route(tokens, experts, top_k);
+  if (rc) return rc;
+  if (!offsets || !aligned4(offsets) || (tokens > 0 && (!logits || !weights || !ids || !pos || !src))) return GLQ_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(logits) & (dt == GLQ_F32 ? 3 : 1)) || !aligned4(weights) || !aligned4(ids) || !aligned4(pos) ||
+      !aligned4(src))
+    return GLQ_ERR_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || ws_bytes < glq_route_workspace(tokens, experts, top_k))
+    return GLQ_ERR_WORKSPACE;
+  RouteArgs a = {logits, tokens, route_blocks(tokens), experts, top_k, (flags & GLQ_ROUTE_NORMALIZE) ? 1 : 0,
+                 weights, ids, pos, src, offsets, reinterpret_cast<int32_t *>(workspace)};
+  if (a.blocks == 0) a.blocks = 1;                    // no tokens: offsets of zero
+  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  if (experts <= 64) launch_pick<1>(a, dt, st);
+  else if (experts <= 128) launch_pick<2>(a, dt, st);
+  else if (experts <= 256) launch_pick<4>(a, dt, st);
+  else if (experts <= 512) launch_pick<8>(a, dt, st);
+  else launch_pick<16>(a, dt, st);
+  int rc2 = hip_status(hipGetLastError(), "route_pick_k");
+  if (rc2 || a.blocks == 1) return rc2;
+  hipLaunchKernelGGL(route_place_k, dim3((unsigned)a.blocks), dim3(kRouteThreads), 0, st, a);
+  return hip_status(hipGetLastError(), "route_place_k");
+}

@@ -22,13 +22,16 @@ GLQ_CB_INT8_2X, GLQ_CB_DEVICE = 0, 1
 FLAG_NO_INPUT_RHT, FLAG_NO_OUTPUT_RHT = 1, 2
 KV_BF16, KV_INT8, KV_INT4 = 0, 1, 2
 ATTN_CAUSAL = 1
+ROPE_PAIRS = 1
+ROUTE_NORMALIZE = 1
 
 EXPORTS = ("glq_build_codebook", "glq_encode_ref", "glq_encode_ldlq", "glq_rht_apply", "glq_decode_weights",
            "glq_fused_linear_workspace", "glq_fused_linear", "glq_fused_linear_noalloc", "glq_status_string",
            "glq_last_error",
            "glq_version", "glq_ep_encode", "glq_ep_build_lut", "glq_ep_decode_weights",
            "glq_ep_fused_linear_workspace", "glq_ep_fused_linear", "glq_kv_append", "glq_kv_read",
-           "glq_attn_decode_workspace", "glq_attn_decode", "glq_attn_prompt")
+           "glq_attn_decode_workspace", "glq_attn_decode", "glq_attn_prompt", "glq_kv_plan", "glq_qk_norm_rope",
+           "glq_route_workspace", "glq_route")
 EP_LANES, EP_TABLES, EP_MAX_SYMS = 64, 5, 256
 EP_LUT_BYTES = 64 + EP_TABLES * 2048 * 4
 
@@ -75,6 +78,21 @@ class PromptStruct(ctypes.Structure):
                 ("cu_k", _vp), ("max_q", _i64), ("scale", _f32)]
 
 
+class PlanStruct(ctypes.Structure):
+    _fields_ = [("batch", _i64), ("max_pages", _i64), ("num_pages", _i64), ("page_size", _i32), ("lens", _vp),
+                ("added", _vp), ("free_pages", _vp), ("num_free", _i64), ("page_table", _vp), ("new_lens", _vp),
+                ("cu_q", _vp), ("max_tokens", _i64), ("slots", _vp), ("positions", _vp), ("max_read", _i64),
+                ("cu_k", _vp), ("read_slots", _vp), ("used", _vp)]
+
+
+class QkStruct(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("q_out", _vp), ("k_out", _vp), ("dt", _i32), ("q_heads", _i32),
+                ("kv_heads", _i32), ("head_dim", _i32), ("q_stride", _i64), ("k_stride", _i64), ("q_out_stride", _i64),
+                ("k_out_stride", _i64), ("tokens", _i64), ("q_weight", _vp), ("k_weight", _vp), ("eps", _f32),
+                ("rotary_dim", _i32), ("positions", _vp), ("rotary", _vp), ("max_positions", _i64), ("v", _vp),
+                ("v_stride", _i64), ("slots", _vp)]
+
+
 _lib.glq_build_codebook.argtypes = [_i32, _vp, _sz, ctypes.POINTER(_sz)]
 _lib.glq_encode_ref.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _f32, ctypes.POINTER(_f32), _vp, _vp, _i32, _vp]
 _lib.glq_encode_ldlq.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _vp, ctypes.c_double, _f32,
@@ -102,13 +120,19 @@ _lib.glq_attn_decode_workspace.restype = _sz
 _lib.glq_attn_decode.argtypes = [_kvc, _vp, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _f32, _vp, _i64, _vp, _sz,
                                  _vp]
 _lib.glq_attn_prompt.argtypes = [ctypes.POINTER(PromptStruct), _u32, _vp]
+_lib.glq_kv_plan.argtypes = [ctypes.POINTER(PlanStruct), _vp]
+_lib.glq_qk_norm_rope.argtypes = [ctypes.POINTER(QkStruct), _kvc, _u32, _vp]
+_lib.glq_route_workspace.argtypes = [_i64, _i32, _i32]
+_lib.glq_route_workspace.restype = _sz
+_lib.glq_route.argtypes = [_vp, _i32, _i64, _i32, _i32, _u32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
 _lib.glq_status_string.argtypes = [_i32]
 _lib.glq_status_string.restype = ctypes.c_char_p
 _lib.glq_version.restype = _u32
 _lib.glq_last_error.restype = ctypes.c_char_p
 for _name in ("glq_build_codebook", "glq_encode_ref", "glq_encode_ldlq", "glq_rht_apply", "glq_decode_weights",
               "glq_fused_linear", "glq_ep_encode", "glq_ep_build_lut", "glq_ep_decode_weights",
-              "glq_ep_fused_linear", "glq_kv_append", "glq_kv_read", "glq_attn_decode", "glq_attn_prompt"):
+              "glq_ep_fused_linear", "glq_kv_append", "glq_kv_read", "glq_attn_decode", "glq_attn_prompt",
+              "glq_kv_plan", "glq_qk_norm_rope", "glq_route"):
     getattr(_lib, _name).restype = ctypes.c_int
 
 
@@ -778,3 +802,147 @@ def attn_prompt(q, k, v, out, cu_q, cu_k=None, max_q: int | None = None, causal:
     _check(_lib.glq_attn_prompt(ctypes.byref(st), ATTN_CAUSAL if causal else 0, _stream_ptr(stream, dev)),
            "glq_attn_prompt")
     return out
+
+
+# ------------------------------------------------- a serving step around those calls
+
+class KvPlan:
+    """Outputs of kv_plan for up to `batch` requests, the rows of page_table (int32
+    [batch, max_pages], kept and written to), max_tokens new tokens and, for reading the
+    cache back, max_read tokens in all:
+
+      new_lens [batch], cu_q [batch + 1], slots and positions [max_tokens], used [1], and
+      with max_read > 0 cu_k [batch + 1] and read_slots [max_read], all int32.
+    """
+
+    def __init__(self, page_table, page_size: int, num_pages: int, max_tokens: int, max_read: int = 0):
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table: must be int32 [batch, max_pages]")
+        batch, max_pages = page_table.shape
+        if min(max_tokens, max_read) < 0:
+            raise ValueError(f"max_tokens, max_read: {max_tokens}, {max_read}")
+        dev = self.device = page_table.device
+        at = _ints(page_table, "page_table", dev, batch, max_pages)
+        self.page_table, self.batch = page_table, batch
+
+        def ints(n):
+            return torch.zeros(n, dtype=torch.int32, device=dev)
+
+        self.new_lens, self.cu_q, self.used = ints(batch), ints(batch + 1), ints(1)
+        self.slots, self.positions = ints(max_tokens), ints(max_tokens)
+        self.cu_k, self.read_slots = (ints(batch + 1), ints(max_read)) if max_read else (None, None)
+        self._st = PlanStruct(batch, max_pages, num_pages, page_size, 0, 0, 0, 0, at, self.new_lens.data_ptr(),
+                              self.cu_q.data_ptr(), max_tokens, self.slots.data_ptr(), self.positions.data_ptr(),
+                              max_read, self.cu_k.data_ptr() if max_read else 0,
+                              self.read_slots.data_ptr() if max_read else 0, self.used.data_ptr())
+
+
+def kv_plan(plan: KvPlan, lens, added, free_pages, stream=None) -> KvPlan:
+    """Pages, slots, positions and offsets of a step (glq_kv_plan): request b has lens[b]
+    tokens cached and added[b] new ones (int32 [batch]), pages that it needs more come from
+    free_pages (int32) in order; plan.used says how many. Slots of -1 drop their
+    token: no page was free, the table is full, or there is no such token."""
+    dev, st = plan.device, PlanStruct.from_buffer_copy(plan._st)
+    st.lens, st.added = _ints(lens, "lens", dev, plan.batch), _ints(added, "added", dev, plan.batch)
+    st.num_free = _last_size(free_pages)
+    st.free_pages = _ints(free_pages, "free_pages", dev, st.num_free)
+    _check(_lib.glq_kv_plan(ctypes.byref(st), _stream_ptr(stream, dev)), "glq_kv_plan")
+    return plan
+
+
+def rotary_table(max_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda"):
+    """float32 [max_positions, rotary_dim]: cosines, then sines, of position * base^(-2 i /
+    rotary_dim), the angles in 64 bits (qk_norm_rope takes any such table)."""
+    turn = torch.exp(torch.arange(rotary_dim // 2, dtype=torch.float64) * (-2.0 * float(np.log(base)) / rotary_dim))
+    angle = torch.arange(max_positions, dtype=torch.float64)[:, None] * turn
+    return torch.cat((angle.cos(), angle.sin()), 1).to(torch.float32).to(device)
+
+
+def _norm_weight(t, name, device, dim):
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != (dim,) or t.device != device or \
+            not t.is_contiguous() or t.data_ptr() % 16:
+        raise ValueError(f"{name}: must be a dense float32 vector of {dim} on {device}, 16-byte aligned")
+    return t.data_ptr()
+
+
+def qk_norm_rope(q, k, positions, rotary, q_out, k_out=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 pairs: bool = False, cache: KvCache | None = None, v=None, slots=None, stream=None):
+    """Norms of the heads of q [tokens, q_heads, head_dim] and k [tokens, kv_heads,
+    head_dim] (where there are weights, float32 [head_dim]), then the rotation by the rows
+    `positions` (int32 [tokens]) of rotary (float32 [max_positions, rotary_dim]: cosines,
+    sines; None: no rotation), of halves or, with pairs, of neighbours (glq_qk_norm_rope).
+    The outputs may be the inputs. With a cache, keys and v are written there too at
+    `slots`, and k_out may be None. Returns q_out, k_out."""
+    dt = _attn_dtype(q, "q")
+    _attn_dtype(k, "k")
+    dev, tokens, heads, dim = q.device, *q.shape
+    kvh = k.shape[1]
+    if dim not in _HEAD_DIMS:
+        raise ValueError(f"q: head_dim {dim}, expected one of {_HEAD_DIMS}")
+    qp, qs = _rows(q, "q", dev, q.dtype, tokens, heads, dim)
+    kp, ks = _rows(k, "k", dev, q.dtype, tokens, kvh, dim)
+    qop, qos = _rows(q_out, "q_out", dev, q.dtype, tokens, heads, dim)
+    kop, kos = (0, 0) if k_out is None else _rows(k_out, "k_out", dev, q.dtype, tokens, kvh, dim)
+    vp = vs = sp = pp = tp = most = rot = 0
+    if cache is not None:
+        if (cache.kv_heads, cache.head_dim, cache.device) != (kvh, dim, dev):
+            raise ValueError(f"cache: {cache.kv_heads} heads of {cache.head_dim} on {cache.device}, k has {kvh} of {dim} on "
+                             f"{dev}")
+        vp, vs = _rows(v, "v", dev, q.dtype, tokens, kvh, dim)
+        sp = _ints(slots, "slots", dev, tokens)
+    elif k_out is None or v is not None or slots is not None:
+        raise ValueError("k_out: missing" if k_out is None else "v, slots: without a cache")
+    if rotary is not None:
+        if not isinstance(rotary, torch.Tensor) or rotary.dtype is not torch.float32 or rotary.dim() != 2 or \
+                rotary.device != dev or not rotary.is_contiguous() or rotary.data_ptr() % 16:
+            raise ValueError(f"rotary: must be dense float32 [max_positions, rotary_dim] on {dev}, 16-byte aligned")
+        tp, (most, rot) = rotary.data_ptr(), rotary.shape
+        if rot < 1 or most < 1:
+            raise ValueError(f"rotary: shape {tuple(rotary.shape)}")
+        pp = _ints(positions, "positions", dev, tokens)
+    st = QkStruct(qp, kp, qop, kop, dt, heads, kvh, dim, qs, ks, qos, kos, tokens,
+                  _norm_weight(q_weight, "q_weight", dev, dim), _norm_weight(k_weight, "k_weight", dev, dim), eps, rot, pp,
+                  tp, most, vp, vs, sp)
+    _check(_lib.glq_qk_norm_rope(ctypes.byref(st), None if cache is None else cache._ref, ROPE_PAIRS if pairs else 0,
+                                 _stream_ptr(stream, dev)), "glq_qk_norm_rope")
+    return q_out, k_out
+
+
+def _floats(t, name, device, *shape):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: must be a device (cuda) tensor")
+    if t.dtype is not torch.float32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected dense float32 {shape} on {device}")
+    return t.data_ptr()
+
+
+def _workspace(t, device):
+    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous on {device}")
+    return t.data_ptr(), t.nbytes
+
+
+def route_workspace_bytes(tokens: int, experts: int, top_k: int) -> int:
+    """Bytes that route needs for this many tokens or fewer."""
+    return int(_lib.glq_route_workspace(tokens, experts, top_k))
+
+
+def route(logits, top_k: int, weights, ids, pos, src, offsets, workspace, normalize: bool = True, stream=None):
+    """Each token's top_k experts of the scores logits [tokens, experts] (float32 or
+    bfloat16; -inf and NaN are not chosen): weights (float32), ids and pos (int32) [tokens,
+    top_k], and the rows in the experts' order, src [tokens * top_k] with offsets
+    [experts + 1] (int32) (glq_route). normalize: weights of the chosen add up to 1."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _ATTN_DTYPES or logits.dim() != 2 or \
+            not logits.is_contiguous() or not logits.is_cuda:
+        raise ValueError("logits: must be dense float32 or bfloat16 [tokens, experts] on a device")
+    dev, (tokens, experts) = logits.device, logits.shape
+    wp = _floats(weights, "weights", dev, tokens, top_k)
+    ip, pp = _ints(ids, "ids", dev, tokens, top_k), _ints(pos, "pos", dev, tokens, top_k)
+    sp, op = _ints(src, "src", dev, tokens * top_k), _ints(offsets, "offsets", dev, experts + 1)
+    wsp, ws = _workspace(workspace, dev)
+    _check(_lib.glq_route(logits.data_ptr(), _ATTN_DTYPES[logits.dtype], tokens, experts, top_k,
+                          ROUTE_NORMALIZE if normalize else 0, wp, ip, pp, sp, op, wsp, ws, _stream_ptr(stream, dev)),
+           "glq_route")
+    return weights, ids, pos, src, offsets

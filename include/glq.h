@@ -499,6 +499,115 @@ typedef struct {
  */
 int glq_attn_prompt(const glq_prompt *P, uint32_t flags, void *hip_stream);
 
+/* ------------------------------------------------------------------------
+ * A serving step around those calls: pages and slots from the requests' lengths,
+ * norms and rotation of queries and keys on their way into the cache, the choice of
+ * experts, and the compressed linears of the experts on ragged groups of rows.
+ * ---------------------------------------------------------------------- */
+
+/* What glq_kv_plan reads and writes: int32 device arrays, none of which may overlap another.
+ * The struct lives in host memory. */
+typedef struct {
+    int64_t batch;                /* requests */
+    int64_t max_pages;            /* columns of the page table, >= 1 */
+    int64_t num_pages;            /* pages of the cache, as in glq_kv_cache */
+    int32_t page_size;            /* a power of two, 16 .. 1024 */
+    const int32_t *lens;          /* [batch] tokens cached so far; below 0 is read as 0 */
+    const int32_t *added;         /* [batch] tokens of this step; below 0 is read as 0 */
+    const int32_t *free_pages;    /* [num_free] pages to take, in this order */
+    int64_t num_free;
+    int32_t *page_table;          /* [batch][max_pages]: the first ceil(lens / page_size) of a row are read,
+                                     those of the pages taken written, the rest is left */
+    int32_t *new_lens;            /* [batch] lens + added */
+    int32_t *cu_q;                /* [batch + 1] first new token of every request */
+    int64_t max_tokens;           /* length of slots and positions; sum of added <= max_tokens */
+    int32_t *slots, *positions;   /* [max_tokens] of the new tokens, request after request */
+    int64_t max_read;             /* length of read_slots, or 0 */
+    int32_t *cu_k;                /* [batch + 1] first cached token, the new ones included; NULL: not wanted */
+    int32_t *read_slots;          /* [max_read] slots of all tokens, the new ones included, for glq_kv_read */
+    int32_t *used;                /* [1] pages wanted from free_pages */
+} glq_plan;
+
+/*
+ * glq_kv_plan -- page tables, slots and offsets of a step from the requests' lengths, on the
+ * device: what glq_kv_append, glq_kv_read, glq_attn_decode and glq_attn_prompt take.
+ * Request b has pages for lens[b] tokens in its row of the table and takes those that
+ * lens[b] + added[b] need more from free_pages, request after request. Its i-th new token
+ * has position lens[b] + i and the slot of that token.
+ *   Not enough free pages: *used says how many were wanted, the missing ones are written as
+ *   -1 and tokens in them have slot -1 (glq_kv_append drops them). So have tokens past
+ *   the table's end and tokens in pages outside 0 .. num_pages - 1.
+ *   Entries behind the last token (a padded batch): slot -1, position 0.
+ *   More tokens than max_tokens or max_read: what does not fit is not written, and offsets
+ *   end at those lengths.
+ * One launch. The caller takes *used pages off its free ones. batch == 0 gives offsets of 0 and empty lists.
+ */
+int glq_kv_plan(const glq_plan *P, void *hip_stream);
+
+/* flags for glq_qk_norm_rope */
+enum { GLQ_ROPE_PAIRS = 1u };
+
+/* Operands of glq_qk_norm_rope. The struct lives in host memory, its pointers are device
+ * pointers; rows of tokens [heads][head_dim] *_stride elements apart (>= heads * head_dim;
+ * pointers and strides multiples of 16 bytes). */
+typedef struct {
+    const void *q, *k;            /* [tokens][q_heads], [tokens][kv_heads][head_dim] of dt */
+    void *q_out, *k_out;          /* the same shapes; each may be its input (same stride), else no overlap.
+                                     k_out may be NULL with a cache */
+    int32_t dt;                   /* glq_dtype of q, k, v and the outputs */
+    int32_t q_heads, kv_heads;    /* >= 1 */
+    int32_t head_dim;             /* 64, 128 or 256 */
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    int64_t tokens;
+    const float *q_weight, *k_weight;   /* [head_dim], 16-byte aligned; NULL: no norm */
+    float eps;                    /* >= 0 */
+    int32_t rotary_dim;           /* dimensions rotated, a multiple of 16 up to head_dim; 0: no rotation */
+    const int32_t *positions;     /* [tokens]; outside 0 .. max_positions - 1 is read as the nearest inside */
+    const float *rotary;          /* [max_positions][rotary_dim]: cosines of the rotary_dim / 2 angles, then sines */
+    int64_t max_positions;
+    const void *v;                /* [tokens][kv_heads][head_dim], with a cache */
+    int64_t v_stride;
+    const int32_t *slots;         /* [tokens], with a cache: as in glq_kv_append */
+} glq_qk;
+
+/*
+ * glq_qk_norm_rope -- per token and head of q and k: y = x * weight / sqrt(mean(x^2) + eps),
+ * then the rotation of its first rotary_dim dimensions by the position's angles:
+ *   (y_i, y_j) -> (y_i cos - y_j sin, y_j cos + y_i sin),   j = i + rotary_dim / 2, or with
+ *   GLQ_ROPE_PAIRS the neighbours 2 i and 2 i + 1,
+ * in float32 with one rounding at the end (a mean of squares that overflows float32 gives zeros).
+ * With a cache C, the rotated keys and v also go into it at the slots, with the values that
+ * glq_kv_append of k_out and v would write. tokens == 0 is a successful no-op;
+ * GLQ_ERR_UNSUPPORTED for rotary_dim % 16 != 0 and other head_dim.
+ */
+int glq_qk_norm_rope(const glq_qk *N, const glq_kv_cache *C, uint32_t flags, void *hip_stream);
+
+/* flags for glq_route */
+enum { GLQ_ROUTE_NORMALIZE = 1u };
+
+/*
+ * glq_route -- every token's top_k experts of the largest scores (the lowest index among
+ * equals) and the tokens in the experts' order.
+ *   logits    device [tokens][experts] of dt. A score of -inf or NaN is never chosen: a token with
+ *             fewer others (a padded row has none) has choices of -1 with weight 0 at the end.
+ *   weights   device [tokens][top_k]: softmax over all scores above -inf, or with
+ *             GLQ_ROUTE_NORMALIZE over the chosen ones, in float32 (a score of +inf gives NaN)
+ *   ids       device [tokens][top_k] experts, largest score first
+ *   offsets   device [experts + 1]: expert e's rows are offsets[e] .. offsets[e + 1] - 1, in the
+ *             tokens' order
+ *   src       device [tokens * top_k] token of every row; -1 behind the last
+ *   pos       device [tokens][top_k] row of every choice, -1 for none
+ *   workspace device, 256-byte aligned, >= glq_route_workspace bytes (0 for sizes it would refuse);
+ *             need not be cleared; concurrent calls need workspaces of their own
+ * No result depends on the order in which workgroups run. 1 <= top_k <= experts.
+ * GLQ_ERR_UNSUPPORTED for more than 1024 experts, top_k above 64 and 2^25 tokens or more. Up to 64 tokens
+ * take one launch, more take two.
+ */
+size_t glq_route_workspace(int64_t tokens, int32_t experts, int32_t top_k);
+int glq_route(const void *logits, glq_dtype dt, int64_t tokens, int32_t experts, int32_t top_k, uint32_t flags,
+              float *weights, int32_t *ids, int32_t *pos, int32_t *src, int32_t *offsets, void *workspace,
+              size_t ws_bytes, void *hip_stream);
+
 /* Static text for a status code. */
 const char *glq_status_string(int status);
 
