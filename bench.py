@@ -52,7 +52,8 @@ sys.path.insert(0, ROOT)
 
 HBM_PEAK_GBS = 8000.0
 MFMA_BF16_PEAK_TFLOPS = 2500.0
-KERNEL_SRCS = [os.path.join(ROOT, "dequant_e8_codebook_amd", "csrc", f) for f in ("glq_decode.h", "glq_kernels.hip")]
+KERNEL_SRCS = [os.path.join(ROOT, "dequant_e8_codebook_amd", "csrc", f) for f in ("glq_decode.h", "glq_fwht.h",
+                                                                                           "glq_kernels.hip")]
 PROFILE_DIR = os.path.join(ROOT, "profiles")
 COPY_BYTES = 256 << 20
 

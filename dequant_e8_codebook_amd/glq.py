@@ -31,7 +31,7 @@ EXPORTS = ("glq_build_codebook", "glq_encode_ref", "glq_encode_ldlq", "glq_rht_a
            "glq_version", "glq_ep_encode", "glq_ep_build_lut", "glq_ep_decode_weights",
            "glq_ep_fused_linear_workspace", "glq_ep_fused_linear", "glq_kv_append", "glq_kv_read",
            "glq_attn_decode_workspace", "glq_attn_decode", "glq_attn_prompt", "glq_kv_plan", "glq_qk_norm_rope",
-           "glq_route_workspace", "glq_route")
+           "glq_route_workspace", "glq_route", "glq_expert_linear_workspace", "glq_expert_linear")
 EP_LANES, EP_TABLES, EP_MAX_SYMS = 64, 5, 256
 EP_LUT_BYTES = 64 + EP_TABLES * 2048 * 4
 
@@ -93,6 +93,16 @@ class QkStruct(ctypes.Structure):
                 ("v_stride", _i64), ("slots", _vp)]
 
 
+class ExpertsStruct(ctypes.Structure):
+    _fields_ = [("count", _i64), ("n", _i64), ("k", _i64), ("bpw", _i32), ("resid_shift", _i32), ("scale", _vp),
+                ("idx1", _vp), ("idx2", _vp), ("sign_k", _vp), ("sign_n", _vp), ("cb", _vp), ("row_scale", _vp)]
+
+
+class ExpertRowsStruct(ctypes.Structure):
+    _fields_ = [("x", _vp), ("y", _vp), ("x_dt", _i32), ("y_dt", _i32), ("x_rows", _i64), ("rows", _i64),
+                ("offsets", _vp), ("src", _vp), ("pos", _vp), ("weights", _vp), ("tokens", _i64), ("top_k", _i32)]
+
+
 _lib.glq_build_codebook.argtypes = [_i32, _vp, _sz, ctypes.POINTER(_sz)]
 _lib.glq_encode_ref.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _f32, ctypes.POINTER(_f32), _vp, _vp, _i32, _vp]
 _lib.glq_encode_ldlq.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _vp, ctypes.c_double, _f32,
@@ -125,6 +135,9 @@ _lib.glq_qk_norm_rope.argtypes = [ctypes.POINTER(QkStruct), _kvc, _u32, _vp]
 _lib.glq_route_workspace.argtypes = [_i64, _i32, _i32]
 _lib.glq_route_workspace.restype = _sz
 _lib.glq_route.argtypes = [_vp, _i32, _i64, _i32, _i32, _u32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.glq_expert_linear_workspace.argtypes = [ctypes.POINTER(ExpertsStruct), _i64]
+_lib.glq_expert_linear_workspace.restype = _sz
+_lib.glq_expert_linear.argtypes = [ctypes.POINTER(ExpertsStruct), ctypes.POINTER(ExpertRowsStruct), _vp, _sz, _vp]
 _lib.glq_status_string.argtypes = [_i32]
 _lib.glq_status_string.restype = ctypes.c_char_p
 _lib.glq_version.restype = _u32
@@ -132,7 +145,7 @@ _lib.glq_last_error.restype = ctypes.c_char_p
 for _name in ("glq_build_codebook", "glq_encode_ref", "glq_encode_ldlq", "glq_rht_apply", "glq_decode_weights",
               "glq_fused_linear", "glq_ep_encode", "glq_ep_build_lut", "glq_ep_decode_weights",
               "glq_ep_fused_linear", "glq_kv_append", "glq_kv_read", "glq_attn_decode", "glq_attn_prompt",
-              "glq_kv_plan", "glq_qk_norm_rope", "glq_route"):
+              "glq_kv_plan", "glq_qk_norm_rope", "glq_route", "glq_expert_linear"):
     getattr(_lib, _name).restype = ctypes.c_int
 
 
@@ -946,3 +959,93 @@ def route(logits, top_k: int, weights, ids, pos, src, offsets, workspace, normal
                           ROUTE_NORMALIZE if normalize else 0, wp, ip, pp, sp, op, wsp, ws, _stream_ptr(stream, dev)),
            "glq_route")
     return weights, ids, pos, src, offsets
+
+
+class Experts:
+    """Device tensors of `count` compressed linears of one shape, and their glq_experts struct.
+
+    scale: float32 [count]; idx1: int16 [count, n, k / 8] (uint16 bits); idx2: the same of
+    uint8 at 3 and int16 at 4 bits a weight, None at 2; sign_k, sign_n: int8 [count, k] and
+    [count, n]; cb: device_codebook; row_scale: float32 [count, n] or None. The tensors are
+    checked here once: keep them as they are.
+    """
+
+    def __init__(self, count: int, n: int, k: int, bpw: int, scale, idx1, idx2, sign_k, sign_n, cb, row_scale=None):
+        if bpw not in (2, 3, 4) or count < 1 or n < 8 or n % 8 or k < 8 or k % 8:
+            raise ValueError(f"{count} experts of {n} x {k} at {bpw} bits: n and k must be multiples of 8, bpw 2, 3 or 4")
+        self.count, self.n, self.k, self.bpw = count, n, k, bpw
+        self.scale, self.idx1, self.idx2, self.sign_k, self.sign_n, self.cb, self.row_scale = (
+            scale, idx1, idx2, sign_k, sign_n, cb, row_scale)
+        dev = self.device = _dev_tensor(idx1, "idx1", shape=(count, n, k // 8), dtypes=(torch.int16,)).device
+        if bpw == 2 and idx2 is not None:
+            raise ValueError("idx2: must be None at 2 bpw")
+        if bpw > 2:
+            _dev_tensor(idx2, "idx2", dev, shape=(count, n, k // 8), dtypes=((torch.uint8,) if bpw == 3 else (torch.int16,)))
+        _dev_tensor(scale, "scale", dev, shape=(count,), dtypes=(torch.float32,))
+        _dev_tensor(sign_k, "sign_k", dev, shape=(count, k), dtypes=(torch.int8,))
+        _dev_tensor(sign_n, "sign_n", dev, shape=(count, n), dtypes=(torch.int8,))
+        _dev_tensor(cb, "cb", dev, min_numel=_codebook_bytes(), dtypes=(torch.uint8,))
+        if row_scale is not None:
+            _dev_tensor(row_scale, "row_scale", dev, shape=(count, n), dtypes=(torch.float32,))
+        for t, nm, a in ((idx1, "idx1", 16), (idx2, "idx2", 16), (cb, "cb", 16), (sign_k, "sign_k", 8), (sign_n, "sign_n", 8)):
+            if t is not None and t.data_ptr() % a:
+                raise ValueError(f"{nm}: must be {a}-byte aligned")
+        self._st = ExpertsStruct(count, n, k, bpw, {2: 0, 3: 1, 4: 2}[bpw], scale.data_ptr(), idx1.data_ptr(),
+                                 0 if idx2 is None else idx2.data_ptr(), sign_k.data_ptr(), sign_n.data_ptr(),
+                                 cb.data_ptr(), 0 if row_scale is None else row_scale.data_ptr())
+        self._ref = ctypes.byref(self._st)
+
+    @staticmethod
+    def stack(layers) -> "Experts":
+        """The experts that a list of Layer (one shape, bit width and codebook) describes, copied together."""
+        first = layers[0]
+        if any((x.n, x.k, x.bpw, x.row_scale is None) != (first.n, first.k, first.bpw, first.row_scale is None)
+               for x in layers):
+            raise ValueError("layers: of one shape and bit width, all with row scales or none")
+
+        def all_of(name):
+            return None if getattr(first, name) is None else torch.stack([getattr(x, name) for x in layers])
+
+        scale = torch.tensor([x.scale for x in layers], dtype=torch.float32, device=first.idx1.device)
+        return Experts(len(layers), first.n, first.k, first.bpw, scale, all_of("idx1"), all_of("idx2"), all_of("sign_k"),
+                       all_of("sign_n"), first.cb, all_of("row_scale"))
+
+
+def expert_linear_workspace_bytes(experts: Experts, rows: int) -> int:
+    """Bytes that expert_linear needs for this many rows or fewer."""
+    return int(_lib.glq_expert_linear_workspace(experts._ref, rows))
+
+
+def _matrix(t, name, device, cols):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: must be a device (cuda) tensor")
+    if t.dtype not in _ATTN_DTYPES or t.dim() != 2 or t.shape[1] != cols or t.device != device or not t.is_contiguous() or \
+            t.data_ptr() % 16:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected dense float32 or bfloat16 [rows, {cols}] "
+                         f"on {device}, 16-byte aligned")
+    return t.data_ptr(), _ATTN_DTYPES[t.dtype], t.shape[0]
+
+
+def expert_linear(experts: Experts, x, y, offsets, workspace, src=None, pos=None, weights=None, stream=None):
+    """Each row through its own expert (glq_expert_linear). Rows are in the experts' order:
+    expert e's are offsets[e] .. offsets[e + 1] - 1 (int32 [count + 1]). Row r is x[src[r]], or
+    x[r] without src; y has the rows, or with pos (int32 [tokens, top_k]) and weights (float32)
+    each token's weighted sum of rows. src, pos, weights and offsets are what route gives."""
+    dev = experts.device
+    xp, xdt, x_rows = _matrix(x, "x", dev, experts.k)
+    yp, ydt, y_rows = _matrix(y, "y", dev, experts.n)
+    rows = x_rows if src is None else _last_size(src)
+    sp = 0 if src is None else _ints(src, "src", dev, rows)
+    pp = wp = top = 0
+    if pos is not None:
+        top = _last_size(pos)
+        pp, wp = _ints(pos, "pos", dev, y_rows, top), _floats(weights, "weights", dev, y_rows, top)
+        if top < 1:
+            raise ValueError("pos: no columns")
+    elif y_rows != rows or weights is not None:
+        raise ValueError(f"y: {y_rows} rows, expected {rows}" if weights is None else "weights: without pos")
+    wsp, ws = _workspace(workspace, dev)
+    st = ExpertRowsStruct(xp, yp, xdt, ydt, x_rows, rows, _ints(offsets, "offsets", dev, experts.count + 1), sp, pp, wp,
+                          y_rows, top)
+    _check(_lib.glq_expert_linear(experts._ref, ctypes.byref(st), wsp, ws, _stream_ptr(stream, dev)), "glq_expert_linear")
+    return y

@@ -608,6 +608,59 @@ int glq_route(const void *logits, glq_dtype dt, int64_t tokens, int32_t experts,
               float *weights, int32_t *ids, int32_t *pos, int32_t *src, int32_t *offsets, void *workspace,
               size_t ws_bytes, void *hip_stream);
 
+/* Compressed linears of `count` experts, all of one shape and bit width: expert e is the layer that
+ * glq_layer would describe with the e-th part of every array. The struct lives in host memory, its
+ * pointers are device pointers owned by the caller. */
+typedef struct {
+    int64_t count;            /* 1 .. 1024 */
+    int64_t n, k;             /* out, in features, both multiples of 8 */
+    int32_t bpw;              /* 2, 3 or 4 */
+    int32_t resid_shift;      /* as in glq_layer */
+    const float *scale;       /* [count], finite, > 0 */
+    const uint16_t *idx1;     /* [count][n][k/8], 16-byte aligned as are idx2 and cb */
+    const void *idx2;         /* [count][n][k/8] as in glq_layer */
+    const int8_t *sign_k;     /* [count][k], 8-byte aligned as is sign_n */
+    const int8_t *sign_n;     /* [count][n] */
+    const void *cb;           /* the GLQ_CB_DEVICE tables */
+    const float *row_scale;   /* [count][n], or NULL: as in glq_layer */
+} glq_experts;
+
+/* Rows of glq_expert_linear. The struct lives in host memory, its pointers are device pointers; x and y are
+ * 16-byte aligned and dense. */
+typedef struct {
+    const void *x;            /* [x_rows][k] of x_dt */
+    void *y;                  /* [rows][n] of y_dt, or with pos [tokens][n] */
+    int32_t x_dt, y_dt;       /* glq_dtype */
+    int64_t x_rows;
+    int64_t rows;             /* rows in the experts' order that there can be */
+    const int32_t *offsets;   /* [count + 1], not decreasing: expert e has rows offsets[e] .. offsets[e + 1] - 1;
+                                 read as the nearest value within 0 .. rows */
+    const int32_t *src;       /* [rows] row of x that a row is; one outside x is a row of zeros. NULL: row r is x[r] */
+    const int32_t *pos;       /* [tokens][top_k] rows to sum up; one that is no expert's row adds nothing. NULL: y is the rows */
+    const float *weights;     /* [tokens][top_k], with pos */
+    int64_t tokens;
+    int32_t top_k;
+} glq_expert_rows;
+
+/*
+ * glq_expert_linear -- each row through its own expert: y_r = U_e^T (s_e W^_e) (V_e x_r) for
+ * the rows r of expert e, as glq_fused_linear does for one layer; with pos (a token's rows, from
+ * glq_route) y_t = sum_j weights[t][j] y_pos[t][j], summed in float32 in the order of j and rounded once.
+ *   x_dt = GLQ_BF16: x~ rounded to bf16 (2^-8 relative at most), weights exact in bf16, float32 sums on the
+ *                    matrix cores, z = s W^ x~ kept in float32
+ *   x_dt = GLQ_F32:  x~ as three bf16 parts that hold its 24 bits, so the products are those of float32 operands;
+ *                    float32 sums
+ *   workspace   device, 256-byte aligned, >= glq_expert_linear_workspace(E, rows) bytes (that of more rows
+ *               serves fewer; 0 for what would be refused). Need not be cleared; concurrent calls need workspaces
+ *               of their own.
+ * Without pos, rows that are no expert's are not written; with it, a token without rows gets zeros. y must not overlap x.
+ * rows == 0 (with pos: tokens == 0) is a successful no-op. GLQ_ERR_UNSUPPORTED for more than 1024 experts,
+ * Hadamard blocks above 16384, and 2^22 rows or tokens. Three launches.
+ */
+size_t glq_expert_linear_workspace(const glq_experts *E, int64_t rows);
+int glq_expert_linear(const glq_experts *E, const glq_expert_rows *R, void *workspace, size_t ws_bytes,
+                      void *hip_stream);
+
 /* Static text for a status code. */
 const char *glq_status_string(int status);
 

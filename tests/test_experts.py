@@ -1,0 +1,336 @@
+"""Compressed linears of experts on ragged groups of rows: GPU results against the plain
+float64 oracle of one layer per expert, the refusals on the CPU, and a step of routing and experts.
+
+Tolerances, per output element, with S the 2-norm over sqrt(n) of its row of the reference (the
+transforms keep 2-norms, so z's rows have it too):
+  bf16     x~ is rounded to bf16: at most 2^-8 relative an element, uniform errors of at most 2^-8 /
+           sqrt(3) in the mean square; their products with independent weights add up to the same part of
+           S. Six standard deviations of it, and half a step of the output, 2^-8 of the value.
+  float32  products of float32 operands, whose float32 sums have 3 k + log2 k + log2 n roundings of
+           2^-24 S at random (log2 k + log2 n <= 28): sqrt(3 k + 28) 2^-24 S, six standard deviations of it
+           (over sqrt(3)). A part of x~ that got lost is 2^-17 of it.
+A token's sum of rows: the sum of weight times either.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import glq as oracle
+
+glq = pytest.importorskip("dequant_e8_codebook_amd.glq")
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+class Set:
+    """Experts of random indices on the device, and each as the oracle takes it."""
+
+    def __init__(self, count, n, k, bpw, seed=0, row_scale=False):
+        rng = np.random.default_rng(seed)
+        self.count, self.n, self.k, self.bpw = count, n, k, bpw
+        self.idx1 = rng.integers(0, 65536, (count, n, k // 8)).astype(np.uint16)
+        self.idx2 = None if bpw == 2 else rng.integers(0, 256 if bpw == 3 else 65536, self.idx1.shape).astype(
+            np.uint8 if bpw == 3 else np.uint16)
+        self.sign_k, self.sign_n = (rng.integers(0, 2, (count, m)).astype(np.int8) * 2 - 1 for m in (k, n))
+        self.scale = rng.uniform(0.01, 0.03, count).astype(np.float32)
+        self.row_scale = rng.uniform(0.5, 2, (count, n)).astype(np.float32) if row_scale else None
+
+    def device(self, cb):
+        def dev(a):
+            return None if a is None else torch.from_numpy(a).cuda()
+        i2 = self.idx2.view(np.int16) if self.bpw == 4 else self.idx2
+        return glq.Experts(self.count, self.n, self.k, self.bpw, dev(self.scale), dev(self.idx1.view(np.int16)), dev(i2),
+                           dev(self.sign_k), dev(self.sign_n), cb, dev(self.row_scale))
+
+    def reference(self, e, x):
+        scale = self.scale[e] if self.row_scale is None else self.scale[e] * self.row_scale[e]
+        return oracle.layer_reference(x, self.idx1[e], None if self.idx2 is None else self.idx2[e], self.bpw, scale,
+                                      self.sign_n[e], self.sign_k[e])
+
+
+@pytest.fixture(scope="module")
+def cb():
+    return glq.device_codebook()
+
+
+def _rows_reference(experts, x, offsets, src, rows):
+    """float64 [rows, n] by the words; rows that are no expert's stay NaN."""
+    out = np.full((rows, experts.n), np.nan)
+    for e in range(experts.count):
+        at = np.arange(max(offsets[e], 0), min(offsets[e + 1], rows))
+        if len(at):
+            of = at if src is None else src[at]
+            take = np.where(((of >= 0) & (of < len(x)))[:, None], x[np.clip(of, 0, len(x) - 1)], 0.0)
+            out[at] = experts.reference(e, take)
+    return out
+
+
+def _tolerance(ref, dtype, k, weights=None):
+    """[rows, n]: see above; with weights [tokens, top], ref is [tokens, top, n]."""
+    size = np.sqrt((ref ** 2).mean(-1, keepdims=True))
+    part = 6 / np.sqrt(3) * (2.0 ** -8 if dtype == "bf16" else np.sqrt(3 * k + 28) * 2.0 ** -24) * size
+    if weights is not None:
+        part = (part * np.abs(weights)[..., None]).sum(1)
+    return part + 1e-30
+
+
+def _held(y, ref, tol, y_dtype):
+    got = y.double().cpu().numpy()
+    tol = tol + (2.0 ** -8 if y_dtype == "bf16" else 2.0 ** -24) * (np.abs(ref) + tol)
+    err = np.abs(got - ref)
+    assert np.isfinite(got).all()
+    assert (err <= tol).all(), f"worst {(err / tol).max():.3g} of the tolerance"
+
+
+def _inputs(seed, rows, k, dtype):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randn(rows, k, generator=gen).to(DTYPES[dtype]).cuda()
+
+
+def _workspace(experts, rows, fill=255):
+    return torch.full((glq.expert_linear_workspace_bytes(experts, rows),), fill, dtype=torch.uint8, device="cuda")
+
+
+def _check_rows(cb, experts, counts, dtype, y_dtype=None, first=0, behind=0, seed=1):
+    """Counts of rows an expert, `first` rows before them and `behind` after them that are none's."""
+    y_dtype = y_dtype or dtype
+    offsets = np.concatenate(([first], first + np.cumsum(counts)))
+    rows = int(offsets[-1]) + behind
+    x = _inputs(seed, rows, experts.k, dtype)
+    y = torch.full((rows, experts.n), 7.0, dtype=DTYPES[y_dtype], device="cuda")
+    handle = experts.device(cb)
+    glq.expert_linear(handle, x, y, torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, rows))
+    ref = _rows_reference(experts, x.double().cpu().numpy(), offsets, None, rows)
+    assert (y[:first] == 7).all() and (y[int(offsets[-1]):] == 7).all()
+    own = slice(first, int(offsets[-1]))
+    _held(y[own], ref[own], _tolerance(ref[own], dtype, experts.k), y_dtype)
+
+
+COUNTS = {"one": [1], "one of many": [0, 0, 1, 0], "empty between": [3, 0, 17, 0, 0, 1], "tiles": [16, 15, 17, 32, 33],
+          "more": [64, 65, 1, 130, 0], "many": [300, 5, 257]}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("bpw", [2, 3, 4])
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("n,k", [(64, 128), (200, 328), (256, 512)])
+def test_rows(cb, dtype, bpw, counts, n, k):
+    counts = COUNTS[counts]
+    _check_rows(cb, Set(len(counts), n, k, bpw, seed=n + bpw), counts, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("n,k,bpw", [(8, 8, 4), (8, 4096, 2), (1416, 16, 3), (24, 1000, 4), (2048, 2048, 4), (1024, 4096, 3),
+                                     (4096, 1024, 2), (520, 2056, 3)])
+def test_shapes(cb, dtype, n, k, bpw):
+    _check_rows(cb, Set(3, n, k, bpw, seed=k), [5, 0, 40], dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,k", [(16384, 64), (64, 16384), (8192, 256), (256, 8192), (9216, 128), (128, 10240), (24, 16392),
+                                 (20480, 64)])
+def test_long_rows(cb, n, k):
+    """Hadamard blocks of 8192 and 16384, rows longer than a workgroup holds."""
+    _check_rows(cb, Set(2, n, k, 2, seed=3), [2, 3], "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bpw", [2, 3, 4])
+@pytest.mark.parametrize("dtype,y_dtype", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+def test_row_scales_and_rows_of_none(cb, bpw, dtype, y_dtype):
+    _check_rows(cb, Set(4, 136, 256, bpw, seed=9, row_scale=True), [7, 70, 0, 20], dtype, y_dtype, first=3, behind=11)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_many_experts(cb, dtype):
+    rng = np.random.default_rng(4)
+    counts = rng.integers(0, 6, 300) * (rng.random(300) < 0.6)
+    counts[-1] = 70
+    _check_rows(cb, Set(300, 64, 64, 3, seed=8), counts, dtype)
+    counts = np.zeros(1024, int)
+    counts[[0, 63, 64, 1023]] = 1, 20, 3, 2
+    _check_rows(cb, Set(1024, 16, 64, 2, seed=8), counts, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("tokens,count,top,n,k,bpw", [(1, 8, 2, 256, 512, 4), (1, 1, 1, 64, 64, 2), (33, 16, 4, 128, 256, 3),
+                                                      (200, 6, 2, 200, 264, 2), (90, 60, 6, 64, 128, 4)])
+def test_routed(cb, dtype, tokens, count, top, n, k, bpw):
+    """route, then the experts with gathered rows and weighted sums; some tokens have no experts."""
+    gen = torch.Generator().manual_seed(tokens)
+    logits = torch.randn(tokens, count, generator=gen)
+    if tokens > 2:
+        logits[tokens - 2:] = -torch.inf
+        logits[0, 1:] = -torch.inf
+    weights, x = torch.empty(tokens, top, device="cuda"), _inputs(2, tokens, k, dtype)
+    ids, pos = (torch.empty(tokens, top, dtype=torch.int32, device="cuda") for _ in range(2))
+    src, offsets = (torch.empty(m, dtype=torch.int32, device="cuda") for m in (tokens * top, count + 1))
+    ws = torch.empty(glq.route_workspace_bytes(tokens, count, top), dtype=torch.uint8, device="cuda")
+    glq.route(logits.cuda(), top, weights, ids, pos, src, offsets, ws)
+    experts = Set(count, n, k, bpw, seed=6)
+    handle = experts.device(cb)
+    y = torch.full((tokens, n), 7.0, dtype=DTYPES[dtype], device="cuda")
+    glq.expert_linear(handle, x, y, offsets, _workspace(handle, tokens * top), src=src, pos=pos, weights=weights)
+    xn, w, ids = x.double().cpu().numpy(), weights.double().cpu().numpy(), ids.cpu().numpy()
+    each = np.zeros((tokens, top, n))
+    for e in range(count):
+        t, j = np.nonzero(ids == e)
+        if len(t):
+            each[t, j] = experts.reference(e, xn[t])
+    _held(y, (each * w[..., None]).sum(1), _tolerance(each, dtype, k, w), dtype)
+    # the same rows, neither gathered nor summed: the sums' parts
+    rows = int(offsets[-1])
+    part = torch.zeros(tokens * top, n, device="cuda")
+    xr = x[src.long().clamp(min=0)]
+    glq.expert_linear(handle, xr, part, offsets, _workspace(handle, tokens * top, 0))
+    again = torch.zeros(tokens, n, device="cuda")
+    for j in range(top):                                   # in the order of the choices
+        p = pos[:, j].long()
+        again = torch.where((p >= 0)[:, None], torch.addcmul(again, part[p.clamp(min=0)], weights[:, j:j + 1]), again)
+    assert rows == (ids >= 0).sum()
+    err = (again - y.float()).abs().cpu().numpy()
+    assert (err <= 2.0 ** -22 * np.abs(each * w[..., None]).sum(1) + (2.0 ** -8 * np.abs(again.cpu().numpy()) if dtype == "bf16"
+                                                                        else 0)).all()
+
+
+@pytest.mark.gpu
+def test_odd_sources_and_positions(cb):
+    """Sources outside x are rows of zeros, positions that are no expert's row add nothing, one row serves twice."""
+    experts = Set(3, 64, 128, 4)
+    handle, x = experts.device(cb), _inputs(5, 6, 128, "f32")
+    src = np.array([5, -1, 6, 0, 5, 2 ** 31 - 1, -2 ** 31, 3], np.int32)
+    offsets = [1, 3, 3, 7]
+    pos = np.array([[1, 2], [3, 3], [0, 7], [-1, 8], [6, 4], [2 ** 31 - 1, -2 ** 31]], np.int32)
+    weights = np.random.default_rng(0).random((6, 2)).astype(np.float32)
+    y = torch.full((6, 64), 7.0, device="cuda")
+    dev = [torch.from_numpy(a).cuda() for a in (src, pos, weights)]
+    glq.expert_linear(handle, x, y, torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, 8), src=dev[0], pos=dev[1],
+                      weights=dev[2])
+    ref = np.nan_to_num(_rows_reference(experts, x.double().cpu().numpy(), offsets, src, 8))
+    ok = (pos >= 1) & (pos < 7)
+    each = np.where(ok[..., None], ref[np.clip(pos, 0, 7)], 0.0)
+    _held(y, (each * weights[..., None]).sum(1), _tolerance(each, "f32", 128, weights), "f32")
+    assert (y[2:4] == 0).all() and (y[5] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("offsets", [[0, 9, 4, 9], [-5, 3, 3, 100], [9, 0, 0, 0], [0, 0, 0, 0], [2 ** 31 - 1] * 4, [-1] * 4])
+def test_offsets_out_of_order_or_range(cb, offsets):
+    """Such offsets may give any rows their values, but leave what is around them and end."""
+    experts = Set(3, 64, 128, 2)
+    handle, x = experts.device(cb), _inputs(5, 9, 128, "bf16")
+    y = torch.full((11, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    glq.expert_linear(handle, x, y[:9], torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, 9, 0))
+    assert torch.isfinite(y).all() and (y[9:] == 7).all()
+    if offsets == [-5, 3, 3, 100]:
+        ref = _rows_reference(experts, x.double().cpu().numpy(), [0, 3, 3, 9], None, 9)
+        _held(y[:9], ref, _tolerance(ref, "bf16", 128), "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_rows_that_are_not_finite(cb, dtype, bad):
+    """They stay in their rows."""
+    experts = Set(2, 64, 128, 3)
+    handle, x = experts.device(cb), _inputs(5, 40, 128, dtype)
+    ref = _rows_reference(experts, x.double().cpu().numpy(), [0, 17, 40], None, 40)
+    x[[3, 39], 5] = bad
+    y = torch.empty(40, 64, dtype=DTYPES[dtype], device="cuda")
+    glq.expert_linear(handle, x, y, torch.tensor([0, 17, 40], dtype=torch.int32).cuda(), _workspace(handle, 40))
+    rows = [r for r in range(40) if r not in (3, 39)]
+    _held(y[rows], ref[rows], _tolerance(ref[rows], dtype, 128), dtype)
+    assert not torch.isfinite(y[[3, 39]]).any()
+
+
+@pytest.mark.gpu
+def test_no_rows(cb):
+    handle = Set(3, 64, 128, 4).device(cb)
+    off = torch.zeros(4, dtype=torch.int32).cuda()
+    ws = _workspace(handle, 0)
+    none = torch.zeros(0, 128, device="cuda")
+    glq.expert_linear(handle, none, torch.zeros(0, 64, device="cuda"), off, ws)
+    y = torch.full((5, 64), 7.0, device="cuda")
+    glq.expert_linear(handle, none, y, off, ws, src=torch.zeros(0, dtype=torch.int32).cuda(),
+                      pos=torch.full((5, 2), -1, dtype=torch.int32).cuda(), weights=torch.ones(5, 2, device="cuda"))
+    assert (y == 0).all()
+
+
+@pytest.mark.gpu
+def test_agrees_with_single_layers(cb):
+    """Experts stacked from layers give what glq_fused_linear gives for each (another order of sums)."""
+    experts = Set(3, 256, 512, 3)
+    layers = [glq.Layer.from_numpy(experts.idx1[e], experts.idx2[e], experts.scale[e], experts.sign_n[e], experts.sign_k[e], cb)
+              for e in range(3)]
+    handle, x, offsets = glq.Experts.stack(layers), _inputs(1, 60, 512, "f32"), [0, 20, 21, 60]
+    y, one = torch.empty(60, 256, device="cuda"), torch.empty(60, 256, device="cuda")
+    glq.expert_linear(handle, x, y, torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, 60))
+    for e, layer in enumerate(layers):
+        part = slice(offsets[e], offsets[e + 1])
+        ws = torch.zeros(glq.workspace_bytes(layer, 60), dtype=torch.uint8, device="cuda")
+        one[part] = glq.fused_linear(layer, x[part].contiguous(), one[part].contiguous(), ws)
+    size = one.double().pow(2).mean(1, keepdim=True).sqrt()
+    tol = 2 * 6 / np.sqrt(3) * np.sqrt(3 * 512 + 28) * 2.0 ** -24
+    assert ((y.double() - one.double()).abs() <= tol * size).all()
+
+
+# ------------------------------------------------- refusals (nothing is launched)
+
+def _experts_struct(**change):
+    st = glq.ExpertsStruct(4, 64, 128, 4, 2, 4096, 4096, 4096, 4096, 4096, 4096, 0)
+    for name, value in change.items():
+        setattr(st, name, value)
+    return ctypes.byref(st)
+
+
+def _rows_struct(**change):
+    st = glq.ExpertRowsStruct(4096, 8192, 1, 1, 10, 20, 4096, 4096, 4096, 4096, 5, 4)
+    for name, value in change.items():
+        setattr(st, name, value)
+    return ctypes.byref(st)
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"count": 0}, -1), ({"n": 0}, -1), ({"n": 60}, -1), ({"k": 4}, -1), ({"k": 132}, -1), ({"bpw": 5}, -1),
+    ({"resid_shift": 1}, -1), ({"scale": 0}, -1), ({"idx1": 0}, -1), ({"idx2": 0}, -1), ({"sign_k": 0}, -1), ({"sign_n": 0}, -1),
+    ({"cb": 0}, -1), ({"scale": 4098}, -1), ({"row_scale": 4098}, -1), ({"idx1": 4104}, -1), ({"idx2": 4104}, -1),
+    ({"sign_k": 4100}, -1), ({"sign_n": 4100}, -1), ({"cb": 4100}, -1), ({"count": 1025}, -2), ({"k": 32768}, -2),
+    ({"n": 32768}, -2), ({"n": 1 << 25}, -2)])
+def test_experts_refusals(change, status):
+    lib, st = glq.raw(), _experts_struct(**change)
+    assert lib.glq_expert_linear(st, _rows_struct(), 4096, 1 << 40, None) == status
+    assert lib.glq_expert_linear_workspace(st, 20) == 0
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"x_dt": 2}, -1), ({"y_dt": -1}, -1), ({"rows": -1}, -1), ({"x_rows": -1}, -1), ({"tokens": -1}, -1), ({"top_k": 0}, -1),
+    ({"weights": 0}, -1), ({"weights": 4098}, -1), ({"pos": 4098}, -1), ({"src": 4098}, -1), ({"src": 0}, -1), ({"y": 0}, -1),
+    ({"y": 8200}, -1), ({"x": 0}, -1), ({"x": 4104}, -1), ({"offsets": 0}, -1), ({"offsets": 4098}, -1), ({"rows": 1 << 23}, -2),
+    ({"tokens": 1 << 23}, -2), ({"x_rows": 1 << 32}, -2), ({"top_k": 2000}, -2), ({"tokens": 0}, 0),
+    ({"pos": 0, "rows": 0}, 0)])
+def test_rows_refusals(change, status):
+    assert glq.raw().glq_expert_linear(_experts_struct(), _rows_struct(**change), 4096, 1 << 40, None) == status
+
+
+def test_workspace_refusals():
+    lib, st = glq.raw(), _experts_struct()
+    need = lib.glq_expert_linear_workspace(st, 20)
+    assert need > 0 and lib.glq_expert_linear_workspace(st, -1) == 0
+    assert lib.glq_expert_linear(st, _rows_struct(), 0, need, None) == -4
+    assert lib.glq_expert_linear(st, _rows_struct(), 4100, need, None) == -4
+    assert lib.glq_expert_linear(st, _rows_struct(), 4096, need - 1, None) == -4
+    assert lib.glq_expert_linear(None, _rows_struct(), 4096, need, None) == -1
+    assert lib.glq_expert_linear(st, None, 4096, need, None) == -1
+    assert all(lib.glq_expert_linear_workspace(st, r) >= lib.glq_expert_linear_workspace(st, r - 1) for r in range(1, 700))
+
+
+def test_binding_refuses_host_tensors():
+    with pytest.raises(ValueError):
+        glq.Experts(1, 8, 8, 2, torch.ones(1), torch.zeros(1, 8, 1, dtype=torch.int16), None, torch.ones(1, 8, dtype=torch.int8),
+                    torch.ones(1, 8, dtype=torch.int8), torch.zeros(1 << 20, dtype=torch.uint8))
