@@ -77,12 +77,20 @@ struct XpRows {
   const float *weights;
   const int8_t *sign_k, *sign_n;
   uint16_t *xt;                // [planes][rows][kp] bf16: x~, or three parts that add up to it; zeros from k on
-  float *rowsum, *z;           // [rows] sums of x~ (bf16 path), [rows][n]
-  int32_t *row_expert;         // [rows]
+  float *rowsum;               // [1 + ks][rows] sums of x~, whole and of each part along k (bf16 path)
+  int32_t *row_exp;            // [rows] exponents of the rows of z (bf16 path)
+  int32_t *row_expert, *row_parts;   // [rows]
+  const void *z;               // [parts][rows][n]: float32, or float16 times 2^row_exp
+  const float *scale, *row_scale;
+  float unit;                  // of the operands: 1, 1/4 or 1/8 of a weight at 2, 3 or 4 bits
   int64_t k, kp, n, x_rows;    // kp: k up to a multiple of 64
-  int32_t count, rows, top;
+  int32_t count, rows, top, ks;
   int log_k, log_n;            // Hadamard blocks
 };
+
+// The product's steps of 64 inputs, and the first one of part `part` of `parts`
+constexpr int kGemmK = 64, kSplitSteps = 256;        // rows of more steps are not split
+__device__ __forceinline__ int part_begin(int64_t steps, int part, int parts) { return (int)(steps * part / parts); }
 
 // The transform of up to 64 NW E elements held E a thread, block 2^logb, each thread
 // with its own elements again afterwards.
@@ -108,13 +116,46 @@ __device__ __forceinline__ void load_signs8(const int8_t *p, float *s) {
   for (int i = 0; i < 8; ++i) s[i] = (float)(int8_t)((i < 4 ? u.x : u.y) >> (8 * (i & 3)));
 }
 
-// One workgroup a row. bf16: x~ rounded to bf16, what the matrix cores take, and the sum of the
-// rounded values, which the biased operands at 3 and 4 bits need. float32: x~ as three bf16 parts,
-// which hold all of its 24 bits.
+// Between the product and U^T the bf16 path keeps z in float16, 11 bits, whose rounding (2^-12) adds nothing to
+// those of x~ and y (2^-9), and halves what is moved. So that any row fits its range, a row's x is taken
+// times 2^-e, e = row_exponent, from the start, and z times 2^e at the end: with M the largest |x| and 2^c >= sqrt(k),
+// the vector x 2^-e is at most 2 long, and so is x~; a weight row in units of the operands (8 v at 4 bits) is
+// at most 8 * 1.25 sqrt(12) sqrt(k / 8) = 12.3 sqrt(k) long, so |z| < 24.6 sqrt(k), below 65504 up to k = 2^21 (35,600).
+// At the other end, a row of k equal elements has its z around 8 and the most uneven one around 8 / sqrt(k): far above
+// 2^-14 either way. The sums of the biased operands stay far from float32's ends as well.
+__device__ __forceinline__ int row_exponent(uint32_t top, int64_t k) {
+  if (top == 0 || top >= 0x7F800000u) return 0;
+  int c = 0;
+  while ((int64_t(1) << (2 * c)) < k) ++c;
+  const int e = (int)(top >> 23);                    // (0: below the normal numbers, as 2^-126)
+  return (e ? e - 127 : -126) + c;
+}
+
+// x times the signs, 8 elements at a time, or zeros
+template <bool F32>
+__device__ __forceinline__ void load_signed8(const XpRows &a, bool in, int64_t from, const int8_t *signs, int64_t o, float *v) {
+  if (in && o < a.k) {
+    float s[8];
+    load8<F32>(reinterpret_cast<const uint8_t *>(a.x) + (F32 ? 4 : 2) * (from * a.k + o), v);
+    load_signs8(signs + o, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= s[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  }
+}
+
+// One workgroup a row. bf16: x~ (times 2^-e) rounded to bf16, what the matrix cores take, and the sum of the
+// rounded values, which the biased operands at 3 and 4 bits need. float32: x~ as three bf16 parts, which
+// hold all of its 24 bits.
 template <int E, int NW, bool F32>
 __global__ void __launch_bounds__(64 * NW) xp_in_k(XpRows a) {
   extern __shared__ __attribute__((aligned(16))) float buf[];       // 64 NW E + 64
   __shared__ float part[NW];
+  __shared__ uint32_t tops[NW];
+  __shared__ float step_sum[F32 ? 1 : kSplitSteps];
+  constexpr int SEG = 64 * NW * E;
   const int tid = threadIdx.x;
   const int32_t r = blockIdx.x;
   if (r < bounded(a.offsets[0], a.rows) || r >= bounded(a.offsets[a.count], a.rows)) return;
@@ -123,26 +164,43 @@ __global__ void __launch_bounds__(64 * NW) xp_in_k(XpRows a) {
   const int64_t from = a.src ? a.src[r] : r;
   const bool in = from >= 0 && from < a.x_rows;
   const int8_t *signs = a.sign_k + (int64_t)e * a.k;
-  const float inv = 1.0f / sqrtf((float)(1 << a.log_k));
-  float sum = 0.0f;
-  for (int64_t s0 = 0; s0 < a.kp; s0 += 64 * NW * E) {
-    float v[E];
+  float v[E], inv = 1.0f / sqrtf((float)(1 << a.log_k)), sum = 0.0f;
+  int shift = 0;
+  for (int64_t s0 = F32 || a.kp <= SEG ? 0 : a.kp / SEG * SEG; s0 >= 0; s0 -= SEG) {     // (the first segment stays in v)
 #pragma unroll
-    for (int h = 0; h < E; h += 8) {
-      const int64_t o = s0 + E * tid + h;
-      float s[8];
-      if (in && o < a.k) {
-        load8<F32>(reinterpret_cast<const uint8_t *>(a.x) + (F32 ? 4 : 2) * (from * a.k + o), v + h);
-        load_signs8(signs + o, s);
+    for (int h = 0; h < E; h += 8) load_signed8<F32>(a, in, from, signs, s0 + E * tid + h, v + h);
+    if constexpr (F32) break;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[h + i] *= s[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[h + i] = 0.0f;
-      }
+    for (int i = 0; i < E; ++i) {
+      const int m = (int)(__float_as_uint(v[i]) & 0x7FFFFFFFu);
+      shift = shift > m ? shift : m;
     }
-    if (s0) __syncthreads();
+  }
+  if constexpr (!F32) {
+    uint32_t top = row_max<32>((uint32_t)shift);
+    const auto both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+    top = both[0] > both[1] ? both[0] : both[1];
+    if constexpr (NW > 1) {
+      if ((tid & 63) == 0) tops[tid >> 6] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < NW; ++w) top = top > tops[w] ? top : tops[w];
+    }
+    shift = row_exponent(top, a.k);
+    if (tid == 0) a.row_exp[r] = shift;
+  }
+  for (int64_t s0 = 0; s0 < a.kp; s0 += SEG) {
+    if (s0) {
+#pragma unroll
+      for (int h = 0; h < E; h += 8) load_signed8<F32>(a, in, from, signs, s0 + E * tid + h, v + h);
+      __syncthreads();
+    }
+    if constexpr (!F32) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = ldexpf(v[i], -shift);
+    }
     row_fwht<E, NW>(v, buf, a.log_k);
+    float here = 0.0f;
 #pragma unroll
     for (int h = 0; h < E; h += 8) {
       const int64_t o = s0 + E * tid + h;
@@ -159,9 +217,18 @@ __global__ void __launch_bounds__(64 * NW) xp_in_k(XpRows a) {
           w[i / 2] = pack_bf16(x[i], x[i + 1]);
           const float lo = bf16_lo(w[i / 2]), hi = bf16_hi(w[i / 2]);
           if constexpr (F32) x[i] -= lo, x[i + 1] -= hi;
-          else sum += lo + hi;
+          else here += lo + hi;
         }
         *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    if constexpr (!F32) {
+      sum += here;
+      if (a.ks > 1) {                                // sums of steps: 64 / E lanes each
+#pragma unroll
+        for (int m = 1; m < 64 / E; m <<= 1) here += lane_xor(here, m);
+        const int64_t o = s0 + E * tid;
+        if (o % kGemmK == 0 && o < a.kp) step_sum[o / kGemmK] = here;
       }
     }
   }
@@ -175,12 +242,30 @@ __global__ void __launch_bounds__(64 * NW) xp_in_k(XpRows a) {
       for (int w = 0; w < NW; ++w) all += part[w];
       a.rowsum[r] = all;
     }
+    if (a.ks > 1 && tid < a.ks) {
+      const int64_t steps = a.kp / kGemmK;
+      float some = 0.0f;
+      for (int s = part_begin(steps, tid, a.ks); s < part_begin(steps, tid + 1, a.ks); ++s) some += step_sum[s];
+      a.rowsum[(1 + tid) * (int64_t)a.rows + r] = some;
+    }
+  }
+}
+
+// 8 elements of z from `at` on, 8 elements aligned.
+template <bool Z16> __device__ __forceinline__ void load_z(const void *z, int64_t at, float *x) {
+  if constexpr (Z16) {
+    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+    const f16x8 v = *reinterpret_cast<const f16x8 *>(reinterpret_cast<const uint16_t *>(z) + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
+  } else {
+    load8<true>(reinterpret_cast<const float *>(z) + at, x);
   }
 }
 
 // One workgroup a row of y: a row's U^T z, or with `pos` the sum of a token's rows, each with its weight, in
-// the order of its choices, in float32.
-template <int E, int NW, bool F32>
+// the order of its choices, in float32. Z16: z in float16 (the bf16 path), its parts along k added up here.
+template <int E, int NW, bool F32, bool Z16>
 __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
   extern __shared__ __attribute__((aligned(16))) float buf[];
   const int tid = threadIdx.x;
@@ -196,17 +281,28 @@ __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
     for (int j = 0; j < a.top; ++j) {
       const int32_t r = a.pos ? a.pos[row_y * a.top + j] : (int32_t)row_y;
       if (r < first || r >= end) continue;           // uniform
-      const float w = a.pos ? a.weights[row_y * a.top + j] * inv : inv;
-      const int8_t *signs = a.sign_n + (int64_t)a.row_expert[r] * a.n;
+      const int e = a.row_expert[r], parts = a.row_parts[r];
+      float w = a.pos ? a.weights[row_y * a.top + j] * inv : inv;
+      w *= a.unit * (Z16 ? ldexpf(a.scale[e], a.row_exp[r]) : a.scale[e]);
+      const int8_t *signs = a.sign_n + (int64_t)e * a.n;
       float v[E];
 #pragma unroll
       for (int h = 0; h < E; h += 8) {
         const int64_t o = s0 + E * tid + h;
-        if (o < a.n) {
-          load8<true>(a.z + (int64_t)r * a.n + o, v + h);
-        } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[h + i] = 0.0f;
+        for (int i = 0; i < 8; ++i) v[h + i] = 0.0f;
+        if (o >= a.n) continue;
+        for (int p = 0; p < parts; ++p) {
+          float x[8];
+          load_z<Z16>(a.z, ((int64_t)p * a.rows + r) * a.n + o, x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[h + i] += x[i];
+        }
+        if (a.row_scale) {
+          float x[8];
+          load8<true>(a.row_scale + (int64_t)e * a.n + o, x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[h + i] *= x[i];
         }
       }
       if (again) __syncthreads();
@@ -236,13 +332,22 @@ struct XpProduct {
   const uint16_t *idx1, *xt;
   const void *idx2;
   const uint8_t *cb;
-  const float *scale, *row_scale, *rowsum;
+  const float *rowsum;
   const int32_t *offsets;
-  float *z;
+  int32_t *row_parts;
+  void *z;                     // [parts][rows][n]
   int64_t n, k, kp;
   int32_t count, rows;
   uint32_t n_groups;           // of 128 weight rows, or of 256
+  int32_t ks;                  // parts along k of the rows that are split
 };
+
+// z of row r (its plane of the part) at weight row j: a sum over inputs in units of the operands, without the scales.
+template <bool F32> __device__ __forceinline__ void store_z(const XpProduct &a, int part, int32_t r, int64_t j, float v) {
+  const int64_t at = ((int64_t)part * a.rows + r) * a.n + j;
+  if constexpr (F32) reinterpret_cast<float *>(a.z)[at] = v;
+  else reinterpret_cast<_Float16 *>(a.z)[at] = (_Float16)v;
+}
 
 // biased operands (bf16 of 192 + u) to bf16 of u, exact
 __device__ __forceinline__ uint4 unbiased(uint4 w) {
@@ -301,8 +406,6 @@ __global__ void __launch_bounds__(512) xp_rows_k(XpProduct a) {
     }
   }
   if (n0 + j >= a.n) return;
-  float post = a.scale[e] * Epi<BPW>::mul;
-  if (a.row_scale) post *= a.row_scale[row];
 #pragma unroll
   for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -310,7 +413,8 @@ __global__ void __launch_bounds__(512) xp_rows_k(XpProduct a) {
       const int32_t r = row0 + 16 * t + 4 * q + i;
       if (r >= row1) continue;
       const float bias = F32 || BPW == 2 ? 0.0f : Epi<BPW>::bias * a.rowsum[r];
-      a.z[(int64_t)r * a.n + n0 + j] = post * (acc[t][i] - bias);
+      store_z<F32>(a, 0, r, n0 + j, acc[t][i] - bias);
+      if (n0 + j == 0) a.row_parts[r] = 1;
     }
 }
 
@@ -318,40 +422,65 @@ __global__ void __launch_bounds__(512) xp_rows_k(XpProduct a) {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// Workgroup b's tile of 256 (TM) rows of an expert by 256 of its weight rows, or false. Whole
-// groups of TM rows come before the experts' remainders, which are shorter, so those fill
-// the end of the launch. Neighbouring tiles (the weight rows of one group of rows) run on one XCD:
-// blocks go to the eight in turn.
-__device__ __forceinline__ bool find_tile(const int32_t *offsets, int count, int32_t rows, uint32_t b, uint32_t n_groups, int tm,
-                                          int &e, int32_t &row0, int32_t &row1, uint32_t &group) {
+// What a workgroup of the product does: rows row0 .. row1 - 1 of expert e, its weight rows from 256 group on, part
+// `part` of `parts` along k.
+struct XpTile { int e; int32_t row0, row1; uint32_t group; int part, parts; };
+
+constexpr uint32_t kCus = 256;                       // of an MI355X; only how work is shared out hangs on it
+
+// Workgroup b's tile, or false. Units are groups of tm rows of an expert, whole ones first, then the experts'
+// remainders, which are shorter. As many whole units as make full rounds on the card come first,
+// unsplit. Where what is left would fill only up to half of a last round, its units are split along k: their
+// parts' z lie in planes of their own that xp_out_k adds up, so no part waits for another. (8 experts of 4096 x 4096,
+// 8192 rows, 448 tiles and 128 of remainders: see launch_gemm.) Neighbouring tiles (the weight rows of one unit) run on
+// one XCD: blocks go to the eight in turn.
+__device__ __forceinline__ bool find_tile(const XpProduct &a, uint32_t b, int tm, XpTile &tile) {
   const int lane = threadIdx.x & 63;
+  auto rows_of = [&](int x, int32_t &lo) {
+    lo = x < a.count ? bounded(a.offsets[x], a.rows) : 0;
+    const int32_t hi = x < a.count ? bounded(a.offsets[x + 1], a.rows) : 0;
+    return hi > lo ? hi - lo : 0;
+  };
   uint32_t whole = 0, rest = 0;
-  for (int c = 0; c < count; c += 64) {
-    const int x = c + lane;
-    const int32_t lo = x < count ? bounded(offsets[x], rows) : 0, hi = x < count ? bounded(offsets[x + 1], rows) : 0;
-    const int32_t mine = hi > lo ? hi - lo : 0;
+  for (int c = 0; c < a.count; c += 64) {
+    int32_t lo;
+    const int32_t mine = rows_of(c + lane, lo);
     uint32_t w = (uint32_t)(mine / tm);
 #pragma unroll
     for (int s = 32; s; s >>= 1) w += __shfl_xor(w, s);
     whole += (uint32_t)__builtin_amdgcn_readfirstlane((int)w);
     rest += __popcll(__ballot(mine % tm != 0));
   }
-  const uint32_t first = whole * n_groups, all = first + rest * n_groups;
+  uint32_t lead = whole + rest;                      // units that are not split
+  if (a.ks > 1) {
+    const uint32_t last = (whole + rest) * a.n_groups % kCus;
+    if (last > 0 && last <= kCus / 2) lead = whole * a.n_groups / kCus * kCus / a.n_groups;
+  }
   auto spread = [](uint32_t i, uint32_t n) {         // i-th block of n -> tile, in runs of an XCD; n: none
     const uint32_t run = (n + 7) / 8, t = (i % 8) * run + i / 8;
     return i / 8 < run && t < n ? t : n;
   };
-  const uint32_t lead = (first + 7) / 8 * 8;         // blocks of the whole groups
-  const bool is_rest = b >= lead;
-  const uint32_t n = is_rest ? all - first : first, t = spread(is_rest ? b - lead : b, n);
-  if (t >= n) return false;
-  const uint32_t u = t / n_groups;
-  group = t % n_groups;
+  const uint32_t first = lead * a.n_groups, blocks = (first + 7) / 8 * 8;
+  tile.part = 0, tile.parts = 1;
+  uint32_t u;
+  if (b < blocks) {
+    const uint32_t t = spread(b, first);
+    if (t >= first) return false;
+    u = t / a.n_groups, tile.group = t % a.n_groups;
+  } else {
+    const uint32_t n = (whole + rest - lead) * a.n_groups * a.ks, t = spread(b - blocks, n);
+    if (t >= n) return false;
+    u = t / (a.n_groups * a.ks);
+    const uint32_t in = t - u * a.n_groups * a.ks;
+    u += lead;
+    tile.part = (int)(in / a.n_groups), tile.parts = a.ks, tile.group = in % a.n_groups;
+  }
+  const bool is_rest = u >= whole;
+  if (is_rest) u -= whole;
   uint32_t before = 0;
-  for (int c = 0; c < count; c += 64) {
-    const int x = c + lane;
-    const int32_t lo = x < count ? bounded(offsets[x], rows) : 0, hi = x < count ? bounded(offsets[x + 1], rows) : 0;
-    const int32_t have = hi > lo ? hi - lo : 0;
+  for (int c = 0; c < a.count; c += 64) {
+    int32_t lo;
+    const int32_t have = rows_of(c + lane, lo);
     const uint32_t mine = is_rest ? (have % tm != 0 ? 1u : 0u) : (uint32_t)(have / tm);
     uint32_t up = mine;
 #pragma unroll
@@ -363,11 +492,11 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int count, int
     const unsigned long long hit = __ballot(mine > 0 && at_first <= u && u < at_first + mine);
     if (hit) {
       const int at = __ffsll((long long)hit) - 1;
-      e = c + at;
-      const int32_t begin = __builtin_amdgcn_readlane(lo, at), end = __builtin_amdgcn_readlane(hi, at);
-      row0 = is_rest ? begin + (end - begin) / tm * tm
-                     : begin + (int32_t)(u - (uint32_t)__builtin_amdgcn_readlane((int)at_first, at)) * tm;
-      row1 = end - row0 < tm ? end : row0 + tm;
+      tile.e = c + at;
+      const int32_t begin = __builtin_amdgcn_readlane(lo, at), end = begin + __builtin_amdgcn_readlane(have, at);
+      tile.row0 = is_rest ? begin + (end - begin) / tm * tm
+                          : begin + (int32_t)(u - (uint32_t)__builtin_amdgcn_readlane((int)at_first, at)) * tm;
+      tile.row1 = end - tile.row0 < tm ? end : tile.row0 + tm;
       return true;
     }
     before += (uint32_t)__builtin_amdgcn_readlane((int)up, 63);
@@ -375,7 +504,7 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int count, int
   return false;
 }
 
-constexpr int kGemmThreads = 512, kGemmK = 64, kGemmLda = kGemmK + 8;
+constexpr int kGemmThreads = 512, kGemmLda = kGemmK + 8;
 // rows of x~ in LDS, of which there are two tiles: 256 of bf16 x~, 64 of each part of float32 x~
 constexpr int gemm_rows(bool f32) { return f32 ? 192 : 256; }
 constexpr size_t gemm_lds(size_t tables, bool f32) { return tables + 2 * sizeof(uint16_t) * gemm_rows(f32) * kGemmLda; }
@@ -387,7 +516,9 @@ constexpr size_t gemm_lds(size_t tables, bool f32) { return tables + 2 * sizeof(
 // so each weight is rebuilt once a workgroup. The step's MFMAs come in runs; the walk of the
 // next step's indices (records, halves, combination) and the tile's loads and writes are spread over them.
 template <int BPW, bool G4, int MB, int P>
-__device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, int e, int32_t row0, int32_t row1, int64_t n0) {
+__device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, const XpTile &tile, int64_t n0) {
+  const int32_t row0 = tile.row0, row1 = tile.row1;
+  const int64_t e = tile.e;
   constexpr bool F32 = P == 3;
   constexpr int TPH = MB < 4 ? MB : 4, HB = MB / TPH;          // MFMA tiles of a run, runs of one of the 4 k-steps
   constexpr int RP = MB < 2 ? 64 : 32 * MB;                    // rows of a part in LDS
@@ -395,8 +526,10 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, int 
   uint16_t *As0 = reinterpret_cast<uint16_t *>(lds + lds_table_bytes<BPW>());
   uint16_t *As1 = As0 + gemm_rows(F32) * kGemmLda;
   const int lane = threadIdx.x & 63, c = lane & 31, p = lane >> 5;
-  const int64_t G = a.k / 8, S = a.kp / kGemmK;
-  const int64_t left = a.n - n0, rows_w = left < 0 ? 0 : left < 32 ? left : 32, wrow = (int64_t)e * a.n + (rows_w ? n0 : 0);
+  const int64_t G = a.k / 8, steps = a.kp / kGemmK;
+  const int64_t begin = part_begin(steps, tile.part, tile.parts);
+  const int64_t S = part_begin(steps, tile.part + 1, tile.parts) - begin;       // steps of this part
+  const int64_t left = a.n - n0, rows_w = left < 0 ? 0 : left < 32 ? left : 32, wrow = e * a.n + (rows_w ? n0 : 0);
   __amdgpu_buffer_rsrc_t xa[P];
 #pragma unroll
   for (int q = 0; q < P; ++q)
@@ -416,7 +549,7 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, int 
 #pragma unroll
       for (int u = 0; u < PIECES; ++u)
         ra[q * PIECES + u] = __builtin_bit_cast(
-            uint4, __builtin_amdgcn_raw_buffer_load_b128(xa[q], va, (int)(2 * kGemmK * s) + u * sa, 0));
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(xa[q], va, (int)(2 * kGemmK * (begin + s)) + u * sa, 0));
   };
   auto store_a = [&](uint16_t *As, const uint4 (&ra)[P * PIECES]) {
 #pragma unroll
@@ -424,7 +557,8 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, int 
       *reinterpret_cast<uint4 *>(As + ((threadIdx.x >> 3) + 64 * i) * kGemmLda + 8 * (threadIdx.x & 7)) = ra[i];
   };
   // indices of step s as stored; those past a row's end meet zeros of x~
-  auto load_idx = [&](int64_t s, uint2 &i1, uint2 &i2) {
+  auto load_idx = [&](int64_t step, uint2 &i1, uint2 &i2) {
+    const int64_t s = begin + step;
     i2 = make_uint2(0u, 0u);
     if constexpr (G4) {
       i1 = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r1, 2 * vi, (int)(16 * s), 0));
@@ -550,38 +684,39 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, int 
   }
   if (s < S) kstep(s, B0, B1);
   // lane (c, p) holds rows 8 (i >> 2) + 4 p + (i & 3) of weight row n0 + c: whole lines of z a half-wave
+  if (n0 == 0 && tile.part == 0 && lane < 32)
+#pragma unroll
+    for (int t = 0; t < MB; ++t)
+      if (row0 + 32 * t + lane < row1) a.row_parts[row0 + 32 * t + lane] = tile.parts;
   if (c >= rows_w) return;
-  float post = a.scale[e] * Epi<BPW>::mul;
-  if (a.row_scale) post *= a.row_scale[wrow + c];
+  const float *rowsum = a.rowsum + (tile.parts > 1 ? 1 + tile.part : 0) * (int64_t)a.rows;
 #pragma unroll
   for (int t = 0; t < MB; ++t)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int32_t r = row0 + 32 * t + 8 * (i >> 2) + 4 * p + (i & 3);
       if (r >= row1) continue;
-      const float bias = F32 || BPW == 2 ? 0.0f : Epi<BPW>::bias * a.rowsum[r];
-      a.z[(int64_t)r * a.n + n0 + c] = post * (acc[t][i] - bias);
+      const float bias = F32 || BPW == 2 ? 0.0f : Epi<BPW>::bias * rowsum[r];
+      store_z<F32>(a, tile.part, r, n0 + c, acc[t][i] - bias);
     }
 }
 
 template <int BPW, bool G4, bool F32>
 __global__ void __launch_bounds__(kGemmThreads, 1) xp_gemm_k(XpProduct a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  int e;
-  int32_t row0, row1;
-  uint32_t group;
-  if (!find_tile(a.offsets, a.count, a.rows, blockIdx.x, a.n_groups, F32 ? 64 : 256, e, row0, row1, group)) return;
+  XpTile tile;
+  if (!find_tile(a, blockIdx.x, F32 ? 64 : 256, tile)) return;
   load_tables<BPW, kGemmThreads>(lds, a.cb);         // (only now: LDS loads in flight must not outlive their workgroup)
-  const int64_t n0 = (int64_t)group * 256 + 32 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t rows = row1 - row0;
+  const int64_t n0 = (int64_t)tile.group * 256 + 32 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t rows = tile.row1 - tile.row0;
   if constexpr (F32) {
-    if (rows > 32) gemm_tile<BPW, G4, 2, 3>(a, lds, e, row0, row1, n0);
-    else gemm_tile<BPW, G4, 1, 3>(a, lds, e, row0, row1, n0);
+    if (rows > 32) gemm_tile<BPW, G4, 2, 3>(a, lds, tile, n0);
+    else gemm_tile<BPW, G4, 1, 3>(a, lds, tile, n0);
   } else {
-    if (rows > 128) gemm_tile<BPW, G4, 8, 1>(a, lds, e, row0, row1, n0);
-    else if (rows > 64) gemm_tile<BPW, G4, 4, 1>(a, lds, e, row0, row1, n0);
-    else if (rows > 32) gemm_tile<BPW, G4, 2, 1>(a, lds, e, row0, row1, n0);
-    else gemm_tile<BPW, G4, 1, 1>(a, lds, e, row0, row1, n0);
+    if (rows > 128) gemm_tile<BPW, G4, 8, 1>(a, lds, tile, n0);
+    else if (rows > 64) gemm_tile<BPW, G4, 4, 1>(a, lds, tile, n0);
+    else if (rows > 32) gemm_tile<BPW, G4, 2, 1>(a, lds, tile, n0);
+    else gemm_tile<BPW, G4, 1, 1>(a, lds, tile, n0);
   }
 }
 
@@ -611,13 +746,13 @@ int log_block(int64_t len) {
   return lb;
 }
 
-template <int E, int NW, bool OUT, bool F32>
+template <int E, int NW, bool OUT, bool F32, bool Z16>
 int launch_transform_k(const XpRows &a, int64_t groups, hipStream_t st) {
   constexpr size_t shm = sizeof(float) * (64 * NW * E + 64);
   if constexpr (OUT) {
-    const int rc = allow_lds<xp_out_k<E, NW, F32>>(shm);
+    const int rc = allow_lds<xp_out_k<E, NW, F32, Z16>>(shm);
     if (rc) return rc;
-    hipLaunchKernelGGL((xp_out_k<E, NW, F32>), dim3((unsigned)groups), dim3(64 * NW), shm, st, a);
+    hipLaunchKernelGGL((xp_out_k<E, NW, F32, Z16>), dim3((unsigned)groups), dim3(64 * NW), shm, st, a);
     return hip_status(hipGetLastError(), "xp_out_k");
   } else {
     const int rc = allow_lds<xp_in_k<E, NW, F32>>(shm);
@@ -628,15 +763,15 @@ int launch_transform_k(const XpRows &a, int64_t groups, hipStream_t st) {
 }
 
 // 8 elements a thread, as many waves as the row (or 8192 of it at a time) takes; whole blocks of 16384 need 16 a thread.
-template <bool OUT, bool F32>
+template <bool OUT, bool F32, bool Z16 = false>
 int launch_transform(const XpRows &a, int64_t groups, hipStream_t st) {
   const int64_t len = OUT ? a.n : a.k;
-  if ((OUT ? a.log_n : a.log_k) == 14) return launch_transform_k<16, 16, OUT, F32>(a, groups, st);
-  if (len <= 512) return launch_transform_k<8, 1, OUT, F32>(a, groups, st);
-  if (len <= 1024) return launch_transform_k<8, 2, OUT, F32>(a, groups, st);
-  if (len <= 2048) return launch_transform_k<8, 4, OUT, F32>(a, groups, st);
-  if (len <= 4096) return launch_transform_k<8, 8, OUT, F32>(a, groups, st);
-  return launch_transform_k<8, 16, OUT, F32>(a, groups, st);
+  if ((OUT ? a.log_n : a.log_k) == 14) return launch_transform_k<16, 16, OUT, F32, Z16>(a, groups, st);
+  if (len <= 512) return launch_transform_k<8, 1, OUT, F32, Z16>(a, groups, st);
+  if (len <= 1024) return launch_transform_k<8, 2, OUT, F32, Z16>(a, groups, st);
+  if (len <= 2048) return launch_transform_k<8, 4, OUT, F32, Z16>(a, groups, st);
+  if (len <= 4096) return launch_transform_k<8, 8, OUT, F32, Z16>(a, groups, st);
+  return launch_transform_k<8, 16, OUT, F32, Z16>(a, groups, st);
 }
 
 template <int BPW, bool G8, bool F32>
@@ -656,8 +791,8 @@ template <int BPW, bool G4, bool F32>
 int launch_gemm(XpProduct a, hipStream_t st) {
   constexpr int TM = F32 ? 64 : 256;
   a.n_groups = (uint32_t)((a.n + 255) / 256);
-  // whole groups of rows and remainders: no more than this, whatever the offsets are; up to 7 blocks to fill the XCDs' runs of each
-  const int64_t groups = (a.rows / TM + (a.count < a.rows ? a.count : a.rows)) * a.n_groups + 16;
+  // no more tiles than this, whatever the offsets are, and up to 7 blocks to fill the XCDs' runs of each kind
+  const int64_t groups = (a.rows / TM + (a.count < a.rows ? a.count : a.rows)) * a.n_groups * a.ks + 16;
   if (groups > 0xFFFFFFFFll / kGemmThreads) return GLQ_ERR_UNSUPPORTED;
   constexpr size_t shm = gemm_lds(lds_table_bytes<BPW>(), F32);
   const int rc = allow_lds<xp_gemm_k<BPW, G4, F32>>(shm);
@@ -667,8 +802,8 @@ int launch_gemm(XpProduct a, hipStream_t st) {
 }
 
 template <int BPW>
-int launch_product(const XpProduct &a, bool f32, hipStream_t st) {
-  if (a.rows >= 32 * (int64_t)a.count) {
+int launch_product(const XpProduct &a, bool gemm, bool f32, hipStream_t st) {
+  if (gemm) {
     if (a.k % 32 == 0) return f32 ? launch_gemm<BPW, true, true>(a, st) : launch_gemm<BPW, true, false>(a, st);
     return f32 ? launch_gemm<BPW, false, true>(a, st) : launch_gemm<BPW, false, false>(a, st);
   }
@@ -689,14 +824,45 @@ int check_experts(const glq_experts *E) {
   return GLQ_OK;
 }
 
-struct XpLayout { int64_t xt, rowsum, row_expert, z, total; };
+// Which product, and how many parts along k its split units have.
+//
+// 256 x 256 tiles where experts have at least 32 rows on average, else 64 x 128.
+struct XpPlan { bool gemm; int ks; };
+XpPlan xp_plan(int64_t count, int64_t n, int64_t k, int64_t rows, bool f32) {
+  XpPlan p = {rows >= 32 * count, 1};
+  const int64_t steps = up64(k) / kGemmK, tm = f32 ? 64 : 256, groups = (n + 255) / 256;
+  if (!p.gemm || steps > kSplitSteps || steps < 16) return p;
+  // the most tiles there can be; as many parts as give each CU one, but none under 8 steps, which would not pay for the copy of
+  // the tables
+  const int64_t most = (rows / tm + (count < rows ? count : rows)) * groups;
+  p.ks = 2;
+  while (p.ks < 8 && most * 2 * p.ks <= kCus && steps / (2 * p.ks) >= 8) p.ks *= 2;
+  return p;
+}
+
+// Bytes of z's planes for up to this many rows: two of either type, or four or eight where the rule above can ask for
+// them, most tiles * parts <= 256 (so rows < tm (256 / (parts groups) + 1)).
+int64_t z_bytes(int64_t n, int64_t rows) {
+  const int64_t groups = (n + 255) / 256;
+  int64_t need = 2 * rows * n * 4;
+  for (const int tm : {64, 256})
+    for (const int ks : {4, 8}) {
+      const int64_t top = tm * ((int64_t)kCus / (ks * groups) + 1), bytes = ks * (rows < top ? rows : top) * n * (tm == 64 ? 4 : 2);
+      if (bytes > need) need = bytes;
+    }
+  return need;
+}
+
+struct XpLayout { int64_t xt, rowsum, row_exp, row_expert, row_parts, z, total; };
 XpLayout xp_layout(const glq_experts *E, int64_t rows) {
   XpLayout w;
   w.xt = 0;
-  w.rowsum = w.xt + up256(rows * up64(E->k) * 6);          // float32 rows: three parts of 2 bytes
-  w.row_expert = w.rowsum + up256(rows * 4);
-  w.z = w.row_expert + up256(rows * 4);
-  w.total = w.z + up256(rows * E->n * 4);
+  w.rowsum = w.xt + up256(rows * up64(E->k) * 6);    // float32 rows: three parts of 2 bytes
+  w.row_exp = w.rowsum + up256(rows * 4 * 9);        // whole, and eight parts at most
+  w.row_expert = w.row_exp + up256(rows * 4);
+  w.row_parts = w.row_expert + up256(rows * 4);
+  w.z = w.row_parts + up256(rows * 4);
+  w.total = w.z + up256(z_bytes(E->n, rows));
   return w;
 }
 
@@ -734,19 +900,28 @@ extern "C" int glq_expert_linear(const glq_experts *E, const glq_expert_rows *R,
   if (!workspace || !aligned_to(workspace, 256) || ws_bytes < glq_expert_linear_workspace(E, R->rows)) return GLQ_ERR_WORKSPACE;
   uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
   const XpLayout l = xp_layout(E, R->rows);
-  const XpRows a = {R->x, R->y, R->offsets, R->src, R->pos, R->weights, E->sign_k, E->sign_n,
-                    reinterpret_cast<uint16_t *>(ws + l.xt), reinterpret_cast<float *>(ws + l.rowsum),
-                    reinterpret_cast<float *>(ws + l.z), reinterpret_cast<int32_t *>(ws + l.row_expert), E->k, up64(E->k), E->n, R->x_rows,
-                    (int32_t)E->count, (int32_t)R->rows, R->pos ? R->top_k : 1, log_block(E->k), log_block(E->n)};
   const bool f32 = R->x_dt == GLQ_F32;
+  const XpPlan plan = xp_plan(E->count, E->n, E->k, R->rows, f32);
+  XpRows a = {};
+  a.x = R->x, a.y = R->y, a.offsets = R->offsets, a.src = R->src, a.pos = R->pos, a.weights = R->weights;
+  a.sign_k = E->sign_k, a.sign_n = E->sign_n, a.scale = E->scale, a.row_scale = E->row_scale;
+  a.unit = E->bpw == 2 ? Epi<2>::mul : E->bpw == 3 ? Epi<3>::mul : Epi<4>::mul;
+  a.xt = reinterpret_cast<uint16_t *>(ws + l.xt), a.rowsum = reinterpret_cast<float *>(ws + l.rowsum);
+  a.row_exp = reinterpret_cast<int32_t *>(ws + l.row_exp), a.row_expert = reinterpret_cast<int32_t *>(ws + l.row_expert);
+  a.row_parts = reinterpret_cast<int32_t *>(ws + l.row_parts), a.z = ws + l.z;
+  a.k = E->k, a.kp = up64(E->k), a.n = E->n, a.x_rows = R->x_rows;
+  a.count = (int32_t)E->count, a.rows = (int32_t)R->rows, a.top = R->pos ? R->top_k : 1, a.ks = plan.ks;
+  a.log_k = log_block(E->k), a.log_n = log_block(E->n);
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   if (R->rows > 0) {
     rc = f32 ? launch_transform<false, true>(a, R->rows, st) : launch_transform<false, false>(a, R->rows, st);
     if (rc) return rc;
-    const XpProduct p = {E->idx1, a.xt, E->idx2, reinterpret_cast<const uint8_t *>(E->cb), E->scale, E->row_scale, a.rowsum,
-                         a.offsets, a.z, E->n, E->k, a.kp, a.count, a.rows, 0};
-    rc = E->bpw == 2 ? launch_product<2>(p, f32, st) : E->bpw == 3 ? launch_product<3>(p, f32, st) : launch_product<4>(p, f32, st);
+    const XpProduct p = {E->idx1, a.xt, E->idx2, reinterpret_cast<const uint8_t *>(E->cb), a.rowsum, a.offsets,
+                         a.row_parts, ws + l.z, E->n, E->k, a.kp, a.count, a.rows, 0, plan.ks};
+    rc = E->bpw == 2 ? launch_product<2>(p, plan.gemm, f32, st) : E->bpw == 3 ? launch_product<3>(p, plan.gemm, f32, st)
+                                                                 : launch_product<4>(p, plan.gemm, f32, st);
     if (rc) return rc;
   }
-  return R->y_dt == GLQ_F32 ? launch_transform<true, true>(a, out, st) : launch_transform<true, false>(a, out, st);
+  if (f32) return R->y_dt == GLQ_F32 ? launch_transform<true, true>(a, out, st) : launch_transform<true, false>(a, out, st);
+  return R->y_dt == GLQ_F32 ? launch_transform<true, true, true>(a, out, st) : launch_transform<true, false, true>(a, out, st);
 }
