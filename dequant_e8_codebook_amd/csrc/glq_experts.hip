@@ -579,6 +579,10 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   };
   uint4 ra[P * PIECES];
   load_a(0, ra);
+  float row_sum = 0.0f;                                        // thread t: of row row0 + t
+  if constexpr (!F32 && BPW > 2)
+    if (threadIdx.x < 256 && (int32_t)threadIdx.x < row1 - row0)
+      row_sum = a.rowsum[(tile.parts > 1 ? 1 + tile.part : 0) * (int64_t)a.rows + row0 + threadIdx.x];
   uint2 i1, i2, j1, j2;
   load_idx(0, i1, i2);
   tables_landed();                                             // and the first tile and indices
@@ -683,22 +687,51 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
     kstep(s + 1, B1, B0);
   }
   if (s < S) kstep(s, B0, B1);
-  // lane (c, p) holds rows 8 (i >> 2) + 4 p + (i & 3) of weight row n0 + c: whole lines of z a half-wave
   if (n0 == 0 && tile.part == 0 && lane < 32)
 #pragma unroll
     for (int t = 0; t < MB; ++t)
       if (row0 + 32 * t + lane < row1) a.row_parts[row0 + 32 * t + lane] = tile.parts;
-  if (c >= rows_w) return;
-  const float *rowsum = a.rowsum + (tile.parts > 1 ? 1 + tile.part : 0) * (int64_t)a.rows;
+  // Lane (c, p) holds rows 8 (i >> 2) + 4 p + (i & 3) of weight row n0 + c. z goes out through the wave's own piece of LDS, 32 rows
+  // at a time, so that a lane stores 16 bytes of a row: element by element, with a load of the row's sum for each,
+  // the end of a tile took 15 of 141 us.
+  constexpr int ES = F32 ? 4 : 2, SB = 32 * ES + 16, CPR = 32 * ES / 16;        // bytes of an element and of a row, chunks a row
+  constexpr bool BIAS = !F32 && BPW > 2;
+  const uint32_t sums = lds_table_bytes<BPW>(), mine = sums + 1024 + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32 * SB;
+  __syncthreads();                                             // the tiles of x~ are done with
+  if constexpr (BIAS) {
+    if (threadIdx.x < 256) lds_stf(sums + 4 * threadIdx.x, row_sum);
+    __syncthreads();
+  }
+  typedef __attribute__((address_space(3))) _Float16 lds_f16_w;
 #pragma unroll
-  for (int t = 0; t < MB; ++t)
+  for (int t = 0; t < MB; ++t) {
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int32_t r = row0 + 32 * t + 8 * (i >> 2) + 4 * p + (i & 3);
-      if (r >= row1) continue;
-      const float bias = F32 || BPW == 2 ? 0.0f : Epi<BPW>::bias * rowsum[r];
-      store_z<F32>(a, tile.part, r, n0 + c, acc[t][i] - bias);
+    for (int g = 0; g < 4; ++g) {
+      uint4 s = make_uint4(0, 0, 0, 0);
+      if constexpr (BIAS) s = lds128(sums + 4 * (32 * t + 8 * g + 4 * p));
+      const float bias[4] = {__uint_as_float(s.x), __uint_as_float(s.y), __uint_as_float(s.z), __uint_as_float(s.w)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = BIAS ? fmaf(-Epi<BPW>::bias, bias[i], acc[t][4 * g + i]) : acc[t][4 * g + i];
+        const uint32_t at = mine + (8 * g + 4 * p + i) * SB + c * ES;
+        if constexpr (F32) lds_stf(at, v);
+        else *reinterpret_cast<lds_f16_w *>((uintptr_t)at) = (_Float16)v;
+      }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");     // other lanes of the wave read it
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 32 * CPR / 64; ++i) {
+      const int chunk = 64 * i + lane, rl = chunk / CPR, pc = chunk % CPR;
+      const uint4 v = lds128(mine + rl * SB + pc * 16);
+      const int32_t r = row0 + 32 * t + rl;
+      const int64_t col = n0 + pc * (16 / ES);
+      if (r < row1 && col < a.n)                               // (n is a multiple of 8)
+        *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(a.z) + (((int64_t)tile.part * a.rows + r) * a.n + col) * ES) = v;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
 }
 
 template <int BPW, bool G4, bool F32>
