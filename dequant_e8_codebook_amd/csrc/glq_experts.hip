@@ -24,6 +24,7 @@ namespace glq {
 namespace {
 
 constexpr int kMaxExperts = 1024;
+constexpr uint32_t kCus = 256;                       // of an MI355X; only how work is shared out hangs on it
 
 // ------------------------------------------------------------ rows and experts
 
@@ -83,7 +84,7 @@ struct XpRows {
   const void *z;               // [parts][rows][n]: float32, or float16 times 2^row_exp
   const float *scale, *row_scale;
   float unit;                  // of the operands: 1, 1/4 or 1/8 of a weight at 2, 3 or 4 bits
-  int64_t k, kp, n, x_rows;    // kp: k up to a multiple of 64
+  int64_t k, kp, n, x_rows, out_rows;    // kp: k up to a multiple of 64
   int32_t count, rows, top, ks;
   int log_k, log_n;            // Hadamard blocks
 };
@@ -326,6 +327,314 @@ __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
   }
 }
 
+// ------------------------------------------------------------ rows of whole blocks of 1024 to 16384
+
+// The same two transforms for rows of at most 16 waves of 1024 elements each, 16 a lane, NW waves a block. The wave's
+// part is that of the single layers' block kernel (registers, one multiply-add a DPP lane stage, lane swaps that keep their
+// layout); the waves of a block then exchange all their values through LDS, four at a time, each summing up its own
+// signs of them: no transpose back, two barriers a row. Workgroups take runs of rows, whose next
+// one is in flight while one is transformed. 8192 rows of 4096 through two of eight experts: in 67 -> see launch_transform.
+
+constexpr int kRowWaves = 16;                        // most waves a row
+
+// Transform over the waves of a block: v of wave w (in its block) becomes the sum over waves j of (-1)^|w & j| v_j.
+// buf: 4 KiB a wave. A barrier lies between the callers' last use of buf and this.
+template <int NW>
+__device__ __forceinline__ void cross_waves(float (&v)[16], float4 *buf, int wave, int lane) {
+  auto put = [&] {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) buf[(4 * wave + q) * 64 + lane] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  };
+  auto add = [&](int from, float s) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 f = buf[(4 * from + q) * 64 + lane];
+      v[4 * q] = fmaf(f.x, s, v[4 * q]), v[4 * q + 1] = fmaf(f.y, s, v[4 * q + 1]);
+      v[4 * q + 2] = fmaf(f.z, s, v[4 * q + 2]), v[4 * q + 3] = fmaf(f.w, s, v[4 * q + 3]);
+    }
+  };
+  auto own = [&](float s) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= s;
+  };
+  auto sign = [&](int bit) { return wave & bit ? -1.0f : 1.0f; };
+  auto four = [&](int b) {                           // bits b and 2 b of the wave's number
+    const float s1 = sign(b), s2 = sign(2 * b);
+    own(s1 * s2);
+    add(wave ^ b, s2);
+    add(wave ^ 2 * b, s1);
+    add(wave ^ 3 * b, 1.0f);
+  };
+  if constexpr (NW == 1) return;
+  put();
+  __syncthreads();
+  if constexpr (NW == 2) own(sign(1)), add(wave ^ 1, 1.0f);
+  else four(1);
+  if constexpr (NW >= 8) {
+    __syncthreads();
+    put();
+    __syncthreads();
+    if constexpr (NW == 8) own(sign(4)), add(wave ^ 4, 1.0f);
+    else four(4);
+  }
+}
+
+// rows [r0, r1) of n from `first` on that workgroup b of `groups` takes
+__device__ __forceinline__ void my_run(int64_t first, int64_t n, int32_t &r0, int32_t &r1) {
+  r0 = (int32_t)(first + n * blockIdx.x / gridDim.x);
+  r1 = (int32_t)(first + n * (blockIdx.x + 1) / gridDim.x);
+}
+
+template <int NW, bool F32>
+__global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
+  extern __shared__ __attribute__((aligned(16))) float4 cross[];
+  __shared__ uint32_t tops[kRowWaves];
+  __shared__ float sums[2][8][kRowWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+  const int32_t first = bounded(a.offsets[0], a.rows), end = bounded(a.offsets[a.count], a.rows);
+  int32_t r0, r1;
+  my_run(first, end > first ? end - first : 0, r0, r1);
+  if (r0 >= r1) return;
+  const int el = 1024 * wave + 8 * rb_ell(lane), eo = 1024 * wave + rb_elem_out(lane, 0);    // elements read, written (+ 512, + 256)
+  constexpr int RAW = F32 ? 4 : 2;
+  uint4 raw[RAW];
+  int32_t sources = 0;
+  auto fetch = [&](int32_t r) {
+    if (a.src && ((r - r0) & 63) == 0) sources = r + lane < r1 ? a.src[r + lane] : -1;
+    const int64_t from = a.src ? __builtin_amdgcn_readlane(sources, (r - r0) & 63) : r;
+    if (from >= 0 && from < a.x_rows) {
+      const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.x) + (F32 ? 4 : 2) * (from * a.k + el));
+      if constexpr (F32) {
+        raw[0] = p[0], raw[1] = p[1], raw[2] = p[128], raw[3] = p[129];
+      } else {
+        raw[0] = p[0], raw[1] = p[64];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < RAW; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+    }
+  };
+  fetch(r0);
+  int e = 0;
+  int32_t until = r0;                                // rows of e end here
+  uint32_t flip[8];                                  // sign bits of the elements, two a word (in place of two bf16)
+  int part_of[2] = {0, 0};                           // part along k of the lane's two runs of 8
+  const int64_t steps = a.kp / kGemmK;
+  if (!F32 && a.ks > 1)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      for (int p = 1; p < a.ks; ++p) part_of[h] += (eo + 256 * h) / kGemmK >= part_begin(steps, p, a.ks);
+  const float inv = rb_sgn(lane) / sqrtf((float)(1 << a.log_k));
+  auto finish = [&](int32_t r) {                     // the row sums of row r, once all its waves have written theirs
+    if (tid <= (a.ks > 1 ? a.ks : 0)) {
+      float some = 0.0f;
+      for (int p = tid ? tid - 1 : 0; p < (tid ? tid : a.ks); ++p)
+        for (int w = 0; w < waves; ++w) some += sums[r & 1][p][w];
+      a.rowsum[tid * (int64_t)a.rows + r] = some;
+    }
+  };
+  for (int32_t r = r0; r < r1; ++r) {
+    if (r >= until) {
+      e = expert_of(a.offsets, a.count, r);
+      until = bounded(a.offsets[e + 1], a.rows);
+      const int8_t *signs = a.sign_k + (int64_t)e * a.k + el;
+      const uint2 s0 = *reinterpret_cast<const uint2 *>(signs), s1 = *reinterpret_cast<const uint2 *>(signs + 512);
+      const uint32_t s[4] = {s0.x, s0.y, s1.x, s1.y};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t two = s[i / 2] >> (16 * (i & 1));
+        flip[i] = (two & 0x80u) << 8 | (two & 0x8000u) << 16;
+      }
+    }
+    if (tid == 0) a.row_expert[r] = e;
+    float v[16];
+    uint32_t top = 0;
+    if constexpr (F32) {
+      const uint32_t w[16] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w,
+                              raw[2].x, raw[2].y, raw[2].z, raw[2].w, raw[3].x, raw[3].y, raw[3].z, raw[3].w};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i] ^ (i & 1 ? flip[i / 2] & 0x80000000u : flip[i / 2] << 16));
+    } else {
+      uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+      u16x2 most = (u16x2)(0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
+        w[i] ^= flip[i];
+        v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+      }
+      top = most.x > most.y ? most.x : most.y;
+      top = row_max<32>(top);
+      const auto both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+      top = both[0] > both[1] ? both[0] : both[1];
+      if (lane == 0) tops[wave] = top;
+    }
+    if (r + 1 < r1) fetch(r + 1);
+    if (waves > 1) __syncthreads();                  // tops; the exchange and the sums of the row before are through
+    if constexpr (!F32) {
+      if (r > r0) finish(r - 1);
+      for (int w = 0; w < waves; ++w) top = top > tops[w] ? top : tops[w];
+      const int shift = row_exponent(top << 16, a.k);
+      if (tid == 0) a.row_exp[r] = shift;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = ldexpf(v[i], -shift);
+    }
+    rb_fwht_wave<0, true>(v, lane);
+    cross_waves<NW>(v, cross, wave, lane);
+    float here[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = v[8 * h + i] * inv;
+#pragma unroll
+      for (int p = 0; p < (F32 ? 3 : 1); ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          w[i / 2] = pack_bf16(x[i], x[i + 1]);
+          const float lo = bf16_lo(w[i / 2]), hi = bf16_hi(w[i / 2]);
+          if constexpr (F32) x[i] -= lo, x[i + 1] -= hi;
+          else here[h] += lo + hi;
+        }
+        *reinterpret_cast<uint4 *>(a.xt + ((int64_t)p * a.rows + r) * a.kp + eo + 256 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    if constexpr (!F32) {
+      for (int p = 0; p < a.ks; ++p) {
+        float some = a.ks == 1 ? here[0] + here[1] : (part_of[0] == p ? here[0] : 0.0f) + (part_of[1] == p ? here[1] : 0.0f);
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) some += lane_xor(some, m);
+        if (lane == 0) sums[r & 1][p][wave] = some;
+      }
+    }
+  }
+  if constexpr (!F32) {
+    __syncthreads();
+    finish(r1 - 1);
+  }
+}
+
+// Items are rows of z: the rows themselves, or each token's choices one after the other. A wave's lanes look up 64 items at a
+// time (row, expert, factor), so the chain of loads behind a choice is gone through once for them all.
+template <int NW, bool F32, bool Z16>
+__global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
+  extern __shared__ __attribute__((aligned(16))) float4 cross[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int32_t first = bounded(a.offsets[0], a.rows), end = bounded(a.offsets[a.count], a.rows);
+  int32_t y0, y1;
+  my_run(a.pos ? 0 : first, a.pos ? a.out_rows : end > first ? end - first : 0, y0, y1);
+  if (y0 >= y1) return;
+  const int el = 1024 * wave + 8 * rb_ell(lane), eo = 1024 * wave + rb_elem_out(lane, 0);
+  const float inv = a.unit / sqrtf((float)(1 << a.log_n));
+  constexpr int RAW = Z16 ? 2 : 4;
+  const int64_t items = (int64_t)(y1 - y0) * a.top;
+  int32_t row = -1, expert = 0, parts = 0;           // of item base + lane
+  float factor = 0.0f;
+  int64_t base = -64;
+  struct Item { int32_t row, parts; float factor; uint4 raw[RAW]; uint2 sign[2]; };
+  auto fetch = [&](int64_t i, Item &it) {
+    if (i >= base + 64) {
+      base = i;
+      row = -1;
+      if (i + lane < items) {
+        row = a.pos ? a.pos[(int64_t)y0 * a.top + i + lane] : (int32_t)(y0 + i + lane);
+        if (row < first || row >= end) row = -1;
+        factor = inv;
+        if (a.pos) factor *= a.weights[(int64_t)y0 * a.top + i + lane];
+      }
+      if (row >= 0) {
+        expert = a.row_expert[row], parts = a.row_parts[row];
+        factor *= a.scale[expert];
+        if constexpr (Z16) factor = ldexpf(factor, a.row_exp[row]);
+      }
+    }
+    const int at = (int)(i - base);
+    it.row = __builtin_amdgcn_readlane(row, at);
+    if (it.row < 0) return;
+    it.parts = __builtin_amdgcn_readlane(parts, at);
+    it.factor = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(factor), at));
+    const int64_t e = __builtin_amdgcn_readlane(expert, at);
+    const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.z) + (Z16 ? 2 : 4) * ((int64_t)it.row * a.n + el));
+    if constexpr (Z16) it.raw[0] = p[0], it.raw[1] = p[64];
+    else it.raw[0] = p[0], it.raw[1] = p[1], it.raw[2] = p[128], it.raw[3] = p[129];
+    const int8_t *signs = a.sign_n + e * a.n + eo;
+    it.sign[0] = *reinterpret_cast<const uint2 *>(signs), it.sign[1] = *reinterpret_cast<const uint2 *>(signs + 256);
+  };
+  typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+  auto spread = [&](const uint4 (&raw)[RAW], float (&x)[16]) {
+    if constexpr (Z16) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f16x8 f = __builtin_bit_cast(f16x8, raw[h]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[8 * h + i] = (float)f[i];
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        x[4 * q] = __uint_as_float(raw[q].x), x[4 * q + 1] = __uint_as_float(raw[q].y);
+        x[4 * q + 2] = __uint_as_float(raw[q].z), x[4 * q + 3] = __uint_as_float(raw[q].w);
+      }
+    }
+  };
+  float acc[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+  Item next;
+  fetch(0, next);
+  int j = 0;
+  int32_t y = y0;
+  for (int64_t i = 0; i < items; ++i) {
+    const Item it = next;
+    if (i + 1 < items) fetch(i + 1, next);
+    if (it.row >= 0) {
+      float v[16];
+      spread(it.raw, v);
+      for (int p = 1; p < it.parts; ++p) {
+        const uint4 *z = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.z) +
+                                                         (Z16 ? 2 : 4) * (((int64_t)p * a.rows + it.row) * a.n + el));
+        uint4 raw[RAW];
+        if constexpr (Z16) raw[0] = z[0], raw[1] = z[64];
+        else raw[0] = z[0], raw[1] = z[1], raw[2] = z[128], raw[3] = z[129];
+        float x[16];
+        spread(raw, x);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] += x[q];
+      }
+      if (a.row_scale) {
+        const int64_t e = a.row_expert[it.row];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x[8];
+          load8<true>(a.row_scale + e * a.n + el + 512 * h, x);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[8 * h + q] *= x[q];
+        }
+      }
+      rb_fwht_wave<0, true>(v, lane);
+      cross_waves<NW>(v, cross, wave, lane);
+      const float f = it.factor * rb_sgn(lane);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const uint2 s = it.sign[q / 8];
+        const uint32_t w = q & 4 ? s.y : s.x;
+        acc[q] = fmaf(__uint_as_float(__float_as_uint(v[q]) ^ ((w << (24 - 8 * (q & 3))) & 0x80000000u)), f, acc[q]);
+      }
+      if constexpr (NW > 1) __syncthreads();         // the exchange is read
+    }
+    if (++j == a.top) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        store8<F32>(reinterpret_cast<uint8_t *>(a.y) + (F32 ? 4 : 2) * ((int64_t)y * a.n + eo + 256 * h), acc + 8 * h);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[q] = 0.0f;
+      j = 0;
+      ++y;
+    }
+  }
+}
+
 // ------------------------------------------------------------ the product
 
 struct XpProduct {
@@ -426,7 +735,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // `part` of `parts` along k.
 struct XpTile { int e; int32_t row0, row1; uint32_t group; int part, parts; };
 
-constexpr uint32_t kCus = 256;                       // of an MI355X; only how work is shared out hangs on it
 
 // Workgroup b's tile, or false. Units are groups of tm rows of an expert, whole ones first, then the experts'
 // remainders, which are shorter. As many whole units as make full rounds on the card come first,
@@ -795,10 +1103,40 @@ int launch_transform_k(const XpRows &a, int64_t groups, hipStream_t st) {
   }
 }
 
+template <int NW, bool OUT, bool F32, bool Z16>
+int launch_blocks_k(const XpRows &a, int64_t most, hipStream_t st) {
+  const int waves = (int)((OUT ? a.n : a.k) / 1024);
+  const size_t shm = NW > 1 ? (size_t)waves * 4096 : 0;
+  const int64_t once = (int64_t)kCus * (24 / waves > 1 ? 24 / waves : 1), groups = most < once ? most : once;
+  if constexpr (OUT) {
+    const int rc = allow_lds<xp_out_blk_k<NW, F32, Z16>>(shm + 2048);          // (and the static part)
+    if (rc) return rc;
+    hipLaunchKernelGGL((xp_out_blk_k<NW, F32, Z16>), dim3((unsigned)groups), dim3(64 * waves), shm, st, a);
+    return hip_status(hipGetLastError(), "xp_out_blk_k");
+  } else {
+    const int rc = allow_lds<xp_in_blk_k<NW, F32>>(shm + 2048);
+    if (rc) return rc;
+    hipLaunchKernelGGL((xp_in_blk_k<NW, F32>), dim3((unsigned)groups), dim3(64 * waves), shm, st, a);
+    return hip_status(hipGetLastError(), "xp_in_blk_k");
+  }
+}
+
+template <bool OUT, bool F32, bool Z16>
+int launch_blocks(const XpRows &a, int64_t most, hipStream_t st) {
+  switch (OUT ? a.log_n : a.log_k) {
+    case 10: return launch_blocks_k<1, OUT, F32, Z16>(a, most, st);
+    case 11: return launch_blocks_k<2, OUT, F32, Z16>(a, most, st);
+    case 12: return launch_blocks_k<4, OUT, F32, Z16>(a, most, st);
+    case 13: return launch_blocks_k<8, OUT, F32, Z16>(a, most, st);
+    default: return launch_blocks_k<16, OUT, F32, Z16>(a, most, st);
+  }
+}
+
 // 8 elements a thread, as many waves as the row (or 8192 of it at a time) takes; whole blocks of 16384 need 16 a thread.
 template <bool OUT, bool F32, bool Z16 = false>
 int launch_transform(const XpRows &a, int64_t groups, hipStream_t st) {
   const int64_t len = OUT ? a.n : a.k;
+  if ((OUT ? a.log_n : a.log_k) >= 10 && len <= 1024 * kRowWaves) return launch_blocks<OUT, F32, Z16>(a, groups, st);
   if ((OUT ? a.log_n : a.log_k) == 14) return launch_transform_k<16, 16, OUT, F32, Z16>(a, groups, st);
   if (len <= 512) return launch_transform_k<8, 1, OUT, F32, Z16>(a, groups, st);
   if (len <= 1024) return launch_transform_k<8, 2, OUT, F32, Z16>(a, groups, st);
@@ -942,7 +1280,7 @@ extern "C" int glq_expert_linear(const glq_experts *E, const glq_expert_rows *R,
   a.xt = reinterpret_cast<uint16_t *>(ws + l.xt), a.rowsum = reinterpret_cast<float *>(ws + l.rowsum);
   a.row_exp = reinterpret_cast<int32_t *>(ws + l.row_exp), a.row_expert = reinterpret_cast<int32_t *>(ws + l.row_expert);
   a.row_parts = reinterpret_cast<int32_t *>(ws + l.row_parts), a.z = ws + l.z;
-  a.k = E->k, a.kp = up64(E->k), a.n = E->n, a.x_rows = R->x_rows;
+  a.k = E->k, a.kp = up64(E->k), a.n = E->n, a.x_rows = R->x_rows, a.out_rows = out;
   a.count = (int32_t)E->count, a.rows = (int32_t)R->rows, a.top = R->pos ? R->top_k : 1, a.ks = plan.ks;
   a.log_k = log_block(E->k), a.log_n = log_block(E->n);
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);

@@ -622,100 +622,6 @@ rht_rows_reg(const void *in, void *out, int64_t rows, int n, int logb, const int
 // 8 rb_ell(l) + 0..7 and 512 + 8 rb_ell(l) + 0..7 of its 1024-element chunk,
 // so each 16-byte load or store of the wave covers one contiguous KiB.
 //
-// The lane stages of rb_fwht_wave pair lanes l and l ^ m for m = 1, 2, 7, 8:
-// each partner read is a single DPP permutation (quad_perm for 1 and 2, the
-// half-row mirror for 7, a rotation by 8 within 16-lane rows for 8), folded
-// into one fused multiply-add per element. Stage j transforms bit j of
-// rb_ell(l) (its pairs differ in exactly that bit), which makes the four
-// stages the Hadamard transform over element bits 3..6. The lower member of
-// a pair (bit j of rb_ell(l) clear) keeps a + b, the upper one a - b instead
-// of b - a: the upper lane's value is then the negated result, a factor
-// rb_sgn(l) = (-1)^popcount(rb_ell(l) & 15) that every later stage carries
-// along unchanged (partners share it) and the output scale removes.
-__device__ __forceinline__ int rb_ell(int l) { return l ^ (((l >> 2) & 1) * 3); }
-__device__ __forceinline__ float rb_sgn(int l) { return (__popc(rb_ell(l) & 15) & 1) ? -1.0f : 1.0f; }
-__device__ __forceinline__ int rb_elem(int p) {
-  return (p & ~1023) | (p & 7) | (((p >> 3) & 1) << 9) | (rb_ell((p >> 4) & 63) << 3);
-}
-
-// One lane stage on 16 registers: v[i] += s * v[i] of the partner lane, the
-// partner read by the DPP control CTRL of a v_fmac_f32_dpp (one VALU
-// operation per element; the compiler does not fold a DPP move into a
-// multiply-add). The leading s_nop gives the two wait states a DPP read needs
-// after a VALU write of its source, which the compiler cannot see through the
-// asm; inside the block each instruction reads its own register only.
-#define RB_FMAC16(CTRL, S)                                                                                  \
-  asm volatile("s_nop 1\n\t"                                                                                \
-               "v_fmac_f32_dpp %0, %0, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
-               "v_fmac_f32_dpp %1, %1, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
-               "v_fmac_f32_dpp %2, %2, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
-               "v_fmac_f32_dpp %3, %3, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
-               "v_fmac_f32_dpp %4, %4, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
-               "v_fmac_f32_dpp %5, %5, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
-               "v_fmac_f32_dpp %6, %6, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
-               "v_fmac_f32_dpp %7, %7, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
-               "v_fmac_f32_dpp %8, %8, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
-               "v_fmac_f32_dpp %9, %9, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
-               "v_fmac_f32_dpp %10, %10, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                        \
-               "v_fmac_f32_dpp %11, %11, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                        \
-               "v_fmac_f32_dpp %12, %12, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                        \
-               "v_fmac_f32_dpp %13, %13, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                        \
-               "v_fmac_f32_dpp %14, %14, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                        \
-               "v_fmac_f32_dpp %15, %15, %16 " CTRL " row_mask:0xf bank_mask:0xf"                            \
-               : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]),         \
-                 "+v"(v[7]), "+v"(v[8]), "+v"(v[9]), "+v"(v[10]), "+v"(v[11]), "+v"(v[12]), "+v"(v[13]),     \
-                 "+v"(v[14]), "+v"(v[15])                                                                    \
-               : "v"(S))
-
-// The FWHT over a wave's 1024 labels (E = 16 registers a lane): registers,
-// then the four DPP lane stages, then lane bits 4 and 5 by lane swaps.
-// Lane bits 4 and 5 (element bits 7 and 8) without the swap back: register
-// pairs (p, p + 8) trade lane bit 4, then lane bit 5, for register bit 3, and
-// the butterfly results stay where the trade left them. Afterwards register
-// bit 3 holds element bit 8, lane bit 5 element bit 7 and lane bit 4 element
-// bit 9 (rb_elem_out); register bits 0..2 are still element bits 0..2, so a
-// lane's 8 registers of one half are 8 consecutive elements.
-template <bool R16>
-__device__ __forceinline__ void rb_stage_swap_keep(float (&v)[16]) {
-#pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const auto r = R16 ? __builtin_amdgcn_permlane16_swap(__float_as_uint(v[p]), __float_as_uint(v[p + 8]), false, false)
-                       : __builtin_amdgcn_permlane32_swap(__float_as_uint(v[p]), __float_as_uint(v[p + 8]), false, false);
-    const float a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
-    v[p] = a + b;
-    v[p + 8] = a - b;
-  }
-}
-
-// element of register i of lane l after rb_fwht_wave<., true>
-__device__ __forceinline__ int rb_elem_out(int l, int i) {
-  return (i & 7) | ((rb_ell(l) & 15) << 3) | (((l >> 5) & 1) << 7) | (((i >> 3) & 1) << 8) | (((l >> 4) & 1) << 9);
-}
-
-template <int FIRST = 0, bool KEEP = false>
-__device__ __forceinline__ void rb_fwht_wave(float (&v)[16], int lane) {
-  // FIRST = 1: the caller has done register stage 0 (element bit 0);
-  // KEEP: the last two stages leave the layout of rb_elem_out
-#pragma unroll
-  for (int s = FIRST; s < 4; ++s) ly_stage_regs<16>(v, s);
-  const int ell = rb_ell(lane);
-  const float s0 = (ell & 1) ? -1.0f : 1.0f, s1 = (ell & 2) ? -1.0f : 1.0f;
-  const float s2 = (ell & 4) ? -1.0f : 1.0f, s3 = (ell & 8) ? -1.0f : 1.0f;
-  RB_FMAC16("quad_perm:[1,0,3,2]", s0);   // lane ^ 1
-  RB_FMAC16("quad_perm:[2,3,0,1]", s1);   // lane ^ 2
-  RB_FMAC16("row_half_mirror", s2);       // lane ^ 7
-  RB_FMAC16("row_ror:8", s3);             // lane ^ 8
-  asm volatile("s_nop 1" ::);
-  if constexpr (KEEP) {
-    rb_stage_swap_keep<true>(v);
-    rb_stage_swap_keep<false>(v);
-  } else {
-    ly_stage_swap<16, true>(v);
-    ly_stage_swap<16, false>(v);
-  }
-}
-#undef RB_FMAC16
-
 template <bool IN_BF16>
 __device__ __forceinline__ void rb_fetch(const void *in, size_t base, uint4 (&r)[IN_BF16 ? 2 : 4]) {
   if constexpr (IN_BF16) {
