@@ -329,19 +329,6 @@ __device__ __forceinline__ int parts_of(int tiles, float inv, int spare) {
   return tiles == 0 ? 0 : (float)(tiles - spare) * inv <= 1.0f ? 1 : (int)__builtin_fmaf((float)tiles, inv, 0.999f);
 }
 
-// inclusive sum, or maximum of values from 0 on, over the lanes up to each (DPP
-// row shifts and broadcasts; the whole wave's in lane 63)
-template <bool MAX> __device__ __forceinline__ int wave_scan(int x) {
-  auto with = [](int a, int b) { return MAX ? (a > b ? a : b) : a + b; };
-  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));   // row_shr 1, 2, 4, 8
-  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
-  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
-  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
-  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));   // row_bcast 15 into rows 1 and 3
-  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));   // row_bcast 31 into rows 2 and 3
-  return x;
-}
-
 // The smallest share for which the launch has workgroups enough for all parts,
 // found by every workgroup alike: up to 64 sequences, one a lane, by bisection;
 // beyond, by parts <= tiles / share + 1.

@@ -190,6 +190,19 @@ __device__ __forceinline__ void append_row(const KvIo &io, const KvPart<D> &p, i
   }
 }
 
+// inclusive sum, or maximum of values from 0 on, over the lanes up to each (DPP
+// row shifts and broadcasts; the whole wave's in lane 63)
+template <bool MAX> __device__ __forceinline__ int wave_scan(int x) {
+  auto with = [](int a, int b) { return MAX ? (a > b ? a : b) : a + b; };
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));   // row_shr 1, 2, 4, 8
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));   // row_bcast 15 into rows 1 and 3
+  x = with(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));   // row_bcast 31 into rows 2 and 3
+  return x;
+}
+
 // ------------------------------------------------------------ argument checks
 
 bool valid_dtype(int dt) { return dt == GLQ_F32 || dt == GLQ_BF16; }

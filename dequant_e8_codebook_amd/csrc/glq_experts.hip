@@ -38,37 +38,6 @@ __device__ __forceinline__ int expert_of(const int32_t *offsets, int count, int3
   return e < count ? e : count - 1;
 }
 
-// Unit u of the row groups, tm rows of one expert each (the last of an expert may be shorter):
-// expert and rows [row0, row1), or false where there are fewer units. Every wave for itself.
-__device__ __forceinline__ bool find_unit(const int32_t *offsets, int count, int32_t rows, uint32_t u, int tm, int &e,
-                                          int32_t &row0, int32_t &row1) {
-  const int lane = threadIdx.x & 63;
-  uint32_t before = 0;
-  for (int c = 0; c < count; c += 64) {
-    const int x = c + lane;
-    const int32_t lo = x < count ? bounded(offsets[x], rows) : 0, hi = x < count ? bounded(offsets[x + 1], rows) : 0;
-    const uint32_t mine = hi > lo ? (uint32_t)((hi - lo - 1) / tm + 1) : 0u;
-    uint32_t up = mine;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const uint32_t y = __shfl_up(up, s);
-      if (lane >= s) up += y;
-    }
-    const uint32_t first = before + up - mine;
-    const unsigned long long hit = __ballot(mine > 0 && first <= u && u < first + mine);
-    if (hit) {
-      const int at = __ffsll((long long)hit) - 1;
-      e = c + at;
-      row0 = __builtin_amdgcn_readlane(lo, at) + (int32_t)(u - (uint32_t)__builtin_amdgcn_readlane((int)first, at)) * tm;
-      const int32_t end = __builtin_amdgcn_readlane(hi, at);
-      row1 = end - row0 < tm ? end : row0 + tm;
-      return true;
-    }
-    before += (uint32_t)__builtin_amdgcn_readlane((int)up, 63);
-  }
-  return false;
-}
-
 // ------------------------------------------------------------ row transforms
 
 struct XpRows {
@@ -90,7 +59,7 @@ struct XpRows {
 };
 
 // The product's steps of 64 inputs, and the first one of part `part` of `parts`
-constexpr int kGemmK = 64, kSplitSteps = 256;        // rows of more steps are not split
+constexpr int kGemmK = 64, kSplitSteps = 256;        // rows of more steps (16384 inputs) are not split
 __device__ __forceinline__ int part_begin(int64_t steps, int part, int parts) { return (int)(steps * part / parts); }
 
 // The transform of up to 64 NW E elements held E a thread, block 2^logb, each thread
@@ -389,7 +358,7 @@ template <int NW, bool F32>
 __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
   extern __shared__ __attribute__((aligned(16))) float4 cross[];
   __shared__ uint32_t tops[kRowWaves];
-  __shared__ float sums[2][8][kRowWaves];
+  __shared__ float sums[2][F32 ? 1 : kSplitSteps];   // of the steps of 64 elements, of this row and the one before
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int32_t first = bounded(a.offsets[0], a.rows), end = bounded(a.offsets[a.count], a.rows);
   int32_t r0, r1;
@@ -418,20 +387,23 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
   int e = 0;
   int32_t until = r0;                                // rows of e end here
   uint32_t flip[8];                                  // sign bits of the elements, two a word (in place of two bf16)
-  int part_of[2] = {0, 0};                           // part along k of the lane's two runs of 8
   const int64_t steps = a.kp / kGemmK;
-  if (!F32 && a.ks > 1)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      for (int p = 1; p < a.ks; ++p) part_of[h] += (eo + 256 * h) / kGemmK >= part_begin(steps, p, a.ks);
   const float inv = rb_sgn(lane) / sqrtf((float)(1 << a.log_k));
-  auto finish = [&](int32_t r) {                     // the row sums of row r, once all its waves have written theirs
-    if (tid <= (a.ks > 1 ? a.ks : 0)) {
-      float some = 0.0f;
-      for (int p = tid ? tid - 1 : 0; p < (tid ? tid : a.ks); ++p)
-        for (int w = 0; w < waves; ++w) some += sums[r & 1][p][w];
-      a.rowsum[tid * (int64_t)a.rows + r] = some;
-    }
+  // The sums of row r, once all its waves have written theirs: eight lanes of the first wave a part along k, then all parts
+  auto finish = [&](int32_t r) {
+    if (wave) return;
+    const int p = lane >> 3;
+    float some = 0.0f;
+    if (p < a.ks)
+      for (int s = part_begin(steps, p, a.ks) + (lane & 7); s < part_begin(steps, p + 1, a.ks); s += 8) some += sums[r & 1][s];
+    some += lane_xor(some, 1);
+    some += lane_xor(some, 2);
+    some += lane_xor(some, 4);
+    if (a.ks > 1 && p < a.ks && (lane & 7) == 0) a.rowsum[(1 + p) * (int64_t)a.rows + r] = some;
+    some += lane_xor(some, 8);
+    some += lane_xor(some, 16);
+    some += lane_xor(some, 32);
+    if (lane == 0) a.rowsum[r] = some;
   };
   for (int32_t r = r0; r < r1; ++r) {
     if (r >= until) {
@@ -501,11 +473,12 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
       }
     }
     if constexpr (!F32) {
-      for (int p = 0; p < a.ks; ++p) {
-        float some = a.ks == 1 ? here[0] + here[1] : (part_of[0] == p ? here[0] : 0.0f) + (part_of[1] == p ? here[1] : 0.0f);
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1) some += lane_xor(some, m);
-        if (lane == 0) sums[r & 1][p][wave] = some;
+      for (int h = 0; h < 2; ++h) {                  // eight neighbouring lanes have a step's 64 elements
+        here[h] += lane_xor(here[h], 1);
+        here[h] += lane_xor(here[h], 2);
+        here[h] += lane_xor(here[h], 4);
+        if ((lane & 7) == 0) sums[r & 1][(eo + 256 * h) / kGemmK] = here[h];
       }
     }
   }
@@ -647,7 +620,8 @@ struct XpProduct {
   void *z;                     // [parts][rows][n]
   int64_t n, k, kp;
   int32_t count, rows;
-  uint32_t n_groups;           // of 128 weight rows, or of 256
+  uint32_t n_groups;           // of 256 weight rows
+  uint32_t likely;             // workgroups that very likely have a tile
   int32_t ks;                  // parts along k of the rows that are split
 };
 
@@ -664,153 +638,89 @@ __device__ __forceinline__ uint4 unbiased(uint4 w) {
   return make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
 }
 
-// Workgroup: 64 rows of an expert by 128 of its weight rows, a wave 16 of those. As in the small-batch product
-// of a layer: a chunk is 32 groups of 8 inputs, lane (j, q) rebuilds groups 8 q .. 8 q + 7 of it for weight
-// row j, and step s of the matrix products takes group 8 q + s.
-template <int BPW, bool G8, bool F32>
-__global__ void __launch_bounds__(512) xp_rows_k(XpProduct a) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  constexpr int P = F32 ? 3 : 1;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 15, q = lane >> 4;
-  int e;
-  int32_t row0, row1;
-  if (!find_unit(a.offsets, a.count, a.rows, blockIdx.x / a.n_groups, 64, e, row0, row1)) return;
-  load_tables<BPW, 512>(lds, a.cb);
-  tables_landed();
-  __syncthreads();
-  const int64_t n0 = (int64_t)(blockIdx.x % a.n_groups) * 128 + 16 * wave, G = a.k / 8;
-  if (n0 >= a.n) return;
-  const int tiles = (row1 - row0 + 15) / 16;
-  const int64_t row = (int64_t)e * a.n + (n0 + j < a.n ? n0 + j : a.n - 1);
-  f32x4 acc[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int64_t c = 0; 32 * c < G; ++c) {
-    const int64_t g0 = 32 * c + 8 * q;
-    const GvRaw raw = gv_load_raw<BPW, G8>(a.idx1, a.idx2, row, G, g0);
-    uint32_t i1[8], i2[8];
-    gv_unpack<BPW>(raw, i1, i2);
-    Dec8<BPW> D;
-    uint4 bv[8];
-    D.run(i1, i2, bv);
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      if constexpr (F32 && BPW > 2) bv[s] = unbiased(bv[s]);
-      if (g0 + s >= G) bv[s] = make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if (t >= tiles) break;
-      const int32_t r = row0 + 16 * t + j < row1 ? row0 + 16 * t + j : row1 - 1;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const uint16_t *x = a.xt + ((int64_t)p * a.rows + r) * a.kp;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const uint4 av = *reinterpret_cast<const uint4 *>(x + 8 * (g0 + s < G ? g0 + s : G - 1));
-          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av), __builtin_bit_cast(bf16x8, bv[s]),
-                                                           acc[t], 0, 0, 0);
-        }
-      }
-    }
-  }
-  if (n0 + j >= a.n) return;
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int32_t r = row0 + 16 * t + 4 * q + i;
-      if (r >= row1) continue;
-      const float bias = F32 || BPW == 2 ? 0.0f : Epi<BPW>::bias * a.rowsum[r];
-      store_z<F32>(a, 0, r, n0 + j, acc[t][i] - bias);
-      if (n0 + j == 0) a.row_parts[r] = 1;
-    }
-}
-
-// ------------------------------------------------------------ many rows: 256 by 256 tiles
+// ------------------------------------------------------------ 256 by 256 tiles
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// What a workgroup of the product does: rows row0 .. row1 - 1 of expert e, its weight rows from 256 group on, part
-// `part` of `parts` along k.
+// A tile: rows row0 .. row1 - 1 of expert e, its weight rows from 256 group on, part `part` of `parts` along k.
 struct XpTile { int e; int32_t row0, row1; uint32_t group; int part, parts; };
 
+// The launch's tiles, numbered. Units are groups of tm rows of an expert, whole ones first, then the experts'
+// remainders, which are shorter. As many whole units as make full rounds on the card come first, unsplit. Where what is left
+// would fill only up to half of a last round, its units are split along k: their parts' z lie in planes of their own that the
+// output's transform adds up, so no part waits for another (4096 tokens, 2 of 8 experts of 4096 x 4096, 576 tiles: 425 -> 400 us
+// whole). Numbers 8 i + x are for XCD x, in runs of neighbouring tiles (the weight rows of one unit).
+struct XpTiles {
+  const XpProduct &a;
+  const int tm, lane;
+  int32_t lo, have;                                  // rows of expert `lane`: begin, number
+  uint32_t whole, rest, lead, first, blocks, all;
 
-// Workgroup b's tile, or false. Units are groups of tm rows of an expert, whole ones first, then the experts'
-// remainders, which are shorter. As many whole units as make full rounds on the card come first,
-// unsplit. Where what is left would fill only up to half of a last round, its units are split along k: their
-// parts' z lie in planes of their own that xp_out_k adds up, so no part waits for another. (8 experts of 4096 x 4096,
-// 8192 rows, 448 tiles and 128 of remainders: see launch_gemm.) Neighbouring tiles (the weight rows of one unit) run on
-// one XCD: blocks go to the eight in turn.
-__device__ __forceinline__ bool find_tile(const XpProduct &a, uint32_t b, int tm, XpTile &tile) {
-  const int lane = threadIdx.x & 63;
-  auto rows_of = [&](int x, int32_t &lo) {
-    lo = x < a.count ? bounded(a.offsets[x], a.rows) : 0;
+  __device__ __forceinline__ void rows_of(int x, int32_t &l, int32_t &n) const {
+    l = x < a.count ? bounded(a.offsets[x], a.rows) : 0;
     const int32_t hi = x < a.count ? bounded(a.offsets[x + 1], a.rows) : 0;
-    return hi > lo ? hi - lo : 0;
-  };
-  uint32_t whole = 0, rest = 0;
-  for (int c = 0; c < a.count; c += 64) {
-    int32_t lo;
-    const int32_t mine = rows_of(c + lane, lo);
-    uint32_t w = (uint32_t)(mine / tm);
-#pragma unroll
-    for (int s = 32; s; s >>= 1) w += __shfl_xor(w, s);
-    whole += (uint32_t)__builtin_amdgcn_readfirstlane((int)w);
-    rest += __popcll(__ballot(mine % tm != 0));
+    n = hi > l ? hi - l : 0;
   }
-  uint32_t lead = whole + rest;                      // units that are not split
-  if (a.ks > 1) {
-    const uint32_t last = (whole + rest) * a.n_groups % kCus;
-    if (last > 0 && last <= kCus / 2) lead = whole * a.n_groups / kCus * kCus / a.n_groups;
-  }
-  auto spread = [](uint32_t i, uint32_t n) {         // i-th block of n -> tile, in runs of an XCD; n: none
-    const uint32_t run = (n + 7) / 8, t = (i % 8) * run + i / 8;
-    return i / 8 < run && t < n ? t : n;
-  };
-  const uint32_t first = lead * a.n_groups, blocks = (first + 7) / 8 * 8;
-  tile.part = 0, tile.parts = 1;
-  uint32_t u;
-  if (b < blocks) {
-    const uint32_t t = spread(b, first);
-    if (t >= first) return false;
-    u = t / a.n_groups, tile.group = t % a.n_groups;
-  } else {
-    const uint32_t n = (whole + rest - lead) * a.n_groups * a.ks, t = spread(b - blocks, n);
-    if (t >= n) return false;
-    u = t / (a.n_groups * a.ks);
-    const uint32_t in = t - u * a.n_groups * a.ks;
-    u += lead;
-    tile.part = (int)(in / a.n_groups), tile.parts = a.ks, tile.group = in % a.n_groups;
-  }
-  const bool is_rest = u >= whole;
-  if (is_rest) u -= whole;
-  uint32_t before = 0;
-  for (int c = 0; c < a.count; c += 64) {
-    int32_t lo;
-    const int32_t have = rows_of(c + lane, lo);
-    const uint32_t mine = is_rest ? (have % tm != 0 ? 1u : 0u) : (uint32_t)(have / tm);
-    uint32_t up = mine;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const uint32_t y = __shfl_up(up, s);
-      if (lane >= s) up += y;
+  __device__ __forceinline__ XpTiles(const XpProduct &product, int rows) : a(product), tm(rows), lane(threadIdx.x & 63) {
+    whole = rest = 0;
+    rows_of(lane, lo, have);
+    for (int c = 0; c < a.count; c += 64) {
+      int32_t l = lo, n = have;
+      if (c) rows_of(c + lane, l, n);
+      whole += (uint32_t)__builtin_amdgcn_readlane(wave_scan<false>(n / tm), 63);
+      rest += __popcll(__ballot(n % tm != 0));
     }
-    const uint32_t at_first = before + up - mine;
-    const unsigned long long hit = __ballot(mine > 0 && at_first <= u && u < at_first + mine);
-    if (hit) {
-      const int at = __ffsll((long long)hit) - 1;
-      tile.e = c + at;
-      const int32_t begin = __builtin_amdgcn_readlane(lo, at), end = begin + __builtin_amdgcn_readlane(have, at);
-      tile.row0 = is_rest ? begin + (end - begin) / tm * tm
-                          : begin + (int32_t)(u - (uint32_t)__builtin_amdgcn_readlane((int)at_first, at)) * tm;
-      tile.row1 = end - tile.row0 < tm ? end : tile.row0 + tm;
-      return true;
+    lead = whole + rest;                             // units that are not split
+    if (a.ks > 1) {
+      const uint32_t last = (whole + rest) * a.n_groups % kCus;
+      if (last > 0 && last <= kCus / 2) lead = whole * a.n_groups / kCus * kCus / a.n_groups;
     }
-    before += (uint32_t)__builtin_amdgcn_readlane((int)up, 63);
+    first = lead * a.n_groups, blocks = (first + 7) / 8 * 8;
+    all = blocks + ((whole + rest - lead) * a.n_groups * a.ks + 7) / 8 * 8;
   }
-  return false;
-}
+  // tile b < all; false where the runs leave a gap
+  __device__ __forceinline__ bool find(uint32_t b, XpTile &tile) const {
+    auto spread = [](uint32_t i, uint32_t n) {       // i-th number -> tile, in runs of an XCD; n: none
+      const uint32_t run = (n + 7) / 8, t = (i % 8) * run + i / 8;
+      return i / 8 < run && t < n ? t : n;
+    };
+    tile.part = 0, tile.parts = 1;
+    uint32_t u;
+    if (b < blocks) {
+      const uint32_t t = spread(b, first);
+      if (t >= first) return false;
+      u = t / a.n_groups, tile.group = t % a.n_groups;
+    } else {
+      const uint32_t n = (whole + rest - lead) * a.n_groups * a.ks, t = spread(b - blocks, n);
+      if (t >= n) return false;
+      u = t / (a.n_groups * a.ks);
+      const uint32_t in = t - u * a.n_groups * a.ks;
+      u += lead;
+      tile.part = (int)(in / a.n_groups), tile.parts = a.ks, tile.group = in % a.n_groups;
+    }
+    const bool is_rest = u >= whole;
+    if (is_rest) u -= whole;
+    uint32_t before = 0;
+    for (int c = 0; c < a.count; c += 64) {
+      int32_t l = lo, n = have;
+      if (c) rows_of(c + lane, l, n);
+      const uint32_t mine = is_rest ? (n % tm != 0 ? 1u : 0u) : (uint32_t)(n / tm), up = (uint32_t)wave_scan<false>((int)mine);
+      const uint32_t at_first = before + up - mine;
+      const unsigned long long hit = __ballot(mine > 0 && at_first <= u && u < at_first + mine);
+      if (hit) {
+        const int at = __ffsll((long long)hit) - 1;
+        tile.e = c + at;
+        const int32_t begin = __builtin_amdgcn_readlane(l, at), end = begin + __builtin_amdgcn_readlane(n, at);
+        tile.row0 = is_rest ? begin + (end - begin) / tm * tm
+                            : begin + (int32_t)(u - (uint32_t)__builtin_amdgcn_readlane((int)at_first, at)) * tm;
+        tile.row1 = end - tile.row0 < tm ? end : tile.row0 + tm;
+        return true;
+      }
+      before += (uint32_t)__builtin_amdgcn_readlane((int)up, 63);
+    }
+    return false;
+  }
+};
 
 constexpr int kGemmThreads = 512, kGemmLda = kGemmK + 8;
 // rows of x~ in LDS, of which there are two tiles: 256 of bf16 x~, 64 of each part of float32 x~
@@ -825,6 +735,7 @@ constexpr size_t gemm_lds(size_t tables, bool f32) { return tables + 2 * sizeof(
 // next step's indices (records, halves, combination) and the tile's loads and writes are spread over them.
 template <int BPW, bool G4, int MB, int P>
 __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, const XpTile &tile, int64_t n0) {
+  const int tid = threadIdx.x;
   const int32_t row0 = tile.row0, row1 = tile.row1;
   const int64_t e = tile.e;
   constexpr bool F32 = P == 3;
@@ -833,7 +744,7 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   constexpr int PIECES = RP / 64;                              // of 64 rows, a part
   uint16_t *As0 = reinterpret_cast<uint16_t *>(lds + lds_table_bytes<BPW>());
   uint16_t *As1 = As0 + gemm_rows(F32) * kGemmLda;
-  const int lane = threadIdx.x & 63, c = lane & 31, p = lane >> 5;
+  const int lane = tid & 63, c = lane & 31, p = lane >> 5;
   const int64_t G = a.k / 8, steps = a.kp / kGemmK;
   const int64_t begin = part_begin(steps, tile.part, tile.parts);
   const int64_t S = part_begin(steps, tile.part + 1, tile.parts) - begin;       // steps of this part
@@ -848,7 +759,7 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   const __amdgpu_buffer_rsrc_t r2 = __builtin_amdgcn_make_buffer_rsrc(
       BPW == 2 ? (void *)a.idx1 : (void *)(reinterpret_cast<const uint8_t *>(a.idx2) + wrow * G * (BPW == 4 ? 2 : 1)), 0,
       (int)(BPW == 2 ? 0 : rows_w * G * (BPW == 4 ? 2 : 1)), 0x00020000);
-  const uint32_t va = (uint32_t)((threadIdx.x >> 3) * a.kp * 2 + 16 * (threadIdx.x & 7));
+  const uint32_t va = (uint32_t)((tid >> 3) * a.kp * 2 + 16 * (tid & 7));
   const uint32_t vi = (uint32_t)(c * G + 4 * p);               // this lane's first index of step 0
   const int sa = (int)(64 * a.kp * 2);
   auto load_a = [&](int64_t s, uint4 (&ra)[P * PIECES]) {
@@ -862,7 +773,7 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   auto store_a = [&](uint16_t *As, const uint4 (&ra)[P * PIECES]) {
 #pragma unroll
     for (int i = 0; i < P * PIECES; ++i)
-      *reinterpret_cast<uint4 *>(As + ((threadIdx.x >> 3) + 64 * i) * kGemmLda + 8 * (threadIdx.x & 7)) = ra[i];
+      *reinterpret_cast<uint4 *>(As + ((tid >> 3) + 64 * i) * kGemmLda + 8 * (tid & 7)) = ra[i];
   };
   // indices of step s as stored; those past a row's end meet zeros of x~
   auto load_idx = [&](int64_t step, uint2 &i1, uint2 &i2) {
@@ -889,8 +800,8 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   load_a(0, ra);
   float row_sum = 0.0f;                                        // thread t: of row row0 + t
   if constexpr (!F32 && BPW > 2)
-    if (threadIdx.x < 256 && (int32_t)threadIdx.x < row1 - row0)
-      row_sum = a.rowsum[(tile.parts > 1 ? 1 + tile.part : 0) * (int64_t)a.rows + row0 + threadIdx.x];
+    if (tid < 256 && tid < row1 - row0)
+      row_sum = a.rowsum[(tile.parts > 1 ? 1 + tile.part : 0) * (int64_t)a.rows + row0 + tid];
   uint2 i1, i2, j1, j2;
   load_idx(0, i1, i2);
   tables_landed();                                             // and the first tile and indices
@@ -1004,10 +915,10 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   // the end of a tile took 15 of 141 us.
   constexpr int ES = F32 ? 4 : 2, SB = 32 * ES + 16, CPR = 32 * ES / 16;        // bytes of an element and of a row, chunks a row
   constexpr bool BIAS = !F32 && BPW > 2;
-  const uint32_t sums = lds_table_bytes<BPW>(), mine = sums + 1024 + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32 * SB;
+  const uint32_t sums = lds_table_bytes<BPW>(), mine = sums + 1024 + (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6) * 32 * SB;
   __syncthreads();                                             // the tiles of x~ are done with
   if constexpr (BIAS) {
-    if (threadIdx.x < 256) lds_stf(sums + 4 * threadIdx.x, row_sum);
+    if (tid < 256) lds_stf(sums + 4 * tid, row_sum);
     __syncthreads();
   }
   typedef __attribute__((address_space(3))) _Float16 lds_f16_w;
@@ -1042,12 +953,20 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   }
 }
 
+// A workgroup a tile, one a CU at a time. (Workgroups that stay and take tile after tile from queues of their XCDs, with one
+// copy of the tables each: level, 282 against 273 us for 512 tiles, and 2 us more where every CU has one tile.) The copy of the tables is
+// under way while the tile is looked for, except in the last workgroups of the launch, which may have none.
 template <int BPW, bool G4, bool F32>
 __global__ void __launch_bounds__(kGemmThreads, 1) xp_gemm_k(XpProduct a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  if (blockIdx.x < a.likely) load_tables<BPW, kGemmThreads>(lds, a.cb);
+  const XpTiles tiles(a, F32 ? 64 : 256);
   XpTile tile;
-  if (!find_tile(a, blockIdx.x, F32 ? 64 : 256, tile)) return;
-  load_tables<BPW, kGemmThreads>(lds, a.cb);         // (only now: LDS loads in flight must not outlive their workgroup)
+  if (blockIdx.x >= tiles.all || !tiles.find(blockIdx.x, tile)) {
+    tables_landed();                                 // LDS loads in flight must not outlive their workgroup
+    return;
+  }
+  if (blockIdx.x >= a.likely) load_tables<BPW, kGemmThreads>(lds, a.cb);
   const int64_t n0 = (int64_t)tile.group * 256 + 32 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t rows = tile.row1 - tile.row0;
   if constexpr (F32) {
@@ -1145,41 +1064,27 @@ int launch_transform(const XpRows &a, int64_t groups, hipStream_t st) {
   return launch_transform_k<8, 16, OUT, F32, Z16>(a, groups, st);
 }
 
-template <int BPW, bool G8, bool F32>
-int launch_rows(XpProduct a, hipStream_t st) {
-  a.n_groups = (uint32_t)((a.n + 127) / 128);
-  // units of 64 rows: no more than this, whatever the offsets are
-  const int64_t groups = (a.rows / 64 + (a.count < a.rows ? a.count : a.rows)) * a.n_groups;
-  if (groups > 0xFFFFFFFFll / 512) return GLQ_ERR_UNSUPPORTED;
-  constexpr size_t shm = lds_table_bytes<BPW>();
-  const int rc = allow_lds<xp_rows_k<BPW, G8, F32>>(shm);
-  if (rc) return rc;
-  hipLaunchKernelGGL((xp_rows_k<BPW, G8, F32>), dim3((unsigned)groups), dim3(512), shm, st, a);
-  return hip_status(hipGetLastError(), "xp_rows_k");
-}
-
 template <int BPW, bool G4, bool F32>
 int launch_gemm(XpProduct a, hipStream_t st) {
   constexpr int TM = F32 ? 64 : 256;
   a.n_groups = (uint32_t)((a.n + 255) / 256);
-  // no more tiles than this, whatever the offsets are, and up to 7 blocks to fill the XCDs' runs of each kind
-  const int64_t groups = (a.rows / TM + (a.count < a.rows ? a.count : a.rows)) * a.n_groups * a.ks + 16;
-  if (groups > 0xFFFFFFFFll / kGemmThreads) return GLQ_ERR_UNSUPPORTED;
+  // no more tiles than this, whatever the offsets are, and up to 7 numbers to fill the XCDs' runs of each kind
+  const int64_t most = (a.rows / TM + (a.count < a.rows ? a.count : a.rows)) * a.n_groups * a.ks + 16;
   constexpr size_t shm = gemm_lds(lds_table_bytes<BPW>(), F32);
+  static_assert(shm <= 160 * 1024, "LDS of a CU");
   const int rc = allow_lds<xp_gemm_k<BPW, G4, F32>>(shm);
   if (rc) return rc;
-  hipLaunchKernelGGL((xp_gemm_k<BPW, G4, F32>), dim3((unsigned)groups), dim3(kGemmThreads), shm, st, a);
+  if (most > 0xFFFFFFFFll / kGemmThreads) return GLQ_ERR_UNSUPPORTED;
+  // (half of the experts with a remainder; where units are split depends on the card's share of the last round)
+  a.likely = (uint32_t)((a.rows / TM + (a.count < a.rows ? a.count : a.rows) / 2) * a.n_groups);
+  hipLaunchKernelGGL((xp_gemm_k<BPW, G4, F32>), dim3((unsigned)most), dim3(kGemmThreads), shm, st, a);
   return hip_status(hipGetLastError(), "xp_gemm_k");
 }
 
 template <int BPW>
-int launch_product(const XpProduct &a, bool gemm, bool f32, hipStream_t st) {
-  if (gemm) {
-    if (a.k % 32 == 0) return f32 ? launch_gemm<BPW, true, true>(a, st) : launch_gemm<BPW, true, false>(a, st);
-    return f32 ? launch_gemm<BPW, false, true>(a, st) : launch_gemm<BPW, false, false>(a, st);
-  }
-  if (a.k % 64 == 0) return f32 ? launch_rows<BPW, true, true>(a, st) : launch_rows<BPW, true, false>(a, st);
-  return f32 ? launch_rows<BPW, false, true>(a, st) : launch_rows<BPW, false, false>(a, st);
+int launch_product(const XpProduct &a, bool f32, hipStream_t st) {     // four indices of a row in one load, or one by one
+  if (a.k % 32 == 0) return f32 ? launch_gemm<BPW, true, true>(a, st) : launch_gemm<BPW, true, false>(a, st);
+  return f32 ? launch_gemm<BPW, false, true>(a, st) : launch_gemm<BPW, false, false>(a, st);
 }
 
 int check_experts(const glq_experts *E) {
@@ -1195,20 +1100,14 @@ int check_experts(const glq_experts *E) {
   return GLQ_OK;
 }
 
-// Which product, and how many parts along k its split units have.
-//
-// 256 x 256 tiles where experts have at least 32 rows on average, else 64 x 128.
-struct XpPlan { bool gemm; int ks; };
-XpPlan xp_plan(int64_t count, int64_t n, int64_t k, int64_t rows, bool f32) {
-  XpPlan p = {rows >= 32 * count, 1};
-  const int64_t steps = up64(k) / kGemmK, tm = f32 ? 64 : 256, groups = (n + 255) / 256;
-  if (!p.gemm || steps > kSplitSteps || steps < 16) return p;
-  // the most tiles there can be; as many parts as give each CU one, but none under 8 steps, which would not pay for the copy of
-  // the tables
-  const int64_t most = (rows / tm + (count < rows ? count : rows)) * groups;
-  p.ks = 2;
-  while (p.ks < 8 && most * 2 * p.ks <= kCus && steps / (2 * p.ks) >= 8) p.ks *= 2;
-  return p;
+// Parts along k of the units that are split (XpTiles): as many as give each CU one, for the most tiles there can be, but none under
+// 4 steps, which would not pay for the transforms' reading more planes.
+int xp_parts(int64_t count, int64_t n, int64_t k, int64_t rows, bool f32) {
+  const int64_t steps = up64(k) / kGemmK, most = (rows / (f32 ? 64 : 256) + (count < rows ? count : rows)) * ((n + 255) / 256);
+  if (steps > kSplitSteps || steps < 8) return 1;
+  int ks = 2;
+  while (ks < 8 && most * 2 * ks <= kCus && steps / (2 * ks) >= 4) ks *= 2;
+  return ks;
 }
 
 // Bytes of z's planes for up to this many rows: two of either type, or four or eight where the rule above can ask for
@@ -1272,7 +1171,7 @@ extern "C" int glq_expert_linear(const glq_experts *E, const glq_expert_rows *R,
   uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
   const XpLayout l = xp_layout(E, R->rows);
   const bool f32 = R->x_dt == GLQ_F32;
-  const XpPlan plan = xp_plan(E->count, E->n, E->k, R->rows, f32);
+  const int ks = xp_parts(E->count, E->n, E->k, R->rows, f32);
   XpRows a = {};
   a.x = R->x, a.y = R->y, a.offsets = R->offsets, a.src = R->src, a.pos = R->pos, a.weights = R->weights;
   a.sign_k = E->sign_k, a.sign_n = E->sign_n, a.scale = E->scale, a.row_scale = E->row_scale;
@@ -1281,16 +1180,15 @@ extern "C" int glq_expert_linear(const glq_experts *E, const glq_expert_rows *R,
   a.row_exp = reinterpret_cast<int32_t *>(ws + l.row_exp), a.row_expert = reinterpret_cast<int32_t *>(ws + l.row_expert);
   a.row_parts = reinterpret_cast<int32_t *>(ws + l.row_parts), a.z = ws + l.z;
   a.k = E->k, a.kp = up64(E->k), a.n = E->n, a.x_rows = R->x_rows, a.out_rows = out;
-  a.count = (int32_t)E->count, a.rows = (int32_t)R->rows, a.top = R->pos ? R->top_k : 1, a.ks = plan.ks;
+  a.count = (int32_t)E->count, a.rows = (int32_t)R->rows, a.top = R->pos ? R->top_k : 1, a.ks = ks;
   a.log_k = log_block(E->k), a.log_n = log_block(E->n);
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   if (R->rows > 0) {
     rc = f32 ? launch_transform<false, true>(a, R->rows, st) : launch_transform<false, false>(a, R->rows, st);
     if (rc) return rc;
     const XpProduct p = {E->idx1, a.xt, E->idx2, reinterpret_cast<const uint8_t *>(E->cb), a.rowsum, a.offsets,
-                         a.row_parts, ws + l.z, E->n, E->k, a.kp, a.count, a.rows, 0, plan.ks};
-    rc = E->bpw == 2 ? launch_product<2>(p, plan.gemm, f32, st) : E->bpw == 3 ? launch_product<3>(p, plan.gemm, f32, st)
-                                                                 : launch_product<4>(p, plan.gemm, f32, st);
+                         a.row_parts, ws + l.z, E->n, E->k, a.kp, a.count, a.rows, 0, 0, ks};
+    rc = E->bpw == 2 ? launch_product<2>(p, f32, st) : E->bpw == 3 ? launch_product<3>(p, f32, st) : launch_product<4>(p, f32, st);
     if (rc) return rc;
   }
   if (f32) return R->y_dt == GLQ_F32 ? launch_transform<true, true>(a, out, st) : launch_transform<true, false>(a, out, st);
