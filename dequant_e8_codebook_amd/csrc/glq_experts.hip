@@ -48,9 +48,9 @@ struct XpRows {
   const int8_t *sign_k, *sign_n;
   uint16_t *xt;                // [planes][rows][kp] bf16: x~, or three parts that add up to it; zeros from k on
   float *rowsum;               // [1 + ks][rows] sums of x~, whole and of each part along k (bf16 path)
-  int32_t *row_exp;            // [rows] exponents of the rows of z (bf16 path)
+  float *row_factor;           // [rows] what z's row is to be multiplied by, but for the transform's 1 / sqrt(block)
   int32_t *row_expert, *row_parts;   // [rows]
-  const void *z;               // [parts][rows][n]: float32, or float16 times 2^row_exp
+  const void *z;               // [parts][rows][n]: float32 or float16, both without row_factor
   const float *scale, *row_scale;
   float unit;                  // of the operands: 1, 1/4 or 1/8 of a weight at 2, 3 or 4 bits
   int64_t k, kp, n, x_rows, out_rows;    // kp: k up to a multiple of 64
@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(64 * NW) xp_in_k(XpRows a) {
       for (int w = 0; w < NW; ++w) top = top > tops[w] ? top : tops[w];
     }
     shift = row_exponent(top, a.k);
-    if (tid == 0) a.row_exp[r] = shift;
   }
+  if (tid == 0) a.row_factor[r] = ldexpf(a.scale[e] * a.unit, shift);
   for (int64_t s0 = 0; s0 < a.kp; s0 += SEG) {
     if (s0) {
 #pragma unroll
@@ -252,8 +252,7 @@ __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
       const int32_t r = a.pos ? a.pos[row_y * a.top + j] : (int32_t)row_y;
       if (r < first || r >= end) continue;           // uniform
       const int e = a.row_expert[r], parts = a.row_parts[r];
-      float w = a.pos ? a.weights[row_y * a.top + j] * inv : inv;
-      w *= a.unit * (Z16 ? ldexpf(a.scale[e], a.row_exp[r]) : a.scale[e]);
+      const float w = (a.pos ? a.weights[row_y * a.top + j] * inv : inv) * a.row_factor[r];
       const int8_t *signs = a.sign_n + (int64_t)e * a.n;
       float v[E];
 #pragma unroll
@@ -385,6 +384,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
   };
   fetch(r0);
   int e = 0;
+  float scale = 0.0f;
   int32_t until = r0;                                // rows of e end here
   uint32_t flip[8];                                  // sign bits of the elements, two a word (in place of two bf16)
   const int64_t steps = a.kp / kGemmK;
@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
     if (r >= until) {
       e = expert_of(a.offsets, a.count, r);
       until = bounded(a.offsets[e + 1], a.rows);
+      scale = a.scale[e] * a.unit;
       const int8_t *signs = a.sign_k + (int64_t)e * a.k + el;
       const uint2 s0 = *reinterpret_cast<const uint2 *>(signs), s1 = *reinterpret_cast<const uint2 *>(signs + 512);
       const uint32_t s[4] = {s0.x, s0.y, s1.x, s1.y};
@@ -418,7 +419,6 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
         flip[i] = (two & 0x80u) << 8 | (two & 0x8000u) << 16;
       }
     }
-    if (tid == 0) a.row_expert[r] = e;
     float v[16];
     uint32_t top = 0;
     if constexpr (F32) {
@@ -443,14 +443,15 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
     }
     if (r + 1 < r1) fetch(r + 1);
     if (waves > 1) __syncthreads();                  // tops; the exchange and the sums of the row before are through
+    int shift = 0;
     if constexpr (!F32) {
       if (r > r0) finish(r - 1);
       for (int w = 0; w < waves; ++w) top = top > tops[w] ? top : tops[w];
-      const int shift = row_exponent(top << 16, a.k);
-      if (tid == 0) a.row_exp[r] = shift;
+      shift = row_exponent(top << 16, a.k);
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = ldexpf(v[i], -shift);
     }
+    if (tid == 0) a.row_expert[r] = e, a.row_factor[r] = ldexpf(scale, shift);
     rb_fwht_wave<0, true>(v, lane);
     cross_waves<NW>(v, cross, wave, lane);
     float here[2] = {0.0f, 0.0f};
@@ -488,38 +489,48 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
   }
 }
 
-// Items are rows of z: the rows themselves, or each token's choices one after the other. A wave's lanes look up 64 items at a
-// time (row, expert, factor), so the chain of loads behind a choice is gone through once for them all.
+// Items are rows of z: the rows themselves, or each token's choices. A wave's lanes look up 64 items at a time (row, expert,
+// factor), so the chain of loads behind a choice is gone through once for them all. With few tokens a workgroup has several sets
+// of waves (GROUPS of them, blockDim over the row's waves): set s takes choices s, s + GROUPS, ... and the sets' sums
+// meet in LDS.
 template <int NW, bool F32, bool Z16>
 __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
   extern __shared__ __attribute__((aligned(16))) float4 cross[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int waves = (int)(a.n >> 10), sets = (int)(blockDim.x >> 6) / waves, set = wave / waves;
   const int32_t first = bounded(a.offsets[0], a.rows), end = bounded(a.offsets[a.count], a.rows);
   int32_t y0, y1;
   my_run(a.pos ? 0 : first, a.pos ? a.out_rows : end > first ? end - first : 0, y0, y1);
   if (y0 >= y1) return;
-  const int el = 1024 * wave + 8 * rb_ell(lane), eo = 1024 * wave + rb_elem_out(lane, 0);
-  const float inv = a.unit / sqrtf((float)(1 << a.log_n));
-  constexpr int RAW = Z16 ? 2 : 4;
-  const int64_t items = (int64_t)(y1 - y0) * a.top;
+  const int el = 1024 * (wave - set * waves) + 8 * rb_ell(lane), eo = 1024 * (wave - set * waves) + rb_elem_out(lane, 0);
+  const float inv = 1.0f / sqrtf((float)(1 << a.log_n));
+  constexpr int RAW = Z16 ? 2 : 4, ES = Z16 ? 2 : 4;
+  const int turns = (a.top + sets - 1) / sets;       // items of a token that a set has
+  const int64_t items = (int64_t)(y1 - y0) * turns;
   int32_t row = -1, expert = 0, parts = 0;           // of item base + lane
   float factor = 0.0f;
   int64_t base = -64;
   struct Item { int32_t row, parts; float factor; uint4 raw[RAW]; uint2 sign[2]; };
+  auto plane = [&](int p, int32_t r, uint4 (&raw)[RAW]) {
+    const uint4 *z = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.z) + ES * (((int64_t)p * a.rows + r) * a.n + el));
+    if constexpr (Z16) raw[0] = z[0], raw[1] = z[64];
+    else raw[0] = z[0], raw[1] = z[1], raw[2] = z[128], raw[3] = z[129];
+  };
   auto fetch = [&](int64_t i, Item &it) {
     if (i >= base + 64) {
       base = i;
       row = -1;
-      if (i + lane < items) {
-        row = a.pos ? a.pos[(int64_t)y0 * a.top + i + lane] : (int32_t)(y0 + i + lane);
+      const int64_t mine = i + lane, y = mine / turns;
+      const int j = (int)(mine - y * turns) * sets + set;
+      if (mine < items && j < a.top) {
+        row = a.pos ? a.pos[(y0 + y) * a.top + j] : (int32_t)(y0 + y);
         if (row < first || row >= end) row = -1;
         factor = inv;
-        if (a.pos) factor *= a.weights[(int64_t)y0 * a.top + i + lane];
+        if (a.pos) factor *= a.weights[(y0 + y) * a.top + j];
       }
       if (row >= 0) {
         expert = a.row_expert[row], parts = a.row_parts[row];
-        factor *= a.scale[expert];
-        if constexpr (Z16) factor = ldexpf(factor, a.row_exp[row]);
+        factor *= a.row_factor[row];
       }
     }
     const int at = (int)(i - base);
@@ -528,9 +539,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
     it.parts = __builtin_amdgcn_readlane(parts, at);
     it.factor = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(factor), at));
     const int64_t e = __builtin_amdgcn_readlane(expert, at);
-    const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.z) + (Z16 ? 2 : 4) * ((int64_t)it.row * a.n + el));
-    if constexpr (Z16) it.raw[0] = p[0], it.raw[1] = p[64];
-    else it.raw[0] = p[0], it.raw[1] = p[1], it.raw[2] = p[128], it.raw[3] = p[129];
+    plane(0, it.row, it.raw);
     const int8_t *signs = a.sign_n + e * a.n + eo;
     it.sign[0] = *reinterpret_cast<const uint2 *>(signs), it.sign[1] = *reinterpret_cast<const uint2 *>(signs + 256);
   };
@@ -556,21 +565,18 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
   Item next;
   fetch(0, next);
-  int j = 0;
+  int turn = 0;
   int32_t y = y0;
   for (int64_t i = 0; i < items; ++i) {
     const Item it = next;
     if (i + 1 < items) fetch(i + 1, next);
+    float v[16];
     if (it.row >= 0) {
-      float v[16];
       spread(it.raw, v);
       for (int p = 1; p < it.parts; ++p) {
-        const uint4 *z = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.z) +
-                                                         (Z16 ? 2 : 4) * (((int64_t)p * a.rows + it.row) * a.n + el));
         uint4 raw[RAW];
-        if constexpr (Z16) raw[0] = z[0], raw[1] = z[64];
-        else raw[0] = z[0], raw[1] = z[1], raw[2] = z[128], raw[3] = z[129];
         float x[16];
+        plane(p, it.row, raw);
         spread(raw, x);
 #pragma unroll
         for (int q = 0; q < 16; ++q) v[q] += x[q];
@@ -586,23 +592,46 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
         }
       }
       rb_fwht_wave<0, true>(v, lane);
-      cross_waves<NW>(v, cross, wave, lane);
-      const float f = it.factor * rb_sgn(lane);
+    } else if (sets > 1) {                           // (the other sets may have a row: the exchange's barriers are all waves')
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const uint2 s = it.sign[q / 8];
-        const uint32_t w = q & 4 ? s.y : s.x;
-        acc[q] = fmaf(__uint_as_float(__float_as_uint(v[q]) ^ ((w << (24 - 8 * (q & 3))) & 0x80000000u)), f, acc[q]);
+      for (int q = 0; q < 16; ++q) v[q] = 0.0f;
+    }
+    if (it.row >= 0 || sets > 1) {
+      cross_waves<NW>(v, cross, wave, lane);
+      if (it.row >= 0) {
+        const float f = it.factor * rb_sgn(lane);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const uint2 s = it.sign[q / 8];
+          const uint32_t w = q & 4 ? s.y : s.x;
+          acc[q] = fmaf(__uint_as_float(__float_as_uint(v[q]) ^ ((w << (24 - 8 * (q & 3))) & 0x80000000u)), f, acc[q]);
+        }
       }
       if constexpr (NW > 1) __syncthreads();         // the exchange is read
     }
-    if (++j == a.top) {
+    if (++turn == turns) {
+      if (sets > 1) {
+        if (set > 0)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        store8<F32>(reinterpret_cast<uint8_t *>(a.y) + (F32 ? 4 : 2) * ((int64_t)y * a.n + eo + 256 * h), acc + 8 * h);
+          for (int q = 0; q < 4; ++q)
+            cross[(4 * wave + q) * 64 + lane] = make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+        __syncthreads();
+        if (set == 0)
+          for (int s = 1; s < sets; ++s)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float4 f = cross[(4 * (wave + s * waves) + q) * 64 + lane];
+              acc[4 * q] += f.x, acc[4 * q + 1] += f.y, acc[4 * q + 2] += f.z, acc[4 * q + 3] += f.w;
+            }
+        __syncthreads();
+      }
+      if (set == 0)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          store8<F32>(reinterpret_cast<uint8_t *>(a.y) + (F32 ? 4 : 2) * ((int64_t)y * a.n + eo + 256 * h), acc + 8 * h);
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[q] = 0.0f;
-      j = 0;
+      turn = 0;
       ++y;
     }
   }
@@ -1025,12 +1054,16 @@ int launch_transform_k(const XpRows &a, int64_t groups, hipStream_t st) {
 template <int NW, bool OUT, bool F32, bool Z16>
 int launch_blocks_k(const XpRows &a, int64_t most, hipStream_t st) {
   const int waves = (int)((OUT ? a.n : a.k) / 1024);
-  const size_t shm = NW > 1 ? (size_t)waves * 4096 : 0;
+  // the output's sets of waves: as many as choices and a workgroup take, where there are fewer tokens than CUs
+  int sets = 1;
+  if (OUT && most <= kCus)
+    while (2 * sets * waves <= kRowWaves && sets < a.top) sets *= 2;
+  const size_t shm = NW > 1 || sets > 1 ? (size_t)waves * sets * 4096 : 0;
   const int64_t once = (int64_t)kCus * (24 / waves > 1 ? 24 / waves : 1), groups = most < once ? most : once;
   if constexpr (OUT) {
     const int rc = allow_lds<xp_out_blk_k<NW, F32, Z16>>(shm + 2048);          // (and the static part)
     if (rc) return rc;
-    hipLaunchKernelGGL((xp_out_blk_k<NW, F32, Z16>), dim3((unsigned)groups), dim3(64 * waves), shm, st, a);
+    hipLaunchKernelGGL((xp_out_blk_k<NW, F32, Z16>), dim3((unsigned)groups), dim3(64 * waves * sets), shm, st, a);
     return hip_status(hipGetLastError(), "xp_out_blk_k");
   } else {
     const int rc = allow_lds<xp_in_blk_k<NW, F32>>(shm + 2048);
@@ -1123,13 +1156,13 @@ int64_t z_bytes(int64_t n, int64_t rows) {
   return need;
 }
 
-struct XpLayout { int64_t xt, rowsum, row_exp, row_expert, row_parts, z, total; };
+struct XpLayout { int64_t xt, rowsum, row_factor, row_expert, row_parts, z, total; };
 XpLayout xp_layout(const glq_experts *E, int64_t rows) {
   XpLayout w;
   w.xt = 0;
   w.rowsum = w.xt + up256(rows * up64(E->k) * 6);    // float32 rows: three parts of 2 bytes
-  w.row_exp = w.rowsum + up256(rows * 4 * 9);        // whole, and eight parts at most
-  w.row_expert = w.row_exp + up256(rows * 4);
+  w.row_factor = w.rowsum + up256(rows * 4 * 9);        // whole, and eight parts at most
+  w.row_expert = w.row_factor + up256(rows * 4);
   w.row_parts = w.row_expert + up256(rows * 4);
   w.z = w.row_parts + up256(rows * 4);
   w.total = w.z + up256(z_bytes(E->n, rows));
@@ -1177,7 +1210,7 @@ extern "C" int glq_expert_linear(const glq_experts *E, const glq_expert_rows *R,
   a.sign_k = E->sign_k, a.sign_n = E->sign_n, a.scale = E->scale, a.row_scale = E->row_scale;
   a.unit = E->bpw == 2 ? Epi<2>::mul : E->bpw == 3 ? Epi<3>::mul : Epi<4>::mul;
   a.xt = reinterpret_cast<uint16_t *>(ws + l.xt), a.rowsum = reinterpret_cast<float *>(ws + l.rowsum);
-  a.row_exp = reinterpret_cast<int32_t *>(ws + l.row_exp), a.row_expert = reinterpret_cast<int32_t *>(ws + l.row_expert);
+  a.row_factor = reinterpret_cast<float *>(ws + l.row_factor), a.row_expert = reinterpret_cast<int32_t *>(ws + l.row_expert);
   a.row_parts = reinterpret_cast<int32_t *>(ws + l.row_parts), a.z = ws + l.z;
   a.k = E->k, a.kp = up64(E->k), a.n = E->n, a.x_rows = R->x_rows, a.out_rows = out;
   a.count = (int32_t)E->count, a.rows = (int32_t)R->rows, a.top = R->pos ? R->top_k : 1, a.ks = ks;
