@@ -14,6 +14,7 @@
 
 #include "glq.h"
 #include "glq_cache.h"
+#include "glq_fwht.h"
 
 namespace glq {
 namespace {
@@ -59,115 +60,163 @@ constexpr int kPlanThreads = 256, kPlanTile = 2048, kPlanChunk = 1024;
 
 enum PlanList { kNew, kRead, kPages };
 
-// Every workgroup writes one tile of one of three lists: the new tokens' slots
-// and positions, all cached tokens' slots, the pages taken. It sums up the requests'
-// counts itself (1024 requests at a time, in 64 bits), which costs less than a
-// launch that would do it for all; an entry finds its request by bisection in
-// LDS. A page taken in this call is read from the list of free pages, never
-// from the table, so no workgroup waits for another.
+// Sums that stop at 2^31 - 1: no list is longer, and what begins there is past its end.
+__device__ __forceinline__ int32_t capped(int32_t x, int32_t y) {
+  const uint32_t s = (uint32_t)x + (uint32_t)y;
+  return s < 0x7FFFFFFFu ? (int32_t)s : INT32_MAX;
+}
+__device__ __forceinline__ int32_t capped_scan(int32_t x) {    // inclusive, over the lanes of a wave
+  x = capped(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));    // row_shr 1, 2, 4, 8
+  x = capped(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
+  x = capped(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
+  x = capped(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
+  x = capped(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));    // row_bcast 15 into rows 1 and 3
+  x = capped(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));    // row_bcast 31 into rows 2 and 3
+  return x;
+}
+
 struct PlanShared {
-  int64_t begin[kPlanChunk], taken[kPlanChunk];      // entries of the list and pages before a request
+  int32_t begin[kPlanChunk], taken[kPlanChunk];      // entries of the list and pages before a request
   int32_t len[kPlanChunk], held[kPlanChunk];
-  int64_t wave_sum[2][kPlanThreads / 64];
+  int32_t wave_sum[2][kPlanThreads / 64];
 };
 
+// Every workgroup writes one tile of one of three lists: the new tokens' slots
+// and positions, all cached tokens' slots, the pages taken. It sums up the requests'
+// counts itself (1024 requests at a time), which costs less than a launch that would do it for all; an
+// entry finds its request by bisection in LDS. A page taken in this call is read from the list of free pages,
+// never from the table, so no workgroup waits for another. A short tile has one entry a thread; in a full one a
+// thread has 8 neighbouring entries, found by one bisection and a few steps, their pages asked for together.
+// Bound by latency: launch, lengths, sums and bisection, pages, 4 us in all.
 // Returns the number of entries that the list has in all (the tokens lists: counted as far as the tile).
 template <PlanList LIST>
-__device__ __forceinline__ int64_t plan_tile(const PlanArgs &a, PlanShared &sh, int64_t tile, bool first) {
-  auto &begin = sh.begin, &taken = sh.taken;
-  auto &len = sh.len, &held = sh.held;
+__device__ __forceinline__ int32_t plan_tile(const PlanArgs &a, PlanShared &sh, int64_t tile, bool first) {
+  auto &begin = sh.begin, &taken = sh.taken, &len = sh.len, &held = sh.held;
   auto &wave_sum = sh.wave_sum;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t most = LIST == kNew ? a.max_tokens : LIST == kRead ? a.max_read : INT64_MAX;
-  const int64_t t0 = tile * kPlanTile;
-  int64_t t1 = t0 + kPlanTile < most ? t0 + kPlanTile : most;
-  const int64_t page = int64_t(1) << a.page_shift;
+  const int32_t most = LIST == kNew ? (int32_t)a.max_tokens : LIST == kRead ? (int32_t)a.max_read : INT32_MAX;
+  const int32_t t0 = tile < INT32_MAX / kPlanTile ? (int32_t)tile * kPlanTile : INT32_MAX;
+  const int32_t t1 = most - t0 < kPlanTile ? (most > t0 ? most : t0) : t0 + kPlanTile;
+  const int32_t page = 1 << a.page_shift, max_pages = (int32_t)a.max_pages, num_free = (int32_t)a.num_free;
   auto pages_of = [&](int64_t tokens) {
     const int64_t p = (tokens + page - 1) >> a.page_shift;
-    return p < a.max_pages ? p : a.max_pages;
+    return p < max_pages ? (int32_t)p : max_pages;
   };
-  int64_t before = 0, pages_before = 0;                        // of the chunks behind
+  int32_t before = 0, pages_before = 0;                        // of the chunks behind
   for (int64_t c = 0; c < a.batch; c += kPlanChunk) {
     if (LIST != kPages && !first && before >= t1) break;       // uniform
-    int64_t n[4], p[4], nsum = 0, psum = 0;
-    int32_t l[4], h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t b = c + 4 * tid + i;
-      const int64_t have = b < a.batch && a.lens[b] > 0 ? a.lens[b] : 0, add = b < a.batch && a.added[b] > 0 ? a.added[b] : 0;
-      const int64_t ph = pages_of(have), pt = pages_of(have + add);
-      l[i] = (int32_t)have;
-      h[i] = (int32_t)ph;
-      p[i] = psum;
-      n[i] = nsum;
-      psum += pt - ph;
-      nsum += LIST == kNew ? add : LIST == kRead ? have + add : pt - ph;
-      if (LIST == kNew && first && b < a.batch)
-        a.new_lens[b] = (int32_t)(have + add < INT32_MAX ? have + add : INT32_MAX);
-    }
-    int64_t nup = nsum, pup = psum;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int64_t x = __shfl_up(nup, s), y = __shfl_up(pup, s);
-      if (lane >= s) nup += x, pup += y;
-    }
-    __syncthreads();                                           // the chunk before is done with LDS
-    if (lane == 63) wave_sum[0][wave] = nup, wave_sum[1][wave] = pup;
-    __syncthreads();
-    int64_t nbase = before + nup - nsum, pbase = pages_before + pup - psum, ntotal = 0, ptotal = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanThreads / 64; ++w) {
-      if (w < wave) nbase += wave_sum[0][w], pbase += wave_sum[1][w];
-      ntotal += wave_sum[0][w], ptotal += wave_sum[1][w];
-    }
+    const int n_here = a.batch - c < kPlanChunk ? (int)(a.batch - c) : kPlanChunk;
+    int32_t n[4], p[4], l[4], h[4], nsum = 0, psum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int at = 4 * tid + i;
-      begin[at] = nbase + n[i];
-      taken[at] = pbase + p[i];
+      const int32_t x = at < n_here ? a.lens[c + at] : 0, y = at < n_here ? a.added[c + at] : 0;
+      l[i] = x > 0 ? x : 0;
+      n[i] = y > 0 ? y : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int32_t ph = pages_of(l[i]), pt = pages_of((int64_t)l[i] + n[i]), all = capped(l[i], n[i]);
+      if (LIST == kNew && first && 4 * tid + i < n_here) a.new_lens[c + 4 * tid + i] = all;
+      const int32_t mine = LIST == kNew ? n[i] : LIST == kRead ? all : pt - ph;
+      h[i] = ph;
+      p[i] = psum, n[i] = nsum;
+      psum = capped(psum, pt - ph), nsum = capped(nsum, mine);
+    }
+    const int32_t nup = capped_scan(nsum), pup = capped_scan(psum);
+    // (sums up to the lane before: the cap is never taken off)
+    const int32_t nlow = __builtin_amdgcn_update_dpp(0, nup, 0x138, 0xF, 0xF, false);    // wave_shr 1
+    const int32_t plow = __builtin_amdgcn_update_dpp(0, pup, 0x138, 0xF, 0xF, false);
+    __syncthreads();                                           // the chunk before is done with LDS
+    if (lane == 63) wave_sum[0][wave] = nup, wave_sum[1][wave] = pup;
+    __syncthreads();
+    int32_t nbase = before, pbase = pages_before, ntotal = before, ptotal = pages_before;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 64; ++w) {
+      if (w < wave) nbase = capped(nbase, wave_sum[0][w]), pbase = capped(pbase, wave_sum[1][w]);
+      ntotal = capped(ntotal, wave_sum[0][w]), ptotal = capped(ptotal, wave_sum[1][w]);
+    }
+    nbase = capped(nbase, nlow), pbase = capped(pbase, plow);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = 4 * tid + i;
+      const int32_t start = capped(nbase, n[i]);
+      begin[at] = at < n_here ? start : INT32_MAX;
+      taken[at] = capped(pbase, p[i]);
       len[at] = l[i];
       held[at] = h[i];
-      if (LIST != kPages && first && c + at < a.batch) {
-        int32_t *cu = LIST == kNew ? a.cu_q : a.cu_k;
-        cu[c + at] = (int32_t)(nbase + n[i] < most ? nbase + n[i] : most);
-      }
+      if (LIST != kPages && first && at < n_here) (LIST == kNew ? a.cu_q : a.cu_k)[c + at] = start < most ? start : most;
     }
     __syncthreads();
-    const int64_t end = before + ntotal < t1 ? before + ntotal : t1;
-    for (int64_t i = (t0 > before ? t0 : before) + tid; i < end; i += kPlanThreads) {
-      int at = 0;                                              // the last request that begins at i or before
+    const int32_t from = t0 > before ? t0 : before, end = ntotal < t1 ? ntotal : t1;
+    int top = 1;                                               // a power of two that holds the requests
+    while (top < n_here) top <<= 1;
+    auto entry = [&](auto per, int32_t i0) {                   // entries i0 .. i0 + PER - 1 within from .. end
+      constexpr int PER = decltype(per)::value;
+      int at = 0;                                              // the last request that begins at the first of them or before
+      const int32_t i1 = i0 > from ? i0 : from;
+      for (int s = top >> 1; s; s >>= 1)
+        if (begin[at + s] <= i1) at += s;
+      int32_t pg[PER], in[PER];
 #pragma unroll
-      for (int s = kPlanChunk / 2; s; s >>= 1)
-        if (begin[at + s] <= i) at += s;
-      const int64_t b = c + at, nth = i - begin[at];
-      if constexpr (LIST == kPages) {
-        a.table[b * a.max_pages + held[at] + nth] = i < a.num_free ? a.free_pages[i] : -1;
-      } else {
-        const int64_t t = LIST == kNew ? len[at] + nth : nth, e = t >> a.page_shift;
-        int32_t pg = -1;
-        if (e < held[at]) {
-          pg = a.table[b * a.max_pages + e];
-        } else if (e < a.max_pages) {
-          const int64_t f = taken[at] + e - held[at];
-          if (f < a.num_free) pg = a.free_pages[f];
-        }
-        const int32_t slot = pg >= 0 && pg < a.num_pages ? (pg << a.page_shift) + (int32_t)(t & (page - 1)) : -1;
-        if constexpr (LIST == kNew) {
-          a.slots[i] = slot;
-          a.positions[i] = (int32_t)(t < INT32_MAX ? t : INT32_MAX);
+      for (int x = 0; x < PER; ++x) {
+        const int32_t i = i0 + x;
+        pg[x] = -1, in[x] = 0;
+        if (i < from || i >= end) continue;
+        if constexpr (PER > 1)
+          while (at + 1 < n_here && begin[at + 1] <= i) ++at;
+        const int32_t nth = i - begin[at];
+        if constexpr (LIST == kPages) {
+          a.table[(c + at) * a.max_pages + held[at] + nth] = i < num_free ? a.free_pages[i] : -1;
         } else {
-          a.read_slots[i] = slot;
+          const int64_t t = LIST == kNew ? (int64_t)len[at] + nth : nth, e = t >> a.page_shift;
+          in[x] = t < INT32_MAX ? (int32_t)t : INT32_MAX;
+          const int64_t f = taken[at] + e - held[at];
+          const int32_t *src = e < held[at] ? a.table + (c + at) * a.max_pages + e : e < max_pages && f < num_free ? a.free_pages + f
+                                                                                                                 : nullptr;
+          if (src) pg[x] = *src;
         }
       }
+      if constexpr (LIST != kPages) {
+        int32_t slot[PER];
+#pragma unroll
+        for (int x = 0; x < PER; ++x)
+          slot[x] = pg[x] >= 0 && pg[x] < a.num_pages ? (pg[x] << a.page_shift) + (in[x] & (page - 1)) : -1;
+        int32_t *list = LIST == kNew ? a.slots : a.read_slots;
+        const bool whole = PER == 8 && i0 >= from && i0 + PER <= end &&
+                           ((reinterpret_cast<uintptr_t>(list) | (LIST == kNew ? reinterpret_cast<uintptr_t>(a.positions) : 0)) & 15) == 0;
+        if constexpr (PER == 8) {
+          if (whole) {
+#pragma unroll
+            for (int x = 0; x < 8; x += 4) {
+              *reinterpret_cast<int4 *>(list + i0 + x) = make_int4(slot[x], slot[x + 1], slot[x + 2], slot[x + 3]);
+              if constexpr (LIST == kNew)
+                *reinterpret_cast<int4 *>(a.positions + i0 + x) = make_int4(in[x], in[x + 1], in[x + 2], in[x + 3]);
+            }
+          }
+        }
+        if (!whole)
+#pragma unroll
+          for (int x = 0; x < PER; ++x)
+            if (i0 + x >= from && i0 + x < end) {
+              list[i0 + x] = slot[x];
+              if constexpr (LIST == kNew) a.positions[i0 + x] = in[x];
+            }
+      }
+    };
+    if (LIST == kPages || end - from <= kPlanThreads) {
+      for (int32_t i = from + tid; i < end; i += kPlanThreads) entry(std::integral_constant<int, 1>(), i);
+    } else {
+      entry(std::integral_constant<int, 8>(), t0 + 8 * tid);
     }
-    before += ntotal;
-    pages_before += ptotal;
+    before = ntotal;
+    pages_before = ptotal;
   }
   if constexpr (LIST == kPages) {
-    if (first && tid == 0) *a.used = (int32_t)(before < INT32_MAX ? before : INT32_MAX);
+    if (first && tid == 0) *a.used = before;
   } else {
-    if (first && tid == 0) (LIST == kNew ? a.cu_q : a.cu_k)[a.batch] = (int32_t)(before < most ? before : most);
-    for (int64_t i = (t0 > before ? t0 : before) + tid; i < t1; i += kPlanThreads) {   // behind the last token
+    if (first && tid == 0) (LIST == kNew ? a.cu_q : a.cu_k)[a.batch] = before < most ? before : most;
+    for (int32_t i = (t0 > before ? t0 : before) + tid; i < t1; i += kPlanThreads) {   // behind the last token
       if constexpr (LIST == kNew) a.slots[i] = -1, a.positions[i] = 0;
       else a.read_slots[i] = -1;
     }
@@ -186,7 +235,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_k(PlanArgs a) {
     // one tile each where no more than max_tokens are new; the lengths alone say how many pages there are
     const int64_t mine = g - a.q_tiles - a.r_tiles;
     for (int64_t tile = mine;; tile += a.p_groups)
-      if (plan_tile<kPages>(a, sh, tile, tile == 0) <= (tile + a.p_groups) * kPlanTile) break;
+      if (plan_tile<kPages>(a, sh, tile, tile == 0) <= (tile + a.p_groups) * kPlanTile) break;     // (ends: entries are below 2^31)
   }
 }
 
@@ -199,8 +248,8 @@ struct NormArgs {
   const float *q_weight, *k_weight, *rotary;
   const int32_t *positions;
   int64_t max_positions;
-  int64_t groups;                    // of D / 8 lanes
-  int32_t q_heads, heads, rot;       // heads: queries, keys, and values where there is a cache
+  uint32_t groups, units;            // groups of D / 8 lanes, of which a token has `units`
+  int32_t q_heads, rot;
   float eps;
   KvIo io;                           // the cache, and v as its dense[1]
 };
@@ -211,78 +260,98 @@ constexpr int kNoCache = -1;
 // sum over those lanes, the partner of an element i of a half rotation (i + rot / 2) is
 // in the lane rot / 16 further, that of a pair rotation in the same lane. Values are float32
 // until the one rounding to the operands' type; the cache gets the rounded key, as
-// if it were appended afterwards. Bound by the memory.
-template <int FMT, int D, bool F32, bool PAIRS>
+// if it were appended afterwards. The lanes of a row take HB heads of one kind (queries, keys or values) of a token, whose
+// loads are in flight together and share the angles and the weights.
+template <int FMT, int D, bool F32, bool PAIRS, int HB>
 __global__ void __launch_bounds__(256) qk_norm_rope_k(NormArgs a) {
   constexpr int LPR = D / 8, ES = F32 ? 4 : 2;
-  const int64_t g = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+  const uint32_t g = (blockIdx.x * 256u + threadIdx.x) / LPR;
   if (g >= a.groups) return;                          // whole rows leave together
-  const int at = threadIdx.x % LPR;
-  const int64_t token = g / a.heads;
-  const int head = (int)(g - token * a.heads), kv_heads = a.io.heads;
-  const int which = head < a.q_heads ? 0 : head < a.q_heads + kv_heads ? 1 : 2;      // query, key, value
-  const int h = which == 0 ? head : head - a.q_heads - (which == 2 ? kv_heads : 0);
-  const uint8_t *from = which == 0 ? reinterpret_cast<const uint8_t *>(a.q) + ES * (token * a.q_stride + (int64_t)h * D)
-                        : which == 1 ? reinterpret_cast<const uint8_t *>(a.k) + ES * (token * a.k_stride + (int64_t)h * D)
-                        : reinterpret_cast<const uint8_t *>(a.io.dense[1]) + ES * (token * a.io.stride[1] + (int64_t)h * D);
-  float x[8];
-  load8<F32>(from + ES * 8 * at, x);
+  const int at = threadIdx.x % LPR, kv_heads = a.io.heads;
+  const int64_t token = g / a.units;
+  const int u = (int)(g - (uint32_t)token * a.units);
+  const int q_units = (a.q_heads + HB - 1) / HB, kv_units = (kv_heads + HB - 1) / HB;
+  const int which = u < q_units ? 0 : u < q_units + kv_units ? 1 : 2;                // query, key, value
+  const int h0 = (which == 0 ? u : which == 1 ? u - q_units : u - q_units - kv_units) * HB;
+  const int heads = (which == 0 ? a.q_heads : kv_heads) - h0;                        // the unit has min(this, HB)
+  const uint8_t *from = reinterpret_cast<const uint8_t *>(which == 0 ? a.q : which == 1 ? a.k : a.io.dense[1]) +
+                        ES * (token * (which == 0 ? a.q_stride : which == 1 ? a.k_stride : a.io.stride[1]) + (int64_t)h0 * D + 8 * at);
+  float x[HB][8];
+#pragma unroll
+  for (int i = 0; i < HB; ++i) load8<F32>(from + ES * D * (i < heads ? i : 0), x[i]);
   if (which < 2) {
     const float *weight = which == 0 ? a.q_weight : a.k_weight;
-    if (weight) {
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-      s = lanes_sum<LPR>(s);
-      const float r = 1.0f / sqrtf(s / (float)D + a.eps);
-      float w[8];
-      load8<true>(weight + 8 * at, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= w[i] * r;
-    }
+    const bool in = 8 * at < a.rot;
+    const int half = a.rot / 16;                      // lanes of one half
+    const bool upper = at >= half;
+    constexpr int ANGLES = PAIRS ? 4 : 8;
+    float cs[ANGLES], sn[ANGLES], w[8];
     if (a.rot > 0) {
       int64_t p = a.positions[token];
       p = p < 0 ? 0 : p < a.max_positions ? p : a.max_positions - 1;
-      const float *row = a.rotary + p * a.rot;
-      const bool in = 8 * at < a.rot;
-      if constexpr (PAIRS) {
-        if (in) {
-          const float4 c = *reinterpret_cast<const float4 *>(row + 4 * at);
-          const float4 n = *reinterpret_cast<const float4 *>(row + a.rot / 2 + 4 * at);
-          const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {n.x, n.y, n.z, n.w};
+      const float *row = a.rotary + p * a.rot + (!in ? 0 : PAIRS ? 4 * at : 8 * (upper ? at - half : at));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float u = x[2 * i], v = x[2 * i + 1];
-            x[2 * i] = u * cs[i] - v * sn[i];
-            x[2 * i + 1] = v * cs[i] + u * sn[i];
-          }
-        }
-      } else {
-        const int half = a.rot / 16;                  // lanes of one half
-        const bool upper = at >= half;
-        const int other = in ? (upper ? threadIdx.x - half : threadIdx.x + half) : threadIdx.x;
-        float y[8];
+      for (int i = 0; i < ANGLES; i += 4) {
+        const float4 c = *reinterpret_cast<const float4 *>(row + i), s = *reinterpret_cast<const float4 *>(row + a.rot / 2 + i);
+        cs[i] = c.x, cs[i + 1] = c.y, cs[i + 2] = c.z, cs[i + 3] = c.w;
+        sn[i] = s.x, sn[i + 1] = s.y, sn[i + 2] = s.z, sn[i + 3] = s.w;
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], other & 63);
-        if (in) {
-          const int f = 8 * (upper ? at - half : at);
-          float cs[8], sn[8];
-          load8<true>(row + f, cs);
-          load8<true>(row + a.rot / 2 + f, sn);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = upper ? x[i] * cs[i] + y[i] * sn[i] : x[i] * cs[i] - y[i] * sn[i];
-        }
+      for (int i = 0; i < ANGLES; ++i) {
+        cs[i] = in ? cs[i] : 1.0f;                    // (lanes past the rotated dimensions)
+        sn[i] = !in ? 0.0f : PAIRS || upper ? sn[i] : -sn[i];
       }
     }
-    if constexpr (!F32) {
+    if (weight) load8<true>(weight + 8 * at, w);
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const uint32_t u = pack_bf16(x[i], x[i + 1]);
-        x[i] = bf16_lo(u), x[i + 1] = bf16_hi(u);
+    for (int i = 0; i < HB; ++i) {
+      if (weight) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(x[i][j], x[i][j], s);
+        s = lanes_sum<LPR>(s);
+        const float r = 1.0f / sqrtf(s / (float)D + a.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] *= w[j] * r;
+      }
+      if (a.rot > 0) {
+        if constexpr (PAIRS) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float c = x[i][2 * j], d = x[i][2 * j + 1];
+            x[i][2 * j] = in ? c * cs[j] - d * sn[j] : c;
+            x[i][2 * j + 1] = in ? d * cs[j] + c * sn[j] : d;
+          }
+        } else {
+          float y[8];
+          if (a.rot == D) {                           // the lane half a row away, without a trip through LDS
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = lane_xor(x[i][j], LPR / 2);
+          } else {
+            const int other = in ? (upper ? threadIdx.x - half : threadIdx.x + half) : threadIdx.x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = __shfl(x[i][j], other & 63);
+          }
+          // (selected, not multiplied by cos = 1 and sin = 0: what is not finite in lanes past the rotation stays as it is)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[i][j] = in ? x[i][j] * cs[j] + y[j] * sn[j] : x[i][j];
+        }
+      }
+      if constexpr (!F32) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const uint32_t two = pack_bf16(x[i][j], x[i][j + 1]);
+          x[i][j] = bf16_lo(two), x[i][j + 1] = bf16_hi(two);
+        }
       }
     }
     uint8_t *to = reinterpret_cast<uint8_t *>(which == 0 ? a.q_out : a.k_out);
-    if (to) store8<F32>(to + ES * (token * (which == 0 ? a.q_out_stride : a.k_out_stride) + (int64_t)h * D + 8 * at), x);
+    if (to) {
+      to += ES * (token * (which == 0 ? a.q_out_stride : a.k_out_stride) + (int64_t)h0 * D + 8 * at);
+#pragma unroll
+      for (int i = 0; i < HB; ++i)
+        if (i < heads) store8<F32>(to + ES * D * i, x[i]);
+    }
   }
   if constexpr (FMT != kNoCache) {
     if (which > 0) {
@@ -290,8 +359,12 @@ __global__ void __launch_bounds__(256) qk_norm_rope_k(NormArgs a) {
       part.slot = (uint32_t)a.io.slots[token];
       if (part.slot < a.io.capacity) {
         const uint32_t pg = part.slot >> a.io.page_shift, in_page = part.slot & ((1u << a.io.page_shift) - 1);
-        part.cached = (((int64_t)pg * kv_heads + h) << a.io.page_shift) + in_page;
-        append_row<FMT, D>(a.io, part, which - 1, at, x);
+#pragma unroll
+        for (int i = 0; i < HB; ++i) {
+          if (i >= heads) break;
+          part.cached = (((int64_t)pg * kv_heads + h0 + i) << a.io.page_shift) + in_page;
+          append_row<FMT, D>(a.io, part, which - 1, at, x[i]);
+        }
       }
     }
   }
@@ -321,12 +394,7 @@ __device__ __forceinline__ uint32_t score_order(float x) {
 __device__ __forceinline__ int32_t group_before(int32_t x, int32_t *sum) {
   __shared__ int32_t part[kRouteThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int32_t up = x;
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) {
-    const int32_t y = __shfl_up(up, s);
-    if (lane >= s) up += y;
-  }
+  const int32_t up = wave_scan<false>(x);
   if (lane == 63) part[wave] = up;
   __syncthreads();
   int32_t base = 0, all = 0;
@@ -353,38 +421,45 @@ __global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
   for (int e = tid; e < a.experts; e += kRouteThreads) chose[e] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens;
-  constexpr int PER = kRouteTokens / (kRouteThreads / 64);     // tokens a wave
+  constexpr int WAVES = kRouteThreads / 64, PER = kRouteTokens / WAVES;        // tokens wave, wave + WAVES, ...
   int32_t mine[PER];                                           // lane j: the token's choice j
+  float x[PER][NV];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int in = wave * PER + i;
-    const int64_t t = t0 + in;
-    mine[i] = -1;
-    if (t >= a.tokens) continue;                               // uniform
-    float x[NV];
-    uint32_t order[NV];
+    const int64_t t = t0 + wave + i * WAVES;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int e = lane + 64 * v;
-      x[v] = -INFINITY;
-      if (e < a.experts) {
+      x[i][v] = -INFINITY;
+      if (e < a.experts && t < a.tokens) {
         const size_t o = (size_t)t * a.experts + e;
-        x[v] = F32 ? reinterpret_cast<const float *>(a.logits)[o]
-                   : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(a.logits)[o] << 16);
+        x[i][v] = F32 ? reinterpret_cast<const float *>(a.logits)[o]
+                      : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(a.logits)[o] << 16);
       }
-      order[v] = score_order(x[v]);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int in = wave + i * WAVES;
+    const int64_t t = t0 + in;
+    mine[i] = -1;
+    if (t >= a.tokens) continue;                               // uniform
+    uint32_t order[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) order[v] = score_order(x[i][v]);
     float value = -INFINITY, peak = 0.0f;
     for (int j = 0; j < a.top; ++j) {
       uint32_t best = 0;
 #pragma unroll
       for (int v = 0; v < NV; ++v) best = order[v] > best ? order[v] : best;
-      best = wave_max(best);
+      best = __builtin_amdgcn_readfirstlane((int)wave_max(best));
       if (best == 0) break;                                    // uniform
-      uint32_t far = 0;                                        // kRouteMost - index: the largest is the lowest index
+      int e = 0;                                               // the lowest index among equals: first v, then lane
 #pragma unroll
-      for (int v = NV - 1; v >= 0; --v) far = order[v] == best ? kRouteMost - (lane + 64 * v) : far;
-      const int e = kRouteMost - (int)wave_max(far);
+      for (int v = NV - 1; v >= 0; --v) {
+        const unsigned long long hit = __ballot(order[v] == best);
+        e = hit ? 64 * v + __ffsll((long long)hit) - 1 : e;
+      }
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (lane + 64 * v == e) order[v] = 0;
@@ -398,7 +473,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
       sum = w;
     } else {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) sum += x[v] > -INFINITY ? expf(x[v] - peak) : 0.0f;
+      for (int v = 0; v < NV; ++v) sum += x[i][v] > -INFINITY ? expf(x[i][v] - peak) : 0.0f;
     }
     sum = lanes_sum<64>(sum);
     if (lane < a.top) {
@@ -425,7 +500,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int in = wave * PER + i;
+    const int in = wave + i * WAVES;
     const int64_t t = t0 + in;
     if (t >= a.tokens || lane >= a.top) continue;
     int32_t at = -1;
@@ -453,12 +528,24 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_k(RouteArgs a) {
   while (width < a.experts) width <<= 1;
   const int parts = kRouteThreads / width, e = tid & (width - 1), part = tid / width;
   int32_t before = 0, all = 0;
-  if (e < a.experts)
-    for (int64_t b = part; b < a.blocks; b += parts) {
+  if (e < a.experts) {
+    int64_t b = part;
+    for (; b + 7 * parts < a.blocks; b += 8 * parts) {         // eight loads in flight
+      int32_t n[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n[i] = a.counts[(b + i * parts) * a.experts + e];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        all += n[i];
+        if (b + i * parts < (int64_t)blockIdx.x) before += n[i];
+      }
+    }
+    for (; b < a.blocks; b += parts) {
       const int32_t n = a.counts[b * a.experts + e];
       all += n;
       if (b < (int64_t)blockIdx.x) before += n;
     }
+  }
   sums[0][tid] = before, sums[1][tid] = all;
   __syncthreads();
   if (tid < width) {
@@ -494,22 +581,33 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_k(RouteArgs a) {
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
-template <int FMT, int D, bool F32>
-int launch_norm(const NormArgs &a, bool pairs, hipStream_t st) {
-  const int64_t blocks = (a.groups * (D / 8) + 255) / 256;
+template <int FMT, int D, bool F32, bool PAIRS, int HB>
+int launch_norm_heads(NormArgs a, int64_t tokens, hipStream_t st) {
+  const int64_t units = (a.q_heads + HB - 1) / HB + (FMT == kNoCache ? 1 : 2) * ((a.io.heads + HB - 1) / HB);
+  const int64_t blocks = (tokens * units * (D / 8) + 255) / 256;
   if (blocks > kMaxGroups) return GLQ_ERR_UNSUPPORTED;
-  auto kern = pairs ? qk_norm_rope_k<FMT, D, F32, true> : qk_norm_rope_k<FMT, D, F32, false>;
-  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, st, a);
+  a.units = (uint32_t)units, a.groups = (uint32_t)(tokens * units);
+  hipLaunchKernelGGL((qk_norm_rope_k<FMT, D, F32, PAIRS, HB>), dim3((unsigned)blocks), dim3(256), 0, st, a);
   return hip_status(hipGetLastError(), "qk_norm_rope_k");
 }
 
+template <int FMT, int D, bool F32>
+int launch_norm(const NormArgs &a, int64_t tokens, bool pairs, hipStream_t st) {
+  // four heads a row of lanes where that leaves every CU eight waves
+  constexpr int HB = 4;
+  const int64_t heads = a.q_heads + (FMT == kNoCache ? 1 : 2) * a.io.heads;
+  if (tokens * heads * (D / 8) >= (int64_t)256 * 8 * 64 * HB)
+    return pairs ? launch_norm_heads<FMT, D, F32, true, HB>(a, tokens, st) : launch_norm_heads<FMT, D, F32, false, HB>(a, tokens, st);
+  return pairs ? launch_norm_heads<FMT, D, F32, true, 1>(a, tokens, st) : launch_norm_heads<FMT, D, F32, false, 1>(a, tokens, st);
+}
+
 template <int FMT>
-int launch_norm_dim(const NormArgs &a, int d, glq_dtype dt, bool pairs, hipStream_t st) {
+int launch_norm_dim(const NormArgs &a, int64_t tokens, int d, glq_dtype dt, bool pairs, hipStream_t st) {
   if (dt == GLQ_F32)
-    return d == 64 ? launch_norm<FMT, 64, true>(a, pairs, st) : d == 128 ? launch_norm<FMT, 128, true>(a, pairs, st)
-                                                                         : launch_norm<FMT, 256, true>(a, pairs, st);
-  return d == 64 ? launch_norm<FMT, 64, false>(a, pairs, st) : d == 128 ? launch_norm<FMT, 128, false>(a, pairs, st)
-                                                                        : launch_norm<FMT, 256, false>(a, pairs, st);
+    return d == 64 ? launch_norm<FMT, 64, true>(a, tokens, pairs, st) : d == 128 ? launch_norm<FMT, 128, true>(a, tokens, pairs, st)
+                                                                         : launch_norm<FMT, 256, true>(a, tokens, pairs, st);
+  return d == 64 ? launch_norm<FMT, 64, false>(a, tokens, pairs, st) : d == 128 ? launch_norm<FMT, 128, false>(a, tokens, pairs, st)
+                                                                        : launch_norm<FMT, 256, false>(a, tokens, pairs, st);
 }
 
 int check_route(int64_t tokens, int32_t experts, int32_t top) {
@@ -587,22 +685,21 @@ extern "C" int glq_qk_norm_rope(const glq_qk *N, const glq_kv_cache *C, uint32_t
   const int64_t heads = (int64_t)N->q_heads + N->kv_heads * (C ? 2 : 1);
   if (N->tokens > (int64_t(1) << 40) / heads) return GLQ_ERR_UNSUPPORTED;
   NormArgs a = {N->q, N->k, N->q_out, N->k_out, N->q_stride, N->k_stride, N->q_out_stride, N->k_out_stride,
-                N->q_weight, N->k_weight, N->rotary, N->positions, N->max_positions, N->tokens * heads,
-                N->q_heads, (int32_t)heads, N->rotary_dim, N->eps, {}};
+                N->q_weight, N->k_weight, N->rotary, N->positions, N->max_positions, 0, 0, N->q_heads, N->rotary_dim, N->eps, {}};
   a.io.heads = N->kv_heads;
   const glq_dtype dt = (glq_dtype)N->dt;
   const bool pairs = flags & GLQ_ROPE_PAIRS;
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
-  if (!C) return launch_norm_dim<kNoCache>(a, d, dt, pairs, st);
+  if (!C) return launch_norm_dim<kNoCache>(a, N->tokens, d, dt, pairs, st);
   a.io.cache[0] = C->k, a.io.cache[1] = C->v;
   a.io.scale[0] = C->k_scale, a.io.scale[1] = C->v_scale;
   a.io.dense[1] = const_cast<void *>(N->v), a.io.stride[1] = N->v_stride;
   a.io.slots = N->slots;
   a.io.page_shift = log2_of(C->page_size), a.io.capacity = (uint32_t)(C->num_pages * C->page_size);
   switch (C->format) {
-    case GLQ_KV_BF16: return launch_norm_dim<GLQ_KV_BF16>(a, d, dt, pairs, st);
-    case GLQ_KV_INT8: return launch_norm_dim<GLQ_KV_INT8>(a, d, dt, pairs, st);
-    default: return launch_norm_dim<GLQ_KV_INT4>(a, d, dt, pairs, st);
+    case GLQ_KV_BF16: return launch_norm_dim<GLQ_KV_BF16>(a, N->tokens, d, dt, pairs, st);
+    case GLQ_KV_INT8: return launch_norm_dim<GLQ_KV_INT8>(a, N->tokens, d, dt, pairs, st);
+    default: return launch_norm_dim<GLQ_KV_INT4>(a, N->tokens, d, dt, pairs, st);
   }
 }
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -131,13 +132,14 @@ _lib.glq_attn_decode.argtypes = [_kvc, _vp, _i32, _i64, _i64, _i32, _vp, _i64, _
                                  _vp]
 _lib.glq_attn_prompt.argtypes = [ctypes.POINTER(PromptStruct), _u32, _vp]
 _lib.glq_kv_plan.argtypes = [ctypes.POINTER(PlanStruct), _vp]
-_lib.glq_qk_norm_rope.argtypes = [ctypes.POINTER(QkStruct), _kvc, _u32, _vp]
+_lib.glq_qk_norm_rope.argtypes = [_vp, _kvc, _u32, _vp]           # (a packed struct's bytes, or byref of a QkStruct)
+_glq_qk_norm_rope = _lib.glq_qk_norm_rope
 _lib.glq_route_workspace.argtypes = [_i64, _i32, _i32]
 _lib.glq_route_workspace.restype = _sz
 _lib.glq_route.argtypes = [_vp, _i32, _i64, _i32, _i32, _u32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
 _lib.glq_expert_linear_workspace.argtypes = [ctypes.POINTER(ExpertsStruct), _i64]
 _lib.glq_expert_linear_workspace.restype = _sz
-_lib.glq_expert_linear.argtypes = [ctypes.POINTER(ExpertsStruct), ctypes.POINTER(ExpertRowsStruct), _vp, _sz, _vp]
+_lib.glq_expert_linear.argtypes = [ctypes.POINTER(ExpertsStruct), _vp, _vp, _sz, _vp]
 _lib.glq_status_string.argtypes = [_i32]
 _lib.glq_status_string.restype = ctypes.c_char_p
 _lib.glq_version.restype = _u32
@@ -836,7 +838,7 @@ class KvPlan:
             raise ValueError(f"max_tokens, max_read: {max_tokens}, {max_read}")
         dev = self.device = page_table.device
         at = _ints(page_table, "page_table", dev, batch, max_pages)
-        self.page_table, self.batch = page_table, batch
+        self.page_table, self.batch, self._index = page_table, batch, dev.index
 
         def ints(n):
             return torch.zeros(n, dtype=torch.int32, device=dev)
@@ -855,11 +857,14 @@ def kv_plan(plan: KvPlan, lens, added, free_pages, stream=None) -> KvPlan:
     tokens cached and added[b] new ones (int32 [batch]), pages that it needs more come from
     free_pages (int32) in order; plan.used says how many. Slots of -1 drop their
     token: no page was free, the table is full, or there is no such token."""
-    dev, st = plan.device, PlanStruct.from_buffer_copy(plan._st)
-    st.lens, st.added = _ints(lens, "lens", dev, plan.batch), _ints(added, "added", dev, plan.batch)
+    index, st = plan._index, PlanStruct.from_buffer_copy(plan._st)
+    st.lens = _dense(lens, "lens", index, torch.int32, 4, plan.batch)
+    st.added = _dense(added, "added", index, torch.int32, 4, plan.batch)
     st.num_free = _last_size(free_pages)
-    st.free_pages = _ints(free_pages, "free_pages", dev, st.num_free)
-    _check(_lib.glq_kv_plan(ctypes.byref(st), _stream_ptr(stream, dev)), "glq_kv_plan")
+    st.free_pages = _dense(free_pages, "free_pages", index, torch.int32, 4, st.num_free)
+    rc = _lib.glq_kv_plan(ctypes.byref(st), _current(stream, index))
+    if rc:
+        raise GlqError(rc, "glq_kv_plan")
     return plan
 
 
@@ -871,13 +876,49 @@ def rotary_table(max_positions: int, rotary_dim: int, base: float = 10000.0, dev
     return torch.cat((angle.cos(), angle.sin()), 1).to(torch.float32).to(device)
 
 
-def _norm_weight(t, name, device, dim):
-    if t is None:
-        return 0
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != (dim,) or t.device != device or \
-            not t.is_contiguous() or t.data_ptr() % 16:
-        raise ValueError(f"{name}: must be a dense float32 vector of {dim} on {device}, 16-byte aligned")
-    return t.data_ptr()
+# What the next calls check of a tensor, a read of the tensor for each thing: a call is as short as its checks.
+
+
+def _dense(t, name, index, dtype, align, *shape):
+    """A dense tensor of this type and shape on cuda:index; its address."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: must be a device (cuda) tensor")
+    at = t.data_ptr()
+    if t.get_device() != index or t.dtype is not dtype or t.shape != shape or at % align or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected dense {dtype} {shape} on cuda:{index}, "
+                         f"{align}-byte aligned")
+    return at
+
+
+def _heads(t, name, index, dtype, total, heads, dim):
+    """As _rows."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: must be a device (cuda) tensor")
+    if t.get_device() != index or t.dtype is not dtype or t.shape != (total, heads, dim):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {(total, heads, dim)} on cuda:{index}")
+    at, step = t.data_ptr(), heads * dim
+    if not t.is_contiguous():
+        step, between, inner = t.stride()
+        if inner != 1 or (heads > 1 and between != dim):
+            raise ValueError(f"{name}: the heads of a row must be dense")
+        if step < heads * dim or step % (4 if dtype is torch.float32 else 8):
+            raise ValueError(f"{name}: rows must not overlap and start at multiples of 16 bytes")
+    if at % 16:
+        raise ValueError(f"{name}: must be 16-byte aligned")
+    return at, step
+
+
+def _current(stream, index):
+    """As _stream_ptr, for cuda:index."""
+    if _current_device() != index:
+        raise ValueError(f"tensors on cuda:{index}, but the current device is cuda:{_current_device()}")
+    if stream is None:
+        return _raw_stream(index) if _raw_stream else torch.cuda.current_stream().cuda_stream
+    return _stream_ptr(stream, torch.device("cuda", index))
+
+
+_QK_STRUCT = struct.Struct("@4P4i5q2Pfi2PqPqP")
+assert _QK_STRUCT.size == ctypes.sizeof(QkStruct)
 
 
 def qk_norm_rope(q, k, positions, rotary, q_out, k_out=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -890,50 +931,45 @@ def qk_norm_rope(q, k, positions, rotary, q_out, k_out=None, q_weight=None, k_we
     `slots`, and k_out may be None. Returns q_out, k_out."""
     dt = _attn_dtype(q, "q")
     _attn_dtype(k, "k")
-    dev, tokens, heads, dim = q.device, *q.shape
-    kvh = k.shape[1]
+    dtype, index, (tokens, heads, dim), kvh = q.dtype, q.get_device(), q.shape, k.shape[1]
+    if index < 0:
+        raise ValueError("q: must be a device (cuda) tensor")
     if dim not in _HEAD_DIMS:
         raise ValueError(f"q: head_dim {dim}, expected one of {_HEAD_DIMS}")
-    qp, qs = _rows(q, "q", dev, q.dtype, tokens, heads, dim)
-    kp, ks = _rows(k, "k", dev, q.dtype, tokens, kvh, dim)
-    qop, qos = _rows(q_out, "q_out", dev, q.dtype, tokens, heads, dim)
-    kop, kos = (0, 0) if k_out is None else _rows(k_out, "k_out", dev, q.dtype, tokens, kvh, dim)
-    vp = vs = sp = pp = tp = most = rot = 0
+    qp, qs = _heads(q, "q", index, dtype, tokens, heads, dim)
+    kp, ks = _heads(k, "k", index, dtype, tokens, kvh, dim)
+    qop, qos = (qp, qs) if q_out is q else _heads(q_out, "q_out", index, dtype, tokens, heads, dim)
+    kop, kos = (0, 0) if k_out is None else (kp, ks) if k_out is k else _heads(k_out, "k_out", index, dtype, tokens, kvh, dim)
+    vp = vs = sp = pp = tp = most = rot = wq = wk = 0
     if cache is not None:
-        if (cache.kv_heads, cache.head_dim, cache.device) != (kvh, dim, dev):
+        if cache.kv_heads != kvh or cache.head_dim != dim or cache.device.index != index:
             raise ValueError(f"cache: {cache.kv_heads} heads of {cache.head_dim} on {cache.device}, k has {kvh} of {dim} on "
-                             f"{dev}")
-        vp, vs = _rows(v, "v", dev, q.dtype, tokens, kvh, dim)
-        sp = _ints(slots, "slots", dev, tokens)
+                             f"cuda:{index}")
+        vp, vs = _heads(v, "v", index, dtype, tokens, kvh, dim)
+        sp = _dense(slots, "slots", index, torch.int32, 4, tokens)
     elif k_out is None or v is not None or slots is not None:
         raise ValueError("k_out: missing" if k_out is None else "v, slots: without a cache")
     if rotary is not None:
-        if not isinstance(rotary, torch.Tensor) or rotary.dtype is not torch.float32 or rotary.dim() != 2 or \
-                rotary.device != dev or not rotary.is_contiguous() or rotary.data_ptr() % 16:
-            raise ValueError(f"rotary: must be dense float32 [max_positions, rotary_dim] on {dev}, 16-byte aligned")
-        tp, (most, rot) = rotary.data_ptr(), rotary.shape
+        most, rot = rotary.shape if isinstance(rotary, torch.Tensor) and rotary.dim() == 2 else (0, 0)
         if rot < 1 or most < 1:
-            raise ValueError(f"rotary: shape {tuple(rotary.shape)}")
-        pp = _ints(positions, "positions", dev, tokens)
-    st = QkStruct(qp, kp, qop, kop, dt, heads, kvh, dim, qs, ks, qos, kos, tokens,
-                  _norm_weight(q_weight, "q_weight", dev, dim), _norm_weight(k_weight, "k_weight", dev, dim), eps, rot, pp,
-                  tp, most, vp, vs, sp)
-    _check(_lib.glq_qk_norm_rope(ctypes.byref(st), None if cache is None else cache._ref, ROPE_PAIRS if pairs else 0,
-                                 _stream_ptr(stream, dev)), "glq_qk_norm_rope")
+            raise ValueError("rotary: must be [max_positions, rotary_dim]")
+        tp = _dense(rotary, "rotary", index, torch.float32, 16, most, rot)
+        pp = _dense(positions, "positions", index, torch.int32, 4, tokens)
+    if q_weight is not None:
+        wq = _dense(q_weight, "q_weight", index, torch.float32, 16, dim)
+    if k_weight is not None:
+        wk = _dense(k_weight, "k_weight", index, torch.float32, 16, dim)
+    st = _QK_STRUCT.pack(qp, kp, qop, kop, dt, heads, kvh, dim, qs, ks, qos, kos, tokens, wq, wk, eps, rot, pp, tp, most,
+                         vp, vs, sp)
+    rc = _glq_qk_norm_rope(st, None if cache is None else cache._ref, 1 if pairs else 0, _current(stream, index))
+    if rc:
+        raise GlqError(rc, "glq_qk_norm_rope")
     return q_out, k_out
 
 
-def _floats(t, name, device, *shape):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name}: must be a device (cuda) tensor")
-    if t.dtype is not torch.float32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected dense float32 {shape} on {device}")
-    return t.data_ptr()
-
-
-def _workspace(t, device):
-    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"workspace: must be contiguous on {device}")
+def _workspace(t, index):
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous on cuda:{index}")
     return t.data_ptr(), t.nbytes
 
 
@@ -950,14 +986,17 @@ def route(logits, top_k: int, weights, ids, pos, src, offsets, workspace, normal
     if not isinstance(logits, torch.Tensor) or logits.dtype not in _ATTN_DTYPES or logits.dim() != 2 or \
             not logits.is_contiguous() or not logits.is_cuda:
         raise ValueError("logits: must be dense float32 or bfloat16 [tokens, experts] on a device")
-    dev, (tokens, experts) = logits.device, logits.shape
-    wp = _floats(weights, "weights", dev, tokens, top_k)
-    ip, pp = _ints(ids, "ids", dev, tokens, top_k), _ints(pos, "pos", dev, tokens, top_k)
-    sp, op = _ints(src, "src", dev, tokens * top_k), _ints(offsets, "offsets", dev, experts + 1)
-    wsp, ws = _workspace(workspace, dev)
-    _check(_lib.glq_route(logits.data_ptr(), _ATTN_DTYPES[logits.dtype], tokens, experts, top_k,
-                          ROUTE_NORMALIZE if normalize else 0, wp, ip, pp, sp, op, wsp, ws, _stream_ptr(stream, dev)),
-           "glq_route")
+    index, (tokens, experts) = logits.get_device(), logits.shape
+    wp = _dense(weights, "weights", index, torch.float32, 4, tokens, top_k)
+    ip = _dense(ids, "ids", index, torch.int32, 4, tokens, top_k)
+    pp = _dense(pos, "pos", index, torch.int32, 4, tokens, top_k)
+    sp = _dense(src, "src", index, torch.int32, 4, tokens * top_k)
+    op = _dense(offsets, "offsets", index, torch.int32, 4, experts + 1)
+    wsp, ws = _workspace(workspace, index)
+    rc = _lib.glq_route(logits.data_ptr(), _ATTN_DTYPES[logits.dtype], tokens, experts, top_k,
+                        ROUTE_NORMALIZE if normalize else 0, wp, ip, pp, sp, op, wsp, ws, _current(stream, index))
+    if rc:
+        raise GlqError(rc, "glq_route")
     return weights, ids, pos, src, offsets
 
 
@@ -977,6 +1016,7 @@ class Experts:
         self.scale, self.idx1, self.idx2, self.sign_k, self.sign_n, self.cb, self.row_scale = (
             scale, idx1, idx2, sign_k, sign_n, cb, row_scale)
         dev = self.device = _dev_tensor(idx1, "idx1", shape=(count, n, k // 8), dtypes=(torch.int16,)).device
+        self._index = dev.index
         if bpw == 2 and idx2 is not None:
             raise ValueError("idx2: must be None at 2 bpw")
         if bpw > 2:
@@ -1016,14 +1056,15 @@ def expert_linear_workspace_bytes(experts: Experts, rows: int) -> int:
     return int(_lib.glq_expert_linear_workspace(experts._ref, rows))
 
 
-def _matrix(t, name, device, cols):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name}: must be a device (cuda) tensor")
-    if t.dtype not in _ATTN_DTYPES or t.dim() != 2 or t.shape[1] != cols or t.device != device or not t.is_contiguous() or \
-            t.data_ptr() % 16:
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected dense float32 or bfloat16 [rows, {cols}] "
-                         f"on {device}, 16-byte aligned")
-    return t.data_ptr(), _ATTN_DTYPES[t.dtype], t.shape[0]
+def _matrix(t, name, index, cols):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _ATTN_DTYPES or t.dim() != 2:
+        raise ValueError(f"{name}: must be a float32 or bfloat16 [rows, {cols}] tensor")
+    rows = t.shape[0]
+    return _dense(t, name, index, t.dtype, 16, rows, cols), _ATTN_DTYPES[t.dtype], rows
+
+
+_ROWS_STRUCT = struct.Struct("@2P2i2q4Pqi4x")
+assert _ROWS_STRUCT.size == ctypes.sizeof(ExpertRowsStruct)
 
 
 def expert_linear(experts: Experts, x, y, offsets, workspace, src=None, pos=None, weights=None, stream=None):
@@ -1031,21 +1072,24 @@ def expert_linear(experts: Experts, x, y, offsets, workspace, src=None, pos=None
     expert e's are offsets[e] .. offsets[e + 1] - 1 (int32 [count + 1]). Row r is x[src[r]], or
     x[r] without src; y has the rows, or with pos (int32 [tokens, top_k]) and weights (float32)
     each token's weighted sum of rows. src, pos, weights and offsets are what route gives."""
-    dev = experts.device
-    xp, xdt, x_rows = _matrix(x, "x", dev, experts.k)
-    yp, ydt, y_rows = _matrix(y, "y", dev, experts.n)
+    index = experts._index
+    xp, xdt, x_rows = _matrix(x, "x", index, experts.k)
+    yp, ydt, y_rows = _matrix(y, "y", index, experts.n)
     rows = x_rows if src is None else _last_size(src)
-    sp = 0 if src is None else _ints(src, "src", dev, rows)
+    sp = 0 if src is None else _dense(src, "src", index, torch.int32, 4, rows)
     pp = wp = top = 0
     if pos is not None:
         top = _last_size(pos)
-        pp, wp = _ints(pos, "pos", dev, y_rows, top), _floats(weights, "weights", dev, y_rows, top)
+        pp = _dense(pos, "pos", index, torch.int32, 4, y_rows, top)
+        wp = _dense(weights, "weights", index, torch.float32, 4, y_rows, top)
         if top < 1:
             raise ValueError("pos: no columns")
     elif y_rows != rows or weights is not None:
         raise ValueError(f"y: {y_rows} rows, expected {rows}" if weights is None else "weights: without pos")
-    wsp, ws = _workspace(workspace, dev)
-    st = ExpertRowsStruct(xp, yp, xdt, ydt, x_rows, rows, _ints(offsets, "offsets", dev, experts.count + 1), sp, pp, wp,
-                          y_rows, top)
-    _check(_lib.glq_expert_linear(experts._ref, ctypes.byref(st), wsp, ws, _stream_ptr(stream, dev)), "glq_expert_linear")
+    op = _dense(offsets, "offsets", index, torch.int32, 4, experts.count + 1)
+    wsp, ws = _workspace(workspace, index)
+    st = _ROWS_STRUCT.pack(xp, yp, xdt, ydt, x_rows, rows, op, sp, pp, wp, y_rows, top)
+    rc = _lib.glq_expert_linear(experts._ref, st, wsp, ws, _current(stream, index))
+    if rc:
+        raise GlqError(rc, "glq_expert_linear")
     return y
