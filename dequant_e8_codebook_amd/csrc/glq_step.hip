@@ -56,9 +56,11 @@ struct PlanArgs {
   uint32_t q_tiles, r_tiles, p_groups;     // workgroups of the three lists
 };
 
-constexpr int kPlanThreads = 256, kPlanTile = 2048, kPlanChunk = 1024;
+constexpr int kPlanThreads = 256, kPlanChunk = 1024;
 
 enum PlanList { kNew, kRead, kPages };
+// entries of a workgroup's tile: one page a thread, whose writes are scattered, eight tokens
+constexpr int kPlanEach = 8, kPlanPages = kPlanThreads, kPlanTokens = kPlanEach * kPlanThreads;
 
 // Sums that stop at 2^31 - 1: no list is longer, and what begins there is past its end.
 __device__ __forceinline__ int32_t capped(int32_t x, int32_t y) {
@@ -95,8 +97,9 @@ __device__ __forceinline__ int32_t plan_tile(const PlanArgs &a, PlanShared &sh, 
   auto &wave_sum = sh.wave_sum;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int32_t most = LIST == kNew ? (int32_t)a.max_tokens : LIST == kRead ? (int32_t)a.max_read : INT32_MAX;
-  const int32_t t0 = tile < INT32_MAX / kPlanTile ? (int32_t)tile * kPlanTile : INT32_MAX;
-  const int32_t t1 = most - t0 < kPlanTile ? (most > t0 ? most : t0) : t0 + kPlanTile;
+  constexpr int TILE = LIST == kPages ? kPlanPages : kPlanTokens;
+  const int32_t t0 = tile < INT32_MAX / TILE ? (int32_t)tile * TILE : INT32_MAX;
+  const int32_t t1 = most - t0 < TILE ? (most > t0 ? most : t0) : t0 + TILE;
   const int32_t page = 1 << a.page_shift, max_pages = (int32_t)a.max_pages, num_free = (int32_t)a.num_free;
   auto pages_of = [&](int64_t tokens) {
     const int64_t p = (tokens + page - 1) >> a.page_shift;
@@ -157,25 +160,34 @@ __device__ __forceinline__ int32_t plan_tile(const PlanArgs &a, PlanShared &sh, 
       const int32_t i1 = i0 > from ? i0 : from;
       for (int s = top >> 1; s; s >>= 1)
         if (begin[at + s] <= i1) at += s;
+      // what the request is, read again only where the next one begins
+      int32_t b0, b1, ln, hd, tk;
+      auto look = [&] { b0 = begin[at], b1 = at + 1 < n_here ? begin[at + 1] : INT32_MAX, ln = len[at], hd = held[at], tk = taken[at]; };
+      look();
+      const int32_t *src[PER];
       int32_t pg[PER], in[PER];
+      bool is[PER];
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
         const int32_t i = i0 + x;
-        pg[x] = -1, in[x] = 0;
-        if (i < from || i >= end) continue;
         if constexpr (PER > 1)
-          while (at + 1 < n_here && begin[at + 1] <= i) ++at;
-        const int32_t nth = i - begin[at];
+          while (b1 <= i && at + 1 < n_here) ++at, look();
+        const int32_t nth = i - b0;
         if constexpr (LIST == kPages) {
-          a.table[(c + at) * a.max_pages + held[at] + nth] = i < num_free ? a.free_pages[i] : -1;
+          if (i >= from && i < end) a.table[(c + at) * a.max_pages + hd + nth] = i < num_free ? a.free_pages[i] : -1;
         } else {
-          const int64_t t = LIST == kNew ? (int64_t)len[at] + nth : nth, e = t >> a.page_shift;
+          const int64_t t = LIST == kNew ? (int64_t)ln + nth : nth, e = t >> a.page_shift, f = tk + e - hd;
           in[x] = t < INT32_MAX ? (int32_t)t : INT32_MAX;
-          const int64_t f = taken[at] + e - held[at];
-          const int32_t *src = e < held[at] ? a.table + (c + at) * a.max_pages + e : e < max_pages && f < num_free ? a.free_pages + f
-                                                                                                                 : nullptr;
-          if (src) pg[x] = *src;
+          const bool here = i >= from && i < end, old = e < hd;
+          is[x] = here && (old || (e < max_pages && f < num_free));
+          src[x] = !is[x] ? a.lens : old ? a.table + (c + at) * a.max_pages + e : a.free_pages + f;   // (some word, not used)
         }
+      }
+      if constexpr (LIST != kPages) {
+#pragma unroll
+        for (int x = 0; x < PER; ++x) pg[x] = *src[x];         // all in flight together
+#pragma unroll
+        for (int x = 0; x < PER; ++x) pg[x] = is[x] ? pg[x] : -1;
       }
       if constexpr (LIST != kPages) {
         int32_t slot[PER];
@@ -183,12 +195,12 @@ __device__ __forceinline__ int32_t plan_tile(const PlanArgs &a, PlanShared &sh, 
         for (int x = 0; x < PER; ++x)
           slot[x] = pg[x] >= 0 && pg[x] < a.num_pages ? (pg[x] << a.page_shift) + (in[x] & (page - 1)) : -1;
         int32_t *list = LIST == kNew ? a.slots : a.read_slots;
-        const bool whole = PER == 8 && i0 >= from && i0 + PER <= end &&
+        const bool whole = PER == kPlanEach && i0 >= from && i0 + PER <= end &&
                            ((reinterpret_cast<uintptr_t>(list) | (LIST == kNew ? reinterpret_cast<uintptr_t>(a.positions) : 0)) & 15) == 0;
-        if constexpr (PER == 8) {
+        if constexpr (PER == kPlanEach) {
           if (whole) {
 #pragma unroll
-            for (int x = 0; x < 8; x += 4) {
+            for (int x = 0; x < PER; x += 4) {
               *reinterpret_cast<int4 *>(list + i0 + x) = make_int4(slot[x], slot[x + 1], slot[x + 2], slot[x + 3]);
               if constexpr (LIST == kNew)
                 *reinterpret_cast<int4 *>(a.positions + i0 + x) = make_int4(in[x], in[x + 1], in[x + 2], in[x + 3]);
@@ -207,7 +219,7 @@ __device__ __forceinline__ int32_t plan_tile(const PlanArgs &a, PlanShared &sh, 
     if (LIST == kPages || end - from <= kPlanThreads) {
       for (int32_t i = from + tid; i < end; i += kPlanThreads) entry(std::integral_constant<int, 1>(), i);
     } else {
-      entry(std::integral_constant<int, 8>(), t0 + 8 * tid);
+      entry(std::integral_constant<int, kPlanEach>(), t0 + kPlanEach * tid);
     }
     before = ntotal;
     pages_before = ptotal;
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_k(PlanArgs a) {
     // one tile each where no more than max_tokens are new; the lengths alone say how many pages there are
     const int64_t mine = g - a.q_tiles - a.r_tiles;
     for (int64_t tile = mine;; tile += a.p_groups)
-      if (plan_tile<kPages>(a, sh, tile, tile == 0) <= (tile + a.p_groups) * kPlanTile) break;     // (ends: entries are below 2^31)
+      if (plan_tile<kPages>(a, sh, tile, tile == 0) <= (tile + a.p_groups) * kPlanPages) break;     // (ends: entries are below 2^31)
   }
 }
 
@@ -381,7 +393,8 @@ struct RouteArgs {
   int32_t *ids, *pos, *src, *offsets, *counts;     // counts [blocks][experts], workspace
 };
 
-constexpr int kRouteTokens = 64, kRouteThreads = 1024, kRouteMost = 1024;
+// tokens a workgroup: 64 where one takes them all, else 32 (8192 tokens of 128 experts: a workgroup for every CU)
+constexpr int kRouteAlone = 64, kRouteTokens = 32, kRouteThreads = 1024, kRouteMost = 1024;
 
 // Order of scores as unsigned numbers, 0 for those that choose nothing (-inf, NaN); both zeros are one.
 __device__ __forceinline__ uint32_t score_order(float x) {
@@ -408,20 +421,20 @@ __device__ __forceinline__ int32_t group_before(int32_t x, int32_t *sum) {
 }
 
 // A wave takes a token, its lanes experts lane, lane + 64, ...: `top` times the largest
-// score left, the lowest index among equals. 64 tokens a workgroup: who chose an
+// score left, the lowest index among equals. Up to 64 tokens a workgroup: who chose an
 // expert is a mask of 64 bits in LDS (or-ed in any order, the same whatever it is), so
 // a choice's place among the workgroup's is the number of lower bits, and nothing
 // depends on which wave comes first. One workgroup alone (up to 64 tokens) goes on
 // to the rows itself: one launch.
-template <int NV, bool F32>
+template <int NV, bool F32, int TOKENS>
 __global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
   __shared__ unsigned long long chose[kRouteMost];
   __shared__ int32_t first[kRouteMost];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int e = tid; e < a.experts; e += kRouteThreads) chose[e] = 0;
   __syncthreads();
-  const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens;
-  constexpr int WAVES = kRouteThreads / 64, PER = kRouteTokens / WAVES;        // tokens wave, wave + WAVES, ...
+  const int64_t t0 = (int64_t)blockIdx.x * TOKENS;
+  constexpr int WAVES = kRouteThreads / 64, PER = TOKENS / WAVES;        // tokens wave, wave + WAVES, ...
   int32_t mine[PER];                                           // lane j: the token's choice j
   float x[PER][NV];
 #pragma unroll
@@ -518,7 +531,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
 }
 
 // Rows of one workgroup's tokens: those of earlier workgroups and of earlier experts come
-// before. Every workgroup adds up all counts (128 by 128 of them for 8192 tokens and
+// before. Every workgroup adds up all counts (256 by 128 of them for 8192 tokens and
 // 128 experts, from L2), instead of a launch between the two that would.
 __global__ void __launch_bounds__(kRouteThreads) route_place_k(RouteArgs a) {
   __shared__ int32_t sums[2][kRouteThreads];                   // before this workgroup's, and all
@@ -616,12 +629,18 @@ int check_route(int64_t tokens, int32_t experts, int32_t top) {
   return GLQ_OK;
 }
 
-int64_t route_blocks(int64_t tokens) { return (tokens + kRouteTokens - 1) / kRouteTokens; }
+int64_t route_blocks(int64_t tokens) { return tokens <= kRouteAlone ? 1 : (tokens + kRouteTokens - 1) / kRouteTokens; }
+
+template <int NV, bool F32>
+void launch_pick_tokens(const RouteArgs &a, hipStream_t st) {
+  if (a.blocks == 1) hipLaunchKernelGGL((route_pick_k<NV, F32, kRouteAlone>), dim3(1), dim3(kRouteThreads), 0, st, a);
+  else hipLaunchKernelGGL((route_pick_k<NV, F32, kRouteTokens>), dim3((unsigned)a.blocks), dim3(kRouteThreads), 0, st, a);
+}
 
 template <int NV>
 void launch_pick(const RouteArgs &a, glq_dtype dt, hipStream_t st) {
-  if (dt == GLQ_F32) hipLaunchKernelGGL((route_pick_k<NV, true>), dim3((unsigned)a.blocks), dim3(kRouteThreads), 0, st, a);
-  else hipLaunchKernelGGL((route_pick_k<NV, false>), dim3((unsigned)a.blocks), dim3(kRouteThreads), 0, st, a);
+  if (dt == GLQ_F32) launch_pick_tokens<NV, true>(a, st);
+  else launch_pick_tokens<NV, false>(a, st);
 }
 
 }  // namespace
@@ -647,15 +666,15 @@ extern "C" int glq_kv_plan(const glq_plan *P, void *hip_stream) {
       P->max_tokens > 0x7FFFFFFF || P->max_read > 0x7FFFFFFF || P->num_free > 0x7FFFFFFF || P->batch > 0x7FFFFFFF ||
       (P->batch > 0 && P->max_pages > (int64_t(1) << 40) / P->batch))
     return GLQ_ERR_UNSUPPORTED;
-  auto tiles = [](int64_t n) { return (uint32_t)((n + kPlanTile - 1) / kPlanTile); };
+  auto tiles = [](int64_t n, int64_t each) { return (uint32_t)((n + each - 1) / each); };
   PlanArgs a = {P->lens, P->added, P->free_pages, P->page_table, P->new_lens, P->cu_q, P->slots, P->positions, P->cu_k,
                 P->read_slots, P->used, P->batch, P->max_pages, P->num_free, P->num_pages, P->max_tokens, P->max_read,
                 log2_of(P->page_size), 1, 0, 0};
-  if (P->max_tokens > 0) a.q_tiles = tiles(P->max_tokens);
-  if (read) a.r_tiles = P->max_read > 0 ? tiles(P->max_read) : 1;
+  if (P->max_tokens > 0) a.q_tiles = tiles(P->max_tokens, kPlanTokens);
+  if (read) a.r_tiles = P->max_read > 0 ? tiles(P->max_read, kPlanTokens) : 1;
   // pages that max_tokens new ones can take
   const int64_t pages = P->max_tokens / P->page_size + P->batch;
-  a.p_groups = pages > 0 ? tiles(pages < P->batch * P->max_pages ? pages : P->batch * P->max_pages) : 1;
+  a.p_groups = pages > 0 ? tiles(pages < P->batch * P->max_pages ? pages : P->batch * P->max_pages, kPlanPages) : 1;
   const int64_t groups = (int64_t)a.q_tiles + a.r_tiles + a.p_groups;
   if (groups > kMaxGroups) return GLQ_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(kv_plan_k, dim3((unsigned)groups), dim3(kPlanThreads), 0, reinterpret_cast<hipStream_t>(hip_stream), a);
@@ -723,7 +742,6 @@ extern "C" int glq_route(const void *logits, glq_dtype dt, int64_t tokens, int32
     return GLQ_ERR_WORKSPACE;
   RouteArgs a = {logits, tokens, route_blocks(tokens), experts, top_k, (flags & GLQ_ROUTE_NORMALIZE) ? 1 : 0,
                  weights, ids, pos, src, offsets, reinterpret_cast<int32_t *>(workspace)};
-  if (a.blocks == 0) a.blocks = 1;                    // no tokens: offsets of zero
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   if (experts <= 64) launch_pick<1>(a, dt, st);
   else if (experts <= 128) launch_pick<2>(a, dt, st);
