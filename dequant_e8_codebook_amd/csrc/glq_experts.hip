@@ -313,7 +313,7 @@ __device__ __forceinline__ void cross_waves(float (&v)[16], float4 *buf, int wav
 #pragma unroll
     for (int q = 0; q < 4; ++q) buf[(4 * wave + q) * 64 + lane] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
   };
-  auto add = [&](int from, float s) {
+  auto add = [&](int from, float s) {                // v + s times the other's
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float4 f = buf[(4 * from + q) * 64 + lane];
@@ -321,28 +321,31 @@ __device__ __forceinline__ void cross_waves(float (&v)[16], float4 *buf, int wav
       v[4 * q + 2] = fmaf(f.z, s, v[4 * q + 2]), v[4 * q + 3] = fmaf(f.w, s, v[4 * q + 3]);
     }
   };
-  auto own = [&](float s) {
+  auto onto = [&](int from, float s) {               // s v + the other's
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= s;
+    for (int q = 0; q < 4; ++q) {
+      const float4 f = buf[(4 * from + q) * 64 + lane];
+      v[4 * q] = fmaf(v[4 * q], s, f.x), v[4 * q + 1] = fmaf(v[4 * q + 1], s, f.y);
+      v[4 * q + 2] = fmaf(v[4 * q + 2], s, f.z), v[4 * q + 3] = fmaf(v[4 * q + 3], s, f.w);
+    }
   };
   auto sign = [&](int bit) { return wave & bit ? -1.0f : 1.0f; };
   auto four = [&](int b) {                           // bits b and 2 b of the wave's number
     const float s1 = sign(b), s2 = sign(2 * b);
-    own(s1 * s2);
+    onto(wave ^ 3 * b, s1 * s2);
     add(wave ^ b, s2);
     add(wave ^ 2 * b, s1);
-    add(wave ^ 3 * b, 1.0f);
   };
   if constexpr (NW == 1) return;
   put();
   __syncthreads();
-  if constexpr (NW == 2) own(sign(1)), add(wave ^ 1, 1.0f);
+  if constexpr (NW == 2) onto(wave ^ 1, sign(1));
   else four(1);
   if constexpr (NW >= 8) {
     __syncthreads();
     put();
     __syncthreads();
-    if constexpr (NW == 8) own(sign(4)), add(wave ^ 4, 1.0f);
+    if constexpr (NW == 8) onto(wave ^ 4, sign(4));
     else four(4);
   }
 }
@@ -386,7 +389,9 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
   int e = 0;
   float scale = 0.0f;
   int32_t until = r0;                                // rows of e end here
-  uint32_t flip[8];                                  // sign bits of the elements, two a word (in place of two bf16)
+  // float32: sign bits of the elements, two a word. bf16: (s0, s1) of a word's two elements, whose product with the word is the first
+  // sum of the transform; that with (s0, -s1) is the first difference
+  uint32_t flip[8];
   const int64_t steps = a.kp / kGemmK;
   const float inv = rb_sgn(lane) / sqrtf((float)(1 << a.log_k));
   // The sums of row r, once all its waves have written theirs: eight lanes of the first wave a part along k, then all parts
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t two = s[i / 2] >> (16 * (i & 1));
-        flip[i] = (two & 0x80u) << 8 | (two & 0x8000u) << 16;
+        flip[i] = ((two & 0x80u) << 8 | (two & 0x8000u) << 16) | (F32 ? 0u : 0x3F803F80u);
       }
     }
     float v[16];
@@ -432,8 +437,9 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
-        w[i] ^= flip[i];
-        v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+        const bf16x2_t x2 = __builtin_bit_cast(bf16x2_t, w[i]);
+        v[2 * i] = __builtin_amdgcn_fdot2_f32_bf16(x2, __builtin_bit_cast(bf16x2_t, flip[i]), 0.0f, false);
+        v[2 * i + 1] = __builtin_amdgcn_fdot2_f32_bf16(x2, __builtin_bit_cast(bf16x2_t, flip[i] ^ 0x80000000u), 0.0f, false);
       }
       top = most.x > most.y ? most.x : most.y;
       top = row_max<32>(top);
@@ -443,32 +449,37 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
     }
     if (r + 1 < r1) fetch(r + 1);
     if (waves > 1) __syncthreads();                  // tops; the exchange and the sums of the row before are through
-    int shift = 0;
+    int shift = 0, before = 0;
     if constexpr (!F32) {
       if (r > r0) finish(r - 1);
       for (int w = 0; w < waves; ++w) top = top > tops[w] ? top : tops[w];
       shift = row_exponent(top << 16, a.k);
+      // 2^-shift waits for the end, where it costs nothing, unless sums of 16384 could leave float32's range before
+      if (shift > 100 || shift < -100) {             // uniform
+        before = -shift;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = ldexpf(v[i], -shift);
+        for (int i = 0; i < 16; ++i) v[i] = ldexpf(v[i], before);
+      }
     }
     if (tid == 0) a.row_expert[r] = e, a.row_factor[r] = ldexpf(scale, shift);
-    rb_fwht_wave<0, true>(v, lane);
+    rb_fwht_wave<F32 ? 0 : 1, true>(v, lane);
     cross_waves<NW>(v, cross, wave, lane);
+    const float scaled = ldexpf(inv, -shift - before);
     float here[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = v[8 * h + i] * inv;
+      for (int i = 0; i < 8; ++i) x[i] = v[8 * h + i] * scaled;
 #pragma unroll
       for (int p = 0; p < (F32 ? 3 : 1); ++p) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           w[i / 2] = pack_bf16(x[i], x[i + 1]);
-          const float lo = bf16_lo(w[i / 2]), hi = bf16_hi(w[i / 2]);
-          if constexpr (F32) x[i] -= lo, x[i + 1] -= hi;
-          else here[h] += lo + hi;
+          if constexpr (F32) x[i] -= bf16_lo(w[i / 2]), x[i + 1] -= bf16_hi(w[i / 2]);
+          else here[h] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w[i / 2]),
+                                                         __builtin_bit_cast(bf16x2_t, 0x3F803F80u), here[h], false);
         }
         *reinterpret_cast<uint4 *>(a.xt + ((int64_t)p * a.rows + r) * a.kp + eo + 256 * h) = make_uint4(w[0], w[1], w[2], w[3]);
       }
@@ -599,13 +610,13 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
     if (it.row >= 0 || sets > 1) {
       cross_waves<NW>(v, cross, wave, lane);
       if (it.row >= 0) {
+        // the factor with each output sign put in its place
         const float f = it.factor * rb_sgn(lane);
+        const uint32_t turn = f < 0.0f ? 0x80808080u : 0u;
+        const uint32_t s[4] = {it.sign[0].x ^ turn, it.sign[0].y ^ turn, it.sign[1].x ^ turn, it.sign[1].y ^ turn};
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const uint2 s = it.sign[q / 8];
-          const uint32_t w = q & 4 ? s.y : s.x;
-          acc[q] = fmaf(__uint_as_float(__float_as_uint(v[q]) ^ ((w << (24 - 8 * (q & 3))) & 0x80000000u)), f, acc[q]);
-        }
+        for (int q = 0; q < 16; ++q)
+          acc[q] = fmaf(v[q], copysignf(f, __uint_as_float(s[q / 4] << (24 - 8 * (q & 3)))), acc[q]);
       }
       if constexpr (NW > 1) __syncthreads();         // the exchange is read
     }
@@ -1059,7 +1070,10 @@ int launch_blocks_k(const XpRows &a, int64_t most, hipStream_t st) {
   if (OUT && most <= kCus)
     while (2 * sets * waves <= kRowWaves && sets < a.top) sets *= 2;
   const size_t shm = NW > 1 || sets > 1 ? (size_t)waves * sets * 4096 : 0;
-  const int64_t once = (int64_t)kCus * (24 / waves > 1 ? 24 / waves : 1), groups = most < once ? most : once;
+  // no more workgroups than run at once, by the registers of the kernels: waves a SIMD
+  constexpr int resident = 4 * (OUT ? 4 : NW == 1 ? 8 : NW == 2 ? 6 : 5);
+  const int per = resident / (waves * sets);
+  const int64_t once = (int64_t)kCus * (per > 1 ? per : 1), groups = most < once ? most : once;
   if constexpr (OUT) {
     const int rc = allow_lds<xp_out_blk_k<NW, F32, Z16>>(shm + 2048);          // (and the static part)
     if (rc) return rc;
