@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
     for (int j = 0; j < a.top; ++j) {
       const int32_t r = a.pos ? a.pos[row_y * a.top + j] : (int32_t)row_y;
       if (r < first || r >= end) continue;           // uniform
-      const int e = a.row_expert[r], parts = a.row_parts[r];
+      const int e = a.row_expert[r], parts = bounded(a.row_parts[r], a.ks);     // (decreasing offsets: rows no tile was for)
       const float w = (a.pos ? a.weights[row_y * a.top + j] * inv : inv) * a.row_factor[r];
       const int8_t *signs = a.sign_n + (int64_t)e * a.n;
       float v[E];
@@ -359,7 +359,7 @@ __device__ __forceinline__ void my_run(int64_t first, int64_t n, int32_t &r0, in
 template <int NW, bool F32>
 __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
   extern __shared__ __attribute__((aligned(16))) float4 cross[];
-  __shared__ uint32_t tops[kRowWaves];
+  __shared__ uint32_t tops[2][F32 ? 1 : kRowWaves];  // of this row and the one before, which waves of other blocks may still read
   __shared__ float sums[2][F32 ? 1 : kSplitSteps];   // of the steps of 64 elements, of this row and the one before
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int32_t first = bounded(a.offsets[0], a.rows), end = bounded(a.offsets[a.count], a.rows);
@@ -445,14 +445,14 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
       top = row_max<32>(top);
       const auto both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
       top = both[0] > both[1] ? both[0] : both[1];
-      if (lane == 0) tops[wave] = top;
+      if (lane == 0) tops[r & 1][wave] = top;
     }
     if (r + 1 < r1) fetch(r + 1);
     if (waves > 1) __syncthreads();                  // tops; the exchange and the sums of the row before are through
     int shift = 0, before = 0;
     if constexpr (!F32) {
       if (r > r0) finish(r - 1);
-      for (int w = 0; w < waves; ++w) top = top > tops[w] ? top : tops[w];
+      for (int w = 0; w < waves; ++w) top = top > tops[r & 1][w] ? top : tops[r & 1][w];
       shift = row_exponent(top << 16, a.k);
       // 2^-shift waits for the end, where it costs nothing, unless sums of 16384 could leave float32's range before
       if (shift > 100 || shift < -100) {             // uniform
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
         if (a.pos) factor *= a.weights[(y0 + y) * a.top + j];
       }
       if (row >= 0) {
-        expert = a.row_expert[row], parts = a.row_parts[row];
+        expert = a.row_expert[row], parts = bounded(a.row_parts[row], a.ks);   // (decreasing offsets: rows no tile was for)
         factor *= a.row_factor[row];
       }
     }
@@ -664,13 +664,6 @@ struct XpProduct {
   uint32_t likely;             // workgroups that very likely have a tile
   int32_t ks;                  // parts along k of the rows that are split
 };
-
-// z of row r (its plane of the part) at weight row j: a sum over inputs in units of the operands, without the scales.
-template <bool F32> __device__ __forceinline__ void store_z(const XpProduct &a, int part, int32_t r, int64_t j, float v) {
-  const int64_t at = ((int64_t)part * a.rows + r) * a.n + j;
-  if constexpr (F32) reinterpret_cast<float *>(a.z)[at] = v;
-  else reinterpret_cast<_Float16 *>(a.z)[at] = (_Float16)v;
-}
 
 // biased operands (bf16 of 192 + u) to bf16 of u, exact
 __device__ __forceinline__ uint4 unbiased(uint4 w) {

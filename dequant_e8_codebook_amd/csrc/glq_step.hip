@@ -662,9 +662,10 @@ extern "C" int glq_kv_plan(const glq_plan *P, void *hip_stream) {
   for (const void *p : words)
     if (!aligned4(p)) return GLQ_ERR_ARG;
   if (P->batch > 0 && (P->new_lens == P->lens || P->new_lens == P->added)) return GLQ_ERR_ARG;
-  if (P->num_pages > 0x7FFFFFFF / P->page_size || P->max_pages > 0x7FFFFFFF / P->page_size ||
-      P->max_tokens > 0x7FFFFFFF || P->max_read > 0x7FFFFFFF || P->num_free > 0x7FFFFFFF || P->batch > 0x7FFFFFFF ||
-      (P->batch > 0 && P->max_pages > (int64_t(1) << 40) / P->batch))
+  // (a tile's entries, and what lies a tile further, are numbered in 32 bits)
+  constexpr int64_t most = 0x7FFFFFFF - 2 * kPlanTokens;
+  if (P->num_pages > 0x7FFFFFFF / P->page_size || P->max_pages > 0x7FFFFFFF / P->page_size || P->max_tokens > most ||
+      P->max_read > most || P->num_free > 0x7FFFFFFF || P->batch > most || (P->batch > 0 && P->max_pages > most / P->batch))
     return GLQ_ERR_UNSUPPORTED;
   auto tiles = [](int64_t n, int64_t each) { return (uint32_t)((n + each - 1) / each); };
   PlanArgs a = {P->lens, P->added, P->free_pages, P->page_table, P->new_lens, P->cu_q, P->slots, P->positions, P->cu_k,
@@ -697,6 +698,8 @@ extern "C" int glq_qk_norm_rope(const glq_qk *N, const glq_kv_cache *C, uint32_t
       !valid_rows(N->k, N->k_stride, N->kv_heads, d, N->dt))
     return GLQ_ERR_ARG;
   if ((N->k_out || !C) && !valid_rows(N->k_out, N->k_out_stride, N->kv_heads, d, N->dt)) return GLQ_ERR_ARG;
+  if ((N->q_out == N->q && N->q_out_stride != N->q_stride) || (N->k_out == N->k && N->k_out_stride != N->k_stride))
+    return GLQ_ERR_ARG;
   if (C && (!valid_rows(N->v, N->v_stride, N->kv_heads, d, N->dt) || !N->slots || !aligned4(N->slots))) return GLQ_ERR_ARG;
   if (!aligned16(N->q_weight) || !aligned16(N->k_weight)) return GLQ_ERR_ARG;
   if (N->rotary_dim > 0 && (!N->positions || !aligned4(N->positions) || !N->rotary || !aligned16(N->rotary) || N->max_positions < 1))

@@ -1038,6 +1038,8 @@ class Experts:
     @staticmethod
     def stack(layers) -> "Experts":
         """The experts that a list of Layer (one shape, bit width and codebook) describes, copied together."""
+        if not layers:
+            raise ValueError("layers: none")
         first = layers[0]
         if any((x.n, x.k, x.bpw, x.row_scale is None) != (first.n, first.k, first.bpw, first.row_scale is None)
                for x in layers):

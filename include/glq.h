@@ -540,6 +540,7 @@ typedef struct {
  *   Entries behind the last token (a padded batch): slot -1, position 0.
  *   More tokens than max_tokens or max_read: what does not fit is not written, and offsets
  *   end at those lengths.
+ * GLQ_ERR_UNSUPPORTED for lists or a page table of 2^31 - 4096 entries or more.
  * One launch. The caller takes *used pages off its free ones. batch == 0 gives offsets of 0 and empty lists.
  */
 int glq_kv_plan(const glq_plan *P, void *hip_stream);
@@ -646,16 +647,17 @@ typedef struct {
  * glq_expert_linear -- each row through its own expert: y_r = U_e^T (s_e W^_e) (V_e x_r) for
  * the rows r of expert e, as glq_fused_linear does for one layer; with pos (a token's rows, from
  * glq_route) y_t = sum_j weights[t][j] y_pos[t][j], summed in float32 in a fixed order and rounded once.
- *   x_dt = GLQ_BF16: x~ rounded to bf16 (2^-8 relative at most), weights exact in bf16, float32 sums on the
- *                    matrix cores, z = s W^ x~ kept in float32
+ *   x_dt = GLQ_BF16: x~ rounded to bf16 (2^-9 of its size), weights exact in bf16, float32 sums on the matrix
+ *                    cores, z = s W^ x~ rounded to float16 (2^-12) with a power of two for each row
  *   x_dt = GLQ_F32:  x~ as three bf16 parts that hold its 24 bits, so the products are those of float32 operands;
- *                    float32 sums
+ *                    float32 sums, z in float32
  *   workspace   device, 256-byte aligned, >= glq_expert_linear_workspace(E, rows) bytes (that of more rows
  *               serves fewer; 0 for what would be refused). Need not be cleared; concurrent calls need workspaces
  *               of their own.
  * Without pos, rows that are no expert's are not written; with it, a token without rows gets zeros. y must not overlap x.
  * rows == 0 (with pos: tokens == 0) is a successful no-op. GLQ_ERR_UNSUPPORTED for more than 1024 experts,
- * Hadamard blocks above 16384, and 2^22 rows or tokens. Three launches.
+ * n or k above 2^21, Hadamard blocks above 16384, 2^22 rows or tokens, top_k above 1024, and about 2^23 tiles of 256
+ * (float32: 64) rows by 256 outputs. Three launches.
  */
 size_t glq_expert_linear_workspace(const glq_experts *E, int64_t rows);
 int glq_expert_linear(const glq_experts *E, const glq_expert_rows *R, void *workspace, size_t ws_bytes,
