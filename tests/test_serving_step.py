@@ -5,6 +5,8 @@ serve several calls, and at sizes where offsets leave 32 bits.
 Each link is held to the plain formula on what the link before it gave, with the tolerances of the tests of the
 single calls; graphs, streams and shared workspaces are held to the same bits as plain calls.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -548,7 +550,7 @@ def test_plan_refuses_lists_past_32_bits(change, status):
                         p + 960, p + 1024)
     for name, value in change.items():
         setattr(st, name, value)
-    assert glq.raw().glq_kv_plan(st, None) == status
+    assert glq.raw().glq_kv_plan(ctypes.byref(st), None) == status
 
 
 @pytest.mark.parametrize("change", [{"q_out_stride": 512}, {"k_out_stride": 512}])
@@ -557,4 +559,4 @@ def test_norm_rope_refuses_its_input_in_another_stride(change):
     st = glq.QkStruct(p, p + 512, p, p + 512, 1, 4, 2, 64, 256, 128, 256, 128, 3, p, p, 1e-6, 64, p, p, 10, 0, 0, 0)
     for name, value in change.items():
         setattr(st, name, value)
-    assert glq.raw().glq_qk_norm_rope(st, None, 0, None) == -1
+    assert glq.raw().glq_qk_norm_rope(ctypes.byref(st), None, 0, None) == -1
