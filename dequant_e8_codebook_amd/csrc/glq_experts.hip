@@ -362,16 +362,17 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
   __shared__ uint32_t tops[2][F32 ? 1 : kRowWaves];  // of this row and the one before, which waves of other blocks may still read
   __shared__ float sums[2][F32 ? 1 : kSplitSteps];   // of the steps of 64 elements, of this row and the one before
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+  // A workgroup for each row there can be: its row is known before the offsets are, and so are its loads.
+  const bool each = gridDim.x == (uint32_t)a.rows;   // uniform
+  int32_t sources = each && a.src ? a.src[blockIdx.x] : 0;
   const int32_t first = bounded(a.offsets[0], a.rows), end = bounded(a.offsets[a.count], a.rows);
-  int32_t r0, r1;
-  my_run(first, end > first ? end - first : 0, r0, r1);
-  if (r0 >= r1) return;
+  int32_t r0 = blockIdx.x, r1 = r0 + 1;
+  if (!each) my_run(first, end > first ? end - first : 0, r0, r1);
   const int el = 1024 * wave + 8 * rb_ell(lane), eo = 1024 * wave + rb_elem_out(lane, 0);    // elements read, written (+ 512, + 256)
   constexpr int RAW = F32 ? 4 : 2;
   uint4 raw[RAW];
-  int32_t sources = 0;
   auto fetch = [&](int32_t r) {
-    if (a.src && ((r - r0) & 63) == 0) sources = r + lane < r1 ? a.src[r + lane] : -1;
+    if (a.src && !each && ((r - r0) & 63) == 0) sources = r + lane < r1 ? a.src[r + lane] : -1;
     const int64_t from = a.src ? __builtin_amdgcn_readlane(sources, (r - r0) & 63) : r;
     if (from >= 0 && from < a.x_rows) {
       const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.x) + (F32 ? 4 : 2) * (from * a.k + el));
@@ -385,7 +386,8 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
       for (int i = 0; i < RAW; ++i) raw[i] = make_uint4(0, 0, 0, 0);
     }
   };
-  fetch(r0);
+  if (r0 < r1) fetch(r0);                            // (of any row there is room for)
+  if (r0 >= r1 || r0 < first || r0 >= end) return;
   int e = 0;
   float scale = 0.0f;
   int32_t until = r0;                                // rows of e end here
