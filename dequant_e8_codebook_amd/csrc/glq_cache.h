@@ -1,6 +1,7 @@
 // glq_cache.h -- the paged key-value cache's rows (library-internal): conversions,
-// the write of a token's head, and the argument checks of the calls on it. Included by the
-// attention calls (glq_attn.hip) and those that prepare for them (glq_step.hip).
+// the write of a token's head, and the argument checks and error text of the calls on it. Included
+// by the attention calls (glq_attn.hip), those of the step around them (glq_step.hip) and, for
+// the checks and conversions, by those of the experts (glq_experts.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 

@@ -53,14 +53,14 @@ struct XpRows {
   const void *z;               // [parts][rows][n]: float32 or float16, both without row_factor
   const float *scale, *row_scale;
   float unit;                  // of the operands: 1, 1/4 or 1/8 of a weight at 2, 3 or 4 bits
-  int64_t k, kp, n, x_rows, out_rows;    // kp: k up to a multiple of 64
+  int64_t k, kp, n, x_rows, out_rows;    // kp: k up to a multiple of 128
   int32_t count, rows, top, ks;
   int log_k, log_n;            // Hadamard blocks
 };
 
-// The product's steps of 64 inputs, and the first one of part `part` of `parts`
+// The product's steps of 64 inputs, and the first one of part `part` of `parts`: steps come in pairs
 constexpr int kGemmK = 64, kSplitSteps = 256;        // rows of more steps (16384 inputs) are not split
-__device__ __forceinline__ int part_begin(int64_t steps, int part, int parts) { return (int)(steps * part / parts); }
+__device__ __forceinline__ int part_begin(int64_t steps, int part, int parts) { return 2 * (int)(steps / 2 * part / parts); }
 
 // The transform of up to 64 NW E elements held E a thread, block 2^logb, each thread
 // with its own elements again afterwards.
@@ -775,14 +775,15 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   const int64_t e = tile.e;
   constexpr bool F32 = P == 3;
   constexpr int TPH = MB < 4 ? MB : 4, HB = MB / TPH;          // MFMA tiles of a run, runs of one of the 4 k-steps
-  constexpr int RP = MB < 2 ? 64 : 32 * MB;                    // rows of a part in LDS
-  constexpr int PIECES = RP / 64;                              // of 64 rows, a part
+  constexpr int KS = MB * P <= 3 ? 2 : 1;                      // 64s of inputs in a step
+  constexpr int RP = 32 * MB;                                  // rows of a part in LDS
+  constexpr int PIECES = RP * KS / 64, LDA = KS * kGemmK + 8;  // loads of 16 bytes a thread, a part; a row in LDS
   uint16_t *As0 = reinterpret_cast<uint16_t *>(lds + lds_table_bytes<BPW>());
   uint16_t *As1 = As0 + gemm_rows(F32) * kGemmLda;
   const int lane = tid & 63, c = lane & 31, p = lane >> 5;
   const int64_t G = a.k / 8, steps = a.kp / kGemmK;
-  const int64_t begin = part_begin(steps, tile.part, tile.parts);
-  const int64_t S = part_begin(steps, tile.part + 1, tile.parts) - begin;       // steps of this part
+  const int64_t begin = part_begin(steps, tile.part, tile.parts) / KS;
+  const int64_t S = part_begin(steps, tile.part + 1, tile.parts) / KS - begin;  // steps of this part
   const int64_t left = a.n - n0, rows_w = left < 0 ? 0 : left < 32 ? left : 32, wrow = e * a.n + (rows_w ? n0 : 0);
   __amdgpu_buffer_rsrc_t xa[P];
 #pragma unroll
@@ -794,41 +795,66 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   const __amdgpu_buffer_rsrc_t r2 = __builtin_amdgcn_make_buffer_rsrc(
       BPW == 2 ? (void *)a.idx1 : (void *)(reinterpret_cast<const uint8_t *>(a.idx2) + wrow * G * (BPW == 4 ? 2 : 1)), 0,
       (int)(BPW == 2 ? 0 : rows_w * G * (BPW == 4 ? 2 : 1)), 0x00020000);
-  const uint32_t va = (uint32_t)((tid >> 3) * a.kp * 2 + 16 * (tid & 7));
-  const uint32_t vi = (uint32_t)(c * G + 4 * p);               // this lane's first index of step 0
-  const int sa = (int)(64 * a.kp * 2);
+  const int row_t = tid / (8 * KS), chunk_t = tid % (8 * KS);
+  const uint32_t va = (uint32_t)(row_t * a.kp * 2 + 16 * chunk_t);
+  const uint32_t vi = (uint32_t)(c * G + 4 * KS * p);          // this lane's first index of step 0
+  const int sa = (int)(64 / KS * a.kp * 2);
   auto load_a = [&](int64_t s, uint4 (&ra)[P * PIECES]) {
 #pragma unroll
     for (int q = 0; q < P; ++q)
 #pragma unroll
       for (int u = 0; u < PIECES; ++u)
         ra[q * PIECES + u] = __builtin_bit_cast(
-            uint4, __builtin_amdgcn_raw_buffer_load_b128(xa[q], va, (int)(2 * kGemmK * (begin + s)) + u * sa, 0));
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(xa[q], va, (int)(2 * KS * kGemmK * (begin + s)) + u * sa, 0));
   };
   auto store_a = [&](uint16_t *As, const uint4 (&ra)[P * PIECES]) {
 #pragma unroll
     for (int i = 0; i < P * PIECES; ++i)
-      *reinterpret_cast<uint4 *>(As + ((tid >> 3) + 64 * i) * kGemmLda + 8 * (tid & 7)) = ra[i];
+      *reinterpret_cast<uint4 *>(As + (row_t + 64 / KS * i) * LDA + 8 * chunk_t) = ra[i];
   };
-  // indices of step s as stored; those past a row's end meet zeros of x~
-  auto load_idx = [&](int64_t step, uint2 &i1, uint2 &i2) {
-    const int64_t s = begin + step;
-    i2 = make_uint2(0u, 0u);
-    if constexpr (G4) {
-      i1 = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r1, 2 * vi, (int)(16 * s), 0));
-      if constexpr (BPW == 3) i2.x = __builtin_amdgcn_raw_buffer_load_b32(r2, vi, (int)(8 * s), 0);
-      if constexpr (BPW == 4) i2 = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r2, 2 * vi, (int)(16 * s), 0));
-    } else {
-      uint32_t w[4], v[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        w[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r1, 2 * vi, (int)(16 * s + 2 * u), 0);
-        if constexpr (BPW == 3) v[u] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r2, vi, (int)(8 * s + u), 0);
-        if constexpr (BPW == 4) v[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r2, 2 * vi, (int)(16 * s + 2 * u), 0);
+  // indices of step s as stored, 4 KS of them; those past a row's end meet zeros of x~
+  struct Indices { uint2 i1[KS], i2[KS]; };
+  auto load_idx = [&](int64_t step, Indices &x) {
+    const int at = (int)(8 * KS * (begin + step));             // in indices
+    if constexpr (G4 && KS == 1) {
+      x.i1[0] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r1, 2 * vi, 2 * at, 0));
+      if constexpr (BPW == 3) x.i2[0].x = __builtin_amdgcn_raw_buffer_load_b32(r2, vi, at, 0);
+      if constexpr (BPW == 4) x.i2[0] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r2, 2 * vi, 2 * at, 0));
+    } else if constexpr (G4) {
+      const uint4 w = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r1, 2 * vi, 2 * at, 0));
+      x.i1[0] = make_uint2(w.x, w.y), x.i1[KS - 1] = make_uint2(w.z, w.w);
+      if constexpr (BPW == 3) {
+        const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r2, vi, at, 0));
+        x.i2[0].x = v.x, x.i2[KS - 1].x = v.y;
       }
-      i1 = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-      if constexpr (BPW == 3) i2.x = v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24;
-      if constexpr (BPW == 4) i2 = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+      if constexpr (BPW == 4) {
+        const uint4 v = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r2, 2 * vi, 2 * at, 0));
+        x.i2[0] = make_uint2(v.x, v.y), x.i2[KS - 1] = make_uint2(v.z, v.w);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < KS; ++h) {
+        uint32_t w[4], v[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int o = at + 4 * h + u;
+          w[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r1, 2 * vi, 2 * o, 0);
+          if constexpr (BPW == 3) v[u] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r2, vi, o, 0);
+          if constexpr (BPW == 4) v[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r2, 2 * vi, 2 * o, 0);
+        }
+        x.i1[h] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        if constexpr (BPW == 3) x.i2[h].x = v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24;
+        if constexpr (BPW == 4) x.i2[h] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+      }
+    }
+  };
+  auto split = [&](const Indices &x, uint32_t (&q1)[8], uint32_t (&q2)[8]) {
+#pragma unroll
+    for (int h = 0; h < KS; ++h) {
+      uint32_t p1[8], p2[8];
+      g8_split<BPW>(x.i1[h], BPW == 2 ? make_uint2(0u, 0u) : x.i2[h], p1, p2);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) q1[4 * h + u] = p1[u], q2[4 * h + u] = p2[u];
     }
   };
   uint4 ra[P * PIECES];
@@ -837,11 +863,11 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   if constexpr (!F32 && BPW > 2)
     if (tid < 256 && tid < row1 - row0)
       row_sum = a.rowsum[(tile.parts > 1 ? 1 + tile.part : 0) * (int64_t)a.rows + row0 + tid];
-  uint2 i1, i2, j1, j2;
-  load_idx(0, i1, i2);
+  Indices now, next;
+  load_idx(0, now);
   tables_landed();                                             // and the first tile and indices
   store_a(As0, ra);
-  load_idx(S > 1 ? 1 : 0, j1, j2);
+  load_idx(S > 1 ? 1 : 0, next);
   load_a(S > 1 ? 1 : 0, ra);
   __syncthreads();
   f32x16 acc[MB];
@@ -849,16 +875,14 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   for (int t = 0; t < MB; ++t)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
-  uint4 B0[8], B1[8];                                          // groups u = 0 .. 3 used
+  uint4 B0[8], B1[8];                                          // groups u = 0 .. 4 KS - 1 used
   auto plain = [](uint4 w) { return F32 && BPW > 2 ? unbiased(w) : w; };
   {
     uint32_t q1[8], q2[8];
-    g8_split<BPW>(i1, i2, q1, q2);
+    split(now, q1, q2);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) B0[u] = plain(decode_ip<BPW>(q1[u], q2[u]));
+    for (int u = 0; u < 4 * KS; ++u) B0[u] = plain(decode_ip<BPW>(q1[u], q2[u]));
   }
-  i1 = j1;
-  i2 = j2;
   uint4 H0[P * TPH], H1[P * TPH];                              // operands of even and odd runs
   auto read_a = [&](const uint16_t *As, int run, uint4 (&h)[P * TPH]) {
     const int u = run / HB, t0 = TPH * (run % HB);
@@ -866,17 +890,17 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
     for (int q = 0; q < P; ++q)
 #pragma unroll
       for (int t = 0; t < TPH; ++t)
-        h[q * TPH + t] = *reinterpret_cast<const uint4 *>(As + (q * RP + 32 * (t0 + t) + c) * kGemmLda + 32 * p + 8 * u);
+        h[q * TPH + t] = *reinterpret_cast<const uint4 *>(As + (q * RP + 32 * (t0 + t) + c) * LDA + 32 * KS * p + 8 * u);
   };
   read_a(As0, 0, H0);
   auto kstep = [&](int64_t s, const uint4 (&bc)[8], uint4 (&bn)[8]) {
     const uint16_t *Acur = (s & 1) ? As1 : As0;
     uint16_t *Anext = (s & 1) ? As0 : As1;
     uint32_t q1[8], q2[8];
-    g8_split<BPW>(i1, i2, q1, q2);                             // of step s + 1
-    load_idx(s + 2 < S ? s + 2 : S - 1, i1, i2);
+    split(next, q1, q2);                                       // of step s + 1
+    load_idx(s + 2 < S ? s + 2 : S - 1, next);
     auto run = [&](int h, const uint4 (&av)[P * TPH], uint4 (&an)[P * TPH]) {
-      if (h + 1 < 4 * HB) read_a(Acur, h + 1, an);
+      if (h + 1 < 4 * KS * HB) read_a(Acur, h + 1, an);
       else read_a(Anext, 0, an);
       const int u = h / HB, t0 = TPH * (h % HB);
 #pragma unroll
@@ -888,7 +912,7 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
     };
     constexpr int NW = BPW == 4 ? 2 : 1;                       // table walks a group
     Dec8<BPW, true> D;
-    D.template p1<0, 4>(q1, q2);
+    D.template p1<0, 4 * KS>(q1, q2);
     if constexpr (HB == 2) {                                   // the eight runs and their mix as in gemm8_bf16
       run(0, H0, H1);
       gm_interleave<4, 3, (4 * NW + (BPW == 3 ? 4 : 0) + 4 + 3) / 4>();
@@ -919,6 +943,25 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
       __syncthreads();
       run(7, H1, H0);
       __builtin_amdgcn_sched_barrier(0);
+    } else if constexpr (KS == 2) {
+      run(0, H0, H1);
+      run(1, H1, H0);
+      __builtin_amdgcn_sched_barrier(0);
+      D.template p2<0, 4>(q1, q2);
+      run(2, H0, H1);
+      D.template p2<4, 8>(q1, q2);
+      run(3, H1, H0);
+      __builtin_amdgcn_sched_barrier(0);
+      store_a(Anext, ra);
+      load_a(s + 2 < S ? s + 2 : S - 1, ra);
+      run(4, H0, H1);
+      run(5, H1, H0);
+      D.template p3<0, 8>(bn);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) bn[u] = plain(bn[u]);
+      run(6, H0, H1);
+      __syncthreads();
+      run(7, H1, H0);
     } else {
       run(0, H0, H1);
       __builtin_amdgcn_sched_barrier(0);
@@ -1032,7 +1075,7 @@ template <auto Kernel> int allow_lds(size_t bytes) {
 }
 
 bool aligned_to(const void *p, int a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-int64_t up64(int64_t v) { return (v + 63) & ~int64_t(63); }
+int64_t up128(int64_t v) { return (v + 127) & ~int64_t(127); }
 int64_t up256(int64_t v) { return (v + 255) & ~int64_t(255); }
 
 int log_block(int64_t len) {
@@ -1145,7 +1188,7 @@ int check_experts(const glq_experts *E) {
 // Parts along k of the units that are split (XpTiles): as many as give each CU one, for the most tiles there can be, but none under
 // 4 steps, which would not pay for the transforms' reading more planes.
 int xp_parts(int64_t count, int64_t n, int64_t k, int64_t rows, bool f32) {
-  const int64_t steps = up64(k) / kGemmK, most = (rows / (f32 ? 64 : 256) + (count < rows ? count : rows)) * ((n + 255) / 256);
+  const int64_t steps = up128(k) / kGemmK, most = (rows / (f32 ? 64 : 256) + (count < rows ? count : rows)) * ((n + 255) / 256);
   if (steps > kSplitSteps || steps < 8) return 1;
   int ks = 2;
   while (ks < 8 && most * 2 * ks <= kCus && steps / (2 * ks) >= 4) ks *= 2;
@@ -1169,7 +1212,7 @@ struct XpLayout { int64_t xt, rowsum, row_factor, row_expert, row_parts, z, tota
 XpLayout xp_layout(const glq_experts *E, int64_t rows) {
   XpLayout w;
   w.xt = 0;
-  w.rowsum = w.xt + up256(rows * up64(E->k) * 6);    // float32 rows: three parts of 2 bytes
+  w.rowsum = w.xt + up256(rows * up128(E->k) * 6);    // float32 rows: three parts of 2 bytes
   w.row_factor = w.rowsum + up256(rows * 4 * 9);        // whole, and eight parts at most
   w.row_expert = w.row_factor + up256(rows * 4);
   w.row_parts = w.row_expert + up256(rows * 4);
@@ -1221,7 +1264,7 @@ extern "C" int glq_expert_linear(const glq_experts *E, const glq_expert_rows *R,
   a.xt = reinterpret_cast<uint16_t *>(ws + l.xt), a.rowsum = reinterpret_cast<float *>(ws + l.rowsum);
   a.row_factor = reinterpret_cast<float *>(ws + l.row_factor), a.row_expert = reinterpret_cast<int32_t *>(ws + l.row_expert);
   a.row_parts = reinterpret_cast<int32_t *>(ws + l.row_parts), a.z = ws + l.z;
-  a.k = E->k, a.kp = up64(E->k), a.n = E->n, a.x_rows = R->x_rows, a.out_rows = out;
+  a.k = E->k, a.kp = up128(E->k), a.n = E->n, a.x_rows = R->x_rows, a.out_rows = out;
   a.count = (int32_t)E->count, a.rows = (int32_t)R->rows, a.top = R->pos ? R->top_k : 1, a.ks = ks;
   a.log_k = log_block(E->k), a.log_n = log_block(E->n);
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);

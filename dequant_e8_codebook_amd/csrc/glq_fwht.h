@@ -1,6 +1,7 @@
 // glq_fwht.h -- the Walsh-Hadamard transform of a workgroup's elements in registers,
 // lane exchanges and one LDS transpose (library-internal). Included by the kernels of single
-// layers (glq_kernels.hip) and of grouped experts (glq_experts.hip).
+// layers (glq_kernels.hip) and of grouped experts (glq_experts.hip); its lane exchange also by
+// glq_step.hip.
 #pragma once
 #include <hip/hip_runtime.h>
 
