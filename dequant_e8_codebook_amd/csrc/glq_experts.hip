@@ -757,6 +757,10 @@ struct XpTiles {
   }
 };
 
+// Tiles of so few rows read x~ from memory straight into operands (see gemm_tile): product of 16 experts of 4096 x 4096 with 4 rows each, at
+// 4 bits 57.0 us through LDS, 49.7 so, at 3 bits 50.0 and 46.0; 64 experts of 1024 x 2048 at 2 bits with 1, 4, 8 and 24 rows
+// 21.6, 21.2, 22.2 and 22.3 against 19.8, 21.6, 24.4 and 34.
+constexpr int kDirectRows = 4;
 constexpr int kGemmThreads = 512, kGemmLda = kGemmK + 8;
 // rows of x~ in LDS, of which there are two tiles: 256 of bf16 x~, 64 of each part of float32 x~
 constexpr int gemm_rows(bool f32) { return f32 ? 192 : 256; }
@@ -768,7 +772,7 @@ constexpr size_t gemm_lds(size_t tables, bool f32) { return tables + 2 * sizeof(
 // barrier a step of 64 inputs) and its weights rebuilt straight into the other operand a step ahead,
 // so each weight is rebuilt once a workgroup. The step's MFMAs come in runs; the walk of the
 // next step's indices (records, halves, combination) and the tile's loads and writes are spread over them.
-template <int BPW, bool G4, int MB, int P>
+template <int BPW, bool G4, int MB, int P, bool DIRECT = false>
 __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, const XpTile &tile, int64_t n0) {
   const int tid = threadIdx.x;
   const int32_t row0 = tile.row0, row1 = tile.row1;
@@ -857,8 +861,16 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
       for (int u = 0; u < 4; ++u) q1[4 * h + u] = p1[u], q2[4 * h + u] = p2[u];
     }
   };
-  uint4 ra[P * PIECES];
-  load_a(0, ra);
+  auto load_x = [&](int64_t s, uint4 (&x)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      x[u] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(xa[0], (uint32_t)(c * a.kp * 2 + 128 * p),
+                                                                             (int)(256 * (begin + s)) + 16 * u, 0));
+  };
+  auto upto = [&](int64_t s) { return s < S ? s : S - 1; };
+  uint4 ra[P * PIECES], X0[8], X1[8];
+  if constexpr (DIRECT) load_x(0, X0);
+  else load_a(0, ra);
   float row_sum = 0.0f;                                        // thread t: of row row0 + t
   if constexpr (!F32 && BPW > 2)
     if (tid < 256 && tid < row1 - row0)
@@ -866,10 +878,12 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   Indices now, next;
   load_idx(0, now);
   tables_landed();                                             // and the first tile and indices
-  store_a(As0, ra);
-  load_idx(S > 1 ? 1 : 0, next);
-  load_a(S > 1 ? 1 : 0, ra);
-  __syncthreads();
+  load_idx(upto(1), next);
+  if constexpr (!DIRECT) {
+    store_a(As0, ra);
+    load_a(upto(1), ra);
+    __syncthreads();
+  }
   f32x16 acc[MB];
 #pragma unroll
   for (int t = 0; t < MB; ++t)
@@ -892,13 +906,13 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
       for (int t = 0; t < TPH; ++t)
         h[q * TPH + t] = *reinterpret_cast<const uint4 *>(As + (q * RP + 32 * (t0 + t) + c) * LDA + 32 * KS * p + 8 * u);
   };
-  read_a(As0, 0, H0);
+  if constexpr (!DIRECT) read_a(As0, 0, H0);
   auto kstep = [&](int64_t s, const uint4 (&bc)[8], uint4 (&bn)[8]) {
     const uint16_t *Acur = (s & 1) ? As1 : As0;
     uint16_t *Anext = (s & 1) ? As0 : As1;
     uint32_t q1[8], q2[8];
     split(next, q1, q2);                                       // of step s + 1
-    load_idx(s + 2 < S ? s + 2 : S - 1, next);
+    load_idx(upto(s + 2), next);
     auto run = [&](int h, const uint4 (&av)[P * TPH], uint4 (&an)[P * TPH]) {
       if (h + 1 < 4 * KS * HB) read_a(Acur, h + 1, an);
       else read_a(Anext, 0, an);
@@ -934,7 +948,7 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
       run(4, H0, H1);
       gm_interleave<4, 2, 1, 1>();
       __builtin_amdgcn_sched_barrier(0);
-      load_a(s + 2 < S ? s + 2 : S - 1, ra);
+      load_a(upto(s + 2), ra);
       run(5, H1, H0);
       gm_interleave<4, 0, 1, 0, 1>();
       __builtin_amdgcn_sched_barrier(0);
@@ -953,7 +967,7 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
       run(3, H1, H0);
       __builtin_amdgcn_sched_barrier(0);
       store_a(Anext, ra);
-      load_a(s + 2 < S ? s + 2 : S - 1, ra);
+      load_a(upto(s + 2), ra);
       run(4, H0, H1);
       run(5, H1, H0);
       D.template p3<0, 8>(bn);
@@ -969,7 +983,7 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
       run(1, H1, H0);
       __builtin_amdgcn_sched_barrier(0);
       store_a(Anext, ra);
-      load_a(s + 2 < S ? s + 2 : S - 1, ra);
+      load_a(upto(s + 2), ra);
       run(2, H0, H1);
       D.template p3<0, 4>(bn);
 #pragma unroll
@@ -978,12 +992,45 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
       run(3, H1, H0);
     }
   };
+  auto dstep = [&](int64_t s, const uint4 (&bc)[8], uint4 (&bn)[8], const uint4 (&xc)[8], uint4 (&xn)[8]) {
+    uint32_t q1[8], q2[8];
+    split(next, q1, q2);                                       // of step s + 1
+    load_idx(upto(s + 2), next);
+    load_x(upto(s + 1), xn);
+    auto mfma = [&](int u) {
+      acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, xc[u]), __builtin_bit_cast(bf16x8, bc[u]), acc[0],
+                                                       0, 0, 0);
+    };
+    Dec8<BPW, true> D;
+    D.template p1<0, 8>(q1, q2);
+    mfma(0);
+    mfma(1);
+    __builtin_amdgcn_sched_barrier(0);
+    D.template p2<0, 4>(q1, q2);
+    mfma(2);
+    D.template p2<4, 8>(q1, q2);
+    mfma(3);
+    __builtin_amdgcn_sched_barrier(0);
+    mfma(4);
+    mfma(5);
+    D.template p3<0, 8>(bn);
+    mfma(6);
+    mfma(7);
+  };
   int64_t s = 0;
   for (; s + 1 < S; s += 2) {
-    kstep(s, B0, B1);
-    kstep(s + 1, B1, B0);
+    if constexpr (DIRECT) {
+      dstep(s, B0, B1, X0, X1);
+      dstep(s + 1, B1, B0, X1, X0);
+    } else {
+      kstep(s, B0, B1);
+      kstep(s + 1, B1, B0);
+    }
   }
-  if (s < S) kstep(s, B0, B1);
+  if (s < S) {
+    if constexpr (DIRECT) dstep(s, B0, B1, X0, X1);
+    else kstep(s, B0, B1);
+  }
   if (n0 == 0 && tile.part == 0 && lane < 32)
 #pragma unroll
     for (int t = 0; t < MB; ++t)
@@ -1054,7 +1101,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) xp_gemm_k(XpProduct a) {
     if (rows > 128) gemm_tile<BPW, G4, 8, 1>(a, lds, tile, n0);
     else if (rows > 64) gemm_tile<BPW, G4, 4, 1>(a, lds, tile, n0);
     else if (rows > 32) gemm_tile<BPW, G4, 2, 1>(a, lds, tile, n0);
-    else gemm_tile<BPW, G4, 1, 1>(a, lds, tile, n0);
+    else if (rows > kDirectRows) gemm_tile<BPW, G4, 1, 1>(a, lds, tile, n0);
+    else gemm_tile<BPW, G4, 1, 1, true>(a, lds, tile, n0);
   }
 }
 
