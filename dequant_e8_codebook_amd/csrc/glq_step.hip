@@ -5,6 +5,7 @@
 //   kv_plan_k        request lengths -> pages taken, slots, positions, offsets
 //   qk_norm_rope_k   norms of query and key heads, rotation, write into the cache
 //   route_pick_k     router scores -> each token's experts and weights
+//   route_group_k    for very many tokens: counts of groups of workgroups
 //   route_place_k    rows in the experts' order, for more tokens than one workgroup takes
 #include <hip/hip_runtime.h>
 
@@ -87,8 +88,10 @@ struct PlanShared {
 // and positions, all cached tokens' slots, the pages taken. It sums up the requests'
 // counts itself (1024 requests at a time), which costs less than a launch that would do it for all; an
 // entry finds its request by bisection in LDS. A page taken in this call is read from the list of free pages,
-// never from the table, so no workgroup waits for another. A short tile has one entry a thread; in a full one a
-// thread has 8 neighbouring entries, found by one bisection and a few steps, their pages asked for together.
+// never from the table, so no workgroup waits for another. In a tile of up to 1024 entries threads take one at a time; in a fuller one a
+// thread has 8 neighbouring entries, found by one bisection and a few steps, their pages asked for together (300 and 1024
+// requests with one new token 4.3 and 6.1 us one at a time, 6.2 and 6.6 by eights; 32 requests of 4096 new tokens in all
+// and 64 of 16384, all read back, 8.4 and 9.8 against 5.7 and 6.0).
 // Bound by latency: launch, lengths, sums and bisection, pages, 4 us in all.
 // Returns the number of entries that the list has in all (the tokens lists: counted as far as the tile).
 template <PlanList LIST>
@@ -216,7 +219,7 @@ __device__ __forceinline__ int32_t plan_tile(const PlanArgs &a, PlanShared &sh, 
             }
       }
     };
-    if (LIST == kPages || end - from <= kPlanThreads) {
+    if (LIST == kPages || end - from <= 4 * kPlanThreads) {
       for (int32_t i = from + tid; i < end; i += kPlanThreads) entry(std::integral_constant<int, 1>(), i);
     } else {
       entry(std::integral_constant<int, kPlanEach>(), t0 + kPlanEach * tid);
@@ -386,15 +389,27 @@ __global__ void __launch_bounds__(256) qk_norm_rope_k(NormArgs a) {
 
 struct RouteArgs {
   const void *logits;
-  int64_t tokens, blocks;
-  int32_t experts, top;
+  int64_t tokens, blocks, groups;                  // groups of blocks that counts are summed up for, 0: none
+  int32_t experts, top, each;                      // tokens a block
   int32_t normalize;
   float *weights;
-  int32_t *ids, *pos, *src, *offsets, *counts;     // counts [blocks][experts], workspace
+  int32_t *ids, *pos, *src, *offsets, *counts;     // counts [blocks][experts], then [groups][experts], workspace
 };
 
-// tokens a workgroup: 64 where one takes them all, else 32 (8192 tokens of 128 experts: a workgroup for every CU)
-constexpr int kRouteAlone = 64, kRouteTokens = 32, kRouteThreads = 1024, kRouteMost = 1024;
+// Tokens a workgroup: one workgroup takes up to 64. Beyond, few tokens each make the choice short and more counts to add up: 128
+// experts, 8 of them, choice and rows for 16, 32 and 64 tokens each: 500 tokens 9.3, 11.1 and 17.5 us, 2048: 9.6, 11.7 and 17.5,
+// 8192: 18.9, 14.1 and 17.8, 32768: 137, 54 and 34. Adding up all counts in each workgroup grows with the square of
+// the tokens, so past 512 workgroups of 64 tokens groups of 256 of them are added up first, in a launch between.
+constexpr int kRouteAlone = 64, kRouteThreads = 1024, kRouteMost = 1024, kRouteGroup = 256;
+constexpr int64_t kRouteShort = 2048, kRouteMiddle = 16384, kRoutePlain = 512;
+inline int route_each(int64_t tokens) { return tokens <= kRouteAlone ? 64 : tokens <= kRouteShort ? 16 : tokens <= kRouteMiddle ? 32 : 64; }
+inline int64_t route_blocks(int64_t tokens) {
+  const int each = route_each(tokens);
+  return tokens < each ? 1 : (tokens + each - 1) / each;
+}
+inline int64_t route_groups(int64_t tokens) {
+  return route_blocks(tokens) <= kRoutePlain ? 0 : (route_blocks(tokens) + kRouteGroup - 1) / kRouteGroup;
+}
 
 // Order of scores as unsigned numbers, 0 for those that choose nothing (-inf, NaN); both zeros are one.
 __device__ __forceinline__ uint32_t score_order(float x) {
@@ -530,8 +545,38 @@ __global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
     for (int64_t r = total + tid; r < a.tokens * a.top; r += kRouteThreads) a.src[r] = -1;
 }
 
+// Counts of kRouteGroup workgroups: their sum, and in place of each the sum of those before it in the group. The threads
+// of an expert take a run of workgroups each, twice over.
+__global__ void __launch_bounds__(kRouteThreads) route_group_k(RouteArgs a) {
+  __shared__ int32_t sums[kRouteThreads];
+  const int tid = threadIdx.x;
+  int width = 1;                                               // experts up to a power of two
+  while (width < a.experts) width <<= 1;
+  const int parts = kRouteThreads / width, e = tid & (width - 1), part = tid / width;
+  const int64_t first = (int64_t)blockIdx.x * kRouteGroup, left = a.blocks - first, n = left < kRouteGroup ? left : kRouteGroup;
+  const int64_t b0 = first + n * part / parts, b1 = first + n * (part + 1) / parts;
+  int32_t sum = 0;
+  if (e < a.experts)
+    for (int64_t b = b0; b < b1; ++b) sum += a.counts[b * a.experts + e];
+  sums[tid] = sum;
+  __syncthreads();
+  if (e >= a.experts) return;
+  int32_t before = 0, all = 0;
+  for (int p = 0; p < parts; ++p) {
+    const int32_t s = sums[e + p * width];
+    all += s;
+    if (p < part) before += s;
+  }
+  for (int64_t b = b0; b < b1; ++b) {
+    const int32_t c = a.counts[b * a.experts + e];
+    a.counts[b * a.experts + e] = before;
+    before += c;
+  }
+  if (part == 0) a.counts[(a.blocks + blockIdx.x) * a.experts + e] = all;
+}
+
 // Rows of one workgroup's tokens: those of earlier workgroups and of earlier experts come
-// before. Every workgroup adds up all counts (256 by 128 of them for 8192 tokens and
+// before. Every workgroup adds up all counts, or those of the groups (256 by 128 of them for 8192 tokens and
 // 128 experts, from L2), instead of a launch between the two that would.
 __global__ void __launch_bounds__(kRouteThreads) route_place_k(RouteArgs a) {
   __shared__ int32_t sums[2][kRouteThreads];                   // before this workgroup's, and all
@@ -540,24 +585,27 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_k(RouteArgs a) {
   int width = 1;                                               // experts up to a power of two
   while (width < a.experts) width <<= 1;
   const int parts = kRouteThreads / width, e = tid & (width - 1), part = tid / width;
+  const int32_t *counts = a.groups ? a.counts + a.blocks * a.experts : a.counts;
+  const int64_t many = a.groups ? a.groups : a.blocks, mine = a.groups ? blockIdx.x / kRouteGroup : blockIdx.x;
   int32_t before = 0, all = 0;
   if (e < a.experts) {
     int64_t b = part;
-    for (; b + 7 * parts < a.blocks; b += 8 * parts) {         // eight loads in flight
+    for (; b + 7 * parts < many; b += 8 * parts) {             // eight loads in flight
       int32_t n[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n[i] = a.counts[(b + i * parts) * a.experts + e];
+      for (int i = 0; i < 8; ++i) n[i] = counts[(b + i * parts) * a.experts + e];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         all += n[i];
-        if (b + i * parts < (int64_t)blockIdx.x) before += n[i];
+        if (b + i * parts < mine) before += n[i];
       }
     }
-    for (; b < a.blocks; b += parts) {
-      const int32_t n = a.counts[b * a.experts + e];
+    for (; b < many; b += parts) {
+      const int32_t n = counts[b * a.experts + e];
       all += n;
-      if (b < (int64_t)blockIdx.x) before += n;
+      if (b < mine) before += n;
     }
+    if (a.groups && part == 0) before += a.counts[(int64_t)blockIdx.x * a.experts + e];      // of the group, before this one
   }
   sums[0][tid] = before, sums[1][tid] = all;
   __syncthreads();
@@ -575,8 +623,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_k(RouteArgs a) {
   }
   if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = total;
   __syncthreads();
-  const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens;
-  const int64_t n = (a.tokens - t0 < kRouteTokens ? a.tokens - t0 : kRouteTokens) * a.top;
+  const int64_t t0 = (int64_t)blockIdx.x * a.each;
+  const int64_t n = (a.tokens - t0 < a.each ? a.tokens - t0 : a.each) * a.top;
   for (int64_t i = tid; i < n; i += kRouteThreads) {
     const int64_t o = t0 * a.top + i;
     const int32_t id = a.ids[o];
@@ -606,10 +654,13 @@ int launch_norm_heads(NormArgs a, int64_t tokens, hipStream_t st) {
 
 template <int FMT, int D, bool F32>
 int launch_norm(const NormArgs &a, int64_t tokens, bool pairs, hipStream_t st) {
-  // four heads a row of lanes where that leaves every CU eight waves
-  constexpr int HB = 4;
+  // Several heads a row of lanes where four would leave every CU eight waves; two where rows become codes, whose maxima take
+  // registers. 32 on 8 heads of 128 in bf16, one, two and four heads: 8192 tokens without a cache 49.5, 41.9 and 39.1 us, into
+  // a bf16 cache 54.1, 46.0 and 43.7, into an int8 one 56.7, 45.3 and 49.4; 512 tokens 5.4, 5.4, 5.8, and 5.8, 5.8, 6.2, and
+  // 6.1, 6.8, 8.0; 1024 tokens 8.8, 8.5, 8.4, and 9.8, 9.0, 9.3, and 11.1, 10.6, 10.9.
+  constexpr int HB = FMT == GLQ_KV_INT8 || FMT == GLQ_KV_INT4 ? 2 : 4;
   const int64_t heads = a.q_heads + (FMT == kNoCache ? 1 : 2) * a.io.heads;
-  if (tokens * heads * (D / 8) >= (int64_t)256 * 8 * 64 * HB)
+  if (tokens * heads * (D / 8) >= (int64_t)256 * 8 * 64 * 4)
     return pairs ? launch_norm_heads<FMT, D, F32, true, HB>(a, tokens, st) : launch_norm_heads<FMT, D, F32, false, HB>(a, tokens, st);
   return pairs ? launch_norm_heads<FMT, D, F32, true, 1>(a, tokens, st) : launch_norm_heads<FMT, D, F32, false, 1>(a, tokens, st);
 }
@@ -629,12 +680,12 @@ int check_route(int64_t tokens, int32_t experts, int32_t top) {
   return GLQ_OK;
 }
 
-int64_t route_blocks(int64_t tokens) { return tokens <= kRouteAlone ? 1 : (tokens + kRouteTokens - 1) / kRouteTokens; }
-
 template <int NV, bool F32>
 void launch_pick_tokens(const RouteArgs &a, hipStream_t st) {
-  if (a.blocks == 1) hipLaunchKernelGGL((route_pick_k<NV, F32, kRouteAlone>), dim3(1), dim3(kRouteThreads), 0, st, a);
-  else hipLaunchKernelGGL((route_pick_k<NV, F32, kRouteTokens>), dim3((unsigned)a.blocks), dim3(kRouteThreads), 0, st, a);
+  const dim3 grid((unsigned)a.blocks), block(kRouteThreads);
+  if (a.each == 64) hipLaunchKernelGGL((route_pick_k<NV, F32, 64>), grid, block, 0, st, a);
+  else if (a.each == 32) hipLaunchKernelGGL((route_pick_k<NV, F32, 32>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((route_pick_k<NV, F32, 16>), grid, block, 0, st, a);
 }
 
 template <int NV>
@@ -727,8 +778,13 @@ extern "C" int glq_qk_norm_rope(const glq_qk *N, const glq_kv_cache *C, uint32_t
 
 extern "C" size_t glq_route_workspace(int64_t tokens, int32_t experts, int32_t top_k) {
   if (check_route(tokens, experts, top_k)) return 0;
-  // (one workgroup needs none; a size of 0 says that the call would be refused)
-  return 256 + (route_blocks(tokens) > 1 ? (size_t)route_blocks(tokens) * experts * 4 : 0);
+  // (one workgroup needs none; a size of 0 says that the call would be refused; fewer tokens can have more workgroups)
+  int64_t most = 0;
+  for (const int64_t t : {tokens, tokens < kRouteShort ? tokens : kRouteShort, tokens < kRouteMiddle ? tokens : kRouteMiddle}) {
+    const int64_t need = route_blocks(t) > 1 ? route_blocks(t) + route_groups(t) : 0;
+    most = need > most ? need : most;
+  }
+  return 256 + (size_t)most * experts * 4;
 }
 
 extern "C" int glq_route(const void *logits, glq_dtype dt, int64_t tokens, int32_t experts, int32_t top_k, uint32_t flags,
@@ -743,8 +799,8 @@ extern "C" int glq_route(const void *logits, glq_dtype dt, int64_t tokens, int32
     return GLQ_ERR_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || ws_bytes < glq_route_workspace(tokens, experts, top_k))
     return GLQ_ERR_WORKSPACE;
-  RouteArgs a = {logits, tokens, route_blocks(tokens), experts, top_k, (flags & GLQ_ROUTE_NORMALIZE) ? 1 : 0,
-                 weights, ids, pos, src, offsets, reinterpret_cast<int32_t *>(workspace)};
+  RouteArgs a = {logits, tokens, route_blocks(tokens), route_groups(tokens), experts, top_k, route_each(tokens),
+                 (flags & GLQ_ROUTE_NORMALIZE) ? 1 : 0, weights, ids, pos, src, offsets, reinterpret_cast<int32_t *>(workspace)};
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   if (experts <= 64) launch_pick<1>(a, dt, st);
   else if (experts <= 128) launch_pick<2>(a, dt, st);
@@ -753,6 +809,11 @@ extern "C" int glq_route(const void *logits, glq_dtype dt, int64_t tokens, int32
   else launch_pick<16>(a, dt, st);
   int rc2 = hip_status(hipGetLastError(), "route_pick_k");
   if (rc2 || a.blocks == 1) return rc2;
+  if (a.groups) {
+    hipLaunchKernelGGL(route_group_k, dim3((unsigned)a.groups), dim3(kRouteThreads), 0, st, a);
+    const int rc3 = hip_status(hipGetLastError(), "route_group_k");
+    if (rc3) return rc3;
+  }
   hipLaunchKernelGGL(route_place_k, dim3((unsigned)a.blocks), dim3(kRouteThreads), 0, st, a);
   return hip_status(hipGetLastError(), "route_place_k");
 }

@@ -602,7 +602,7 @@ enum { GLQ_ROUTE_NORMALIZE = 1u };
  *             need not be cleared; concurrent calls need workspaces of their own
  * No result depends on the order in which workgroups run. 1 <= top_k <= experts.
  * GLQ_ERR_UNSUPPORTED for more than 1024 experts, top_k above 64 and 2^25 tokens or more. Up to 64 tokens
- * take one launch, more take two.
+ * take one launch, more take two, more than 32768 three.
  */
 size_t glq_route_workspace(int64_t tokens, int32_t experts, int32_t top_k);
 int glq_route(const void *logits, glq_dtype dt, int64_t tokens, int32_t experts, int32_t top_k, uint32_t flags,

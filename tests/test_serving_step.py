@@ -307,6 +307,67 @@ def test_route_workspace_and_sizes(gen):
         _check_route(logits.cpu(), top, True, [t.cpu() for t in (w[:tokens], ids[:tokens], pos[:tokens], src[:-1], offsets[:-1])])
 
 
+def _route_many(gen, tokens, experts, top):
+    logits = torch.randn(tokens, experts, generator=gen)
+    if tokens > 1000:
+        logits[tokens // 2:tokens // 2 + 300] = -torch.inf       # a padded batch's rows in the middle
+    size = glq.route_workspace_bytes(tokens, experts, top)
+    ws = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    w = torch.empty(tokens, top, device="cuda")
+    ids, pos = (torch.empty(tokens, top, dtype=torch.int32, device="cuda") for _ in range(2))
+    src, offsets = torch.empty(tokens * top, dtype=torch.int32, device="cuda"), _ints([0] * (experts + 1))
+    glq.route(logits.cuda(), top, w, ids, pos, src, offsets, ws[:size])
+    assert (ws[size:] == 0xA5).all()
+    score, expert = torch.sort(logits.double(), descending=True, stable=True)
+    score, expert = score[:, :top], expert[:, :top]
+    real = score > -torch.inf
+    assert torch.equal(ids.cpu().long(), torch.where(real, expert, -1))
+    flat = torch.where(real, expert, experts).flatten()
+    order, rows = torch.argsort(flat, stable=True), int(real.sum())
+    place = torch.empty_like(order)
+    place[order] = torch.arange(len(order))
+    assert torch.equal(pos.cpu().long().flatten(), torch.where(real.flatten(), place, -1))
+    assert torch.equal(src.cpu().long()[:rows], order[:rows] // top) and (src[rows:] == -1).all()
+    assert torch.equal(offsets.cpu().long()[1:], torch.bincount(flat, minlength=experts + 1)[:experts].cumsum(0)) and offsets[0] == 0
+    want = torch.where(real, torch.softmax(score.where(real, -1e300), 1), 0.0)
+    reach = (score[:, :1] - score[:, -1:]).nan_to_num(0.0)
+    assert ((w.double().cpu() - want).abs() <= (2 * (reach + 2) + 25) * 2.0 ** -24 * want + 2.0 ** -126).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,experts,top", [(2048, 24, 3), (2049, 24, 3), (16384, 16, 2), (16385, 16, 2), (32768, 8, 2),
+                                                (32769, 8, 2), (100000, 60, 4), (70000, 300, 2), (300001, 8, 1), (40000, 1024, 3)])
+def test_route_of_many_tokens(gen, tokens, experts, top):
+    """Each number of tokens a workgroup takes, at its ends, and counts added up by groups."""
+    _route_many(gen, tokens, experts, top)
+
+
+def test_route_workspace_grows():
+    for experts in (1, 60, 1024):
+        sizes = [glq.route_workspace_bytes(t, experts, 1) for t in (1, 64, 65, 1000, 2048, 2049, 5000, 16384, 16385, 32768, 32769, 10 ** 6)]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("bpw", [2, 3, 4])
+@pytest.mark.parametrize("n,k", [(264, 4096), (40, 4104), (520, 1088)])
+def test_few_rows_an_expert(cb, dtype, bpw, n, k):
+    """Tiles of one to five rows, along k in parts and whole, indices in fours and one by one."""
+    experts = Set(7, n, k, bpw, seed=8)
+    handle = experts.device(cb)
+    for counts in ([1, 0, 0, 0, 0, 0, 0], [1, 4, 5, 0, 2, 3, 1]):
+        ends = np.concatenate(([0], np.cumsum(counts)))
+        rows = int(ends[-1])
+        x = torch.randn(rows, k, generator=torch.Generator().manual_seed(n)).to(DTYPES[dtype]).cuda()
+        y = torch.full((rows + 1, n), 7.0, dtype=x.dtype, device="cuda")
+        ws = torch.full((glq.expert_linear_workspace_bytes(handle, rows),), 255, dtype=torch.uint8, device="cuda")
+        glq.expert_linear(handle, x, y[:rows], _ints(ends.tolist()), ws)
+        ref = _rows_reference(experts, x.double().cpu().numpy(), ends, None, rows)
+        assert (y[rows] == 7).all()
+        _held(y[:rows], ref, _tolerance(ref, dtype, k), dtype)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("k", [5120, 7168, 6144])
 def test_rows_of_several_blocks_and_sizes(cb, k):
