@@ -3,11 +3,17 @@
 //
 // With the rows in the experts' order, row r of expert e: y_r = U_e^T (s_e W^_e) (V_e x_r),
 // a layer as in glq_kernels.hip for each expert, all of them in three launches:
-//   xp_in_k     x~_r = V_e x_r, rows gathered from their tokens
-//   xp_rows_k   z_r = s_e W^_e x~_r, the weights rebuilt inside the product
-//   xp_out_k    y_r = U_e^T z_r, or a token's weighted sum of them
-// How many rows an expert has is known on the device only: launches are sized by
-// the most there can be, and a workgroup without rows ends at once.
+//   xp_in_k, xp_in_blk_k     x~_r = V_e x_r, rows gathered from their tokens
+//   xp_gemm_k                z_r = W^_e x~_r, the weights rebuilt inside the product
+//   xp_out_k, xp_out_blk_k   y_r = U_e^T (s_e z_r), or a token's weighted sum of them
+// (_blk_k: rows of whole blocks of 1024 to 16384 elements; the others any multiple of 8). How many rows an expert has
+// is known on the device only: launches are sized by the most there can be, and a workgroup without rows ends at once.
+//
+// What bounds them (times of the kernels on their own): 8192 rows, 1024 an expert, of 4096 through 4096 x 4096 at 2 bits: input
+// transform 44 us (3.0 TB/s of rows read and x~ written; VALU 54% busy), product 250 us (1.10 PFLOP/s; the bf16 product of one
+// layer of that size reaches the same), output transform 34.5 us (3.9 TB/s). Few rows: 64 experts of 1024 x 2048 at 2 bits,
+// 24 rows each: 8, 22.5 (1.5 TB/s of indices; the table lookups' passes through the LDS unit) and 4.8 us, of which about 4 each are the
+// launch, the chain of dependent loads (offsets, rows, data) and in the product the copy of the tables.
 #include <hip/hip_runtime.h>
 
 #include <atomic>
@@ -301,7 +307,8 @@ __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
 // part is that of the single layers' block kernel (registers, one multiply-add a DPP lane stage, lane swaps that keep their
 // layout); the waves of a block then exchange all their values through LDS, four at a time, each summing up its own
 // signs of them: no transpose back, two barriers a row. Workgroups take runs of rows, whose next
-// one is in flight while one is transformed. 8192 rows of 4096 through two of eight experts: in 67 -> see launch_transform.
+// one is in flight while one is transformed. 8192 rows of 4096: in 44 us, out 34.5, and 67 and 52 by the general kernels
+// above; one token's two rows 4.6 and 5.8 us.
 
 constexpr int kRowWaves = 16;                        // most waves a row
 
@@ -504,8 +511,8 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
 
 // Items are rows of z: the rows themselves, or each token's choices. A wave's lanes look up 64 items at a time (row, expert,
 // factor), so the chain of loads behind a choice is gone through once for them all. With few tokens a workgroup has several sets
-// of waves (GROUPS of them, blockDim over the row's waves): set s takes choices s, s + GROUPS, ... and the sets' sums
-// meet in LDS.
+// of waves (blockDim over the row's waves): set s takes choices s, s + sets, ... and the sets' sums meet in LDS, always in
+// the same order.
 template <int NW, bool F32, bool Z16>
 __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
   extern __shared__ __attribute__((aligned(16))) float4 cross[];
@@ -757,7 +764,8 @@ struct XpTiles {
   }
 };
 
-// Tiles of so few rows read x~ from memory straight into operands (see gemm_tile): product of 16 experts of 4096 x 4096 with 4 rows each, at
+// Tiles of so few rows read x~ from memory straight into operands, which takes that load off the LDS unit and costs the vector
+// memory path 2 lines a row and load: product of 16 experts of 4096 x 4096 with 4 rows each, at
 // 4 bits 57.0 us through LDS, 49.7 so, at 3 bits 50.0 and 46.0; 64 experts of 1024 x 2048 at 2 bits with 1, 4, 8 and 24 rows
 // 21.6, 21.2, 22.2 and 22.3 against 19.8, 21.6, 24.4 and 34.
 constexpr int kDirectRows = 4;
@@ -769,9 +777,14 @@ constexpr size_t gemm_lds(size_t tables, bool f32) { return tables + 2 * sizeof(
 // One tile's loop over k and its end, for 32 MB rows or fewer (row0 .. row1 - 1) and P parts of x~.
 //
 // A wave owns 32 weight rows for all rows of the tile: MFMA 32x32x16 with x~ from LDS (double-buffered, one
-// barrier a step of 64 inputs) and its weights rebuilt straight into the other operand a step ahead,
+// barrier a step) and its weights rebuilt straight into the other operand a step ahead,
 // so each weight is rebuilt once a workgroup. The step's MFMAs come in runs; the walk of the
 // next step's indices (records, halves, combination) and the tile's loads and writes are spread over them.
+// A step is 64 inputs, or 128 where the tile has few rows: lane half p then has the groups 8 p .. 8 p + 7 of 8 inputs, 16 bytes
+// of indices in one load. Few rows are bound by the LDS unit: of 226 passes a wave and step at 2 bits 162 are the lookups (random banks) and
+// 64 the operands of x~ (64 experts of 1024 x 2048, 24 rows: 22.4 us, in steps of 64 23.7). What did not help there: indices asked for four
+// steps ahead, records looked up a step ahead (24.7), lanes of rows that are not there masked out of the reads (24.2), 16 waves.
+// DIRECT: x~ of the few rows from memory straight into operands, asked for a step ahead; no tiles, no barrier.
 template <int BPW, bool G4, int MB, int P, bool DIRECT = false>
 __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, const XpTile &tile, int64_t n0) {
   const int tid = threadIdx.x;
@@ -1151,12 +1164,14 @@ int launch_transform_k(const XpRows &a, int64_t groups, hipStream_t st) {
 template <int NW, bool OUT, bool F32, bool Z16>
 int launch_blocks_k(const XpRows &a, int64_t most, hipStream_t st) {
   const int waves = (int)((OUT ? a.n : a.k) / 1024);
-  // the output's sets of waves: as many as choices and a workgroup take, where there are fewer tokens than CUs
+  // the output's sets of waves: as many as choices and a workgroup take, where there are no more tokens than CUs (32 tokens of 8
+  // choices, rows of 2048: 5.3 us, by one set 8.7; one token of two, rows of 4096: 7.1 and 10.3)
   int sets = 1;
   if (OUT && most <= kCus)
     while (2 * sets * waves <= kRowWaves && sets < a.top) sets *= 2;
   const size_t shm = NW > 1 || sets > 1 ? (size_t)waves * sets * 4096 : 0;
-  // no more workgroups than run at once, by the registers of the kernels: waves a SIMD
+  // no more workgroups than run at once, by the registers of the kernels (waves a SIMD): more would leave some CUs a second
+  // run of rows. NW = 4, 2048 and 8192 rows: in 14.5 and 44 us, with 6 waves a SIMD 16.7 and 49; out 11.1 and 34.5, and 12.7 and 36
   constexpr int resident = 4 * (OUT ? 4 : NW == 1 ? 8 : NW == 2 ? 6 : 5);
   const int per = resident / (waves * sets);
   const int64_t once = (int64_t)kCus * (per > 1 ? per : 1), groups = most < once ? most : once;
@@ -1234,7 +1249,8 @@ int check_experts(const glq_experts *E) {
 }
 
 // Parts along k of the units that are split (XpTiles): as many as give each CU one, for the most tiles there can be, but none under
-// 4 steps, which would not pay for the transforms' reading more planes.
+// 4 steps, which would not pay for the transforms' reading more planes. 2 of 8 experts of 4096 x 4096 at 4 bits, a row each, 32
+// tiles: product 16 us in 8 parts, 32 in 2.
 int xp_parts(int64_t count, int64_t n, int64_t k, int64_t rows, bool f32) {
   const int64_t steps = up128(k) / kGemmK, most = (rows / (f32 ? 64 : 256) + (count < rows ? count : rows)) * ((n + 255) / 256);
   if (steps > kSplitSteps || steps < 8) return 1;

@@ -92,7 +92,8 @@ struct PlanShared {
 // thread has 8 neighbouring entries, found by one bisection and a few steps, their pages asked for together (300 and 1024
 // requests with one new token 4.3 and 6.1 us one at a time, 6.2 and 6.6 by eights; 32 requests of 4096 new tokens in all
 // and 64 of 16384, all read back, 8.4 and 9.8 against 5.7 and 6.0).
-// Bound by latency: launch, lengths, sums and bisection, pages, 4 us in all.
+// Bound by latency: launch, lengths, sums and bisection, pages: 3.2 us for 32 requests with one new token, 6.0 for 64 with 16384
+// new tokens and all of 145,000 read back.
 // Returns the number of entries that the list has in all (the tokens lists: counted as far as the tile).
 template <PlanList LIST>
 __device__ __forceinline__ int32_t plan_tile(const PlanArgs &a, PlanShared &sh, int64_t tile, bool first) {
@@ -276,7 +277,8 @@ constexpr int kNoCache = -1;
 // in the lane rot / 16 further, that of a pair rotation in the same lane. Values are float32
 // until the one rounding to the operands' type; the cache gets the rounded key, as
 // if it were appended afterwards. The lanes of a row take HB heads of one kind (queries, keys or values) of a token, whose
-// loads are in flight together and share the angles and the weights.
+// loads are in flight together and share the angles and the weights. Bound by what it reads and writes: 8192 tokens, 32 on 8 heads
+// of 128 in bf16 with the write into a bf16 cache 43.7 us, 4.8 TB/s; 32 tokens 3.9 us, launch and two loads one after the other.
 template <int FMT, int D, bool F32, bool PAIRS, int HB>
 __global__ void __launch_bounds__(256) qk_norm_rope_k(NormArgs a) {
   constexpr int LPR = D / 8, ES = F32 ? 4 : 2;
@@ -440,7 +442,8 @@ __device__ __forceinline__ int32_t group_before(int32_t x, int32_t *sum) {
 // expert is a mask of 64 bits in LDS (or-ed in any order, the same whatever it is), so
 // a choice's place among the workgroup's is the number of lower bits, and nothing
 // depends on which wave comes first. One workgroup alone (up to 64 tokens) goes on
-// to the rows itself: one launch.
+// to the rows itself: one launch. Bound by the chain of `top` maxima over the wave, each of lane exchanges and a ballot: 4.6 us for a token a
+// wave with 8 of 128 experts, of which the launch and the scores are 2.5; 10^6 tokens 457 us, 1.3 TB/s of scores and choices.
 template <int NV, bool F32, int TOKENS>
 __global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
   __shared__ unsigned long long chose[kRouteMost];
