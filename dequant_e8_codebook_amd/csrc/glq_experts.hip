@@ -895,8 +895,8 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   if constexpr (!DIRECT) {
     store_a(As0, ra);
     load_a(upto(1), ra);
-    __syncthreads();
   }
+  __syncthreads();                                             // of all waves
   f32x16 acc[MB];
 #pragma unroll
   for (int t = 0; t < MB; ++t)

@@ -366,6 +366,11 @@ def test_few_rows_an_expert(cb, dtype, bpw, n, k):
         ref = _rows_reference(experts, x.double().cpu().numpy(), ends, None, rows)
         assert (y[rows] == 7).all()
         _held(y[:rows], ref, _tolerance(ref, dtype, k), dtype)
+        for _ in range(25):                                      # the same bits each time, whatever the workspace held
+            again = torch.full_like(y, 7.0)
+            ws.fill_(255)
+            glq.expert_linear(handle, x, again[:rows], _ints(ends.tolist()), ws)
+            assert torch.equal(y, again)
 
 
 @pytest.mark.gpu
