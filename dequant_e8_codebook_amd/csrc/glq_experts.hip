@@ -671,7 +671,7 @@ struct XpProduct {
   int32_t count, rows;
   uint32_t n_groups;           // of 256 weight rows
   uint32_t likely;             // workgroups that very likely have a tile
-  int32_t ks;                  // parts along k of the rows that are split
+  int32_t ks;                  // parts along k, at most, of the rows that are split
 };
 
 // biased operands (bf16 of 192 + u) to bf16 of u, exact
@@ -688,15 +688,15 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 struct XpTile { int e; int32_t row0, row1; uint32_t group; int part, parts; };
 
 // The launch's tiles, numbered. Units are groups of tm rows of an expert, whole ones first, then the experts'
-// remainders, which are shorter. As many whole units as make full rounds on the card come first, unsplit. Where what is left
-// would fill only up to half of a last round, its units are split along k: their parts' z lie in planes of their own that the
-// output's transform adds up, so no part waits for another (4096 tokens, 2 of 8 experts of 4096 x 4096, 576 tiles: 425 -> 400 us
-// whole). Numbers 8 i + x are for XCD x, in runs of neighbouring tiles (the weight rows of one unit).
+// remainders, which are shorter. Where the last round on the card has few enough tiles, its units are split along k, into as many of up
+// to ks parts as find a CU each: their parts' z lie in planes of their own that the output's transform adds up, so no part
+// waits for another (see xp_parts for figures). Numbers 8 i + x are for XCD x, in runs of neighbouring tiles (the
+// weight rows of one unit).
 struct XpTiles {
   const XpProduct &a;
   const int tm, lane;
   int32_t lo, have;                                  // rows of expert `lane`: begin, number
-  uint32_t whole, rest, lead, first, blocks, all;
+  uint32_t whole, rest, lead, first, parts, blocks, all;
 
   __device__ __forceinline__ void rows_of(int x, int32_t &l, int32_t &n) const {
     l = x < a.count ? bounded(a.offsets[x], a.rows) : 0;
@@ -713,12 +713,12 @@ struct XpTiles {
       rest += __popcll(__ballot(n % tm != 0));
     }
     lead = whole + rest;                             // units that are not split
-    if (a.ks > 1) {
-      const uint32_t last = (whole + rest) * a.n_groups % kCus;
-      if (last > 0 && last <= kCus / 2) lead = whole * a.n_groups / kCus * kCus / a.n_groups;
-    }
+    parts = 1;
+    const uint32_t tail = (lead * a.n_groups % kCus + a.n_groups - 1) / a.n_groups;      // those of the last round
+    while (2 * parts <= (uint32_t)a.ks && 2 * parts * tail * a.n_groups <= kCus) parts *= 2;
+    if (parts > 1) lead -= tail;
     first = lead * a.n_groups, blocks = (first + 7) / 8 * 8;
-    all = blocks + ((whole + rest - lead) * a.n_groups * a.ks + 7) / 8 * 8;
+    all = blocks + ((whole + rest - lead) * a.n_groups * parts + 7) / 8 * 8;
   }
   // tile b < all; false where the runs leave a gap
   __device__ __forceinline__ bool find(uint32_t b, XpTile &tile) const {
@@ -733,12 +733,12 @@ struct XpTiles {
       if (t >= first) return false;
       u = t / a.n_groups, tile.group = t % a.n_groups;
     } else {
-      const uint32_t n = (whole + rest - lead) * a.n_groups * a.ks, t = spread(b - blocks, n);
+      const uint32_t n = (whole + rest - lead) * a.n_groups * parts, t = spread(b - blocks, n);
       if (t >= n) return false;
-      u = t / (a.n_groups * a.ks);
-      const uint32_t in = t - u * a.n_groups * a.ks;
+      u = t / (a.n_groups * parts);
+      const uint32_t in = t - u * a.n_groups * parts;
       u += lead;
-      tile.part = (int)(in / a.n_groups), tile.parts = a.ks, tile.group = in % a.n_groups;
+      tile.part = (int)(in / a.n_groups), tile.parts = (int)parts, tile.group = in % a.n_groups;
     }
     const bool is_rest = u >= whole;
     if (is_rest) u -= whole;
@@ -886,8 +886,12 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   else load_a(0, ra);
   float row_sum = 0.0f;                                        // thread t: of row row0 + t
   if constexpr (!F32 && BPW > 2)
-    if (tid < 256 && tid < row1 - row0)
-      row_sum = a.rowsum[(tile.parts > 1 ? 1 + tile.part : 0) * (int64_t)a.rows + row0 + tid];
+    if (tid < 256 && tid < row1 - row0) {
+      const float *sums = a.rowsum + row0 + tid;
+      if (tile.parts == 1) row_sum = sums[0];
+      else                                                     // (there are ks sums, some for each part)
+        for (int i = a.ks / tile.parts, at = 1 + tile.part * i; i > 0; --i, ++at) row_sum += sums[at * (int64_t)a.rows];
+    }
   Indices now, next;
   load_idx(0, now);
   tables_landed();                                             // and the first tile and indices
@@ -1216,8 +1220,10 @@ template <int BPW, bool G4, bool F32>
 int launch_gemm(XpProduct a, hipStream_t st) {
   constexpr int TM = F32 ? 64 : 256;
   a.n_groups = (uint32_t)((a.n + 255) / 256);
-  // no more tiles than this, whatever the offsets are, and up to 7 numbers to fill the XCDs' runs of each kind
-  const int64_t most = (a.rows / TM + (a.count < a.rows ? a.count : a.rows)) * a.n_groups * a.ks + 16;
+  // no more tiles than this, whatever the offsets are, parts of no more than fill the card, and up to 7 numbers to fill the XCDs'
+  // runs of each kind
+  const int64_t tiles = (a.rows / TM + (a.count < a.rows ? a.count : a.rows)) * a.n_groups, more = tiles * (a.ks - 1);
+  const int64_t most = tiles + (more < kCus ? more : kCus) + 16;
   constexpr size_t shm = gemm_lds(lds_table_bytes<BPW>(), F32);
   static_assert(shm <= 160 * 1024, "LDS of a CU");
   const int rc = allow_lds<xp_gemm_k<BPW, G4, F32>>(shm);
@@ -1248,19 +1254,19 @@ int check_experts(const glq_experts *E) {
   return GLQ_OK;
 }
 
-// Parts along k of the units that are split (XpTiles): as many as give each CU one, for the most tiles there can be, but none under
-// 4 steps, which would not pay for the transforms' reading more planes. 2 of 8 experts of 4096 x 4096 at 4 bits, a row each, 32
-// tiles: product 16 us in 8 parts, 32 in 2.
+// Most parts along k of the units that are split (XpTiles): two planes of float32 z and four of float16 always have room (z_bytes), four or
+// eight as many as give each CU one for the most tiles there can be; none under 4 steps, which would not pay for the
+// transforms' reading more planes.
 int xp_parts(int64_t count, int64_t n, int64_t k, int64_t rows, bool f32) {
   const int64_t steps = up128(k) / kGemmK, most = (rows / (f32 ? 64 : 256) + (count < rows ? count : rows)) * ((n + 255) / 256);
   if (steps > kSplitSteps || steps < 8) return 1;
-  int ks = 2;
+  int ks = f32 || steps < 16 ? 2 : 4;
   while (ks < 8 && most * 2 * ks <= kCus && steps / (2 * ks) >= 4) ks *= 2;
   return ks;
 }
 
-// Bytes of z's planes for up to this many rows: two of either type, or four or eight where the rule above can ask for
-// them, most tiles * parts <= 256 (so rows < tm (256 / (parts groups) + 1)).
+// Bytes of z's planes for up to this many rows: two of float32, which are four of float16, or four or eight of either where the rule
+// above can ask for them, most tiles * parts <= 256 (so rows < tm (256 / (parts groups) + 1)).
 int64_t z_bytes(int64_t n, int64_t rows) {
   const int64_t groups = (n + 255) / 256;
   int64_t need = 2 * rows * n * 4;
