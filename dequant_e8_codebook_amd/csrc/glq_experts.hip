@@ -765,9 +765,9 @@ struct XpTiles {
 };
 
 // Tiles of so few rows read x~ from memory straight into operands, which takes that load off the LDS unit and costs the vector
-// memory path 2 lines a row and load: product of 16 experts of 4096 x 4096 with 4 rows each, at
-// 4 bits 57.0 us through LDS, 49.7 so, at 3 bits 50.0 and 46.0; 64 experts of 1024 x 2048 at 2 bits with 1, 4, 8 and 24 rows
-// 21.6, 21.2, 22.2 and 22.3 against 19.8, 21.6, 24.4 and 34.
+// memory path 2 lines a row and load. Products through LDS and so: 16 experts of 4096 x 4096 with 4 rows each, at 4 bits 60.5 and
+// 54.0 us, at 3 bits 50.7 and 47.7; 8 of them with one row at 4 bits 33.4 and 30.4; 64 of 1024 x 2048 at 2 bits with 1, 3, 8
+// and 24 rows 22.8, 22.5, 22.2 and 22.3, and 21.4, 22.4, 24.4 and 34; parts of 4 steps (4 of 1024 x 1024, 4 rows) 8.7 and 9.2.
 constexpr int kDirectRows = 4;
 constexpr int kGemmThreads = 512, kGemmLda = kGemmK + 8;
 // rows of x~ in LDS, of which there are two tiles: 256 of bf16 x~, 64 of each part of float32 x~
@@ -1256,7 +1256,9 @@ int check_experts(const glq_experts *E) {
 
 // Most parts along k of the units that are split (XpTiles): two planes of float32 z and four of float16 always have room (z_bytes), four or
 // eight as many as give each CU one for the most tiles there can be; none under 4 steps, which would not pay for the
-// transforms' reading more planes.
+// transforms' reading more planes. 2 of 8 experts of 4096 x 4096 at 4 bits, a row each, 32 tiles: product 14 us in 8 parts,
+// 32 in 2. 8192 rows over 8 experts of that size at 3 bits, 576 tiles: the call 401 us with 4 units in 4 parts, 422 with the last
+// 20 units in 2, 450 unsplit.
 int xp_parts(int64_t count, int64_t n, int64_t k, int64_t rows, bool f32) {
   const int64_t steps = up128(k) / kGemmK, most = (rows / (f32 ? 64 : 256) + (count < rows ? count : rows)) * ((n + 255) / 256);
   if (steps > kSplitSteps || steps < 8) return 1;
