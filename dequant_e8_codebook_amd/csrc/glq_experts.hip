@@ -1276,7 +1276,7 @@ int check_experts(const glq_experts *E) {
 // eight as many as give each CU one for the most tiles there can be; none under 4 steps, which would not pay for the
 // transforms' reading more planes. 2 of 8 experts of 4096 x 4096 at 4 bits, a row each, 32 tiles: product 14 us in 8 parts,
 // 32 in 2. 8192 rows over 8 experts of that size at 3 bits, 576 tiles: the call 401 us with 4 units in 4 parts, 422 with the last
-// 20 units in 2, 450 unsplit.
+// 20 units in 2.
 int xp_parts(int64_t count, int64_t n, int64_t k, int64_t rows, bool f32) {
   const int64_t steps = up128(k) / kGemmK, most = (rows / (f32 ? 64 : 256) + (count < rows ? count : rows)) * ((n + 255) / 256);
   if (steps > kSplitSteps || steps < 8) return 1;
