@@ -398,13 +398,17 @@ struct RouteArgs {
   int32_t *ids, *pos, *src, *offsets, *counts;     // counts [blocks][experts], then [groups][experts], workspace
 };
 
-// Tokens a workgroup: one workgroup takes up to 64. Beyond, few tokens each make the choice short and more counts to add up: 128
-// experts, 8 of them, choice and rows for 16, 32 and 64 tokens each: 500 tokens 9.3, 11.1 and 17.5 us, 2048: 9.6, 11.7 and 17.5,
-// 8192: 18.9, 14.1 and 17.8, 32768: 137, 54 and 34. Adding up all counts in each workgroup grows with the square of
-// the tokens, so past 512 workgroups of 64 tokens groups of 256 of them are added up first, in a launch between.
+// Tokens a workgroup, a multiple of its waves. Up to 64 tokens take one workgroup, with as few a wave as they need (16 of 64 experts' tokens
+// 4.0 us, in the form for 64 7.4). Beyond, few tokens each make the choice short and more counts to add up: 8 of 128
+// experts, choice and rows for 16, 32 and 64 tokens each: 500 tokens 9.3, 10.7 and 15.7 us, 2048: 9.8, 11.4 and 15.8, 4096 of 1024 experts:
+// 34, 31 and 40, 8192 of 128: 19.2, 13.5 and 16.6. Adding up all counts in each workgroup grows with the square of
+// the tokens (32768: 137, 54 and 33), so past 512 workgroups groups of 256 of them are added up first, in a launch between.
 constexpr int kRouteAlone = 64, kRouteThreads = 1024, kRouteMost = 1024, kRouteGroup = 256;
 constexpr int64_t kRouteShort = 2048, kRouteMiddle = 16384, kRoutePlain = 512;
-inline int route_each(int64_t tokens) { return tokens <= kRouteAlone ? 64 : tokens <= kRouteShort ? 16 : tokens <= kRouteMiddle ? 32 : 64; }
+inline int route_each(int64_t tokens) {
+  if (tokens <= kRouteAlone) return tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
+  return tokens <= kRouteShort ? 16 : tokens <= kRouteMiddle ? 32 : 64;
+}
 inline int64_t route_blocks(int64_t tokens) {
   const int each = route_each(tokens);
   return tokens < each ? 1 : (tokens + each - 1) / each;
@@ -418,6 +422,10 @@ __device__ __forceinline__ uint32_t score_order(float x) {
   const uint32_t u = __float_as_uint(x + 0.0f);
   if (!(x > -INFINITY)) return 0u;
   return (int32_t)u < 0 ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float score_of(uint32_t order) {    // (order > 0)
+  return __uint_as_float((int32_t)order < 0 ? order & 0x7FFFFFFFu : ~order);
 }
 
 // Exclusive sums of one number a thread over the workgroup's threads; total in *sum.
@@ -442,8 +450,9 @@ __device__ __forceinline__ int32_t group_before(int32_t x, int32_t *sum) {
 // expert is a mask of 64 bits in LDS (or-ed in any order, the same whatever it is), so
 // a choice's place among the workgroup's is the number of lower bits, and nothing
 // depends on which wave comes first. One workgroup alone (up to 64 tokens) goes on
-// to the rows itself: one launch. Bound by the chain of `top` maxima over the wave, each of lane exchanges and a ballot: 4.6 us for a token a
-// wave with 8 of 128 experts, of which the launch and the scores are 2.5; 10^6 tokens 457 us, 1.3 TB/s of scores and choices.
+// to the rows itself: one launch. Bound by the VALU work of `top` maxima over the wave, each of lane exchanges and a ballot: 4.5 us
+// for a token a wave with 8 of 128 experts, 7.7 for two, of which the launch and the scores are 2.5; 10^6 tokens 430 us,
+// 1.3 TB/s of scores and choices.
 template <int NV, bool F32, int TOKENS>
 __global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
   __shared__ unsigned long long chose[kRouteMost];
@@ -453,11 +462,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * TOKENS;
   constexpr int WAVES = kRouteThreads / 64, PER = TOKENS / WAVES;        // tokens wave, wave + WAVES, ...
+  // The tokens of a wave side by side, so that their chains of maxima overlap. A score that is not chosen yet is its order.
   int32_t mine[PER];                                           // lane j: the token's choice j
+  float value[PER], peak[PER];                                 // its score; the largest one
+  uint32_t order[PER][NV];
   float x[PER][NV];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int64_t t = t0 + wave + i * WAVES;
+    mine[i] = -1, value[i] = -INFINITY, peak[i] = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int e = lane + 64 * v;
@@ -470,41 +483,51 @@ __global__ void __launch_bounds__(kRouteThreads) route_pick_k(RouteArgs a) {
     }
   }
 #pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int v = 0; v < NV; ++v) order[i][v] = score_order(x[i][v]);
+  for (int j = 0; j < a.top; ++j) {
+    uint32_t best[PER], any = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      best[i] = 0;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) best[i] = order[i][v] > best[i] ? order[i][v] : best[i];
+      best[i] = wave_max(best[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      best[i] = __builtin_amdgcn_readfirstlane((int)best[i]);
+      any |= best[i];
+    }
+    if (any == 0) break;                                       // uniform: nothing left of any token
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      int e = -1;                                              // the lowest index among equals: first v, then lane
+#pragma unroll
+      for (int v = NV - 1; v >= 0; --v) {
+        const unsigned long long hit = __ballot(order[i][v] == best[i]);
+        e = hit ? 64 * v + __ffsll((long long)hit) - 1 : e;
+      }
+      if (best[i] == 0) continue;                              // uniform: nothing left of this one
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (lane + 64 * v == e) order[i][v] = 0;
+      const float s = score_of(best[i]);
+      if (j == 0) peak[i] = s;
+      if (lane == j) mine[i] = e, value[i] = s;
+    }
+  }
+#pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int in = wave + i * WAVES;
     const int64_t t = t0 + in;
-    mine[i] = -1;
     if (t >= a.tokens) continue;                               // uniform
-    uint32_t order[NV];
+    const float w = mine[i] >= 0 ? expf(value[i] - peak[i]) : 0.0f;
+    float sum = w;
+    if (!a.normalize) {                                        // the others
 #pragma unroll
-    for (int v = 0; v < NV; ++v) order[v] = score_order(x[i][v]);
-    float value = -INFINITY, peak = 0.0f;
-    for (int j = 0; j < a.top; ++j) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) best = order[v] > best ? order[v] : best;
-      best = __builtin_amdgcn_readfirstlane((int)wave_max(best));
-      if (best == 0) break;                                    // uniform
-      int e = 0;                                               // the lowest index among equals: first v, then lane
-#pragma unroll
-      for (int v = NV - 1; v >= 0; --v) {
-        const unsigned long long hit = __ballot(order[v] == best);
-        e = hit ? 64 * v + __ffsll((long long)hit) - 1 : e;
-      }
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (lane + 64 * v == e) order[v] = 0;
-      const float s = __uint_as_float((int32_t)best < 0 ? best & 0x7FFFFFFFu : ~best);
-      if (j == 0) peak = s;
-      if (lane == j) mine[i] = e, value = s;
-    }
-    const float w = mine[i] >= 0 ? expf(value - peak) : 0.0f;
-    float sum = 0.0f;
-    if (a.normalize) {
-      sum = w;
-    } else {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) sum += x[i][v] > -INFINITY ? expf(x[i][v] - peak) : 0.0f;
+      for (int v = 0; v < NV; ++v) sum += order[i][v] ? expf(score_of(order[i][v]) - peak[i]) : 0.0f;
     }
     sum = lanes_sum<64>(sum);
     if (lane < a.top) {
