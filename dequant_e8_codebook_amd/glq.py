@@ -896,6 +896,10 @@ def _heads(t, name, index, dtype, total, heads, dim):
         raise ValueError(f"{name}: must be a device (cuda) tensor")
     if t.get_device() != index or t.dtype is not dtype or t.shape != (total, heads, dim):
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {(total, heads, dim)} on cuda:{index}")
+    return _heads_at(t, name, dtype, heads, dim)
+
+
+def _heads_at(t, name, dtype, heads, dim):
     at, step = t.data_ptr(), heads * dim
     if not t.is_contiguous():
         step, between, inner = t.stride()
@@ -930,14 +934,17 @@ def qk_norm_rope(q, k, positions, rotary, q_out, k_out=None, q_weight=None, k_we
     The outputs may be the inputs. With a cache, keys and v are written there too at
     `slots`, and k_out may be None. Returns q_out, k_out."""
     dt = _attn_dtype(q, "q")
-    _attn_dtype(k, "k")
-    dtype, index, (tokens, heads, dim), kvh = q.dtype, q.get_device(), q.shape, k.shape[1]
+    if not isinstance(k, torch.Tensor):
+        raise ValueError("k: must be a device (cuda) tensor")
+    dtype, index, (tokens, heads, dim), (of_k, kvh, dim_k) = q.dtype, q.get_device(), q.shape, k.shape
     if index < 0:
         raise ValueError("q: must be a device (cuda) tensor")
     if dim not in _HEAD_DIMS:
         raise ValueError(f"q: head_dim {dim}, expected one of {_HEAD_DIMS}")
-    qp, qs = _heads(q, "q", index, dtype, tokens, heads, dim)
-    kp, ks = _heads(k, "k", index, dtype, tokens, kvh, dim)
+    if of_k != tokens or dim_k != dim or k.dtype is not dtype or k.get_device() != index:
+        raise ValueError(f"k: {k.dtype} {tuple(k.shape)} on {k.device}, expected {dtype} {(tokens, kvh, dim)} on cuda:{index}")
+    qp, qs = _heads_at(q, "q", dtype, heads, dim)
+    kp, ks = _heads_at(k, "k", dtype, kvh, dim)
     qop, qos = (qp, qs) if q_out is q else _heads(q_out, "q_out", index, dtype, tokens, heads, dim)
     kop, kos = (0, 0) if k_out is None else (kp, ks) if k_out is k else _heads(k_out, "k_out", index, dtype, tokens, kvh, dim)
     vp = vs = sp = pp = tp = most = rot = wq = wk = 0
