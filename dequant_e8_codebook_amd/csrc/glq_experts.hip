@@ -92,8 +92,8 @@ __device__ __forceinline__ void load_signs8(const int8_t *p, float *s) {
   for (int i = 0; i < 8; ++i) s[i] = (float)(int8_t)((i < 4 ? u.x : u.y) >> (8 * (i & 3)));
 }
 
-// Between the product and U^T the bf16 path keeps z in float16, 11 bits, whose rounding (2^-12) adds nothing to
-// those of x~ and y (2^-9), and halves what is moved. So that any row fits its range, a row's x is taken
+// Between the product and U^T the bf16 path keeps z in float16, 11 bits, whose rounding (2^-11 relative at most) adds
+// 1% to that of x~ (2^-8, both at random and added in squares), and halves what is moved. So that any row fits its range, a row's x is taken
 // times 2^-e, e = row_exponent, from the start, and z times 2^e at the end: with M the largest |x| and 2^c >= sqrt(k),
 // the vector x 2^-e is at most 2 long, and so is x~; a weight row in units of the operands (8 v at 4 bits) is
 // at most 8 * 1.25 sqrt(12) sqrt(k / 8) = 12.3 sqrt(k) long, so |z| < 24.6 sqrt(k), below 65504 up to k = 2^21 (35,600).
