@@ -750,9 +750,9 @@ extern "C" int glq_kv_plan(const glq_plan *P, void *hip_stream) {
                 log2_of(P->page_size), 1, 0, 0};
   if (P->max_tokens > 0) a.q_tiles = tiles(P->max_tokens, kPlanTokens);
   if (read) a.r_tiles = P->max_read > 0 ? tiles(P->max_read, kPlanTokens) : 1;
-  // pages that max_tokens new ones can take
-  const int64_t pages = P->max_tokens / P->page_size + P->batch;
-  a.p_groups = pages > 0 ? tiles(pages < P->batch * P->max_pages ? pages : P->batch * P->max_pages, kPlanPages) : 1;
+  // pages that max_tokens new ones can take, as far as the table has room; without any, the workgroup that writes *used
+  const int64_t taken = P->max_tokens / P->page_size + P->batch, room = P->batch * P->max_pages, pages = taken < room ? taken : room;
+  a.p_groups = pages > 0 ? tiles(pages, kPlanPages) : 1;
   const int64_t groups = (int64_t)a.q_tiles + a.r_tiles + a.p_groups;
   if (groups > kMaxGroups) return GLQ_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(kv_plan_k, dim3((unsigned)groups), dim3(kPlanThreads), 0, reinterpret_cast<hipStream_t>(hip_stream), a);

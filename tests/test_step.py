@@ -144,6 +144,24 @@ def test_plan_nothing():
     assert plan.slots.tolist() == [-1] * 6 and plan.positions.tolist() == [0] * 6 and plan.read_slots.tolist() == [-1] * 2
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 1024])
+@pytest.mark.parametrize("max_tokens", [0, 15, 16, 17, 1024, 4096, 100000])
+@pytest.mark.parametrize("max_read", [0, 40])
+def test_plan_no_requests(page, max_tokens, max_read):
+    """Every output is written for a batch of none, whatever the lists hold."""
+    plan = glq.KvPlan(torch.zeros(0, 3, dtype=torch.int32).cuda(), page, 4, max_tokens, max_read)
+    none = torch.zeros(0, dtype=torch.int32).cuda()
+    for t in (plan.used, plan.cu_q, plan.slots, plan.positions, plan.cu_k, plan.read_slots):
+        if t is not None:
+            t.fill_(9)
+    glq.kv_plan(plan, none, none, none)
+    assert plan.used.tolist() == [0] and plan.cu_q.tolist() == [0]
+    assert (plan.slots == -1).all() and (plan.positions == 0).all()
+    if max_read:
+        assert plan.cu_k.tolist() == [0] and (plan.read_slots == -1).all()
+
+
 # ------------------------------------------------------ norms and rotation
 
 def _turn_reference(x, weight, eps, cos, sin, pairs):
