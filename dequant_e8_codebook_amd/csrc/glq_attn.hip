@@ -113,6 +113,7 @@ template <int FMT, int D> struct Tile {
   static constexpr int VW = VB < 4 ? 1 : VB / 4;
   uint32_t k[2][KW], v[8][VW];
   float ks[8], vs[8];
+  uint32_t gone;                                     // bit s: half s lies on a page outside the cache
 };
 
 // dimension of element e of k-step c in quarter g (the order in which a lane's K
@@ -128,14 +129,31 @@ template <int FMT, int D> __device__ __forceinline__ int k_dim(int c, int g, int
 // what no kernel of this call writes: read by scalar loads where the address is uniform
 typedef __attribute__((address_space(4))) const int32_t *scalar_ints;
 
-// the pages of a tile's two halves (a half past the end repeats the first)
-struct Pages { uint32_t p[2]; };
+// The pages of a tile's two halves (a half past the end repeats the first). A plan that found no free page
+// writes one outside the cache, and what lies in any page inside is another request's: the tokens of
+// such a half are loaded from kNowhere, and their scores are -inf from the start (masked after the product, in every tile
+// of a loop that otherwise has its mask behind it, they took 64 registers: 30,000 tokens in bf16 43.5 us, 30.0 so, and 29.7 were no
+// page looked at).
+struct Pages { uint32_t p[2], gone; };
+struct Nowhere {
+  uint8_t row[16 * 512];                             // 16 tokens of the longest rows
+  float scale[16];
+};
+// (chosen between as global addresses: of generic ones the compiler makes flat loads: 32 of up to 4096 in 8 bits 43.8 us, 39.2 so)
+typedef __attribute__((address_space(1))) const uint8_t *global_bytes;
+template <class T> __device__ __forceinline__ const T *either(bool one, const T *x, const T *y) {
+  const global_bytes a = (global_bytes)(uintptr_t)x, b = (global_bytes)(uintptr_t)y;
+  return (const T *)(const uint8_t *)(one ? a : b);
+}
+__device__ const Nowhere kNowhere __attribute__((aligned(16))) = {{}, {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1}};
 __device__ __forceinline__ Pages pages_of(const DecodeArgs &a, scalar_ints table, int t, int end) {
   Pages x;
+  x.gone = 0;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int32_t page = table[(t + 16 * s < end ? t + 16 * s : t) >> a.page_shift];
     x.p[s] = page < 0 ? 0u : page < a.num_pages ? (uint32_t)page : (uint32_t)a.num_pages - 1;
+    x.gone |= x.p[s] != (uint32_t)page ? 1u << s : 0u;
   }
   return x;
 }
@@ -146,26 +164,29 @@ __device__ __forceinline__ void load_tile(const DecodeArgs &a, const Pages &page
   using T = Tile<FMT, D>;
   const int g = lane >> 4, n = lane & 15;
   const uint8_t *kp = reinterpret_cast<const uint8_t *>(a.k), *vp = reinterpret_cast<const uint8_t *>(a.v);
+  x.gone = pages.gone;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int ts = t + 16 * s < end ? t + 16 * s : t;
     const int64_t row = (((int64_t)pages.p[s] * a.heads + h) << a.page_shift) + (ts & ((1 << a.page_shift) - 1));
-    const uint8_t *kr = kp + row * T::RB + n * T::RB;
+    const bool gone = pages.gone >> s & 1;           // uniform
+    static_assert(16 * T::RB <= sizeof kNowhere.row, "rows of a half");
+    const uint8_t *kr = either(gone, kNowhere.row, kp + row * T::RB) + n * T::RB;
     if constexpr (T::RB >= 64) {
 #pragma unroll
       for (int i = 0; i < T::RB / 64; ++i) load_words<4>(kr + 64 * i + 16 * g, &x.k[s][4 * i]);
     } else {
       load_words<2>(kr + 8 * g, x.k[s]);
     }
-    const uint8_t *vr = vp + row * T::RB + 4 * g * T::RB + n * T::VB;
+    const uint8_t *vr = either(gone, kNowhere.row, vp + row * T::RB) + 4 * g * T::RB + n * T::VB;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if constexpr (T::VB == 2) x.v[4 * s + r][0] = *reinterpret_cast<const uint16_t *>(vr + r * T::RB);
       else load_words<T::VW>(vr + r * T::RB, x.v[4 * s + r]);
     }
     if constexpr (FMT != GLQ_KV_BF16) {
-      const float4 u = *reinterpret_cast<const float4 *>(a.ks + row + 4 * g);
-      const float4 w = *reinterpret_cast<const float4 *>(a.vs + row + 4 * g);
+      const float4 u = *reinterpret_cast<const float4 *>(either(gone, kNowhere.scale, a.ks + row) + 4 * g);
+      const float4 w = *reinterpret_cast<const float4 *>(either(gone, kNowhere.scale, a.vs + row) + 4 * g);
       x.ks[4 * s] = u.x, x.ks[4 * s + 1] = u.y, x.ks[4 * s + 2] = u.z, x.ks[4 * s + 3] = u.w;
       x.vs[4 * s] = w.x, x.vs[4 * s + 1] = w.y, x.vs[4 * s + 2] = w.z, x.vs[4 * s + 3] = w.w;
     }
@@ -439,7 +460,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
   const int t0 = 128 * tile0 + 32 * wave, end = min(at.len, 128 * tile1);
   {
     Tile<FMT, D> tile;
-    Pages next = {{0, 0}};
+    Pages next = {{0, 0}, 0};
     if (t0 < end) {
       const Pages first = pages_of(a, table, t0, end);
       next = pages_of(a, table, t0 + 128 < end ? t0 + 128 : t0, end);
@@ -478,7 +499,8 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
       float s[8];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        f32x4 c4 = {s0, s0, s0, s0};
+        const float c0 = x.gone >> half & 1 ? -INFINITY : s0;
+        f32x4 c4 = {c0, c0, c0, c0};
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
           const bf16x8 kk = k_operand<FMT, D, BIASED>(x, half, c, nib);

@@ -431,8 +431,9 @@ size_t glq_attn_decode_workspace(const glq_kv_cache *C, int64_t batch, int32_t q
  *               out_stride elements apart (>= q_heads * head_dim; pointers and
  *               strides multiples of 16 bytes)
  *   page_table  device int32 [batch][max_pages]; entries past a sequence's
- *               length are not used. An entry outside the cache is read as
- *               the nearest page inside it.
+ *               length are not used. The tokens of an entry outside the cache
+ *               (-1, where glq_kv_plan found no free page) are left out, as if
+ *               the sequence did not have them.
  *   lens        device int32 [batch], read as 0 .. max_len; a length of 0 gives
  *               a row of zeros
  *   max_len     host: no length exceeds it; <= max_pages * page_size. The
@@ -535,8 +536,10 @@ typedef struct {
  * lens[b] + added[b] need more from free_pages, request after request. Its i-th new token
  * has position lens[b] + i and the slot of that token.
  *   Not enough free pages: *used says how many were wanted, the missing ones are written as
- *   -1 and tokens in them have slot -1 (glq_kv_append drops them). So have tokens past
- *   the table's end and tokens in pages outside 0 .. num_pages - 1.
+ *   -1 and tokens in them have slot -1: glq_kv_append drops them, glq_kv_read gives zeros for them,
+ *   glq_attn_decode leaves them out. So have tokens past the table's end (whose length glq_attn_decode reads as
+ *   its max_len) and tokens in pages outside 0 .. num_pages - 1. new_lens counts them all the same: where
+ *   *used > num_free, the caller knows that some requests of this step have to wait and be planned again.
  *   Entries behind the last token (a padded batch): slot -1, position 0.
  *   More tokens than max_tokens or max_read: what does not fit is not written, and offsets
  *   end at those lengths.

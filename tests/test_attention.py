@@ -319,6 +319,40 @@ def test_decode_one_workspace_for_many_calls(gen):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("page,lens", [(16, [300, 33, 16, 1, 700]), (128, [20011, 129, 4000])])
+def test_decode_leaves_out_pages_outside_the_cache(gen, fmt, dim, dtype, page, lens):
+    """Tokens on such pages count for nothing: what other pages hold, NaN here, is no stand-in for them."""
+    cache, q, table, ln, _, _ = _decode_case(gen, fmt, lens, 6, 2, dim, page, dtype)
+    pages = cache.k.shape[0]
+    full, bad = table.cpu(), [-1, pages, 2 ** 31 - 1, -2 ** 31]
+    gone = torch.rand(full.shape, generator=gen) < 0.3
+    gone |= (full == 0) | (full == pages - 1)              # their tokens' places are taken by the NaN below
+    gone[0, 0] = gone[1] = True                            # a first page, a whole sequence
+    gone[-1, (lens[-1] - 1) // page] = True                # a last page
+    out_of = torch.tensor(bad)[torch.randint(0, 4, full.shape, generator=gen)].to(torch.int32)
+    keys, values = [], []
+    for b, n in enumerate(lens):
+        t = torch.arange(n)
+        slots = (full[b].long()[t // page] * page + t % page).to(torch.int32).cuda()
+        kv = [torch.empty(n, 2, dim, device="cuda") for _ in range(2)]
+        glq.kv_read(cache, slots, *kv)
+        keys.append(kv[0].cpu()), values.append(kv[1].cpu())
+    for x in (cache.k, cache.v) if fmt == "bf16" else (cache.k_scale, cache.v_scale):
+        x[0] = math.nan
+        x[-1] = math.nan
+    out, _ = _decode(cache, q, torch.where(gone, out_of, full).cuda(), ln, max(lens))
+    for b, n in enumerate(lens):
+        seen = ~gone[b, torch.arange(n) // page].expand(1, n)
+        for h in range(6):
+            ref, mag = _ref_attend(q[b, h:h + 1].cpu(), keys[b][:, h // 3], values[b][:, h // 3], dim ** -0.5, seen)
+            _held(out[b, h:h + 1], ref, mag, dtype)
+    assert not out[1].any()
+
+
+@pytest.mark.gpu
 def test_decode_nothing_cached(gen):
     cache, q, table, ln, _, _ = _decode_case(gen, "bf16", [0, 0, 0], 2, 1, 64, 16, "bf16")
     out, _ = _decode(cache, q, table, ln, 0)

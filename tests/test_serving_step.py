@@ -187,6 +187,33 @@ def test_prompts_then_tokens(cb, gen, fmt, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", list(FORMATS))
+def test_attention_after_a_plan_without_pages(cb, gen, fmt):
+    """A request that got no page attends over what it has in the cache, and over nobody else's tokens."""
+    page, dim, lens, added = 16, 64, [16, 16, 30], [1, 1, 1]
+    table = torch.full((3, 4), -1, dtype=torch.int32)
+    table[0, 0], table[1, 0], table[2, :2] = 0, 3, torch.tensor([2, 1])
+    plan = glq.KvPlan(table.cuda(), page, 5, 3)
+    cache = glq.KvCache.empty(5, page, 2, dim, FORMATS[fmt])
+    old = torch.randn(5 * page, 2, dim, generator=gen).to(torch.bfloat16).cuda()
+    glq.kv_append(cache, old, old, _ints(list(range(5 * page))))
+    q, k = torch.randn(3, 4, dim, generator=gen).cuda().to(torch.bfloat16), torch.randn(3, 2, dim, generator=gen).cuda().to(torch.bfloat16)
+    glq.kv_plan(plan, _ints(lens), _ints(added), _ints([4]))       # one page for the two that need one
+    assert plan.used.tolist() == [2] and plan.slots.tolist()[1] == -1 and plan.new_lens.tolist() == [17, 17, 31]
+    glq.qk_norm_rope(q, k, plan.positions, glq.rotary_table(64, dim), q, k, cache=cache, v=k, slots=plan.slots)
+    out = torch.zeros_like(q)
+    ws = torch.zeros(glq.attn_decode_workspace_bytes(cache, 3, 4, 64), dtype=torch.uint8, device="cuda")
+    glq.attn_decode(cache, q, plan.page_table, plan.new_lens, out, ws, 64)
+    for b, slots in enumerate(([*range(16), 64], list(range(48, 64)), [*range(32, 48), *range(16, 31)])):
+        kv = [torch.empty(len(slots), 2, dim, device="cuda") for _ in range(2)]
+        glq.kv_read(cache, _ints(slots), *kv)
+        for h in range(4):
+            ref, mag = _ref_attend(q[b, h:h + 1].cpu(), kv[0][:, h // 2].cpu(), kv[1][:, h // 2].cpu(), dim ** -0.5,
+                                   torch.ones(1, len(slots), dtype=torch.bool))
+            held_attention(out[b, h:h + 1], ref, mag, "bf16")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("page", [16, 32])
 def test_step_in_a_graph(cb, gen, dtype, page):
