@@ -54,8 +54,9 @@ struct XpRows {
   const int8_t *sign_k, *sign_n;
   uint16_t *xt;                // [planes][rows][kp] bf16: x~, or three parts that add up to it; zeros from k on
   float *rowsum;               // [1 + ks][rows] sums of x~, whole and of each part along k (bf16 path)
-  float *row_factor;           // [rows] what z's row is to be multiplied by, but for the transform's 1 / sqrt(block)
-  int32_t *row_expert, *row_parts;   // [rows]
+  float *row_factor;           // [rows] what z's row is to be multiplied by, but for the transform's 1 / sqrt(block) and
+  int32_t *row_expert;         // [rows] the power of two in the upper half of this (put_factor); the lower half: the expert
+  int32_t *row_parts;          // [rows]
   const void *z;               // [parts][rows][n]: float32 or float16, both without row_factor
   const float *scale, *row_scale;
   float unit;                  // of the operands: 1, 1/4 or 1/8 of a weight at 2, 3 or 4 bits
@@ -107,6 +108,16 @@ __device__ __forceinline__ int row_exponent(uint32_t top, int64_t k) {
   return (e ? e - 127 : -126) + c;
 }
 
+// z's row is to be multiplied by scale 2^shift, which may leave float32's range where y does not: shift reaches 138, and a
+// row of one large element has a z and a y far below M sqrt(k). So it is kept as a factor between 2^-60 and 2^60 and the
+// power of two that is left, which z takes before its transform: with z 2^rest = y / factor, neither comes near the range's ends.
+__device__ __forceinline__ void put_factor(const XpRows &a, int32_t r, int expert, float scale, int shift) {
+  const int e = (int)(__float_as_uint(scale) >> 23) - 127, all = e + shift, within = all < -60 ? -60 : all > 60 ? 60 : all;
+  a.row_factor[r] = ldexpf(scale, within - e);
+  a.row_expert[r] = (all - within) * 65536 + expert;
+}
+static_assert(kMaxExperts <= 65536, "an expert's number in 16 bits");
+
 // x times the signs, 8 elements at a time, or zeros
 template <bool F32>
 __device__ __forceinline__ void load_signed8(const XpRows &a, bool in, int64_t from, const int8_t *signs, int64_t o, float *v) {
@@ -136,7 +147,6 @@ __global__ void __launch_bounds__(64 * NW) xp_in_k(XpRows a) {
   const int32_t r = blockIdx.x;
   if (r < bounded(a.offsets[0], a.rows) || r >= bounded(a.offsets[a.count], a.rows)) return;
   const int e = expert_of(a.offsets, a.count, r);
-  if (tid == 0) a.row_expert[r] = e;
   const int64_t from = a.src ? a.src[r] : r;
   const bool in = from >= 0 && from < a.x_rows;
   const int8_t *signs = a.sign_k + (int64_t)e * a.k;
@@ -164,7 +174,7 @@ __global__ void __launch_bounds__(64 * NW) xp_in_k(XpRows a) {
     }
     shift = row_exponent(top, a.k);
   }
-  if (tid == 0) a.row_factor[r] = ldexpf(a.scale[e] * a.unit, shift);
+  if (tid == 0) put_factor(a, r, e, a.scale[e] * a.unit, shift);
   for (int64_t s0 = 0; s0 < a.kp; s0 += SEG) {
     if (s0) {
 #pragma unroll
@@ -257,7 +267,8 @@ __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
     for (int j = 0; j < a.top; ++j) {
       const int32_t r = a.pos ? a.pos[row_y * a.top + j] : (int32_t)row_y;
       if (r < first || r >= end) continue;           // uniform
-      const int e = a.row_expert[r], parts = bounded(a.row_parts[r], a.ks);     // (decreasing offsets: rows no tile was for)
+      const int expert = a.row_expert[r], e = expert & 0xFFFF, rest = expert >> 16;
+      const int parts = bounded(a.row_parts[r], a.ks);         // (decreasing offsets: rows no tile was for)
       const float w = (a.pos ? a.weights[row_y * a.top + j] * inv : inv) * a.row_factor[r];
       const int8_t *signs = a.sign_n + (int64_t)e * a.n;
       float v[E];
@@ -280,6 +291,9 @@ __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
           for (int i = 0; i < 8; ++i) v[h + i] *= x[i];
         }
       }
+      if (rest)                                      // uniform, and rare
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = ldexpf(v[i], rest);
       if (again) __syncthreads();
       again = true;
       row_fwht<E, NW>(v, buf, a.log_n);
@@ -470,7 +484,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
         for (int i = 0; i < 16; ++i) v[i] = ldexpf(v[i], before);
       }
     }
-    if (tid == 0) a.row_expert[r] = e, a.row_factor[r] = ldexpf(scale, shift);
+    if (tid == 0) put_factor(a, r, e, scale, shift);
     rb_fwht_wave<F32 ? 0 : 1, true>(v, lane);
     cross_waves<NW>(v, cross, wave, lane);
     const float scaled = ldexpf(inv, -shift - before);
@@ -530,7 +544,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
   int32_t row = -1, expert = 0, parts = 0;           // of item base + lane
   float factor = 0.0f;
   int64_t base = -64;
-  struct Item { int32_t row, parts; float factor; uint4 raw[RAW]; uint2 sign[2]; };
+  struct Item { int32_t row, parts, expert; float factor; uint4 raw[RAW]; uint2 sign[2]; };
   auto plane = [&](int p, int32_t r, uint4 (&raw)[RAW]) {
     const uint4 *z = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.z) + ES * (((int64_t)p * a.rows + r) * a.n + el));
     if constexpr (Z16) raw[0] = z[0], raw[1] = z[64];
@@ -558,9 +572,9 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
     if (it.row < 0) return;
     it.parts = __builtin_amdgcn_readlane(parts, at);
     it.factor = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(factor), at));
-    const int64_t e = __builtin_amdgcn_readlane(expert, at);
+    it.expert = __builtin_amdgcn_readlane(expert, at);
     plane(0, it.row, it.raw);
-    const int8_t *signs = a.sign_n + e * a.n + eo;
+    const int8_t *signs = a.sign_n + (int64_t)(it.expert & 0xFFFF) * a.n + eo;
     it.sign[0] = *reinterpret_cast<const uint2 *>(signs), it.sign[1] = *reinterpret_cast<const uint2 *>(signs + 256);
   };
   typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -602,7 +616,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
         for (int q = 0; q < 16; ++q) v[q] += x[q];
       }
       if (a.row_scale) {
-        const int64_t e = a.row_expert[it.row];
+        const int64_t e = it.expert & 0xFFFF;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float x[8];
@@ -611,6 +625,9 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
           for (int q = 0; q < 8; ++q) v[8 * h + q] *= x[q];
         }
       }
+      if (it.expert >> 16)                           // uniform, and rare (put_factor)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = ldexpf(v[q], it.expert >> 16);
       rb_fwht_wave<0, true>(v, lane);
     } else if (sets > 1) {                           // (the other sets may have a row: the exchange's barriers are all waves')
 #pragma unroll

@@ -171,6 +171,33 @@ def test_sizes_of_inputs(cb, size, counts):
     _held(y, ref, _tolerance(ref, "bf16", 256), "bf16")
 
 
+def _held_at_the_ends(experts, x, y, offsets, y_dtype):
+    """As _held, with no absolute term but a few of the smallest numbers (x~ and z are at least as large as y here)."""
+    ref = _rows_reference(experts, x.double().cpu().numpy(), offsets, None, len(x))
+    size = np.sqrt((ref ** 2).mean(-1, keepdims=True))
+    tol = 6 / np.sqrt(3) * 2.0 ** -8 * size
+    tol = tol + (2.0 ** -8 if y_dtype == "bf16" else 2.0 ** -24) * (np.abs(ref) + tol) + 2.0 ** -126
+    got = y.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert (np.abs(got - ref) <= tol).all(), f"worst {(np.abs(got - ref) / tol).max():.3g} of the tolerance"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("y_dtype", list(DTYPES))
+@pytest.mark.parametrize("n,k,rows", [(128, 256, 3), (1024, 4096, 3), (1024, 1024, 700), (264, 5120, 40)])
+@pytest.mark.parametrize("size,scale", [(123, 0), (123, -30), (110, 13), (60, 60), (-60, -60), (-110, 0), (-126, 0), (-126, 100), (-130, 120)])
+def test_factors_at_the_ends_of_float32(cb, y_dtype, n, k, rows, size, scale):
+    """A row's power of two times its scale may leave the range that y does not leave."""
+    experts = Set(2, n, k, 2, seed=7)
+    experts.scale[:] = 2.0 ** scale
+    handle, x = experts.device(cb), torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+    x[torch.arange(rows), torch.arange(rows) * 7 % k] = 2.0 ** size
+    offsets = [0, rows // 3, rows]
+    y = torch.empty(rows, n, dtype=DTYPES[y_dtype], device="cuda")
+    glq.expert_linear(handle, x, y, torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, rows))
+    _held_at_the_ends(experts, x, y, offsets, y_dtype)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("bpw", [2, 3, 4])
 @pytest.mark.parametrize("dtype,y_dtype", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
