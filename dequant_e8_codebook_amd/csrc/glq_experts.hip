@@ -392,20 +392,22 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
   const int el = 1024 * wave + 8 * rb_ell(lane), eo = 1024 * wave + rb_elem_out(lane, 0);    // elements read, written (+ 512, + 256)
   constexpr int RAW = F32 ? 4 : 2;
   uint4 raw[RAW];
-  auto fetch = [&](int32_t r) {
-    if (a.src && !each && ((r - r0) & 63) == 0) sources = r + lane < r1 ? a.src[r + lane] : -1;
-    const int64_t from = a.src ? __builtin_amdgcn_readlane(sources, (r - r0) & 63) : r;
+  auto load = [&](int64_t from, uint4 (&to)[RAW]) {
     if (from >= 0 && from < a.x_rows) {
       const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.x) + (F32 ? 4 : 2) * (from * a.k + el));
       if constexpr (F32) {
-        raw[0] = p[0], raw[1] = p[1], raw[2] = p[128], raw[3] = p[129];
+        to[0] = p[0], to[1] = p[1], to[2] = p[128], to[3] = p[129];
       } else {
-        raw[0] = p[0], raw[1] = p[64];
+        to[0] = p[0], to[1] = p[64];
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < RAW; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < RAW; ++i) to[i] = make_uint4(0, 0, 0, 0);
     }
+  };
+  auto fetch = [&](int32_t r) {
+    if (a.src && !each && ((r - r0) & 63) == 0) sources = r + lane < r1 ? a.src[r + lane] : -1;
+    load(a.src ? __builtin_amdgcn_readlane(sources, (r - r0) & 63) : r, raw);
   };
   if (r0 < r1) fetch(r0);                            // (of any row there is room for)
   if (r0 >= r1 || r0 < first || r0 >= end) return;
@@ -477,11 +479,19 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_in_blk_k(XpRows a) {
       if (r > r0) finish(r - 1);
       for (int w = 0; w < waves; ++w) top = top > tops[r & 1][w] ? top : tops[r & 1][w];
       shift = row_exponent(top << 16, a.k);
-      // 2^-shift waits for the end, where it costs nothing, unless sums of 16384 could leave float32's range before
-      if (shift > 100 || shift < -100) {             // uniform
+      // 2^-shift waits for the end, where it costs nothing, unless sums of 16384 could leave float32's range before: such rows
+      // are read again, as their first sums are among those
+      if (shift > 100 || shift < -100) {             // uniform, and rare
         before = -shift;
+        uint4 again[RAW];
+        load(a.src ? a.src[r] : r, again);
+        const uint32_t w[8] = {again[0].x, again[0].y, again[0].z, again[0].w, again[1].x, again[1].y, again[1].z, again[1].w};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = ldexpf(v[i], before);
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t u = w[i] ^ (flip[i] & 0x80008000u);
+          const float lo = ldexpf(bf16_lo(u), before), hi = ldexpf(bf16_hi(u), before);
+          v[2 * i] = lo + hi, v[2 * i + 1] = lo - hi;
+        }
       }
     }
     if (tid == 0) put_factor(a, r, e, scale, shift);

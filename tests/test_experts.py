@@ -199,6 +199,22 @@ def test_factors_at_the_ends_of_float32(cb, y_dtype, n, k, rows, size, scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("k,rows", [(256, 3), (4096, 3), (1024, 1400), (2048, 3), (16384, 3), (5120, 40)])
+@pytest.mark.parametrize("size,scale", [(127, -24), (126, -24), (-126, 60), (-133, 60), (-110, 60)])
+def test_rows_at_the_ends_of_bfloat16(cb, k, rows, size, scale):
+    """Sums of neighbours that float32 does not hold, and elements below the normal numbers."""
+    experts = Set(2, 256, k, 2, seed=7)
+    experts.scale[:] = 2.0 ** scale
+    gen = torch.Generator().manual_seed(k)
+    x = ((1 + 0.99 * torch.rand(rows, k, generator=gen, dtype=torch.float64)) * 2.0 ** size).to(torch.bfloat16)
+    x = torch.where(torch.rand(rows, k, generator=gen) < 0.5, -x, x).clamp(-torch.finfo(torch.bfloat16).max, torch.finfo(torch.bfloat16).max).cuda()
+    handle, offsets = experts.device(cb), [0, rows // 3, rows]
+    y = torch.empty(rows, 256, device="cuda")
+    glq.expert_linear(handle, x, y, torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, rows))
+    _held_at_the_ends(experts, x, y, offsets, "f32")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("bpw", [2, 3, 4])
 @pytest.mark.parametrize("dtype,y_dtype", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
 def test_row_scales_and_rows_of_none(cb, bpw, dtype, y_dtype):
