@@ -20,6 +20,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <type_traits>
 
 #include "glq.h"
 #include "glq_cache.h"
@@ -56,12 +57,13 @@ struct XpRows {
   float *rowsum;               // [1 + ks][rows] sums of x~, whole and of each part along k (bf16 path)
   float *row_factor;           // [rows] what z's row is to be multiplied by, but for the transform's 1 / sqrt(block) and
   int32_t *row_expert;         // [rows] the power of two in the upper half of this (put_factor); the lower half: the expert
-  int32_t *row_parts;          // [rows]
-  const void *z;               // [parts][rows][n]: float32 or float16, both without row_factor
+  int32_t *row_parts;          // [rows] parts along k of the row's tile (0: it had none) and 16 times its first part's row of zs
+  const void *z;               // [rows][n] of rows in one part: float32 or float16, both without row_factor
+  const float *zs;             // rows of n of those in several: part p's is zs_step rows times p further
   const float *scale, *row_scale;
   float unit;                  // of the operands: 1, 1/4 or 1/8 of a weight at 2, 3 or 4 bits
   int64_t k, kp, n, x_rows, out_rows;    // kp: k up to a multiple of 128
-  int32_t count, rows, top, ks;
+  int32_t count, rows, top, ks, zs_step;
   int log_k, log_n;            // Hadamard blocks
 };
 
@@ -93,8 +95,9 @@ __device__ __forceinline__ void load_signs8(const int8_t *p, float *s) {
   for (int i = 0; i < 8; ++i) s[i] = (float)(int8_t)((i < 4 ? u.x : u.y) >> (8 * (i & 3)));
 }
 
-// Between the product and U^T the bf16 path keeps z in float16, 11 bits, whose rounding (2^-11 relative at most) adds
-// 1% to that of x~ (2^-8, both at random and added in squares), and halves what is moved. So that any row fits its range, a row's x is taken
+// Between the product and U^T z is float32, and for many rows with x and y in bf16 float16, 11 bits, rounded once: that
+// (2^-11 relative at most) adds 1% to the roundings of x~ and y (2^-8 each, at random and added in squares), and halves what is moved. Parts
+// along k are float32 always, as sums are. So that any row fits its range, a row's x is taken
 // times 2^-e, e = row_exponent, from the start, and z times 2^e at the end: with M the largest |x| and 2^c >= sqrt(k),
 // the vector x 2^-e is at most 2 long, and so is x~; a weight row in units of the operands (8 v at 4 bits) is
 // at most 8 * 1.25 sqrt(12) sqrt(k / 8) = 12.3 sqrt(k) long, so |z| < 24.6 sqrt(k), below 65504 up to k = 2^21 (35,600).
@@ -115,6 +118,7 @@ __device__ __forceinline__ void put_factor(const XpRows &a, int32_t r, int exper
   const int e = (int)(__float_as_uint(scale) >> 23) - 127, all = e + shift, within = all < -60 ? -60 : all > 60 ? 60 : all;
   a.row_factor[r] = ldexpf(scale, within - e);
   a.row_expert[r] = (all - within) * 65536 + expert;
+  a.row_parts[r] = 0;                                // (decreasing offsets: rows no tile is for)
 }
 static_assert(kMaxExperts <= 65536, "an expert's number in 16 bits");
 
@@ -237,20 +241,16 @@ __global__ void __launch_bounds__(64 * NW) xp_in_k(XpRows a) {
   }
 }
 
-// 8 elements of z from `at` on, 8 elements aligned.
-template <bool Z16> __device__ __forceinline__ void load_z(const void *z, int64_t at, float *x) {
-  if constexpr (Z16) {
-    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-    const f16x8 v = *reinterpret_cast<const f16x8 *>(reinterpret_cast<const uint16_t *>(z) + at);
+// 8 float16 values at p (16-byte aligned)
+__device__ __forceinline__ void load_f16(const uint16_t *p, float *x) {
+  typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+  const f16x8 v = *reinterpret_cast<const f16x8 *>(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
-  } else {
-    load8<true>(reinterpret_cast<const float *>(z) + at, x);
-  }
+  for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
 }
 
 // One workgroup a row of y: a row's U^T z, or with `pos` the sum of a token's rows, each with its weight, in
-// the order of its choices, in float32. Z16: z in float16 (the bf16 path), its parts along k added up here.
+// the order of its choices, in float32. Z16: z in float16. Parts along k are added up here.
 template <int E, int NW, bool F32, bool Z16>
 __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
   extern __shared__ __attribute__((aligned(16))) float buf[];
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
       const int32_t r = a.pos ? a.pos[row_y * a.top + j] : (int32_t)row_y;
       if (r < first || r >= end) continue;           // uniform
       const int expert = a.row_expert[r], e = expert & 0xFFFF, rest = expert >> 16;
-      const int parts = bounded(a.row_parts[r], a.ks);         // (decreasing offsets: rows no tile was for)
+      const int where = a.row_parts[r], parts = where & 15;
       const float w = (a.pos ? a.weights[row_y * a.top + j] * inv : inv) * a.row_factor[r];
       const int8_t *signs = a.sign_n + (int64_t)e * a.n;
       float v[E];
@@ -278,11 +278,16 @@ __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[h + i] = 0.0f;
         if (o >= a.n) continue;
-        for (int p = 0; p < parts; ++p) {
-          float x[8];
-          load_z<Z16>(a.z, ((int64_t)p * a.rows + r) * a.n + o, x);
+        if (parts == 1) {
+          if constexpr (Z16) load_f16(reinterpret_cast<const uint16_t *>(a.z) + (int64_t)r * a.n + o, v + h);
+          else load8<true>(reinterpret_cast<const float *>(a.z) + (int64_t)r * a.n + o, v + h);
+        } else {
+          for (int p = 0; p < parts; ++p) {
+            float x[8];
+            load8<true>(a.zs + ((where >> 4) + (int64_t)p * a.zs_step) * a.n + o, x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[h + i] += x[i];
+            for (int i = 0; i < 8; ++i) v[h + i] += x[i];
+          }
         }
         if (a.row_scale) {
           float x[8];
@@ -548,18 +553,18 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
   if (y0 >= y1) return;
   const int el = 1024 * (wave - set * waves) + 8 * rb_ell(lane), eo = 1024 * (wave - set * waves) + rb_elem_out(lane, 0);
   const float inv = 1.0f / sqrtf((float)(1 << a.log_n));
-  constexpr int RAW = Z16 ? 2 : 4, ES = Z16 ? 2 : 4;
+  constexpr int RAW = Z16 ? 2 : 4;
   const int turns = (a.top + sets - 1) / sets;       // items of a token that a set has
   const int64_t items = (int64_t)(y1 - y0) * turns;
-  int32_t row = -1, expert = 0, parts = 0;           // of item base + lane
+  int32_t row = -1, expert = 0, where = 0;           // of item base + lane
   float factor = 0.0f;
   int64_t base = -64;
-  struct Item { int32_t row, parts, expert; float factor; uint4 raw[RAW]; uint2 sign[2]; };
-  auto plane = [&](int p, int32_t r, uint4 (&raw)[RAW]) {
-    const uint4 *z = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(a.z) + ES * (((int64_t)p * a.rows + r) * a.n + el));
-    if constexpr (Z16) raw[0] = z[0], raw[1] = z[64];
-    else raw[0] = z[0], raw[1] = z[1], raw[2] = z[128], raw[3] = z[129];
+  struct Item { int32_t row, where, expert; float factor; uint4 raw[RAW]; uint2 sign[2]; };
+  auto load_row = [&](const float *row, uint4 (&raw)[4]) {
+    const uint4 *z = reinterpret_cast<const uint4 *>(row + el);
+    raw[0] = z[0], raw[1] = z[1], raw[2] = z[128], raw[3] = z[129];
   };
+  auto part = [&](int p, const Item &it) { return a.zs + ((it.where >> 4) + (int64_t)p * a.zs_step) * a.n; };
   auto fetch = [&](int64_t i, Item &it) {
     if (i >= base + 64) {
       base = i;
@@ -573,35 +578,35 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
         if (a.pos) factor *= a.weights[(y0 + y) * a.top + j];
       }
       if (row >= 0) {
-        expert = a.row_expert[row], parts = bounded(a.row_parts[row], a.ks);   // (decreasing offsets: rows no tile was for)
+        expert = a.row_expert[row], where = a.row_parts[row];
         factor *= a.row_factor[row];
+        if (where == 0) row = -1;
       }
     }
     const int at = (int)(i - base);
     it.row = __builtin_amdgcn_readlane(row, at);
     if (it.row < 0) return;
-    it.parts = __builtin_amdgcn_readlane(parts, at);
+    it.where = __builtin_amdgcn_readlane(where, at);
     it.factor = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(factor), at));
     it.expert = __builtin_amdgcn_readlane(expert, at);
-    plane(0, it.row, it.raw);
+    if constexpr (Z16) {                             // (parts, of a launch's last units, are asked for when their turn comes)
+      if ((it.where & 15) == 1) {                    // uniform
+        const uint4 *z = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(a.z) + (int64_t)it.row * a.n + el);
+        it.raw[0] = z[0], it.raw[1] = z[64];
+      }
+    } else {                                         // (one address and no branch: where paths with other loads met, they were waited for)
+      const float *whole = reinterpret_cast<const float *>(a.z) + (int64_t)it.row * a.n;
+      load_row((it.where & 15) == 1 ? whole : part(0, it), it.raw);
+    }
     const int8_t *signs = a.sign_n + (int64_t)(it.expert & 0xFFFF) * a.n + eo;
     it.sign[0] = *reinterpret_cast<const uint2 *>(signs), it.sign[1] = *reinterpret_cast<const uint2 *>(signs + 256);
   };
   typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-  auto spread = [&](const uint4 (&raw)[RAW], float (&x)[16]) {
-    if constexpr (Z16) {
+  auto spread = [&](const uint4 (&raw)[4], float (&x)[16]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f16x8 f = __builtin_bit_cast(f16x8, raw[h]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[8 * h + i] = (float)f[i];
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        x[4 * q] = __uint_as_float(raw[q].x), x[4 * q + 1] = __uint_as_float(raw[q].y);
-        x[4 * q + 2] = __uint_as_float(raw[q].z), x[4 * q + 3] = __uint_as_float(raw[q].w);
-      }
+    for (int q = 0; q < 4; ++q) {
+      x[4 * q] = __uint_as_float(raw[q].x), x[4 * q + 1] = __uint_as_float(raw[q].y);
+      x[4 * q + 2] = __uint_as_float(raw[q].z), x[4 * q + 3] = __uint_as_float(raw[q].w);
     }
   };
   float acc[16];
@@ -616,11 +621,27 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
     if (i + 1 < items) fetch(i + 1, next);
     float v[16];
     if (it.row >= 0) {
-      spread(it.raw, v);
-      for (int p = 1; p < it.parts; ++p) {
-        uint4 raw[RAW];
+      const int parts = it.where & 15;
+      if constexpr (Z16) {
+        if (parts > 1) {
+          uint4 raw[4];
+          load_row(part(0, it), raw);
+          spread(raw, v);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const f16x8 f = __builtin_bit_cast(f16x8, it.raw[h]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[8 * h + q] = (float)f[q];
+          }
+        }
+      } else {
+        spread(it.raw, v);
+      }
+      for (int p = 1; p < parts; ++p) {
+        uint4 raw[4];
         float x[16];
-        plane(p, it.row, raw);
+        load_row(part(p, it), raw);
         spread(raw, x);
 #pragma unroll
         for (int q = 0; q < 16; ++q) v[q] += x[q];
@@ -693,9 +714,13 @@ struct XpProduct {
   const float *rowsum;
   const int32_t *offsets;
   int32_t *row_parts;
-  void *z;                     // [parts][rows][n]
+  void *z;                     // [rows][n], and the parts' sums beside: as in XpRows
+  float *zs;
   int64_t n, k, kp;
   int32_t count, rows;
+  int32_t zs_step;             // `rows`, or with zs_own the rows of a tile
+  bool zs_own;                 // each unit has rows of zs to itself
+  bool z16;                    // z in float16
   uint32_t n_groups;           // of 256 weight rows
   uint32_t likely;             // workgroups that very likely have a tile
   int32_t ks;                  // parts along k, at most, of the rows that are split
@@ -712,7 +737,8 @@ __device__ __forceinline__ uint4 unbiased(uint4 w) {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // A tile: rows row0 .. row1 - 1 of expert e, its weight rows from 256 group on, part `part` of `parts` along k.
-struct XpTile { int e; int32_t row0, row1; uint32_t group; int part, parts; };
+// zs: row of part 0's sums of row0.
+struct XpTile { int e; int32_t row0, row1; uint32_t group; int part, parts; int32_t zs; };
 
 // The launch's tiles, numbered. Units are groups of tm rows of an expert, whole ones first, then the experts'
 // remainders, which are shorter. Where the last round on the card has few enough tiles, its units are split along k, into as many of up
@@ -753,7 +779,7 @@ struct XpTiles {
       const uint32_t run = (n + 7) / 8, t = (i % 8) * run + i / 8;
       return i / 8 < run && t < n ? t : n;
     };
-    tile.part = 0, tile.parts = 1;
+    tile.part = 0, tile.parts = 1, tile.zs = 0;
     uint32_t u;
     if (b < blocks) {
       const uint32_t t = spread(b, first);
@@ -764,6 +790,7 @@ struct XpTiles {
       if (t >= n) return false;
       u = t / (a.n_groups * parts);
       const uint32_t in = t - u * a.n_groups * parts;
+      tile.zs = (int32_t)(u * parts) * tm;
       u += lead;
       tile.part = (int)(in / a.n_groups), tile.parts = (int)parts, tile.group = in % a.n_groups;
     }
@@ -783,6 +810,7 @@ struct XpTiles {
         tile.row0 = is_rest ? begin + (end - begin) / tm * tm
                             : begin + (int32_t)(u - (uint32_t)__builtin_amdgcn_readlane((int)at_first, at)) * tm;
         tile.row1 = end - tile.row0 < tm ? end : tile.row0 + tm;
+        if (!a.zs_own) tile.zs = tile.row0;
         return true;
       }
       before += (uint32_t)__builtin_amdgcn_readlane((int)up, 63);
@@ -1094,47 +1122,61 @@ __device__ __forceinline__ void gemm_tile(const XpProduct &a, uint8_t *lds, cons
   if (n0 == 0 && tile.part == 0 && lane < 32)
 #pragma unroll
     for (int t = 0; t < MB; ++t)
-      if (row0 + 32 * t + lane < row1) a.row_parts[row0 + 32 * t + lane] = tile.parts;
+      if (row0 + 32 * t + lane < row1)
+        a.row_parts[row0 + 32 * t + lane] = tile.parts == 1 ? 1 : tile.parts | (tile.zs + 32 * t + lane) << 4;
   // Lane (c, p) holds rows 8 (i >> 2) + 4 p + (i & 3) of weight row n0 + c. z goes out through the wave's own piece of LDS, 32 rows
   // at a time, so that a lane stores 16 bytes of a row: element by element, with a load of the row's sum for each,
   // the end of a tile took 15 of 141 us.
-  constexpr int ES = F32 ? 4 : 2, SB = 32 * ES + 16, CPR = 32 * ES / 16;        // bytes of an element and of a row, chunks a row
   constexpr bool BIAS = !F32 && BPW > 2;
-  const uint32_t sums = lds_table_bytes<BPW>(), mine = sums + 1024 + (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6) * 32 * SB;
+  const uint32_t sums = lds_table_bytes<BPW>();
   __syncthreads();                                             // the tiles of x~ are done with
   if constexpr (BIAS) {
     if (tid < 256) lds_stf(sums + 4 * tid, row_sum);
     __syncthreads();
   }
   typedef __attribute__((address_space(3))) _Float16 lds_f16_w;
+  auto leave = [&](auto wide) {
+    constexpr bool W = decltype(wide)::value;                  // float32, or float16
+    constexpr int ES = W ? 4 : 2, SB = 32 * ES + 16, CPR = 32 * ES / 16;        // bytes of an element and of a row, chunks a row
+    const uint32_t mine = sums + 1024 + (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6) * 32 * SB;
+    uint8_t *to = reinterpret_cast<uint8_t *>(tile.parts == 1 ? a.z : a.zs) +
+                  (int64_t)(tile.parts == 1 ? row0 : tile.zs + tile.part * a.zs_step) * a.n * ES;
 #pragma unroll
-  for (int t = 0; t < MB; ++t) {
-    __builtin_amdgcn_wave_barrier();
+    for (int t = 0; t < MB; ++t) {
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      uint4 s = make_uint4(0, 0, 0, 0);
-      if constexpr (BIAS) s = lds128(sums + 4 * (32 * t + 8 * g + 4 * p));
-      const float bias[4] = {__uint_as_float(s.x), __uint_as_float(s.y), __uint_as_float(s.z), __uint_as_float(s.w)};
+      for (int g = 0; g < 4; ++g) {
+        uint4 s = make_uint4(0, 0, 0, 0);
+        if constexpr (BIAS) s = lds128(sums + 4 * (32 * t + 8 * g + 4 * p));
+        const float bias[4] = {__uint_as_float(s.x), __uint_as_float(s.y), __uint_as_float(s.z), __uint_as_float(s.w)};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = BIAS ? fmaf(-Epi<BPW>::bias, bias[i], acc[t][4 * g + i]) : acc[t][4 * g + i];
-        const uint32_t at = mine + (8 * g + 4 * p + i) * SB + c * ES;
-        if constexpr (F32) lds_stf(at, v);
-        else *reinterpret_cast<lds_f16_w *>((uintptr_t)at) = (_Float16)v;
+        for (int i = 0; i < 4; ++i) {
+          const float v = BIAS ? fmaf(-Epi<BPW>::bias, bias[i], acc[t][4 * g + i]) : acc[t][4 * g + i];
+          const uint32_t at = mine + (8 * g + 4 * p + i) * SB + c * ES;
+          if constexpr (W) lds_stf(at, v);
+          else *reinterpret_cast<lds_f16_w *>((uintptr_t)at) = (_Float16)v;
+        }
       }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");     // other lanes of the wave read it
-    __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // other lanes of the wave read it
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < 32 * CPR / 64; ++i) {
-      const int chunk = 64 * i + lane, rl = chunk / CPR, pc = chunk % CPR;
-      const uint4 v = lds128(mine + rl * SB + pc * 16);
-      const int32_t r = row0 + 32 * t + rl;
-      const int64_t col = n0 + pc * (16 / ES);
-      if (r < row1 && col < a.n)                               // (n is a multiple of 8)
-        *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(a.z) + (((int64_t)tile.part * a.rows + r) * a.n + col) * ES) = v;
+      for (int i = 0; i < 32 * CPR / 64; ++i) {
+        const int chunk = 64 * i + lane, rl = chunk / CPR, pc = chunk % CPR;
+        const uint4 v = lds128(mine + rl * SB + pc * 16);
+        const int32_t r = 32 * t + rl;
+        const int64_t col = n0 + pc * (16 / ES);
+        if (row0 + r < row1 && col < a.n)                      // (n is a multiple of 8)
+          *reinterpret_cast<uint4 *>(to + (r * a.n + col) * ES) = v;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
+  static_assert(1024 + 8 * 32 * (32 * 4 + 16) <= 2 * sizeof(uint16_t) * gemm_rows(F32) * kGemmLda, "a wave's piece");
+  if constexpr (F32) {
+    leave(std::true_type());
+  } else {
+    if (a.z16 && tile.parts == 1) leave(std::false_type());
+    else leave(std::true_type());
   }
 }
 
@@ -1299,33 +1341,32 @@ int check_experts(const glq_experts *E) {
   return GLQ_OK;
 }
 
-// Most parts along k of the units that are split (XpTiles): two planes of float32 z and four of float16 always have room (z_bytes), four or
+// Most parts along k of the units that are split (XpTiles): two, four where bf16 rows are long, and four or
 // eight as many as give each CU one for the most tiles there can be; none under 4 steps, which would not pay for the
-// transforms' reading more planes. 2 of 8 experts of 4096 x 4096 at 4 bits, a row each, 32 tiles: product 14 us in 8 parts,
-// 32 in 2. 8192 rows over 8 experts of that size at 3 bits, 576 tiles: the call 401 us with 4 units in 4 parts, 422 with the last
-// 20 units in 2.
+// transforms' reading more sums. 2 of 8 experts of 4096 x 4096 at 4 bits, a row each, 32 tiles: product 14 us in 8 parts,
+// 32 in 2. 8192 rows over 8 experts of that size at 3 bits, 576 tiles: the call 343 us with its last 4 units in 4 parts,
+// 353 with 20 in 2; of 4096 x 1024 (16 steps) at 2 bits 133 and 126.
 int xp_parts(int64_t count, int64_t n, int64_t k, int64_t rows, bool f32) {
   const int64_t steps = up128(k) / kGemmK, most = (rows / (f32 ? 64 : 256) + (count < rows ? count : rows)) * ((n + 255) / 256);
   if (steps > kSplitSteps || steps < 8) return 1;
-  int ks = f32 || steps < 16 ? 2 : 4;
+  int ks = f32 || steps < 32 ? 2 : 4;
   while (ks < 8 && most * 2 * ks <= kCus && steps / (2 * ks) >= 4) ks *= 2;
   return ks;
 }
 
-// Bytes of z's planes for up to this many rows: two of float32, which are four of float16, or four or eight of either where the rule
-// above can ask for them, most tiles * parts <= 256 (so rows < tm (256 / (parts groups) + 1)).
-int64_t z_bytes(int64_t n, int64_t rows) {
-  const int64_t groups = (n + 255) / 256;
-  int64_t need = 2 * rows * n * 4;
-  for (const int tm : {64, 256})
-    for (const int ks : {4, 8}) {
-      const int64_t top = tm * ((int64_t)kCus / (ks * groups) + 1), bytes = ks * (rows < top ? rows : top) * n * (tm == 64 ? 4 : 2);
-      if (bytes > need) need = bytes;
-    }
-  return need;
+// Rows of the parts' sums (zs) in tiles of tm rows: ks times the rows, or, where that is less, the tiles' own: no more than a
+// tile a CU is split (XpTiles).
+int64_t zs_rows(int64_t n, int64_t rows, int ks, int tm) {
+  const int64_t own = (int64_t)tm * (kCus / ((n + 255) / 256));
+  return ks == 1 ? 0 : rows * ks < own ? rows * ks : own;
+}
+// As many at least, for up to this many rows of either type.
+int64_t zs_most(int64_t n, int64_t k, int64_t rows) {
+  const int64_t steps = up128(k) / kGemmK;
+  return steps > kSplitSteps || steps < 8 ? 0 : zs_rows(n, rows, 8, 256);
 }
 
-struct XpLayout { int64_t xt, rowsum, row_factor, row_expert, row_parts, z, total; };
+struct XpLayout { int64_t xt, rowsum, row_factor, row_expert, row_parts, z, zs, total; };
 XpLayout xp_layout(const glq_experts *E, int64_t rows) {
   XpLayout w;
   w.xt = 0;
@@ -1334,7 +1375,8 @@ XpLayout xp_layout(const glq_experts *E, int64_t rows) {
   w.row_expert = w.row_factor + up256(rows * 4);
   w.row_parts = w.row_expert + up256(rows * 4);
   w.z = w.row_parts + up256(rows * 4);
-  w.total = w.z + up256(z_bytes(E->n, rows));
+  w.zs = w.z + up256(rows * E->n * 4);
+  w.total = w.zs + up256(zs_most(E->n, E->k, rows) * E->n * 4);
   return w;
 }
 
@@ -1373,14 +1415,20 @@ extern "C" int glq_expert_linear(const glq_experts *E, const glq_expert_rows *R,
   uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
   const XpLayout l = xp_layout(E, R->rows);
   const bool f32 = R->x_dt == GLQ_F32;
-  const int ks = xp_parts(E->count, E->n, E->k, R->rows, f32);
+  const int ks = xp_parts(E->count, E->n, E->k, R->rows, f32), tm = f32 ? 64 : 256;
+  // z in float16 where both ends are bfloat16 and in float32 it would be more than the 32 MB that the L2s hold. In float16 and float32,
+  // rows of 4096 through 8 experts of 4096 x 4096 at 2 bits: 1024 rows 98 and 100 us, 2048: 118 and 122, 4096: 182 and 190,
+  // 8192: 320 and 332; 65,536 rows, 64 of 2048 x 1024: 432 and 518; 2048 rows, 8 of 1024 x 1024: 35 and 35
+  const bool z16 = !f32 && R->y_dt == GLQ_BF16 && R->rows * E->n >= (int64_t(1) << 23);
   XpRows a = {};
   a.x = R->x, a.y = R->y, a.offsets = R->offsets, a.src = R->src, a.pos = R->pos, a.weights = R->weights;
   a.sign_k = E->sign_k, a.sign_n = E->sign_n, a.scale = E->scale, a.row_scale = E->row_scale;
   a.unit = E->bpw == 2 ? Epi<2>::mul : E->bpw == 3 ? Epi<3>::mul : Epi<4>::mul;
   a.xt = reinterpret_cast<uint16_t *>(ws + l.xt), a.rowsum = reinterpret_cast<float *>(ws + l.rowsum);
   a.row_factor = reinterpret_cast<float *>(ws + l.row_factor), a.row_expert = reinterpret_cast<int32_t *>(ws + l.row_expert);
-  a.row_parts = reinterpret_cast<int32_t *>(ws + l.row_parts), a.z = ws + l.z;
+  a.row_parts = reinterpret_cast<int32_t *>(ws + l.row_parts), a.z = ws + l.z, a.zs = reinterpret_cast<float *>(ws + l.zs);
+  const bool zs_own = zs_rows(E->n, R->rows, ks, tm) < R->rows * ks;
+  a.zs_step = zs_own ? tm : (int32_t)R->rows;
   a.k = E->k, a.kp = up128(E->k), a.n = E->n, a.x_rows = R->x_rows, a.out_rows = out;
   a.count = (int32_t)E->count, a.rows = (int32_t)R->rows, a.top = R->pos ? R->top_k : 1, a.ks = ks;
   a.log_k = log_block(E->k), a.log_n = log_block(E->n);
@@ -1389,10 +1437,11 @@ extern "C" int glq_expert_linear(const glq_experts *E, const glq_expert_rows *R,
     rc = f32 ? launch_transform<false, true>(a, R->rows, st) : launch_transform<false, false>(a, R->rows, st);
     if (rc) return rc;
     const XpProduct p = {E->idx1, a.xt, E->idx2, reinterpret_cast<const uint8_t *>(E->cb), a.rowsum, a.offsets,
-                         a.row_parts, ws + l.z, E->n, E->k, a.kp, a.count, a.rows, 0, 0, ks};
+                         a.row_parts, ws + l.z, reinterpret_cast<float *>(ws + l.zs), E->n, E->k, a.kp, a.count, a.rows,
+                         a.zs_step, zs_own, z16, 0, 0, ks};
     rc = E->bpw == 2 ? launch_product<2>(p, f32, st) : E->bpw == 3 ? launch_product<3>(p, f32, st) : launch_product<4>(p, f32, st);
     if (rc) return rc;
   }
-  if (f32) return R->y_dt == GLQ_F32 ? launch_transform<true, true>(a, out, st) : launch_transform<true, false>(a, out, st);
-  return R->y_dt == GLQ_F32 ? launch_transform<true, true, true>(a, out, st) : launch_transform<true, false, true>(a, out, st);
+  if (R->y_dt == GLQ_F32) return launch_transform<true, true>(a, out, st);
+  return z16 ? launch_transform<true, false, true>(a, out, st) : launch_transform<true, false>(a, out, st);
 }

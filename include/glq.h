@@ -651,7 +651,8 @@ typedef struct {
  * the rows r of expert e, as glq_fused_linear does for one layer; with pos (a token's rows, from
  * glq_route) y_t = sum_j weights[t][j] y_pos[t][j], summed in float32 in a fixed order and rounded once.
  *   x_dt = GLQ_BF16: x~ rounded to bf16 (2^-8 relative at most), weights exact in bf16, float32 sums on the matrix
- *                    cores, z = s W^ x~ rounded to float16 (2^-11 relative at most) with a power of two for each row
+ *                    cores, z = s W^ x~ in float32. With y_dt = GLQ_BF16 and rows * n >= 2^23 z is rounded to float16 once
+ *                    (2^-11 relative at most, with a power of two for each row), where its sum is not split along k
  *   x_dt = GLQ_F32:  x~ as three bf16 parts that hold its 24 bits, so the products are those of float32 operands;
  *                    float32 sums, z in float32
  *   workspace   device, 256-byte aligned, >= glq_expert_linear_workspace(E, rows) bytes (that of more rows

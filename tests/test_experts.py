@@ -214,6 +214,75 @@ def test_rows_at_the_ends_of_bfloat16(cb, k, rows, size, scale):
     _held_at_the_ends(experts, x, y, offsets, "f32")
 
 
+def _held_to_float32(experts, x, y, offsets, y_dtype, partial=1.0):
+    """For x whose x~ is exact in bf16: what is left are float32 sums (of parts `partial` times as large as z), and y's rounding."""
+    ref = _rows_reference(experts, x.double().cpu().numpy(), offsets, None, len(x))
+    tol = _tolerance(ref, "f32", experts.k) * partial
+    _held(y, ref, tol, y_dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bpw", [2, 3, 4])
+@pytest.mark.parametrize("row_scale", [False, True])
+@pytest.mark.parametrize("count,rows,n,k", [(2, 3, 1024, 4096), (2, 40, 136, 256), (2, 700, 1024, 1024), (3, 300, 264, 1024),
+                                            (2, 1100, 2048, 256)])
+def test_float32_outputs_of_bfloat16_rows(cb, bpw, row_scale, count, rows, n, k):
+    """Nothing but x~ has fewer than float32's bits on the way to a float32 y: rows of two elements, whose x~ are 1 + 2^-6 or 1 - 2^-6
+    times a power of two, so that z has more bits than 11."""
+    experts = Set(count, n, k, bpw, seed=5, row_scale=row_scale)
+    handle, x = experts.device(cb), torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+    r = torch.arange(rows)                                       # (odd elements: x~ changes its sign from one to the next)
+    x[r, r * 6 % k + 1] = 2.0
+    x[r, (r * 6 + 2 + 2 * (r % 5)) % k + 1] = 2.0 ** -5
+    offsets = [rows * e // count for e in range(count + 1)]
+    y = torch.empty(rows, n, device="cuda")
+    glq.expert_linear(handle, x, y, torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, rows))
+    _held_to_float32(experts, x, y, offsets, "f32")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bpw", [2, 3, 4])
+@pytest.mark.parametrize("y_dtype", list(DTYPES))
+@pytest.mark.parametrize("n,k,counts", [(256, 4096, [3]), (1024, 4096, [2, 1]), (264, 1024, [40, 20]), (4096, 1024, [2100, 76])])
+def test_parts_along_k_that_cancel(cb, bpw, y_dtype, n, k, counts):
+    """Sums of parts are float32 sums: the weights of both halves of a row are the same and x~ of the second is that of
+    the first with another sign, but for 2^-6 of it, which is all that z is."""
+    experts = Set(len(counts), n, k, bpw, seed=5)
+    for idx in (experts.idx1, experts.idx2):
+        if idx is not None:
+            idx[:, :, k // 16:] = idx[:, :, :k // 16]
+    rows, offsets = sum(counts), np.concatenate(([0], np.cumsum(counts)))
+    handle, x = experts.device(cb), torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+    at = torch.arange(rows) * 6 % (k // 2) + 1
+    x[torch.arange(rows), k // 2 + at] = 2.0
+    x[torch.arange(rows), at] = 2.0 ** -5
+    y = torch.empty(rows, n, dtype=DTYPES[y_dtype], device="cuda")
+    glq.expert_linear(handle, x, y, torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, rows))
+    _held_to_float32(experts, x, y, offsets, y_dtype, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,k", [(1000, 64), (1024, 128), (8200, 64)])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_rows_and_outputs_of_8_million_elements(cb, n, k, dtype):
+    """Where z of bfloat16 calls is float16: just below that size, at it and above, summed up and not."""
+    experts = Set(3, n, k, 3, seed=11)
+    handle, most = experts.device(cb), -(-2 ** 23 // n)
+    for rows in (most - 1, most, most + 300):
+        offsets, x = [0, 100, rows // 2, rows], _inputs(rows, rows, k, dtype)
+        y = torch.empty(rows, n, dtype=x.dtype, device="cuda")
+        dev = torch.tensor(offsets, dtype=torch.int32).cuda()
+        glq.expert_linear(handle, x, y, dev, _workspace(handle, rows))
+        ref = _rows_reference(experts, x.double().cpu().numpy(), offsets, None, rows)
+        _held(y, ref, _tolerance(ref, dtype, k), dtype)
+        pos = torch.tensor([[0, rows - 1], [rows // 2, -1], [rows - 2, 150]], dtype=torch.int32)
+        w = torch.tensor([[0.5, 2.0], [1.0, 3.0], [-1.0, 0.25]])
+        s = torch.empty(3, n, dtype=x.dtype, device="cuda")
+        glq.expert_linear(handle, x, s, dev, _workspace(handle, rows), pos=pos.cuda(), weights=w.cuda())
+        each = np.where((pos >= 0).numpy()[..., None], ref[pos.numpy().clip(0)], 0.0)
+        _held(s, (each * w.numpy()[..., None]).sum(1), _tolerance(each, dtype, k, w.numpy()), dtype)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("bpw", [2, 3, 4])
 @pytest.mark.parametrize("dtype,y_dtype", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
