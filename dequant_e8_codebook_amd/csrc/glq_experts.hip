@@ -249,6 +249,14 @@ __device__ __forceinline__ void load_f16(const uint16_t *p, float *x) {
   for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
 }
 
+// 8 floats from any multiple of 4 bytes on, as row scales may lie
+__device__ __forceinline__ void load_words8(const float *p, float *x) {
+  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+  const f32x4_any a = reinterpret_cast<const f32x4_any *>(p)[0], b = reinterpret_cast<const f32x4_any *>(p)[1];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
+}
+
 // One workgroup a row of y: a row's U^T z, or with `pos` the sum of a token's rows, each with its weight, in
 // the order of its choices, in float32. Z16: z in float16. Parts along k are added up here.
 template <int E, int NW, bool F32, bool Z16>
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(64 * NW) xp_out_k(XpRows a) {
         }
         if (a.row_scale) {
           float x[8];
-          load8<true>(a.row_scale + (int64_t)e * a.n + o, x);
+          load_words8(a.row_scale + (int64_t)e * a.n + o, x);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[h + i] *= x[i];
         }
@@ -651,7 +659,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) xp_out_blk_k(XpRows a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float x[8];
-          load8<true>(a.row_scale + e * a.n + el + 512 * h, x);
+          load_words8(a.row_scale + e * a.n + el + 512 * h, x);
 #pragma unroll
           for (int q = 0; q < 8; ++q) v[8 * h + q] *= x[q];
         }

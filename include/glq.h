@@ -626,7 +626,7 @@ typedef struct {
     const int8_t *sign_k;     /* [count][k], 8-byte aligned as is sign_n */
     const int8_t *sign_n;     /* [count][n] */
     const void *cb;           /* the GLQ_CB_DEVICE tables */
-    const float *row_scale;   /* [count][n], or NULL: as in glq_layer */
+    const float *row_scale;   /* [count][n] at any multiple of 4 bytes, or NULL: as in glq_layer */
 } glq_experts;
 
 /* Rows of glq_expert_linear. The struct lives in host memory, its pointers are device pointers; x and y are

@@ -291,6 +291,24 @@ def test_row_scales_and_rows_of_none(cb, bpw, dtype, y_dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [136, 1024, 8192])
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_row_scales_at_any_word(cb, n, at):
+    experts = Set(2, n, 256, 3, seed=9, row_scale=True)
+    handle, x, offsets = experts.device(cb), _inputs(4, 30, 256, "bf16"), torch.tensor([0, 11, 30], dtype=torch.int32).cuda()
+    y, moved = (torch.empty(30, n, device="cuda") for _ in range(2))
+    glq.expert_linear(handle, x, y, offsets, _workspace(handle, 30))
+    flat = torch.zeros(2 * n + at, device="cuda")
+    flat[at:] = handle.row_scale.flatten()
+    off = glq.Experts(2, n, 256, 3, handle.scale, handle.idx1, handle.idx2, handle.sign_k, handle.sign_n, cb, flat[at:].view(2, n))
+    assert off.row_scale.data_ptr() % 16 == 4 * at
+    glq.expert_linear(off, x, moved, offsets, _workspace(off, 30))
+    assert torch.equal(y, moved)
+    ref = _rows_reference(experts, x.double().cpu().numpy(), [0, 11, 30], None, 30)
+    _held(y, ref, _tolerance(ref, "bf16", 256), "f32")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(DTYPES))
 def test_many_experts(cb, dtype):
     rng = np.random.default_rng(4)
