@@ -140,6 +140,23 @@ def test_long_rows(cb, n, k):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("bpw", [2, 3, 4])
+@pytest.mark.parametrize("n,k", [(64, 49152), (49152, 64), (64, 24576), (24576, 64), (128, 10240), (24, 16392), (8, 20480)])
+def test_rows_longer_than_a_workgroup(cb, dtype, bpw, n, k):
+    """Rows in several segments: their sums, their three parts in float32, blocks of 16384 more than once."""
+    experts = Set(2, n, k, bpw, seed=3)
+    offsets, x = [0, 2, 5], _inputs(1, 5, k, dtype)
+    handle, y = experts.device(cb), torch.full((6, n), 7.0, dtype=DTYPES[dtype], device="cuda")
+    glq.expert_linear(handle, x, y[:5], torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, 5))
+    ref = _rows_reference(experts, x.double().cpu().numpy(), offsets, None, 5)
+    # (the size of 8 outputs by the whole matrix's rows)
+    size = ref if n > 8 else np.broadcast_to(np.sqrt(k * 12.0) * experts.scale.max(), ref.shape)
+    assert (y[5] == 7).all()
+    _held(y[:5], ref, _tolerance(size, dtype, k), dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("n,k,bpw,counts", [(264, 4096, 3, [40]), (64, 8192, 4, [300]), (512, 2048, 4, [33, 70]),
                                             (256, 1096, 2, [70, 0]), (1000, 1416, 3, [257, 100, 31])])
 def test_split_along_k(cb, dtype, n, k, bpw, counts):
@@ -363,6 +380,84 @@ def test_routed(cb, dtype, tokens, count, top, n, k, bpw):
     err = (again - y.float()).abs().cpu().numpy()
     tol = (5 + 2 * top) * 2.0 ** -24 * np.abs(each * w[..., None]).sum(1) * 1.01
     assert (err <= tol + (2.0 ** -8 * (np.abs(again.cpu().numpy()) + tol) if dtype == "bf16" else 0)).all()
+
+
+def _combined(rows, pos, weights, dtype, k):
+    """The sums of rows that pos [tokens, top] names (none where it is -1), and what _tolerance gives them."""
+    out, tol = np.zeros((len(pos), rows.shape[1])), 0.0
+    for p, w in zip(pos.T, weights.T):
+        each = np.where((p >= 0)[:, None], rows[p.clip(0)], 0.0)
+        out += each * w[:, None]
+        tol = tol + _tolerance(each, dtype, k) * np.abs(w)[:, None]
+    return out, tol
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("row_scale", [False, True])
+@pytest.mark.parametrize("tokens,count,top,n,k,bpw", [
+    (1, 4, 2, 1024, 1024, 2), (1, 3, 1, 8192, 2048, 3), (5, 8, 8, 2048, 1024, 4), (64, 8, 3, 1024, 4096, 2), (256, 6, 2, 4096, 1024, 3),
+    (257, 6, 2, 4096, 1024, 3), (300, 5, 3, 5120, 2048, 2), (40, 8, 8, 1024, 5120, 4), (9, 2, 2, 16384, 1024, 2), (33, 7, 5, 6144, 6144, 3)])
+def test_routed_rows_of_whole_blocks(cb, dtype, row_scale, tokens, count, top, n, k, bpw):
+    """Sets of waves that share a token's choices and one alone; tokens without experts or with fewer than top."""
+    gen = torch.Generator().manual_seed(tokens + n)
+    logits = torch.randn(tokens, count, generator=gen)
+    if tokens > 4:
+        logits[1] = logits[tokens - 1] = -torch.inf
+        logits[3, 1:] = -torch.inf
+    weights, x = torch.empty(tokens, top, device="cuda"), _inputs(2, tokens, k, dtype)
+    ids, pos = (torch.empty(tokens, top, dtype=torch.int32, device="cuda") for _ in range(2))
+    src, offsets = (torch.empty(m, dtype=torch.int32, device="cuda") for m in (tokens * top, count + 1))
+    ws = torch.empty(glq.route_workspace_bytes(tokens, count, top), dtype=torch.uint8, device="cuda")
+    glq.route(logits.cuda(), top, weights, ids, pos, src, offsets, ws)
+    experts = Set(count, n, k, bpw, seed=6, row_scale=row_scale)
+    handle = experts.device(cb)
+    y = torch.full((tokens + 1, n), 7.0, dtype=DTYPES[dtype], device="cuda")
+    glq.expert_linear(handle, x, y[:tokens], offsets, _workspace(handle, tokens * top), src=src, pos=pos, weights=weights)
+    rows = np.nan_to_num(_rows_reference(experts, x.double().cpu().numpy(), offsets.cpu().numpy(), src.cpu().numpy(), tokens * top))
+    ref, tol = _combined(rows, pos.cpu().numpy(), weights.double().cpu().numpy(), dtype, k)
+    _held(y[:tokens], ref, tol, dtype)
+    assert (y[tokens] == 7).all() and (tokens <= 4 or not y[[1, tokens - 1]].any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("tokens,top,n", [(4700, 8, 8192), (2400, 7, 16384), (300, 64, 5120), (200, 100, 1024)])
+def test_many_choices_a_workgroup(cb, dtype, tokens, top, n):
+    """More than 64 choices for a workgroup or a set of its waves, whose rows are looked up 64 at a time; some are none."""
+    experts, rows = Set(2, n, 128, 2, seed=6, row_scale=True), 90
+    handle, x = experts.device(cb), _inputs(3, rows, 128, dtype)
+    rng = np.random.default_rng(tokens)
+    pos = rng.integers(-1, rows, (tokens, top)).astype(np.int32)
+    weights = (rng.random((tokens, top)) / top).astype(np.float32)
+    y = torch.empty(tokens, n, dtype=DTYPES[dtype], device="cuda")
+    glq.expert_linear(handle, x, y, torch.tensor([0, 31, rows], dtype=torch.int32).cuda(), _workspace(handle, rows),
+                      pos=torch.from_numpy(pos).cuda(), weights=torch.from_numpy(weights).cuda())
+    each = _rows_reference(experts, x.double().cpu().numpy(), [0, 31, rows], None, rows)
+    ref, tol = _combined(each, pos, weights.astype(np.float64), dtype, 128)
+    # (the float32 sum of `top` terms has as many roundings more, of 2^-24 of their sizes)
+    tol = tol + top * 2.0 ** -24 * np.abs(each).max() * np.abs(weights).sum(1, keepdims=True)
+    _held(y, ref, tol, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("k,rows", [(16384, 17000), (8192, 33500)])
+def test_long_runs_of_gathered_rows(cb, dtype, k, rows):
+    """More than 64 gathered rows a workgroup of the input transform, whose sources are read 64 at a time."""
+    experts, tokens = Set(3, 8, k, 2, seed=6), 50
+    handle, x = experts.device(cb), _inputs(3, tokens, k, dtype)
+    src = np.random.default_rng(k).integers(-1, tokens + 1, rows).astype(np.int32)
+    offsets = [0, rows // 3, rows // 3, rows]
+    y = torch.empty(rows, 8, device="cuda")
+    glq.expert_linear(handle, x, y, torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, rows), src=torch.from_numpy(src).cuda())
+    xn = np.concatenate((x.double().cpu().numpy(), np.zeros((1, k))))
+    at = np.where((src >= 0) & (src < tokens), src, tokens)
+    e = np.where(np.arange(rows) < offsets[1], 0, 2)
+    ref = np.stack([experts.reference(i, xn) for i in range(3)])[e, at]
+    # (its size by the whole matrix's rows: 8 outputs are too few to take it from)
+    size = np.sqrt((xn ** 2).mean(1, keepdims=True))[at] * np.sqrt(k) * experts.scale.max() * np.sqrt(12.0)
+    _held(y, ref, _tolerance(np.broadcast_to(size, ref.shape), dtype, k), "f32")
 
 
 @pytest.mark.gpu

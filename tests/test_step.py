@@ -252,6 +252,69 @@ def test_norm_rope_into_the_cache(gen, fmt, dtype, dim, pairs):
                 assert torch.equal(caches[0].k_scale, c.k_scale) and torch.equal(caches[0].v_scale, c.v_scale)
 
 
+def _tokens_of_a_prompt(heads, dim):
+    """The fewest tokens of so many heads that are a prompt to the kernel, whose lanes then take several heads each."""
+    return -(-2 ** 19 // (heads * dim // 8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim,rot", [(64, 64), (64, 16), (128, 128), (128, 96), (256, 256), (256, 48)])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("heads,kv_heads", [(7, 7), (6, 3), (5, 1), (32, 8)])
+def test_norm_rope_of_prompts(gen, dtype, dim, rot, pairs, heads, kv_heads):
+    """On both sides of the number of tokens from which lanes take several heads, of counts that four does and does not divide."""
+    most = _tokens_of_a_prompt(heads + kv_heads, dim)
+    table, w = glq.rotary_table(500, rot, 10000.0, "cpu"), [1 + 0.5 * torch.randn(dim, generator=gen) for _ in range(2)]
+    for tokens in (most - 1, most):
+        q, k, _ = _qkv(gen, tokens, heads, kv_heads, dim, dtype)
+        positions = torch.randint(0, 500, (tokens,), generator=gen).to(torch.int32)
+        outs = [torch.full((tokens + 1, h, dim), 7.0, dtype=DTYPES[dtype], device="cuda") for h in (heads, kv_heads)]
+        args = (positions.cuda(), table.cuda())
+        ws = [t.cuda() for t in w]
+        glq.qk_norm_rope(q, k, *args, outs[0][:tokens], outs[1][:tokens], *ws, eps=1e-5, pairs=pairs)
+        cos, sin = table[positions.long()].chunk(2, 1)
+        for x, out, weight in zip((q, k), outs, w):
+            ref, mag = _turn_reference(x.double().cpu(), weight, 1e-5, cos, sin, pairs)
+            _held_turn(out[:tokens], ref, mag, dtype)
+            assert (out[tokens] == 7).all()
+        glq.qk_norm_rope(q, k, *args, q, k, *ws, eps=1e-5, pairs=pairs)
+        assert torch.equal(q, outs[0][:tokens]) and torch.equal(k, outs[1][:tokens])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim,rot", [(64, 64), (128, 96), (256, 256)])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("heads,kv_heads", [(7, 7), (6, 3), (5, 1), (32, 8)])
+def test_norm_rope_of_prompts_into_the_cache(gen, fmt, dtype, dim, rot, pairs, heads, kv_heads):
+    """The cache holds what glq_kv_append of the outputs writes, bit for bit, and nothing else of it changes."""
+    form, page = {"bf16": glq.KV_BF16, "int8": glq.KV_INT8, "int4": glq.KV_INT4}[fmt], 32
+    most = _tokens_of_a_prompt(heads + 2 * kv_heads, dim)
+    table, w = glq.rotary_table(most, rot), [torch.rand(dim, generator=gen).cuda() + 0.5 for _ in range(2)]
+    for tokens in (most - 1, most):
+        pages = -(-tokens // page) + 2
+        q, k, v = _qkv(gen, tokens, heads, kv_heads, dim, dtype)
+        slots = torch.randperm(pages * page, generator=gen)[:tokens].to(torch.int32)
+        slots[1], slots[3], slots[-1] = -1, pages * page, 2 ** 31 - 1
+        slots, positions = slots.cuda(), torch.arange(tokens, dtype=torch.int32).cuda()
+        caches = [glq.KvCache.empty(pages, page, kv_heads, dim, form) for _ in range(3)]
+        outs = [torch.empty(t.shape, dtype=t.dtype, device="cuda") for t in (q, k, q, k)]
+        glq.qk_norm_rope(q, k, positions, table, outs[0], outs[1], *w, pairs=pairs, cache=caches[0], v=v, slots=slots)
+        glq.kv_append(caches[1], outs[1], v, slots)
+        ref, mag = _turn_reference(k.double().cpu(), w[1].cpu(), 1e-6, *table[:tokens].cpu().chunk(2, 1), pairs)
+        _held_turn(outs[1], ref, mag, dtype)
+        glq.qk_norm_rope(q, k, positions, table, outs[2], None, *w, pairs=pairs, cache=caches[2], v=v, slots=slots)
+        assert torch.equal(outs[0], outs[2])
+        glq.qk_norm_rope(q, k, positions, table, q, k, *w, pairs=pairs, cache=caches[0], v=v, slots=slots)      # in place
+        assert torch.equal(q, outs[0]) and torch.equal(k, outs[1])
+        for c in (caches[0], caches[2]):
+            assert torch.equal(caches[1].k, c.k) and torch.equal(caches[1].v, c.v)
+            if form != glq.KV_BF16:
+                assert torch.equal(caches[1].k_scale, c.k_scale) and torch.equal(caches[1].v_scale, c.v_scale)
+
+
 @pytest.mark.gpu
 def test_norm_rope_positions_and_special_values(gen):
     """Positions outside the table are the nearest inside; what is not finite stays in its head."""
