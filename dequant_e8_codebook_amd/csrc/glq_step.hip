@@ -681,10 +681,16 @@ int launch_norm_heads(NormArgs a, int64_t tokens, hipStream_t st) {
 template <int FMT, int D, bool F32>
 int launch_norm(const NormArgs &a, int64_t tokens, bool pairs, hipStream_t st) {
   // Several heads a row of lanes where four would leave every CU eight waves; two where rows become codes, whose maxima take
-  // registers. 32 on 8 heads of 128 in bf16, one, two and four heads: 8192 tokens without a cache 49.5, 41.9 and 39.1 us, into
-  // a bf16 cache 54.1, 46.0 and 43.7, into an int8 one 56.7, 45.3 and 49.4; 512 tokens 5.4, 5.4, 5.8, and 5.8, 5.8, 6.2, and
-  // 6.1, 6.8, 8.0; 1024 tokens 8.8, 8.5, 8.4, and 9.8, 9.0, 9.3, and 11.1, 10.6, 10.9.
-  constexpr int HB = FMT == GLQ_KV_INT8 || FMT == GLQ_KV_INT4 ? 2 : 4;
+  // registers, and of float32, which has twice the loads in flight. One, two and four heads (us a call in a graph, three or four sets of
+  // tensors in turn; 32 on 8 heads of 128, those of 16 on 4 of 256 are within 5% of them):
+  //   bf16     8192 tokens without a cache 50.1, 44.3, 41.1, into bf16 60.8, 51.5, 50.6, int8 63.4, 51.5, 54.7, int4 62.7, 54.0, 53.2
+  //            1024 tokens (the first with several) 9.2, 8.2, 8.6, and 10.0, 9.8, 10.0, and 10.8, 10.6, 12.3, and 10.8, 10.5, 12.4
+  //            512 tokens (the last with one) 5.3, 5.5, 5.8, and 6.4, 6.4, 7.0, and 6.8, 7.1, 8.9, and 6.6, 7.2, 8.8
+  //   float32  8192 tokens 69.9, 66.0, 67.8, into bf16 79.1, 77.2, 80.3, int8 80.1, 76.4, 79.4, int4 78.5, 75.1, 78.2
+  //            1024 tokens 11.8, 11.7, 12.2, and 13.4, 12.8, 13.5, and 13.5, 13.6, 15.7, and 13.6, 13.5, 15.7
+  // Heads of 64 gain later (32 on 8, bf16: 2048 tokens 9.1, 8.1, 8.6, into int8 10.7, 11.3, 12.6; 8192 24.9, 22.8, 21.2 and 34.7, 31.3, 34.2;
+  // 16 on 2 of 64, float32 into int8, 8192 tokens: 19.4, 22.0, 20.2, the most that the rule loses).
+  constexpr int HB = F32 || FMT == GLQ_KV_INT8 || FMT == GLQ_KV_INT4 ? 2 : 4;
   const int64_t heads = a.q_heads + (FMT == kNoCache ? 1 : 2) * a.io.heads;
   if (tokens * heads * (D / 8) >= (int64_t)256 * 8 * 64 * 4)
     return pairs ? launch_norm_heads<FMT, D, F32, true, HB>(a, tokens, st) : launch_norm_heads<FMT, D, F32, false, HB>(a, tokens, st);
