@@ -544,7 +544,9 @@ typedef struct {
  *   More tokens than max_tokens or max_read: what does not fit is not written, and offsets
  *   end at those lengths.
  * GLQ_ERR_UNSUPPORTED for lists or a page table of 2^31 - 4096 entries or more.
- * One launch. The caller takes *used pages off its free ones. batch == 0 gives offsets of 0 and empty lists.
+ * One launch. The caller takes *used pages off its free ones before the next call, a replay of a captured one among them, which
+ * would hand out the same pages again: on the host, or on the device without waiting (free_pages moved down by *used, entries of -1 after
+ * the last one). batch == 0 gives offsets of 0 and empty lists.
  */
 int glq_kv_plan(const glq_plan *P, void *hip_stream);
 

@@ -246,6 +246,44 @@ def test_step_in_a_graph(cb, gen, dtype, page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 64])
+def test_steps_in_a_graph_without_the_host(cb, gen, page):
+    """A captured step that takes its own pages off the free list and hands its lengths on, replayed many times before the
+    host looks: what single steps with a list on the host give. A replay that did not would hand out the same pages again."""
+    device, host = (Server(cb, "int8", batch=5, most=5, page=page) for _ in range(2))
+    at, none = torch.arange(device.pages, device="cuda"), torch.full((1,), -1, dtype=torch.int32, device="cuda")
+
+    def step():
+        device.step()
+        left = torch.cat((device.free_dev, none))
+        device.free_dev.copy_(left[(at + device.plan.used).clamp(max=device.pages)])
+        device.lens.copy_(device.plan.new_lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                                                   # (no tokens yet: changes nothing)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for added in [[1, 1, 1, 1, 1], [1, 0, 1, 0, 1], [0, 0, 0, 0, 0], [1, 1, 1, 1, 0]]:
+        state = gen.get_state()
+        device.inputs(gen, added)
+        gen.set_state(state)
+        host.inputs(gen, added)
+        torch.cuda.synchronize()
+        for _ in range(19):                                      # (q and k are rotated in place, again each time)
+            graph.replay()
+        for _ in range(19):
+            host.step()
+            host.after()
+        torch.cuda.synchronize()
+        for a, b in zip(device.results(), host.results()):
+            assert torch.equal(a, b)
+        assert torch.equal(device.lens, host.lens) and torch.equal(device.free_dev, host.free_dev)
+
+
+@pytest.mark.gpu
 def test_two_graphs_share_workspaces(cb, gen):
     """Two captured steps of different sizes in the same workspaces, replayed in turn."""
     a, b = Server(cb, batch=3, most=70, seed=5), Server(cb, batch=3, most=3, seed=6)
