@@ -1,14 +1,16 @@
 """A compressed attention block serving one user: prompt in chunks, then tokens.
 
 The q/k/v and output projections are compressed linears (glq_fused_linear), the
-keys and values live in a paged 8-bit or 4-bit cache, rotated along the head dimension
-before they are written (glq_rht_apply; queries and keys get the same rotation,
-so their scores do not change, and outlier channels spread over the codes).
+keys and values live in a paged 8-bit or 4-bit cache, whose pages, slots and positions
+come from the lengths alone (glq_kv_plan). Queries and keys are normed and turned by their
+positions (glq_qk_norm_rope), then rotated along the head dimension before they are
+written (glq_rht_apply; queries and keys get the same rotation, so their scores do not
+change, and outlier channels spread over the codes).
 
-  prompt chunk   projections -> rotate -> glq_kv_append -> glq_kv_read of what
-                 is cached -> glq_attn_prompt -> output projection
-  next token     projections -> rotate -> glq_kv_append -> glq_attn_decode ->
-                 output projection
+  prompt chunk   plan -> projections -> norm, positions, rotate -> glq_kv_append ->
+                 glq_kv_read of what is cached -> glq_attn_prompt -> output projection
+  next token     plan -> projections -> norm, positions, rotate -> glq_kv_append ->
+                 glq_attn_decode -> output projection
 
 Run on an MI355X:  python examples/attention_block.py [--cache int4] [--tokens 8]
 It prints how far the outputs are from the same block in float64 on the dense weights.
@@ -56,42 +58,46 @@ class Block:
         self.qkv = Linear((heads + 2 * kv_heads) * dim, hidden, bpw, rng, cb, max_tokens)
         self.out = Linear(hidden, heads * dim, bpw, rng, cb, max_tokens)
         self.signs = torch.from_numpy(rng.integers(0, 2, dim).astype(np.int8) * 2 - 1).cuda()
+        self.norms = [torch.from_numpy(rng.uniform(0.5, 1.5, dim).astype(np.float32)).cuda() for _ in range(2)]
+        self.angles = glq.rotary_table(max_tokens, dim)
         pages = -(-max_tokens // page)
         self.page, self.cache = page, glq.KvCache.empty(pages + 3, page, kv_heads, dim, cache_format)
-        # the user's pages, wherever they were free
-        self.table = torch.from_numpy(rng.permutation(pages + 3)[:pages].astype(np.int32)).cuda()[None]
+        self.free = torch.from_numpy(rng.permutation(pages + 3).astype(np.int32)).cuda()      # of the cache's pages, all
+        table = torch.full((1, pages), -1, dtype=torch.int32, device="cuda")
+        self.plan = glq.KvPlan(table, page, pages + 3, max_tokens, max_tokens)
+        self.lens = torch.zeros(1, dtype=torch.int32, device="cuda")
         self.ws = torch.zeros(glq.attn_decode_workspace_bytes(self.cache, 1, heads, max_tokens), dtype=torch.uint8,
                               device="cuda")
         self.max_tokens, self.length = max_tokens, 0
 
-    def _slots(self, first, count):
-        t = torch.arange(first, first + count, device="cuda")
-        return (self.table[0].long()[t // self.page] * self.page + t % self.page).to(torch.int32)
-
     def _project(self, x):
-        """Rotated queries and keys, and values, of new tokens; keys and values cached."""
-        parts = self.qkv(x).view(x.shape[0], -1, self.dim).split((self.heads, self.kv_heads, self.kv_heads), 1)
-        q, k = (p.contiguous() for p in parts[:2])
+        """Queries of new tokens, ready for attention; their keys and values are in the cache."""
+        n, plan = x.shape[0], self.plan
+        glq.kv_plan(plan, self.lens, torch.full_like(self.lens, n), self.free)
+        self.lens.copy_(plan.new_lens)
+        # the pages taken, as many as plan.used says: one user's lengths are known here without waiting for it
+        self.free = self.free[-(-(self.length + n) // self.page) - -(-self.length // self.page):]
+        self.length += n
+        q, k, v = self.qkv(x).view(n, -1, self.dim).split((self.heads, self.kv_heads, self.kv_heads), 1)
+        q, k = glq.qk_norm_rope(q, k, plan.positions[:n], self.angles, *(torch.empty(t.shape, dtype=x.dtype, device="cuda") for t in (q, k)),
+                                *self.norms)
         for p in (q, k):
             glq.rht_apply(p, p, self.signs, False)
-        glq.kv_append(self.cache, k, parts[2], self._slots(self.length, x.shape[0]))
-        self.length += x.shape[0]
+        glq.kv_append(self.cache, k, v, plan.slots[:n])
         return q
 
     def prompt(self, x):
         """The next tokens of the prompt, [tokens, hidden]."""
-        q = self._project(x)
+        q, plan = self._project(x), self.plan
         k, v = (torch.empty(self.length, self.kv_heads, self.dim, dtype=x.dtype, device="cuda") for _ in range(2))
-        glq.kv_read(self.cache, self._slots(0, self.length), k, v)
-        cu = torch.tensor([[0, x.shape[0]], [0, self.length]], dtype=torch.int32, device="cuda")
-        o = glq.attn_prompt(q, k, v, torch.empty_like(q), cu[0], cu[1], max_q=x.shape[0])
+        glq.kv_read(self.cache, plan.read_slots[:self.length], k, v)
+        o = glq.attn_prompt(q, k, v, torch.empty_like(q), plan.cu_q, plan.cu_k, max_q=x.shape[0])
         return self.out(o.flatten(1))
 
     def token(self, x):
         """One new token, [1, hidden]."""
-        q = self._project(x)
-        lens = torch.tensor([self.length], dtype=torch.int32, device="cuda")
-        o = glq.attn_decode(self.cache, q, self.table, lens, torch.empty_like(q), self.ws, self.max_tokens)
+        q, plan = self._project(x), self.plan
+        o = glq.attn_decode(self.cache, q, plan.page_table, plan.new_lens, torch.empty_like(q), self.ws, self.max_tokens)
         return self.out(o.flatten(1))
 
     def reference(self, x):
@@ -99,6 +105,12 @@ class Block:
         x = x.double().cpu()
         n, d, g = x.shape[0], self.dim, self.heads // self.kv_heads
         q, k, v = (x @ self.qkv.dense().T).view(n, -1, d).split((self.heads, self.kv_heads, self.kv_heads), 1)
+        cos, sin = self.angles[:n].double().cpu()[:, None].chunk(2, -1)
+
+        def turned(t, w):
+            a, b = (t * w.double().cpu() / torch.sqrt((t * t).mean(-1, keepdim=True) + 1e-6)).chunk(2, -1)
+            return torch.cat((a * cos - b * sin, b * cos + a * sin), -1)
+        q, k = turned(q, self.norms[0]), turned(k, self.norms[1])
         k, v = (t.repeat_interleave(g, 1).transpose(0, 1) for t in (k, v))
         s = q.transpose(0, 1) @ k.transpose(1, 2) * d ** -0.5
         s = s.masked_fill(torch.ones(n, n, dtype=torch.bool).triu(1), -torch.inf)
