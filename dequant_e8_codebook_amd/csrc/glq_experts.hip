@@ -115,7 +115,7 @@ __device__ __forceinline__ int row_exponent(uint32_t top, int64_t k) {
 // row of one large element has a z and a y far below M sqrt(k). So it is kept as a factor between 2^-60 and 2^60 and the
 // power of two that is left, which z takes before its transform: with z 2^rest = y / factor, neither comes near the range's ends.
 __device__ __forceinline__ void put_factor(const XpRows &a, int32_t r, int expert, float scale, int shift) {
-  const int e = (int)(__float_as_uint(scale) >> 23) - 127, all = e + shift, within = all < -60 ? -60 : all > 60 ? 60 : all;
+  const int e = (int)(__float_as_uint(scale) >> 23 & 255u) - 127, all = e + shift, within = all < -60 ? -60 : all > 60 ? 60 : all;
   a.row_factor[r] = ldexpf(scale, within - e);
   a.row_expert[r] = (all - within) * 65536 + expert;
   a.row_parts[r] = 0;                                // (decreasing offsets: rows no tile is for)

@@ -581,7 +581,8 @@ typedef struct {
  * then the rotation of its first rotary_dim dimensions by the position's angles:
  *   (y_i, y_j) -> (y_i cos - y_j sin, y_j cos + y_i sin),   j = i + rotary_dim / 2, or with
  *   GLQ_ROPE_PAIRS the neighbours 2 i and 2 i + 1,
- * in float32 with one rounding at the end (a mean of squares that overflows float32 gives zeros).
+ * in float32 with one rounding at the end (a mean of squares that overflows float32 gives zeros; with an eps of 0, one that
+ * vanishes, of elements below about 1e-23 or of zeros alone, gives NaN or infinities).
  * With a cache C, the rotated keys and v also go into it at the slots, with the values that
  * glq_kv_append of k_out and v would write. tokens == 0 is a successful no-op;
  * GLQ_ERR_UNSUPPORTED for rotary_dim % 16 != 0 and other head_dim.

@@ -216,6 +216,23 @@ def test_factors_at_the_ends_of_float32(cb, y_dtype, n, k, rows, size, scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("n,k", [(64, 128), (1024, 1024)])
+def test_scales_of_any_sign(cb, dtype, n, k):
+    """An expert's scale is a factor like any other: below zero, and zero."""
+    experts = Set(3, n, k, 4, seed=7)
+    experts.scale[:] = -0.02, 0.0, -1.5 * 2.0 ** -70
+    handle, offsets = experts.device(cb), [0, 5, 9, 12]
+    x = _inputs(2, 12, k, dtype)
+    x[9:] *= 2.0 ** 60
+    y = torch.empty(12, n, dtype=DTYPES[dtype], device="cuda")
+    glq.expert_linear(handle, x, y, torch.tensor(offsets, dtype=torch.int32).cuda(), _workspace(handle, 12))
+    ref = _rows_reference(experts, x.double().cpu().numpy(), offsets, None, 12)
+    _held(y, ref, _tolerance(ref, dtype, k), dtype)
+    assert not y[5:9].any()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("k,rows", [(256, 3), (4096, 3), (1024, 1400), (2048, 3), (16384, 3), (5120, 40)])
 @pytest.mark.parametrize("size,scale", [(127, -24), (126, -24), (-126, 60), (-133, 60), (-110, 60)])
 def test_rows_at_the_ends_of_bfloat16(cb, k, rows, size, scale):
