@@ -131,9 +131,9 @@ typedef __attribute__((address_space(4))) const int32_t *scalar_ints;
 
 // The pages of a tile's two halves (a half past the end repeats the first). A plan that found no free page
 // writes one outside the cache, and what lies in any page inside is another request's: the tokens of
-// such a half are loaded from kNowhere, and their scores are -inf from the start (masked after the product, in every tile
-// of a loop that otherwise has its mask behind it, they took 64 registers: 30,000 tokens in bf16 43.5 us, 30.0 so, and 29.7 were no
-// page looked at).
+// such a half are loaded from kNowhere, and their scores become -inf. Loaded from a page inside, their values would need a mask
+// too, whatever they are: in every tile, not the last alone, that took 64 registers (30,000 tokens in bf16 43.5 us, 29.6 so, and 29.5 where no
+// page was looked at).
 struct Pages { uint32_t p[2], gone; };
 struct Nowhere {
   uint8_t row[16 * 512];                             // 16 tokens of the longest rows
@@ -499,8 +499,7 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
       float s[8];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const float c0 = x.gone >> half & 1 ? -INFINITY : s0;
-        f32x4 c4 = {c0, c0, c0, c0};
+        f32x4 c4 = {s0, s0, s0, s0};
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
           const bf16x8 kk = k_operand<FMT, D, BIASED>(x, half, c, nib);
@@ -510,6 +509,10 @@ __global__ void __launch_bounds__(256, (decode_per_cu(D, F32))) attn_decode_k(De
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           s[4 * half + r] = FMT == GLQ_KV_BF16 ? c4[r] : c4[r] * x.ks[4 * half + r];
+      }
+      if (x.gone) {                                  // uniform
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = x.gone >> (j >> 2) & 1 ? -INFINITY : s[j];
       }
       if (t + 32 > end) {                            // tokens past the end: no weight, and values that are 0
 #pragma unroll
