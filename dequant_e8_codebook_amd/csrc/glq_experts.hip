@@ -10,10 +10,10 @@
 // is known on the device only: launches are sized by the most there can be, and a workgroup without rows ends at once.
 //
 // What bounds them (times of the kernels on their own): 8192 rows, 1024 an expert, of 4096 through 4096 x 4096 at 2 bits: input
-// transform 44 us (3.0 TB/s of rows read and x~ written; VALU 54% busy), product 250 us (1.10 PFLOP/s; the bf16 product of one
-// layer of that size reaches the same), output transform 34.5 us (3.9 TB/s). Few rows: 64 experts of 1024 x 2048 at 2 bits,
-// 24 rows each: 8, 22.5 (1.5 TB/s of indices; the table lookups' passes through the LDS unit) and 4.8 us, of which about 4 each are the
-// launch, the chain of dependent loads (offsets, rows, data) and in the product the copy of the tables.
+// transform 44 us (3.0 TB/s of rows read and x~ written; VALU 78% busy), product 250 us (1.10 PFLOP/s; the bf16 product of one
+// layer of that size reaches the same), output transform 34.5 us (3.9 TB/s; VALU 72%). Few rows: 64 experts of 1024 x 2048 at 2 bits,
+// 24 rows each: 8, 22.5 (1.5 TB/s of indices; the LDS unit is busy 45% of it, two thirds of that conflicts of the table lookups) and 4.8 us, of which
+// about 4 each are the launch, the chain of dependent loads (offsets, rows, data) and in the product the copy of the tables.
 #include <hip/hip_runtime.h>
 
 #include <atomic>

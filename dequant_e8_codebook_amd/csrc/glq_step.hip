@@ -277,8 +277,9 @@ constexpr int kNoCache = -1;
 // in the lane rot / 16 further, that of a pair rotation in the same lane. Values are float32
 // until the one rounding to the operands' type; the cache gets the rounded key, as
 // if it were appended afterwards. The lanes of a row take HB heads of one kind (queries, keys or values) of a token, whose
-// loads are in flight together and share the angles and the weights. Bound by what it reads and writes: 8192 tokens, 32 on 8 heads
-// of 128 in bf16 with the write into a bf16 cache 43.7 us, 4.8 TB/s; 32 tokens 3.9 us, launch and two loads one after the other.
+// loads are in flight together and share the angles and the weights. 8192 tokens, 32 on 8 heads of 128 in bf16 with the write into a
+// bf16 cache: 48 us from tensors that no cache holds, 4.7 TB/s, bound by what it reads and writes; 39 on the same tensors again, where the VALU is 94%
+// busy. 32 tokens 4.2 us, launch and two loads one after the other.
 template <int FMT, int D, bool F32, bool PAIRS, int HB>
 __global__ void __launch_bounds__(256) qk_norm_rope_k(NormArgs a) {
   constexpr int LPR = D / 8, ES = F32 ? 4 : 2;
